@@ -493,6 +493,90 @@ int pa_decode_launches(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_
                        int32_t max_blocks_per_seq, int32_t block_size, int32_t num_splits,
                        int32_t sm_count);
 
+/*
+ * Rotary positions.  A plan holds, for every pair of dimensions that turns,
+ * how far one position turns it; pa_rope_init fills it on the host once, and
+ * calls read it by value.  The turn is a 64-bit fixed-point fraction of a full
+ * turn (2^64 = one turn), so that position * turn modulo 2^64 is the exact
+ * angle's fraction at any position: far positions lose nothing.
+ */
+#define PA_ROPE_MAX_PAIRS 64
+typedef struct {
+    uint64_t turn[PA_ROPE_MAX_PAIRS]; /* per position, in 2^-64 turns */
+    float magnitude;                  /* factor on cos and sin */
+    int32_t rot_dim;                  /* dimensions that turn, from the head's first one */
+    int32_t layout;                   /* PA_ROPE_HALF or PA_ROPE_INTERLEAVED */
+} pa_rope;
+
+enum {
+    PA_ROPE_HALF = 0,       /* pair i = dimensions i and i + rot_dim / 2 */
+    PA_ROPE_INTERLEAVED = 1 /* pair i = dimensions 2 i and 2 i + 1 */
+};
+
+/* How the frequencies f_i = base^(-2 i / rot_dim) (radians per position) change for long contexts. */
+enum {
+    PA_ROPE_PLAIN = 0,  /* not at all */
+    PA_ROPE_LINEAR = 1, /* f_i / factor */
+    PA_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    PA_ROPE_YARN = 3,   /* f_i where a pair turns more than `high` times over
+                           original_positions, f_i / factor where fewer than
+                           `low` times, a ramp over the pairs between; cos and
+                           sin times 0.1 ln(factor) + 1 (Peng et al., "YaRN",
+                           2023) */
+    PA_ROPE_BANDED = 4  /* f_i where a pair turns more than `high` times over
+                           original_positions, f_i / factor where fewer than
+                           `low` times, a blend linear in the turns between */
+};
+typedef struct {
+    int32_t kind;              /* PA_ROPE_PLAIN .. PA_ROPE_BANDED */
+    double factor;             /* > 0 (PA_ROPE_YARN: >= 1) */
+    double original_positions; /* > 0 for PA_ROPE_YARN and PA_ROPE_BANDED */
+    double low, high;          /* 0 < low < high for the same two */
+    double magnitude;          /* > 0: the factor on cos and sin; 0: the kind's own */
+} pa_rope_scaling;
+
+/*
+ * Fill *rope.  rot_dim: a multiple of 16 up to 128 (PA_EUNSUPPORTED
+ * otherwise); base > 1 and finite; scaling: NULL for none.  Host-only.
+ */
+int pa_rope_init(pa_rope *rope, int32_t rot_dim, int32_t layout, double base,
+                 const pa_rope_scaling *scaling);
+
+/*
+ * Rotary positions and the slot-mapping write in one launch, the step before
+ * attention: every query head and every new key head of token i is turned to
+ * positions[i], the queries go to q_out, and the turned keys and the values go
+ * into the pools through slot_mapping as pa_cache_write writes them.  For pair
+ * (a, b) with angle t: a' = m (a cos t - b sin t), b' = m (a sin t + b cos t), in
+ * fp32, rounded once; dimensions from rot_dim on are copied.
+ * q_out, q: device bf16, row i (token i's [Hq, D]) at i * q_out_stride and
+ * i * q_stride elements; k_new, v_new: device bf16, row i ([Hkv, D]) at
+ * i * k_stride, i * v_stride (slices of one fused projection's output, for
+ * instance).  Strides are multiples of 8 elements and at least the row's
+ * length.  q_out may be q itself with the same stride.  positions: device
+ * int32 [n_tokens], any value; slot_mapping: device int64 [n_tokens], with
+ * pa_cache_write's rules (a negative slot: the token's K and V are not
+ * written; its queries are turned all the same).  rope->rot_dim <= head_dim.
+ * n_tokens == 0 is a no-op.
+ */
+int pa_rope_write(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                  const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                  const int32_t *positions, const int64_t *slot_mapping, int64_t n_tokens,
+                  int32_t Hq, void *k_cache, void *v_cache, pa_cache_desc cache,
+                  const pa_rope *rope, int32_t *status, pa_stream_t stream);
+
+/*
+ * pa_rope_write into FP8 pools: turned keys and values stored as
+ * pa_cache_write_fp8 stores values, the keys quantised from their fp32 turned
+ * values (not rounded to bf16 between).
+ */
+int pa_rope_write_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                      const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                      const int32_t *positions, const int64_t *slot_mapping, int64_t n_tokens,
+                      int32_t Hq, void *k_cache, void *v_cache, pa_cache_desc cache,
+                      float k_scale, float v_scale, const pa_rope *rope, int32_t *status,
+                      pa_stream_t stream);
+
 /* Static description of a return code. */
 const char *pa_strerror(int code);
 

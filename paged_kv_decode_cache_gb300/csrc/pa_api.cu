@@ -444,6 +444,11 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
 
 }  // namespace
 
+namespace pa {
+int check_cache(const pa_cache_desc &c) { return check_cache_desc(c); }
+bool pdl_on() { return pdl_enabled(); }
+}  // namespace pa
+
 extern "C" {
 
 int pa_version(void) { return 200; }

@@ -217,6 +217,16 @@ __device__ __forceinline__ uint2 e4m3x8_from_bf16(const uint4 &in, float scale) 
     return make_uint2(out[0], out[1]);
 }
 
+// The same for 8 fp32 values (keys turned by their rotary angle).
+__device__ __forceinline__ uint2 e4m3x8_from_f32(const float (&f)[8], float scale) {
+    uint32_t out[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        out[k >> 2] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(f[k] / scale, __NV_SATFINITE, __NV_E4M3))
+                       << (8 * (k & 3));
+    return make_uint2(out[0], out[1]);
+}
+
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a tile of
 // 128-byte rows written by TMA with CU_TENSOR_MAP_SWIZZLE_128B (the chunk
 // index is XOR-ed with the row index modulo 8; tiles are 1024-byte aligned).

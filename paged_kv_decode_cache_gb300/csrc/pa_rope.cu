@@ -1,0 +1,248 @@
+// Rotary positions fused with the slot-mapping cache write: one launch turns a
+// step's query heads and new key heads and writes K and V into the pools.
+//
+// Pair (a, b) of a head at position p turns by t = p f: a' = m (a cos t - b sin t),
+// b' = m (a sin t + b cos t).  The plan holds f / 2 pi as a 64-bit fraction of a turn;
+// p times it modulo 2^64 is the angle's exact fraction, whose top 32 bits, as
+// a signed number of half turns, go to sincospi.  (p f in fp32 is off by p 2^-25
+// radians: 0.03 at a million.)
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kUnit = 16;          // elements per thread: 8 pairs, two 16-byte chunks
+constexpr int kMaxThreads = 512;
+
+struct RopeArgs {
+    __nv_bfloat16 *q_out;
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_out_stride, q_stride, k_stride, v_stride;
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t n_slots;
+    uint8_t *k_cache, *v_cache;
+    int32_t *status;
+    int hq, hkv, head_dim;
+    float k_scale, v_scale;        // FP8 pools
+};
+
+// One CTA per token; thread = one unit of 16 elements of one head of q, k or
+// v.  In either layout unit u < rot_dim / 16 holds the pairs 8 u .. 8 u + 7: two
+// chunks rot_dim / 2 apart (half layout), or 16 elements in a row
+// (interleaved).  A warp then reads and writes whole 128-byte lines.  The
+// token's rot_dim / 2 angles are computed once, by as many threads, while the
+// loads are in flight.
+template <bool F8>
+__global__ void __launch_bounds__(kMaxThreads)
+rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
+    __shared__ float2 turn[PA_ROPE_MAX_PAIRS];  // (cos, sin) of the token's pairs
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t tok = blockIdx.x;
+    const int units = a.head_dim / kUnit, rot_units = rope.rot_dim / kUnit;
+    const bool half = rope.layout == PA_ROPE_HALF;
+    const int total = (a.hq + 2 * a.hkv) * units;
+    const int64_t slot = a.slots[tok];
+    const bool write = slot >= 0 && slot < a.n_slots;
+    if (slot >= a.n_slots && threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_SLOT);
+
+    bool ready = false;
+    for (int x = threadIdx.x; x < total || !ready; x += blockDim.x) {
+        const int head = x / units, u = x % units;
+        const bool live = x < total && (head < a.hq || write);
+        const bool rotates = u < rot_units && head < a.hq + a.hkv;
+        const int e0 = rotates && half ? 8 * u : kUnit * u;                       // first chunk
+        const int e1 = rotates && half ? rope.rot_dim / 2 + 8 * u : kUnit * u + 8;  // second chunk
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+        if (live) {
+            const __nv_bfloat16 *src =
+                head < a.hq ? a.q + tok * a.q_stride + head * a.head_dim
+                : head < a.hq + a.hkv ? a.k + tok * a.k_stride + (head - a.hq) * a.head_dim
+                                      : a.v + tok * a.v_stride + (head - a.hq - a.hkv) * a.head_dim;
+            lo = *reinterpret_cast<const uint4 *>(src + e0);
+            hi = *reinterpret_cast<const uint4 *>(src + e1);
+        }
+        if (!ready) {  // (the first pass of every thread: the loads above are in flight)
+            for (int i = threadIdx.x; i < rope.rot_dim / 2; i += blockDim.x) {
+                const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(a.positions[tok])) * rope.turn[i];
+                float s, c;
+                sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
+                turn[i] = make_float2(c * rope.magnitude, s * rope.magnitude);
+            }
+            __syncthreads();
+            ready = true;
+        }
+        if (!live) continue;
+        const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+        float f0[8], f1[8];  // the two chunks' values
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f0[2 * i] = bf16lo(w0[i]), f0[2 * i + 1] = bf16hi(w0[i]);
+            f1[2 * i] = bf16lo(w1[i]), f1[2 * i + 1] = bf16hi(w1[i]);
+        }
+        if (rotates) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 t = turn[8 * u + i];
+                if (half) {
+                    const float x0 = f0[i], x1 = f1[i];
+                    f0[i] = x0 * t.x - x1 * t.y;
+                    f1[i] = x0 * t.y + x1 * t.x;
+                } else {
+                    float *f = i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
+                    const float x0 = f[0], x1 = f[1];
+                    f[0] = x0 * t.x - x1 * t.y;
+                    f[1] = x0 * t.y + x1 * t.x;
+                }
+            }
+        }
+        const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
+        if (F8 && !is_q) {
+            const float scale = is_v ? a.v_scale : a.k_scale;
+            const int h = head - a.hq - (is_v ? a.hkv : 0);
+            uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
+            *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale);
+            *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale);
+        } else {
+            __nv_bfloat16 *dst =
+                is_q ? a.q_out + tok * a.q_out_stride + head * a.head_dim
+                     : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
+                           (slot * a.hkv + head - a.hq - (is_v ? a.hkv : 0)) * a.head_dim;
+            uint32_t o0[4], o1[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0[2 * i], f0[2 * i + 1]);
+                const __nv_bfloat162 b1 = __floats2bfloat162_rn(f1[2 * i], f1[2 * i + 1]);
+                o0[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b0) : w0[i];  // (a copy keeps its bits)
+                o1[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b1) : w1[i];
+            }
+            *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+        }
+    }
+}
+
+int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
+               int64_t k_stride, const void *v_new, int64_t v_stride, const int32_t *positions,
+               const int64_t *slot_mapping, int64_t n_tokens, int32_t Hq, void *k_cache, void *v_cache,
+               const pa_cache_desc &cache, float k_scale, float v_scale, const pa_rope *rope, int32_t *status,
+               cudaStream_t stream) {
+    if (n_tokens < 0 || Hq <= 0 || !rope) return PA_EINVAL;
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (rope->rot_dim <= 0 || rope->rot_dim % kUnit != 0 ||
+        (rope->layout != PA_ROPE_HALF && rope->layout != PA_ROPE_INTERLEAVED))
+        return PA_EINVAL;
+    if (rope->rot_dim > cache.head_dim) return PA_EINVAL;
+    if (f8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale)))
+        return PA_EINVAL;
+    if (n_tokens > INT32_MAX || static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(cache.num_kv_heads) > (1 << 20))
+        return PA_EUNSUPPORTED;
+    if (n_tokens == 0) return PA_OK;
+    if (!q_out || !q || !k_new || !v_new || !positions || !slot_mapping || !k_cache || !v_cache) return PA_EINVAL;
+    for (const void *p : {static_cast<const void *>(q_out), q, k_new, v_new, static_cast<const void *>(k_cache),
+                          static_cast<const void *>(v_cache)})
+        if (!is_aligned(p, 16)) return PA_EINVAL;
+    if (!is_aligned(positions, 4) || !is_aligned(slot_mapping, 8)) return PA_EINVAL;
+    const int64_t q_row = static_cast<int64_t>(Hq) * cache.head_dim;
+    const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
+    if (q_out_stride < q_row || q_stride < q_row || k_stride < kv_row || v_stride < kv_row ||
+        ((q_out_stride | q_stride | k_stride | v_stride) & 7))
+        return PA_EINVAL;
+    RopeArgs a{static_cast<__nv_bfloat16 *>(q_out), static_cast<const __nv_bfloat16 *>(q),
+               static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new),
+               q_out_stride, q_stride, k_stride, v_stride, positions, slot_mapping,
+               static_cast<int64_t>(cache.num_blocks) * cache.block_size, static_cast<uint8_t *>(k_cache),
+               static_cast<uint8_t *>(v_cache), status, Hq, cache.num_kv_heads, cache.head_dim, k_scale, v_scale};
+    const int units = (Hq + 2 * cache.num_kv_heads) * (cache.head_dim / kUnit);
+    const int threads = std::min(kMaxThreads, (units + 31) / 32 * 32);
+    const dim3 grid(static_cast<unsigned>(n_tokens));
+    const cudaError_t e =
+        f8 ? launch_maybe_cooperative(rope_write_kernel<true>, grid, threads, 0, stream, false, pdl_on(), a, *rope)
+           : launch_maybe_cooperative(rope_write_kernel<false>, grid, threads, 0, stream, false, pdl_on(), a, *rope);
+    return e == cudaSuccess ? PA_OK : PA_ECUDA;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+int pa_rope_init(pa_rope *rope, int32_t rot_dim, int32_t layout, double base, const pa_rope_scaling *scaling) {
+    if (!rope || rot_dim <= 0) return PA_EINVAL;
+    if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED) return PA_EINVAL;
+    if (rot_dim % pa::kUnit != 0 || rot_dim > 2 * PA_ROPE_MAX_PAIRS) return PA_EUNSUPPORTED;
+    if (!(base > 1.0) || !std::isfinite(base)) return PA_EINVAL;
+    const pa_rope_scaling none{PA_ROPE_PLAIN, 1.0, 0.0, 0.0, 0.0, 0.0};
+    const pa_rope_scaling &sc = scaling ? *scaling : none;
+    const bool by_turns = sc.kind == PA_ROPE_YARN || sc.kind == PA_ROPE_BANDED;
+    if (sc.kind < PA_ROPE_PLAIN || sc.kind > PA_ROPE_BANDED) return PA_EINVAL;
+    if (sc.kind != PA_ROPE_PLAIN && (!(sc.factor > 0.0) || !std::isfinite(sc.factor))) return PA_EINVAL;
+    if (sc.kind == PA_ROPE_YARN && sc.factor < 1.0) return PA_EINVAL;
+    if (by_turns && (!(sc.original_positions > 0.0) || !std::isfinite(sc.original_positions) || !(sc.low > 0.0) ||
+                     !(sc.high > sc.low) || !std::isfinite(sc.high)))
+        return PA_EINVAL;
+    if (!(sc.magnitude >= 0.0) || !std::isfinite(sc.magnitude)) return PA_EINVAL;
+
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    const double b = sc.kind == PA_ROPE_NTK
+                         ? base * std::pow(sc.factor, rot_dim / static_cast<double>(rot_dim - 2))
+                         : base;
+    // YaRN: the (real) pair index whose frequency makes n turns over the original positions
+    auto pair_of = [&](double n) {
+        return rot_dim * std::log(sc.original_positions / (n * kTwoPi)) / (2.0 * std::log(base));
+    };
+    double lo = 0.0, hi = 0.0;
+    if (sc.kind == PA_ROPE_YARN) {
+        lo = std::max(std::floor(pair_of(sc.high)), 0.0);
+        hi = std::min(std::ceil(pair_of(sc.low)), static_cast<double>(rot_dim - 1));
+    }
+    for (int i = 0; i < PA_ROPE_MAX_PAIRS; ++i) {
+        rope->turn[i] = 0;
+        if (i >= rot_dim / 2) continue;
+        double f = std::pow(b, -2.0 * i / rot_dim);
+        double slow = 0.0;  // share of the frequency that is divided by the factor
+        if (sc.kind == PA_ROPE_LINEAR) slow = 1.0;
+        if (sc.kind == PA_ROPE_YARN) slow = std::clamp((i - lo) / std::max(hi - lo, 0.001), 0.0, 1.0);
+        if (sc.kind == PA_ROPE_BANDED)
+            slow = 1.0 - std::clamp((sc.original_positions * f / kTwoPi - sc.low) / (sc.high - sc.low), 0.0, 1.0);
+        if (slow > 0.0) f = f / sc.factor * slow + f * (1.0 - slow);
+        double turns = f / kTwoPi;
+        turns -= std::floor(turns);  // (a factor below 1 can push it past one turn)
+        rope->turn[i] = static_cast<uint64_t>(std::llround(std::ldexp(turns, 62))) << 2;
+    }
+    rope->magnitude = static_cast<float>(sc.magnitude > 0.0             ? sc.magnitude
+                                         : sc.kind == PA_ROPE_YARN ? 0.1 * std::log(sc.factor) + 1.0
+                                                                   : 1.0);
+    rope->rot_dim = rot_dim;
+    rope->layout = layout;
+    return PA_OK;
+}
+
+int pa_rope_write(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
+                  int64_t k_stride, const void *v_new, int64_t v_stride, const int32_t *positions,
+                  const int64_t *slot_mapping, int64_t n_tokens, int32_t Hq, void *k_cache, void *v_cache,
+                  pa_cache_desc cache, const pa_rope *rope, int32_t *status, pa_stream_t stream) {
+    return pa::rope_write(false, q_out, q_out_stride, q, q_stride, k_new, k_stride, v_new, v_stride, positions,
+                          slot_mapping, n_tokens, Hq, k_cache, v_cache, cache, 1.f, 1.f, rope, status, stream);
+}
+
+int pa_rope_write_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
+                      int64_t k_stride, const void *v_new, int64_t v_stride, const int32_t *positions,
+                      const int64_t *slot_mapping, int64_t n_tokens, int32_t Hq, void *k_cache, void *v_cache,
+                      pa_cache_desc cache, float k_scale, float v_scale, const pa_rope *rope, int32_t *status,
+                      pa_stream_t stream) {
+    return pa::rope_write(true, q_out, q_out_stride, q, q_stride, k_new, k_stride, v_new, v_stride, positions,
+                          slot_mapping, n_tokens, Hq, k_cache, v_cache, cache, k_scale, v_scale, rope, status,
+                          stream);
+}
+
+}  // extern "C"

@@ -42,6 +42,23 @@ class CacheDesc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+PA_ROPE_MAX_PAIRS = 64
+PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDED = 0, 1, 2, 3, 4
+
+
+class Rope(ctypes.Structure):
+    """A rotary plan (pa_rope), filled by :func:`pa_rope_init`."""
+    _fields_ = [("turn", ctypes.c_uint64 * PA_ROPE_MAX_PAIRS), ("magnitude", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -78,6 +95,11 @@ _SIGNATURES = {
                                _F32, _I32, _P, _SZ, _P, _P], ctypes.c_int),
     "pa_decode_step_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, CacheDesc, _F32, _F32, _P, _I32, _P, _I32,
                             _I32, _F32, _I32, _P, _SZ, _P, _P], ctypes.c_int),
+    "pa_rope_init": ([_P, _I32, _I32, ctypes.c_double, _P], ctypes.c_int),
+    "pa_rope_write": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _P, _P, CacheDesc,
+                       _P, _P, _P], ctypes.c_int),
+    "pa_rope_write_fp8": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _P, _P,
+                           CacheDesc, _F32, _F32, _P, _P, _P], ctypes.c_int),
     "pa_set_option": ([_I32, _I32], ctypes.c_int),
     "pa_get_option": ([_I32], ctypes.c_int),
     "pa_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -531,3 +553,80 @@ def pa_decode_splitkv_noalloc(out, lse, q, k_cache, v_cache, block_tables, seq_l
                                          block_tables.shape[1], _ptr(seq_lens), B, Hq,
                                          float(scale), num_splits, _ptr(status), _stream(stream))
     _check("pa_decode_splitkv_noalloc", rc)
+
+
+_ROPE_LAYOUTS = {"half": PA_ROPE_HALF, "interleaved": PA_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": PA_ROPE_PLAIN, "linear": PA_ROPE_LINEAR, "ntk": PA_ROPE_NTK,
+                  "yarn": PA_ROPE_YARN, "banded": PA_ROPE_BANDED}
+
+
+def pa_rope_init(rot_dim: int, base: float, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original_positions: float = 0.0, low: float = 0.0,
+                 high: float = 0.0, magnitude: float = 0.0) -> Rope:
+    """A rotary plan for pa_rope_write: layout "half" or "interleaved"; scaling
+    "none", "linear", "ntk", "yarn" or "banded"."""
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {', '.join(_ROPE_LAYOUTS)}")
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_ROPE_SCALINGS)}")
+    rope = Rope()
+    sc = RopeScaling(_ROPE_SCALINGS[scaling], factor, original_positions, low, high, magnitude)
+    _check("pa_rope_init", lib().pa_rope_init(ctypes.byref(rope), rot_dim, _ROPE_LAYOUTS[layout],
+                                              base, ctypes.byref(sc)))
+    return rope
+
+
+def _need_rows(t: torch.Tensor, name: str):
+    """A bf16 CUDA tensor [N, H, D] whose rows [H, D] are contiguous (any stride between them)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [N, H, D]")
+    if t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name}: every row [H, D] must be contiguous")
+
+
+def _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope):
+    for t, name in ((q_out, "q_out"), (q, "q"), (k_new, "k_new"), (v_new, "v_new")):
+        _need_rows(t, name)
+    _need(positions, "positions", torch.int32, 1)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a plan made by pa_rope_init")
+    n = q.shape[0]
+    if q_out.shape != q.shape or v_new.shape != k_new.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("q_out / q, K / V or the pools differ in shape")
+    if k_new.shape[0] != n or positions.shape[0] != n or slot_mapping.shape[0] != n:
+        raise ValueError("q, k_new, positions and slot_mapping must have as many tokens")
+    if k_new.shape[1:] != k_cache.shape[2:] or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("k_new must be [N, Hkv, D] and q [N, Hq, D] matching the pool")
+    if n == 1:  # (a single row's stride says nothing)
+        strides = [t.shape[1] * t.shape[2] for t in (q_out, q, k_new, v_new)]
+    else:
+        strides = [t.stride(0) for t in (q_out, q, k_new, v_new)]
+    return (_ptr(q_out), strides[0], _ptr(q), strides[1], _ptr(k_new), strides[2], _ptr(v_new),
+            strides[3], _ptr(positions), _ptr(slot_mapping), n, q.shape[1], _ptr(k_cache),
+            _ptr(v_cache), cache_desc(k_cache))
+
+
+@_on_tensors_device
+def pa_rope_write(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
+                  status=None, stream=None):
+    """Turn q into q_out, and write the turned k_new and v_new through slot_mapping."""
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope)
+    rc = lib().pa_rope_write(*args, ctypes.byref(rope), _ptr(status), _stream(stream))
+    _check("pa_rope_write", rc)
+
+
+@_on_tensors_device
+def pa_rope_write_fp8(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, k_scale,
+                      v_scale, rope, status=None, stream=None):
+    """pa_rope_write into uint8 e4m3 pools."""
+    _need_pool8(k_cache, "k_cache")
+    _need_pool8(v_cache, "v_cache")
+    args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope)
+    rc = lib().pa_rope_write_fp8(*args, float(k_scale), float(v_scale), ctypes.byref(rope),
+                                 _ptr(status), _stream(stream))
+    _check("pa_rope_write_fp8", rc)
