@@ -129,9 +129,12 @@ enum {
     PA_STATUS_BAD_BLOCK = 1,  /* block table entry outside [0, num_blocks) */
     PA_STATUS_BAD_SLOT = 2,   /* slot_mapping entry >= num_blocks * block_size */
     PA_STATUS_BAD_SEQLEN = 4, /* seq_len < 0 or > max_blocks_per_seq * block_size */
-    PA_STATUS_TIMEOUT = 8     /* a bounded wait (an async copy, an MMA, the
+    PA_STATUS_TIMEOUT = 8,    /* a bounded wait (an async copy, an MMA, the
                                  split merge's arrival) gave up after about a
                                  second; that call's outputs are not valid */
+    PA_STATUS_NO_BLOCKS = 16, /* pa_sequences_fork: the pool has no free block left
+                                 for some row */
+    PA_STATUS_BAD_PARENT = 32 /* pa_sequences_fork: a parent >= B_old */
 };
 
 /*
@@ -576,6 +579,81 @@ int pa_rope_write_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t 
                       int32_t Hq, void *k_cache, void *v_cache, pa_cache_desc cache,
                       float k_scale, float v_scale, const pa_rope *rope, int32_t *status,
                       pa_stream_t stream);
+
+/*
+ * Pages of the cache.  A block's reference count says how many table entries
+ * (and other holders: a prefix cache) name it; 0 is a free block.  Tables,
+ * lengths and counts are written whole into new arrays, beside the old ones
+ * (which must be other memory), so a caller swaps the two; nothing depends on
+ * the order in which GPU threads run.  `pools`: HOST array of n_pools device
+ * pointers, the K and V pools of every layer that share the tables, each
+ * 16-byte aligned and described by `cache` with elem_bytes per value (2: bf16, 1:
+ * FP8); at most 256; it is read during the call only.  workspace: device,
+ * 256-byte aligned, of the stated size, else PA_EWORKSPACE; no initial value.
+ */
+
+/*
+ * Sequences forked, reordered and dropped, with copy on write.  Row i of the
+ * new state is row parents[i] of the old one (parents: device int32 [B_new];
+ * negative: no sequence, length 0; several rows may have one parent), sharing
+ * its blocks; new_refs = refs - the old rows' references + the new rows'.
+ * Each row is then made ready for its next token, at position L = its length:
+ *   - its last block is partial: it keeps it when every reference to that block
+ *     is a new row's partial last block and no row before it has the same one;
+ *     else its last block's L % bs token rows are copied, in every pool, into a
+ *     free block that takes its place;
+ *   - L is a multiple of the block size: it gets a free block (when L fills its
+ *     table: none, and PA_STATUS_BAD_SEQLEN).
+ * Free blocks are those with no reference left, given out lowest id first in
+ * row order; when they run out the row keeps sharing its last block,
+ * its slot is -1 and PA_STATUS_NO_BLOCKS is set.
+ * new_tables: device int32 [B_new, max_blocks_per_seq], -1 past the row's
+ * blocks; new_lens: device int32 [B_new] (the parents' lengths: the caller adds
+ * the token it writes); new_refs: device int32 [num_blocks]; slot_mapping:
+ * device int64 [B_new], the slot of position L, -1 for none.
+ * tables, lens: device int32 [B_old, max_blocks_per_seq], [B_old]; refs:
+ * device int32 [num_blocks].  B_old, B_new <= 4096.
+ * A table entry outside the pool sets PA_STATUS_BAD_BLOCK and becomes -1; a
+ * parent >= B_old sets PA_STATUS_BAD_PARENT and counts as negative.
+ */
+int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
+                      int64_t *slot_mapping, const int32_t *tables, const int32_t *lens,
+                      const int32_t *refs, const int32_t *parents, int32_t B_old, int32_t B_new,
+                      int32_t max_blocks_per_seq, void *const *pools, int32_t n_pools,
+                      int32_t elem_bytes, pa_cache_desc cache, void *workspace,
+                      size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* Workspace bytes of pa_sequences_fork (0 on bad arguments). */
+size_t pa_fork_workspace_bytes(int32_t B_old, int32_t B_new, int32_t num_blocks);
+
+/*
+ * Live blocks moved to the front: with n blocks whose count is not 0, the k-th
+ * such block with an id >= n moves, in every pool, to the k-th free id below n.
+ * remap: device int32 [num_blocks], every old id's new one, -1 for a free
+ * block (for holders other than the tables); new_refs: device int32
+ * [num_blocks], the counts at their new ids, 0 from n on; new_tables: device
+ * int32 [B, max_blocks_per_seq], the tables' entries remapped, -1 past each
+ * row's blocks; n_live: device int32, n.  A used entry that names a free block
+ * or lies outside the pool becomes -1 and sets PA_STATUS_BAD_BLOCK.  The moved blocks'
+ * old places keep their contents and are free.
+ */
+int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live,
+                      const int32_t *tables, const int32_t *lens, const int32_t *refs, int32_t B,
+                      int32_t max_blocks_per_seq, void *const *pools, int32_t n_pools,
+                      int32_t elem_bytes, pa_cache_desc cache, void *workspace,
+                      size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* Workspace bytes of pa_blocks_compact (0 on bad arguments). */
+size_t pa_compact_workspace_bytes(int32_t num_blocks);
+
+/*
+ * Whole blocks copied within every pool: pairs is device int32 [n_pairs, 2]
+ * (8-byte aligned), source and destination; a negative source is padding and is
+ * skipped, an id outside the pool is skipped and sets PA_STATUS_BAD_BLOCK.  A
+ * destination must not be another pair's source or destination.
+ */
+int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache,
+                   const int32_t *pairs, int32_t n_pairs, int32_t *status, pa_stream_t stream);
 
 /* Static description of a return code. */
 const char *pa_strerror(int code);

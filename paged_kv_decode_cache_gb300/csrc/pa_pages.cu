@@ -1,0 +1,587 @@
+// Pages of the cache: sequences forked, reordered and dropped with copy on
+// write (pa_sequences_fork), live blocks moved to the front of the pools
+// (pa_blocks_compact), blocks copied (pa_blocks_copy).
+//
+// The state is functional: new tables, lengths and reference counts are
+// written whole beside the old ones, so a call can be captured and repeated.
+// A planning kernel works out what goes where (integers only; the lowest free
+// ids are given out in row order, so that the result does not depend on
+// scheduling), and one copy kernel moves the pages of all pools.
+//
+// The planning kernel is ONE thread-block cluster: its phases need every
+// earlier write, and a cluster barrier costs a fraction of a launch or a
+// grid-wide wait.  Shared counters are L2 atomics on integers, whose order
+// cannot show.
+#include <algorithm>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxPlanCtas = 8;        // portable cluster size
+constexpr int kMaxRows = 4096;         // sequences per fork
+constexpr int kMaxPools = 256;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;           // 16-byte loads in flight per thread
+constexpr int kPiece = kCopyThreads * kCopyVecs * 16;  // bytes of a block per CTA and turn: 16 KB
+
+// Block-wide exclusive prefix sum over kPlanThreads threads; *total gets the sum.
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    const int before = warp ? warp_sums[warp - 1] : 0;
+    *total = warp_sums[31];
+    __syncthreads();  // (warp_sums is free again)
+    return before + x - v;
+}
+
+// What a plan hands to the copy kernel.
+struct CopyList {
+    int32_t count;      // entries used
+    int32_t pad[3];
+    // int4 entries follow: source block, destination block, token rows
+};
+
+struct ForkArgs {
+    int32_t *new_tables, *new_lens, *new_refs;
+    int64_t *slots;
+    const int32_t *tables, *lens, *refs, *parents;
+    int32_t *status;
+    CopyList *list;
+    int32_t *free_list;   // [B_new] the lowest free ids
+    int32_t *tail_count;  // [num_blocks] new rows whose partial last block it is
+    int32_t *tail_first;  // [num_blocks] the first of them
+    int32_t *cta_count;   // [kMaxPlanCtas]
+    int B_old, B_new, max_blocks, num_blocks, block_size;
+};
+
+__device__ __forceinline__ int checked_len(int L, int lmax, int32_t *status) {
+    if (L >= 0 && L <= lmax) return L;
+    set_status(status, PA_STATUS_BAD_SEQLEN);
+    return L < 0 ? 0 : lmax;
+}
+
+// The number of free ids a thread's segment [lo, hi) of the counts holds.
+__device__ __forceinline__ int count_zero(const int32_t *refs, int lo, int hi) {
+    int n = 0;
+    for (int i = lo; i < hi; ++i) n += __ldcg(refs + i) == 0;
+    return n;
+}
+
+// Row i of the new state is row parents[i] of the old one, sharing its blocks.
+// An old row with c children changes every count of its blocks by c - 1, so
+// rows with one child (most of them) touch no count.  Then the block of the
+// next token, position L: a row keeps its partial last block when every
+// reference to it is some new row's last block and this is the first such
+// row; any other row copies it to a free block; a row that ends with a full
+// block takes a free one.
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a) {
+    extern __shared__ int32_t smem[];
+    int32_t *row_parent = smem;                     // [B_new], -1: no sequence
+    int32_t *row_len = row_parent + a.B_new;        // [B_new]
+    int32_t *row_rank = row_len + a.B_new;          // [B_new] needs a block: which one; else -1
+    int32_t *children = row_rank + a.B_new;         // [B_old]
+    __shared__ int32_t warp_sums[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int cta = blockIdx.x, ctas = gridDim.x;
+    const int gid = cta * kPlanThreads + tid, gthreads = ctas * kPlanThreads;
+    const int bs = a.block_size, mb = a.max_blocks, lmax = mb * bs;
+
+    // ---- the rows' parents and lengths (every CTA for itself), the counts copied
+    for (int j = tid; j < a.B_old; j += kPlanThreads) children[j] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.B_new; i += kPlanThreads) {
+        int p = a.parents[i], L = 0;
+        if (p >= a.B_old) {
+            set_status(a.status, PA_STATUS_BAD_PARENT);
+            p = -1;
+        }
+        if (p >= 0) {
+            L = checked_len(a.lens[p], lmax, a.status);
+            atomicAdd(children + p, 1);
+            const int t = L % bs ? a.tables[static_cast<int64_t>(p) * mb + L / bs] : -1;
+            if (cta == 0 && t >= 0 && t < a.num_blocks) {
+                a.tail_count[t] = 0;
+                a.tail_first[t] = INT32_MAX;
+            }
+        }
+        row_parent[i] = p < 0 ? -1 : p;
+        row_len[i] = L;
+    }
+    for (int i = gid; i < a.num_blocks; i += gthreads) a.new_refs[i] = a.refs[i];
+    cluster_sync();
+
+    // ---- references dropped and added; tables copied (a warp per row)
+    for (int j = gid >> 5; j < a.B_old; j += gthreads >> 5) {
+        const int change = children[j] - 1;
+        if (change == 0) continue;
+        const int nb = (checked_len(a.lens[j], lmax, a.status) + bs - 1) / bs;
+        for (int e = lane; e < nb; e += 32) {
+            const int id = a.tables[static_cast<int64_t>(j) * mb + e];
+            if (id >= 0 && id < a.num_blocks) atomicAdd(a.new_refs + id, change);
+            else set_status(a.status, PA_STATUS_BAD_BLOCK);
+        }
+    }
+    for (int i = gid >> 5; i < a.B_new; i += gthreads >> 5) {
+        const int p = row_parent[i], nb = (row_len[i] + bs - 1) / bs;
+        for (int e = lane; e < mb; e += 32) {
+            int id = -1;
+            if (e < nb) {
+                id = a.tables[static_cast<int64_t>(p) * mb + e];
+                if (id < 0 || id >= a.num_blocks) {
+                    set_status(a.status, PA_STATUS_BAD_BLOCK);
+                    id = -1;
+                } else if (e == nb - 1 && row_len[i] % bs) {
+                    atomicAdd(a.tail_count + id, 1);
+                    atomicMin(a.tail_first + id, i);
+                }
+            }
+            a.new_tables[static_cast<int64_t>(i) * mb + e] = id;
+        }
+    }
+    cluster_sync();
+
+    // ---- which rows need a block (every CTA for itself), in row order
+    auto tail_of = [&](int i) { return __ldcg(a.new_tables + static_cast<int64_t>(i) * mb + row_len[i] / bs); };
+    int needed = 0, copies = 0;
+    const int per_row = (a.B_new + kPlanThreads - 1) / kPlanThreads;
+    {
+        const int i0 = min(tid * per_row, a.B_new), i1 = min(i0 + per_row, a.B_new);
+        int mine = 0;  // rows that need a block, and << 16 those that copy into it
+        for (int i = i0; i < i1; ++i) {
+            int need = 0;
+            if (row_parent[i] >= 0) {
+                const int L = row_len[i];
+                if (L % bs == 0) {
+                    need = L < lmax;
+                } else {
+                    const int t = tail_of(i);
+                    if (t >= 0 && !(__ldcg(a.tail_count + t) == __ldcg(a.new_refs + t) && __ldcg(a.tail_first + t) == i))
+                        need = 1 | 1 << 16;
+                }
+            }
+            row_rank[i] = need;
+            mine += need;
+        }
+        int total;
+        int at = block_scan(mine, warp_sums, &total);
+        needed = total & 0xffff, copies = total >> 16;
+        for (int i = i0; i < i1; ++i) {
+            const int need = row_rank[i];
+            row_rank[i] = need ? at : -1;  // its block's rank, and << 16 its copy's
+            at += need;
+        }
+        __syncthreads();
+    }
+
+    // ---- the `needed` lowest free ids: each CTA a slice, each thread a segment
+    int n_free = 0;
+    if (needed > 0) {  // (the same in every CTA)
+        const int slice = (a.num_blocks + ctas - 1) / ctas;
+        const int s0 = min(cta * slice, a.num_blocks), s1 = min(s0 + slice, a.num_blocks);
+        const int seg = (slice + kPlanThreads - 1) / kPlanThreads;
+        const int lo = min(s0 + tid * seg, s1), hi = min(lo + seg, s1);
+        int total;
+        int at = block_scan(count_zero(a.new_refs, lo, hi), warp_sums, &total);
+        if (tid == 0) a.cta_count[cta] = total;
+        cluster_sync();
+        for (int c = 0; c < ctas; ++c) {
+            const int n = __ldcg(a.cta_count + c);
+            if (c < cta) at += n;
+            n_free += n;
+        }
+        for (int i = lo; i < hi && at < needed; ++i)
+            if (__ldcg(a.new_refs + i) == 0) a.free_list[at++] = i;
+        cluster_sync();
+    }
+
+    // ---- the rows' last blocks, slots and copies
+    int4 *entries = reinterpret_cast<int4 *>(a.list + 1);
+    if (gid == 0) a.list->count = copies;
+    for (int i = gid; i < a.B_new; i += gthreads) {
+        const int L = row_len[i], off = L % bs, e = L / bs;
+        int64_t slot = -1;
+        if (row_rank[i] >= 0) {
+            const int rank = row_rank[i] & 0xffff;
+            const int tail = off ? tail_of(i) : -1;
+            int id = -1;
+            if (rank < n_free) {
+                id = __ldcg(a.free_list + rank);
+                a.new_tables[static_cast<int64_t>(i) * mb + e] = id;
+                a.new_refs[id] = 1;
+                if (off) atomicSub(a.new_refs + tail, 1);
+                slot = static_cast<int64_t>(id) * bs + off;
+            } else {
+                set_status(a.status, PA_STATUS_NO_BLOCKS);
+            }
+            if (off) entries[row_rank[i] >> 16] = make_int4(id < 0 ? -1 : tail, id, off, 0);
+        } else if (row_parent[i] >= 0) {
+            const int tail = off ? tail_of(i) : -1;
+            if (tail >= 0) slot = static_cast<int64_t>(tail) * bs + off;
+            else if (!off) set_status(a.status, PA_STATUS_BAD_SEQLEN);  // the table is full
+        }
+        a.slots[i] = slot;
+        a.new_lens[i] = L;
+    }
+}
+
+struct CompactArgs {
+    int32_t *new_tables, *new_refs, *remap, *n_live;
+    const int32_t *tables, *lens, *refs;
+    int32_t *status;
+    CopyList *list;
+    int32_t *holes;       // [num_blocks] free ids below the live count, ascending
+    int32_t *cta_count;   // [kMaxPlanCtas]
+    int B, max_blocks, num_blocks, block_size;
+};
+
+// With n live blocks of which A already lie below n, the n - A others move to
+// the n - A free ids below n, both in ascending order.  A block's rank among
+// the live ones gives both lists' indices: live id >= n has rank r - A, free id
+// below n has rank id - r.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
+    __shared__ int32_t warp_sums[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, cta = blockIdx.x, ctas = gridDim.x;
+    const int slice = (a.num_blocks + ctas - 1) / ctas;
+    const int s0 = min(cta * slice, a.num_blocks), s1 = min(s0 + slice, a.num_blocks);
+    const int seg = (slice + kPlanThreads - 1) / kPlanThreads;
+    const int lo = min(s0 + tid * seg, s1), hi = min(lo + seg, s1);
+    int total, n = 0;
+    int rank = block_scan(hi - lo - count_zero(a.refs, lo, hi), warp_sums, &total);
+    if (tid == 0) a.cta_count[cta] = total;
+    cluster_sync();
+    for (int c = 0; c < ctas; ++c) {
+        const int k = __ldcg(a.cta_count + c);
+        if (c < cta) rank += k;
+        n += k;
+    }
+    // ---- what stays, the holes, and how many blocks move
+    int r = rank;
+    for (int i = lo; i < hi; ++i) {
+        const int refs = a.refs[i];
+        if (i == n) a.list->count = n - r;
+        if (refs != 0) {
+            if (i < n) {
+                a.remap[i] = i;
+                a.new_refs[i] = refs;
+            }
+            ++r;
+        } else {
+            a.remap[i] = -1;
+            if (i < n) a.holes[i - r] = i;
+        }
+        if (i >= n) a.new_refs[i] = 0;
+    }
+    if (cta == 0 && tid == 0) {
+        *a.n_live = n;
+        if (n == a.num_blocks) a.list->count = 0;
+    }
+    cluster_sync();
+    // ---- the moves
+    int4 *entries = reinterpret_cast<int4 *>(a.list + 1);
+    const int first = n - __ldcg(&a.list->count);  // A
+    r = rank;
+    for (int i = lo; i < hi; ++i) {
+        const int refs = a.refs[i];
+        if (refs == 0) continue;
+        if (i >= n) {
+            const int to = __ldcg(a.holes + (r - first));
+            entries[r - first] = make_int4(i, to, a.block_size, 0);
+            a.remap[i] = to;
+            a.new_refs[to] = refs;
+        }
+        ++r;
+    }
+}
+
+struct CopyArgs {
+    const CopyList *list;       // or null: `pairs`
+    const int2 *pairs;          // (source, destination), n of them, whole blocks
+    int n_pairs;
+    int n_pools;
+    int row_bytes;              // of a token
+    int block_size, num_blocks;
+    int32_t *status;
+    // tables to rewrite while at it (pa_blocks_compact), or null
+    int32_t *new_tables;
+    const int32_t *tables, *lens, *remap;
+    int B, max_blocks;
+    uint8_t *pools[kMaxPools];
+};
+
+// Moves the listed blocks' first rows in every pool.  A turn is 16 KB of one
+// block of one pool, copied by one CTA with four 16-byte loads per thread in
+// flight; CTAs take turns in a stride, so that the list's length (which only the GPU
+// knows) spreads over all of them.  Destinations are free blocks and sources live
+// ones, so turns never meet.
+__global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if (a.new_tables) {
+        const int64_t n = static_cast<int64_t>(a.B) * a.max_blocks;
+        for (int64_t x = blockIdx.x * static_cast<int64_t>(kCopyThreads) + threadIdx.x; x < n;
+             x += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
+            const int b = static_cast<int>(x / a.max_blocks), e = static_cast<int>(x % a.max_blocks);
+            const int L = checked_len(a.lens[b], a.max_blocks * a.block_size, a.status);
+            int id = -1;
+            if (e < (L + a.block_size - 1) / a.block_size) {
+                id = a.tables[x];
+                id = id >= 0 && id < a.num_blocks ? a.remap[id] : -1;
+                if (id < 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+            }
+            a.new_tables[x] = id;
+        }
+    }
+    const int count = a.list ? a.list->count : a.n_pairs;
+    const int4 *entries = reinterpret_cast<const int4 *>(a.list + 1);
+    const int64_t block_bytes = static_cast<int64_t>(a.block_size) * a.row_bytes;
+    const int pieces = static_cast<int>((block_bytes + kPiece - 1) / kPiece);
+    const int64_t turns = static_cast<int64_t>(count) * a.n_pools * pieces;
+    for (int64_t t = blockIdx.x; t < turns; t += gridDim.x) {
+        const int piece = static_cast<int>(t % pieces);
+        const int64_t u = t / pieces;
+        const int pool = static_cast<int>(u % a.n_pools), k = static_cast<int>(u / a.n_pools);
+        int src, dst, rows = a.block_size;
+        if (a.list) {
+            const int4 e = entries[k];
+            src = e.x, dst = e.y, rows = e.z;
+        } else {
+            const int2 e = a.pairs[k];
+            src = e.x, dst = e.y;
+            if (src >= a.num_blocks || dst >= a.num_blocks || (src >= 0 && dst < 0)) {
+                if (threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                continue;
+            }
+        }
+        if (src < 0) continue;
+        const int64_t from = static_cast<int64_t>(piece) * kPiece;
+        const int64_t left = static_cast<int64_t>(rows) * a.row_bytes - from;
+        if (left <= 0) continue;
+        const int vecs = static_cast<int>((left < kPiece ? left : static_cast<int64_t>(kPiece)) / 16);
+        const uint4 *in = reinterpret_cast<const uint4 *>(a.pools[pool] + src * block_bytes + from);
+        uint4 *out = reinterpret_cast<uint4 *>(a.pools[pool] + dst * block_bytes + from);
+        uint4 v[kCopyVecs];
+#pragma unroll
+        for (int i = 0; i < kCopyVecs; ++i) {
+            const int x = i * kCopyThreads + threadIdx.x;
+            if (x < vecs) v[i] = __ldcs(in + x);
+        }
+#pragma unroll
+        for (int i = 0; i < kCopyVecs; ++i) {
+            const int x = i * kCopyThreads + threadIdx.x;
+            if (x < vecs) __stcs(out + x, v[i]);
+        }
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return -1;
+    return n;
+}
+
+int check_pools(void *const *pools, int32_t n_pools, int32_t elem_bytes, const pa_cache_desc &c) {
+    if (n_pools < 0 || (n_pools > 0 && !pools)) return PA_EINVAL;
+    if (elem_bytes != 1 && elem_bytes != 2) return PA_EINVAL;
+    const int rc = check_cache(c);
+    if (rc) return rc;
+    if (n_pools > kMaxPools) return PA_EUNSUPPORTED;
+    if (static_cast<int64_t>(c.num_kv_heads) * c.head_dim * elem_bytes > (1 << 24)) return PA_EUNSUPPORTED;
+    for (int i = 0; i < n_pools; ++i)
+        if (!pools[i] || !is_aligned(pools[i], 16)) return PA_EINVAL;
+    return PA_OK;
+}
+
+// Enough CTAs for `turns` (an upper bound; < 0: unknown, fill the GPU), at most
+// eight resident per SM.
+int launch_copy(CopyArgs &a, void *const *pools, int32_t n_pools, int32_t elem_bytes, const pa_cache_desc &c,
+                int32_t *status, int64_t turns, cudaStream_t stream) {
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ECUDA;
+    a.n_pools = n_pools;
+    a.row_bytes = c.num_kv_heads * c.head_dim * elem_bytes;
+    a.block_size = c.block_size;
+    a.num_blocks = c.num_blocks;
+    a.status = status;
+    for (int i = 0; i < n_pools; ++i) a.pools[i] = static_cast<uint8_t *>(pools[i]);
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(turns, static_cast<int64_t>(sms) * 8));
+    const cudaError_t e = launch_maybe_cooperative(copy_blocks_kernel, dim3(static_cast<unsigned>(grid)), kCopyThreads,
+                                                   0, stream, false, pdl_on(), a);
+    return e == cudaSuccess ? PA_OK : PA_ECUDA;
+}
+
+int64_t pieces_of(const pa_cache_desc &c, int32_t elem_bytes) {
+    const int64_t bytes = static_cast<int64_t>(c.block_size) * c.num_kv_heads * c.head_dim * elem_bytes;
+    return (bytes + kPiece - 1) / kPiece;
+}
+
+// CTAs of a planning cluster: one per 4096 words it reads, up to eight.
+int plan_ctas(int64_t words) {
+    int n = 1;
+    while (n < kMaxPlanCtas && words > 4096 * static_cast<int64_t>(n)) n *= 2;
+    return n;
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+size_t pa_fork_workspace_bytes(int32_t B_old, int32_t B_new, int32_t num_blocks) {
+    if (B_old < 0 || B_new < 0 || num_blocks <= 0) return 0;
+    return pa::up(sizeof(pa::CopyList) + 16 * static_cast<size_t>(B_new)) + pa::up(4 * static_cast<size_t>(B_new)) +
+           2 * pa::up(4 * static_cast<size_t>(num_blocks)) + 256;
+}
+
+size_t pa_compact_workspace_bytes(int32_t num_blocks) {
+    if (num_blocks <= 0) return 0;
+    return pa::up(sizeof(pa::CopyList) + 16 * static_cast<size_t>(num_blocks)) +
+           pa::up(4 * static_cast<size_t>(num_blocks)) + 256;
+}
+
+int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs, int64_t *slot_mapping,
+                      const int32_t *tables, const int32_t *lens, const int32_t *refs, const int32_t *parents,
+                      int32_t B_old, int32_t B_new, int32_t max_blocks_per_seq, void *const *pools, int32_t n_pools,
+                      int32_t elem_bytes, pa_cache_desc cache, void *workspace, size_t workspace_bytes,
+                      int32_t *status, pa_stream_t stream) {
+    if (B_old < 0 || B_new < 0 || max_blocks_per_seq <= 0) return PA_EINVAL;
+    int rc = pa::check_pools(pools, n_pools, elem_bytes, cache);
+    if (rc) return rc;
+    if (B_old > pa::kMaxRows || B_new > pa::kMaxRows) return PA_EUNSUPPORTED;
+    if (static_cast<int64_t>(max_blocks_per_seq) * cache.block_size > INT32_MAX / 2) return PA_EUNSUPPORTED;
+    if (!new_refs || !refs || (B_old > 0 && (!tables || !lens)) ||
+        (B_new > 0 && (!new_tables || !new_lens || !slot_mapping || !parents)))
+        return PA_EINVAL;
+    if (new_refs == refs || (B_new > 0 && (new_tables == tables || new_lens == lens))) return PA_EINVAL;
+    for (const void *p : {static_cast<const void *>(new_tables), static_cast<const void *>(new_lens),
+                          static_cast<const void *>(new_refs), static_cast<const void *>(tables),
+                          static_cast<const void *>(lens), static_cast<const void *>(refs),
+                          static_cast<const void *>(parents)})
+        if (!pa::is_aligned(p, 4)) return PA_EINVAL;
+    if (!pa::is_aligned(slot_mapping, 8)) return PA_EINVAL;
+    if (!workspace || workspace_bytes < pa_fork_workspace_bytes(B_old, B_new, cache.num_blocks) ||
+        !pa::is_aligned(workspace, 256))
+        return PA_EWORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    auto take = [&](size_t bytes) {
+        uint8_t *p = ws;
+        ws += pa::up(bytes);
+        return p;
+    };
+    pa::ForkArgs a{};
+    a.new_tables = new_tables, a.new_lens = new_lens, a.new_refs = new_refs, a.slots = slot_mapping;
+    a.tables = tables, a.lens = lens, a.refs = refs, a.parents = parents, a.status = status;
+    a.list = reinterpret_cast<pa::CopyList *>(take(sizeof(pa::CopyList) + 16 * static_cast<size_t>(B_new)));
+    a.free_list = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(B_new)));
+    a.tail_count = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(cache.num_blocks)));
+    a.tail_first = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(cache.num_blocks)));
+    a.cta_count = reinterpret_cast<int32_t *>(take(256));
+    a.B_old = B_old, a.B_new = B_new, a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
+    const int ctas = pa::plan_ctas(cache.num_blocks + static_cast<int64_t>(B_old + B_new) * max_blocks_per_seq);
+    const int smem = (3 * B_new + B_old) * 4;
+    static std::atomic<uint64_t> smem_attr_done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(pa::fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 4 * pa::kMaxRows * 4) != cudaSuccess)
+            return PA_ECUDA;
+        smem_attr_done.fetch_or(bit, std::memory_order_release);
+    }
+    if (pa::launch_clustered(pa::fork_plan_kernel, dim3(ctas), ctas, pa::kPlanThreads, smem, stream, pa::pdl_on(), a) !=
+        cudaSuccess)
+        return PA_ECUDA;
+    if (B_new == 0 || n_pools == 0) return PA_OK;
+    pa::CopyArgs c{};
+    c.list = a.list;
+    return pa::launch_copy(c, pools, n_pools, elem_bytes, cache, status,
+                           static_cast<int64_t>(B_new) * n_pools * pa::pieces_of(cache, elem_bytes), stream);
+}
+
+int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live, const int32_t *tables,
+                      const int32_t *lens, const int32_t *refs, int32_t B, int32_t max_blocks_per_seq,
+                      void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, void *workspace,
+                      size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
+    if (B < 0 || max_blocks_per_seq <= 0) return PA_EINVAL;
+    int rc = pa::check_pools(pools, n_pools, elem_bytes, cache);
+    if (rc) return rc;
+    if (static_cast<int64_t>(max_blocks_per_seq) * cache.block_size > INT32_MAX / 2) return PA_EUNSUPPORTED;
+    if (!new_refs || !remap || !n_live || !refs || (B > 0 && (!new_tables || !tables || !lens))) return PA_EINVAL;
+    if (new_refs == refs || remap == refs || remap == new_refs) return PA_EINVAL;
+    for (const void *p : {static_cast<const void *>(new_tables), static_cast<const void *>(new_refs),
+                          static_cast<const void *>(remap), static_cast<const void *>(n_live),
+                          static_cast<const void *>(tables), static_cast<const void *>(lens),
+                          static_cast<const void *>(refs)})
+        if (!pa::is_aligned(p, 4)) return PA_EINVAL;
+    if (!workspace || workspace_bytes < pa_compact_workspace_bytes(cache.num_blocks) ||
+        !pa::is_aligned(workspace, 256))
+        return PA_EWORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    pa::CompactArgs a{};
+    a.new_tables = new_tables, a.new_refs = new_refs, a.remap = remap, a.n_live = n_live;
+    a.tables = tables, a.lens = lens, a.refs = refs, a.status = status;
+    a.list = reinterpret_cast<pa::CopyList *>(ws);
+    ws += pa::up(sizeof(pa::CopyList) + 16 * static_cast<size_t>(cache.num_blocks));
+    a.holes = reinterpret_cast<int32_t *>(ws);
+    a.cta_count = reinterpret_cast<int32_t *>(ws + pa::up(4 * static_cast<size_t>(cache.num_blocks)));
+    a.B = B, a.max_blocks = max_blocks_per_seq, a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
+    const int ctas = pa::plan_ctas(cache.num_blocks);
+    if (pa::launch_clustered(pa::compact_plan_kernel, dim3(ctas), ctas, pa::kPlanThreads, 0, stream, pa::pdl_on(), a) !=
+        cudaSuccess)
+        return PA_ECUDA;
+    if (B == 0 && n_pools == 0) return PA_OK;
+    pa::CopyArgs c{};
+    c.list = a.list;
+    if (B > 0) c.new_tables = new_tables;
+    c.tables = tables, c.lens = lens, c.remap = remap, c.B = B, c.max_blocks = max_blocks_per_seq;
+    // (at most half of the blocks move)
+    const int64_t turns = static_cast<int64_t>(cache.num_blocks / 2) * n_pools * pa::pieces_of(cache, elem_bytes);
+    const int64_t entries = static_cast<int64_t>(B) * max_blocks_per_seq / pa::kCopyThreads;
+    return pa::launch_copy(c, pools, n_pools, elem_bytes, cache, status, std::max(turns, entries), stream);
+}
+
+int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, const int32_t *pairs,
+                   int32_t n_pairs, int32_t *status, pa_stream_t stream) {
+    if (n_pairs < 0) return PA_EINVAL;
+    int rc = pa::check_pools(pools, n_pools, elem_bytes, cache);
+    if (rc) return rc;
+    if (n_pairs == 0 || n_pools == 0) return PA_OK;
+    if (!pairs || !pa::is_aligned(pairs, 8)) return PA_EINVAL;
+    pa::CopyArgs c{};
+    c.pairs = reinterpret_cast<const int2 *>(pairs);
+    c.n_pairs = n_pairs;
+    return pa::launch_copy(c, pools, n_pools, elem_bytes, cache, status,
+                           static_cast<int64_t>(n_pairs) * n_pools * pa::pieces_of(cache, elem_bytes), stream);
+}
+
+}  // extern "C"

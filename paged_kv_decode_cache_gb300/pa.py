@@ -42,6 +42,7 @@ class CacheDesc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+PA_STATUS_NO_BLOCKS, PA_STATUS_BAD_PARENT = 16, 32
 PA_ROPE_MAX_PAIRS = 64
 PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
 PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDED = 0, 1, 2, 3, 4
@@ -100,6 +101,13 @@ _SIGNATURES = {
                        _P, _P, _P], ctypes.c_int),
     "pa_rope_write_fp8": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _P, _P,
                            CacheDesc, _F32, _F32, _P, _P, _P], ctypes.c_int),
+    "pa_sequences_fork": ([_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _P, _I32, _I32, CacheDesc, _P,
+                           _SZ, _P, _P], ctypes.c_int),
+    "pa_fork_workspace_bytes": ([_I32, _I32, _I32], _SZ),
+    "pa_blocks_compact": ([_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _P, _I32, _I32, CacheDesc, _P, _SZ, _P,
+                           _P], ctypes.c_int),
+    "pa_compact_workspace_bytes": ([_I32], _SZ),
+    "pa_blocks_copy": ([_P, _I32, _I32, CacheDesc, _P, _I32, _P, _P], ctypes.c_int),
     "pa_set_option": ([_I32, _I32], ctypes.c_int),
     "pa_get_option": ([_I32], ctypes.c_int),
     "pa_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -630,3 +638,111 @@ def pa_rope_write_fp8(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, 
     rc = lib().pa_rope_write_fp8(*args, float(k_scale), float(v_scale), ctypes.byref(rope),
                                  _ptr(status), _stream(stream))
     _check("pa_rope_write_fp8", rc)
+
+
+class PoolSet:
+    """The K and V pools (of every layer) that share block tables, as pa_sequences_fork,
+    pa_blocks_compact and pa_blocks_copy take them: bf16 or uint8 tensors
+    [num_blocks, block_size, Hkv, D], all alike.  Holds the tensors."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        if not self.pools:
+            raise ValueError("a PoolSet needs at least one pool")
+        first = self.pools[0]
+        if first.dtype not in (torch.bfloat16, torch.uint8):
+            raise TypeError(f"pools must be torch.bfloat16 or torch.uint8, got {first.dtype}")
+        for t in self.pools:
+            _need(t, "every pool", first.dtype, 4)
+            if t.shape != first.shape or t.device != first.device:
+                raise ValueError("the pools differ in shape or device")
+        self.device = first.device
+        self.num_blocks = first.shape[0]
+        self.desc = cache_desc(first)
+        self.elem_bytes = first.element_size()
+        self._ptrs = (ctypes.c_void_p * len(self.pools))(*[t.data_ptr() for t in self.pools])
+
+    def __len__(self):
+        return len(self.pools)
+
+
+def _state(tables, lens, refs, pools):
+    if not isinstance(pools, PoolSet):
+        raise TypeError("pools must be a PoolSet")
+    _need(tables, "tables", torch.int32, 2)
+    _need(lens, "lens", torch.int32, 1)
+    _need(refs, "refs", torch.int32, 1)
+    if refs.device != pools.device:
+        raise ValueError("the pools are on another device")
+    if lens.shape[0] != tables.shape[0] or refs.shape[0] != pools.num_blocks:
+        raise ValueError("tables, lens and refs must be [B, max_blocks], [B] and [num_blocks]")
+
+
+def _space(workspace):
+    if workspace is None:
+        return 0
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.numel() * workspace.element_size()
+
+
+def pa_fork_workspace_bytes(B_old: int, B_new: int, num_blocks: int) -> int:
+    return int(lib().pa_fork_workspace_bytes(B_old, B_new, num_blocks))
+
+
+def pa_compact_workspace_bytes(num_blocks: int) -> int:
+    return int(lib().pa_compact_workspace_bytes(num_blocks))
+
+
+@_on_tensors_device
+def pa_sequences_fork(new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents, pools,
+                      workspace, status=None, stream=None):
+    """New row i is old row parents[i] (negative: none), blocks shared, last blocks copied on write;
+    slot_mapping gets the slot of every row's next token."""
+    _state(tables, lens, refs, pools)
+    _need(new_tables, "new_tables", torch.int32, 2)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _need(new_refs, "new_refs", torch.int32, 1)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    _need(parents, "parents", torch.int32, 1)
+    n, mb = parents.shape[0], tables.shape[1]
+    if tuple(new_tables.shape) != (n, mb) or new_lens.shape[0] != n or slot_mapping.shape[0] != n or \
+            new_refs.shape != refs.shape:
+        raise ValueError("the new tables, lens, refs and slots do not match parents and the old state")
+    rc = lib().pa_sequences_fork(_ptr(new_tables), _ptr(new_lens), _ptr(new_refs), _ptr(slot_mapping),
+                                 _ptr(tables), _ptr(lens), _ptr(refs), _ptr(parents), tables.shape[0], n, mb,
+                                 pools._ptrs, len(pools), pools.elem_bytes, pools.desc, _ptr(workspace),
+                                 _space(workspace), _ptr(status), _stream(stream))
+    _check("pa_sequences_fork", rc)
+
+
+@_on_tensors_device
+def pa_blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace,
+                      status=None, stream=None):
+    """Live blocks moved to the front of every pool; remap: every old block id's new one (-1: free)."""
+    _state(tables, lens, refs, pools)
+    _need(new_tables, "new_tables", torch.int32, 2)
+    _need(new_refs, "new_refs", torch.int32, 1)
+    _need(remap, "remap", torch.int32, 1)
+    _need(n_live, "n_live", torch.int32, 1)
+    if new_tables.shape != tables.shape or new_refs.shape != refs.shape or remap.shape != refs.shape or \
+            n_live.shape[0] != 1:
+        raise ValueError("new_tables, new_refs, remap and n_live do not match the old state")
+    rc = lib().pa_blocks_compact(_ptr(new_tables), _ptr(new_refs), _ptr(remap), _ptr(n_live), _ptr(tables),
+                                 _ptr(lens), _ptr(refs), tables.shape[0], tables.shape[1], pools._ptrs,
+                                 len(pools), pools.elem_bytes, pools.desc, _ptr(workspace), _space(workspace),
+                                 _ptr(status), _stream(stream))
+    _check("pa_blocks_compact", rc)
+
+
+@_on_tensors_device
+def pa_blocks_copy(pools, pairs, status=None, stream=None):
+    """Copy whole blocks within every pool: pairs int32 [n, 2], source and destination."""
+    if not isinstance(pools, PoolSet):
+        raise TypeError("pools must be a PoolSet")
+    _need(pairs, "pairs", torch.int32, 2)
+    if pairs.shape[1] != 2 or pairs.device != pools.device:
+        raise ValueError("pairs must be [n, 2] on the pools' device")
+    rc = lib().pa_blocks_copy(pools._ptrs, len(pools), pools.elem_bytes, pools.desc, _ptr(pairs), pairs.shape[0],
+                              _ptr(status), _stream(stream))
+    _check("pa_blocks_copy", rc)
