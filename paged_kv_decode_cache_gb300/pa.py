@@ -42,6 +42,7 @@ class CacheDesc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+PA_LOGITS_BF16, PA_LOGITS_F32 = 0, 1
 PA_STATUS_NO_BLOCKS, PA_STATUS_BAD_PARENT = 16, 32
 PA_ROPE_MAX_PAIRS = 64
 PA_ROPE_HALF, PA_ROPE_INTERLEAVED = 0, 1
@@ -108,6 +109,9 @@ _SIGNATURES = {
                            _P], ctypes.c_int),
     "pa_compact_workspace_bytes": ([_I32], _SZ),
     "pa_blocks_copy": ([_P, _I32, _I32, CacheDesc, _P, _I32, _P, _P], ctypes.c_int),
+    "pa_beam_select": ([_P, _P, _P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P],
+                       ctypes.c_int),
+    "pa_beam_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32], _SZ),
     "pa_set_option": ([_I32, _I32], ctypes.c_int),
     "pa_get_option": ([_I32], ctypes.c_int),
     "pa_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -746,3 +750,41 @@ def pa_blocks_copy(pools, pairs, status=None, stream=None):
     rc = lib().pa_blocks_copy(pools._ptrs, len(pools), pools.elem_bytes, pools.desc, _ptr(pairs), pairs.shape[0],
                               _ptr(status), _stream(stream))
     _check("pa_blocks_copy", rc)
+
+
+_LOGITS = {torch.bfloat16: PA_LOGITS_BF16, torch.float32: PA_LOGITS_F32}
+
+
+def pa_beam_workspace_bytes(groups: int, beams: int, vocab: int, K: int, dtype: torch.dtype) -> int:
+    if dtype not in _LOGITS:
+        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {dtype}")
+    return int(lib().pa_beam_workspace_bytes(groups, beams, vocab, K, _LOGITS[dtype]))
+
+
+@_on_tensors_device
+def pa_beam_select(scores, tokens, parents, logits, cum, finished=None, eos=-1, workspace=None, stream=None):
+    """The K best of beams x vocabulary for every request: logits [groups * beams, vocab] (rows may be
+    strided), cum [groups, beams], finished uint8 [groups, beams]; scores, tokens, parents [groups, K]."""
+    if logits.dtype not in _LOGITS:
+        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    if logits.dim() != 2 or not logits.is_cuda or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be a CUDA tensor [groups * beams, vocab] with contiguous rows")
+    _need(cum, "cum", torch.float32, 2)
+    _need(scores, "scores", torch.float32, 2)
+    _need(tokens, "tokens", torch.int32, 2)
+    _need(parents, "parents", torch.int32, 2)
+    groups, beams = cum.shape
+    rows, vocab = logits.shape
+    K = scores.shape[1]
+    if rows != groups * beams or scores.shape[0] != groups or tokens.shape != scores.shape or \
+            parents.shape != scores.shape:
+        raise ValueError("logits must be [groups * beams, vocab]; scores, tokens and parents [groups, K]")
+    if finished is not None:
+        _need(finished, "finished", torch.uint8, 2)
+        if finished.shape != cum.shape:
+            raise ValueError("finished must be [groups, beams]")
+    stride = vocab if rows == 1 else logits.stride(0)
+    rc = lib().pa_beam_select(_ptr(scores), _ptr(tokens), _ptr(parents), _ptr(logits), _LOGITS[logits.dtype],
+                              stride, _ptr(cum), _ptr(finished), eos, groups, beams, vocab, K, _ptr(workspace),
+                              _space(workspace), _stream(stream))
+    _check("pa_beam_select", rc)
