@@ -687,6 +687,56 @@ int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void 
 size_t pa_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t K,
                                int32_t logits_type);
 
+/*
+ * Rules on the scores of an attention call.  With s = scale * <q, K[t]> for
+ * the query at position pos and head h:
+ *   s <- softcap * tanh(s / softcap)            softcap > 0
+ *   s <- s + alibi_slopes[h] * (t - pos)        alibi_slopes not NULL
+ * and the query sees token t < L when t < prefix_lens[b], or when t <= pos and
+ * (window == 0 or t > pos - window): a sliding window beside which the first tokens
+ * stay seen, and a prefix whose tokens see one another in both directions.
+ */
+typedef struct {
+    float softcap;              /* 0: none; finite, not negative */
+    const float *alibi_slopes;  /* device fp32 [Hq], any values, or NULL */
+    int32_t window;             /* tokens, the query's own among them; 0: all */
+    const int32_t *prefix_lens; /* device int32 [B] or NULL: none */
+    int32_t max_prefix;         /* no prefix_lens[b] is above it (one that is, or is
+                                   negative, sets PA_STATUS_BAD_SEQLEN and is
+                                   clamped); with a window it bounds the partitions */
+} pa_score_rules;
+
+/*
+ * Attention under such rules: pa_decode_mq's (q_len queries per sequence, the
+ * last q_len positions; q_len = 1: pa_decode_splitkv's) arguments and results, and
+ * its supported shapes.  Blocks of which no query of a CTA sees a token are
+ * neither loaded nor looked up, so their table entries may be stale.  A query
+ * that sees no token gives out = 0 and lse = -inf.  num_splits: 0 =
+ * pa_scored_num_splits on the current device, 1 = no split, P > 1 = split with
+ * pa_decode_splitkv's workspace contract for pa_splitkv_workspace_bytes(B * q_len, Hq, D,
+ * P) bytes; the partitions then divide the tokens that can be seen.
+ */
+int pa_decode_scored(void *out, float *lse, const void *q, int32_t q_len, const void *k_cache,
+                     const void *v_cache, pa_cache_desc cache, const int32_t *block_tables,
+                     int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t B, int32_t Hq,
+                     float scale, const pa_score_rules *rules, int32_t num_splits, void *workspace,
+                     size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* pa_decode_scored over FP8 pools, as pa_decode_splitkv_fp8 reads them (head_dim 128 only). */
+int pa_decode_scored_fp8(void *out, float *lse, const void *q, int32_t q_len, const void *k_cache,
+                         const void *v_cache, pa_cache_desc cache, float k_scale, float v_scale,
+                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *seq_lens, int32_t B, int32_t Hq, float scale,
+                         const pa_score_rules *rules, int32_t num_splits, void *workspace,
+                         size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* Split count for pa_decode_scored by the rule of pa_choose_num_splits_mq over
+ * the tokens that can be seen (max_prefix: 0 without prefix_lens); sm_count 0:
+ * the current device's.  P >= 1, or PA_EINVAL / PA_EUNSUPPORTED / PA_ECUDA. */
+int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D,
+                         int32_t max_blocks_per_seq, int32_t block_size, int32_t window,
+                         int32_t max_prefix, int32_t sm_count);
+
 /* Static description of a return code. */
 const char *pa_strerror(int code);
 

@@ -26,8 +26,22 @@ cudaError_t launch_decode_tc_f8(int HC, int GP, int G, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, const DecodeParams &p, int B,
                                 cudaStream_t stream);
 
+// The same kernels with score rules (pa_decode_scored).
+cudaError_t launch_decode_cc_d64_scored(int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                        const DecodeParams &p, int B, cudaStream_t stream);
+cudaError_t launch_decode_cc_d128_scored(int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                         const DecodeParams &p, int B, cudaStream_t stream);
+cudaError_t launch_decode_tc_scored(int HC, int GP, int G, const CUtensorMap &kmap,
+                                    const CUtensorMap &vmap, const DecodeParams &p, int B,
+                                    cudaStream_t stream);
+cudaError_t launch_decode_tc_f8_scored(int HC, int GP, int G, const CUtensorMap &kmap,
+                                       const CUtensorMap &vmap, const DecodeParams &p, int B,
+                                       cudaStream_t stream);
+
 cudaError_t launch_decode_cc(int D, int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                             const DecodeParams &p, int B, cudaStream_t stream) {
+                             const DecodeParams &p, int B, bool scored, cudaStream_t stream) {
+    if (scored && D == 128) return launch_decode_cc_d128_scored(G, kmap, vmap, p, B, stream);
+    if (scored && D == 64) return launch_decode_cc_d64_scored(G, kmap, vmap, p, B, stream);
     if (D == 128) return launch_decode_cc_d128(G, kmap, vmap, p, B, stream);
     if (D == 64) return launch_decode_cc_d64(G, kmap, vmap, p, B, stream);
     return cudaErrorInvalidValue;
@@ -315,6 +329,14 @@ int64_t prefill_tiles(int G, int q_len) {
     return (q_len + qpt - 1) / qpt;
 }
 
+// Query positions of one CTA of a scored call, at most: a prefill tile's, or what
+// the decode kernels hold (FP8 calls run those for any q_len; the larger bound
+// keeps their split count the same).
+int queries_per_cta(int G, int q_len);
+int scored_positions(int G, int q_len) {
+    return prefill_shape(G, q_len) ? std::min(q_len, prefill_positions_per_tile(G)) : queries_per_cta(G, q_len);
+}
+
 // Query positions per tensor-core CTA for q_len queries of G heads each: as
 // many as fit the kernel's column limit (G * positions <= 32).
 int queries_per_cta(int G, int q_len) {
@@ -351,6 +373,15 @@ struct Fp8Scales {
     float k_scale, v_scale;
 };
 
+// Tokens that the queries of one CTA of a scored call can see at most, over
+// every sequence: its virtual tokens (pa_score.cuh).  `positions`: query
+// positions per CTA.
+int64_t scored_tokens(int64_t lmax, int32_t window, int32_t max_prefix, int positions) {
+    if (window <= 0) return lmax;
+    const int64_t seen = round_up(max_prefix, 16) + round_up(static_cast<int64_t>(window) + positions + 14, 16);
+    return std::min(lmax, seen);
+}
+
 // This step's new K/V for the fused write of pa_decode_step (all null: none).
 struct NewTokens {
     const void *k_new = nullptr;
@@ -363,7 +394,8 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
                const int32_t *block_tables, int32_t max_blocks, const int32_t *seq_lens,
                int32_t B, int32_t Hq, float scale, int32_t P, int32_t *status,
                cudaStream_t stream, int32_t *counters = nullptr, const NewTokens &nt = NewTokens(),
-               int32_t q_len = 1, const Fp8Scales *f8 = nullptr, const PassOpts &po = PassOpts()) {
+               int32_t q_len = 1, const Fp8Scales *f8 = nullptr, const PassOpts &po = PassOpts(),
+               const pa_score_rules *rules = nullptr) {
     const int G = Hq / c.num_kv_heads;
     const int qpc = queries_per_cta(G, q_len);
     Kernel k;
@@ -389,6 +421,17 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
          po.part_offset) && k != Kernel::kTensorCore)
         return PA_EUNSUPPORTED;  // cascade passes: tensor cores only
     p.chunk = pa_partition_tokens(max_blocks, c.block_size, P);
+    if (rules) {
+        const int64_t lmax = static_cast<int64_t>(max_blocks) * c.block_size;
+        p.soft_cap = rules->softcap * 1.4426950408889634f;
+        p.inv_cap = rules->softcap > 0.f ? 1.f / p.soft_cap : 0.f;
+        p.slopes = rules->alibi_slopes;
+        p.window = rules->window < lmax ? rules->window : 0;  // (a longer one hides nothing)
+        p.prefix_lens = rules->prefix_lens;
+        p.max_prefix = rules->prefix_lens ? static_cast<int32_t>(std::min<int64_t>(rules->max_prefix, lmax)) : 0;
+        const int64_t seen = scored_tokens(lmax, p.window, p.max_prefix, scored_positions(G, q_len));
+        p.chunk = static_cast<int32_t>(round_up((seen + P - 1) / P, 16));
+    }
     p.counters = counters;
     // (a cluster merges its own P partials only: not a pass that shares its
     // rows' partial slots with another pass)
@@ -412,7 +455,7 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
         rc = make_kv_map_heads(&kmap, k_cache, c, 1);
         if (!rc) rc = make_kv_map_heads(&vmap, v_cache, c, 1);
         if (rc) return rc;
-        e = pa::launch_prefill_tc(kmap, vmap, p, B, G, stream);
+        e = pa::launch_prefill_tc(kmap, vmap, p, B, G, rules != nullptr, stream);
     } else if (k == Kernel::kTensorCore) {
         int HC = 1, GP = 1;
         if (!tc_shape(G * qpc, c.num_kv_heads, &HC, &GP)) return PA_EUNSUPPORTED;
@@ -425,18 +468,20 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
             rc = make_kv_map_fp8(&kmap, k_cache, c, HC);
             if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, c, HC);
             if (rc) return rc;
-            e = pa::launch_decode_tc_f8(HC, GP, G, kmap, vmap, p, B, stream);
+            e = rules ? pa::launch_decode_tc_f8_scored(HC, GP, G, kmap, vmap, p, B, stream)
+                      : pa::launch_decode_tc_f8(HC, GP, G, kmap, vmap, p, B, stream);
         } else {
             rc = make_kv_map_heads(&kmap, k_cache, c, HC);
             if (!rc) rc = make_kv_map_heads(&vmap, v_cache, c, HC);
             if (rc) return rc;
-            e = pa::launch_decode_tc(HC, GP, G, kmap, vmap, p, B, stream);
+            e = rules ? pa::launch_decode_tc_scored(HC, GP, G, kmap, vmap, p, B, stream)
+                      : pa::launch_decode_tc(HC, GP, G, kmap, vmap, p, B, stream);
         }
     } else {
         rc = make_kv_map(&kmap, k_cache, c);
         if (!rc) rc = make_kv_map(&vmap, v_cache, c);
         if (rc) return rc;
-        e = pa::launch_decode_cc(c.head_dim, G, kmap, vmap, p, B, stream);
+        e = pa::launch_decode_cc(c.head_dim, G, kmap, vmap, p, B, rules != nullptr, stream);
     }
     if (e == cudaErrorCooperativeLaunchTooLarge && counters) return PA_ETOOLARGE;
     return e == cudaSuccess ? PA_OK : PA_ECUDA;
@@ -626,6 +671,32 @@ int pa_combine(void *out, float *lse, const float *part_o, const float *part_lse
 }
 
 namespace {
+// Partitions of a scored call: the rule of pa_choose_num_splits_mq over the
+// tokens that it can see, of which there are at least one tile.
+int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_blocks_per_seq,
+                  int32_t block_size, int32_t window, int32_t max_prefix, int sms) {
+    if (window < 0 || max_prefix < 0 || q_len <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq <= 0 ||
+        block_size <= 0 || block_size % 16 != 0)
+        return PA_EINVAL;
+    const int G = Hq / Hkv;
+    Kernel k;
+    int rc = pick_kernel(G * queries_per_cta(G, q_len), D, &k);
+    if (rc) return rc;
+    const int64_t lmax = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    if (lmax > INT32_MAX / 2) return PA_EUNSUPPORTED;
+    const int64_t seen = scored_tokens(lmax, window < lmax ? window : 0, static_cast<int32_t>(std::min<int64_t>(max_prefix, lmax)),
+                                       scored_positions(G, q_len));
+    return pa_choose_num_splits_mq(B, q_len, Hq, Hkv, D, static_cast<int32_t>(round_up(seen, 16) / 16), 16, sms);
+}
+
+int check_rules(const pa_score_rules *r) {
+    if (!r || !(r->softcap >= 0.f) || !std::isfinite(r->softcap) || r->window < 0) return PA_EINVAL;
+    if (r->softcap > 0.f && r->softcap < 1e-30f) return PA_EINVAL;
+    if (r->prefix_lens && r->max_prefix < 0) return PA_EINVAL;
+    if (!aligned(r->alibi_slopes, 4) || !aligned(r->prefix_lens, 4)) return PA_EINVAL;
+    return PA_OK;
+}
+
 // Whether a split call (P partitions) merges its partials in the same launch:
 // its cooperative grid must fit on the GPU at once (sm_count x the kernel's
 // CTAs per SM) and a merge task must hold every partition; the prefill-shaped
@@ -653,7 +724,8 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
                    int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t B, int32_t Hq,
                    float scale, int32_t num_splits, void *workspace, size_t workspace_bytes,
                    int32_t *status, cudaStream_t stream, const NewTokens &nt, int32_t q_len = 1,
-                   const Fp8Scales *f8 = nullptr, bool library_scratch = false) {
+                   const Fp8Scales *f8 = nullptr, bool library_scratch = false,
+                   const pa_score_rules *rules = nullptr) {
     int rc = check_decode_args(q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                                seq_lens, B, Hq, scale);
     if (rc) return rc;
@@ -665,15 +737,17 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
     if (P == 0) {
         const int sms = sm_count_current();
         if (sms <= 0) return PA_ECUDA;
-        P = pa_choose_num_splits_mq(B, q_len, Hq, cache.num_kv_heads, cache.head_dim,
-                                    max_blocks_per_seq, cache.block_size, sms);
+        P = rules ? scored_splits(B, q_len, Hq, cache.num_kv_heads, cache.head_dim, max_blocks_per_seq,
+                                  cache.block_size, rules->window, rules->prefix_lens ? rules->max_prefix : 0, sms)
+                  : pa_choose_num_splits_mq(B, q_len, Hq, cache.num_kv_heads, cache.head_dim,
+                                            max_blocks_per_seq, cache.block_size, sms);
         if (P < 0) return P;
     }
     if (P > 65535) return PA_EUNSUPPORTED;
     if (P == 1)
         return run_decode(false, out, lse, nullptr, nullptr, q, k_cache, v_cache, cache,
                           block_tables, max_blocks_per_seq, seq_lens, B, Hq, scale, 1, status,
-                          stream, nullptr, nt, q_len, f8);
+                          stream, nullptr, nt, q_len, f8, PassOpts(), rules);
     // rows of the partials: (sequence, query position, head)
     const int32_t Bq = B * q_len;
     const size_t need = pa_splitkv_workspace_bytes(Bq, Hq, cache.head_dim, P);
@@ -697,12 +771,12 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
             return PA_ECUDA;
         rc = run_decode(true, out, lse, part_o, part_lse, q, k_cache, v_cache, cache, block_tables,
                         max_blocks_per_seq, seq_lens, B, Hq, scale, P, status, stream, counters, nt,
-                        q_len, f8);
+                        q_len, f8, PassOpts(), rules);
         if (rc != PA_ETOOLARGE) return rc;
     }
     rc = run_decode(true, nullptr, nullptr, part_o, part_lse, q, k_cache, v_cache, cache,
                     block_tables, max_blocks_per_seq, seq_lens, B, Hq, scale, P, status, stream,
-                    nullptr, nt, q_len, f8);
+                    nullptr, nt, q_len, f8, PassOpts(), rules);
     if (rc) return rc;
     cudaError_t e = pa::launch_combine(out, lse, part_o, part_lse, static_cast<int>(Bq * Hq), P,
                                        cache.head_dim, stream);
@@ -735,6 +809,44 @@ int pa_decode_mq(void *out, float *lse, const void *q, int32_t q_len, const void
     return splitkv_common(out, lse, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                           seq_lens, B, Hq, scale, num_splits, workspace, workspace_bytes, status,
                           stream, NewTokens(), q_len);
+}
+
+int pa_decode_scored(void *out, float *lse, const void *q, int32_t q_len, const void *k_cache,
+                     const void *v_cache, pa_cache_desc cache, const int32_t *block_tables,
+                     int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t B, int32_t Hq,
+                     float scale, const pa_score_rules *rules, int32_t num_splits, void *workspace,
+                     size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
+    if (q_len < 1 || q_len > 65535) return PA_EINVAL;
+    const int rc = check_rules(rules);
+    if (rc) return rc;
+    return splitkv_common(out, lse, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                          seq_lens, B, Hq, scale, num_splits, workspace, workspace_bytes, status,
+                          stream, NewTokens(), q_len, nullptr, false, rules);
+}
+
+int pa_decode_scored_fp8(void *out, float *lse, const void *q, int32_t q_len, const void *k_cache,
+                         const void *v_cache, pa_cache_desc cache, float k_scale, float v_scale,
+                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *seq_lens, int32_t B, int32_t Hq, float scale,
+                         const pa_score_rules *rules, int32_t num_splits, void *workspace,
+                         size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
+    if (q_len < 1 || q_len > 65535) return PA_EINVAL;
+    if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+        return PA_EINVAL;
+    const int rc = check_rules(rules);
+    if (rc) return rc;
+    const Fp8Scales f8{k_scale, v_scale};
+    return splitkv_common(out, lse, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                          seq_lens, B, Hq, scale, num_splits, workspace, workspace_bytes, status,
+                          stream, NewTokens(), q_len, &f8, false, rules);
+}
+
+int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D,
+                         int32_t max_blocks_per_seq, int32_t block_size, int32_t window,
+                         int32_t max_prefix, int32_t sm_count) {
+    const int sms = sm_count > 0 ? sm_count : sm_count == 0 ? sm_count_current() : 0;
+    if (sms <= 0) return sm_count < 0 ? PA_EINVAL : PA_ECUDA;
+    return scored_splits(B, q_len, Hq, Hkv, D, max_blocks_per_seq, block_size, window, max_prefix, sms);
 }
 
 int pa_cache_write_fp8(const void *k_new, const void *v_new, const int64_t *slot_mapping,

@@ -28,6 +28,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_score.cuh"
 #include "pa_split_merge.cuh"
 
 namespace pa {
@@ -53,7 +54,7 @@ struct CcCfg {
     static constexpr int kDPV = D / 32;                         // output dims per lane
 };
 
-template <int D, int G, int NW, int NST>
+template <int D, int G, int NW, int NST, bool SC>
 __global__ void __launch_bounds__(NW * 32)
 decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const DecodeParams p) {
@@ -76,7 +77,10 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         L = L < 0 ? 0 : lmax;
     }
     const int t_begin = part * p.chunk;
-    const int t_end = min(t_begin + p.chunk, L);
+    Seen sn{};  // SC: the partition counts virtual tokens, sn.real() of which are read
+    if constexpr (SC) sn = seen_by(p, b, L, L - 1, 1, tid == 0 && part == 0 && g == 0);
+    auto real = [&](int t) { return SC ? sn.real(t) : t; };
+    const int t_end = min(t_begin + p.chunk, SC ? sn.end : L);
     const int ntiles = t_end > t_begin ? (t_end - t_begin + kTile - 1) / kTile : 0;
     const int32_t *bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
 
@@ -103,12 +107,12 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const uint64_t policy = l2_evict_first_policy();
 
     auto tile_phys = [&](int j) -> int {  // physical block of this warp's j-th tile
-        const int tok0 = t_begin + (warp + j * NW) * kTile;
+        const int tok0 = real(t_begin + (warp + j * NW) * kTile);
         return bt[tok0 / bs];
     };
     auto issue = [&](int j) {  // lane 0 only
         const int s = j % NST;
-        const int tok0 = t_begin + (warp + j * NW) * kTile;
+        const int tok0 = real(t_begin + (warp + j * NW) * kTile);
         const int phys = bt[tok0 / bs];
         if (phys < 0 || phys >= p.num_blocks) {
             set_status(p.status, PA_STATUS_BAD_BLOCK);
@@ -159,6 +163,11 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (lane == 0) issue(issued);
     }
 
+    float slope[SC ? G : 1];  // in log2 units
+    if constexpr (SC) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) slope[h] = p.slopes ? p.slopes[g * G + h] * 1.4426950408889634f : 0.f;
+    }
     float m_run[G], l_run[G], o[G][C::kDPV];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
@@ -222,12 +231,25 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 }
             }
             float sc[G], alpha[G];
-            const bool live = t < nvalid;
+            const int tok = real(tok0);   // the tile's first token
+            const bool live = t < nvalid && (!SC || sn.any(tok + t));
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 float v = acc0[h] + acc1[h];
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 sc[h] = live ? v : -INFINITY;
+            }
+            if constexpr (SC) {  // the rules, on finite values (a token not seen may hold anything)
+                if (p.soft_cap > 0.f) {
+#pragma unroll
+                    for (int h = 0; h < G; ++h) sc[h] = live ? sc[h] : 0.f;
+                    cap_scores<G>(sc, p.inv_cap, p.soft_cap);
+                }
+#pragma unroll
+                for (int h = 0; h < G; ++h) {
+                    if (p.slopes) sc[h] = fmaf(slope[h], static_cast<float>(tok + t - (L - 1)), sc[h]);
+                    sc[h] = live ? sc[h] : -INFINITY;
+                }
             }
             // ---- online softmax over the 16 tokens (lanes 16..31 mirror 0..15)
 #pragma unroll
@@ -238,9 +260,11 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
                 mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
                 const float m_new = fmaxf(m_run[h], mt);
-                alpha[h] = fast_exp2(m_run[h] - m_new);
+                // (SC: a warp's first tiles may hold no token that is seen)
+                const float m_sub = SC && m_new == -INFINITY ? 0.f : m_new;
+                alpha[h] = fast_exp2(m_run[h] - m_sub);
                 m_run[h] = m_new;
-                const float pv = fast_exp2(sc[h] - m_new);
+                const float pv = fast_exp2(sc[h] - m_sub);
                 sc[h] = pv;
                 float lt = pv;
                 lt += __shfl_xor_sync(0xffffffffu, lt, 1);
@@ -269,6 +293,7 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 for (int k = 0; k < C::kDPV; ++k) o[h][k] *= alpha[h];
             const uint8_t *vrow = vt + pv_sub * kTile * kSubBytes + pv_byte;
             for (int tt = 0; tt < nvalid; ++tt) {
+                if (SC && !sn.any(tok + tt)) continue;
                 float vv[C::kDPV];
                 if constexpr (C::kDPV == 4) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(vrow + swz128(tt, pv_chunk));
@@ -378,13 +403,13 @@ cudaError_t ensure_smem_attr(std::atomic<uint64_t> &done, Kernel kern, int bytes
     return e;
 }
 
-template <int D, int G>
+template <int D, int G, bool SC = false>
 cudaError_t launch_cc_instance(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                const DecodeParams &p, int B, cudaStream_t stream) {
     constexpr int NW = 4;
     constexpr int NST = (D == 128) ? 3 : 4;
     using C = CcCfg<D, G, NW, NST>;
-    auto kern = decode_cc_kernel<D, G, NW, NST>;
+    auto kern = decode_cc_kernel<D, G, NW, NST, SC>;
     static std::atomic<uint64_t> smem_attr_done{0};
     cudaError_t e = ensure_smem_attr(smem_attr_done, kern, C::kSmemBytes);
     if (e != cudaSuccess) return e;

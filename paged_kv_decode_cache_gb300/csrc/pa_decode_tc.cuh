@@ -77,6 +77,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_score.cuh"
 #include "pa_split_merge.cuh"
 #include "pa_tcgen05.cuh"
 
@@ -99,7 +100,7 @@ constexpr int kTcSmemLimit = 227 * 1024;
 // to the 1024-byte swizzle-atom boundary
 constexpr int kAlignSlack = 1024 - 16;
 
-template <int HC, int GP, bool F8 = false>
+template <int HC, int GP, bool F8 = false, bool SC = false>
 struct TcCfg {
     static constexpr int kN = HC * GP;                          // MMA N
     // FP8 converter warps: 8 (warps 8-11 widen K, 12-15 V) where the softmax
@@ -132,7 +133,8 @@ struct TcCfg {
     // TMEM slot, merge ticket.  Thread t writes its row t of red, so rows are
     // GP + 1 floats apart where that fits (a warp's stores then fall in 32
     // different banks; GP apart they share 32 / GP banks).
-    static constexpr int red_bytes(int gpr) { return (kTcRows * gpr + 4 * kN) * 4 + 16; }
+    // SC: also every column's distance slope and position.
+    static constexpr int red_bytes(int gpr) { return (kTcRows * gpr + (SC ? 6 : 4) * kN) * 4 + 16; }
     // S buffers in TMEM (FP8 pools with N >= 32 keep 2, to leave room for the
     // widened operands: three buffers of each at N = 32 beat 4 S buffers and
     // two of each, 17.3 against 17.5 us on the 7B layer)
@@ -271,12 +273,12 @@ __host__ __device__ constexpr int vt_row_k(int m) {
     return (m & ~15) | (((m >> 1) & 3) << 2) | (((m >> 3) & 1) << 1) | (m & 1);
 }
 
-template <int HC, int GP, bool F8>
-__global__ void __launch_bounds__((TcCfg<HC, GP, F8>::kThreads), 1)
+template <int HC, int GP, bool F8, bool SC>
+__global__ void __launch_bounds__((TcCfg<HC, GP, F8, SC>::kThreads), 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const DecodeParams p, int G) {
     constexpr int D = 128;
-    using C = TcCfg<HC, GP, F8>;
+    using C = TcCfg<HC, GP, F8, SC>;
     constexpr int kThreads = C::kThreads;
     constexpr int N = C::kN, NK = C::kNK, NV = C::kNV, NBP = C::kNBP, NBS = C::kNBS;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -294,6 +296,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     volatile int *abort_flag = reinterpret_cast<volatile int *>(alpha_s + 2 * N);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(alpha_s + 2 * N + 1);
     int *ticket = reinterpret_cast<int *>(alpha_s + 2 * N + 2);
+    float *slope_s = alpha_s + 2 * N + 4;                            // SC: [N] slopes, log2 units
+    int *pos_s = reinterpret_cast<int *>(slope_s + N);               // SC: [N] positions
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
     uint64_t *kfull = bars, *kempty = bars + NK, *vfull = bars + 2 * NK, *vempty = vfull + NV;
     uint64_t *sdone = vempty + NV, *sfree = sdone + NBS, *pready = sfree + NBS;
@@ -333,12 +337,20 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             const int lp = p.seq_len_const >= 0 ? p.seq_len_const
                                                 : *reinterpret_cast<const volatile int32_t *>(p.seq_lens + bz) -
                                                       p.seq_len_offset;
-            const int lim = min(t0 + p.chunk, min(lp, p.max_blocks * p.block_size));
+            int lim = min(t0 + p.chunk, min(lp, p.max_blocks * p.block_size));
+            int place = tok;  // its real place in the sequence
+            if constexpr (SC) {
+                const int lc = max(0, min(lp, p.max_blocks * p.block_size));
+                const int q0 = static_cast<int>(blockIdx.y / p.head_groups) * p.q_per_cta;
+                const Seen sn = seen_by(p, bz, lc, lc - p.q_len + q0, min(p.q_per_cta, p.q_len - q0), false);
+                lim = min(t0 + p.chunk, sn.end);
+                place = sn.real(tok);
+            }
             if (tok < lim) {
                 const int phys = *reinterpret_cast<const volatile int32_t *>(
-                    p.block_tables + static_cast<int64_t>(bz) * p.table_stride + tok / p.block_size);
+                    p.block_tables + static_cast<int64_t>(bz) * p.table_stride + place / p.block_size);
                 if (phys >= 0 && phys < p.num_blocks) {
-                    const int row = phys * p.block_size + tok % p.block_size;
+                    const int row = phys * p.block_size + place % p.block_size;
                     if constexpr (F8) {
                         tma_prefetch_3d(&kmap, 0, row, hg0);
                         tma_prefetch_3d(&vmap, 0, row, hg0);
@@ -398,12 +410,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int tile = lane >> 1, sub = lane & 1;
     const bool carrier = producer && lane < 2 * C::kTiles;
     int *my_look = look_ring + (is_v ? (kTcLook + 1) * 32 : 0) + lane;  // slot j at my_look[32 * j]
+    Seen sn{};  // SC: the partition counts virtual tokens, sn.real() of which are read
+    auto real = [&](int t) { return SC ? sn.real(t) : t; };
     auto look_ahead = [&](int c, int t_stop) {  // copy chunk c's block id; one commit group per chunk
         const int tok0 = t_begin + c * C::kT + tile * kTile;
-        if (carrier && tok0 < t_stop) cp_async_4(my_look + 32 * (c % (kTcLook + 1)), bt + tok0 / bs);
+        if (carrier && tok0 < t_stop) cp_async_4(my_look + 32 * (c % (kTcLook + 1)), bt + real(tok0) / bs);
         cp_async_commit();
     };
-    if (producer) {
+    if (producer && !SC) {
 #pragma unroll
         for (int c = 0; c < kTcLook; ++c) look_ahead(c, t_lim);
     }
@@ -433,7 +447,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // (causal); no key past this CTA's last query is read.  Non-causal
     // (cascade prefix pass): every query sees all L keys.
     const int qbase = p.causal ? L - p.q_len + qi0 : L;
-    const int t_end = min(t_begin + p.chunk, max(0, min(L, p.causal ? qbase + nq : L)));
+    if constexpr (SC) sn = seen_by(p, b, L, qbase, nq, tid == 0 && part == 0 && g0 == 0);
+    const int t_end = min(t_begin + p.chunk, SC ? sn.end : max(0, min(L, p.causal ? qbase + nq : L)));
+    if (producer && SC) {  // (a token's place depends on the length)
+#pragma unroll
+        for (int c = 0; c < kTcLook; ++c) look_ahead(c, t_end);
+    }
     const int nch = t_end > t_begin ? (t_end - t_begin + C::kT - 1) / C::kT : 0;
 
     if (nch == 0) {  // empty range: zero output, lse = -inf
@@ -557,13 +576,13 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 __syncwarp();
                 if (valid && sub == 0)
                     tma_load_3d(ring + s * C::kStageBytes + tile * C::kBoxBytes, map, 0,
-                                phys * bs + tok0 % bs, g0, &full[s], policy);
+                                phys * bs + real(tok0) % bs, g0, &full[s], policy);
             } else {
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(__popc(vm)) * C::kBoxBytes);
                 __syncwarp();
                 if (valid)
                     tma_load_4d(ring + s * C::kStageBytes + sub * C::kSubTile + tile * C::kBoxBytes, map, 0,
-                                phys * bs + tok0 % bs, g0, sub, &full[s], policy);
+                                phys * bs + real(tok0) % bs, g0, sub, &full[s], policy);
             }
             issued = c + 1;
         }
@@ -608,6 +627,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         *abort_flag = 0;
     }
     if (tid < N) m_ref[tid] = -INFINITY;
+    if (SC && tid < N) {
+        const int hh = tid / GP, c = tid % GP;
+        slope_s[tid] = p.slopes && c < Gq ? p.slopes[(g0 + hh) * G + c % G] * 1.4426950408889634f : 0.f;
+        pos_s[tid] = qbase + c / G;
+    }
 #pragma unroll
     for (int j = 0; j < kQLoads; ++j) {  // Q operand row n = (head', q), 16-byte chunk c
         const int i = tid + j * kThreads, n = i / (D / 8), c = i % (D / 8);
@@ -783,7 +807,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             const uint32_t vm = static_cast<uint32_t>(mk);
             const int tok_c = t_begin + c * C::kT;
             constexpr uint32_t kAllTiles = 0x55555555u & ((1u << (2 * C::kTiles)) - 1u);
-            const bool whole = (vm & kAllTiles) == kAllTiles && tok_c + C::kT <= t_end;
+            // (SC: all of it in the prefix, or none of it before the window)
+            const bool whole = (vm & kAllTiles) == kAllTiles && tok_c + C::kT <= t_end &&
+                               (!SC || tok_c + C::kT <= sn.prefix || real(tok_c) >= sn.start);
             // pass u: dims 16 dc .. 16 dc + 15 (dc = 2 q4 + u); load k takes row groups
             // g = 2 k, 2 k + 1, lane t giving the address of row t % 8 of matrix
             // t / 8 = 2 (g - 2 k) + h (rows 16 g + 8 h .. + 7)
@@ -808,8 +834,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                             const int tl = (2 * k + gg) / HC;
                             const bool tile_ok = (vm >> (2 * tl)) & 1u;
                             const int r0 = tok_c + tl * kTile + 2 * (lane & 3);
-                            ka = (tile_ok && r0 < t_end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 1 < t_end ? 0xffff0000u : 0u);
-                            kb = (tile_ok && r0 + 8 < t_end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 9 < t_end ? 0xffff0000u : 0u);
+                            auto seen = [&](int r) { return tile_ok && r < t_end && (!SC || sn.any(real(r))); };
+                            ka = (seen(r0) ? 0x0000ffffu : 0u) | (seen(r0 + 1) ? 0xffff0000u : 0u);
+                            kb = (seen(r0 + 8) ? 0x0000ffffu : 0u) | (seen(r0 + 9) ? 0xffff0000u : 0u);
                         }
                         // repetition g = 2 k + gg of the store: columns 8 g + 2 (t % 4) (+ 1)
                         w[8 * k + 4 * gg + 0] = a.x & ka;  // dim 2 (t / 4): lane t / 4, rows of h = 0
@@ -899,15 +926,32 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tc5::fence_before_sync();
             __syncwarp();  // (one arrival per warp, once all its lanes have read)
             if (lane == 0) mbar_arrive(&sfree[sbuf]);  // S buffer read: QK c + NBS may overwrite it
-            const bool valid = ok && in_pool;
+            const int tok = real(t_begin + c * C::kT + my_tok);  // this row's token
+            const bool valid = ok && in_pool && (!SC || sn.any(tok));
             // causal: column q (query qi0 + q / G) sees this row's token only if
-            // the token is not past the query's position
-            const int cmin = max(0, t_begin + c * C::kT + my_tok - qbase) * G;
+            // the token is not past the query's position (SC: and not before its window,
+            // unless it is in the prefix)
+            int cmin = max(0, tok - qbase) * G;
+            int cmax = Gq;
+            if constexpr (SC) {
+                if (tok < sn.prefix) cmin = 0;
+                else if (p.window > 0) cmax = min(nq, max(0, tok + p.window - qbase)) * G;
+            }
             float sc[GP];
             bool over = false;
+            if constexpr (SC) {  // the rules, on finite values (a row not seen may hold anything)
+#pragma unroll
+                for (int q = 0; q < GP; ++q) sc[q] = valid ? sv[q] * sl2 : 0.f;
+                if (p.soft_cap > 0.f) cap_scores<GP>(sc, p.inv_cap, p.soft_cap);
+                if (p.slopes) {
+#pragma unroll
+                    for (int q = 0; q < GP; ++q)
+                        sc[q] = fmaf(slope_s[my_head * GP + q], static_cast<float>(tok - pos_s[my_head * GP + q]), sc[q]);
+                }
+            }
 #pragma unroll
             for (int q = 0; q < GP; ++q) {
-                sc[q] = (valid && q < Gq && q >= cmin) ? sv[q] * sl2 : -INFINITY;
+                sc[q] = (valid && q < cmax && q >= cmin) ? (SC ? sc[q] : sv[q] * sl2) : -INFINITY;
                 over |= sc[q] > mr[q] + kTcLazyTau;
             }
             // one vote per chunk: does any reference max have to move (or is the CTA aborting)?
@@ -1111,11 +1155,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                                               reinterpret_cast<float *>(ps));
 }
 
-template <int HC, int GP, bool F8>
+template <int HC, int GP, bool F8, bool SC = false>
 cudaError_t launch_tc_instance(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                const DecodeParams &p, int B, int G, cudaStream_t stream) {
-    using C = TcCfg<HC, GP, F8>;
-    auto kern = decode_tc_kernel<HC, GP, F8>;
+    using C = TcCfg<HC, GP, F8, SC>;
+    auto kern = decode_tc_kernel<HC, GP, F8, SC>;
     static std::atomic<uint64_t> smem_attr_done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -84,17 +84,28 @@ struct DecodeParams {
     int32_t part_stride;
     int32_t part_offset;
     int32_t table_stride;   // entries between block-table rows (>= max_blocks)
+    // Score rules (pa_decode_scored; the kernels' SC instances): scores in log2
+    // units, soft_cap = cap * log2(e) (0: none), inv_cap its reciprocal; slopes
+    // fp32 [Hq] or null; window tokens back, 0: all; the first prefix_lens[b]
+    // (at most max_prefix) tokens seen by every query.  The partitions then
+    // count virtual tokens (pa_score.cuh).
+    float soft_cap;
+    float inv_cap;
+    const float *slopes;
+    int32_t window;
+    const int32_t *prefix_lens;
+    int32_t max_prefix;
 };
 
 // CUDA-core decode kernel launch (pa_decode_cc_d*.cu).  Returns a cudaError_t.
 cudaError_t launch_decode_cc(int D, int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                             const DecodeParams &p, int B, cudaStream_t stream);
+                             const DecodeParams &p, int B, bool scored, cudaStream_t stream);
 
 // Prefill-shaped multi-query kernel (pa_prefill_tc.cu): grid (num_splits,
 // query tiles x Hkv, B); p.q_per_cta query positions per tile; writes out/lse,
 // or fp32 partials when p.split (no in-launch merge).
 cudaError_t launch_prefill_tc(const CUtensorMap &kmap, const CUtensorMap &vmap, const DecodeParams &p,
-                              int B, int G, cudaStream_t stream);
+                              int B, int G, bool scored, cudaStream_t stream);
 
 cudaError_t launch_combine(void *out, float *lse, const float *part_o, const float *part_lse,
                            int rows, int P, int D, cudaStream_t stream);

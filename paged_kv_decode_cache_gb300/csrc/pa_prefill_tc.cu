@@ -39,6 +39,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_score.cuh"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
@@ -79,6 +80,7 @@ static_assert(kPfSmemBytes <= 227 * 1024, "shared memory");
 static_assert(kPfNP * kPfPBuf >= kPfRows * 128 * 4, "the epilogue stages fp32 rows in the P buffers");
 static_assert(kPfStage % 1024 == 0 && kPfQHalf % 1024 == 0 && kPfPPart % 1024 == 0, "swizzle atoms");
 
+template <bool SC>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const DecodeParams p, int G) {
@@ -121,7 +123,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // Query qi0 + k sits at position qbase + k and sees keys up to it (causal);
     // without the causal rule every query sees all L keys.
     const int qbase = L - p.q_len + qi0;
-    const int t_stop = p.causal ? min(L, qbase + nq) : L;
+    Seen sn{};  // SC: the partition counts virtual tokens, sn.real() of which are read
+    if constexpr (SC) sn = seen_by(p, b, L, qbase, nq, tid == 0 && part == 0 && blockIdx.y == 0);
+    auto real = [&](int t) { return SC ? sn.real(t) : t; };
+    const int t_stop = SC ? sn.end : p.causal ? min(L, qbase + nq) : L;
     const int t_begin = part * p.chunk;
     const int t_end = min(t_begin + p.chunk, max(0, t_stop));
     const int nch = t_end > t_begin ? (t_end - t_begin + kPfT - 1) / kPfT : 0;
@@ -146,7 +151,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int ntiles = (t_end - t_begin + kTile - 1) / kTile;  // <= kPrefillMaxTiles (host)
     const int32_t *bt = p.block_tables + static_cast<int64_t>(b) * p.table_stride;
     for (int i = tid; i < ntiles; i += kPfThreads) {
-        const int tok = t_begin + i * kTile;
+        const int tok = real(t_begin + i * kTile);
         const int phys = bt[tok / bs];
         int row = -1;
         if (phys >= 0 && phys < p.num_blocks) row = phys * bs + tok % bs;
@@ -299,6 +304,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const uint32_t ocol = tmem + kPfColO + grp * 128;   // this group's O
         uint8_t *prow = ps + grp * kPfPBuf + r * kSubBytes;   // this group's P row r
         float m_ref = -INFINITY, l = 0.f;
+        const float slope = SC && p.slopes && row_ok ? p.slopes[g * G + r % G] * 1.4426950408889634f : 0.f;
         for (int c = grp; c < nch; c += 2) {
             const bool ok = __all_sync(0xffffffffu, wait_or_abort(&sdone[grp], (c / 2) & 1));
             float sv[kPfT];
@@ -328,9 +334,42 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             // Most chunks are seen whole by every row of the warp: no mask then.
             const int tok_last = tok0 + kPfT - 1;
-            const bool whole = __all_sync(0xffffffffu, row_ok && all_tiles && tok_last < t_end && tok_last <= pos);
+            const int real_last = real(tok_last);
+            const int oldest = SC && p.window > 0 ? pos - p.window + 1 : 0;  // the first token of the row's window
+            const bool whole = __all_sync(
+                0xffffffffu, row_ok && all_tiles && tok_last < t_end &&
+                                 ((real_last <= pos && real(tok0) >= oldest) || (SC && tok_last < sn.prefix)));
             float mx = -INFINITY;
-            if (whole) {
+            if constexpr (SC) {  // the rules, on finite values (a token not seen may hold anything)
+#pragma unroll
+                for (int k = 0; k < kPfT; ++k) {
+                    const int t = real(tok0 + k / kTile * kTile) + k % kTile;
+                    const bool valid = whole || (row_ok && tile_ok[k / kTile] && tok0 + k < t_end &&
+                                                 (t < sn.prefix || (t <= pos && t >= oldest)));
+                    sv[k] = valid ? sv[k] * sl2 : -INFINITY;
+                }
+                if (p.soft_cap > 0.f) {
+                    uint32_t hidden[2] = {0u, 0u};
+#pragma unroll
+                    for (int k = 0; k < kPfT; ++k) {
+                        hidden[k / 32] |= static_cast<uint32_t>(sv[k] == -INFINITY) << (k % 32);
+                        sv[k] = sv[k] == -INFINITY ? 0.f : sv[k];
+                    }
+                    cap_scores<kPfT>(sv, p.inv_cap, p.soft_cap);
+#pragma unroll
+                    for (int k = 0; k < kPfT; ++k)
+                        if (hidden[k / 32] >> (k % 32) & 1u) sv[k] = -INFINITY;
+                }
+                if (p.slopes) {
+#pragma unroll
+                    for (int k = 0; k < kPfT; ++k) {
+                        const int t = real(tok0 + k / kTile * kTile) + k % kTile;
+                        sv[k] = fmaf(slope, static_cast<float>(t - pos), sv[k]);  // (-inf stays)
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kPfT; ++k) mx = fmaxf(mx, sv[k]);
+            } else if (whole) {
 #pragma unroll
                 for (int k = 0; k < kPfT; ++k) {
                     sv[k] *= sl2;
@@ -405,7 +444,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // the V stage is in chunk c's phase: PV c - 2 has finished, and the
             // one PV issuer works in chunk order, so PV c - 3, the stage's
             // previous user, was issued before it.)
-            if (c == nch - 1) {
+            // (SC: so are rows of its tiles that no query of the tile sees.)
+            if (SC && !(tok_last < sn.prefix || (real(tok0) >= sn.start && real_last < sn.stop))) {
+                if (wait_or_abort(&vfull[c % kPfNV], (c / kPfNV) & 1)) {
+                    uint8_t *vt = vring + (c % kPfNV) * kPfStage;
+                    for (int i = r; i < kPfT * 16; i += kPfRows) {
+                        const int row = i / 16, hc = i % 16;
+                        if (tok0 + row < t_end && sn.any(real(tok0 + row))) continue;
+                        *reinterpret_cast<uint4 *>(vt + (hc >> 3) * kPfHalf + swz128(row, hc & 7)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+            } else if (c == nch - 1) {
                 const int z0 = t_end - tok0;
                 const int z1 = min(kPfT, (t_end + kTile - 1) / kTile * kTile - tok0);
                 if (z1 > z0 && wait_or_abort(&vfull[c % kPfNV], (c / kPfNV) & 1)) {
@@ -501,23 +551,31 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
 }  // namespace
 
-cudaError_t launch_prefill_tc(const CUtensorMap &kmap, const CUtensorMap &vmap, const DecodeParams &p,
-                              int B, int G, cudaStream_t stream) {
+namespace {
+template <bool SC>
+cudaError_t launch_prefill(const CUtensorMap &kmap, const CUtensorMap &vmap, const DecodeParams &p, int B, int G,
+                           cudaStream_t stream) {
     static std::atomic<uint64_t> smem_attr_done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(prefill_tc_kernel<SC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kPfSmemBytes);
         if (e != cudaSuccess) return e;
         smem_attr_done.fetch_or(bit, std::memory_order_release);
     }
     const int qtiles = (p.q_len + p.q_per_cta - 1) / p.q_per_cta;
     const dim3 grid(p.num_splits, qtiles * p.num_kv_heads, B);
-    return launch_maybe_cooperative(prefill_tc_kernel, grid, kPfThreads, kPfSmemBytes, stream, false,
+    return launch_maybe_cooperative(prefill_tc_kernel<SC>, grid, kPfThreads, kPfSmemBytes, stream, false,
                                     p.pdl != 0, kmap, vmap, p, G);
+}
+}  // namespace
+
+cudaError_t launch_prefill_tc(const CUtensorMap &kmap, const CUtensorMap &vmap, const DecodeParams &p,
+                              int B, int G, bool scored, cudaStream_t stream) {
+    return scored ? launch_prefill<true>(kmap, vmap, p, B, G, stream) : launch_prefill<false>(kmap, vmap, p, B, G, stream);
 }
 
 }  // namespace pa

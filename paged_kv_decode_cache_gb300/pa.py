@@ -61,6 +61,12 @@ class RopeScaling(ctypes.Structure):
                 ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 
+class ScoreRules(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int32), ("prefix_lens", ctypes.c_void_p),
+                ("max_prefix", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -112,6 +118,11 @@ _SIGNATURES = {
     "pa_beam_select": ([_P, _P, _P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P],
                        ctypes.c_int),
     "pa_beam_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "pa_decode_scored": ([_P, _P, _P, _I32, _P, _P, CacheDesc, _P, _I32, _P, _I32, _I32, _F32, _P, _I32,
+                          _P, _SZ, _P, _P], ctypes.c_int),
+    "pa_decode_scored_fp8": ([_P, _P, _P, _I32, _P, _P, CacheDesc, _F32, _F32, _P, _I32, _P, _I32, _I32,
+                              _F32, _P, _I32, _P, _SZ, _P, _P], ctypes.c_int),
+    "pa_scored_num_splits": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], ctypes.c_int),
     "pa_set_option": ([_I32, _I32], ctypes.c_int),
     "pa_get_option": ([_I32], ctypes.c_int),
     "pa_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -788,3 +799,78 @@ def pa_beam_select(scores, tokens, parents, logits, cum, finished=None, eos=-1, 
                               stride, _ptr(cum), _ptr(finished), eos, groups, beams, vocab, K, _ptr(workspace),
                               _space(workspace), _stream(stream))
     _check("pa_beam_select", rc)
+
+
+def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
+                         block_size: int, window: int = 0, max_prefix: int = 0, sm_count: int = 0) -> int:
+    r = lib().pa_scored_num_splits(B, q_len, Hq, Hkv, D, max_blocks_per_seq, block_size, window, max_prefix,
+                                   sm_count)
+    _check("pa_scored_num_splits", min(r, 0))
+    return r
+
+
+def _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap, alibi_slopes, window,
+                   prefix_lens, max_prefix):
+    """(q_len, B, Hq, rules) of a scored call; q is [B, Hq, D] or [B, q_len, Hq, D]."""
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {tuple(q.shape)}")
+    _need(q, "q", torch.bfloat16, q.dim())
+    _need(out, "out", torch.bfloat16, q.dim())
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    q_len = q.shape[1] if q.dim() == 4 else 1
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[3] != D or \
+            block_tables.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("inconsistent out / q / cache / table shapes")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, q.dim() - 1)
+        if lse.shape != q.shape[:-1]:
+            raise ValueError("lse must have q's shape without its last dimension")
+    if alibi_slopes is not None:
+        _need(alibi_slopes, "alibi_slopes", torch.float32, 1)
+        if alibi_slopes.shape[0] != Hq:
+            raise ValueError("alibi_slopes must be [Hq]")
+    if prefix_lens is not None:
+        _need(prefix_lens, "prefix_lens", torch.int32, 1)
+        if prefix_lens.shape[0] != B:
+            raise ValueError("prefix_lens must be [B]")
+        if max_prefix is None:
+            max_prefix = block_tables.shape[1] * k_cache.shape[1]
+    return q_len, B, Hq, ScoreRules(softcap, None if alibi_slopes is None else alibi_slopes.data_ptr(), window,
+                                    None if prefix_lens is None else prefix_lens.data_ptr(), max_prefix or 0)
+
+
+@_on_tensors_device
+def pa_decode_scored(out, lse, q, k_cache, v_cache, block_tables, seq_lens, scale, softcap=0.0,
+                     alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None, num_splits=0,
+                     workspace=None, status=None, stream=None):
+    """Split-KV decode (q [B, Hq, D]) or causal multi-query decode (q [B, q_len, Hq, D]) with capped
+    scores, a distance bias, a sliding window and a prefix that every query sees.  max_prefix: a bound
+    on prefix_lens (default: the table's tokens)."""
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    q_len, B, Hq, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
+                                         alibi_slopes, window, prefix_lens, max_prefix)
+    rc = lib().pa_decode_scored(_ptr(out), _ptr(lse), _ptr(q), q_len, _ptr(k_cache), _ptr(v_cache),
+                                cache_desc(k_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
+                                B, Hq, scale, ctypes.byref(rules), num_splits, _ptr(workspace),
+                                _space(workspace), _ptr(status), _stream(stream))
+    _check("pa_decode_scored", rc)
+
+
+@_on_tensors_device
+def pa_decode_scored_fp8(out, lse, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
+                         softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None,
+                         num_splits=0, workspace=None, status=None, stream=None):
+    """pa_decode_scored over uint8 e4m3 pools with per-pool scales."""
+    _need_pool8(k_cache, "k_cache")
+    _need_pool8(v_cache, "v_cache")
+    q_len, B, Hq, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
+                                         alibi_slopes, window, prefix_lens, max_prefix)
+    rc = lib().pa_decode_scored_fp8(_ptr(out), _ptr(lse), _ptr(q), q_len, _ptr(k_cache), _ptr(v_cache),
+                                    cache_desc(k_cache), k_scale, v_scale, _ptr(block_tables),
+                                    block_tables.shape[1], _ptr(seq_lens), B, Hq, scale, ctypes.byref(rules),
+                                    num_splits, _ptr(workspace), _space(workspace), _ptr(status),
+                                    _stream(stream))
+    _check("pa_decode_scored_fp8", rc)
