@@ -27,107 +27,132 @@ struct RopeArgs {
     int64_t q_out_stride, q_stride, k_stride, v_stride;
     const int32_t *positions;
     const int64_t *slots;
-    int64_t n_slots;
+    int64_t n, n_slots;
     uint8_t *k_cache, *v_cache;
     int32_t *status;
     int hq, hkv, head_dim;
     float k_scale, v_scale;        // FP8 pools
 };
 
-// One CTA per token; thread = one unit of 16 elements of one head of q, k or
-// v.  In either layout unit u < rot_dim / 16 holds the pairs 8 u .. 8 u + 7: two
-// chunks rot_dim / 2 apart (half layout), or 16 elements in a row
+// Thread = one unit of 16 elements of one head of q, k or v, for the TB tokens of
+// its CTA.  In either layout unit u < rot_dim / 16 holds the pairs 8 u .. 8 u + 7:
+// two chunks rot_dim / 2 apart (half layout), or 16 elements in a row
 // (interleaved).  A warp then reads and writes whole 128-byte lines.  The
-// token's rot_dim / 2 angles are computed once, by as many threads, while the
-// loads are in flight.
-template <bool F8>
+// tokens' angles are computed once per CTA, one per thread at a time, while the
+// first loads (up to 4 tokens of each unit) are in flight.
+template <bool F8, int TB>
 __global__ void __launch_bounds__(kMaxThreads)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
-    __shared__ float2 turn[PA_ROPE_MAX_PAIRS];  // (cos, sin) of the token's pairs
+    constexpr int kAhead = TB < 4 ? TB : 4;                   // tokens loaded at once
+    __shared__ float2 turn[TB][PA_ROPE_MAX_PAIRS];            // (cos, sin) of the tokens' pairs
+    __shared__ int64_t slot_s[TB];                            // -1: not written
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t tok = blockIdx.x;
-    const int units = a.head_dim / kUnit, rot_units = rope.rot_dim / kUnit;
+    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TB;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(TB), a.n - tok0));
+    const int units = a.head_dim / kUnit, rot_units = rope.rot_dim / kUnit, pairs = rope.rot_dim / 2;
     const bool half = rope.layout == PA_ROPE_HALF;
     const int total = (a.hq + 2 * a.hkv) * units;
-    const int64_t slot = a.slots[tok];
-    const bool write = slot >= 0 && slot < a.n_slots;
-    if (slot >= a.n_slots && threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_SLOT);
-
     bool ready = false;
     for (int x = threadIdx.x; x < total || !ready; x += blockDim.x) {
-        const int head = x / units, u = x % units;
-        const bool live = x < total && (head < a.hq || write);
-        const bool rotates = u < rot_units && head < a.hq + a.hkv;
+        const int head = min(x, total - 1) / units, u = x % units;
+        const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
+        const bool rotates = u < rot_units && !is_v;
         const int e0 = rotates && half ? 8 * u : kUnit * u;                       // first chunk
         const int e1 = rotates && half ? rope.rot_dim / 2 + 8 * u : kUnit * u + 8;  // second chunk
-        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-        if (live) {
-            const __nv_bfloat16 *src =
-                head < a.hq ? a.q + tok * a.q_stride + head * a.head_dim
-                : head < a.hq + a.hkv ? a.k + tok * a.k_stride + (head - a.hq) * a.head_dim
-                                      : a.v + tok * a.v_stride + (head - a.hq - a.hkv) * a.head_dim;
-            lo = *reinterpret_cast<const uint4 *>(src + e0);
-            hi = *reinterpret_cast<const uint4 *>(src + e1);
-        }
-        if (!ready) {  // (the first pass of every thread: the loads above are in flight)
-            for (int i = threadIdx.x; i < rope.rot_dim / 2; i += blockDim.x) {
-                const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(a.positions[tok])) * rope.turn[i];
-                float s, c;
-                sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
-                turn[i] = make_float2(c * rope.magnitude, s * rope.magnitude);
+        const int h = head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq);
+        const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+        const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + tok0 * stride + h * a.head_dim;
+        for (int t0 = 0; t0 < tokens || !ready; t0 += kAhead) {
+            uint4 lo[kAhead], hi[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                lo[j] = hi[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (t0 + j < tokens && x < total) {
+                    lo[j] = *reinterpret_cast<const uint4 *>(src + (t0 + j) * stride + e0);
+                    hi[j] = *reinterpret_cast<const uint4 *>(src + (t0 + j) * stride + e1);
+                }
             }
-            __syncthreads();
-            ready = true;
-        }
-        if (!live) continue;
-        const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
-        float f0[8], f1[8];  // the two chunks' values
+            if (!ready) {  // (every thread's first pass: the loads above are in flight)
+                for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
+                    const int t = i / pairs, k = i % pairs;
+                    const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(a.positions[tok0 + t])) * rope.turn[k];
+                    float s, c;
+                    sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
+                    turn[t][k] = make_float2(c * rope.magnitude, s * rope.magnitude);
+                }
+                if (threadIdx.x < tokens) {
+                    const int64_t slot = a.slots[tok0 + threadIdx.x];
+                    if (slot >= a.n_slots) set_status(a.status, PA_STATUS_BAD_SLOT);
+                    slot_s[threadIdx.x] = slot < a.n_slots ? slot : -1;
+                }
+                __syncthreads();
+                ready = true;
+            }
+            if (x >= total) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f0[2 * i] = bf16lo(w0[i]), f0[2 * i + 1] = bf16hi(w0[i]);
-            f1[2 * i] = bf16lo(w1[i]), f1[2 * i + 1] = bf16hi(w1[i]);
-        }
-        if (rotates) {
+            for (int j = 0; j < kAhead; ++j) {
+                const int t = t0 + j;
+                if (t >= tokens) break;
+                const int64_t slot = slot_s[t];
+                if (!is_q && slot < 0) continue;
+                const uint32_t w0[4] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w}, w1[4] = {hi[j].x, hi[j].y, hi[j].z, hi[j].w};
+                float f0[8], f1[8];  // the two chunks' values
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 t = turn[8 * u + i];
-                if (half) {
-                    const float x0 = f0[i], x1 = f1[i];
-                    f0[i] = x0 * t.x - x1 * t.y;
-                    f1[i] = x0 * t.y + x1 * t.x;
+                for (int i = 0; i < 4; ++i) {
+                    f0[2 * i] = bf16lo(w0[i]), f0[2 * i + 1] = bf16hi(w0[i]);
+                    f1[2 * i] = bf16lo(w1[i]), f1[2 * i + 1] = bf16hi(w1[i]);
+                }
+                if (rotates) {
+                    const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][8 * u]);  // two pairs each
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 two = cs[i / 2];
+                        const float c = i & 1 ? two.z : two.x, s = i & 1 ? two.w : two.y;
+                        float *fa = half ? f0 + i : i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
+                        float *fb = half ? f1 + i : fa + 1;
+                        const float x0 = *fa, x1 = *fb;
+                        *fa = x0 * c - x1 * s;
+                        *fb = x0 * s + x1 * c;
+                    }
+                }
+                if (F8 && !is_q) {
+                    const float scale = is_v ? a.v_scale : a.k_scale;
+                    uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
+                    *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale);
+                    *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale);
                 } else {
-                    float *f = i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
-                    const float x0 = f[0], x1 = f[1];
-                    f[0] = x0 * t.x - x1 * t.y;
-                    f[1] = x0 * t.y + x1 * t.x;
+                    __nv_bfloat16 *dst = is_q ? a.q_out + (tok0 + t) * a.q_out_stride + h * a.head_dim
+                                              : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
+                                                    (slot * a.hkv + h) * a.head_dim;
+                    uint32_t o0[4], o1[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0[2 * i], f0[2 * i + 1]);
+                        const __nv_bfloat162 b1 = __floats2bfloat162_rn(f1[2 * i], f1[2 * i + 1]);
+                        o0[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b0) : w0[i];  // (a copy keeps its bits)
+                        o1[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b1) : w1[i];
+                    }
+                    *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                    *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
                 }
             }
         }
-        const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
-        if (F8 && !is_q) {
-            const float scale = is_v ? a.v_scale : a.k_scale;
-            const int h = head - a.hq - (is_v ? a.hkv : 0);
-            uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
-            *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale);
-            *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale);
-        } else {
-            __nv_bfloat16 *dst =
-                is_q ? a.q_out + tok * a.q_out_stride + head * a.head_dim
-                     : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
-                           (slot * a.hkv + head - a.hq - (is_v ? a.hkv : 0)) * a.head_dim;
-            uint32_t o0[4], o1[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0[2 * i], f0[2 * i + 1]);
-                const __nv_bfloat162 b1 = __floats2bfloat162_rn(f1[2 * i], f1[2 * i + 1]);
-                o0[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b0) : w0[i];  // (a copy keeps its bits)
-                o1[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b1) : w1[i];
-            }
-            *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-        }
     }
+}
+
+// Tokens per CTA: one where there are few (every SM then has some), eight where
+// there are many.
+constexpr int kManyTokens = 8, kManyFrom = 2048;
+
+template <bool F8>
+cudaError_t launch_rope(const RopeArgs &a, const pa_rope &rope, int threads, cudaStream_t stream) {
+    if (a.n < kManyFrom)
+        return launch_maybe_cooperative(rope_write_kernel<F8, 1>, dim3(static_cast<unsigned>(a.n)), threads, 0, stream,
+                                        false, pdl_on(), a, rope);
+    return launch_maybe_cooperative(rope_write_kernel<F8, kManyTokens>,
+                                    dim3(static_cast<unsigned>((a.n + kManyTokens - 1) / kManyTokens)), threads, 0,
+                                    stream, false, pdl_on(), a, rope);
 }
 
 int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
@@ -159,15 +184,12 @@ int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_
         return PA_EINVAL;
     RopeArgs a{static_cast<__nv_bfloat16 *>(q_out), static_cast<const __nv_bfloat16 *>(q),
                static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new),
-               q_out_stride, q_stride, k_stride, v_stride, positions, slot_mapping,
+               q_out_stride, q_stride, k_stride, v_stride, positions, slot_mapping, n_tokens,
                static_cast<int64_t>(cache.num_blocks) * cache.block_size, static_cast<uint8_t *>(k_cache),
                static_cast<uint8_t *>(v_cache), status, Hq, cache.num_kv_heads, cache.head_dim, k_scale, v_scale};
     const int units = (Hq + 2 * cache.num_kv_heads) * (cache.head_dim / kUnit);
     const int threads = std::min(kMaxThreads, (units + 31) / 32 * 32);
-    const dim3 grid(static_cast<unsigned>(n_tokens));
-    const cudaError_t e =
-        f8 ? launch_maybe_cooperative(rope_write_kernel<true>, grid, threads, 0, stream, false, pdl_on(), a, *rope)
-           : launch_maybe_cooperative(rope_write_kernel<false>, grid, threads, 0, stream, false, pdl_on(), a, *rope);
+    const cudaError_t e = f8 ? launch_rope<true>(a, *rope, threads, stream) : launch_rope<false>(a, *rope, threads, stream);
     return e == cudaSuccess ? PA_OK : PA_ECUDA;
 }
 
