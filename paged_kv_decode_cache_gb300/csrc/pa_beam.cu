@@ -7,10 +7,11 @@
 // row's logits gives both its (max, sum) and its K largest logits; lse enters
 // only when the rows of a request are joined.  A CTA takes a slice of a row, in chunks
 // that it holds in registers: 4 16-byte vectors per thread, all in flight at once.
-// The K-th largest of the threads' maxima bounds the K-th largest value from
-// below, so that only about K of a chunk's 8192 values ever leave the
-// registers; the list of the best K so far raises the bound for the next
-// chunk.  The last CTA of a request to finish joins its lists.
+// The K-th largest of the first chunk's thread maxima bounds the K-th largest
+// value from below, so that only about K of a chunk's 8192 values ever leave the
+// registers, into a pool in shared memory; no warp waits for another until the
+// pool is a quarter full, when its K best raise the bound.  The last CTA of a
+// request to finish joins its lists.
 //
 // Sums: exp in fp32 from x - max (exact for bf16), fp32 sums of 8 per vector
 // and of a thread's vectors, 64 bits across threads and slices.  Scores are
@@ -32,7 +33,7 @@ constexpr int kChunkVecs = kThreads * kVecs;
 constexpr int kMaxK = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxJoin = 4096;                // candidates a request's join holds
-constexpr int kSpill = 448;                   // values of a chunk that may leave the registers
+constexpr int kPool = 2 * kThreads;            // candidates of a slice at a time
 constexpr int kTargetCtas = 8 * 152;          // slices: about 8 CTAs per SM
 constexpr int kMinSliceVecs = 2 * kThreads;   // and no smaller than two vectors per thread
 
@@ -123,13 +124,179 @@ struct BeamArgs {
     Candidate *part_list;  // [rows, slices, K]
 };
 
+// A row's vectors: vector i holds entries i E .. i E + E - 1, whatever the row's
+// alignment, so that equal rows give equal sums to the last bit.  A row that starts
+// `skew` bytes past a 16-byte boundary takes each vector from two aligned ones.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs a) {
+struct Row {
+    static constexpr int E = Vec<T>::kElems;
+    const T *x;
+    const uint4 *grid;
+    int skew, vocab;
+    int whole;   // vectors below it lie (both aligned halves) inside the row
+
+    __device__ Row(const T *row, int n) : x(row), vocab(n) {
+        skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);
+        grid = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(x) - skew);
+        whole = skew ? (vocab + skew / static_cast<int>(sizeof(T))) / E - 1 : vocab / E;
+    }
+    template <int W>
+    __device__ void load_skewed(uint4 (&raw)[kVecs], int i0, int end) const {  // skew = 4 W + (0 or 2) bytes
+        const int bits = (skew & 3) * 8;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = i0 + j * kThreads;
+            if (i >= end || i >= whole) continue;
+            const uint4 lo = __ldg(grid + i), hi = __ldg(grid + i + 1);
+            const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            raw[j] = make_uint4(__funnelshift_r(w[W], w[W + 1], bits), __funnelshift_r(w[W + 1], w[W + 2], bits),
+                                __funnelshift_r(w[W + 2], w[W + 3], bits), __funnelshift_r(w[W + 3], w[W + 4], bits));
+        }
+    }
+    // Vectors i0, i0 + kThreads, ... below end, NaN as -inf, and -inf past the end.
+    __device__ void load(uint4 (&raw)[kVecs], int i0, int end) const {
+        using V = Vec<T>;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) raw[j] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
+        if (skew == 0) {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int i = i0 + j * kThreads;
+                if (i < end && i < whole) raw[j] = __ldcs(grid + i);
+            }
+        } else if (skew < 4) {
+            load_skewed<0>(raw, i0, end);
+        } else if (skew < 8) {
+            load_skewed<1>(raw, i0, end);
+        } else if (skew < 12) {
+            load_skewed<2>(raw, i0, end);
+        } else {
+            load_skewed<3>(raw, i0, end);
+        }
+        if (i0 + (kVecs - 1) * kThreads >= whole) {  // the row's end: entry by entry
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int i = i0 + j * kThreads;
+                if (i < whole || i >= end) continue;
+                uint32_t w[4] = {V::kFill, V::kFill, V::kFill, V::kFill};
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (i * E + e < vocab) V::put(w, e, x[i * E + e]);
+                raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            raw[j] = make_uint4(V::clean(raw[j].x), V::clean(raw[j].y), V::clean(raw[j].z), V::clean(raw[j].w));
+    }
+};
+
+// The largest key that at least K of the threads' keys reach (0: fewer than K
+// do), bit by bit from the top; a CTA-wide count per bit.
+template <int kKeyLow>
+__device__ __forceinline__ uint32_t kth_key(uint32_t mine, int K) {
+    uint32_t key = 0u;
+    for (int bit = 31; bit >= kKeyLow; --bit)
+        if (__syncthreads_count(mine >= (key | 1u << bit)) >= K) key |= 1u << bit;
+    return key;
+}
+
+// pool[0 .. n) reduced to its min(n, K) first candidates, in order: an entry's
+// place is the number of entries before it.  n <= 2 kThreads.
+__device__ __forceinline__ int keep_first(Candidate *pool, int n, int K) {
+    Candidate c[2];
+    int place[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = u * kThreads + threadIdx.x;
+        place[u] = K;
+        if (i < n) {
+            c[u] = pool[i];
+            int before_it = 0;
+            for (int j = 0; j < n; ++j) before_it += before(pool[j], c[u]);
+            place[u] = before_it;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (place[u] < K) pool[place[u]] = c[u];
+    __syncthreads();
+    return min(n, K);
+}
+
+// The K first candidates of vectors [v0, v1) whatever their order: for rows
+// that overfill the pool (long runs of equal values, or values that rise along the
+// row).  Each chunk's exact K-th largest value by bisection over its key, then, among
+// the values equal to it, the lowest entries by bisection over the entry.
+// pool: the list so far in [0, kept), the chunk's share after it.
+template <typename T>
+__device__ __noinline__ int exact_slice(const Row<T> &row, int v0, int v1, int K, Candidate *pool, int *count) {
+    using V = Vec<T>;
+    constexpr int E = V::kElems;
+    const int tid = threadIdx.x;
+    int kept = 0;
+    float floor = -INFINITY;   // values at or below it are not among the K largest
+    for (int c0 = v0; c0 < v1; c0 += kChunkVecs) {
+        uint4 raw[kVecs];
+        row.load(raw, c0 + tid, v1);
+        auto each = [&](auto &&f) {  // f(value, vocabulary entry) of this thread's values above the floor
+            for (int j = 0; j < kVecs; ++j)
+                for (int e = 0; e < E; ++e) {
+                    const float v = V::get(raw[j], e);
+                    if (v > floor) f(v, (c0 + j * kThreads + tid) * E + e);
+                }
+        };
+        auto total = [&](auto &&pred) {
+            __syncthreads();
+            if (tid == 0) *count = 0;
+            __syncthreads();
+            int c = 0;
+            each([&](float v, int i) { c += pred(v, i); });
+            c = __reduce_add_sync(0xffffffffu, c);
+            if ((tid & 31) == 0 && c) atomicAdd(count, c);
+            __syncthreads();
+            return *count;
+        };
+        const int above = total([](float, int) { return 1; });
+        if (above == 0) continue;
+        float kth = floor;   // with fewer than K above the floor, all of them
+        int last = -1;       // the highest entry of a value equal to it that is taken
+        if (above > K) {
+            uint32_t key = 0u;
+            for (int bit = 31; bit >= V::kKeyLow; --bit) {
+                const uint32_t t = key | 1u << bit;
+                if (total([&](float v, int) { return order_key(v) >= t; }) >= K) key = t;
+            }
+            kth = key_value<V::kKeyLow>(key);
+            const int need = K - total([&](float v, int) { return v > kth; });
+            last = 0;
+            for (int bit = 30; bit >= 0; --bit) {
+                const int t = last | 1 << bit;
+                if (total([&](float v, int i) { return v == kth && i < t; }) < need) last = t;
+            }
+        }
+        __syncthreads();
+        if (tid == 0) *count = kept;
+        __syncthreads();
+        each([&](float v, int i) {
+            if (!(v > kth || (v == kth && i <= last))) return;
+            const int at = atomicAdd(count, 1);
+            if (at < kPool) pool[at] = Candidate{v, i};
+        });
+        __syncthreads();
+        kept = keep_first(pool, min(*count, kPool), K);
+        if (kept == K) floor = pool[K - 1].x;
+    }
+    return kept;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
     extern __shared__ uint64_t join_keys[];  // [beams * slices * K], then as many int32 (the join)
-    __shared__ Candidate best[kMaxK];        // the slice's K largest so far, in order
-    __shared__ Candidate pool[kMaxK + kSpill];
+    __shared__ Candidate pool[kPool];        // candidates for the slice's K largest
     __shared__ int count, ticket;
     __shared__ float red_max[kThreads / 32];
     __shared__ double red_sum[kThreads / 32];
@@ -137,74 +304,28 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
-    const int group = row / a.beams, K = a.K;
-    const bool done = a.finished && a.finished[row];
+    const int row_id = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
+    const int group = row_id / a.beams, K = a.K;
+    const bool done = a.finished && a.finished[row_id];
 
     if (!done) {
-        // Vector i holds entries i E .. i E + E - 1, whatever the row's alignment, so
-        // that equal rows give equal sums to the last bit.  A row that starts
-        // `skew` bytes past a 16-byte boundary takes each vector from two aligned ones.
-        const T *x = static_cast<const T *>(a.logits) + row * a.row_stride;
-        const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);
-        const uint4 *grid = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(x) - skew);
+        const Row<T> row(static_cast<const T *>(a.logits) + row_id * a.row_stride, a.vocab);
         const int vecs = (a.vocab + E - 1) / E;
         const int per = (vecs + a.slices - 1) / a.slices;
         const int v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
-        // vectors below `whole` lie (both aligned halves) inside the row
-        const int whole = skew ? (a.vocab + skew / static_cast<int>(sizeof(T))) / E - 1 : a.vocab / E;
+        const int period = max(1, kPool / 3 / K);   // chunks between looks at the pool
         float m = -INFINITY, sum = 0.f;   // this thread's maximum and sum of exp(x - m)
-        float floor = -INFINITY;          // values at or below it are not among the slice's K largest
-        int kept = 0;                     // entries of `best`
-        for (int c0 = v0; c0 < v1; c0 += kChunkVecs) {
+        float cut = -INFINITY;            // values below it, or with `strict` at it, are not among the K largest
+        bool strict = true, overfull = false;
+        if (tid == 0) count = 0;
+        __syncthreads();
+        int chunk = 0;
+        for (int c0 = v0; c0 < v1; c0 += kChunkVecs, ++chunk) {
             uint4 raw[kVecs];
-            auto load = [&](auto words) {  // skew = 4 words + (0 or 2) bytes
-                constexpr int W = decltype(words)::value;
-                const int bits = (skew & 3) * 8;
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    const int i = c0 + j * kThreads + tid;
-                    raw[j] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
-                    if (i >= v1 || i >= whole) continue;
-                    const uint4 lo = __ldg(grid + i), hi = __ldg(grid + i + 1);
-                    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    raw[j] = make_uint4(__funnelshift_r(w[W], w[W + 1], bits), __funnelshift_r(w[W + 1], w[W + 2], bits),
-                                        __funnelshift_r(w[W + 2], w[W + 3], bits),
-                                        __funnelshift_r(w[W + 3], w[W + 4], bits));
-                }
-            };
-            if (skew == 0) {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    const int i = c0 + j * kThreads + tid;
-                    raw[j] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
-                    if (i < v1 && i < whole) raw[j] = __ldcs(grid + i);
-                }
-            } else if (skew < 4) {
-                load(Int<0>{});
-            } else if (skew < 8) {
-                load(Int<1>{});
-            } else if (skew < 12) {
-                load(Int<2>{});
-            } else {
-                load(Int<3>{});
-            }
-            if (v1 > whole && c0 + kChunkVecs > whole) {  // the row's end: entry by entry
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    const int i = c0 + j * kThreads + tid;
-                    if (i < whole || i >= v1) continue;
-                    uint32_t w[4] = {V::kFill, V::kFill, V::kFill, V::kFill};
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (i * E + e < a.vocab) V::put(w, e, x[i * E + e]);
-                    raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
+            row.load(raw, c0 + tid, v1);
             float vmax[kVecs], cmax = -INFINITY;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
-                raw[j] = make_uint4(V::clean(raw[j].x), V::clean(raw[j].y), V::clean(raw[j].z), V::clean(raw[j].w));
                 vmax[j] = V::max(raw[j]);
                 cmax = fmaxf(cmax, vmax[j]);
             }
@@ -226,93 +347,50 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
                     sum += s[0];
                 }
             }
-            // ---- the chunk's share of the K largest
-            const int above = __syncthreads_count(cmax > floor);
-            if (above == 0) continue;
-            float cut = floor;      // take values > cut, or >= cut with `ties`
-            bool ties = false;
-            if (above > K) {        // the K-th largest of the threads' maxima
-                const uint32_t mine = cmax > floor ? order_key(cmax) : 0u;
-                uint32_t key = 0u;
-                for (int bit = 31; bit >= V::kKeyLow; --bit)
-                    if (__syncthreads_count(mine >= (key | 1u << bit)) >= K) key |= 1u << bit;
-                cut = key_value<V::kKeyLow>(key);
-                ties = true;
+            // ---- candidates: the first chunk's bound is the K-th largest of its threads' maxima
+            if (chunk == 0) {
+                const uint32_t key = kth_key<V::kKeyLow>(cmax > -INFINITY ? order_key(cmax) : 0u, K);
+                if (key) {
+                    cut = key_value<V::kKeyLow>(key);
+                    strict = false;
+                }
             }
-            auto passes = [&](float v) { return ties ? v >= cut : v > cut; };
-            auto each = [&](auto &&f) {  // f(value, vocabulary entry) of this thread's values that pass
-                if (!passes(cmax)) return;
+            auto passes = [&](float v) { return strict ? v > cut : v >= cut; };
+            if (passes(cmax)) {
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     if (!passes(vmax[j])) continue;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         const float v = V::get(raw[j], e);
-                        if (passes(v)) f(v, (c0 + j * kThreads + tid) * E + e);
+                        if (!passes(v)) continue;
+                        const int at = atomicAdd(&count, 1);
+                        if (at < kPool) pool[at] = Candidate{v, (c0 + j * kThreads + tid) * E + e};
                     }
                 }
-            };
-            if (tid == 0) count = 0;
-            __syncthreads();
-            each([&](float v, int i) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kSpill) pool[K + at] = Candidate{v, i};
-            });
-            __syncthreads();
-            int n = count;
-            if (n > kSpill) {
-                // Too many (equal values, or a few threads with most of the
-                // large ones): the exact K-th largest value by bisection over its
-                // key, then, among the values equal to it, the lowest entries by
-                // bisection over the entry.
-                auto total = [&](auto &&pred) {
-                    __syncthreads();
-                    if (tid == 0) count = 0;
-                    __syncthreads();
-                    int c = 0;
-                    each([&](float v, int i) { c += pred(v, i); });
-                    c = __reduce_add_sync(0xffffffffu, c);
-                    if (lane == 0 && c) atomicAdd(&count, c);
-                    __syncthreads();
-                    return count;
-                };
-                uint32_t key = 0u;
-                for (int bit = 31; bit >= V::kKeyLow; --bit) {
-                    const uint32_t t = key | 1u << bit;
-                    if (total([&](float v, int) { return order_key(v) >= t; }) >= K) key = t;
-                }
-                const float kth = key_value<V::kKeyLow>(key);
-                const int need = K - total([&](float v, int) { return v > kth; });
-                int last = 0;   // the highest entry of an equal value that is taken
-                for (int bit = 30; bit >= 0; --bit) {
-                    const int t = last | 1 << bit;
-                    if (total([&](float v, int i) { return v == kth && i < t; }) < need) last = t;
-                }
-                __syncthreads();
-                if (tid == 0) count = 0;
-                __syncthreads();
-                each([&](float v, int i) {
-                    if (!(v > kth || (v == kth && i <= last))) return;
-                    const int at = atomicAdd(&count, 1);
-                    if (at < K) pool[K + at] = Candidate{v, i};
-                });
-                __syncthreads();
-                n = min(count, K);   // (K)
             }
-            // ---- joined with the list: an entry's place is the number of entries before it
-            if (tid < K) pool[tid] = tid < kept ? best[tid] : Candidate{-INFINITY, INT32_MAX};
-            __syncthreads();
-            for (int i = tid; i < K + n; i += kThreads) {
-                const Candidate c = pool[i];
-                if (c.v == INT32_MAX) continue;
-                int place = 0;
-                for (int j = 0; j < K + n; ++j) place += before(pool[j], c);
-                if (place < K) best[place] = c;
+            if (chunk % period == period - 1) {  // raise the bound before the pool fills
+                __syncthreads();
+                const int n = count;
+                __syncthreads();
+                if (n > kPool) {
+                    overfull = true;
+                    cut = INFINITY, strict = true;
+                } else if (n > kPool / 4) {
+                    const int kept = keep_first(pool, n, K);
+                    if (tid == 0) count = kept;
+                    if (kept == K) {
+                        cut = pool[K - 1].x;   // (later entries of an equal value come after it)
+                        strict = true;
+                    }
+                    __syncthreads();
+                }
             }
-            kept = min(K, kept + n);
-            __syncthreads();
-            if (kept == K) floor = best[K - 1].x;
         }
+        __syncthreads();
+        int kept;
+        if (overfull || count > kPool) kept = exact_slice<T>(row, v0, v1, K, pool, &count);
+        else kept = keep_first(pool, count, K);
         // ---- the slice's maximum, sum and list
         float top = m;
 #pragma unroll
@@ -326,14 +404,14 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamArgs
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) red_sum[warp] = z;
         __syncthreads();
-        const int64_t part = static_cast<int64_t>(row) * a.slices + slice;
+        const int64_t part = static_cast<int64_t>(row_id) * a.slices + slice;
         if (tid == 0) {
             double s = 0.0;
             for (int i = 0; i < kThreads / 32; ++i) s += red_sum[i];
             a.part_max[part] = top;
             a.part_sum[part] = s;
         }
-        if (tid < K) a.part_list[part * K + tid] = tid < kept ? best[tid] : Candidate{-INFINITY, -1};
+        if (tid < K) a.part_list[part * K + tid] = tid < kept ? pool[tid] : Candidate{-INFINITY, -1};
     }
 
     // ---- the request's last CTA joins its rows' slices
