@@ -686,7 +686,33 @@ int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, 
     if (lmax > INT32_MAX / 2) return PA_EUNSUPPORTED;
     const int64_t seen = scored_tokens(lmax, window < lmax ? window : 0, static_cast<int32_t>(std::min<int64_t>(max_prefix, lmax)),
                                        scored_positions(G, q_len));
-    return pa_choose_num_splits_mq(B, q_len, Hq, Hkv, D, static_cast<int32_t>(round_up(seen, 16) / 16), 16, sms);
+    const int tiles = static_cast<int>(round_up(seen, 16) / 16);
+    const int P = pa_choose_num_splits_mq(B, q_len, Hq, Hkv, D, tiles, 16, sms);
+    if (P < 1 || B < 1 || k != Kernel::kTensorCore || prefill_shape(G, q_len)) return P;
+    // That rule fills one wave, which for batches of 20 to 150 CTAs leaves SMs idle (64 CTAs
+    // on 152 SMs: P = 2) and, when the sequences' lengths differ, waits for the
+    // longest one's partitions.  In units of one CTA streaming the longest sequence, P
+    // partitions take about
+    //   ceil(units P / SMs) / P                        sequences all of that length
+    //   max(1 / P, units / (2 SMs) + 1 / (2 P))        lengths spread evenly below it
+    // and each wave after the first about 8 us more (a chunk takes 1.05 us).  P has the least
+    // sum of the two, among those that keep at least 8 tiles.  FP8, 64 sequences of 8 heads, up to
+    // 4096 tokens: P = 4 takes 163 us full and 112 us spread, P = 2 155 and 155; 40
+    // sequences: P = 11 111 and 77, P = 3 108 and 108; 16 keep P = 9 (45 and 44).
+    const int qpc = queries_per_cta(G, q_len);
+    const double units = static_cast<double>(units_per_split(k, B, G, Hkv, qpc, (q_len + qpc - 1) / qpc));
+    int hc = 1, gp = 1;
+    tc_shape(G * qpc, Hkv, &hc, &gp);
+    const double wave_cost = 8.0 / (1.05 * std::max(1, tiles * 16 * hc / 128));
+    auto cost = [&](int n) {
+        const double waves = std::ceil(units * n / sms);
+        return waves / n + std::max(1.0 / n, units / (2.0 * sms) + 0.5 / n) + 2.0 * wave_cost * (waves - 1.0);
+    };
+    int best = P;
+    for (int n = P + 1; n <= std::min(64, tiles / 8); ++n)
+        if (cost(n) < cost(best)) best = n;
+    const int chunk = static_cast<int>(round_up((static_cast<int64_t>(tiles) * 16 + best - 1) / best, 16));
+    return (tiles * 16 + chunk - 1) / chunk;   // (no empty partition)
 }
 
 int check_rules(const pa_score_rules *r) {

@@ -340,31 +340,32 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 0xffffffffu, row_ok && all_tiles && tok_last < t_end &&
                                  ((real_last <= pos && real(tok0) >= oldest) || (SC && tok_last < sn.prefix)));
             float mx = -INFINITY;
-            if constexpr (SC) {  // the rules, on finite values (a token not seen may hold anything)
+            if constexpr (SC) {  // the rules, then what is not seen masked (whatever it holds)
 #pragma unroll
-                for (int k = 0; k < kPfT; ++k) {
-                    const int t = real(tok0 + k / kTile * kTile) + k % kTile;
-                    const bool valid = whole || (row_ok && tile_ok[k / kTile] && tok0 + k < t_end &&
-                                                 (t < sn.prefix || (t <= pos && t >= oldest)));
-                    sv[k] = valid ? sv[k] * sl2 : -INFINITY;
-                }
-                if (p.soft_cap > 0.f) {
-                    uint32_t hidden[2] = {0u, 0u};
-#pragma unroll
-                    for (int k = 0; k < kPfT; ++k) {
-                        hidden[k / 32] |= static_cast<uint32_t>(sv[k] == -INFINITY) << (k % 32);
-                        sv[k] = sv[k] == -INFINITY ? 0.f : sv[k];
-                    }
-                    cap_scores<kPfT>(sv, p.inv_cap, p.soft_cap);
-#pragma unroll
-                    for (int k = 0; k < kPfT; ++k)
-                        if (hidden[k / 32] >> (k % 32) & 1u) sv[k] = -INFINITY;
-                }
+                for (int k = 0; k < kPfT; ++k) sv[k] *= sl2;
+                if (p.soft_cap > 0.f) cap_scores<kPfT>(sv, p.inv_cap, p.soft_cap);
                 if (p.slopes) {
 #pragma unroll
-                    for (int k = 0; k < kPfT; ++k) {
-                        const int t = real(tok0 + k / kTile * kTile) + k % kTile;
-                        sv[k] = fmaf(slope, static_cast<float>(t - pos), sv[k]);  // (-inf stays)
+                    for (int k = 0; k < kPfTilesPerChunk; ++k) {
+                        const float at = static_cast<float>(real(tok0 + k * kTile) - pos);
+#pragma unroll
+                        for (int e = 0; e < kTile; ++e)
+                            sv[k * kTile + e] = fmaf(slope, at + static_cast<float>(e), sv[k * kTile + e]);
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int k = 0; k < kPfTilesPerChunk; ++k) {
+                        // the tile's tokens that the row sees: below the prefix's end, or from the
+                        // window's start to the row's position; all before the range's end
+                        const int first = real(tok0 + k * kTile);
+                        auto below = [&](int end) { return (1u << min(max(end - first, 0), kTile)) - 1u; };
+                        uint32_t seen = below(sn.prefix) | (below(pos + 1) & ~below(oldest));
+                        seen &= (1u << min(max(t_end - tok0 - k * kTile, 0), kTile)) - 1u;
+                        if (!row_ok || !tile_ok[k]) seen = 0u;
+#pragma unroll
+                        for (int e = 0; e < kTile; ++e)
+                            sv[k * kTile + e] = seen >> e & 1u ? sv[k * kTile + e] : -INFINITY;
                     }
                 }
 #pragma unroll

@@ -48,40 +48,60 @@ __device__ __forceinline__ Seen seen_by(const DecodeParams &p, int b, int L, int
     return s;
 }
 
+// Two fp32 lanes per instruction (fma.rn.f32x2 and its like).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // c tanh(x / c) in log2 units: x and cap are times log2(e), inv_cap = 1 / cap.
-// Below u = 0.625 an odd polynomial (a least-squares fit of tanh(u) / u in u^2,
-// weighted towards its largest error: 6e-8 of the value in fp32), above 1 - 2 / (e^2u + 1).  Most
-// scores are small next to the cap; a warp whose scores all are skips the rest.
+// With u = x / cap below 0.625, x (1 + u^2 p(u^2)) with a least-squares fit of
+// tanh(u) / u weighted towards its largest error: 6e-8 of the value in fp32.  Most
+// scores are small next to the cap, and a warp whose scores all are stops there (9
+// operations, two scores each); otherwise all take 1 - 2 / (e^2u + 1), whose
+// error is 2^-22 of the cap.
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float inv_cap, float cap) {
     bool big = false;
+    const float edge = 0.625f * cap;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] *= inv_cap;
-        big |= !(fabsf(x[i]) < 0.625f);
-    }
+    for (int i = 0; i < N; ++i) big |= !(fabsf(x[i]) < edge);
     if (!__any_sync(0xffffffffu, big)) {
+        const uint64_t ic = pack2(inv_cap, inv_cap);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float t = x[i] * x[i];
-            float p = fmaf(t, -0x1.72ef1ep-8f, 0x1.515ceep-6f);
-            p = fmaf(t, p, -0x1.b81542p-5f);
-            p = fmaf(t, p, 0x1.11058p-3f);
-            p = fmaf(t, p, -0x1.555524p-2f);
-            x[i] = cap * fmaf(x[i] * t, p, x[i]);
+        for (int i = 0; i < N; i += 2) {
+            const uint64_t v = pack2(x[i], x[i + 1 < N ? i + 1 : i]);
+            const uint64_t u = mul2(v, ic), t = mul2(u, u);
+            uint64_t p = fma2(t, pack2(-0x1.72ef1ep-8f, -0x1.72ef1ep-8f), pack2(0x1.515ceep-6f, 0x1.515ceep-6f));
+            p = fma2(t, p, pack2(-0x1.b81542p-5f, -0x1.b81542p-5f));
+            p = fma2(t, p, pack2(0x1.11058p-3f, 0x1.11058p-3f));
+            p = fma2(t, p, pack2(-0x1.555524p-2f, -0x1.555524p-2f));
+            float a, b;
+            unpack2(fma2(mul2(v, t), p, v), a, b);
+            x[i] = a;
+            if (i + 1 < N) x[i + 1] = b;
         }
         return;
     }
+    const float k = 2.8853900817779268f * inv_cap;  // e^2u = 2^(k x)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float u = x[i], t = u * u, a = fabsf(u);
-        float p = fmaf(t, -0x1.72ef1ep-8f, 0x1.515ceep-6f);
-        p = fmaf(t, p, -0x1.b81542p-5f);
-        p = fmaf(t, p, 0x1.11058p-3f);
-        p = fmaf(t, p, -0x1.555524p-2f);
-        const float near = fmaf(u * t, p, u);
-        const float far = copysignf(1.f - __fdividef(2.f, fast_exp2(a * 2.8853900817779268f) + 1.f), u);
-        x[i] = cap * (a < 0.625f ? near : far);
+        const float far = fmaf(-cap, __fdividef(2.f, fast_exp2(fabsf(x[i]) * k) + 1.f), cap);
+        x[i] = copysignf(far, x[i]);
     }
 }
 
