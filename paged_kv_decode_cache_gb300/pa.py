@@ -578,6 +578,73 @@ def pa_decode_splitkv_noalloc(out, lse, q, k_cache, v_cache, block_tables, seq_l
     _check("pa_decode_splitkv_noalloc", rc)
 
 
+# ---------------------------------------------------------------------------------------------
+# The operators around a decode step: rotary positions, score rules, beams, pages.
+#
+# These calls are short on the GPU (2 to 20 us), so their wrappers spend little on the host: one
+# pass over the arguments that checks them and takes their addresses, no intermediate objects, the
+# current stream's handle without a Stream object (about 7 us a call, of which the launches take 2
+# to 3; the wrappers above take 20 to 25).
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_entry_points = {}
+
+
+def _device_of(t, name: str) -> int:
+    """The index of the CUDA device that a tensor is on: the call's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _at(t, name: str, dtype: torch.dtype, ndim: int, dev: int) -> int:
+    """The address of a contiguous tensor of this type on this device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or \
+            not t.is_contiguous() or t.get_device() != dev:
+        _need(t, name, dtype, ndim)
+        raise ValueError(f"tensors on several devices ({name} is on {t.device})")
+    return t.data_ptr()
+
+
+def _status_at(status, dev: int):
+    return None if status is None else _at(status, "status", torch.int32, 1, dev)
+
+
+def _space_at(workspace, dev: int):
+    """(address, bytes) of a workspace tensor of any type, (None, 0) without one."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
+            workspace.get_device() != dev:
+        raise ValueError("workspace must be a contiguous CUDA tensor on the call's device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def _enqueue(name: str, dev: int, stream, *args):
+    """Call the entry point on device `dev` and `stream` (default: the device's current one)."""
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(lib(), name)
+    if stream is None:
+        s = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{name}: stream on {stream.device}, tensors on cuda:{dev}")
+    else:
+        s = stream.cuda_stream
+    if _current_device() == dev:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != PA_OK:
+        raise PAError(name, rc, pa_strerror(rc))
+
+
 _ROPE_LAYOUTS = {"half": PA_ROPE_HALF, "interleaved": PA_ROPE_INTERLEAVED}
 _ROPE_SCALINGS = {"none": PA_ROPE_PLAIN, "linear": PA_ROPE_LINEAR, "ntk": PA_ROPE_NTK,
                   "yarn": PA_ROPE_YARN, "banded": PA_ROPE_BANDED}
@@ -599,60 +666,54 @@ def pa_rope_init(rot_dim: int, base: float, layout: str = "half", scaling: str =
     return rope
 
 
-def _need_rows(t: torch.Tensor, name: str):
-    """A bf16 CUDA tensor [N, H, D] whose rows [H, D] are contiguous (any stride between them)."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [N, H, D]")
-    if t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+def _rows_at(t, name: str, n: int, heads: int, d: int, dev: int):
+    """(address, stride between rows) of a bf16 tensor [n, heads, d] with contiguous rows [heads, d]."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.dim() != 3 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor [N, H, D] on the call's device")
+    if tuple(t.shape) != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and heads > 1):
         raise ValueError(f"{name}: every row [H, D] must be contiguous")
+    return t.data_ptr(), row if n > 1 else heads * d  # (a single row's stride says nothing)
 
 
-def _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope):
-    for t, name in ((q_out, "q_out"), (q, "q"), (k_new, "k_new"), (v_new, "v_new")):
-        _need_rows(t, name)
-    _need(positions, "positions", torch.int32, 1)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+def _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope, pool_dtype):
+    dev = _device_of(q, "q")
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a plan made by pa_rope_init")
-    n = q.shape[0]
-    if q_out.shape != q.shape or v_new.shape != k_new.shape or v_cache.shape != k_cache.shape:
-        raise ValueError("q_out / q, K / V or the pools differ in shape")
-    if k_new.shape[0] != n or positions.shape[0] != n or slot_mapping.shape[0] != n:
-        raise ValueError("q, k_new, positions and slot_mapping must have as many tokens")
-    if k_new.shape[1:] != k_cache.shape[2:] or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("k_new must be [N, Hkv, D] and q [N, Hq, D] matching the pool")
-    if n == 1:  # (a single row's stride says nothing)
-        strides = [t.shape[1] * t.shape[2] for t in (q_out, q, k_new, v_new)]
-    else:
-        strides = [t.stride(0) for t in (q_out, q, k_new, v_new)]
-    return (_ptr(q_out), strides[0], _ptr(q), strides[1], _ptr(k_new), strides[2], _ptr(v_new),
-            strides[3], _ptr(positions), _ptr(slot_mapping), n, q.shape[1], _ptr(k_cache),
-            _ptr(v_cache), cache_desc(k_cache))
+    kc = _at(k_cache, "k_cache", pool_dtype, 4, dev)
+    vc = _at(v_cache, "v_cache", pool_dtype, 4, dev)
+    nb, bs, hkv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or q.dim() != 3:
+        raise ValueError("the pools differ in shape, or q is not [N, Hq, D]")
+    n, hq = q.size(0), q.size(1)
+    pos = _at(positions, "positions", torch.int32, 1, dev)
+    slots = _at(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    if positions.size(0) != n or slot_mapping.size(0) != n:
+        raise ValueError("q, positions and slot_mapping must have as many tokens")
+    return dev, (*_rows_at(q_out, "q_out", n, hq, d, dev), *_rows_at(q, "q", n, hq, d, dev),
+                 *_rows_at(k_new, "k_new", n, hkv, d, dev), *_rows_at(v_new, "v_new", n, hkv, d, dev),
+                 pos, slots, n, hq, kc, vc, CacheDesc(nb, bs, hkv, d))
 
 
-@_on_tensors_device
 def pa_rope_write(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
                   status=None, stream=None):
     """Turn q into q_out, and write the turned k_new and v_new through slot_mapping."""
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope)
-    rc = lib().pa_rope_write(*args, ctypes.byref(rope), _ptr(status), _stream(stream))
-    _check("pa_rope_write", rc)
+    dev, args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
+                             torch.bfloat16)
+    _enqueue("pa_rope_write", dev, stream, *args, ctypes.byref(rope), _status_at(status, dev))
 
 
-@_on_tensors_device
 def pa_rope_write_fp8(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, k_scale,
                       v_scale, rope, status=None, stream=None):
     """pa_rope_write into uint8 e4m3 pools."""
-    _need_pool8(k_cache, "k_cache")
-    _need_pool8(v_cache, "v_cache")
-    args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope)
-    rc = lib().pa_rope_write_fp8(*args, float(k_scale), float(v_scale), ctypes.byref(rope),
-                                 _ptr(status), _stream(stream))
-    _check("pa_rope_write_fp8", rc)
+    dev, args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
+                             torch.uint8)
+    _enqueue("pa_rope_write_fp8", dev, stream, *args, k_scale, v_scale, ctypes.byref(rope),
+             _status_at(status, dev))
 
 
 class PoolSet:
@@ -672,6 +733,7 @@ class PoolSet:
             if t.shape != first.shape or t.device != first.device:
                 raise ValueError("the pools differ in shape or device")
         self.device = first.device
+        self.device_index = first.get_device()
         self.num_blocks = first.shape[0]
         self.desc = cache_desc(first)
         self.elem_bytes = first.element_size()
@@ -681,24 +743,10 @@ class PoolSet:
         return len(self.pools)
 
 
-def _state(tables, lens, refs, pools):
+def _pools_of(pools) -> PoolSet:
     if not isinstance(pools, PoolSet):
         raise TypeError("pools must be a PoolSet")
-    _need(tables, "tables", torch.int32, 2)
-    _need(lens, "lens", torch.int32, 1)
-    _need(refs, "refs", torch.int32, 1)
-    if refs.device != pools.device:
-        raise ValueError("the pools are on another device")
-    if lens.shape[0] != tables.shape[0] or refs.shape[0] != pools.num_blocks:
-        raise ValueError("tables, lens and refs must be [B, max_blocks], [B] and [num_blocks]")
-
-
-def _space(workspace):
-    if workspace is None:
-        return 0
-    if not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace.numel() * workspace.element_size()
+    return pools
 
 
 def pa_fork_workspace_bytes(B_old: int, B_new: int, num_blocks: int) -> int:
@@ -709,58 +757,48 @@ def pa_compact_workspace_bytes(num_blocks: int) -> int:
     return int(lib().pa_compact_workspace_bytes(num_blocks))
 
 
-@_on_tensors_device
 def pa_sequences_fork(new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents, pools,
                       workspace, status=None, stream=None):
     """New row i is old row parents[i] (negative: none), blocks shared, last blocks copied on write;
     slot_mapping gets the slot of every row's next token."""
-    _state(tables, lens, refs, pools)
-    _need(new_tables, "new_tables", torch.int32, 2)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    _need(new_refs, "new_refs", torch.int32, 1)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    _need(parents, "parents", torch.int32, 1)
-    n, mb = parents.shape[0], tables.shape[1]
-    if tuple(new_tables.shape) != (n, mb) or new_lens.shape[0] != n or slot_mapping.shape[0] != n or \
-            new_refs.shape != refs.shape:
-        raise ValueError("the new tables, lens, refs and slots do not match parents and the old state")
-    rc = lib().pa_sequences_fork(_ptr(new_tables), _ptr(new_lens), _ptr(new_refs), _ptr(slot_mapping),
-                                 _ptr(tables), _ptr(lens), _ptr(refs), _ptr(parents), tables.shape[0], n, mb,
-                                 pools._ptrs, len(pools), pools.elem_bytes, pools.desc, _ptr(workspace),
-                                 _space(workspace), _ptr(status), _stream(stream))
-    _check("pa_sequences_fork", rc)
+    dev, i32 = _pools_of(pools).device_index, torch.int32
+    args = (_at(new_tables, "new_tables", i32, 2, dev), _at(new_lens, "new_lens", i32, 1, dev),
+            _at(new_refs, "new_refs", i32, 1, dev), _at(slot_mapping, "slot_mapping", torch.int64, 1, dev),
+            _at(tables, "tables", i32, 2, dev), _at(lens, "lens", i32, 1, dev),
+            _at(refs, "refs", i32, 1, dev), _at(parents, "parents", i32, 1, dev))
+    n, old, mb = parents.size(0), tables.size(0), tables.size(1)
+    if lens.size(0) != old or refs.size(0) != pools.num_blocks or new_refs.size(0) != pools.num_blocks:
+        raise ValueError("tables, lens and refs must be [B, max_blocks], [B] and [num_blocks]")
+    if new_tables.size(0) != n or new_tables.size(1) != mb or new_lens.size(0) != n or \
+            slot_mapping.size(0) != n:
+        raise ValueError("the new tables, lens and slots must have a row for every parent")
+    _enqueue("pa_sequences_fork", dev, stream, *args, old, n, mb, pools._ptrs, len(pools.pools),
+             pools.elem_bytes, pools.desc, *_space_at(workspace, dev), _status_at(status, dev))
 
 
-@_on_tensors_device
 def pa_blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace,
                       status=None, stream=None):
     """Live blocks moved to the front of every pool; remap: every old block id's new one (-1: free)."""
-    _state(tables, lens, refs, pools)
-    _need(new_tables, "new_tables", torch.int32, 2)
-    _need(new_refs, "new_refs", torch.int32, 1)
-    _need(remap, "remap", torch.int32, 1)
-    _need(n_live, "n_live", torch.int32, 1)
-    if new_tables.shape != tables.shape or new_refs.shape != refs.shape or remap.shape != refs.shape or \
-            n_live.shape[0] != 1:
-        raise ValueError("new_tables, new_refs, remap and n_live do not match the old state")
-    rc = lib().pa_blocks_compact(_ptr(new_tables), _ptr(new_refs), _ptr(remap), _ptr(n_live), _ptr(tables),
-                                 _ptr(lens), _ptr(refs), tables.shape[0], tables.shape[1], pools._ptrs,
-                                 len(pools), pools.elem_bytes, pools.desc, _ptr(workspace), _space(workspace),
-                                 _ptr(status), _stream(stream))
-    _check("pa_blocks_compact", rc)
+    dev, i32 = _pools_of(pools).device_index, torch.int32
+    args = (_at(new_tables, "new_tables", i32, 2, dev), _at(new_refs, "new_refs", i32, 1, dev),
+            _at(remap, "remap", i32, 1, dev), _at(n_live, "n_live", i32, 1, dev),
+            _at(tables, "tables", i32, 2, dev), _at(lens, "lens", i32, 1, dev), _at(refs, "refs", i32, 1, dev))
+    B, mb, nb = tables.size(0), tables.size(1), pools.num_blocks
+    if lens.size(0) != B or refs.size(0) != nb or new_refs.size(0) != nb or remap.size(0) != nb or \
+            new_tables.size(0) != B or new_tables.size(1) != mb or n_live.size(0) != 1:
+        raise ValueError("tables [B, max_blocks], lens [B], counts and remap [num_blocks], n_live [1]")
+    _enqueue("pa_blocks_compact", dev, stream, *args, B, mb, pools._ptrs, len(pools.pools),
+             pools.elem_bytes, pools.desc, *_space_at(workspace, dev), _status_at(status, dev))
 
 
-@_on_tensors_device
 def pa_blocks_copy(pools, pairs, status=None, stream=None):
     """Copy whole blocks within every pool: pairs int32 [n, 2], source and destination."""
-    if not isinstance(pools, PoolSet):
-        raise TypeError("pools must be a PoolSet")
-    _need(pairs, "pairs", torch.int32, 2)
-    if pairs.shape[1] != 2 or pairs.device != pools.device:
-        raise ValueError("pairs must be [n, 2] on the pools' device")
-    rc = lib().pa_blocks_copy(pools._ptrs, len(pools), pools.elem_bytes, pools.desc, _ptr(pairs), pairs.shape[0],
-                              _ptr(status), _stream(stream))
-    _check("pa_blocks_copy", rc)
+    dev = _pools_of(pools).device_index
+    at = _at(pairs, "pairs", torch.int32, 2, dev)
+    if pairs.size(1) != 2:
+        raise ValueError("pairs must be [n, 2]")
+    _enqueue("pa_blocks_copy", dev, stream, pools._ptrs, len(pools.pools), pools.elem_bytes, pools.desc, at,
+             pairs.size(0), _status_at(status, dev))
 
 
 _LOGITS = {torch.bfloat16: PA_LOGITS_BF16, torch.float32: PA_LOGITS_F32}
@@ -772,33 +810,32 @@ def pa_beam_workspace_bytes(groups: int, beams: int, vocab: int, K: int, dtype: 
     return int(lib().pa_beam_workspace_bytes(groups, beams, vocab, K, _LOGITS[dtype]))
 
 
-@_on_tensors_device
 def pa_beam_select(scores, tokens, parents, logits, cum, finished=None, eos=-1, workspace=None, stream=None):
     """The K best of beams x vocabulary for every request: logits [groups * beams, vocab] (rows may be
     strided), cum [groups, beams], finished uint8 [groups, beams]; scores, tokens, parents [groups, K]."""
-    if logits.dtype not in _LOGITS:
+    dev = _device_of(logits, "logits")
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
-    if logits.dim() != 2 or not logits.is_cuda or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be a CUDA tensor [groups * beams, vocab] with contiguous rows")
-    _need(cum, "cum", torch.float32, 2)
-    _need(scores, "scores", torch.float32, 2)
-    _need(tokens, "tokens", torch.int32, 2)
-    _need(parents, "parents", torch.int32, 2)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.size(1) > 1):
+        raise ValueError("logits must be [groups * beams, vocab] with contiguous rows")
+    args = (_at(scores, "scores", torch.float32, 2, dev), _at(tokens, "tokens", torch.int32, 2, dev),
+            _at(parents, "parents", torch.int32, 2, dev))
+    at_cum = _at(cum, "cum", torch.float32, 2, dev)
     groups, beams = cum.shape
     rows, vocab = logits.shape
-    K = scores.shape[1]
-    if rows != groups * beams or scores.shape[0] != groups or tokens.shape != scores.shape or \
+    K = scores.size(1)
+    if rows != groups * beams or scores.size(0) != groups or tokens.shape != scores.shape or \
             parents.shape != scores.shape:
         raise ValueError("logits must be [groups * beams, vocab]; scores, tokens and parents [groups, K]")
+    done = None
     if finished is not None:
-        _need(finished, "finished", torch.uint8, 2)
+        done = _at(finished, "finished", torch.uint8, 2, dev)
         if finished.shape != cum.shape:
             raise ValueError("finished must be [groups, beams]")
-    stride = vocab if rows == 1 else logits.stride(0)
-    rc = lib().pa_beam_select(_ptr(scores), _ptr(tokens), _ptr(parents), _ptr(logits), _LOGITS[logits.dtype],
-                              stride, _ptr(cum), _ptr(finished), eos, groups, beams, vocab, K, _ptr(workspace),
-                              _space(workspace), _stream(stream))
-    _check("pa_beam_select", rc)
+    _enqueue("pa_beam_select", dev, stream, *args, logits.data_ptr(), kind,
+             logits.stride(0) if rows > 1 else vocab, at_cum, done, eos, groups, beams, vocab, K,
+             *_space_at(workspace, dev))
 
 
 def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
@@ -810,67 +847,60 @@ def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_bloc
 
 
 def _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap, alibi_slopes, window,
-                   prefix_lens, max_prefix):
-    """(q_len, B, Hq, rules) of a scored call; q is [B, Hq, D] or [B, q_len, Hq, D]."""
-    if q.dim() not in (3, 4):
+                   prefix_lens, max_prefix, pool_dtype):
+    """(device, the arguments up to the cache, those from the tables on, the rules); q is [B, Hq, D] or
+    [B, q_len, Hq, D]."""
+    dev = _device_of(q, "q")
+    nd = q.dim()
+    if nd != 3 and nd != 4:
         raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {tuple(q.shape)}")
-    _need(q, "q", torch.bfloat16, q.dim())
-    _need(out, "out", torch.bfloat16, q.dim())
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
-    q_len = q.shape[1] if q.dim() == 4 else 1
-    if out.shape != q.shape or v_cache.shape != k_cache.shape or k_cache.shape[3] != D or \
-            block_tables.shape[0] != B or seq_lens.shape[0] != B:
+    at_q, at_out = _at(q, "q", torch.bfloat16, nd, dev), _at(out, "out", torch.bfloat16, nd, dev)
+    kc, vc = _at(k_cache, "k_cache", pool_dtype, 4, dev), _at(v_cache, "v_cache", pool_dtype, 4, dev)
+    bt = _at(block_tables, "block_tables", torch.int32, 2, dev)
+    sl = _at(seq_lens, "seq_lens", torch.int32, 1, dev)
+    shape = q.shape
+    B, Hq, D = shape[0], shape[-2], shape[-1]
+    nb, bs, hkv, d = k_cache.shape
+    mb = block_tables.size(1)
+    if out.shape != shape or v_cache.shape != k_cache.shape or d != D or block_tables.size(0) != B or \
+            seq_lens.size(0) != B:
         raise ValueError("inconsistent out / q / cache / table shapes")
+    at_lse = slopes = prefix = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, q.dim() - 1)
-        if lse.shape != q.shape[:-1]:
+        at_lse = _at(lse, "lse", torch.float32, nd - 1, dev)
+        if lse.shape != shape[:-1]:
             raise ValueError("lse must have q's shape without its last dimension")
     if alibi_slopes is not None:
-        _need(alibi_slopes, "alibi_slopes", torch.float32, 1)
-        if alibi_slopes.shape[0] != Hq:
+        slopes = _at(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
+        if alibi_slopes.size(0) != Hq:
             raise ValueError("alibi_slopes must be [Hq]")
     if prefix_lens is not None:
-        _need(prefix_lens, "prefix_lens", torch.int32, 1)
-        if prefix_lens.shape[0] != B:
+        prefix = _at(prefix_lens, "prefix_lens", torch.int32, 1, dev)
+        if prefix_lens.size(0) != B:
             raise ValueError("prefix_lens must be [B]")
         if max_prefix is None:
-            max_prefix = block_tables.shape[1] * k_cache.shape[1]
-    return q_len, B, Hq, ScoreRules(softcap, None if alibi_slopes is None else alibi_slopes.data_ptr(), window,
-                                    None if prefix_lens is None else prefix_lens.data_ptr(), max_prefix or 0)
+            max_prefix = mb * bs
+    return dev, (at_out, at_lse, at_q, shape[1] if nd == 4 else 1, kc, vc, CacheDesc(nb, bs, hkv, d)), \
+        (bt, mb, sl, B, Hq), ScoreRules(softcap, slopes, window, prefix, max_prefix or 0)
 
 
-@_on_tensors_device
 def pa_decode_scored(out, lse, q, k_cache, v_cache, block_tables, seq_lens, scale, softcap=0.0,
                      alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None, num_splits=0,
                      workspace=None, status=None, stream=None):
     """Split-KV decode (q [B, Hq, D]) or causal multi-query decode (q [B, q_len, Hq, D]) with capped
     scores, a distance bias, a sliding window and a prefix that every query sees.  max_prefix: a bound
     on prefix_lens (default: the table's tokens)."""
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    q_len, B, Hq, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
-                                         alibi_slopes, window, prefix_lens, max_prefix)
-    rc = lib().pa_decode_scored(_ptr(out), _ptr(lse), _ptr(q), q_len, _ptr(k_cache), _ptr(v_cache),
-                                cache_desc(k_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
-                                B, Hq, scale, ctypes.byref(rules), num_splits, _ptr(workspace),
-                                _space(workspace), _ptr(status), _stream(stream))
-    _check("pa_decode_scored", rc)
+    dev, head, tail, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
+                                            alibi_slopes, window, prefix_lens, max_prefix, torch.bfloat16)
+    _enqueue("pa_decode_scored", dev, stream, *head, *tail, scale, ctypes.byref(rules), num_splits,
+             *_space_at(workspace, dev), _status_at(status, dev))
 
 
-@_on_tensors_device
 def pa_decode_scored_fp8(out, lse, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
                          softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None,
                          num_splits=0, workspace=None, status=None, stream=None):
     """pa_decode_scored over uint8 e4m3 pools with per-pool scales."""
-    _need_pool8(k_cache, "k_cache")
-    _need_pool8(v_cache, "v_cache")
-    q_len, B, Hq, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
-                                         alibi_slopes, window, prefix_lens, max_prefix)
-    rc = lib().pa_decode_scored_fp8(_ptr(out), _ptr(lse), _ptr(q), q_len, _ptr(k_cache), _ptr(v_cache),
-                                    cache_desc(k_cache), k_scale, v_scale, _ptr(block_tables),
-                                    block_tables.shape[1], _ptr(seq_lens), B, Hq, scale, ctypes.byref(rules),
-                                    num_splits, _ptr(workspace), _space(workspace), _ptr(status),
-                                    _stream(stream))
-    _check("pa_decode_scored_fp8", rc)
+    dev, head, tail, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
+                                            alibi_slopes, window, prefix_lens, max_prefix, torch.uint8)
+    _enqueue("pa_decode_scored_fp8", dev, stream, *head, k_scale, v_scale, *tail, scale, ctypes.byref(rules),
+             num_splits, *_space_at(workspace, dev), _status_at(status, dev))
