@@ -663,8 +663,8 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
  * one pass over the logits.
  * logits: device, row r = group * beams + w at r * row_stride elements, bf16
  * (PA_LOGITS_BF16) or fp32 (PA_LOGITS_F32), 16-byte aligned base, row_stride >= vocab
- * (rows need no alignment of their own).  -inf excludes an entry; NaN counts as
- * -inf; a +inf leaves its beam without candidates.  cum: device fp32
+ * (rows need no alignment of their own).  -inf excludes an entry; a NaN or +inf
+ * leaves its beam without candidates.  cum: device fp32
  * [groups, beams], the beams' scores so far (-inf: no candidates).  finished:
  * device bytes [groups, beams] or NULL: a finished beam's one continuation is
  * (eos, cum), and its logits are not read; eos in [0, vocab).

@@ -6,11 +6,11 @@
 // Within a row the scores are ordered as the logits, so one pass over a
 // row's logits gives both its (max, sum) and its K largest logits; lse enters
 // only when the rows of a request are joined.  A CTA takes a slice of a row, in chunks
-// that it holds in registers: 4 16-byte vectors per thread, all in flight at once.
-// The K-th largest of the first chunk's thread maxima bounds the K-th largest
+// of 4 16-byte vectors per thread.
+// What K of the first chunk's thread maxima reach bounds the K-th largest
 // value from below, so that only about K of a chunk's 8192 values ever leave the
-// registers, into a pool in shared memory; no warp waits for another until the
-// pool is a quarter full, when its K best raise the bound.  The last CTA of a
+// registers, into a pool in shared memory, whose K best raise the bound after
+// 1, 2, 4, ... chunks; between those looks no warp waits for another.  The last CTA of a
 // request to finish joins its lists.
 //
 // Sums: exp in fp32 from x - max (exact for bf16), fp32 sums of 8 per vector
@@ -30,11 +30,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;                      // 16-byte vectors per thread and chunk
 constexpr int kChunkVecs = kThreads * kVecs;
+constexpr int kWarpVecs = 32 * kVecs;
+constexpr int kStages = 3;                    // chunks of a warp's ring
+constexpr int kRingBytes = kThreads / 32 * kStages * (kWarpVecs + 1) * 16;
 constexpr int kMaxK = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxJoin = 4096;                // candidates a request's join holds
 constexpr int kPool = 2 * kThreads;            // candidates of a slice at a time
-constexpr int kTargetCtas = 8 * 152;          // slices: about 8 CTAs per SM
+constexpr int kTargetCtas = 8 * 152;          // slices: about two waves of 4 CTAs per SM
 constexpr int kMinSliceVecs = 2 * kThreads;   // and no smaller than two vectors per thread
 
 template <int N>
@@ -49,16 +52,6 @@ struct Vec {  // a 16-byte vector of logits
     // bits of the order-preserving key that a value can differ in: the top ones
     static constexpr int kKeyLow = k16 ? 16 : 0;
     static constexpr uint32_t kFill = k16 ? 0xff80ff80u : 0xff800000u;  // -inf
-    // NaN -> -inf, two bf16 values or one fp32
-    __device__ static uint32_t clean(uint32_t w) {
-        if constexpr (k16) {
-            const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w),
-                                             __nv_bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80)));
-            return *reinterpret_cast<const uint32_t *>(&x);
-        } else {
-            return __float_as_uint(fmaxf(__uint_as_float(w), -INFINITY));
-        }
-    }
     __device__ static float get(const uint4 &v, int e) {
         const uint32_t w = (&v.x)[k16 ? e >> 1 : e];
         if constexpr (k16) return e & 1 ? bf16hi(w) : bf16lo(w);
@@ -101,13 +94,16 @@ __device__ __forceinline__ double key_value(uint64_t k) {
     return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
 }
 
-struct Candidate {
-    float x;
-    int32_t v;  // vocabulary entry, -1: none
-};
-__device__ __forceinline__ bool before(const Candidate &a, const Candidate &b) {
-    return a.x > b.x || (a.x == b.x && a.v < b.v);
+// A candidate of a slice as one number: its logit's order, then the lower
+// vocabulary entry first.  0: none.
+__device__ __forceinline__ uint64_t candidate(float x, int v) {
+    return static_cast<uint64_t>(order_key(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(v));
 }
+__device__ __forceinline__ float candidate_value(uint64_t c) {
+    const uint32_t k = static_cast<uint32_t>(c >> 32);
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ int candidate_entry(uint64_t c) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(c)); }
 
 struct BeamArgs {
     float *scores;
@@ -121,12 +117,17 @@ struct BeamArgs {
     int32_t *tickets;      // [groups], zero between calls
     float *part_max;       // [rows, slices]
     double *part_sum;      // [rows, slices]
-    Candidate *part_list;  // [rows, slices, K]
+    uint64_t *part_list;   // [rows, slices, K] candidates
 };
 
 // A row's vectors: vector i holds entries i E .. i E + E - 1, whatever the row's
 // alignment, so that equal rows give equal sums to the last bit.  A row that starts
 // `skew` bytes past a 16-byte boundary takes each vector from two aligned ones.
+//
+// Warp w's share of a chunk is vectors c0 + w kWarpVecs + j 32 + lane (j < kVecs),
+// which it streams through its own ring in shared memory, two chunks ahead
+// (cp.async; only the warp waits for it): 128 KB in flight per SM, where loads to
+// registers, one chunk at a time, kept 64 KB in flight half of the time.
 template <typename T>
 struct Row {
     static constexpr int E = Vec<T>::kElems;
@@ -140,71 +141,107 @@ struct Row {
         grid = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(x) - skew);
         whole = skew ? (vocab + skew / static_cast<int>(sizeof(T))) / E - 1 : vocab / E;
     }
-    template <int W>
-    __device__ void load_skewed(uint4 (&raw)[kVecs], int i0, int end) const {  // skew = 4 W + (0 or 2) bytes
-        const int bits = (skew & 3) * 8;
+    // This warp's share of the chunk at c0 (vectors below `end`) on its way to `slot`.
+    __device__ __forceinline__ void fetch(uint4 *slot, int c0, int end) const {
+        const int lane = threadIdx.x & 31, first = c0 + static_cast<int>(threadIdx.x >> 5) * kWarpVecs;
+        int stop = min(end, whole);        // aligned vectors needed
+        stop += skew && stop > 0 ? 1 : 0;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int i = i0 + j * kThreads;
-            if (i >= end || i >= whole) continue;
-            const uint4 lo = __ldg(grid + i), hi = __ldg(grid + i + 1);
+            const int i = j * 32 + lane;
+            if (first + i < stop) cp_async_16(slot + i, grid + first + i);
+        }
+        if (lane == 0 && skew && first + kWarpVecs < stop) cp_async_16(slot + kWarpVecs, grid + first + kWarpVecs);
+    }
+    template <int W>
+    __device__ __forceinline__ void take_skewed(uint4 (&raw)[kVecs], const uint4 *slot) const {  // skew = 4 W + (0 or 2)
+        const int lane = threadIdx.x & 31, bits = (skew & 3) * 8;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const uint4 lo = slot[j * 32 + lane], hi = slot[j * 32 + lane + 1];
             const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             raw[j] = make_uint4(__funnelshift_r(w[W], w[W + 1], bits), __funnelshift_r(w[W + 1], w[W + 2], bits),
                                 __funnelshift_r(w[W + 2], w[W + 3], bits), __funnelshift_r(w[W + 3], w[W + 4], bits));
         }
     }
-    // Vectors i0, i0 + kThreads, ... below end, NaN as -inf, and -inf past the end.
-    __device__ void load(uint4 (&raw)[kVecs], int i0, int end) const {
+    // The chunk's vectors of this thread, fetched before: -inf past the end, and
+    // the row's end entry by entry.
+    __device__ __forceinline__ void take(uint4 (&raw)[kVecs], const uint4 *slot, int c0, int end) const {
         using V = Vec<T>;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) raw[j] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
         if (skew == 0) {
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int i = i0 + j * kThreads;
-                if (i < end && i < whole) raw[j] = __ldcs(grid + i);
-            }
+            for (int j = 0; j < kVecs; ++j) raw[j] = slot[j * 32 + (threadIdx.x & 31)];
         } else if (skew < 4) {
-            load_skewed<0>(raw, i0, end);
+            take_skewed<0>(raw, slot);
         } else if (skew < 8) {
-            load_skewed<1>(raw, i0, end);
+            take_skewed<1>(raw, slot);
         } else if (skew < 12) {
-            load_skewed<2>(raw, i0, end);
+            take_skewed<2>(raw, slot);
         } else {
-            load_skewed<3>(raw, i0, end);
+            take_skewed<3>(raw, slot);
         }
-        if (i0 + (kVecs - 1) * kThreads >= whole) {  // the row's end: entry by entry
+        if (c0 + kChunkVecs <= min(end, whole)) return;   // (the same for the CTA)
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int i = i0 + j * kThreads;
-                if (i < whole || i >= end) continue;
-                uint32_t w[4] = {V::kFill, V::kFill, V::kFill, V::kFill};
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = vector_of(c0, j);
+            if (i < end && i < whole) continue;
+            uint32_t w[4] = {V::kFill, V::kFill, V::kFill, V::kFill};
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (i * E + e < vocab) V::put(w, e, x[i * E + e]);
-                raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int e = 0; e < E; ++e)
+                if (i < end && i * E + e < vocab) V::put(w, e, x[i * E + e]);
+            raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-            raw[j] = make_uint4(V::clean(raw[j].x), V::clean(raw[j].y), V::clean(raw[j].z), V::clean(raw[j].w));
+    }
+    __device__ __forceinline__ static int vector_of(int c0, int j) {
+        return c0 + static_cast<int>(threadIdx.x >> 5) * kWarpVecs + j * 32 + static_cast<int>(threadIdx.x & 31);
     }
 };
 
-// The largest key that at least K of the threads' keys reach (0: fewer than K
-// do), bit by bit from the top; a CTA-wide count per bit.
+// A key that at least K of the threads' keys reach (0: fewer than K are not 0).
+// Each warp's ceil(K / 8)-th largest, and the lowest of the eight: two barriers, and
+// for values in no order about twice as many keys reach it as the K-th largest.
+// Where a warp has too few keys, or values that rise along the row let far more
+// reach it, the K-th largest, bit by bit from the top with a CTA-wide count per bit.
 template <int kKeyLow>
-__device__ __forceinline__ uint32_t kth_key(uint32_t mine, int K) {
-    uint32_t key = 0u;
+__device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *warp_keys) {
+    const int lane = threadIdx.x & 31;
+    uint32_t left = mine, best = 0;
+    for (int r = 0; r < (K + kThreads / 32 - 1) / (kThreads / 32); ++r) {
+        best = __reduce_max_sync(0xffffffffu, left);
+        const uint32_t who = __ballot_sync(0xffffffffu, left == best);
+        if (lane == __ffs(who) - 1) left = 0;
+    }
+    if (lane == 0) warp_keys[threadIdx.x >> 5] = best;
+    __syncthreads();
+    uint32_t key = warp_keys[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) key = min(key, warp_keys[i]);
+    if (__syncthreads_count(key && mine >= key) <= 3 * K + 16 && key) return key;
+    key = 0;
     for (int bit = 31; bit >= kKeyLow; --bit)
         if (__syncthreads_count(mine >= (key | 1u << bit)) >= K) key |= 1u << bit;
     return key;
 }
 
+// How many of pool[0 .. n) come before c; four at a time, so the pool has room for 3
+// more entries, which the caller has set to 0.
+__device__ __forceinline__ int place_of(uint64_t c, const uint64_t *pool, int n) {
+    int place = 0;
+#pragma unroll 2
+    for (int j = 0; j < n; j += 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(pool + j);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(pool + j + 2);
+        place += (a.x > c) + (a.y > c) + (b.x > c) + (b.y > c);
+    }
+    return place;
+}
+
 // pool[0 .. n) reduced to its min(n, K) first candidates, in order: an entry's
-// place is the number of entries before it.  n <= 2 kThreads.
-__device__ __forceinline__ int keep_first(Candidate *pool, int n, int K) {
-    Candidate c[2];
+// place is the number of entries before it.  n <= kPool = 2 kThreads.
+__device__ __noinline__ int keep_first(uint64_t *pool, int n, int K) {
+    if (threadIdx.x < 3) pool[n + threadIdx.x] = 0;
+    __syncthreads();
+    uint64_t c[2];
     int place[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -212,9 +249,7 @@ __device__ __forceinline__ int keep_first(Candidate *pool, int n, int K) {
         place[u] = K;
         if (i < n) {
             c[u] = pool[i];
-            int before_it = 0;
-            for (int j = 0; j < n; ++j) before_it += before(pool[j], c[u]);
-            place[u] = before_it;
+            place[u] = place_of(c[u], pool, n);
         }
     }
     __syncthreads();
@@ -225,13 +260,37 @@ __device__ __forceinline__ int keep_first(Candidate *pool, int n, int K) {
     return min(n, K);
 }
 
+// A vector's values from `cut` on (with `strict`: above it) to the pool.  Out of
+// line: one or two lanes of a warp get here per chunk, mostly for one value, and one
+// copy of the loop stays in the instruction cache where 32 unrolled ones did not.
+template <typename T>
+__device__ __noinline__ void append(uint4 v, int entry, float cut, bool strict, uint64_t *pool, int *count) {
+    constexpr int E = Vec<T>::kElems;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float x = Vec<T>::get(v, e);
+        hits |= static_cast<uint32_t>(strict ? x > cut : x >= cut) << e;
+    }
+#pragma unroll 1
+    while (hits) {
+        const int e = __ffs(hits) - 1, w = Vec<T>::k16 ? e >> 1 : e;
+        hits &= hits - 1;
+        const uint32_t word = w & 2 ? (w & 1 ? v.w : v.z) : (w & 1 ? v.y : v.x);
+        const float x = !Vec<T>::k16 ? __uint_as_float(word) : e & 1 ? bf16hi(word) : bf16lo(word);
+        const int at = atomicAdd(count, 1);
+        if (at < kPool) pool[at] = candidate(x, entry + e);
+    }
+}
+
 // The K first candidates of vectors [v0, v1) whatever their order: for rows
 // that overfill the pool (long runs of equal values, or values that rise along the
 // row).  Each chunk's exact K-th largest value by bisection over its key, then, among
 // the values equal to it, the lowest entries by bisection over the entry.
 // pool: the list so far in [0, kept), the chunk's share after it.
 template <typename T>
-__device__ __noinline__ int exact_slice(const Row<T> &row, int v0, int v1, int K, Candidate *pool, int *count) {
+__device__ __noinline__ int exact_slice(const Row<T> &row, int v0, int v1, int K, uint64_t *pool, int *count,
+                                        uint4 *slot) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
     const int tid = threadIdx.x;
@@ -239,12 +298,17 @@ __device__ __noinline__ int exact_slice(const Row<T> &row, int v0, int v1, int K
     float floor = -INFINITY;   // values at or below it are not among the K largest
     for (int c0 = v0; c0 < v1; c0 += kChunkVecs) {
         uint4 raw[kVecs];
-        row.load(raw, c0 + tid, v1);
+        __syncwarp();
+        row.fetch(slot, c0, v1);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+        row.take(raw, slot, c0, v1);
         auto each = [&](auto &&f) {  // f(value, vocabulary entry) of this thread's values above the floor
             for (int j = 0; j < kVecs; ++j)
                 for (int e = 0; e < E; ++e) {
                     const float v = V::get(raw[j], e);
-                    if (v > floor) f(v, (c0 + j * kThreads + tid) * E + e);
+                    if (v > floor) f(v, Row<T>::vector_of(c0, j) * E + e);
                 }
         };
         auto total = [&](auto &&pred) {
@@ -282,11 +346,11 @@ __device__ __noinline__ int exact_slice(const Row<T> &row, int v0, int v1, int K
         each([&](float v, int i) {
             if (!(v > kth || (v == kth && i <= last))) return;
             const int at = atomicAdd(count, 1);
-            if (at < kPool) pool[at] = Candidate{v, i};
+            if (at < kPool) pool[at] = candidate(v, i);
         });
         __syncthreads();
         kept = keep_first(pool, min(*count, kPool), K);
-        if (kept == K) floor = pool[K - 1].x;
+        if (kept == K) floor = candidate_value(pool[K - 1]);
     }
     return kept;
 }
@@ -295,12 +359,15 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
-    extern __shared__ uint64_t join_keys[];  // [beams * slices * K], then as many int32 (the join)
-    __shared__ Candidate pool[kPool];        // candidates for the slice's K largest
+    extern __shared__ __align__(16) uint64_t dyn_smem[];  // the warps' rings; then 24 bytes per entry of the join
+    __shared__ uint32_t warp_keys[kThreads / 32];
+    __shared__ __align__(16) uint64_t pool[kPool + 4];  // candidates for the slice's K largest
     __shared__ int count, ticket;
     __shared__ float red_max[kThreads / 32];
     __shared__ double red_sum[kThreads / 32];
-    __shared__ double lse[kMaxBeams];
+    __shared__ double lse[kMaxBeams], beam_cum[kMaxBeams];
+    __shared__ bool beam_done[kMaxBeams];
+    __shared__ uint64_t bound;
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -313,16 +380,30 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         const int vecs = (a.vocab + E - 1) / E;
         const int per = (vecs + a.slices - 1) / a.slices;
         const int v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
-        const int period = max(1, kPool / 3 / K);   // chunks between looks at the pool
+        const int period = max(1, kPool / 3 / K);   // chunks between looks at the pool, at most
+        int look = 0;                               // the chunk after which the next one is
         float m = -INFINITY, sum = 0.f;   // this thread's maximum and sum of exp(x - m)
         float cut = -INFINITY;            // values below it, or with `strict` at it, are not among the K largest
         bool strict = true, overfull = false;
         if (tid == 0) count = 0;
         __syncthreads();
+        uint4(*ring)[kWarpVecs + 1] = reinterpret_cast<uint4(*)[kWarpVecs + 1]>(
+            reinterpret_cast<uint4 *>(dyn_smem) + warp * kStages * (kWarpVecs + 1));   // [kStages], this warp's
+#pragma unroll
+        for (int u = 0; u < kStages - 1; ++u) {
+            if (v0 + u * kChunkVecs < v1) row.fetch(ring[u], v0 + u * kChunkVecs, v1);
+            cp_async_commit();
+        }
         int chunk = 0;
         for (int c0 = v0; c0 < v1; c0 += kChunkVecs, ++chunk) {
+            const int next = c0 + (kStages - 1) * kChunkVecs;
+            if (next < v1) row.fetch(ring[(chunk + kStages - 1) % kStages], next, v1);
+            cp_async_commit();
+            cp_async_wait<kStages - 1>();
+            __syncwarp();    // (every lane's copies of this chunk have landed)
             uint4 raw[kVecs];
-            row.load(raw, c0 + tid, v1);
+            row.take(raw, ring[chunk % kStages], c0, v1);
+            __syncwarp();    // (and are read: the next fetch may go there)
             float vmax[kVecs], cmax = -INFINITY;
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
@@ -334,22 +415,27 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 sum *= fast_exp2((m - cmax) * 1.4426950408889634f);  // (m = -inf: 0)
                 m = cmax;
             }
-            if (m > -INFINITY) {
+            const float minus = m > -INFINITY ? -m : 0.f;   // (a NaN goes into the sum all the same)
 #pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    float s[E];
+            for (int j = 0; j < kVecs; ++j) {
+                float e2[E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) s[e] = fast_exp2((V::get(raw[j], e) - m) * 1.4426950408889634f);
-#pragma unroll
-                    for (int o = E / 2; o > 0; o >>= 1)
-#pragma unroll
-                        for (int e = 0; e < o; ++e) s[e] += s[e + o];
-                    sum += s[0];
+                for (int e = 0; e < E; e += 2) {
+                    const uint64_t t = mul2(add2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(minus, minus)),
+                                            pack2(1.4426950408889634f, 1.4426950408889634f));
+                    unpack2(t, e2[e], e2[e + 1]);
+                    e2[e] = fast_exp2(e2[e]);
+                    e2[e + 1] = fast_exp2(e2[e + 1]);
                 }
+#pragma unroll
+                for (int o = E / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int e = 0; e < o; ++e) e2[e] += e2[e + o];
+                sum += e2[0];
             }
-            // ---- candidates: the first chunk's bound is the K-th largest of its threads' maxima
+            // ---- candidates: those that reach what K of the first chunk's thread maxima reach
             if (chunk == 0) {
-                const uint32_t key = kth_key<V::kKeyLow>(cmax > -INFINITY ? order_key(cmax) : 0u, K);
+                const uint32_t key = reached_by<V::kKeyLow>(cmax > -INFINITY ? order_key(cmax) : 0u, K, warp_keys);
                 if (key) {
                     cut = key_value<V::kKeyLow>(key);
                     strict = false;
@@ -358,29 +444,22 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             auto passes = [&](float v) { return strict ? v > cut : v >= cut; };
             if (passes(cmax)) {
 #pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    if (!passes(vmax[j])) continue;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float v = V::get(raw[j], e);
-                        if (!passes(v)) continue;
-                        const int at = atomicAdd(&count, 1);
-                        if (at < kPool) pool[at] = Candidate{v, (c0 + j * kThreads + tid) * E + e};
-                    }
-                }
+                for (int j = 0; j < kVecs; ++j)
+                    if (passes(vmax[j])) append<T>(raw[j], Row<T>::vector_of(c0, j) * E, cut, strict, pool, &count);
             }
-            if (chunk % period == period - 1) {  // raise the bound before the pool fills
+            if (chunk == look) {   // the K best so far raise the bound, before the pool fills
+                look += min(chunk + 1, period);
                 __syncthreads();
                 const int n = count;
                 __syncthreads();
                 if (n > kPool) {
                     overfull = true;
                     cut = INFINITY, strict = true;
-                } else if (n > kPool / 4) {
+                } else if (n > K) {
                     const int kept = keep_first(pool, n, K);
                     if (tid == 0) count = kept;
                     if (kept == K) {
-                        cut = pool[K - 1].x;   // (later entries of an equal value come after it)
+                        cut = candidate_value(pool[K - 1]);   // (later entries of an equal value come after it)
                         strict = true;
                     }
                     __syncthreads();
@@ -389,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         }
         __syncthreads();
         int kept;
-        if (overfull || count > kPool) kept = exact_slice<T>(row, v0, v1, K, pool, &count);
+        if (overfull || count > kPool) kept = exact_slice<T>(row, v0, v1, K, pool, &count, ring[0]);
         else kept = keep_first(pool, count, K);
         // ---- the slice's maximum, sum and list
         float top = m;
@@ -399,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, red_max[i]);
-        double z = m > -INFINITY ? static_cast<double>(sum * fast_exp2((m - top) * 1.4426950408889634f)) : 0.0;
+        double z = m > -INFINITY ? sum * fast_exp2((m - top) * 1.4426950408889634f) : sum;  // (sum: 0 or NaN)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) red_sum[warp] = z;
@@ -411,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             a.part_max[part] = top;
             a.part_sum[part] = s;
         }
-        if (tid < K) a.part_list[part * K + tid] = tid < kept ? pool[tid] : Candidate{-INFINITY, -1};
+        if (tid < K) a.part_list[part * K + tid] = tid < kept ? pool[tid] : 0;
     }
 
     // ---- the request's last CTA joins its rows' slices
@@ -423,79 +502,89 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     __threadfence();
     if (tid == 0) a.tickets[group] = 0;
     const int first_row = group * a.beams;
+    // ---- everything the slices left, in one round trip
+    const int lists = a.beams * a.slices, entries = lists * K;
+    uint64_t *keys = dyn_smem;                                      // [entries] candidates, then scores' keys
+    uint64_t *top_keys = keys + entries;                            // [entries] those that the bound leaves
+    int *index = reinterpret_cast<int *>(top_keys + entries);       // [entries] place in beams x vocabulary
+    int *top_index = index + entries;                               // [entries]
+    double *slice_sum = reinterpret_cast<double *>(top_keys);       // [lists], then the maxima
+    float *slice_max = reinterpret_cast<float *>(index);            // [lists]
+    const int64_t part0 = static_cast<int64_t>(first_row) * a.slices;
+    for (int i = tid; i < entries; i += kThreads)
+        keys[i] = __ldcg(reinterpret_cast<const unsigned long long *>(a.part_list) + part0 * K + i);
+    for (int l = tid; l < lists; l += kThreads) {
+        slice_max[l] = __ldcg(a.part_max + part0 + l);
+        slice_sum[l] = __ldcg(a.part_sum + part0 + l);
+    }
     if (tid < a.beams) {
-        double M = -INFINITY, z = 0.0;
-        const int64_t part = static_cast<int64_t>(first_row + tid) * a.slices;
-        if (!(a.finished && a.finished[first_row + tid])) {
-            for (int s = 0; s < a.slices; ++s) M = fmax(M, static_cast<double>(__ldcg(a.part_max + part + s)));
-            for (int s = 0; s < a.slices; ++s) {
-                const double ms = __ldcg(a.part_max + part + s);
-                if (ms > -INFINITY) z += __ldcg(a.part_sum + part + s) * exp(ms - M);
-            }
+        beam_cum[tid] = a.cum[first_row + tid];
+        beam_done[tid] = a.finished && a.finished[first_row + tid];
+    }
+    if (tid == 0) count = 0, bound = 1;
+    __syncthreads();
+    if (tid < a.beams) {
+        float M = -INFINITY;
+        double z = 0.0;
+        if (!beam_done[tid]) {
+            for (int s = tid * a.slices; s < (tid + 1) * a.slices; ++s) M = fmaxf(M, slice_max[s]);
+            for (int s = tid * a.slices; s < (tid + 1) * a.slices; ++s)
+                z += slice_sum[s] * (slice_max[s] > -INFINITY ? fast_exp2((slice_max[s] - M) * 1.4426950408889634f) : 1.f);
         }
         lse[tid] = M > -INFINITY ? M + log(z) : INFINITY;
     }
-    if (tid == 0) count = 0;
     __syncthreads();
-    // key of list l's entry k (0: none): the score's order; *index its place in beams x vocabulary
-    auto entry = [&](int l, int k, int *index) -> uint64_t {
-        const int w = l / a.slices;
-        const double cum = a.cum[first_row + w];
-        double score;
-        if (a.finished && a.finished[first_row + w]) {  // its one continuation
-            if (l % a.slices || k) return 0;
-            *index = w * a.vocab + a.eos;
-            score = cum;
-        } else {
-            const int2 c = __ldcg(reinterpret_cast<const int2 *>(
-                a.part_list + (static_cast<int64_t>(first_row) * a.slices + l) * K + k));
-            if (c.y < 0) return 0;
-            *index = w * a.vocab + c.y;
-            score = cum + (static_cast<double>(__int_as_float(c.x)) - lse[w]);
+    // ---- every candidate's score, as a key (0: none)
+    for (int i = tid; i < entries; i += kThreads) {
+        const int l = i / K, w = l / a.slices;
+        const uint64_t c = keys[i];
+        uint64_t key = 0;
+        double score = -INFINITY;
+        if (beam_done[w]) {  // its one continuation
+            if (l % a.slices == 0 && i % K == 0) score = beam_cum[w];
+            index[i] = w * a.vocab + a.eos;
+        } else if (c) {
+            score = beam_cum[w] + (static_cast<double>(candidate_value(c)) - lse[w]);
+            index[i] = w * a.vocab + candidate_entry(c);
         }
-        return score > -INFINITY ? order_key(score) : 0;  // (not -inf, not NaN)
-    };
-    const int lists = a.beams * a.slices;
-    int *join_index = reinterpret_cast<int *>(join_keys + lists * K);
+        if (score > -INFINITY) key = order_key(score);  // (not -inf, not NaN)
+        keys[i] = key;
+    }
+    __syncthreads();
     // The K-th largest list head bounds the K-th best score from below.
-    uint64_t least = 1;
     if (lists > K) {
-        for (int l = tid; l < lists; l += kThreads) join_keys[l] = entry(l, 0, join_index + l);
-        __syncthreads();
-        __shared__ uint64_t bound;
-        if (tid == 0) bound = 1;
-        __syncthreads();
         for (int l = tid; l < lists; l += kThreads) {
-            const uint64_t k = join_keys[l];
+            const uint64_t k = keys[l * K];
             int place = 0;
-            for (int j = 0; j < lists; ++j) place += join_keys[j] > k || (join_keys[j] == k && j < l);
+#pragma unroll 8
+            for (int j = 0; j < lists; ++j)
+                place += static_cast<int>(keys[j * K] > k) | (static_cast<int>(keys[j * K] == k) & static_cast<int>(j < l));
             if (place == K - 1 && k) bound = k;
         }
         __syncthreads();
-        least = bound;
-        __syncthreads();
     }
-    for (int i = tid; i < lists * K; i += kThreads) {
-        int index;
-        const uint64_t k = entry(i / K, i % K, &index);
-        if (k >= least) {
+    for (int i = tid; i < entries; i += kThreads) {
+        const uint64_t k = keys[i];
+        if (k >= bound) {
             const int at = atomicAdd(&count, 1);
-            join_keys[at] = k;
-            join_index[at] = index;
+            top_keys[at] = k;
+            top_index[at] = index[i];
         }
     }
     __syncthreads();
     const int n = count;
     const int64_t out = static_cast<int64_t>(group) * K;
     for (int i = tid; i < n; i += kThreads) {
-        const uint64_t k = join_keys[i];
-        const int index = join_index[i];
+        const uint64_t k = top_keys[i];
+        const int at = top_index[i];
         int place = 0;
-        for (int j = 0; j < n; ++j) place += join_keys[j] > k || (join_keys[j] == k && join_index[j] < index);
+#pragma unroll 8
+        for (int j = 0; j < n; ++j)   // (no branch: short-circuits cost 50 ns per entry)
+            place += static_cast<int>(top_keys[j] > k) | (static_cast<int>(top_keys[j] == k) & static_cast<int>(top_index[j] < at));
         if (place < K) {
             a.scores[out + place] = static_cast<float>(key_value(k));
-            a.tokens[out + place] = index % a.vocab;
-            a.parents[out + place] = first_row + index / a.vocab;
+            a.tokens[out + place] = at % a.vocab;
+            a.parents[out + place] = first_row + at / a.vocab;
         }
     }
     for (int i = n + tid; i < K; i += kThreads) {  // fewer candidates than K
@@ -507,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
 
 int elem_size(int32_t type) { return type == PA_LOGITS_BF16 ? 2 : type == PA_LOGITS_F32 ? 4 : 0; }
 
-// Slices of a row: enough CTAs to fill the GPU several times over, each with
-// at least two vectors per thread, and no more lists than the join holds.
+// Slices of a row: two waves of CTAs (256 rows: 5 slices beat 2, 4, 8 and 12), each with at
+// least two vectors per thread, and no more lists than the join holds.
 int slices_of(int64_t rows, int beams, int vocab, int K, int elem) {
     const int64_t vecs = (static_cast<int64_t>(vocab) * elem + 15) / 16;
     int64_t s = std::min((vecs + kMinSliceVecs - 1) / kMinSliceVecs, (kTargetCtas + rows - 1) / rows);
@@ -569,15 +658,15 @@ int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void 
     ws += pa::up(4 * parts);
     a.part_sum = reinterpret_cast<double *>(ws);
     ws += pa::up(8 * parts);
-    a.part_list = reinterpret_cast<pa::Candidate *>(ws);
-    const int smem = beams * a.slices * K * 12;
+    a.part_list = reinterpret_cast<uint64_t *>(ws);
+    const int smem = std::max(pa::kRingBytes, beams * a.slices * K * 24);
     auto kern = logits_type == PA_LOGITS_BF16 ? pa::beam_select_kernel<__nv_bfloat16> : pa::beam_select_kernel<float>;
     static std::atomic<uint64_t> smem_attr_done[2];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done[logits_type].load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::kMaxJoin * 12) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::kMaxJoin * 24) != cudaSuccess)
             return PA_ECUDA;
         smem_attr_done[logits_type].fetch_or(bit, std::memory_order_release);
     }

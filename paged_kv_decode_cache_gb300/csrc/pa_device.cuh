@@ -173,6 +173,11 @@ __device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gmem_src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src)
                  : "memory");
 }
+// The same for 16 bytes, both addresses aligned to them, past L1.
+__device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gmem_src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -196,6 +201,31 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// Two fp32 lanes per instruction (fma.rn.f32x2 and its like).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // Two bf16 packed in a 32-bit word -> two floats (exact: bf16 is the top half of fp32).
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -217,14 +247,32 @@ __device__ __forceinline__ uint2 e4m3x8_from_bf16(const uint4 &in, float scale) 
     return make_uint2(out[0], out[1]);
 }
 
-// The same for 8 fp32 values (keys turned by their rotary angle).
-__device__ __forceinline__ uint2 e4m3x8_from_f32(const float (&f)[8], float scale) {
-    uint32_t out[2] = {0u, 0u};
+// The same for 8 fp32 values (keys turned by their rotary angle), faster: a
+// product with 1 / scale (at most 2 units in the last place off the quotient)
+// gives the same code unless it lies that near the middle between two codes.
+// Those, and quotients below the smallest normal code (whose steps have another
+// width; NaN too), are divided.  inv: 1 / scale, or NaN for a scale so small or
+// large that the product could leave fp32's normal range (every quotient is
+// then divided).  A rounding middle has the bits 100..0 below the three
+// mantissa bits that a code keeps.
+__device__ __forceinline__ uint2 e4m3x8_from_f32(const float (&f)[8], float scale, float inv) {
+    float q[8];
+    bool divide = false;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        out[k >> 2] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(f[k] / scale, __NV_SATFINITE, __NV_E4M3))
-                       << (8 * (k & 3));
-    return make_uint2(out[0], out[1]);
+    for (int k = 0; k < 8; ++k) {
+        q[k] = f[k] * inv;
+        const uint32_t off = (__float_as_uint(q[k]) & 0xfffffu) - (0x80000u - 4u);
+        divide |= off <= 8u || !(fabsf(q[k]) >= 0x1p-6f);
+    }
+    if (divide) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = f[k] / scale;
+    }
+    uint32_t out[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        out[k] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * k], q[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(out[0] | out[1] << 16, out[2] | out[3] << 16);
 }
 
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a tile of

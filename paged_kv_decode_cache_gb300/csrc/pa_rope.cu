@@ -32,6 +32,7 @@ struct RopeArgs {
     int32_t *status;
     int hq, hkv, head_dim;
     float k_scale, v_scale;        // FP8 pools
+    float k_inv, v_inv;            // their reciprocals (e4m3x8_from_f32)
 };
 
 // Thread = one unit of 16 elements of one head of q, k or v, for the TB tokens of
@@ -39,11 +40,11 @@ struct RopeArgs {
 // two chunks rot_dim / 2 apart (half layout), or 16 elements in a row
 // (interleaved).  A warp then reads and writes whole 128-byte lines.  The
 // tokens' angles are computed once per CTA, one per thread at a time, while the
-// first loads (up to 4 tokens of each unit) are in flight.
+// first loads (up to 2 tokens of each unit) are in flight.
 template <bool F8, int TB>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
-    constexpr int kAhead = TB < 4 ? TB : 4;                   // tokens loaded at once
+    constexpr int kAhead = TB < 2 ? TB : 2;                   // tokens loaded at once
     __shared__ float2 turn[TB][PA_ROPE_MAX_PAIRS];            // (cos, sin) of the tokens' pairs
     __shared__ int64_t slot_s[TB];                            // -1: not written
     griddep_wait();
@@ -117,10 +118,10 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
                     }
                 }
                 if (F8 && !is_q) {
-                    const float scale = is_v ? a.v_scale : a.k_scale;
+                    const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
                     uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
-                    *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale);
-                    *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale);
+                    *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale, inv);
+                    *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale, inv);
                 } else {
                     __nv_bfloat16 *dst = is_q ? a.q_out + (tok0 + t) * a.q_out_stride + h * a.head_dim
                                               : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
@@ -140,6 +141,8 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
         }
     }
 }
+
+float reciprocal(float scale) { return scale > 0x1p-100f && scale < 0x1p100f ? 1.f / scale : NAN; }
 
 // Tokens per CTA: one where there are few (every SM then has some), eight where
 // there are many.
@@ -186,7 +189,7 @@ int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_
                static_cast<const __nv_bfloat16 *>(k_new), static_cast<const __nv_bfloat16 *>(v_new),
                q_out_stride, q_stride, k_stride, v_stride, positions, slot_mapping, n_tokens,
                static_cast<int64_t>(cache.num_blocks) * cache.block_size, static_cast<uint8_t *>(k_cache),
-               static_cast<uint8_t *>(v_cache), status, Hq, cache.num_kv_heads, cache.head_dim, k_scale, v_scale};
+               static_cast<uint8_t *>(v_cache), status, Hq, cache.num_kv_heads, cache.head_dim, k_scale, v_scale, reciprocal(k_scale), reciprocal(v_scale)};
     const int units = (Hq + 2 * cache.num_kv_heads) * (cache.head_dim / kUnit);
     const int threads = std::min(kMaxThreads, (units + 31) / 32 * 32);
     const cudaError_t e = f8 ? launch_rope<true>(a, *rope, threads, stream) : launch_rope<false>(a, *rope, threads, stream);

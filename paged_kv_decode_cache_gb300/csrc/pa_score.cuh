@@ -48,26 +48,6 @@ __device__ __forceinline__ Seen seen_by(const DecodeParams &p, int b, int L, int
     return s;
 }
 
-// Two fp32 lanes per instruction (fma.rn.f32x2 and its like).
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // c tanh(x / c) in log2 units: x and cap are times log2(e), inv_cap = 1 / cap.
 // With u = x / cap below 0.625, x (1 + u^2 p(u^2)) with a least-squares fit of
 // tanh(u) / u weighted towards its largest error: 6e-8 of the value in fp32.  Most

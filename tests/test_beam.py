@@ -34,9 +34,9 @@ def plain(logits, cum, finished, eos, K):
             if finished is not None and finished[g, w]:
                 found.append((np.array([c]), np.array([w * x.shape[1] + eos])))
                 continue
-            row = np.where(np.isnan(x[g * beams + w]), -np.inf, x[g * beams + w])
+            row = x[g * beams + w]
             top = row.max()
-            if not np.isfinite(top):
+            if not np.isfinite(top):   # (NaN, +inf, or nothing allowed)
                 continue
             s = c + (row - (top + np.log(np.exp(row - top).sum())))
             found.append((s, w * x.shape[1] + np.arange(x.shape[1])))
@@ -132,7 +132,9 @@ def test_finished_dead_and_masked_beams(dtype):
     logits[1] = -math.inf                       # nothing allowed
     logits[2, 2:] = -math.inf                   # two entries allowed
     logits[4] = math.nan                        # a finished beam's logits are not read
-    logits[6, 17] = math.nan                    # counts as -inf
+    logits[6, 17] = math.nan                    # leaves its beam without candidates
+    logits[7, :] = -math.inf                    # so does one among entries that are not allowed
+    logits[7, 4001] = math.nan
     logits[9, 5] = math.inf                     # leaves its beam without candidates
     cum = spread((4, 3), 4)
     cum[2, 0] = -math.inf                       # dead

@@ -259,3 +259,22 @@ def test_wrapper_refuses_what_does_not_fit():
         pa.pa_rope_write(q, q, k, v, pos.long(), slots, kc, vc, rope)
     with pytest.raises(TypeError):
         pa.pa_rope_write(q, q, k, v, pos, slots, kc, vc, {"rot_dim": 64})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1.0, 0.03, 1.0 / 448, 3.3e-5, 7.7, 1e-37, 3e38, 0.02340001])
+def test_fp8_codes_equal_the_cache_write(scale):
+    """Every bf16 value: the values' codes, and the keys' where nothing turns (position 0), are
+    pa_cache_write_fp8's, byte for byte."""
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(128, 4, 128).cuda()
+    finite = torch.where(torch.isfinite(every), every, torch.ones_like(every))
+    slots = torch.randperm(128, generator=torch.Generator().manual_seed(1)).cuda()
+    pools = [torch.zeros(8, 16, 4, 128, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    pa.pa_cache_write_fp8(finite, every, slots, pools[0], pools[1], scale, scale)
+    q = torch.zeros(128, 4, 128, dtype=torch.bfloat16, device="cuda")
+    pa.pa_rope_write_fp8(q, q, finite, every, torch.zeros(128, dtype=torch.int32, device="cuda"), slots, pools[2],
+                         pools[3], scale, scale, pa.pa_rope_init(128, 1e4))
+    torch.cuda.synchronize()
+    assert torch.equal(pools[1], pools[3])
+    # (a turned -0 may come out as +0)
+    assert torch.equal(torch.where(pools[0] == 0x80, 0, pools[0]), torch.where(pools[2] == 0x80, 0, pools[2]))
