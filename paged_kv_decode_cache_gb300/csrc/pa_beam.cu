@@ -6,12 +6,13 @@
 // Within a row the scores are ordered as the logits, so one pass over a
 // row's logits gives both its (max, sum) and its K largest logits; lse enters
 // only when the rows of a request are joined.  A CTA takes a slice of a row, in chunks
-// of 4 16-byte vectors per thread.
-// What K of the first chunk's thread maxima reach bounds the K-th largest
-// value from below, so that only about K of a chunk's 8192 values ever leave the
-// registers, into a pool in shared memory, whose K best raise the bound after
-// 1, 2, 4, ... chunks; between those looks no warp waits for another.  The last CTA of a
-// request to finish joins its lists.
+// of 4 16-byte vectors per thread; a thread's part of a chunk is a group.  The
+// stream itself only sums and notes each group's maximum: it has no branch and
+// no barrier.  After up to 16 chunks, what K of the threads' maxima reach bounds
+// the K-th largest value from below, and only the groups that reach it (about twice K) are
+// read again, from L2, for the values themselves.  (Taking candidates out
+// while streaming cost more than the stream: 50 us against 27 for 256 rows of
+// 151937.)  The last CTA of a request to finish joins its lists.
 //
 // Sums: exp in fp32 from x - max (exact for bf16), fp32 sums of 8 per vector
 // and of a thread's vectors, 64 bits across threads and slices.  Scores are
@@ -31,13 +32,15 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 4;                      // 16-byte vectors per thread and chunk
 constexpr int kChunkVecs = kThreads * kVecs;
 constexpr int kWarpVecs = 32 * kVecs;
-constexpr int kStages = 3;                    // chunks of a warp's ring
+constexpr int kStages = 2;                    // chunks of a warp's ring
+constexpr int kGroupBytes = 8192;             // the groups' maxima between two looks for candidates
+constexpr int kGroups = 256;                  // groups that a look can take
 constexpr int kRingBytes = kThreads / 32 * kStages * (kWarpVecs + 1) * 16;
 constexpr int kMaxK = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxJoin = 4096;                // candidates a request's join holds
 constexpr int kPool = 2 * kThreads;            // candidates of a slice at a time
-constexpr int kTargetCtas = 8 * 152;          // slices: about two waves of 4 CTAs per SM
+constexpr int kWaveCtas = 4 * 152;            // slices: one wave of 4 CTAs per SM
 constexpr int kMinSliceVecs = 2 * kThreads;   // and no smaller than two vectors per thread
 
 template <int N>
@@ -75,6 +78,11 @@ struct Vec {  // a 16-byte vector of logits
         }
     }
 };
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float &d, float x) { d = x; }
+__device__ __forceinline__ void from_float(__nv_bfloat16 &d, float x) { d = __float2bfloat16_rn(x); }
 
 // Order-preserving map of a float (no NaN; -0 as +0) to an unsigned integer, and back.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -125,9 +133,8 @@ struct BeamArgs {
 // `skew` bytes past a 16-byte boundary takes each vector from two aligned ones.
 //
 // Warp w's share of a chunk is vectors c0 + w kWarpVecs + j 32 + lane (j < kVecs),
-// which it streams through its own ring in shared memory, two chunks ahead
-// (cp.async; only the warp waits for it): 128 KB in flight per SM, where loads to
-// registers, one chunk at a time, kept 64 KB in flight half of the time.
+// which it streams through its own ring in shared memory, a chunk ahead (cp.async;
+// only the warp waits for it): 64 KB in flight per SM throughout.
 template <typename T>
 struct Row {
     static constexpr int E = Vec<T>::kElems;
@@ -260,29 +267,6 @@ __device__ __noinline__ int keep_first(uint64_t *pool, int n, int K) {
     return min(n, K);
 }
 
-// A vector's values from `cut` on (with `strict`: above it) to the pool.  Out of
-// line: one or two lanes of a warp get here per chunk, mostly for one value, and one
-// copy of the loop stays in the instruction cache where 32 unrolled ones did not.
-template <typename T>
-__device__ __noinline__ void append(uint4 v, int entry, float cut, bool strict, uint64_t *pool, int *count) {
-    constexpr int E = Vec<T>::kElems;
-    uint32_t hits = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float x = Vec<T>::get(v, e);
-        hits |= static_cast<uint32_t>(strict ? x > cut : x >= cut) << e;
-    }
-#pragma unroll 1
-    while (hits) {
-        const int e = __ffs(hits) - 1, w = Vec<T>::k16 ? e >> 1 : e;
-        hits &= hits - 1;
-        const uint32_t word = w & 2 ? (w & 1 ? v.w : v.z) : (w & 1 ? v.y : v.x);
-        const float x = !Vec<T>::k16 ? __uint_as_float(word) : e & 1 ? bf16hi(word) : bf16lo(word);
-        const int at = atomicAdd(count, 1);
-        if (at < kPool) pool[at] = candidate(x, entry + e);
-    }
-}
-
 // The K first candidates of vectors [v0, v1) whatever their order: for rows
 // that overfill the pool (long runs of equal values, or values that rise along the
 // row).  Each chunk's exact K-th largest value by bisection over its key, then, among
@@ -362,7 +346,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     extern __shared__ __align__(16) uint64_t dyn_smem[];  // the warps' rings; then 24 bytes per entry of the join
     __shared__ uint32_t warp_keys[kThreads / 32];
     __shared__ __align__(16) uint64_t pool[kPool + 4];  // candidates for the slice's K largest
-    __shared__ int count, ticket;
+    __shared__ int count, groups, ticket;
+    constexpr int kBatch = kGroupBytes / (kThreads * static_cast<int>(sizeof(T)));   // chunks: 16 (fp32: 8)
+    __shared__ T group_max[kBatch * kThreads];               // [kBatch][kThreads], exact in T
+    __shared__ int group_at[kGroups];
     __shared__ float red_max[kThreads / 32];
     __shared__ double red_sum[kThreads / 32];
     __shared__ double lse[kMaxBeams], beam_cum[kMaxBeams];
@@ -380,13 +367,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         const int vecs = (a.vocab + E - 1) / E;
         const int per = (vecs + a.slices - 1) / a.slices;
         const int v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
-        const int period = max(1, kPool / 3 / K);   // chunks between looks at the pool, at most
-        int look = 0;                               // the chunk after which the next one is
         float m = -INFINITY, sum = 0.f;   // this thread's maximum and sum of exp(x - m)
-        float cut = -INFINITY;            // values below it, or with `strict` at it, are not among the K largest
-        bool strict = true, overfull = false;
-        if (tid == 0) count = 0;
-        __syncthreads();
+        float floor = -INFINITY;          // values at or below it are not among the slice's K largest
+        bool overfull = false;
+        int kept = 0;                     // the K largest so far, pool[0 .. kept)
         uint4(*ring)[kWarpVecs + 1] = reinterpret_cast<uint4(*)[kWarpVecs + 1]>(
             reinterpret_cast<uint4 *>(dyn_smem) + warp * kStages * (kWarpVecs + 1));   // [kStages], this warp's
 #pragma unroll
@@ -394,82 +378,90 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             if (v0 + u * kChunkVecs < v1) row.fetch(ring[u], v0 + u * kChunkVecs, v1);
             cp_async_commit();
         }
-        int chunk = 0;
-        for (int c0 = v0; c0 < v1; c0 += kChunkVecs, ++chunk) {
-            const int next = c0 + (kStages - 1) * kChunkVecs;
-            if (next < v1) row.fetch(ring[(chunk + kStages - 1) % kStages], next, v1);
-            cp_async_commit();
-            cp_async_wait<kStages - 1>();
-            __syncwarp();    // (every lane's copies of this chunk have landed)
-            uint4 raw[kVecs];
-            row.take(raw, ring[chunk % kStages], c0, v1);
-            __syncwarp();    // (and are read: the next fetch may go there)
-            float vmax[kVecs], cmax = -INFINITY;
+        int stage = 0;
+        for (int b0 = v0; b0 < v1; b0 += kBatch * kChunkVecs) {
+            const int b1 = min(b0 + kBatch * kChunkVecs, v1);
+            // ---- stream: sums, and each thread's maximum of each chunk
+            float bmax = -INFINITY;
+            T *gmax = group_max + tid;
+            for (int c0 = b0; c0 < b1; c0 += kChunkVecs, gmax += kThreads) {
+                const int next = c0 + (kStages - 1) * kChunkVecs;
+                if (next < v1) row.fetch(ring[stage ? stage - 1 : kStages - 1], next, v1);
+                cp_async_commit();
+                cp_async_wait<kStages - 1>();
+                __syncwarp();    // (every lane's copies of this chunk have landed)
+                uint4 raw[kVecs];
+                row.take(raw, ring[stage], c0, v1);
+                __syncwarp();    // (and are read: the next fetch may go there)
+                stage = stage == kStages - 1 ? 0 : stage + 1;
+                float cmax = V::max(raw[0]);
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                vmax[j] = V::max(raw[j]);
-                cmax = fmaxf(cmax, vmax[j]);
-            }
-            // ---- sum of exponentials
-            if (cmax > m) {
-                sum *= fast_exp2((m - cmax) * 1.4426950408889634f);  // (m = -inf: 0)
-                m = cmax;
-            }
-            const float minus = m > -INFINITY ? -m : 0.f;   // (a NaN goes into the sum all the same)
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                float e2[E];
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const uint64_t t = mul2(add2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(minus, minus)),
-                                            pack2(1.4426950408889634f, 1.4426950408889634f));
-                    unpack2(t, e2[e], e2[e + 1]);
-                    e2[e] = fast_exp2(e2[e]);
-                    e2[e + 1] = fast_exp2(e2[e + 1]);
+                for (int j = 1; j < kVecs; ++j) cmax = fmaxf(cmax, V::max(raw[j]));
+                from_float(*gmax, cmax);
+                bmax = fmaxf(bmax, cmax);
+                if (cmax > m) {
+                    sum *= fast_exp2((m - cmax) * 1.4426950408889634f);  // (m = -inf: 0)
+                    m = cmax;
                 }
+                const float minus = m > -INFINITY ? -m : 0.f;   // (a NaN goes into the sum all the same)
 #pragma unroll
-                for (int o = E / 2; o > 0; o >>= 1)
+                for (int j = 0; j < kVecs; ++j) {
+                    float e2[E];
 #pragma unroll
-                    for (int e = 0; e < o; ++e) e2[e] += e2[e + o];
-                sum += e2[0];
-            }
-            // ---- candidates: those that reach what K of the first chunk's thread maxima reach
-            if (chunk == 0) {
-                const uint32_t key = reached_by<V::kKeyLow>(cmax > -INFINITY ? order_key(cmax) : 0u, K, warp_keys);
-                if (key) {
-                    cut = key_value<V::kKeyLow>(key);
-                    strict = false;
-                }
-            }
-            auto passes = [&](float v) { return strict ? v > cut : v >= cut; };
-            if (passes(cmax)) {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-                    if (passes(vmax[j])) append<T>(raw[j], Row<T>::vector_of(c0, j) * E, cut, strict, pool, &count);
-            }
-            if (chunk == look) {   // the K best so far raise the bound, before the pool fills
-                look += min(chunk + 1, period);
-                __syncthreads();
-                const int n = count;
-                __syncthreads();
-                if (n > kPool) {
-                    overfull = true;
-                    cut = INFINITY, strict = true;
-                } else if (n > K) {
-                    const int kept = keep_first(pool, n, K);
-                    if (tid == 0) count = kept;
-                    if (kept == K) {
-                        cut = candidate_value(pool[K - 1]);   // (later entries of an equal value come after it)
-                        strict = true;
+                    for (int e = 0; e < E; e += 2) {
+                        const uint64_t t = mul2(add2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(minus, minus)),
+                                                pack2(1.4426950408889634f, 1.4426950408889634f));
+                        unpack2(t, e2[e], e2[e + 1]);
+                        e2[e] = fast_exp2(e2[e]);
+                        e2[e + 1] = fast_exp2(e2[e + 1]);
                     }
-                    __syncthreads();
+#pragma unroll
+                    for (int o = E / 2; o > 0; o >>= 1)
+#pragma unroll
+                        for (int e = 0; e < o; ++e) e2[e] += e2[e + o];
+                    sum += e2[0];
                 }
             }
+            // ---- the groups (a thread's values of a chunk) that may hold one of the K largest
+            const uint32_t key = reached_by<V::kKeyLow>(bmax > floor ? order_key(bmax) : 0u, K, warp_keys);
+            const float cut = key ? key_value<V::kKeyLow>(key) : floor;
+            const bool strict = key == 0;   // (fewer than K threads have any value above the floor: all such values)
+            if (tid == 0) groups = 0, count = kept;
+            __syncthreads();
+            if (bmax > floor && (strict ? bmax > cut : bmax >= cut)) {
+                gmax = group_max + tid;
+                for (int c0 = b0; c0 < b1; c0 += kChunkVecs, gmax += kThreads)
+                    if (strict ? to_float(*gmax) > cut : to_float(*gmax) >= cut) {
+                        const int at = atomicAdd(&groups, 1);
+                        if (at < kGroups) group_at[at] = Row<T>::vector_of(c0, 0);   // its first vector
+                    }
+            }
+            __syncthreads();
+            const int n_groups = groups;
+            if (n_groups > kGroups) overfull = true;
+            // ---- a warp per group: its values again, now from L2
+            static_assert(kVecs * E <= 32, "a group's values, one per lane");
+#pragma unroll 4
+            for (int g = warp; g < min(n_groups, kGroups); g += kThreads / 32) {
+                const int v = group_at[g] + lane / E * 32, i = v * E + lane % E;
+                const float value = lane < kVecs * E && v < v1 && i < a.vocab ? to_float(row.x[i]) : -INFINITY;
+                if (strict ? value > cut : value >= cut) {
+                    const int at = atomicAdd(&count, 1);
+                    if (at < kPool) pool[at] = candidate(value, i);
+                }
+            }
+            __syncthreads();
+            if (count > kPool) overfull = true;
+            if (overfull) {
+                kept = 0, floor = INFINITY;   // (the sums go on; the list is made again below)
+                __syncthreads();
+                continue;
+            }
+            kept = keep_first(pool, count, K);
+            if (kept == K) floor = candidate_value(pool[K - 1]);   // (later entries of an equal value come after it)
         }
         __syncthreads();
-        int kept;
-        if (overfull || count > kPool) kept = exact_slice<T>(row, v0, v1, K, pool, &count, ring[0]);
-        else kept = keep_first(pool, count, K);
+        if (overfull) kept = exact_slice<T>(row, v0, v1, K, pool, &count, ring[0]);
         // ---- the slice's maximum, sum and list
         float top = m;
 #pragma unroll
@@ -551,14 +543,18 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         keys[i] = key;
     }
     __syncthreads();
-    // The K-th largest list head bounds the K-th best score from below.
-    if (lists > K) {
-        for (int l = tid; l < lists; l += kThreads) {
-            const uint64_t k = keys[l * K];
+    // The K-th largest of the lists' first few (2 K in all) bounds the K-th best
+    // score from below.
+    {
+        const int each = min(K, (2 * K + lists - 1) / lists), heads = lists * each;
+        for (int i = tid; i < heads; i += kThreads) top_keys[i] = keys[i / each * K + i % each];
+        __syncthreads();
+        for (int i = tid; i < heads; i += kThreads) {
+            const uint64_t k = top_keys[i];
             int place = 0;
 #pragma unroll 8
-            for (int j = 0; j < lists; ++j)
-                place += static_cast<int>(keys[j * K] > k) | (static_cast<int>(keys[j * K] == k) & static_cast<int>(j < l));
+            for (int j = 0; j < heads; ++j)
+                place += static_cast<int>(top_keys[j] > k) | (static_cast<int>(top_keys[j] == k) & static_cast<int>(j < i));
             if (place == K - 1 && k) bound = k;
         }
         __syncthreads();
@@ -596,11 +592,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
 
 int elem_size(int32_t type) { return type == PA_LOGITS_BF16 ? 2 : type == PA_LOGITS_F32 ? 4 : 0; }
 
-// Slices of a row: two waves of CTAs (256 rows: 5 slices beat 2, 4, 8 and 12), each with at
-// least two vectors per thread, and no more lists than the join holds.
+// Slices of a row: as many CTAs as the GPU holds at once (256 rows: 2 slices take 35
+// us, 3 to 5 37 to 38), each with at least two vectors per thread, and no more
+// lists than the join holds.
 int slices_of(int64_t rows, int beams, int vocab, int K, int elem) {
     const int64_t vecs = (static_cast<int64_t>(vocab) * elem + 15) / 16;
-    int64_t s = std::min((vecs + kMinSliceVecs - 1) / kMinSliceVecs, (kTargetCtas + rows - 1) / rows);
+    int64_t s = std::min((vecs + kMinSliceVecs - 1) / kMinSliceVecs, std::max<int64_t>(1, kWaveCtas / rows));
     s = std::min<int64_t>(s, kMaxJoin / (beams * K));
     return static_cast<int>(std::max<int64_t>(1, s));
 }
