@@ -261,8 +261,8 @@ __device__ __forceinline__ uint2 e4m3x8_from_f32(const float (&f)[8], float scal
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         q[k] = f[k] * inv;
-        const uint32_t off = (__float_as_uint(q[k]) & 0xfffffu) - (0x80000u - 4u);
-        divide |= off <= 8u || !(fabsf(q[k]) >= 0x1p-6f);
+        const uint32_t off = (__float_as_uint(q[k]) << 12) - ((0x80000u - 4u) << 12);  // the bits below
+        divide |= off <= 8u << 12 || !(fabsf(q[k]) >= 0x1p-6f);
     }
     if (divide) {
 #pragma unroll

@@ -40,12 +40,11 @@ struct RopeArgs {
 // two chunks rot_dim / 2 apart (half layout), or 16 elements in a row
 // (interleaved).  A warp then reads and writes whole 128-byte lines.  The
 // tokens' angles are computed once per CTA, one per thread at a time, while the
-// first loads (up to 2 tokens of each unit) are in flight.
+// first loads are in flight; each token is loaded while the one before it is turned.
 template <bool F8, int TB>
 __global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
-    constexpr int kAhead = TB < 2 ? TB : 2;                   // tokens loaded at once
-    __shared__ float2 turn[TB][PA_ROPE_MAX_PAIRS];            // (cos, sin) of the tokens' pairs
+    __shared__ __align__(16) float2 turn[TB][PA_ROPE_MAX_PAIRS];  // (cos, sin) of the tokens' pairs
     __shared__ int64_t slot_s[TB];                            // -1: not written
     griddep_wait();
     griddep_launch_dependents();
@@ -64,23 +63,25 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
         const int h = head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq);
         const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
         const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + tok0 * stride + h * a.head_dim;
-        for (int t0 = 0; t0 < tokens || !ready; t0 += kAhead) {
-            uint4 lo[kAhead], hi[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                lo[j] = hi[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (t0 + j < tokens && x < total) {
-                    lo[j] = *reinterpret_cast<const uint4 *>(src + (t0 + j) * stride + e0);
-                    hi[j] = *reinterpret_cast<const uint4 *>(src + (t0 + j) * stride + e1);
-                }
+        uint4 next_lo, next_hi;
+        auto load = [&](int t) {
+            next_lo = next_hi = make_uint4(0u, 0u, 0u, 0u);
+            if (t < tokens && x < total) {
+                next_lo = *reinterpret_cast<const uint4 *>(src + t * stride + e0);
+                next_hi = *reinterpret_cast<const uint4 *>(src + t * stride + e1);
             }
+        };
+        load(0);
+        for (int t = 0; t < tokens || !ready; ++t) {
+            const uint4 lo = next_lo, hi = next_hi;
+            if (TB > 1) load(t + 1);   // (in place too: another token than the one written below)
             if (!ready) {  // (every thread's first pass: the loads above are in flight)
                 for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
-                    const int t = i / pairs, k = i % pairs;
-                    const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(a.positions[tok0 + t])) * rope.turn[k];
+                    const int at = i / pairs, k = i % pairs;
+                    const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(a.positions[tok0 + at])) * rope.turn[k];
                     float s, c;
                     sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
-                    turn[t][k] = make_float2(c * rope.magnitude, s * rope.magnitude);
+                    turn[at][k] = make_float2(c * rope.magnitude, s * rope.magnitude);
                 }
                 if (threadIdx.x < tokens) {
                     const int64_t slot = a.slots[tok0 + threadIdx.x];
@@ -91,52 +92,47 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
                 ready = true;
             }
             if (x >= total) continue;
+            const int64_t slot = slot_s[t];
+            if (!is_q && slot < 0) continue;
+            const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+            float f0[8], f1[8];  // the two chunks' values
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int t = t0 + j;
-                if (t >= tokens) break;
-                const int64_t slot = slot_s[t];
-                if (!is_q && slot < 0) continue;
-                const uint32_t w0[4] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w}, w1[4] = {hi[j].x, hi[j].y, hi[j].z, hi[j].w};
-                float f0[8], f1[8];  // the two chunks' values
+            for (int i = 0; i < 4; ++i) {
+                f0[2 * i] = bf16lo(w0[i]), f0[2 * i + 1] = bf16hi(w0[i]);
+                f1[2 * i] = bf16lo(w1[i]), f1[2 * i + 1] = bf16hi(w1[i]);
+            }
+            if (rotates) {
+                const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][8 * u]);  // two pairs each
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 two = cs[i / 2];
+                    const float c = i & 1 ? two.z : two.x, s = i & 1 ? two.w : two.y;
+                    float *fa = half ? f0 + i : i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
+                    float *fb = half ? f1 + i : fa + 1;
+                    const float x0 = *fa, x1 = *fb;
+                    *fa = x0 * c - x1 * s;
+                    *fb = x0 * s + x1 * c;
+                }
+            }
+            if (F8 && !is_q) {
+                const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
+                uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
+                *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale, inv);
+                *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale, inv);
+            } else {
+                __nv_bfloat16 *dst = is_q ? a.q_out + (tok0 + t) * a.q_out_stride + h * a.head_dim
+                                          : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
+                                                (slot * a.hkv + h) * a.head_dim;
+                uint32_t o0[4], o1[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f0[2 * i] = bf16lo(w0[i]), f0[2 * i + 1] = bf16hi(w0[i]);
-                    f1[2 * i] = bf16lo(w1[i]), f1[2 * i + 1] = bf16hi(w1[i]);
+                    const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0[2 * i], f0[2 * i + 1]);
+                    const __nv_bfloat162 b1 = __floats2bfloat162_rn(f1[2 * i], f1[2 * i + 1]);
+                    o0[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b0) : w0[i];  // (a copy keeps its bits)
+                    o1[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b1) : w1[i];
                 }
-                if (rotates) {
-                    const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][8 * u]);  // two pairs each
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 two = cs[i / 2];
-                        const float c = i & 1 ? two.z : two.x, s = i & 1 ? two.w : two.y;
-                        float *fa = half ? f0 + i : i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
-                        float *fb = half ? f1 + i : fa + 1;
-                        const float x0 = *fa, x1 = *fb;
-                        *fa = x0 * c - x1 * s;
-                        *fb = x0 * s + x1 * c;
-                    }
-                }
-                if (F8 && !is_q) {
-                    const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
-                    uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
-                    *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale, inv);
-                    *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale, inv);
-                } else {
-                    __nv_bfloat16 *dst = is_q ? a.q_out + (tok0 + t) * a.q_out_stride + h * a.head_dim
-                                              : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
-                                                    (slot * a.hkv + h) * a.head_dim;
-                    uint32_t o0[4], o1[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 b0 = __floats2bfloat162_rn(f0[2 * i], f0[2 * i + 1]);
-                        const __nv_bfloat162 b1 = __floats2bfloat162_rn(f1[2 * i], f1[2 * i + 1]);
-                        o0[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b0) : w0[i];  // (a copy keeps its bits)
-                        o1[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b1) : w1[i];
-                    }
-                    *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                    *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                }
+                *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
             }
         }
     }
@@ -144,18 +140,22 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
 
 float reciprocal(float scale) { return scale > 0x1p-100f && scale < 0x1p100f ? 1.f / scale : NAN; }
 
-// Tokens per CTA: one where there are few (every SM then has some), eight where
-// there are many.
-constexpr int kManyTokens = 8, kManyFrom = 2048;
+// Tokens per CTA: one where there are few (512 tokens of 32 heads: 4.0 us, with
+// four per CTA 6.4), four from 768 (1024 tokens of 36 heads: 8.3 against 6.0 us),
+// eight from 4096 (16384 tokens into FP8 pools: 54.6 us, with four 57.8).
+constexpr int kFourFrom = 768, kEightFrom = 4096;
+
+template <bool F8, int TB>
+cudaError_t launch_rope_instance(const RopeArgs &a, const pa_rope &rope, int threads, cudaStream_t stream) {
+    return launch_maybe_cooperative(rope_write_kernel<F8, TB>, dim3(static_cast<unsigned>((a.n + TB - 1) / TB)), threads,
+                                    0, stream, false, pdl_on(), a, rope);
+}
 
 template <bool F8>
 cudaError_t launch_rope(const RopeArgs &a, const pa_rope &rope, int threads, cudaStream_t stream) {
-    if (a.n < kManyFrom)
-        return launch_maybe_cooperative(rope_write_kernel<F8, 1>, dim3(static_cast<unsigned>(a.n)), threads, 0, stream,
-                                        false, pdl_on(), a, rope);
-    return launch_maybe_cooperative(rope_write_kernel<F8, kManyTokens>,
-                                    dim3(static_cast<unsigned>((a.n + kManyTokens - 1) / kManyTokens)), threads, 0,
-                                    stream, false, pdl_on(), a, rope);
+    return a.n < kFourFrom    ? launch_rope_instance<F8, 1>(a, rope, threads, stream)
+           : a.n < kEightFrom ? launch_rope_instance<F8, 4>(a, rope, threads, stream)
+                              : launch_rope_instance<F8, 8>(a, rope, threads, stream);
 }
 
 int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
