@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import itertools
 import os
 import re
@@ -581,48 +583,65 @@ def pa_decode_splitkv_noalloc(out, lse, q, k_cache, v_cache, block_tables, seq_l
 # ---------------------------------------------------------------------------------------------
 # The operators around a decode step: rotary positions, score rules, beams, pages.
 #
-# These calls are short on the GPU (2 to 20 us), so their wrappers spend little on the host: one
-# pass over the arguments that checks them and takes their addresses, no intermediate objects, the
-# current stream's handle without a Stream object (about 7 us a call, of which the launches take 2
-# to 3; the wrappers above take 20 to 25).
+# These calls are short on the GPU (2 to 12 us), so their wrappers spend little on the host: the
+# tensors are checked, and their addresses and sizes taken, by one call into C++
+# (csrc/pa_tensors.cpp), and the current stream's handle comes without a Stream object.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _entry_points = {}
 
-
-def _device_of(t, name: str) -> int:
-    """The index of the CUDA device that a tensor is on: the call's device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+_STATUS = ("status", "i32", 1, "optional")
+_SPACE = ("workspace", "any", 0, "space")
 
 
-def _at(t, name: str, dtype: torch.dtype, ndim: int, dev: int) -> int:
-    """The address of a contiguous tensor of this type on this device."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or \
-            not t.is_contiguous() or t.get_device() != dev:
-        _need(t, name, dtype, ndim)
-        raise ValueError(f"tensors on several devices ({name} is on {t.device})")
-    return t.data_ptr()
+def _tensor_specs():
+    """What each wrapper below takes: name -> (argument, type, dimensions, kind) of its tensors."""
+    specs = {}
+    for pool in ("bf16", "u8"):
+        cache = (("k_cache", pool, 4, "whole"), ("v_cache", pool, 4, "whole"))
+        specs["rope", pool] = (
+            ("q_out", "bf16", 3, "rows"), ("q", "bf16", 3, "rows"), ("k_new", "bf16", 3, "rows"),
+            ("v_new", "bf16", 3, "rows"), ("positions", "i32", 1, "whole"),
+            ("slot_mapping", "i64", 1, "whole"), *cache, _STATUS)
+        for nd in (3, 4):
+            specs["scored", pool, nd] = (
+                ("out", "bf16", nd, "whole"), ("lse", "f32", nd - 1, "optional"), ("q", "bf16", nd, "whole"), *cache,
+                ("block_tables", "i32", 2, "whole"), ("seq_lens", "i32", 1, "whole"),
+                ("alibi_slopes", "f32", 1, "optional"), ("prefix_lens", "i32", 1, "optional"), _SPACE, _STATUS)
+    specs["fork"] = (
+        ("new_tables", "i32", 2, "whole"), ("new_lens", "i32", 1, "whole"), ("new_refs", "i32", 1, "whole"),
+        ("slot_mapping", "i64", 1, "whole"), ("tables", "i32", 2, "whole"), ("lens", "i32", 1, "whole"),
+        ("refs", "i32", 1, "whole"), ("parents", "i32", 1, "whole"), _SPACE, _STATUS)
+    specs["compact"] = (
+        ("new_tables", "i32", 2, "whole"), ("new_refs", "i32", 1, "whole"), ("remap", "i32", 1, "whole"),
+        ("n_live", "i32", 1, "whole"), ("tables", "i32", 2, "whole"), ("lens", "i32", 1, "whole"),
+        ("refs", "i32", 1, "whole"), _SPACE, _STATUS)
+    specs["copy"] = (("pairs", "i32", 2, "whole"), _STATUS)
+    specs["beam"] = (
+        ("scores", "f32", 2, "whole"), ("tokens", "i32", 2, "whole"), ("parents", "i32", 2, "whole"),
+        ("logits", "logits", 2, "rows"), ("cum", "f32", 2, "whole"), ("finished", "u8", 2, "optional"), _SPACE)
+    return specs
 
 
-def _status_at(status, dev: int):
-    return None if status is None else _at(status, "status", torch.int32, 1, dev)
+_take_tensors = None
+_specs = {}
 
 
-def _space_at(workspace, dev: int):
-    """(address, bytes) of a workspace tensor of any type, (None, 0) without one."""
-    if workspace is None:
-        return None, 0
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or \
-            workspace.get_device() != dev:
-        raise ValueError("workspace must be a contiguous CUDA tensor on the call's device")
-    return workspace.data_ptr(), workspace.nbytes
+def _take(spec, *tensors):
+    """(device, address, sizes, ...) of the tensors a wrapper is given, checked against its spec."""
+    global _take_tensors
+    if _take_tensors is None:
+        if not os.path.exists(_build.TENSORS):
+            raise RuntimeError(f"{_build.TENSORS} is missing: build it with "
+                               "paged_kv_decode_cache_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_pa_tensors", _build.TENSORS)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_tensors", loader))
+        loader.exec_module(module)
+        _specs.update({k: module.make_spec(v) for k, v in _tensor_specs().items()})
+        _take_tensors = module.take
+    return _take_tensors(_specs[spec], *tensors)
 
 
 def _enqueue(name: str, dev: int, stream, *args):
@@ -666,54 +685,34 @@ def pa_rope_init(rot_dim: int, base: float, layout: str = "half", scaling: str =
     return rope
 
 
-def _rows_at(t, name: str, n: int, heads: int, d: int, dev: int):
-    """(address, stride between rows) of a bf16 tensor [n, heads, d] with contiguous rows [heads, d]."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
-    if t.dim() != 3 or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor [N, H, D] on the call's device")
-    if tuple(t.shape) != (n, heads, d):
-        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
-    row, head, one = t.stride()
-    if (one != 1 and d > 1) or (head != d and heads > 1):
-        raise ValueError(f"{name}: every row [H, D] must be contiguous")
-    return t.data_ptr(), row if n > 1 else heads * d  # (a single row's stride says nothing)
-
-
-def _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope, pool_dtype):
-    dev = _device_of(q, "q")
+def _rope_write(name, pool, q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, scales, rope,
+                status, stream):
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a plan made by pa_rope_init")
-    kc = _at(k_cache, "k_cache", pool_dtype, 4, dev)
-    vc = _at(v_cache, "v_cache", pool_dtype, 4, dev)
-    nb, bs, hkv, d = k_cache.shape
-    if v_cache.shape != k_cache.shape or q.dim() != 3:
-        raise ValueError("the pools differ in shape, or q is not [N, Hq, D]")
-    n, hq = q.size(0), q.size(1)
-    pos = _at(positions, "positions", torch.int32, 1, dev)
-    slots = _at(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    if positions.size(0) != n or slot_mapping.size(0) != n:
-        raise ValueError("q, positions and slot_mapping must have as many tokens")
-    return dev, (*_rows_at(q_out, "q_out", n, hq, d, dev), *_rows_at(q, "q", n, hq, d, dev),
-                 *_rows_at(k_new, "k_new", n, hkv, d, dev), *_rows_at(v_new, "v_new", n, hkv, d, dev),
-                 pos, slots, n, hq, kc, vc, CacheDesc(nb, bs, hkv, d))
+    (dev, qo, n1, h1, d1, qo_row, qa, n, hq, d, q_row, ka, n2, hkv, d2, k_row, va, n3, h3, d3, v_row, pos, n4, slots, n5,
+     kc, nb, bs, ch, cd, vc, nb2, bs2, ch2, cd2, st, _) = _take(
+        ("rope", pool), q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, status)
+    if not (n == n1 == n2 == n3 == n4 == n5):
+        raise ValueError("q_out, q, k_new, v_new, positions and slot_mapping must have as many tokens")
+    if h1 != hq or h3 != hkv or not (d == d1 == d2 == d3 == cd == cd2) or ch != hkv or ch2 != hkv or nb2 != nb or \
+            bs2 != bs:
+        raise ValueError("q_out and q must be [N, Hq, D], k_new and v_new [N, Hkv, D] matching the pools")
+    _enqueue(name, dev, stream, qo, qo_row, qa, q_row, ka, k_row, va, v_row, pos, slots, n, hq, kc, vc,
+             CacheDesc(nb, bs, ch, cd), *scales, ctypes.byref(rope), st)
 
 
 def pa_rope_write(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
                   status=None, stream=None):
     """Turn q into q_out, and write the turned k_new and v_new through slot_mapping."""
-    dev, args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
-                             torch.bfloat16)
-    _enqueue("pa_rope_write", dev, stream, *args, ctypes.byref(rope), _status_at(status, dev))
+    _rope_write("pa_rope_write", "bf16", q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, (), rope,
+                status, stream)
 
 
 def pa_rope_write_fp8(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, k_scale,
                       v_scale, rope, status=None, stream=None):
     """pa_rope_write into uint8 e4m3 pools."""
-    dev, args = _rope_inputs(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
-                             torch.uint8)
-    _enqueue("pa_rope_write_fp8", dev, stream, *args, k_scale, v_scale, ctypes.byref(rope),
-             _status_at(status, dev))
+    _rope_write("pa_rope_write_fp8", "u8", q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache,
+                (k_scale, v_scale), rope, status, stream)
 
 
 class PoolSet:
@@ -757,48 +756,47 @@ def pa_compact_workspace_bytes(num_blocks: int) -> int:
     return int(lib().pa_compact_workspace_bytes(num_blocks))
 
 
+def _enqueue_on_pools(name, dev, stream, pools, *args):
+    if dev != pools.device_index:
+        raise ValueError(f"{name}: the pools are on another device")
+    _enqueue(name, dev, stream, *args)
+
+
 def pa_sequences_fork(new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents, pools,
                       workspace, status=None, stream=None):
     """New row i is old row parents[i] (negative: none), blocks shared, last blocks copied on write;
     slot_mapping gets the slot of every row's next token."""
-    dev, i32 = _pools_of(pools).device_index, torch.int32
-    args = (_at(new_tables, "new_tables", i32, 2, dev), _at(new_lens, "new_lens", i32, 1, dev),
-            _at(new_refs, "new_refs", i32, 1, dev), _at(slot_mapping, "slot_mapping", torch.int64, 1, dev),
-            _at(tables, "tables", i32, 2, dev), _at(lens, "lens", i32, 1, dev),
-            _at(refs, "refs", i32, 1, dev), _at(parents, "parents", i32, 1, dev))
-    n, old, mb = parents.size(0), tables.size(0), tables.size(1)
-    if lens.size(0) != old or refs.size(0) != pools.num_blocks or new_refs.size(0) != pools.num_blocks:
+    _pools_of(pools)
+    (dev, nt, n1, mb1, nl, n2, nr, nb1, slots, n3, ta, old, mb, le, old1, re, nb, pr, n, ws, ws_bytes, st, _) = _take(
+        "fork", new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents, workspace, status)
+    if old1 != old or nb != pools.num_blocks or nb1 != nb:
         raise ValueError("tables, lens and refs must be [B, max_blocks], [B] and [num_blocks]")
-    if new_tables.size(0) != n or new_tables.size(1) != mb or new_lens.size(0) != n or \
-            slot_mapping.size(0) != n:
+    if not (n == n1 == n2 == n3) or mb1 != mb:
         raise ValueError("the new tables, lens and slots must have a row for every parent")
-    _enqueue("pa_sequences_fork", dev, stream, *args, old, n, mb, pools._ptrs, len(pools.pools),
-             pools.elem_bytes, pools.desc, *_space_at(workspace, dev), _status_at(status, dev))
+    _enqueue_on_pools("pa_sequences_fork", dev, stream, pools, nt, nl, nr, slots, ta, le, re, pr, old, n, mb, pools._ptrs,
+                      len(pools.pools), pools.elem_bytes, pools.desc, ws, ws_bytes, st)
 
 
 def pa_blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace,
                       status=None, stream=None):
     """Live blocks moved to the front of every pool; remap: every old block id's new one (-1: free)."""
-    dev, i32 = _pools_of(pools).device_index, torch.int32
-    args = (_at(new_tables, "new_tables", i32, 2, dev), _at(new_refs, "new_refs", i32, 1, dev),
-            _at(remap, "remap", i32, 1, dev), _at(n_live, "n_live", i32, 1, dev),
-            _at(tables, "tables", i32, 2, dev), _at(lens, "lens", i32, 1, dev), _at(refs, "refs", i32, 1, dev))
-    B, mb, nb = tables.size(0), tables.size(1), pools.num_blocks
-    if lens.size(0) != B or refs.size(0) != nb or new_refs.size(0) != nb or remap.size(0) != nb or \
-            new_tables.size(0) != B or new_tables.size(1) != mb or n_live.size(0) != 1:
+    _pools_of(pools)
+    (dev, nt, n1, mb1, nr, nb1, rm, nb2, nlv, one, ta, n, mb, le, n2, re, nb, ws, ws_bytes, st, _) = _take(
+        "compact", new_tables, new_refs, remap, n_live, tables, lens, refs, workspace, status)
+    if not (n == n1 == n2) or mb1 != mb or not (nb == nb1 == nb2 == pools.num_blocks) or one != 1:
         raise ValueError("tables [B, max_blocks], lens [B], counts and remap [num_blocks], n_live [1]")
-    _enqueue("pa_blocks_compact", dev, stream, *args, B, mb, pools._ptrs, len(pools.pools),
-             pools.elem_bytes, pools.desc, *_space_at(workspace, dev), _status_at(status, dev))
+    _enqueue_on_pools("pa_blocks_compact", dev, stream, pools, nt, nr, rm, nlv, ta, le, re, n, mb, pools._ptrs,
+                      len(pools.pools), pools.elem_bytes, pools.desc, ws, ws_bytes, st)
 
 
 def pa_blocks_copy(pools, pairs, status=None, stream=None):
     """Copy whole blocks within every pool: pairs int32 [n, 2], source and destination."""
-    dev = _pools_of(pools).device_index
-    at = _at(pairs, "pairs", torch.int32, 2, dev)
-    if pairs.size(1) != 2:
+    _pools_of(pools)
+    dev, at, n, two, st, _ = _take("copy", pairs, status)
+    if two != 2:
         raise ValueError("pairs must be [n, 2]")
-    _enqueue("pa_blocks_copy", dev, stream, pools._ptrs, len(pools.pools), pools.elem_bytes, pools.desc, at,
-             pairs.size(0), _status_at(status, dev))
+    _enqueue_on_pools("pa_blocks_copy", dev, stream, pools, pools._ptrs, len(pools.pools), pools.elem_bytes, pools.desc, at,
+                      n, st)
 
 
 _LOGITS = {torch.bfloat16: PA_LOGITS_BF16, torch.float32: PA_LOGITS_F32}
@@ -813,29 +811,14 @@ def pa_beam_workspace_bytes(groups: int, beams: int, vocab: int, K: int, dtype: 
 def pa_beam_select(scores, tokens, parents, logits, cum, finished=None, eos=-1, workspace=None, stream=None):
     """The K best of beams x vocabulary for every request: logits [groups * beams, vocab] (rows may be
     strided), cum [groups, beams], finished uint8 [groups, beams]; scores, tokens, parents [groups, K]."""
-    dev = _device_of(logits, "logits")
-    kind = _LOGITS.get(logits.dtype)
-    if kind is None:
-        raise TypeError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.size(1) > 1):
-        raise ValueError("logits must be [groups * beams, vocab] with contiguous rows")
-    args = (_at(scores, "scores", torch.float32, 2, dev), _at(tokens, "tokens", torch.int32, 2, dev),
-            _at(parents, "parents", torch.int32, 2, dev))
-    at_cum = _at(cum, "cum", torch.float32, 2, dev)
-    groups, beams = cum.shape
-    rows, vocab = logits.shape
-    K = scores.size(1)
-    if rows != groups * beams or scores.size(0) != groups or tokens.shape != scores.shape or \
-            parents.shape != scores.shape:
+    (dev, sc, g1, K, tk, g2, K2, pr, g3, K3, kind, lo, rows, vocab, row, cu, groups, beams, fi, g4, b4, ws,
+     ws_bytes) = _take("beam", scores, tokens, parents, logits, cum, finished, workspace)
+    if rows != groups * beams or not (groups == g1 == g2 == g3) or K2 != K or K3 != K:
         raise ValueError("logits must be [groups * beams, vocab]; scores, tokens and parents [groups, K]")
-    done = None
-    if finished is not None:
-        done = _at(finished, "finished", torch.uint8, 2, dev)
-        if finished.shape != cum.shape:
-            raise ValueError("finished must be [groups, beams]")
-    _enqueue("pa_beam_select", dev, stream, *args, logits.data_ptr(), kind,
-             logits.stride(0) if rows > 1 else vocab, at_cum, done, eos, groups, beams, vocab, K,
-             *_space_at(workspace, dev))
+    if finished is not None and (g4 != groups or b4 != beams):
+        raise ValueError("finished must be [groups, beams]")
+    _enqueue("pa_beam_select", dev, stream, sc, tk, pr, lo, kind, row, cu, fi or None, eos, groups, beams, vocab, K, ws,
+             ws_bytes)
 
 
 def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
@@ -846,42 +829,36 @@ def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_bloc
     return r
 
 
-def _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap, alibi_slopes, window,
-                   prefix_lens, max_prefix, pool_dtype):
-    """(device, the arguments up to the cache, those from the tables on, the rules); q is [B, Hq, D] or
-    [B, q_len, Hq, D]."""
-    dev = _device_of(q, "q")
-    nd = q.dim()
-    if nd != 3 and nd != 4:
+def _decode_scored(name, pool, out, lse, q, k_cache, v_cache, scales, block_tables, seq_lens, scale, softcap,
+                   alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace, status, stream):
+    nd = q.dim() if isinstance(q, torch.Tensor) else 3
+    if nd == 3:
+        (dev, oa, B1, H1, D1, la, B2, H2, qa, B, Hq, D, kc, nb, bs, hkv, d, vc, nb2, bs2, hkv2, d2, bt, B3, mb, sl, B4, al,
+         H5, pf, B5, ws, ws_bytes, st, _) = _take(("scored", pool, 3), out, lse, q, k_cache, v_cache, block_tables,
+                                                  seq_lens, alibi_slopes, prefix_lens, workspace, status)
+        q_len = Q1 = Q2 = 1
+    elif nd == 4:
+        (dev, oa, B1, Q1, H1, D1, la, B2, Q2, H2, qa, B, q_len, Hq, D, kc, nb, bs, hkv, d, vc, nb2, bs2, hkv2, d2, bt, B3,
+         mb, sl, B4, al, H5, pf, B5, ws, ws_bytes, st, _) = _take(
+            ("scored", pool, 4), out, lse, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, prefix_lens,
+            workspace, status)
+    else:
         raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {tuple(q.shape)}")
-    at_q, at_out = _at(q, "q", torch.bfloat16, nd, dev), _at(out, "out", torch.bfloat16, nd, dev)
-    kc, vc = _at(k_cache, "k_cache", pool_dtype, 4, dev), _at(v_cache, "v_cache", pool_dtype, 4, dev)
-    bt = _at(block_tables, "block_tables", torch.int32, 2, dev)
-    sl = _at(seq_lens, "seq_lens", torch.int32, 1, dev)
-    shape = q.shape
-    B, Hq, D = shape[0], shape[-2], shape[-1]
-    nb, bs, hkv, d = k_cache.shape
-    mb = block_tables.size(1)
-    if out.shape != shape or v_cache.shape != k_cache.shape or d != D or block_tables.size(0) != B or \
-            seq_lens.size(0) != B:
+    if B1 != B or Q1 != q_len or H1 != Hq or D1 != D or nb2 != nb or bs2 != bs or hkv2 != hkv or d != D or d2 != D or \
+            B3 != B or B4 != B:
         raise ValueError("inconsistent out / q / cache / table shapes")
-    at_lse = slopes = prefix = None
-    if lse is not None:
-        at_lse = _at(lse, "lse", torch.float32, nd - 1, dev)
-        if lse.shape != shape[:-1]:
-            raise ValueError("lse must have q's shape without its last dimension")
-    if alibi_slopes is not None:
-        slopes = _at(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
-        if alibi_slopes.size(0) != Hq:
-            raise ValueError("alibi_slopes must be [Hq]")
+    if lse is not None and (B2 != B or Q2 != q_len or H2 != Hq):
+        raise ValueError("lse must have q's shape without its last dimension")
+    if alibi_slopes is not None and H5 != Hq:
+        raise ValueError("alibi_slopes must be [Hq]")
     if prefix_lens is not None:
-        prefix = _at(prefix_lens, "prefix_lens", torch.int32, 1, dev)
-        if prefix_lens.size(0) != B:
+        if B5 != B:
             raise ValueError("prefix_lens must be [B]")
         if max_prefix is None:
             max_prefix = mb * bs
-    return dev, (at_out, at_lse, at_q, shape[1] if nd == 4 else 1, kc, vc, CacheDesc(nb, bs, hkv, d)), \
-        (bt, mb, sl, B, Hq), ScoreRules(softcap, slopes, window, prefix, max_prefix or 0)
+    rules = ScoreRules(softcap, al, window, pf, max_prefix or 0)
+    _enqueue(name, dev, stream, oa, la, qa, q_len, kc, vc, CacheDesc(nb, bs, hkv, d), *scales, bt, mb, sl, B, Hq, scale,
+             ctypes.byref(rules), num_splits, ws, ws_bytes, st)
 
 
 def pa_decode_scored(out, lse, q, k_cache, v_cache, block_tables, seq_lens, scale, softcap=0.0,
@@ -890,17 +867,13 @@ def pa_decode_scored(out, lse, q, k_cache, v_cache, block_tables, seq_lens, scal
     """Split-KV decode (q [B, Hq, D]) or causal multi-query decode (q [B, q_len, Hq, D]) with capped
     scores, a distance bias, a sliding window and a prefix that every query sees.  max_prefix: a bound
     on prefix_lens (default: the table's tokens)."""
-    dev, head, tail, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
-                                            alibi_slopes, window, prefix_lens, max_prefix, torch.bfloat16)
-    _enqueue("pa_decode_scored", dev, stream, *head, *tail, scale, ctypes.byref(rules), num_splits,
-             *_space_at(workspace, dev), _status_at(status, dev))
+    _decode_scored("pa_decode_scored", "bf16", out, lse, q, k_cache, v_cache, (), block_tables, seq_lens, scale, softcap,
+                   alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace, status, stream)
 
 
 def pa_decode_scored_fp8(out, lse, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
                          softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None,
                          num_splits=0, workspace=None, status=None, stream=None):
     """pa_decode_scored over uint8 e4m3 pools with per-pool scales."""
-    dev, head, tail, rules = _scored_inputs(out, lse, q, k_cache, v_cache, block_tables, seq_lens, softcap,
-                                            alibi_slopes, window, prefix_lens, max_prefix, torch.uint8)
-    _enqueue("pa_decode_scored_fp8", dev, stream, *head, k_scale, v_scale, *tail, scale, ctypes.byref(rules),
-             num_splits, *_space_at(workspace, dev), _status_at(status, dev))
+    _decode_scored("pa_decode_scored_fp8", "u8", out, lse, q, k_cache, v_cache, (k_scale, v_scale), block_tables, seq_lens,
+                   scale, softcap, alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace, status, stream)
