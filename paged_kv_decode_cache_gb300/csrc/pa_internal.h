@@ -135,6 +135,7 @@ cudaError_t launch_cache_write_fp8(const void *k_new, const void *v_new, const i
 
 // Host-side checks and switches that entry points outside pa_api.cu share.
 int check_cache(const pa_cache_desc &c);  // PA_OK, PA_EINVAL or PA_EUNSUPPORTED
+int sm_count();                           // of the current device, < 0 on error
 bool pdl_on();                            // programmatic stream serialization (PA_OPT_PDL)
 inline bool is_aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 

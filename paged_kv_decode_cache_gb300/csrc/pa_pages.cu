@@ -25,8 +25,9 @@ constexpr int kMaxPlanCtas = 8;        // portable cluster size
 constexpr int kMaxRows = 4096;         // sequences per fork
 constexpr int kMaxPools = 256;
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;           // 16-byte loads in flight per thread
-constexpr int kPiece = kCopyThreads * kCopyVecs * 16;  // bytes of a block per CTA and turn: 16 KB
+constexpr int kPiece = 16 * 1024;      // bytes of a block per CTA and turn
+constexpr int kOwnTurns = 16;          // turns of a copy that a lone planning CTA makes itself
+constexpr int kPlanWords = 4096;       // words of counts and tables per planning CTA
 
 // Block-wide exclusive prefix sum over kPlanThreads threads; *total gets the sum.
 __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
@@ -62,6 +63,69 @@ struct CopyList {
     // int4 entries follow: source block, destination block, token rows
 };
 
+struct CopyArgs {
+    const CopyList *list;       // or null: `pairs`
+    const int2 *pairs;          // (source, destination), n of them, whole blocks
+    int n_pairs;
+    int n_pools;
+    int row_bytes;              // of a token
+    int block_size, num_blocks;
+    int32_t *status;
+    // tables to rewrite while at it (pa_blocks_compact), or null
+    int32_t *new_tables;
+    const int32_t *tables, *lens, *remap;
+    int B, max_blocks;
+    uint8_t *pools[kMaxPools];
+};
+
+// Turns first, first + step, ... of a copy.  A turn is 16 KB of one block of one
+// pool, copied by one CTA with four 16-byte loads per thread (of kCopyThreads) in
+// flight.
+template <int kThreads>
+__device__ __forceinline__ void copy_turns(const CopyArgs &a, int count, int first, int step) {
+    constexpr int kEach = kPiece / 16 / kThreads;
+    const int4 *entries = reinterpret_cast<const int4 *>(a.list + 1);
+    const int64_t block_bytes = static_cast<int64_t>(a.block_size) * a.row_bytes;
+    const int pieces = static_cast<int>((block_bytes + kPiece - 1) / kPiece);
+    const int64_t turns = static_cast<int64_t>(count) * a.n_pools * pieces;
+#pragma unroll 4
+    for (int64_t t = first; t < turns; t += step) {
+        const int piece = static_cast<int>(t % pieces);
+        const int64_t u = t / pieces;
+        const int pool = static_cast<int>(u % a.n_pools), k = static_cast<int>(u / a.n_pools);
+        int src, dst, rows = a.block_size;
+        if (a.list) {
+            const int4 e = __ldcg(entries + k);
+            src = e.x, dst = e.y, rows = e.z;
+        } else {
+            const int2 e = a.pairs[k];
+            src = e.x, dst = e.y;
+            if (src >= a.num_blocks || dst >= a.num_blocks || (src >= 0 && dst < 0)) {
+                if (threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                continue;
+            }
+        }
+        if (src < 0) continue;
+        const int64_t from = static_cast<int64_t>(piece) * kPiece;
+        const int64_t left = static_cast<int64_t>(rows) * a.row_bytes - from;
+        if (left <= 0) continue;
+        const int vecs = static_cast<int>((left < kPiece ? left : static_cast<int64_t>(kPiece)) / 16);
+        const uint4 *in = reinterpret_cast<const uint4 *>(a.pools[pool] + src * block_bytes + from);
+        uint4 *out = reinterpret_cast<uint4 *>(a.pools[pool] + dst * block_bytes + from);
+        uint4 v[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int x = i * kThreads + threadIdx.x;
+            if (x < vecs) v[i] = __ldcs(in + x);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int x = i * kThreads + threadIdx.x;
+            if (x < vecs) __stcs(out + x, v[i]);
+        }
+    }
+}
+
 struct ForkArgs {
     int32_t *new_tables, *new_lens, *new_refs;
     int64_t *slots;
@@ -88,6 +152,20 @@ __device__ __forceinline__ int count_zero(const int32_t *refs, int lo, int hi) {
     return n;
 }
 
+// f(entry, block id) for a table row's first n entries, by one warp, four loads
+// per lane in flight.
+template <typename F>
+__device__ __forceinline__ void for_entries(const int32_t *row, int n, int lane, F &&f) {
+    for (int e0 = lane; e0 < n; e0 += 128) {
+        int id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) id[u] = e0 + 32 * u < n ? __ldg(row + e0 + 32 * u) : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (e0 + 32 * u < n) f(e0 + 32 * u, id[u]);
+    }
+}
+
 // Row i of the new state is row parents[i] of the old one, sharing its blocks.
 // An old row with c children changes every count of its blocks by c - 1, so
 // rows with one child (most of them) touch no count.  Then the block of the
@@ -95,76 +173,96 @@ __device__ __forceinline__ int count_zero(const int32_t *refs, int lo, int hi) {
 // reference to it is some new row's last block and this is the first such
 // row; any other row copies it to a free block; a row that ends with a full
 // block takes a free one.
-__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a) {
+// kSmall: one CTA, which keeps the counts and lists in shared memory, so that only the
+// first loads, the tables and the copies themselves wait for memory (4 beams of a
+// request: 9.7 -> 6.3 us).  `copy.list`: the plan's, for a copy so small that this CTA makes
+// it itself; null: another launch does.
+template <bool kSmall>
+__global__ void __launch_bounds__(kPlanThreads)
+fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     extern __shared__ int32_t smem[];
     int32_t *row_parent = smem;                     // [B_new], -1: no sequence
     int32_t *row_len = row_parent + a.B_new;        // [B_new]
-    int32_t *row_rank = row_len + a.B_new;          // [B_new] needs a block: which one; else -1
+    int32_t *row_tail = row_len + a.B_new;          // [B_new] partial last block, -1: none, or outside the pool
+    int32_t *row_rank = row_tail + a.B_new;         // [B_new] needs a block: which one; else -1
     int32_t *children = row_rank + a.B_new;         // [B_old]
+    int32_t *old_len = children + a.B_old;          // [B_old]
+    int32_t *near = old_len + a.B_old;              // kSmall: the arrays below
+    int32_t *refs = kSmall ? near : a.new_refs;                            // [num_blocks]
+    int32_t *tail_count = kSmall ? near + a.num_blocks : a.tail_count;      // [num_blocks]
+    int32_t *tail_first = kSmall ? near + 2 * a.num_blocks : a.tail_first;  // [num_blocks]
+    int32_t *free_list = kSmall ? near + 3 * a.num_blocks : a.free_list;    // [B_new]
+    auto get = [](const int32_t *p) { return kSmall ? *p : __ldcg(p); };   // (what other CTAs write is read from L2)
+    auto everyone = [] {
+        if (kSmall) __syncthreads();
+        else cluster_sync();
+    };
     __shared__ int32_t warp_sums[32];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31;
-    const int cta = blockIdx.x, ctas = gridDim.x;
+    const int cta = kSmall ? 0 : blockIdx.x, ctas = kSmall ? 1 : gridDim.x;
     const int gid = cta * kPlanThreads + tid, gthreads = ctas * kPlanThreads;
     const int bs = a.block_size, mb = a.max_blocks, lmax = mb * bs;
 
     // ---- the rows' parents and lengths (every CTA for itself), the counts copied
-    for (int j = tid; j < a.B_old; j += kPlanThreads) children[j] = 0;
+    for (int j = tid; j < a.B_old; j += kPlanThreads) {
+        children[j] = 0;
+        old_len[j] = checked_len(a.lens[j], lmax, a.status);
+    }
+    for (int i = tid; i < a.B_new; i += kPlanThreads) row_parent[i] = a.parents[i];
+    for (int i = gid; i < a.num_blocks; i += gthreads) {
+        refs[i] = a.refs[i];
+        if (kSmall) tail_count[i] = 0, tail_first[i] = INT32_MAX;
+    }
     __syncthreads();
     for (int i = tid; i < a.B_new; i += kPlanThreads) {
-        int p = a.parents[i], L = 0;
+        int p = row_parent[i], L = 0, t = -1;
         if (p >= a.B_old) {
             set_status(a.status, PA_STATUS_BAD_PARENT);
             p = -1;
         }
         if (p >= 0) {
-            L = checked_len(a.lens[p], lmax, a.status);
+            L = old_len[p];
             atomicAdd(children + p, 1);
-            const int t = L % bs ? a.tables[static_cast<int64_t>(p) * mb + L / bs] : -1;
-            if (cta == 0 && t >= 0 && t < a.num_blocks) {
-                a.tail_count[t] = 0;
-                a.tail_first[t] = INT32_MAX;
-            }
+            if (L % bs) t = a.tables[static_cast<int64_t>(p) * mb + L / bs];
+            if (t >= a.num_blocks) t = -1;
+            if (!kSmall && cta == 0 && t >= 0) tail_count[t] = 0, tail_first[t] = INT32_MAX;
         }
         row_parent[i] = p < 0 ? -1 : p;
         row_len[i] = L;
+        row_tail[i] = t < 0 ? -1 : t;
     }
-    for (int i = gid; i < a.num_blocks; i += gthreads) a.new_refs[i] = a.refs[i];
-    cluster_sync();
+    everyone();
 
     // ---- references dropped and added; tables copied (a warp per row)
     for (int j = gid >> 5; j < a.B_old; j += gthreads >> 5) {
         const int change = children[j] - 1;
         if (change == 0) continue;
-        const int nb = (checked_len(a.lens[j], lmax, a.status) + bs - 1) / bs;
-        for (int e = lane; e < nb; e += 32) {
-            const int id = a.tables[static_cast<int64_t>(j) * mb + e];
-            if (id >= 0 && id < a.num_blocks) atomicAdd(a.new_refs + id, change);
+        for_entries(a.tables + static_cast<int64_t>(j) * mb, (old_len[j] + bs - 1) / bs, lane, [&](int, int id) {
+            if (id >= 0 && id < a.num_blocks) atomicAdd(refs + id, change);
             else set_status(a.status, PA_STATUS_BAD_BLOCK);
-        }
+        });
     }
     for (int i = gid >> 5; i < a.B_new; i += gthreads >> 5) {
         const int p = row_parent[i], nb = (row_len[i] + bs - 1) / bs;
-        for (int e = lane; e < mb; e += 32) {
-            int id = -1;
-            if (e < nb) {
-                id = a.tables[static_cast<int64_t>(p) * mb + e];
-                if (id < 0 || id >= a.num_blocks) {
-                    set_status(a.status, PA_STATUS_BAD_BLOCK);
-                    id = -1;
-                } else if (e == nb - 1 && row_len[i] % bs) {
-                    atomicAdd(a.tail_count + id, 1);
-                    atomicMin(a.tail_first + id, i);
-                }
-            }
-            a.new_tables[static_cast<int64_t>(i) * mb + e] = id;
+        int32_t *row = a.new_tables + static_cast<int64_t>(i) * mb;
+        if (lane == 0 && row_tail[i] >= 0) {
+            atomicAdd(tail_count + row_tail[i], 1);
+            atomicMin(tail_first + row_tail[i], i);
         }
+        for_entries(a.tables + static_cast<int64_t>(max(p, 0)) * mb, nb, lane, [&](int e, int id) {
+            if (id < 0 || id >= a.num_blocks) {
+                set_status(a.status, PA_STATUS_BAD_BLOCK);
+                id = -1;
+            }
+            row[e] = id;
+        });
+        for (int e = nb + lane; e < mb; e += 32) row[e] = -1;
     }
-    cluster_sync();
+    everyone();
 
     // ---- which rows need a block (every CTA for itself), in row order
-    auto tail_of = [&](int i) { return __ldcg(a.new_tables + static_cast<int64_t>(i) * mb + row_len[i] / bs); };
     int needed = 0, copies = 0;
     const int per_row = (a.B_new + kPlanThreads - 1) / kPlanThreads;
     {
@@ -173,14 +271,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
         for (int i = i0; i < i1; ++i) {
             int need = 0;
             if (row_parent[i] >= 0) {
-                const int L = row_len[i];
-                if (L % bs == 0) {
-                    need = L < lmax;
-                } else {
-                    const int t = tail_of(i);
-                    if (t >= 0 && !(__ldcg(a.tail_count + t) == __ldcg(a.new_refs + t) && __ldcg(a.tail_first + t) == i))
-                        need = 1 | 1 << 16;
-                }
+                const int L = row_len[i], t = row_tail[i];
+                if (L % bs == 0) need = L < lmax;
+                else if (t >= 0 && !(get(tail_count + t) == get(refs + t) && get(tail_first + t) == i)) need = 1 | 1 << 16;
             }
             row_rank[i] = need;
             mine += need;
@@ -203,47 +296,55 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
         const int s0 = min(cta * slice, a.num_blocks), s1 = min(s0 + slice, a.num_blocks);
         const int seg = (slice + kPlanThreads - 1) / kPlanThreads;
         const int lo = min(s0 + tid * seg, s1), hi = min(lo + seg, s1);
-        int total;
-        int at = block_scan(count_zero(a.new_refs, lo, hi), warp_sums, &total);
-        if (tid == 0) a.cta_count[cta] = total;
-        cluster_sync();
-        for (int c = 0; c < ctas; ++c) {
-            const int n = __ldcg(a.cta_count + c);
-            if (c < cta) at += n;
-            n_free += n;
+        int total, mine = 0;
+        for (int i = lo; i < hi; ++i) mine += get(refs + i) == 0;
+        int at = block_scan(mine, warp_sums, &total);
+        n_free = total;
+        if (!kSmall) {
+            if (tid == 0) a.cta_count[cta] = total;
+            cluster_sync();
+            n_free = 0;
+            for (int c = 0; c < ctas; ++c) {
+                const int n = __ldcg(a.cta_count + c);
+                if (c < cta) at += n;
+                n_free += n;
+            }
         }
         for (int i = lo; i < hi && at < needed; ++i)
-            if (__ldcg(a.new_refs + i) == 0) a.free_list[at++] = i;
-        cluster_sync();
+            if (get(refs + i) == 0) free_list[at++] = i;
+        everyone();
     }
 
     // ---- the rows' last blocks, slots and copies
     int4 *entries = reinterpret_cast<int4 *>(a.list + 1);
     if (gid == 0) a.list->count = copies;
     for (int i = gid; i < a.B_new; i += gthreads) {
-        const int L = row_len[i], off = L % bs, e = L / bs;
+        const int L = row_len[i], off = L % bs, e = L / bs, tail = row_tail[i];
         int64_t slot = -1;
         if (row_rank[i] >= 0) {
             const int rank = row_rank[i] & 0xffff;
-            const int tail = off ? tail_of(i) : -1;
             int id = -1;
             if (rank < n_free) {
-                id = __ldcg(a.free_list + rank);
+                id = get(free_list + rank);
                 a.new_tables[static_cast<int64_t>(i) * mb + e] = id;
-                a.new_refs[id] = 1;
-                if (off) atomicSub(a.new_refs + tail, 1);
+                refs[id] = 1;
+                if (off) atomicSub(refs + tail, 1);
                 slot = static_cast<int64_t>(id) * bs + off;
             } else {
                 set_status(a.status, PA_STATUS_NO_BLOCKS);
             }
             if (off) entries[row_rank[i] >> 16] = make_int4(id < 0 ? -1 : tail, id, off, 0);
         } else if (row_parent[i] >= 0) {
-            const int tail = off ? tail_of(i) : -1;
             if (tail >= 0) slot = static_cast<int64_t>(tail) * bs + off;
             else if (!off) set_status(a.status, PA_STATUS_BAD_SEQLEN);  // the table is full
         }
         a.slots[i] = slot;
         a.new_lens[i] = L;
+    }
+    if (kSmall) {
+        __syncthreads();
+        for (int i = tid; i < a.num_blocks; i += kPlanThreads) a.new_refs[i] = refs[i];
+        if (copy.list) copy_turns<kPlanThreads>(copy, copies, 0, 1);
     }
 }
 
@@ -318,26 +419,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
     }
 }
 
-struct CopyArgs {
-    const CopyList *list;       // or null: `pairs`
-    const int2 *pairs;          // (source, destination), n of them, whole blocks
-    int n_pairs;
-    int n_pools;
-    int row_bytes;              // of a token
-    int block_size, num_blocks;
-    int32_t *status;
-    // tables to rewrite while at it (pa_blocks_compact), or null
-    int32_t *new_tables;
-    const int32_t *tables, *lens, *remap;
-    int B, max_blocks;
-    uint8_t *pools[kMaxPools];
-};
-
-// Moves the listed blocks' first rows in every pool.  A turn is 16 KB of one
-// block of one pool, copied by one CTA with four 16-byte loads per thread in
-// flight; CTAs take turns in a stride, so that the list's length (which only the GPU
-// knows) spreads over all of them.  Destinations are free blocks and sources live
-// ones, so turns never meet.
+// Moves the listed blocks' first rows in every pool.  CTAs take turns in a
+// stride, so that the list's length (which only the GPU knows) spreads over all of
+// them.  Destinations are free blocks and sources live ones, so turns never meet.
 __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
     griddep_wait();
     griddep_launch_dependents();
@@ -356,54 +440,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
             a.new_tables[x] = id;
         }
     }
-    const int count = a.list ? a.list->count : a.n_pairs;
-    const int4 *entries = reinterpret_cast<const int4 *>(a.list + 1);
-    const int64_t block_bytes = static_cast<int64_t>(a.block_size) * a.row_bytes;
-    const int pieces = static_cast<int>((block_bytes + kPiece - 1) / kPiece);
-    const int64_t turns = static_cast<int64_t>(count) * a.n_pools * pieces;
-    for (int64_t t = blockIdx.x; t < turns; t += gridDim.x) {
-        const int piece = static_cast<int>(t % pieces);
-        const int64_t u = t / pieces;
-        const int pool = static_cast<int>(u % a.n_pools), k = static_cast<int>(u / a.n_pools);
-        int src, dst, rows = a.block_size;
-        if (a.list) {
-            const int4 e = entries[k];
-            src = e.x, dst = e.y, rows = e.z;
-        } else {
-            const int2 e = a.pairs[k];
-            src = e.x, dst = e.y;
-            if (src >= a.num_blocks || dst >= a.num_blocks || (src >= 0 && dst < 0)) {
-                if (threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-                continue;
-            }
-        }
-        if (src < 0) continue;
-        const int64_t from = static_cast<int64_t>(piece) * kPiece;
-        const int64_t left = static_cast<int64_t>(rows) * a.row_bytes - from;
-        if (left <= 0) continue;
-        const int vecs = static_cast<int>((left < kPiece ? left : static_cast<int64_t>(kPiece)) / 16);
-        const uint4 *in = reinterpret_cast<const uint4 *>(a.pools[pool] + src * block_bytes + from);
-        uint4 *out = reinterpret_cast<uint4 *>(a.pools[pool] + dst * block_bytes + from);
-        uint4 v[kCopyVecs];
-#pragma unroll
-        for (int i = 0; i < kCopyVecs; ++i) {
-            const int x = i * kCopyThreads + threadIdx.x;
-            if (x < vecs) v[i] = __ldcs(in + x);
-        }
-#pragma unroll
-        for (int i = 0; i < kCopyVecs; ++i) {
-            const int x = i * kCopyThreads + threadIdx.x;
-            if (x < vecs) __stcs(out + x, v[i]);
-        }
-    }
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return -1;
-    return n;
+    copy_turns<kCopyThreads>(a, a.list ? a.list->count : a.n_pairs, blockIdx.x, gridDim.x);
 }
 
 int check_pools(void *const *pools, int32_t n_pools, int32_t elem_bytes, const pa_cache_desc &c) {
@@ -418,18 +455,20 @@ int check_pools(void *const *pools, int32_t n_pools, int32_t elem_bytes, const p
     return PA_OK;
 }
 
-// Enough CTAs for `turns` (an upper bound; < 0: unknown, fill the GPU), at most
-// eight resident per SM.
-int launch_copy(CopyArgs &a, void *const *pools, int32_t n_pools, int32_t elem_bytes, const pa_cache_desc &c,
-                int32_t *status, int64_t turns, cudaStream_t stream) {
-    const int sms = sm_count();
-    if (sms <= 0) return PA_ECUDA;
+void set_pools(CopyArgs &a, void *const *pools, int32_t n_pools, int32_t elem_bytes, const pa_cache_desc &c,
+               int32_t *status) {
     a.n_pools = n_pools;
     a.row_bytes = c.num_kv_heads * c.head_dim * elem_bytes;
     a.block_size = c.block_size;
     a.num_blocks = c.num_blocks;
     a.status = status;
     for (int i = 0; i < n_pools; ++i) a.pools[i] = static_cast<uint8_t *>(pools[i]);
+}
+
+// Enough CTAs for `turns` (an upper bound), at most eight resident per SM.
+int launch_copy(const CopyArgs &a, int64_t turns, cudaStream_t stream) {
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ECUDA;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(turns, static_cast<int64_t>(sms) * 8));
     const cudaError_t e = launch_maybe_cooperative(copy_blocks_kernel, dim3(static_cast<unsigned>(grid)), kCopyThreads,
                                                    0, stream, false, pdl_on(), a);
@@ -441,10 +480,10 @@ int64_t pieces_of(const pa_cache_desc &c, int32_t elem_bytes) {
     return (bytes + kPiece - 1) / kPiece;
 }
 
-// CTAs of a planning cluster: one per 4096 words it reads, up to eight.
+// CTAs of a planning cluster: one per kPlanWords words it reads, up to eight.
 int plan_ctas(int64_t words) {
     int n = 1;
-    while (n < kMaxPlanCtas && words > 4096 * static_cast<int64_t>(n)) n *= 2;
+    while (n < kMaxPlanCtas && words > kPlanWords * static_cast<int64_t>(n)) n *= 2;
     return n;
 }
 
@@ -507,25 +546,31 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     a.B_old = B_old, a.B_new = B_new, a.max_blocks = max_blocks_per_seq;
     a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
     const int ctas = pa::plan_ctas(cache.num_blocks + static_cast<int64_t>(B_old + B_new) * max_blocks_per_seq);
-    const int smem = (3 * B_new + B_old) * 4;
-    static std::atomic<uint64_t> smem_attr_done{0};
+    const bool small = ctas == 1;
+    const int64_t turns = static_cast<int64_t>(B_new) * n_pools * pa::pieces_of(cache, elem_bytes);
+    const bool own_copy = small && turns <= pa::kOwnTurns;
+    pa::CopyArgs c{};
+    pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
+    c.list = own_copy ? a.list : nullptr;
+    int smem = (4 * B_new + 2 * B_old) * 4;
+    if (small) smem += (3 * cache.num_blocks + B_new) * 4;
+    auto kern = small ? pa::fork_plan_kernel<true> : pa::fork_plan_kernel<false>;
+    static std::atomic<uint64_t> smem_attr_done[2];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
     const uint64_t bit = 1ull << (dev & 63);
-    if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(pa::fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 4 * pa::kMaxRows * 4) != cudaSuccess)
+    if (!(smem_attr_done[small].load(std::memory_order_acquire) & bit)) {
+        // (small: fewer than 4096 words of counts and tables, rows up to the limit)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (7 * pa::kMaxRows + 3 * pa::kPlanWords) * 4) != cudaSuccess)
             return PA_ECUDA;
-        smem_attr_done.fetch_or(bit, std::memory_order_release);
+        smem_attr_done[small].fetch_or(bit, std::memory_order_release);
     }
-    if (pa::launch_clustered(pa::fork_plan_kernel, dim3(ctas), ctas, pa::kPlanThreads, smem, stream, pa::pdl_on(), a) !=
-        cudaSuccess)
+    if (pa::launch_clustered(kern, dim3(ctas), ctas, pa::kPlanThreads, smem, stream, pa::pdl_on(), a, c) != cudaSuccess)
         return PA_ECUDA;
-    if (B_new == 0 || n_pools == 0) return PA_OK;
-    pa::CopyArgs c{};
+    if (turns == 0 || own_copy) return PA_OK;
     c.list = a.list;
-    return pa::launch_copy(c, pools, n_pools, elem_bytes, cache, status,
-                           static_cast<int64_t>(B_new) * n_pools * pa::pieces_of(cache, elem_bytes), stream);
+    return pa::launch_copy(c, turns, stream);
 }
 
 int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live, const int32_t *tables,
@@ -561,13 +606,14 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
         return PA_ECUDA;
     if (B == 0 && n_pools == 0) return PA_OK;
     pa::CopyArgs c{};
+    pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.list = a.list;
     if (B > 0) c.new_tables = new_tables;
     c.tables = tables, c.lens = lens, c.remap = remap, c.B = B, c.max_blocks = max_blocks_per_seq;
     // (at most half of the blocks move)
     const int64_t turns = static_cast<int64_t>(cache.num_blocks / 2) * n_pools * pa::pieces_of(cache, elem_bytes);
     const int64_t entries = static_cast<int64_t>(B) * max_blocks_per_seq / pa::kCopyThreads;
-    return pa::launch_copy(c, pools, n_pools, elem_bytes, cache, status, std::max(turns, entries), stream);
+    return pa::launch_copy(c, std::max(turns, entries), stream);
 }
 
 int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, const int32_t *pairs,
@@ -578,10 +624,10 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
     if (n_pairs == 0 || n_pools == 0) return PA_OK;
     if (!pairs || !pa::is_aligned(pairs, 8)) return PA_EINVAL;
     pa::CopyArgs c{};
+    pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.pairs = reinterpret_cast<const int2 *>(pairs);
     c.n_pairs = n_pairs;
-    return pa::launch_copy(c, pools, n_pools, elem_bytes, cache, status,
-                           static_cast<int64_t>(n_pairs) * n_pools * pa::pieces_of(cache, elem_bytes), stream);
+    return pa::launch_copy(c, static_cast<int64_t>(n_pairs) * n_pools * pa::pieces_of(cache, elem_bytes), stream);
 }
 
 }  // extern "C"
