@@ -333,7 +333,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             const int c = ln / C::kTiles, tl = ln % C::kTiles;
             const int bz = blockIdx.z, hg0 = (blockIdx.y % p.head_groups) * HC;
             const int t0 = static_cast<int>(blockIdx.x) * p.chunk;
-            const int tok = t0 + c * C::kT + tl * kTile;
+            int tok = t0 + c * C::kT + tl * kTile;
             const int lp = p.seq_len_const >= 0 ? p.seq_len_const
                                                 : *reinterpret_cast<const volatile int32_t *>(p.seq_lens + bz) -
                                                       p.seq_len_offset;
@@ -344,9 +344,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 const int q0 = static_cast<int>(blockIdx.y / p.head_groups) * p.q_per_cta;
                 const Seen sn = seen_by(p, bz, lc, lc - p.q_len + q0, min(p.q_per_cta, p.q_len - q0), false);
                 lim = min(t0 + p.chunk, sn.end);
+                if (p.slopes) tok += ((max(lim - t0, 1) - 1) / C::kT - 2 * c) * C::kT;  // (the last chunks come first)
                 place = sn.real(tok);
             }
-            if (tok < lim) {
+            if (tok < lim && tok >= t0) {
                 const int phys = *reinterpret_cast<const volatile int32_t *>(
                     p.block_tables + static_cast<int64_t>(bz) * p.table_stride + place / p.block_size);
                 if (phys >= 0 && phys < p.num_blocks) {
@@ -412,9 +413,15 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     int *my_look = look_ring + (is_v ? (kTcLook + 1) * 32 : 0) + lane;  // slot j at my_look[32 * j]
     Seen sn{};  // SC: the partition counts virtual tokens, sn.real() of which are read
     auto real = [&](int t) { return SC ? sn.real(t) : t; };
+    // First (virtual) token of chunk c.  Under a distance bias the last chunk comes
+    // first and meets its largest scores at once: in order, every chunk of a steep
+    // head moved the reference maxima (43 of 189 us on 64 ragged sequences).
+    int t_first = t_begin;
+    const int t_step = SC && p.slopes ? -C::kT : C::kT;
+    auto chunk_at = [&](int c) { return SC ? t_first + c * t_step : t_begin + c * C::kT; };
     auto look_ahead = [&](int c, int t_stop) {  // copy chunk c's block id; one commit group per chunk
-        const int tok0 = t_begin + c * C::kT + tile * kTile;
-        if (carrier && tok0 < t_stop) cp_async_4(my_look + 32 * (c % (kTcLook + 1)), bt + real(tok0) / bs);
+        const int tok0 = chunk_at(c) + tile * kTile;
+        if (carrier && tok0 < t_stop && tok0 >= t_begin) cp_async_4(my_look + 32 * (c % (kTcLook + 1)), bt + real(tok0) / bs);
         cp_async_commit();
     };
     if (producer && !SC) {
@@ -449,11 +456,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int qbase = p.causal ? L - p.q_len + qi0 : L;
     if constexpr (SC) sn = seen_by(p, b, L, qbase, nq, tid == 0 && part == 0 && g0 == 0);
     const int t_end = min(t_begin + p.chunk, SC ? sn.end : max(0, min(L, p.causal ? qbase + nq : L)));
+    const int nch = t_end > t_begin ? (t_end - t_begin + C::kT - 1) / C::kT : 0;
+    if (SC && p.slopes) t_first = t_begin + (nch - 1) * C::kT;
     if (producer && SC) {  // (a token's place depends on the length)
 #pragma unroll
         for (int c = 0; c < kTcLook; ++c) look_ahead(c, t_end);
     }
-    const int nch = t_end > t_begin ? (t_end - t_begin + C::kT - 1) / C::kT : 0;
 
     if (nch == 0) {  // empty range: zero output, lse = -inf
         cp_async_wait<0>();
@@ -533,7 +541,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 const bool ok = wait_or_abort(&empty[s], ((c / nst) - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) return false;
             }
-            const int tok0 = t_begin + c * C::kT + tile * kTile;
+            const int tok0 = chunk_at(c) + tile * kTile;
             bool valid = false;
             if (carrier && tok0 < t_end) {
                 if (phys >= 0 && phys < p.num_blocks) valid = true;
@@ -544,7 +552,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             // (and, FP8, for the V converter, which zeroes the V rows not loaded)
             if (lane == 0 && !is_v) mask_ring[c % C::kMaskRing] = (static_cast<uint64_t>(c) << 32) | vm;
             if (F8 && lane == 0 && is_v) vmask_ring[c % C::kMaskRing] = (static_cast<uint64_t>(c) << 32) | vm;
-            const int chunk0 = t_begin + c * C::kT;
+            const int chunk0 = chunk_at(c);
             if (writes && last_pos >= chunk0 && last_pos < chunk0 + C::kT) {  // holds position L - 1
                 const int ph = __shfl_sync(0xffffffffu, phys, 2 * ((last_pos - chunk0) / kTile));
                 if (slot_is_position(slot_b, ph, last_pos, bs) && ph < p.num_blocks) {
@@ -805,11 +813,25 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             if (c >= NOB && !wait_or_abort(&vopfree[ob], ((c / NOB) - 1) & 1)) break;
             tc5::fence_after_sync();
             const uint32_t vm = static_cast<uint32_t>(mk);
-            const int tok_c = t_begin + c * C::kT;
+            const int tok_c = chunk_at(c);
             constexpr uint32_t kAllTiles = 0x55555555u & ((1u << (2 * C::kTiles)) - 1u);
-            // (SC: all of it in the prefix, or none of it before the window)
-            const bool whole = (vm & kAllTiles) == kAllTiles && tok_c + C::kT <= t_end &&
-                               (!SC || tok_c + C::kT <= sn.prefix || real(tok_c) >= sn.start);
+            const bool whole = (vm & kAllTiles) == kAllTiles && tok_c + C::kT <= t_end;
+            // SC: rows inside the range that no query sees (before the window, past the
+            // prefix) get zero codes here, in the few chunks that have any, so that the
+            // passes below stay as they are without rules (masks computed in them cost
+            // up to 40%).  Each of the four warps, which all read every row, writes them
+            // itself: no barrier that an aborting warp could miss.
+            if (SC && !(tok_c + C::kT <= sn.prefix || real(tok_c) >= sn.start)) {
+#pragma unroll 1
+                for (int r = lane; r < kTcRows; r += 32) {
+                    if (sn.any(real(tok_c + r / (kTile * HC) * kTile + (r & 15)))) continue;
+                    uint4 *vrow = reinterpret_cast<uint4 *>(vring + (c % NV) * C::kStageBytes + r * kSubBytes);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) vrow[j] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();  // (the stage's next TMA load comes after these)
+                __syncwarp();
+            }
             // pass u: dims 16 dc .. 16 dc + 15 (dc = 2 q4 + u); load k takes row groups
             // g = 2 k, 2 k + 1, lane t giving the address of row t % 8 of matrix
             // t / 8 = 2 (g - 2 k) + h (rows 16 g + 8 h .. + 7)
@@ -834,9 +856,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                             const int tl = (2 * k + gg) / HC;
                             const bool tile_ok = (vm >> (2 * tl)) & 1u;
                             const int r0 = tok_c + tl * kTile + 2 * (lane & 3);
-                            auto seen = [&](int r) { return tile_ok && r < t_end && (!SC || sn.any(real(r))); };
-                            ka = (seen(r0) ? 0x0000ffffu : 0u) | (seen(r0 + 1) ? 0xffff0000u : 0u);
-                            kb = (seen(r0 + 8) ? 0x0000ffffu : 0u) | (seen(r0 + 9) ? 0xffff0000u : 0u);
+                            ka = (tile_ok && r0 < t_end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 1 < t_end ? 0xffff0000u : 0u);
+                            kb = (tile_ok && r0 + 8 < t_end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 9 < t_end ? 0xffff0000u : 0u);
                         }
                         // repetition g = 2 k + gg of the store: columns 8 g + 2 (t % 4) (+ 1)
                         w[8 * k + 4 * gg + 0] = a.x & ka;  // dim 2 (t / 4): lane t / 4, rows of h = 0
@@ -872,6 +893,26 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         float mr[GP];
 #pragma unroll
         for (int q = 0; q < GP; ++q) mr[q] = -INFINITY;
+        // SC: the rules on one row's scores, for its token.  This row's head's slopes
+        // stay in registers where they fit, and a single query's distance is one
+        // number per row (from shared memory, both took as long as the softmax).
+        // A row that is not seen may hold anything: it is masked afterwards.
+        constexpr bool kSlopeRegs = SC && GP <= 16;
+        float slope_r[kSlopeRegs ? GP : 1];
+        if constexpr (kSlopeRegs) {
+#pragma unroll
+            for (int q = 0; q < GP; ++q) slope_r[q] = slope_s[my_head * GP + q];
+        }
+        auto apply_rules = [&](float(&x)[GP], int tok) {
+            if (p.soft_cap > 0.f) cap_scores<GP>(x, p.inv_cap, p.soft_cap);
+            if (p.slopes) {
+                const float one = static_cast<float>(tok - qbase);
+#pragma unroll
+                for (int q = 0; q < GP; ++q)
+                    x[q] = fmaf(kSlopeRegs ? slope_r[kSlopeRegs ? q : 0] : slope_s[my_head * GP + q],
+                                p.q_len == 1 ? one : static_cast<float>(tok - pos_s[my_head * GP + q]), x[q]);
+            }
+        };
         for (int c = 0; c < nch; ++c) {
             const int sbuf = c % NBS, pbuf = c % NBP;
             bool ok = wait_or_abort(&sdone[sbuf], (c / NBS) & 1);
@@ -898,7 +939,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
             ok = __all_sync(0xffffffffu, ok);
             const bool in_pool =
-                t_begin + c * C::kT + my_tok < t_end && ((static_cast<uint32_t>(mk) >> (2 * my_tile)) & 1u);
+                chunk_at(c) + my_tok < t_end && ((static_cast<uint32_t>(mk) >> (2 * my_tile)) & 1u);
             float sv[GP];  // this row's head's GP scores
             if (ok) {
                 tc5::fence_after_sync();
@@ -926,7 +967,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tc5::fence_before_sync();
             __syncwarp();  // (one arrival per warp, once all its lanes have read)
             if (lane == 0) mbar_arrive(&sfree[sbuf]);  // S buffer read: QK c + NBS may overwrite it
-            const int tok = real(t_begin + c * C::kT + my_tok);  // this row's token
+            const int tok = real(chunk_at(c) + my_tok);  // this row's token
             const bool valid = ok && in_pool && (!SC || sn.any(tok));
             // causal: column q (query qi0 + q / G) sees this row's token only if
             // the token is not past the query's position (SC: and not before its window,
@@ -939,15 +980,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
             float sc[GP];
             bool over = false;
-            if constexpr (SC) {  // the rules, on finite values (a row not seen may hold anything)
+            if constexpr (SC) {
 #pragma unroll
-                for (int q = 0; q < GP; ++q) sc[q] = valid ? sv[q] * sl2 : 0.f;
-                if (p.soft_cap > 0.f) cap_scores<GP>(sc, p.inv_cap, p.soft_cap);
-                if (p.slopes) {
-#pragma unroll
-                    for (int q = 0; q < GP; ++q)
-                        sc[q] = fmaf(slope_s[my_head * GP + q], static_cast<float>(tok - pos_s[my_head * GP + q]), sc[q]);
-                }
+                for (int q = 0; q < GP; ++q) sc[q] = sv[q] * sl2;
+                apply_rules(sc, tok);
             }
 #pragma unroll
             for (int q = 0; q < GP; ++q) {

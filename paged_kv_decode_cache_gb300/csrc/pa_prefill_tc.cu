@@ -130,6 +130,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int t_begin = part * p.chunk;
     const int t_end = min(t_begin + p.chunk, max(0, t_stop));
     const int nch = t_end > t_begin ? (t_end - t_begin + kPfT - 1) / kPfT : 0;
+    // The chunk's place in the range: under a distance bias the last comes first and
+    // meets its largest scores at once.
+    auto place_of = [&](int c) { return SC && p.slopes ? nch - 1 - c : c; };
     // output row of tile row r: ((b * q_len + position) * Hq + g * G + member)
     const int64_t orow0 = (static_cast<int64_t>(b) * p.q_len + qi0) * Hq + static_cast<int64_t>(g) * G;
     auto out_row = [&](int r) -> int64_t { return orow0 + static_cast<int64_t>(r / G) * Hq + r % G; };
@@ -229,7 +232,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (lane == 0) mbar_arrive_expect_tx(&full[s], 2u * kPfTilesPerChunk * kPfBox);
             __syncwarp();
             if (lane < 2 * kPfTilesPerChunk) {
-                const int ti = c * kPfTilesPerChunk + tile;
+                const int ti = place_of(c) * kPfTilesPerChunk + tile;
                 const int row = ti < ntiles ? tile_row[ti] : -1;
                 tma_load_4d(ring + s * kPfStage + half * kPfHalf + tile * kPfBox, map, 0,
                             row >= 0 ? row : oob_row, g, half, &full[s], policy);
@@ -323,12 +326,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             __syncwarp();  // (one arrival per warp, once all its lanes have read)
             if (lane == 0) mbar_arrive(&sfree[grp]);  // S buffer read: QK c + 2 may overwrite it
             if (!ok || *abort_flag) break;
-            const int tok0 = t_begin + c * kPfT;
+            const int tok0 = t_begin + place_of(c) * kPfT;
             bool tile_ok[kPfTilesPerChunk];
             bool all_tiles = true;
 #pragma unroll
             for (int k = 0; k < kPfTilesPerChunk; ++k) {
-                const int ti = c * kPfTilesPerChunk + k;
+                const int ti = place_of(c) * kPfTilesPerChunk + k;
                 tile_ok[k] = ti < ntiles && tile_row[ti] >= 0;
                 all_tiles &= tile_ok[k];
             }
@@ -456,7 +459,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                             make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-            } else if (c == nch - 1) {
+            } else if (!SC && c == nch - 1) {
                 const int z0 = t_end - tok0;
                 const int z1 = min(kPfT, (t_end + kTile - 1) / kTile * kTile - tok0);
                 if (z1 > z0 && wait_or_abort(&vfull[c % kPfNV], (c / kPfNV) & 1)) {
