@@ -697,9 +697,10 @@ int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, 
     //   ceil(units P / SMs) / P                        sequences all of that length
     //   max(1 / P, units / (2 SMs) + 1 / (2 P))        lengths spread evenly below it
     // and each wave after the first about 8 us more (a chunk takes 1.05 us).  P has the least
-    // sum of the two, among those that keep at least 8 tiles.  FP8, 64 sequences of 8 heads, up to
-    // 4096 tokens: P = 4 takes 163 us full and 112 us spread, P = 2 155 and 155; 40
-    // sequences: P = 11 111 and 77, P = 3 108 and 108; 16 keep P = 9 (45 and 44).
+    // sum of the two, among those that keep at least 8 tiles.  FP8, sequences of 8
+    // heads up to 4096 tokens: 64 of them with P = 7 take 113 us full and 81 us spread
+    // (P = 2: 109 and 109); 40 with P = 7 78 and 61 (P = 3: 78 and 77); 100 with P = 3 150
+    // and 134 (P = 1: 201 and 200).
     const int qpc = queries_per_cta(G, q_len);
     const double units = static_cast<double>(units_per_split(k, B, G, Hkv, qpc, (q_len + qpc - 1) / qpc));
     int hc = 1, gp = 1;

@@ -344,8 +344,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                  ((real_last <= pos && real(tok0) >= oldest) || (SC && tok_last < sn.prefix)));
             float mx = -INFINITY;
             if constexpr (SC) {  // the rules, then what is not seen masked (whatever it holds)
+                // (two scores per instruction, here and in the exponentials below)
 #pragma unroll
-                for (int k = 0; k < kPfT; ++k) sv[k] *= sl2;
+                for (int k = 0; k < kPfT; k += 2)
+                    unpack2(mul2(pack2(sv[k], sv[k + 1]), pack2(sl2, sl2)), sv[k], sv[k + 1]);
                 if (p.soft_cap > 0.f) cap_scores<kPfT>(sv, p.inv_cap, p.soft_cap);
                 if (p.slopes) {
 #pragma unroll
@@ -372,7 +374,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < kPfT; ++k) mx = fmaxf(mx, sv[k]);
+                for (int k = 0; k < kPfT; k += 2) mx = fmaxf(mx, fmaxf(sv[k], sv[k + 1]));
             } else if (whole) {
 #pragma unroll
                 for (int k = 0; k < kPfT; ++k) {
@@ -418,19 +420,35 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // no key yet subtracts 0, not -inf).  The row sum adds p itself: hi +
             // lo equals it to about 2^-17.
             const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+            uint64_t l2 = 0;  // SC: the chunk's sums of even and odd scores
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t hw[kPfT / 4], lw[kPfT / 4];
 #pragma unroll
                 for (int k = 0; k < kPfT / 2; k += 2) {
-                    const float p0 = fast_exp2(sv[hf * kPfT / 2 + k] - m_use);
-                    const float p1 = fast_exp2(sv[hf * kPfT / 2 + k + 1] - m_use);
+                    float x0 = sv[hf * kPfT / 2 + k], x1 = sv[hf * kPfT / 2 + k + 1];
+                    if constexpr (SC) {
+                        unpack2(add2(pack2(x0, x1), pack2(-m_use, -m_use)), x0, x1);
+                    } else {
+                        x0 -= m_use;
+                        x1 -= m_use;
+                    }
+                    const float p0 = fast_exp2(x0);
+                    const float p1 = fast_exp2(x1);
                     const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
                     const float2 hv = __bfloat1622float2(h);
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - hv.x, p1 - hv.y);
+                    float d0, d1;
+                    if constexpr (SC) {
+                        unpack2(add2(pack2(p0, p1), pack2(-hv.x, -hv.y)), d0, d1);
+                        l2 = add2(l2, pack2(p0, p1));
+                    } else {
+                        d0 = p0 - hv.x;
+                        d1 = p1 - hv.y;
+                        l += p0 + p1;
+                    }
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(d0, d1);
                     hw[k / 2] = *reinterpret_cast<const uint32_t *>(&h);
                     lw[k / 2] = *reinterpret_cast<const uint32_t *>(&lo);
-                    l += p0 + p1;
                 }
 #pragma unroll
                 for (int j = 0; j < kPfT / 16; ++j) {  // 16-byte chunk 4 hf + j: tokens 8 (4 hf + j) ..
@@ -441,6 +459,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     *reinterpret_cast<uint4 *>(prow + kPfPPart + off) =
                         make_uint4(lw[4 * j], lw[4 * j + 1], lw[4 * j + 2], lw[4 * j + 3]);
                 }
+            }
+            if constexpr (SC) {
+                float even, odd;
+                unpack2(l2, even, odd);
+                l += even + odd;
             }
             // V rows that were loaded from the pool but lie past the range (the
             // tail of the tile holding key t_end - 1) may hold anything, even
