@@ -36,11 +36,12 @@ struct RopeArgs {
 };
 
 // Thread = one unit of 16 elements of one head of q, k or v, for the TB tokens of
-// its CTA.  In either layout unit u < rot_dim / 16 holds the pairs 8 u .. 8 u + 7:
-// two chunks rot_dim / 2 apart (half layout), or 16 elements in a row
-// (interleaved).  A warp then reads and writes whole 128-byte lines.  The
-// tokens' angles are computed once per CTA, one per thread at a time, while the
-// first loads are in flight; each token is loaded while the one before it is turned.
+// its CTA: two 16-byte chunks half of the turning dimensions apart (of the others
+// where nothing turns), which holds 8 whole pairs in either layout.  Neighbouring
+// threads take neighbouring chunks, so that a warp reads and writes whole lines.
+// The tokens' angles are computed once per CTA, one per thread at a time, while
+// the first loads are in flight; each token is loaded while the one before it is
+// turned.
 template <bool F8, int TB>
 __global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
@@ -58,8 +59,10 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
         const int head = min(x, total - 1) / units, u = x % units;
         const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
         const bool rotates = u < rot_units && !is_v;
-        const int e0 = rotates && half ? 8 * u : kUnit * u;                       // first chunk
-        const int e1 = rotates && half ? rope.rot_dim / 2 + 8 * u : kUnit * u + 8;  // second chunk
+        // its two chunks: half of the dimensions that turn, or of the others, apart
+        const int from = rotates || is_v ? 0 : rope.rot_dim;
+        const int dims = rotates ? rope.rot_dim : a.head_dim - from;
+        const int e0 = from + 8 * (from ? u - rot_units : u), e1 = e0 + dims / 2;
         const int h = head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq);
         const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
         const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + tok0 * stride + h * a.head_dim;
@@ -102,10 +105,13 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
                 f1[2 * i] = bf16lo(w1[i]), f1[2 * i + 1] = bf16hi(w1[i]);
             }
             if (rotates) {
-                const float4 *cs = reinterpret_cast<const float4 *>(&turn[t][8 * u]);  // two pairs each
+                // pairs 8 u .. 8 u + 7, one of each in either chunk (half), or 4 u .. 4 u + 3 in
+                // the first and as many, rot_dim / 4 on, in the second (interleaved)
+                const float4 *c0 = reinterpret_cast<const float4 *>(&turn[t][half ? 8 * u : 4 * u]);
+                const float4 *c1 = half ? c0 + 2 : reinterpret_cast<const float4 *>(&turn[t][rope.rot_dim / 4 + 4 * u]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 two = cs[i / 2];
+                    const float4 two = i < 4 ? c0[i / 2] : c1[i / 2 - 2];
                     const float c = i & 1 ? two.z : two.x, s = i & 1 ? two.w : two.y;
                     float *fa = half ? f0 + i : i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
                     float *fb = half ? f1 + i : fa + 1;
@@ -141,8 +147,8 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
 float reciprocal(float scale) { return scale > 0x1p-100f && scale < 0x1p100f ? 1.f / scale : NAN; }
 
 // Tokens per CTA: one where there are few (512 tokens of 32 heads: 4.0 us, with
-// four per CTA 6.4), four from 768 (1024 tokens of 36 heads: 8.3 against 6.0 us),
-// eight from 4096 (16384 tokens into FP8 pools: 54.6 us, with four 57.8).
+// four per CTA 6.4), four from 768 (1024 tokens of 36 heads: 6.3 us, with one 8.3),
+// eight from 4096 (16384 tokens into FP8 pools: 54.3 us, with four 57.8).
 constexpr int kFourFrom = 768, kEightFrom = 4096;
 
 template <bool F8, int TB>
