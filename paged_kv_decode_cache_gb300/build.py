@@ -1,6 +1,6 @@
 """Build libpagedattn.so (the CUDA library behind include/pa.h) in-tree, and the
-binding's C++ argument checks (``_build/_pa_tensors.so``, a CPython extension
-that reads torch tensors' fields; g++ and torch's headers).
+binding's C++ calls (``_build/_pa_binding.so``, a CPython extension that reads
+torch tensors' fields; g++ and torch's headers).
 
 Each .cu file is compiled for sm_103a by its own nvcc process (in parallel),
 then linked into ``paged_kv_decode_cache_gb300/_build/libpagedattn.so``.
@@ -23,7 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpagedattn.so")
-TENSORS = os.path.join(BUILD, "_pa_tensors.so")
+BINDING = os.path.join(BUILD, "_pa_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,9 +44,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(TENSORS):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TENSORS))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -66,20 +66,20 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def _compile_tensors() -> None:
-    """The binding's argument checks (csrc/pa_tensors.cpp) against this machine's torch."""
+def _compile_binding() -> None:
+    """The binding's C++ calls (csrc/pa_binding.cpp) against this machine's torch."""
     import torch
     import torch.utils.cpp_extension as ext
-    tmp = TENSORS + f".tmp{os.getpid()}"
+    tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           os.path.join(CSRC, "pa_tensors.cpp"), "-o", tmp,
+           os.path.join(CSRC, "pa_binding.cpp"), "-o", tmp,
            *[f"-I{d}" for d in ext.include_paths() + [sysconfig.get_paths()["include"]]],
-           *[f"-L{d}" for d in ext.library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10",
+           *[f"-L{d}" for d in ext.library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"building the binding's checks failed:\n{r.stderr}")
-    os.replace(tmp, TENSORS)
+        raise RuntimeError(f"building the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -88,9 +88,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        tensors = ex.submit(_compile_tensors)
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, srcs))
-        tensors.result()
+        binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for _, log in results:
             f.write(log)

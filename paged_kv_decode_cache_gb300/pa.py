@@ -583,85 +583,29 @@ def pa_decode_splitkv_noalloc(out, lse, q, k_cache, v_cache, block_tables, seq_l
 # ---------------------------------------------------------------------------------------------
 # The operators around a decode step: rotary positions, score rules, beams, pages.
 #
-# These calls are short on the GPU (2 to 12 us), so their wrappers spend little on the host: the
-# tensors are checked, and their addresses and sizes taken, by one call into C++
-# (csrc/pa_tensors.cpp), and the current stream's handle comes without a Stream object.
+# These calls are short on the GPU (2 to 12 us), so they spend little on the host: one call into C++
+# (csrc/pa_binding.cpp) checks the tensors and calls the library on the current stream.
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_entry_points = {}
-
-_STATUS = ("status", "i32", 1, "optional")
-_SPACE = ("workspace", "any", 0, "space")
+_native = None
 
 
-def _tensor_specs():
-    """What each wrapper below takes: name -> (argument, type, dimensions, kind) of its tensors."""
-    specs = {}
-    for pool in ("bf16", "u8"):
-        cache = (("k_cache", pool, 4, "whole"), ("v_cache", pool, 4, "whole"))
-        specs["rope", pool] = (
-            ("q_out", "bf16", 3, "rows"), ("q", "bf16", 3, "rows"), ("k_new", "bf16", 3, "rows"),
-            ("v_new", "bf16", 3, "rows"), ("positions", "i32", 1, "whole"),
-            ("slot_mapping", "i64", 1, "whole"), *cache, _STATUS)
-        for nd in (3, 4):
-            specs["scored", pool, nd] = (
-                ("out", "bf16", nd, "whole"), ("lse", "f32", nd - 1, "optional"), ("q", "bf16", nd, "whole"), *cache,
-                ("block_tables", "i32", 2, "whole"), ("seq_lens", "i32", 1, "whole"),
-                ("alibi_slopes", "f32", 1, "optional"), ("prefix_lens", "i32", 1, "optional"), _SPACE, _STATUS)
-    specs["fork"] = (
-        ("new_tables", "i32", 2, "whole"), ("new_lens", "i32", 1, "whole"), ("new_refs", "i32", 1, "whole"),
-        ("slot_mapping", "i64", 1, "whole"), ("tables", "i32", 2, "whole"), ("lens", "i32", 1, "whole"),
-        ("refs", "i32", 1, "whole"), ("parents", "i32", 1, "whole"), _SPACE, _STATUS)
-    specs["compact"] = (
-        ("new_tables", "i32", 2, "whole"), ("new_refs", "i32", 1, "whole"), ("remap", "i32", 1, "whole"),
-        ("n_live", "i32", 1, "whole"), ("tables", "i32", 2, "whole"), ("lens", "i32", 1, "whole"),
-        ("refs", "i32", 1, "whole"), _SPACE, _STATUS)
-    specs["copy"] = (("pairs", "i32", 2, "whole"), _STATUS)
-    specs["beam"] = (
-        ("scores", "f32", 2, "whole"), ("tokens", "i32", 2, "whole"), ("parents", "i32", 2, "whole"),
-        ("logits", "logits", 2, "rows"), ("cum", "f32", 2, "whole"), ("finished", "u8", 2, "optional"), _SPACE)
-    return specs
-
-
-_take_tensors = None
-_specs = {}
-
-
-def _take(spec, *tensors):
-    """(device, address, sizes, ...) of the tensors a wrapper is given, checked against its spec."""
-    global _take_tensors
-    if _take_tensors is None:
-        if not os.path.exists(_build.TENSORS):
-            raise RuntimeError(f"{_build.TENSORS} is missing: build it with "
-                               "paged_kv_decode_cache_gb300.build.build()")
-        loader = importlib.machinery.ExtensionFileLoader("_pa_tensors", _build.TENSORS)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_tensors", loader))
+def _binding():
+    """The C++ calls, loaded on first use (raises if they have not been built)."""
+    global _native
+    if _native is None:
+        lib()
+        path = _build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with paged_kv_decode_cache_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_pa_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_binding", loader))
         loader.exec_module(module)
-        _specs.update({k: module.make_spec(v) for k, v in _tensor_specs().items()})
-        _take_tensors = module.take
-    return _take_tensors(_specs[spec], *tensors)
-
-
-def _enqueue(name: str, dev: int, stream, *args):
-    """Call the entry point on device `dev` and `stream` (default: the device's current one)."""
-    fn = _entry_points.get(name)
-    if fn is None:
-        fn = _entry_points[name] = getattr(lib(), name)
-    if stream is None:
-        s = _raw_stream(dev)
-    elif stream.device.index != dev:
-        raise ValueError(f"{name}: stream on {stream.device}, tensors on cuda:{dev}")
-    else:
-        s = stream.cuda_stream
-    if _current_device() == dev:
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc != PA_OK:
-        raise PAError(name, rc, pa_strerror(rc))
+        raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        module.init(library_path(), PAError, raw_stream, current_device, torch.cuda.set_device)
+        _native = module
+    return _native
 
 
 _ROPE_LAYOUTS = {"half": PA_ROPE_HALF, "interleaved": PA_ROPE_INTERLEAVED}
@@ -685,34 +629,18 @@ def pa_rope_init(rot_dim: int, base: float, layout: str = "half", scaling: str =
     return rope
 
 
-def _rope_write(name, pool, q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, scales, rope,
-                status, stream):
-    if not isinstance(rope, Rope):
-        raise TypeError("rope must be a plan made by pa_rope_init")
-    (dev, qo, n1, h1, d1, qo_row, qa, n, hq, d, q_row, ka, n2, hkv, d2, k_row, va, n3, h3, d3, v_row, pos, n4, slots, n5,
-     kc, nb, bs, ch, cd, vc, nb2, bs2, ch2, cd2, st, _) = _take(
-        ("rope", pool), q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, status)
-    if not (n == n1 == n2 == n3 == n4 == n5):
-        raise ValueError("q_out, q, k_new, v_new, positions and slot_mapping must have as many tokens")
-    if h1 != hq or h3 != hkv or not (d == d1 == d2 == d3 == cd == cd2) or ch != hkv or ch2 != hkv or nb2 != nb or \
-            bs2 != bs:
-        raise ValueError("q_out and q must be [N, Hq, D], k_new and v_new [N, Hkv, D] matching the pools")
-    _enqueue(name, dev, stream, qo, qo_row, qa, q_row, ka, k_row, va, v_row, pos, slots, n, hq, kc, vc,
-             CacheDesc(nb, bs, ch, cd), *scales, ctypes.byref(rope), st)
-
-
 def pa_rope_write(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, rope,
                   status=None, stream=None):
     """Turn q into q_out, and write the turned k_new and v_new through slot_mapping."""
-    _rope_write("pa_rope_write", "bf16", q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, (), rope,
-                status, stream)
+    (_native or _binding()).rope_write(False, q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, None,
+                                       None, rope, status, stream)
 
 
 def pa_rope_write_fp8(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, k_scale,
                       v_scale, rope, status=None, stream=None):
     """pa_rope_write into uint8 e4m3 pools."""
-    _rope_write("pa_rope_write_fp8", "u8", q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache,
-                (k_scale, v_scale), rope, status, stream)
+    (_native or _binding()).rope_write(True, q_out, q, k_new, v_new, positions, slot_mapping, k_cache, v_cache, k_scale,
+                                       v_scale, rope, status, stream)
 
 
 class PoolSet:
@@ -722,30 +650,16 @@ class PoolSet:
 
     def __init__(self, pools):
         self.pools = list(pools)
-        if not self.pools:
-            raise ValueError("a PoolSet needs at least one pool")
-        first = self.pools[0]
-        if first.dtype not in (torch.bfloat16, torch.uint8):
-            raise TypeError(f"pools must be torch.bfloat16 or torch.uint8, got {first.dtype}")
-        for t in self.pools:
-            _need(t, "every pool", first.dtype, 4)
-            if t.shape != first.shape or t.device != first.device:
-                raise ValueError("the pools differ in shape or device")
-        self.device = first.device
-        self.device_index = first.get_device()
-        self.num_blocks = first.shape[0]
-        self.desc = cache_desc(first)
-        self.elem_bytes = first.element_size()
-        self._ptrs = (ctypes.c_void_p * len(self.pools))(*[t.data_ptr() for t in self.pools])
+        self._handle = _binding().pools(*self.pools)
 
     def __len__(self):
         return len(self.pools)
 
 
-def _pools_of(pools) -> PoolSet:
+def _pools_of(pools):
     if not isinstance(pools, PoolSet):
         raise TypeError("pools must be a PoolSet")
-    return pools
+    return pools._handle
 
 
 def pa_fork_workspace_bytes(B_old: int, B_new: int, num_blocks: int) -> int:
@@ -756,47 +670,24 @@ def pa_compact_workspace_bytes(num_blocks: int) -> int:
     return int(lib().pa_compact_workspace_bytes(num_blocks))
 
 
-def _enqueue_on_pools(name, dev, stream, pools, *args):
-    if dev != pools.device_index:
-        raise ValueError(f"{name}: the pools are on another device")
-    _enqueue(name, dev, stream, *args)
-
-
 def pa_sequences_fork(new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents, pools,
                       workspace, status=None, stream=None):
     """New row i is old row parents[i] (negative: none), blocks shared, last blocks copied on write;
     slot_mapping gets the slot of every row's next token."""
-    _pools_of(pools)
-    (dev, nt, n1, mb1, nl, n2, nr, nb1, slots, n3, ta, old, mb, le, old1, re, nb, pr, n, ws, ws_bytes, st, _) = _take(
-        "fork", new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents, workspace, status)
-    if old1 != old or nb != pools.num_blocks or nb1 != nb:
-        raise ValueError("tables, lens and refs must be [B, max_blocks], [B] and [num_blocks]")
-    if not (n == n1 == n2 == n3) or mb1 != mb:
-        raise ValueError("the new tables, lens and slots must have a row for every parent")
-    _enqueue_on_pools("pa_sequences_fork", dev, stream, pools, nt, nl, nr, slots, ta, le, re, pr, old, n, mb, pools._ptrs,
-                      len(pools.pools), pools.elem_bytes, pools.desc, ws, ws_bytes, st)
+    (_native or _binding()).sequences_fork(new_tables, new_lens, new_refs, slot_mapping, tables, lens, refs, parents,
+                                           _pools_of(pools), workspace, status, stream)
 
 
 def pa_blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace,
                       status=None, stream=None):
     """Live blocks moved to the front of every pool; remap: every old block id's new one (-1: free)."""
-    _pools_of(pools)
-    (dev, nt, n1, mb1, nr, nb1, rm, nb2, nlv, one, ta, n, mb, le, n2, re, nb, ws, ws_bytes, st, _) = _take(
-        "compact", new_tables, new_refs, remap, n_live, tables, lens, refs, workspace, status)
-    if not (n == n1 == n2) or mb1 != mb or not (nb == nb1 == nb2 == pools.num_blocks) or one != 1:
-        raise ValueError("tables [B, max_blocks], lens [B], counts and remap [num_blocks], n_live [1]")
-    _enqueue_on_pools("pa_blocks_compact", dev, stream, pools, nt, nr, rm, nlv, ta, le, re, n, mb, pools._ptrs,
-                      len(pools.pools), pools.elem_bytes, pools.desc, ws, ws_bytes, st)
+    (_native or _binding()).blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, _pools_of(pools),
+                                           workspace, status, stream)
 
 
 def pa_blocks_copy(pools, pairs, status=None, stream=None):
     """Copy whole blocks within every pool: pairs int32 [n, 2], source and destination."""
-    _pools_of(pools)
-    dev, at, n, two, st, _ = _take("copy", pairs, status)
-    if two != 2:
-        raise ValueError("pairs must be [n, 2]")
-    _enqueue_on_pools("pa_blocks_copy", dev, stream, pools, pools._ptrs, len(pools.pools), pools.elem_bytes, pools.desc, at,
-                      n, st)
+    (_native or _binding()).blocks_copy(_pools_of(pools), pairs, status, stream)
 
 
 _LOGITS = {torch.bfloat16: PA_LOGITS_BF16, torch.float32: PA_LOGITS_F32}
@@ -811,14 +702,7 @@ def pa_beam_workspace_bytes(groups: int, beams: int, vocab: int, K: int, dtype: 
 def pa_beam_select(scores, tokens, parents, logits, cum, finished=None, eos=-1, workspace=None, stream=None):
     """The K best of beams x vocabulary for every request: logits [groups * beams, vocab] (rows may be
     strided), cum [groups, beams], finished uint8 [groups, beams]; scores, tokens, parents [groups, K]."""
-    (dev, sc, g1, K, tk, g2, K2, pr, g3, K3, kind, lo, rows, vocab, row, cu, groups, beams, fi, g4, b4, ws,
-     ws_bytes) = _take("beam", scores, tokens, parents, logits, cum, finished, workspace)
-    if rows != groups * beams or not (groups == g1 == g2 == g3) or K2 != K or K3 != K:
-        raise ValueError("logits must be [groups * beams, vocab]; scores, tokens and parents [groups, K]")
-    if finished is not None and (g4 != groups or b4 != beams):
-        raise ValueError("finished must be [groups, beams]")
-    _enqueue("pa_beam_select", dev, stream, sc, tk, pr, lo, kind, row, cu, fi or None, eos, groups, beams, vocab, K, ws,
-             ws_bytes)
+    (_native or _binding()).beam_select(scores, tokens, parents, logits, cum, finished, eos, workspace, stream)
 
 
 def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_blocks_per_seq: int,
@@ -829,51 +713,21 @@ def pa_scored_num_splits(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_bloc
     return r
 
 
-def _decode_scored(name, pool, out, lse, q, k_cache, v_cache, scales, block_tables, seq_lens, scale, softcap,
-                   alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace, status, stream):
-    nd = q.dim() if isinstance(q, torch.Tensor) else 3
-    if nd == 3:
-        (dev, oa, B1, H1, D1, la, B2, H2, qa, B, Hq, D, kc, nb, bs, hkv, d, vc, nb2, bs2, hkv2, d2, bt, B3, mb, sl, B4, al,
-         H5, pf, B5, ws, ws_bytes, st, _) = _take(("scored", pool, 3), out, lse, q, k_cache, v_cache, block_tables,
-                                                  seq_lens, alibi_slopes, prefix_lens, workspace, status)
-        q_len = Q1 = Q2 = 1
-    elif nd == 4:
-        (dev, oa, B1, Q1, H1, D1, la, B2, Q2, H2, qa, B, q_len, Hq, D, kc, nb, bs, hkv, d, vc, nb2, bs2, hkv2, d2, bt, B3,
-         mb, sl, B4, al, H5, pf, B5, ws, ws_bytes, st, _) = _take(
-            ("scored", pool, 4), out, lse, q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, prefix_lens,
-            workspace, status)
-    else:
-        raise ValueError(f"q must be [B, Hq, D] or [B, q_len, Hq, D], got {tuple(q.shape)}")
-    if B1 != B or Q1 != q_len or H1 != Hq or D1 != D or nb2 != nb or bs2 != bs or hkv2 != hkv or d != D or d2 != D or \
-            B3 != B or B4 != B:
-        raise ValueError("inconsistent out / q / cache / table shapes")
-    if lse is not None and (B2 != B or Q2 != q_len or H2 != Hq):
-        raise ValueError("lse must have q's shape without its last dimension")
-    if alibi_slopes is not None and H5 != Hq:
-        raise ValueError("alibi_slopes must be [Hq]")
-    if prefix_lens is not None:
-        if B5 != B:
-            raise ValueError("prefix_lens must be [B]")
-        if max_prefix is None:
-            max_prefix = mb * bs
-    rules = ScoreRules(softcap, al, window, pf, max_prefix or 0)
-    _enqueue(name, dev, stream, oa, la, qa, q_len, kc, vc, CacheDesc(nb, bs, hkv, d), *scales, bt, mb, sl, B, Hq, scale,
-             ctypes.byref(rules), num_splits, ws, ws_bytes, st)
-
-
 def pa_decode_scored(out, lse, q, k_cache, v_cache, block_tables, seq_lens, scale, softcap=0.0,
                      alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None, num_splits=0,
                      workspace=None, status=None, stream=None):
     """Split-KV decode (q [B, Hq, D]) or causal multi-query decode (q [B, q_len, Hq, D]) with capped
     scores, a distance bias, a sliding window and a prefix that every query sees.  max_prefix: a bound
     on prefix_lens (default: the table's tokens)."""
-    _decode_scored("pa_decode_scored", "bf16", out, lse, q, k_cache, v_cache, (), block_tables, seq_lens, scale, softcap,
-                   alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace, status, stream)
+    (_native or _binding()).decode_scored(False, out, lse, q, k_cache, v_cache, None, None, block_tables, seq_lens, scale,
+                                          softcap, alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace,
+                                          status, stream)
 
 
 def pa_decode_scored_fp8(out, lse, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
                          softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, max_prefix=None,
                          num_splits=0, workspace=None, status=None, stream=None):
     """pa_decode_scored over uint8 e4m3 pools with per-pool scales."""
-    _decode_scored("pa_decode_scored_fp8", "u8", out, lse, q, k_cache, v_cache, (k_scale, v_scale), block_tables, seq_lens,
-                   scale, softcap, alibi_slopes, window, prefix_lens, max_prefix, num_splits, workspace, status, stream)
+    (_native or _binding()).decode_scored(True, out, lse, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                                          scale, softcap, alibi_slopes, window, prefix_lens, max_prefix, num_splits,
+                                          workspace, status, stream)
