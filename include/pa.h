@@ -667,7 +667,7 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
  * leaves its beam without candidates.  cum: device fp32
  * [groups, beams], the beams' scores so far (-inf: no candidates).  finished:
  * device bytes [groups, beams] or NULL: a finished beam's one continuation is
- * (eos, cum), and its logits are not read; eos in [0, vocab).
+ * (eos, cum), whatever its logits; eos in [0, vocab).
  * scores: device fp32 [groups, K]; tokens, parents: device int32 [groups, K],
  * parents[i] = group * beams + w (as pa_sequences_fork takes them).  Where fewer than K
  * entries have a score above -inf, the rest are (-inf, -1, -1).

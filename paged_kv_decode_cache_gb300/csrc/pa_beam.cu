@@ -11,8 +11,11 @@
 // no barrier.  After up to 16 chunks, what K of the threads' maxima reach bounds
 // the K-th largest value from below, and only the groups that reach it (about twice K) are
 // read again, from L2, for the values themselves.  (Taking candidates out
-// while streaming cost more than the stream: 50 us against 27 for 256 rows of
-// 151937.)  The last CTA of a request to finish joins its lists.
+// while streaming cost as much again: 62 us against 30 for 256 rows of 151937 in
+// bf16.)  The last CTA of a request to finish joins its lists.  Those 30 us are
+// the stream's 17 (4.5 TB/s: one wave of CTAs, which all start and end at once), 6 to 7
+// for the candidates, 5 to 6 for the join and 2 for the launch; 4 rows of 32000
+// take 9, a chain of latencies.
 //
 // Sums: exp in fp32 from x - max (exact for bf16), fp32 sums of 8 per vector
 // and of a thread's vectors, 64 bits across threads and slices.  Scores are
@@ -21,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -39,9 +43,13 @@ constexpr int kRingBytes = kThreads / 32 * kStages * (kWarpVecs + 1) * 16;
 constexpr int kMaxK = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxJoin = 4096;                // candidates a request's join holds
+constexpr int kJoinBytes = 20;                // of shared memory per candidate of a join
+constexpr int kDirect = 128;                  // entries that a join ranks without a bound first
+constexpr int kHeads = 1024;                  // lists' first entries that make the bound
+// a score's two roundings in fp32, and its lse's: within 2^-24 of |cum| + |x| + |lse| each
+constexpr float kSlack = 4.76837158e-7f;      // 2^-21
 constexpr int kPool = 2 * kThreads;            // candidates of a slice at a time
 constexpr int kWaveCtas = 4 * 152;            // slices: one wave of 4 CTAs per SM
-constexpr int kMinSliceVecs = 2 * kThreads;   // and no smaller than two vectors per thread
 
 template <int N>
 struct Int {
@@ -230,6 +238,33 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *w
     return key;
 }
 
+// ln z for z >= 1, to 2^-23 or so: CUDA's log(double) is a chain of some 60
+// FP64 instructions, 1 us here, which a GB300 SM issues at 1/64 of its FP32 rate.
+// z = 2^e m with m in [0.6875, 1.375): e ln 2 in 64 bits, and |ln m| < 0.38 in 32.
+__device__ __forceinline__ double log_of_sum(double z) {
+    if (!(z < INFINITY)) return z;
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(z));
+    const int up = (u >> 49 & 7) >= 3;   // 1.375 and above is halved
+    const int e = static_cast<int>(u >> 52) - 1023 + up;
+    const double m = __longlong_as_double(static_cast<long long>((u & 0xfffffffffffffull) | static_cast<uint64_t>(1023 - up) << 52));
+    const float mf = static_cast<float>(m);
+    return e * 0.6931471805599453 + static_cast<double>(logf(mf) + static_cast<float>(m - mf) / mf);
+}
+
+// Sum of f(j) over j in [0, n) by a team of 2^t threads; every thread of the CTA calls.
+template <typename F>
+__device__ __forceinline__ int team_sum(int n, int team, F &&f) {
+    int sum = 0;
+#pragma unroll 8
+    for (int j = threadIdx.x & (team - 1); j < n; j += team) sum += f(j);
+    for (int o = team >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+// Threads of the CTA for each of n entries: a power of two, at most a warp.
+__device__ __forceinline__ int team_of(int n) {
+    return n > kThreads / 2 ? 1 : min(32, 1 << (31 - __clz(kThreads / max(n, 1))));
+}
+
 // How many of pool[0 .. n) come before c; four at a time, so the pool has room for 3
 // more entries, which the caller has set to 0.
 __device__ __forceinline__ int place_of(uint64_t c, const uint64_t *pool, int n) {
@@ -343,7 +378,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
-    extern __shared__ __align__(16) uint64_t dyn_smem[];  // the warps' rings; then 24 bytes per entry of the join
+    extern __shared__ __align__(16) uint64_t dyn_smem[];  // the warps' rings; then kJoinBytes per entry of the join
     __shared__ uint32_t warp_keys[kThreads / 32];
     __shared__ __align__(16) uint64_t pool[kPool + 4];  // candidates for the slice's K largest
     __shared__ int count, groups, ticket;
@@ -352,32 +387,41 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     __shared__ int group_at[kGroups];
     __shared__ float red_max[kThreads / 32];
     __shared__ double red_sum[kThreads / 32];
-    __shared__ double lse[kMaxBeams], beam_cum[kMaxBeams];
-    __shared__ bool beam_done[kMaxBeams];
-    __shared__ uint64_t bound;
+    __shared__ double lse[kMaxBeams];
+    __shared__ float beam_cum[kMaxBeams], base[kMaxBeams], slack[kMaxBeams];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_id = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
     const int group = row_id / a.beams, K = a.K;
+    const int first_row = group * a.beams;
+    const Row<T> row(static_cast<const T *>(a.logits) + row_id * a.row_stride, a.vocab);
+    const int vecs = (a.vocab + E - 1) / E;
+    const int per = (vecs + a.slices - 1) / a.slices;
+    const int v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
+    uint4(*ring)[kWarpVecs + 1] = reinterpret_cast<uint4(*)[kWarpVecs + 1]>(
+        reinterpret_cast<uint4 *>(dyn_smem) + warp * kStages * (kWarpVecs + 1));   // [kStages], this warp's
+#pragma unroll
+    for (int u = 0; u < kStages - 1; ++u) {   // (on its way before `finished` is looked at)
+        if (v0 + u * kChunkVecs < v1) row.fetch(ring[u], v0 + u * kChunkVecs, v1);
+        cp_async_commit();
+    }
     const bool done = a.finished && a.finished[row_id];
+    if (tid < a.beams) beam_cum[tid] = a.cum[first_row + tid];   // (for the join, which would wait for them)
 
-    if (!done) {
-        const Row<T> row(static_cast<const T *>(a.logits) + row_id * a.row_stride, a.vocab);
-        const int vecs = (a.vocab + E - 1) / E;
-        const int per = (vecs + a.slices - 1) / a.slices;
-        const int v0 = min(slice * per, vecs), v1 = min(v0 + per, vecs);
+    const int64_t part = static_cast<int64_t>(row_id) * a.slices + slice;
+    if (done) {   // its one continuation, as the only entry of a row with lse = 0
+        cp_async_wait<0>();
+        if (tid == 0) {
+            a.part_max[part] = slice == 0 ? 0.f : -INFINITY;
+            a.part_sum[part] = slice == 0 ? 1.0 : 0.0;
+        }
+        if (tid < K) a.part_list[part * K + tid] = slice == 0 && tid == 0 ? candidate(0.f, a.eos) : 0;
+    } else {
         float m = -INFINITY, sum = 0.f;   // this thread's maximum and sum of exp(x - m)
         float floor = -INFINITY;          // values at or below it are not among the slice's K largest
         bool overfull = false;
         int kept = 0;                     // the K largest so far, pool[0 .. kept)
-        uint4(*ring)[kWarpVecs + 1] = reinterpret_cast<uint4(*)[kWarpVecs + 1]>(
-            reinterpret_cast<uint4 *>(dyn_smem) + warp * kStages * (kWarpVecs + 1));   // [kStages], this warp's
-#pragma unroll
-        for (int u = 0; u < kStages - 1; ++u) {
-            if (v0 + u * kChunkVecs < v1) row.fetch(ring[u], v0 + u * kChunkVecs, v1);
-            cp_async_commit();
-        }
         int stage = 0;
         for (int b0 = v0; b0 < v1; b0 += kBatch * kChunkVecs) {
             const int b1 = min(b0 + kBatch * kChunkVecs, v1);
@@ -439,16 +483,26 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             __syncthreads();
             const int n_groups = groups;
             if (n_groups > kGroups) overfull = true;
-            // ---- a warp per group: its values again, now from L2
+            // ---- a warp per group: its values again, now from L2 (four groups' on their way at once)
             static_assert(kVecs * E <= 32, "a group's values, one per lane");
-#pragma unroll 4
-            for (int g = warp; g < min(n_groups, kGroups); g += kThreads / 32) {
-                const int v = group_at[g] + lane / E * 32, i = v * E + lane % E;
-                const float value = lane < kVecs * E && v < v1 && i < a.vocab ? to_float(row.x[i]) : -INFINITY;
-                if (strict ? value > cut : value >= cut) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < kPool) pool[at] = candidate(value, i);
+            constexpr int kAtOnce = 4, kWarps = kThreads / 32;
+            const int found = min(n_groups, kGroups);
+            for (int g0 = warp; g0 < found; g0 += kAtOnce * kWarps) {
+                float value[kAtOnce];
+                int entry[kAtOnce];
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int g = g0 + u * kWarps, v = group_at[min(g, kGroups - 1)] + lane / E * 32;
+                    entry[u] = v * E + lane % E;
+                    value[u] = g < found && lane < kVecs * E && v < v1 && entry[u] < a.vocab ? to_float(row.x[entry[u]])
+                                                                                             : -INFINITY;
                 }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u)
+                    if (strict ? value[u] > cut : value[u] >= cut) {
+                        const int at = atomicAdd(&count, 1);
+                        if (at < kPool) pool[at] = candidate(value[u], entry[u]);
+                    }
             }
             __syncthreads();
             if (count > kPool) overfull = true;
@@ -475,12 +529,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) red_sum[warp] = z;
         __syncthreads();
-        const int64_t part = static_cast<int64_t>(row_id) * a.slices + slice;
         if (tid == 0) {
-            double s = 0.0;
-            for (int i = 0; i < kThreads / 32; ++i) s += red_sum[i];
+            static_assert(kThreads == 256, "eight warps' sums");
             a.part_max[part] = top;
-            a.part_sum[part] = s;
+            a.part_sum[part] = ((red_sum[0] + red_sum[1]) + (red_sum[2] + red_sum[3])) +
+                               ((red_sum[4] + red_sum[5]) + (red_sum[6] + red_sum[7]));
         }
         if (tid < K) a.part_list[part * K + tid] = tid < kept ? pool[tid] : 0;
     }
@@ -493,15 +546,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     if (ticket != a.beams * a.slices - 1) return;
     __threadfence();
     if (tid == 0) a.tickets[group] = 0;
-    const int first_row = group * a.beams;
     // ---- everything the slices left, in one round trip
     const int lists = a.beams * a.slices, entries = lists * K;
-    uint64_t *keys = dyn_smem;                                      // [entries] candidates, then scores' keys
-    uint64_t *top_keys = keys + entries;                            // [entries] those that the bound leaves
-    int *index = reinterpret_cast<int *>(top_keys + entries);       // [entries] place in beams x vocabulary
-    int *top_index = index + entries;                               // [entries]
+    uint64_t *keys = dyn_smem;                                      // [entries] candidates
+    uint64_t *top_keys = keys + entries;                            // [entries] scores' keys, of those that the bound leaves
+    int *top_index = reinterpret_cast<int *>(top_keys + entries);   // [entries] place in beams x vocabulary
     double *slice_sum = reinterpret_cast<double *>(top_keys);       // [lists], then the maxima
-    float *slice_max = reinterpret_cast<float *>(index);            // [lists]
+    float *slice_max = reinterpret_cast<float *>(top_index);        // [lists]
     const int64_t part0 = static_cast<int64_t>(first_row) * a.slices;
     for (int i = tid; i < entries; i += kThreads)
         keys[i] = __ldcg(reinterpret_cast<const unsigned long long *>(a.part_list) + part0 * K + i);
@@ -509,75 +560,74 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         slice_max[l] = __ldcg(a.part_max + part0 + l);
         slice_sum[l] = __ldcg(a.part_sum + part0 + l);
     }
-    if (tid < a.beams) {
-        beam_cum[tid] = a.cum[first_row + tid];
-        beam_done[tid] = a.finished && a.finished[first_row + tid];
-    }
-    if (tid == 0) count = 0, bound = 1;
+    if (tid == 0) count = 0;
     __syncthreads();
-    if (tid < a.beams) {
+    for (int w = warp; w < a.beams; w += kThreads / 32) {   // a warp per beam
+        const float *of_max = slice_max + w * a.slices;
+        const double *of_sum = slice_sum + w * a.slices;
         float M = -INFINITY;
         double z = 0.0;
-        if (!beam_done[tid]) {
-            for (int s = tid * a.slices; s < (tid + 1) * a.slices; ++s) M = fmaxf(M, slice_max[s]);
-            for (int s = tid * a.slices; s < (tid + 1) * a.slices; ++s)
-                z += slice_sum[s] * (slice_max[s] > -INFINITY ? fast_exp2((slice_max[s] - M) * 1.4426950408889634f) : 1.f);
+        for (int i = lane; i < a.slices; i += 32) M = fmaxf(M, of_max[i]);
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int i = lane; i < a.slices; i += 32)
+            z += of_sum[i] * (of_max[i] > -INFINITY ? fast_exp2((of_max[i] - M) * 1.4426950408889634f) : 1.f);
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < a.slices) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0) {
+            const double row_lse = M > -INFINITY ? M + log_of_sum(z) : INFINITY;
+            const float cum = beam_cum[w], l = static_cast<float>(row_lse);
+            lse[w] = row_lse;
+            base[w] = cum > -INFINITY && l < INFINITY ? fmaxf(cum - l, -FLT_MAX) : -INFINITY;   // (-inf: no candidates)
+            slack[w] = kSlack * (fabsf(cum) + fabsf(l));
         }
-        lse[tid] = M > -INFINITY ? M + log(z) : INFINITY;
     }
     __syncthreads();
-    // ---- every candidate's score, as a key (0: none)
+    // ---- the candidates that may be among the K best: a score's range in fp32, what K
+    // of the lower ends of the lists' first few reach, and 64 bits only
+    // for those whose upper end reaches it.  (An SM's few FP64 units take some 250
+    // cycles for one operation of every thread.)  Few candidates are all taken.
+    auto range_of = [&](int w, uint64_t c, float &lo, float &hi) {
+        if (c == 0 || !(base[w] > -INFINITY)) return false;
+        const float x = candidate_value(c), s = fmaxf(x + base[w], -FLT_MAX), d = slack[w] + kSlack * fabsf(x);
+        lo = d < INFINITY ? s - d : -INFINITY;
+        hi = s + d;
+        return true;
+    };
+    const int spread = lane * (kThreads / 32) + warp;   // (consecutive entries: one to a warp)
+    const float per_entry = 1.f / (a.slices * K);       // (below 2^-12: (i + 0.5) times it is never near a whole number)
+    float lo, hi;
+    uint32_t bound = 0;
+    if (entries > kDirect) {
+        const int each = min(K, (kHeads + lists - 1) / lists);
+        uint32_t mine = 0;
+        for (int i = spread; i < lists * each; i += kThreads) {
+            const int l = i / each;
+            if (range_of(l / a.slices, keys[l * K + i % each], lo, hi)) mine = max(mine, order_key(lo));
+        }
+        bound = reached_by<0>(mine, K, warp_keys);
+    }
+    const float cut = bound ? key_value<0>(bound) : -INFINITY;
     for (int i = tid; i < entries; i += kThreads) {
-        const int l = i / K, w = l / a.slices;
+        const int w = static_cast<int>((i + 0.5f) * per_entry);
         const uint64_t c = keys[i];
-        uint64_t key = 0;
-        double score = -INFINITY;
-        if (beam_done[w]) {  // its one continuation
-            if (l % a.slices == 0 && i % K == 0) score = beam_cum[w];
-            index[i] = w * a.vocab + a.eos;
-        } else if (c) {
-            score = beam_cum[w] + (static_cast<double>(candidate_value(c)) - lse[w]);
-            index[i] = w * a.vocab + candidate_entry(c);
-        }
-        if (score > -INFINITY) key = order_key(score);  // (not -inf, not NaN)
-        keys[i] = key;
+        if (!range_of(w, c, lo, hi) || !(hi >= cut)) continue;
+        const double score = beam_cum[w] + (candidate_value(c) - lse[w]);   // (in 64 bits)
+        if (!(score > -INFINITY)) continue;
+        const int at = atomicAdd(&count, 1);
+        top_keys[at] = order_key(score);
+        top_index[at] = w * a.vocab + candidate_entry(c);
     }
     __syncthreads();
-    // The K-th largest of the lists' first few (2 K in all) bounds the K-th best
-    // score from below.
-    {
-        const int each = min(K, (2 * K + lists - 1) / lists), heads = lists * each;
-        for (int i = tid; i < heads; i += kThreads) top_keys[i] = keys[i / each * K + i % each];
-        __syncthreads();
-        for (int i = tid; i < heads; i += kThreads) {
-            const uint64_t k = top_keys[i];
-            int place = 0;
-#pragma unroll 8
-            for (int j = 0; j < heads; ++j)
-                place += static_cast<int>(top_keys[j] > k) | (static_cast<int>(top_keys[j] == k) & static_cast<int>(j < i));
-            if (place == K - 1 && k) bound = k;
-        }
-        __syncthreads();
-    }
-    for (int i = tid; i < entries; i += kThreads) {
-        const uint64_t k = keys[i];
-        if (k >= bound) {
-            const int at = atomicAdd(&count, 1);
-            top_keys[at] = k;
-            top_index[at] = index[i];
-        }
-    }
-    __syncthreads();
-    const int n = count;
+    const int n = count, team = team_of(n);
     const int64_t out = static_cast<int64_t>(group) * K;
-    for (int i = tid; i < n; i += kThreads) {
-        const uint64_t k = top_keys[i];
-        const int at = top_index[i];
-        int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j)   // (no branch: short-circuits cost 50 ns per entry)
-            place += static_cast<int>(top_keys[j] > k) | (static_cast<int>(top_keys[j] == k) & static_cast<int>(top_index[j] < at));
-        if (place < K) {
+    for (int i0 = 0; i0 < n; i0 += kThreads / team) {
+        const int i = i0 + tid / team;
+        const uint64_t k = i < n ? top_keys[i] : 0;
+        const int at = i < n ? top_index[i] : 0;
+        const int place = team_sum(n, team, [&](int j) {   // (no branch: short-circuits cost 50 ns per entry)
+            return static_cast<int>(top_keys[j] > k) | (static_cast<int>(top_keys[j] == k) & static_cast<int>(top_index[j] < at));
+        });
+        if (i < n && place < K && (tid & (team - 1)) == 0) {
             a.scores[out + place] = static_cast<float>(key_value(k));
             a.tokens[out + place] = at % a.vocab;
             a.parents[out + place] = first_row + at / a.vocab;
@@ -592,12 +642,17 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
 
 int elem_size(int32_t type) { return type == PA_LOGITS_BF16 ? 2 : type == PA_LOGITS_F32 ? 4 : 0; }
 
-// Slices of a row: as many CTAs as the GPU holds at once (256 rows: 2 slices take 35
-// us, 3 to 5 37 to 38), each with at least two vectors per thread, and no more
-// lists than the join holds.
+// Slices of a row: no more CTAs than the GPU holds at once (256 rows: 2 slices take
+// less than 3 to 5), each with at least a chunk.  A chunk more per slice costs a
+// CTA about 0.4 us and 100 candidates more in the join 0.15, so of C chunks and
+// beams x K candidates per slice, s^2 is about 300 C / (beams K); half of that, since
+// CTAs that share an SM slow one another (64 rows of 151937, 8 beams, K = 16: 4
+// slices 18 us, 9 slices 21; one request of them: 4 15.5, 6 16, 19 14.8).  And no more
+// than the join holds.
 int slices_of(int64_t rows, int beams, int vocab, int K, int elem) {
-    const int64_t vecs = (static_cast<int64_t>(vocab) * elem + 15) / 16;
-    int64_t s = std::min((vecs + kMinSliceVecs - 1) / kMinSliceVecs, std::max<int64_t>(1, kWaveCtas / rows));
+    const int64_t vecs = (static_cast<int64_t>(vocab) * elem + 15) / 16, chunks = (vecs + kChunkVecs - 1) / kChunkVecs;
+    int64_t s = std::min(chunks, std::max<int64_t>(1, kWaveCtas / rows));
+    while (s > 1 && s * s * beams * K > 150 * chunks) --s;
     s = std::min<int64_t>(s, kMaxJoin / (beams * K));
     return static_cast<int>(std::max<int64_t>(1, s));
 }
@@ -656,14 +711,14 @@ int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void 
     a.part_sum = reinterpret_cast<double *>(ws);
     ws += pa::up(8 * parts);
     a.part_list = reinterpret_cast<uint64_t *>(ws);
-    const int smem = std::max(pa::kRingBytes, beams * a.slices * K * 24);
+    const int smem = std::max(pa::kRingBytes, beams * a.slices * K * pa::kJoinBytes);
     auto kern = logits_type == PA_LOGITS_BF16 ? pa::beam_select_kernel<__nv_bfloat16> : pa::beam_select_kernel<float>;
     static std::atomic<uint64_t> smem_attr_done[2];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done[logits_type].load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::kMaxJoin * 24) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::kMaxJoin * pa::kJoinBytes) != cudaSuccess)
             return PA_ECUDA;
         smem_attr_done[logits_type].fetch_or(bit, std::memory_order_release);
     }
