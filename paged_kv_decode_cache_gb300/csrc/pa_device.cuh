@@ -250,23 +250,26 @@ __device__ __forceinline__ uint2 e4m3x8_from_bf16(const uint4 &in, float scale) 
 // The same for 8 fp32 values (keys turned by their rotary angle), faster: a
 // product with 1 / scale (at most 2 units in the last place off the quotient)
 // gives the same code unless it lies that near the middle between two codes.
-// Those, and quotients below the smallest normal code (whose steps have another
-// width), are divided; a NaN has one code either way.  inv: 1 / scale, or NaN for a
+// Those are divided; a NaN has one code either way.  inv: 1 / scale, or NaN for a
 // scale so small or large that the product could leave fp32's normal range
 // (everything is then divided).  A rounding middle has the bits 100..0 below the
-// three mantissa bits that a code keeps: `near` is the least distance above 4 units
-// before one, in units of 2^-12 of those bits.
+// three mantissa bits that a code keeps; below the smallest normal code, 2^-6, the
+// codes' steps are those of [2^-6, 2^-5), so 2^-6 is added first (rounded to a unit
+// there).  `near` is the least distance above 4 units before a middle, in
+// units of 2^-12 of those bits.
 __device__ __forceinline__ uint2 e4m3x8_from_f32(const float (&f)[8], float scale, float inv) {
-    float q[8], least = INFINITY;
+    float q[8];
     uint32_t near = 0xffffffffu;
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
         unpack2(mul2(pack2(f[k], f[k + 1]), pack2(inv, inv)), q[k], q[k + 1]);
-        near = min(near, min(__float_as_uint(q[k]) * 4096u - ((0x80000u - 4u) << 12),
-                             __float_as_uint(q[k + 1]) * 4096u - ((0x80000u - 4u) << 12)));
-        least = fminf(least, fminf(fabsf(q[k]), fabsf(q[k + 1])));
+#pragma unroll
+        for (int u = k; u < k + 2; ++u) {
+            const float a = fabsf(q[u]), m = a < 0x1p-6f ? a + 0x1p-6f : a;
+            near = min(near, __float_as_uint(m) * 4096u - ((0x80000u - 4u) << 12));
+        }
     }
-    if (near <= 8u << 12 || least < 0x1p-6f || inv != inv) {
+    if (near <= 8u << 12 || inv != inv) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k] = f[k] / scale;
     }

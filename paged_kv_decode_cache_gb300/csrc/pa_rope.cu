@@ -42,17 +42,16 @@ struct RopeArgs {
 // The tokens' angles are computed once per CTA, one per thread at a time, while
 // the first loads are in flight; each token is loaded while the one before it is
 // turned.
-template <bool F8, int TB>
+template <bool F8, int TB, bool HALF>
 __global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
     __shared__ __align__(16) float2 turn[TB][PA_ROPE_MAX_PAIRS];  // (cos, sin) of the tokens' pairs
-    __shared__ int64_t slot_s[TB];                            // -1: not written
+    __shared__ int64_t row_s[TB];                             // the slots' rows in the pools, in elements (-1: not written)
     griddep_wait();
     griddep_launch_dependents();
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TB;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(TB), a.n - tok0));
     const int units = a.head_dim / kUnit, rot_units = rope.rot_dim / kUnit, pairs = rope.rot_dim / 2;
-    const bool half = rope.layout == PA_ROPE_HALF;
     const int total = (a.hq + 2 * a.hkv) * units;
     bool ready = false;
     for (int x = threadIdx.x; x < total || !ready; x += blockDim.x) {
@@ -62,17 +61,20 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
         // its two chunks: half of the dimensions that turn, or of the others, apart
         const int from = rotates || is_v ? 0 : rope.rot_dim;
         const int dims = rotates ? rope.rot_dim : a.head_dim - from;
-        const int e0 = from + 8 * (from ? u - rot_units : u), e1 = e0 + dims / 2;
+        const int e0 = from + 8 * (from ? u - rot_units : u);
         const int h = head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq);
         const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-        const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + tok0 * stride + h * a.head_dim;
+        const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + tok0 * stride + h * a.head_dim + e0;
+        __nv_bfloat16 *q_dst = a.q_out + tok0 * a.q_out_stride + h * a.head_dim + e0;
+        const int apart = dims / 2;
         uint4 next_lo, next_hi;
         auto load = [&](int t) {
             next_lo = next_hi = make_uint4(0u, 0u, 0u, 0u);
             if (t < tokens && x < total) {
-                next_lo = *reinterpret_cast<const uint4 *>(src + t * stride + e0);
-                next_hi = *reinterpret_cast<const uint4 *>(src + t * stride + e1);
+                next_lo = *reinterpret_cast<const uint4 *>(src);
+                next_hi = *reinterpret_cast<const uint4 *>(src + apart);
             }
+            src += stride;
         };
         load(0);
         for (int t = 0; t < tokens || !ready; ++t) {
@@ -89,14 +91,14 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
                 if (threadIdx.x < tokens) {
                     const int64_t slot = a.slots[tok0 + threadIdx.x];
                     if (slot >= a.n_slots) set_status(a.status, PA_STATUS_BAD_SLOT);
-                    slot_s[threadIdx.x] = slot < a.n_slots ? slot : -1;
+                    row_s[threadIdx.x] = slot < 0 || slot >= a.n_slots ? -1 : slot * a.hkv * a.head_dim;
                 }
                 __syncthreads();
                 ready = true;
             }
             if (x >= total) continue;
-            const int64_t slot = slot_s[t];
-            if (!is_q && slot < 0) continue;
+            const int64_t row = row_s[t];
+            if (!is_q && row < 0) continue;
             const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
             float f0[8], f1[8];  // the two chunks' values
 #pragma unroll
@@ -107,14 +109,14 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
             if (rotates) {
                 // pairs 8 u .. 8 u + 7, one of each in either chunk (half), or 4 u .. 4 u + 3 in
                 // the first and as many, rot_dim / 4 on, in the second (interleaved)
-                const float4 *c0 = reinterpret_cast<const float4 *>(&turn[t][half ? 8 * u : 4 * u]);
-                const float4 *c1 = half ? c0 + 2 : reinterpret_cast<const float4 *>(&turn[t][rope.rot_dim / 4 + 4 * u]);
+                const float4 *c0 = reinterpret_cast<const float4 *>(&turn[t][HALF ? 8 * u : 4 * u]);
+                const float4 *c1 = HALF ? c0 + 2 : reinterpret_cast<const float4 *>(&turn[t][rope.rot_dim / 4 + 4 * u]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float4 two = i < 4 ? c0[i / 2] : c1[i / 2 - 2];
                     const float c = i & 1 ? two.z : two.x, s = i & 1 ? two.w : two.y;
-                    float *fa = half ? f0 + i : i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
-                    float *fb = half ? f1 + i : fa + 1;
+                    float *fa = HALF ? f0 + i : i < 4 ? f0 + 2 * i : f1 + 2 * i - 8;
+                    float *fb = HALF ? f1 + i : fa + 1;
                     const float x0 = *fa, x1 = *fb;
                     *fa = x0 * c - x1 * s;
                     *fb = x0 * s + x1 * c;
@@ -122,13 +124,13 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
             }
             if (F8 && !is_q) {
                 const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
-                uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + (slot * a.hkv + h) * a.head_dim;
-                *reinterpret_cast<uint2 *>(dst + e0) = e4m3x8_from_f32(f0, scale, inv);
-                *reinterpret_cast<uint2 *>(dst + e1) = e4m3x8_from_f32(f1, scale, inv);
+                uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + row + h * a.head_dim + e0;
+                *reinterpret_cast<uint2 *>(dst) = e4m3x8_from_f32(f0, scale, inv);
+                *reinterpret_cast<uint2 *>(dst + apart) = e4m3x8_from_f32(f1, scale, inv);
             } else {
-                __nv_bfloat16 *dst = is_q ? a.q_out + (tok0 + t) * a.q_out_stride + h * a.head_dim
-                                          : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) +
-                                                (slot * a.hkv + h) * a.head_dim;
+                __nv_bfloat16 *dst = is_q ? q_dst + t * a.q_out_stride
+                                          : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) + row +
+                                                h * a.head_dim + e0;
                 uint32_t o0[4], o1[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -137,8 +139,8 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
                     o0[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b0) : w0[i];  // (a copy keeps its bits)
                     o1[i] = rotates ? *reinterpret_cast<const uint32_t *>(&b1) : w1[i];
                 }
-                *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                *reinterpret_cast<uint4 *>(dst + apart) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
             }
         }
     }
@@ -153,8 +155,10 @@ constexpr int kFourFrom = 768, kEightFrom = 4096;
 
 template <bool F8, int TB>
 cudaError_t launch_rope_instance(const RopeArgs &a, const pa_rope &rope, int threads, cudaStream_t stream) {
-    return launch_maybe_cooperative(rope_write_kernel<F8, TB>, dim3(static_cast<unsigned>((a.n + TB - 1) / TB)), threads,
-                                    0, stream, false, pdl_on(), a, rope);
+    return launch_maybe_cooperative(rope.layout == PA_ROPE_HALF ? rope_write_kernel<F8, TB, true>
+                                                                : rope_write_kernel<F8, TB, false>,
+                                    dim3(static_cast<unsigned>((a.n + TB - 1) / TB)), threads, 0, stream, false, pdl_on(),
+                                    a, rope);
 }
 
 template <bool F8>
