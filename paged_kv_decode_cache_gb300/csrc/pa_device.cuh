@@ -247,29 +247,30 @@ __device__ __forceinline__ uint2 e4m3x8_from_bf16(const uint4 &in, float scale) 
     return make_uint2(out[0], out[1]);
 }
 
-// The same for 8 fp32 values (keys turned by their rotary angle), faster: a
-// product with 1 / scale (at most 2 units in the last place off the quotient)
-// gives the same code unless it lies that near the middle between two codes.
-// Those are divided; a NaN has one code either way.  inv: 1 / scale, or NaN for a
-// scale so small or large that the product could leave fp32's normal range
-// (everything is then divided).  A rounding middle has the bits 100..0 below the
-// three mantissa bits that a code keeps; below the smallest normal code, 2^-6, the
-// codes' steps are those of [2^-6, 2^-5), so 2^-6 is added first (rounded to a unit
-// there).  `near` is the least distance above 4 units before a middle, in
-// units of 2^-12 of those bits.
+// The same for 8 fp32 values (keys turned by their rotary angle), without division
+// instructions: q = f inv, then twice q += inv (f - q scale).  The residual of an fma
+// is exact; the first step brings q next to the quotient, and the second one rounds
+// it correctly (Markstein's theorem: inv is 1 / scale rounded to nearest).  Where
+// that gives an infinity or a NaN (f is one, or a quotient leaves fp32's range), and
+// where inv is NaN (a scale outside 2^-60 .. 2^60, for which a residual could
+// underflow), the values are divided.
 __device__ __forceinline__ uint2 e4m3x8_from_f32(const float (&f)[8], float scale, float inv) {
     float q[8];
-    uint32_t near = 0xffffffffu;
+    const uint64_t inv2 = pack2(inv, inv), minus = pack2(-scale, -scale);
+    uint64_t odd = 0;   // (0, 0), or NaN
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        unpack2(mul2(pack2(f[k], f[k + 1]), pack2(inv, inv)), q[k], q[k + 1]);
-#pragma unroll
-        for (int u = k; u < k + 2; ++u) {
-            const float a = fabsf(q[u]), m = a < 0x1p-6f ? a + 0x1p-6f : a;
-            near = min(near, __float_as_uint(m) * 4096u - ((0x80000u - 4u) << 12));
-        }
+        const uint64_t f2 = pack2(f[k], f[k + 1]);
+        uint64_t q2 = mul2(f2, inv2);
+        q2 = fma2(fma2(q2, minus, f2), inv2, q2);
+        q2 = fma2(fma2(q2, minus, f2), inv2, q2);
+        odd = fma2(q2, 0, odd);
+        unpack2(q2, q[k], q[k + 1]);
+        q[k] = copysignf(q[k], f[k]), q[k + 1] = copysignf(q[k + 1], f[k + 1]);   // (a zero's sign)
     }
-    if (near <= 8u << 12 || inv != inv) {
+    float odd0, odd1;
+    unpack2(odd, odd0, odd1);
+    if (!(odd0 + odd1 == 0.f)) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k] = f[k] / scale;
     }

@@ -35,71 +35,89 @@ struct RopeArgs {
     float k_inv, v_inv;            // their reciprocals (e4m3x8_from_f32)
 };
 
-// Thread = one unit of 16 elements of one head of q, k or v, for the TB tokens of
-// its CTA: two 16-byte chunks half of the turning dimensions apart (of the others
+// Thread = one unit of 16 elements of one head of q, k or v, for groups of TB
+// tokens: two 16-byte chunks half of the turning dimensions apart (of the others
 // where nothing turns), which holds 8 whole pairs in either layout.  Neighbouring
 // threads take neighbouring chunks, so that a warp reads and writes whole lines.
-// The tokens' angles are computed once per CTA, one per thread at a time, while
-// the first loads are in flight; each token is loaded while the one before it is
-// turned.
+// A CTA's groups are gridDim.x apart: while one is turned, the next one's angles are
+// computed (one per thread at a time, kept in shared memory for all heads) from
+// positions read a group earlier, and a thread's loads run kAhead tokens ahead,
+// across groups.
 template <bool F8, int TB, bool HALF>
 __global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
-    __shared__ __align__(16) float2 turn[TB][PA_ROPE_MAX_PAIRS];  // (cos, sin) of the tokens' pairs
-    __shared__ int64_t row_s[TB];                             // the slots' rows in the pools, in elements (-1: not written)
+    constexpr int kAhead = TB < 2 ? 1 : 2;
+    static_assert(TB % kAhead == 0, "a token's registers are known at compile time");
+    __shared__ __align__(16) float2 turn[2][TB][PA_ROPE_MAX_PAIRS];  // (cos, sin) of the pairs: this group's, the next one's
+    __shared__ int32_t pos_s[2][TB];                             // positions of the next two groups
+    __shared__ int64_t row_s[3][TB];                             // rows in the pools, in elements (-1: not written)
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TB;
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(TB), a.n - tok0));
+    const int tid = threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * TB;   // a CTA's groups, in tokens
     const int units = a.head_dim / kUnit, rot_units = rope.rot_dim / kUnit, pairs = rope.rot_dim / 2;
-    const int total = (a.hq + 2 * a.hkv) * units;
-    bool ready = false;
-    for (int x = threadIdx.x; x < total || !ready; x += blockDim.x) {
-        const int head = min(x, total - 1) / units, u = x % units;
-        const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
-        const bool rotates = u < rot_units && !is_v;
-        // its two chunks: half of the dimensions that turn, or of the others, apart
-        const int from = rotates || is_v ? 0 : rope.rot_dim;
-        const int dims = rotates ? rope.rot_dim : a.head_dim - from;
-        const int e0 = from + 8 * (from ? u - rot_units : u);
-        const int h = head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq);
-        const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-        const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + tok0 * stride + h * a.head_dim + e0;
-        __nv_bfloat16 *q_dst = a.q_out + tok0 * a.q_out_stride + h * a.head_dim + e0;
-        const int apart = dims / 2;
-        uint4 next_lo, next_hi;
-        auto load = [&](int t) {
-            next_lo = next_hi = make_uint4(0u, 0u, 0u, 0u);
-            if (t < tokens && x < total) {
-                next_lo = *reinterpret_cast<const uint4 *>(src);
-                next_hi = *reinterpret_cast<const uint4 *>(src + apart);
-            }
-            src += stride;
-        };
-        load(0);
-        for (int t = 0; t < tokens || !ready; ++t) {
-            const uint4 lo = next_lo, hi = next_hi;
-            if (TB > 1) load(t + 1);   // (in place too: another token than the one written below)
-            if (!ready) {  // (every thread's first pass: the loads above are in flight)
-                for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
-                    const int at = i / pairs, k = i % pairs;
-                    const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(a.positions[tok0 + at])) * rope.turn[k];
-                    float s, c;
-                    sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
-                    turn[at][k] = make_float2(c * rope.magnitude, s * rope.magnitude);
-                }
-                if (threadIdx.x < tokens) {
-                    const int64_t slot = a.slots[tok0 + threadIdx.x];
-                    if (slot >= a.n_slots) set_status(a.status, PA_STATUS_BAD_SLOT);
-                    row_s[threadIdx.x] = slot < 0 || slot >= a.n_slots ? -1 : slot * a.hkv * a.head_dim;
-                }
-                __syncthreads();
-                ready = true;
-            }
-            if (x >= total) continue;
-            const int64_t row = row_s[t];
+    const int total = (a.hq + 2 * a.hkv) * units, x = blockIdx.y * blockDim.x + tid;
+    const int head = min(x, total - 1) / units, u = x % units;
+    const bool is_q = head < a.hq, is_v = head >= a.hq + a.hkv;
+    const bool rotates = u < rot_units && !is_v;
+    // its two chunks: half of the dimensions that turn, or of the others, apart
+    const int from = rotates || is_v ? 0 : rope.rot_dim;
+    const int apart = (rotates ? rope.rot_dim : a.head_dim - from) / 2;
+    const int e0 = from + 8 * (from ? u - rot_units : u);
+    const int at_head = (head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq)) * a.head_dim + e0;
+    const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+    const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + at_head;
+    uint4 lo[kAhead], hi[kAhead];
+    auto load = [&](int b, int64_t tok) {
+        lo[b] = hi[b] = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < a.n && x < total) {
+            lo[b] = *reinterpret_cast<const uint4 *>(src + tok * stride);
+            hi[b] = *reinterpret_cast<const uint4 *>(src + tok * stride + apart);
+        }
+    };
+    auto row_of = [&](int64_t tok) -> int64_t {
+        const int64_t slot = a.slots[tok];
+        if (slot >= a.n_slots) set_status(a.status, PA_STATUS_BAD_SLOT);
+        return slot < 0 || slot >= a.n_slots ? -1 : slot * a.hkv * a.head_dim;
+    };
+    auto angles = [&](int buf, int tokens, auto &&position) {
+        for (int i = tid; i < tokens * pairs; i += blockDim.x) {
+            const int at = i / pairs, k = i % pairs;
+            const uint64_t f = static_cast<uint64_t>(static_cast<int64_t>(position(at))) * rope.turn[k];
+            float s, c;
+            sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &s, &c);
+            turn[buf][at][k] = make_float2(c * rope.magnitude, s * rope.magnitude);
+        }
+    };
+    auto tokens_from = [&](int64_t tok) { return static_cast<int>(min(static_cast<int64_t>(TB), a.n - tok)); };
+
+    int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TB;
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) load(b, tok0 + b);
+    angles(0, tokens_from(tok0), [&](int at) { return a.positions[tok0 + at]; });
+    if (tid < TB && tok0 + tid < a.n) row_s[0][tid] = row_of(tok0 + tid);
+    if (tid < TB && tok0 + step + tid < a.n) {
+        pos_s[1][tid] = a.positions[tok0 + step + tid];
+        row_s[1][tid] = row_of(tok0 + step + tid);
+    }
+    __syncthreads();
+    for (int buf = 0, row3 = 0;; buf ^= 1, row3 = row3 == 2 ? 0 : row3 + 1, tok0 += step) {
+        const bool more = tok0 + step < a.n, mine = tid < TB && tok0 + 2 * step + tid < a.n;
+        int32_t pos2 = 0;
+        int64_t row2 = -1;
+        if (mine) pos2 = a.positions[tok0 + 2 * step + tid], row2 = row_of(tok0 + 2 * step + tid);
+        if (more) angles(buf ^ 1, tokens_from(tok0 + step), [&](int at) { return pos_s[buf ^ 1][at]; });
+        const int tokens = tokens_from(tok0);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const uint4 mine_lo = lo[t % kAhead], mine_hi = hi[t % kAhead];
+            // (in place too: another token than the one written below)
+            if (TB > 1) load(t % kAhead, t + kAhead < TB ? tok0 + t + kAhead : tok0 + step + t + kAhead - TB);
+            if (t >= tokens || x >= total) continue;
+            const int64_t row = row_s[row3][t];
             if (!is_q && row < 0) continue;
-            const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+            const uint32_t w0[4] = {mine_lo.x, mine_lo.y, mine_lo.z, mine_lo.w};
+            const uint32_t w1[4] = {mine_hi.x, mine_hi.y, mine_hi.z, mine_hi.w};
             float f0[8], f1[8];  // the two chunks' values
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -109,8 +127,9 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
             if (rotates) {
                 // pairs 8 u .. 8 u + 7, one of each in either chunk (half), or 4 u .. 4 u + 3 in
                 // the first and as many, rot_dim / 4 on, in the second (interleaved)
-                const float4 *c0 = reinterpret_cast<const float4 *>(&turn[t][HALF ? 8 * u : 4 * u]);
-                const float4 *c1 = HALF ? c0 + 2 : reinterpret_cast<const float4 *>(&turn[t][rope.rot_dim / 4 + 4 * u]);
+                const float2 *turns = turn[buf][t];
+                const float4 *c0 = reinterpret_cast<const float4 *>(turns + (HALF ? 8 * u : 4 * u));
+                const float4 *c1 = HALF ? c0 + 2 : reinterpret_cast<const float4 *>(turns + rope.rot_dim / 4 + 4 * u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float4 two = i < 4 ? c0[i / 2] : c1[i / 2 - 2];
@@ -124,13 +143,12 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
             }
             if (F8 && !is_q) {
                 const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
-                uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + row + h * a.head_dim + e0;
+                uint8_t *dst = (is_v ? a.v_cache : a.k_cache) + row + at_head;
                 *reinterpret_cast<uint2 *>(dst) = e4m3x8_from_f32(f0, scale, inv);
                 *reinterpret_cast<uint2 *>(dst + apart) = e4m3x8_from_f32(f1, scale, inv);
             } else {
-                __nv_bfloat16 *dst = is_q ? q_dst + t * a.q_out_stride
-                                          : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) + row +
-                                                h * a.head_dim + e0;
+                __nv_bfloat16 *dst = is_q ? a.q_out + (tok0 + t) * a.q_out_stride + at_head
+                                          : reinterpret_cast<__nv_bfloat16 *>(is_v ? a.v_cache : a.k_cache) + row + at_head;
                 uint32_t o0[4], o1[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -143,29 +161,32 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
                 *reinterpret_cast<uint4 *>(dst + apart) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
             }
         }
+        if (!more) break;
+        if (mine) pos_s[buf][tid] = pos2, row_s[row3 == 0 ? 2 : row3 - 1][tid] = row2;
+        __syncthreads();
     }
 }
 
-float reciprocal(float scale) { return scale > 0x1p-100f && scale < 0x1p100f ? 1.f / scale : NAN; }
+float reciprocal(float scale) { return scale > 0x1p-60f && scale < 0x1p60f ? 1.f / scale : NAN; }
 
-// Tokens per CTA: one where there are few (512 tokens of 32 heads: 4.0 us, with
-// four per CTA 6.4), four from 768 (1024 tokens of 36 heads: 6.3 us, with one 8.3),
-// eight from 4096 (16384 tokens into FP8 pools: 54.3 us, with four 57.8).
-constexpr int kFourFrom = 768, kEightFrom = 4096;
+// Tokens per group: one, and a CTA for each, where there are few; else four, and as
+// many CTAs as the GPU holds at once.
+constexpr int kFourFrom = 768;
 
 template <bool F8, int TB>
-cudaError_t launch_rope_instance(const RopeArgs &a, const pa_rope &rope, int threads, cudaStream_t stream) {
+cudaError_t launch_rope_instance(const RopeArgs &a, const pa_rope &rope, cudaStream_t stream) {
+    const int units = (a.hq + 2 * a.hkv) * (a.head_dim / kUnit), parts = (units + kMaxThreads - 1) / kMaxThreads;
+    const int threads = ((units + parts - 1) / parts + 31) / 32 * 32;
+    int64_t ctas = (a.n + TB - 1) / TB;
+    if (TB > 1) ctas = std::min<int64_t>(ctas, std::max(1, sm_count() * std::max(1, kMaxThreads * 2 / threads) / parts));
     return launch_maybe_cooperative(rope.layout == PA_ROPE_HALF ? rope_write_kernel<F8, TB, true>
                                                                 : rope_write_kernel<F8, TB, false>,
-                                    dim3(static_cast<unsigned>((a.n + TB - 1) / TB)), threads, 0, stream, false, pdl_on(),
-                                    a, rope);
+                                    dim3(static_cast<unsigned>(ctas), parts), threads, 0, stream, false, pdl_on(), a, rope);
 }
 
 template <bool F8>
-cudaError_t launch_rope(const RopeArgs &a, const pa_rope &rope, int threads, cudaStream_t stream) {
-    return a.n < kFourFrom    ? launch_rope_instance<F8, 1>(a, rope, threads, stream)
-           : a.n < kEightFrom ? launch_rope_instance<F8, 4>(a, rope, threads, stream)
-                              : launch_rope_instance<F8, 8>(a, rope, threads, stream);
+cudaError_t launch_rope(const RopeArgs &a, const pa_rope &rope, cudaStream_t stream) {
+    return a.n < kFourFrom ? launch_rope_instance<F8, 1>(a, rope, stream) : launch_rope_instance<F8, 4>(a, rope, stream);
 }
 
 int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
@@ -200,9 +221,7 @@ int rope_write(bool f8, void *q_out, int64_t q_out_stride, const void *q, int64_
                q_out_stride, q_stride, k_stride, v_stride, positions, slot_mapping, n_tokens,
                static_cast<int64_t>(cache.num_blocks) * cache.block_size, static_cast<uint8_t *>(k_cache),
                static_cast<uint8_t *>(v_cache), status, Hq, cache.num_kv_heads, cache.head_dim, k_scale, v_scale, reciprocal(k_scale), reciprocal(v_scale)};
-    const int units = (Hq + 2 * cache.num_kv_heads) * (cache.head_dim / kUnit);
-    const int threads = std::min(kMaxThreads, (units + 31) / 32 * 32);
-    const cudaError_t e = f8 ? launch_rope<true>(a, *rope, threads, stream) : launch_rope<false>(a, *rope, threads, stream);
+    const cudaError_t e = f8 ? launch_rope<true>(a, *rope, stream) : launch_rope<false>(a, *rope, stream);
     return e == cudaSuccess ? PA_OK : PA_ECUDA;
 }
 
