@@ -27,10 +27,13 @@ constexpr int kMaxPools = 256;
 constexpr int kCopyThreads = 256;
 constexpr int kPiece = 16 * 1024;      // bytes of a block per CTA and turn
 constexpr int kOwnTurns = 16;          // turns of a copy that a lone planning CTA makes itself
+constexpr int kNearBlocks = 2048;     // blocks whose compaction is planned by every CTA
 constexpr int kPlanWords = 4096;       // words of counts and tables per planning CTA
 
-// Block-wide exclusive prefix sum over kPlanThreads threads; *total gets the sum.
+// Block-wide exclusive prefix sum over kThreads threads; *total gets the sum.
+template <int kThreads = kPlanThreads>
 __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
@@ -41,17 +44,17 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int s = warp_sums[lane];
+        int s = lane < kWarps ? warp_sums[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
-        warp_sums[lane] = s;
+        if (lane < kWarps) warp_sums[lane] = s;
     }
     __syncthreads();
     const int before = warp ? warp_sums[warp - 1] : 0;
-    *total = warp_sums[31];
+    *total = warp_sums[kWarps - 1];
     __syncthreads();  // (warp_sums is free again)
     return before + x - v;
 }
@@ -80,11 +83,10 @@ struct CopyArgs {
 
 // Turns first, first + step, ... of a copy.  A turn is 16 KB of one block of one
 // pool, copied by one CTA with four 16-byte loads per thread (of kCopyThreads) in
-// flight.
-template <int kThreads>
-__device__ __forceinline__ void copy_turns(const CopyArgs &a, int count, int first, int step) {
+// flight.  entry(k): the k-th copy's source (< 0: none), destination and token rows.
+template <int kThreads, typename Entry>
+__device__ __forceinline__ void copy_turns(const CopyArgs &a, int count, int first, int step, Entry &&entry) {
     constexpr int kEach = kPiece / 16 / kThreads;
-    const int4 *entries = reinterpret_cast<const int4 *>(a.list + 1);
     const int64_t block_bytes = static_cast<int64_t>(a.block_size) * a.row_bytes;
     const int pieces = static_cast<int>((block_bytes + kPiece - 1) / kPiece);
     const int64_t turns = static_cast<int64_t>(count) * a.n_pools * pieces;
@@ -92,19 +94,9 @@ __device__ __forceinline__ void copy_turns(const CopyArgs &a, int count, int fir
     for (int64_t t = first; t < turns; t += step) {
         const int piece = static_cast<int>(t % pieces);
         const int64_t u = t / pieces;
-        const int pool = static_cast<int>(u % a.n_pools), k = static_cast<int>(u / a.n_pools);
-        int src, dst, rows = a.block_size;
-        if (a.list) {
-            const int4 e = __ldcg(entries + k);
-            src = e.x, dst = e.y, rows = e.z;
-        } else {
-            const int2 e = a.pairs[k];
-            src = e.x, dst = e.y;
-            if (src >= a.num_blocks || dst >= a.num_blocks || (src >= 0 && dst < 0)) {
-                if (threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-                continue;
-            }
-        }
+        const int pool = static_cast<int>(u % a.n_pools);
+        const int4 e = entry(static_cast<int>(u / a.n_pools));
+        const int src = e.x, dst = e.y, rows = e.z;
         if (src < 0) continue;
         const int64_t from = static_cast<int64_t>(piece) * kPiece;
         const int64_t left = static_cast<int64_t>(rows) * a.row_bytes - from;
@@ -125,6 +117,12 @@ __device__ __forceinline__ void copy_turns(const CopyArgs &a, int count, int fir
         }
     }
 }
+
+// A plan's list as entries of a copy.
+struct Listed {
+    const CopyList *list;
+    __device__ __forceinline__ int4 operator()(int k) const { return __ldcg(reinterpret_cast<const int4 *>(list + 1) + k); }
+};
 
 struct ForkArgs {
     int32_t *new_tables, *new_lens, *new_refs;
@@ -344,7 +342,7 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     if (kSmall) {
         __syncthreads();
         for (int i = tid; i < a.num_blocks; i += kPlanThreads) a.new_refs[i] = refs[i];
-        if (copy.list) copy_turns<kPlanThreads>(copy, copies, 0, 1);
+        if (copy.list) copy_turns<kPlanThreads>(copy, copies, 0, 1, Listed{copy.list});
     }
 }
 
@@ -419,28 +417,108 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
     }
 }
 
+// Rewrites the tables; new_id(id): where a block of the pool went, or -1.
+template <typename NewId>
+__device__ __forceinline__ void rewrite_tables(const CopyArgs &a, NewId &&new_id) {
+    const int64_t n = static_cast<int64_t>(a.B) * a.max_blocks;
+    for (int64_t x = blockIdx.x * static_cast<int64_t>(kCopyThreads) + threadIdx.x; x < n;
+         x += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
+        const int b = static_cast<int>(x / a.max_blocks), e = static_cast<int>(x % a.max_blocks);
+        const int L = checked_len(a.lens[b], a.max_blocks * a.block_size, a.status);
+        int id = -1;
+        if (e < (L + a.block_size - 1) / a.block_size) {
+            id = a.tables[x];
+            id = id >= 0 && id < a.num_blocks ? new_id(id) : -1;
+            if (id < 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+        }
+        a.new_tables[x] = id;
+    }
+}
+
 // Moves the listed blocks' first rows in every pool.  CTAs take turns in a
 // stride, so that the list's length (which only the GPU knows) spreads over all of
 // them.  Destinations are free blocks and sources live ones, so turns never meet.
 __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
     griddep_wait();
     griddep_launch_dependents();
-    if (a.new_tables) {
-        const int64_t n = static_cast<int64_t>(a.B) * a.max_blocks;
-        for (int64_t x = blockIdx.x * static_cast<int64_t>(kCopyThreads) + threadIdx.x; x < n;
-             x += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
-            const int b = static_cast<int>(x / a.max_blocks), e = static_cast<int>(x % a.max_blocks);
-            const int L = checked_len(a.lens[b], a.max_blocks * a.block_size, a.status);
-            int id = -1;
-            if (e < (L + a.block_size - 1) / a.block_size) {
-                id = a.tables[x];
-                id = id >= 0 && id < a.num_blocks ? a.remap[id] : -1;
-                if (id < 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-            }
-            a.new_tables[x] = id;
+    if (a.new_tables) rewrite_tables(a, [&](int id) { return a.remap[id]; });
+    if (a.list) {
+        copy_turns<kCopyThreads>(a, a.list->count, blockIdx.x, gridDim.x, Listed{a.list});
+        return;
+    }
+    copy_turns<kCopyThreads>(a, a.n_pairs, blockIdx.x, gridDim.x, [&](int k) {
+        const int2 e = a.pairs[k];
+        const bool bad = e.x >= a.num_blocks || e.y >= a.num_blocks || (e.x >= 0 && e.y < 0);
+        if (bad && threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+        return make_int4(bad ? -1 : e.x, e.y, a.block_size, 0);
+    });
+}
+
+// The plan and the copy in one launch, for pools of up to kNearBlocks blocks: every CTA
+// makes the plan for itself in shared memory (2 us, the counts being a few KB in
+// L2; a second launch and the way through memory are 2.5) and takes its turns
+// of the copy; the first one writes the new counts.
+__global__ void __launch_bounds__(kCopyThreads)
+compact_near_kernel(const CompactArgs a, const __grid_constant__ CopyArgs copy) {
+    constexpr int kEach = kNearBlocks / kCopyThreads;   // ids per thread
+    __shared__ int32_t warp_sums[kCopyThreads / 32];
+    __shared__ int32_t remap[kNearBlocks], holes[kNearBlocks / 2], movers[kNearBlocks / 2];
+    __shared__ int32_t stay;   // live blocks that keep their id
+    griddep_wait();
+    griddep_launch_dependents();
+    const int first_id = threadIdx.x * kEach, nb = a.num_blocks;
+    int refs[kEach], live = 0, n;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        refs[u] = first_id + u < nb ? a.refs[first_id + u] : 0;
+        live += refs[u] != 0;
+    }
+    const int rank = block_scan<kCopyThreads>(live, warp_sums, &n);
+    if (threadIdx.x == 0 && n == nb) stay = n;
+    int r = rank;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int i = first_id + u;
+        if (i >= nb) break;
+        if (i == n) stay = r;
+        if (refs[u] == 0) {
+            remap[i] = -1;
+            if (i < n) holes[i - r] = i;   // (at most n and nb - n of them)
+        } else {
+            if (i < n) remap[i] = i;
+            ++r;
         }
     }
-    copy_turns<kCopyThreads>(a, a.list ? a.list->count : a.n_pairs, blockIdx.x, gridDim.x);
+    __syncthreads();
+    const int moves = n - stay;
+    r = rank;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int i = first_id + u;
+        if (i < nb && refs[u] != 0) {
+            if (i >= n) {
+                const int k = r - stay;
+                movers[k] = i;
+                remap[i] = holes[k];
+            }
+            ++r;
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *a.n_live = n;
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int i = first_id + u;
+            if (i >= nb) break;
+            a.remap[i] = remap[i];
+            if (i >= n) a.new_refs[i] = 0;
+            if (refs[u] != 0) a.new_refs[remap[i]] = refs[u];
+        }
+    }
+    if (copy.new_tables) rewrite_tables(copy, [&](int id) { return remap[id]; });
+    copy_turns<kCopyThreads>(copy, moves, blockIdx.x, gridDim.x,
+                             [&](int k) { return make_int4(movers[k], holes[k], a.block_size, 0); });
 }
 
 int check_pools(void *const *pools, int32_t n_pools, int32_t elem_bytes, const pa_cache_desc &c) {
@@ -466,12 +544,13 @@ void set_pools(CopyArgs &a, void *const *pools, int32_t n_pools, int32_t elem_by
 }
 
 // Enough CTAs for `turns` (an upper bound), at most eight resident per SM.
-int launch_copy(const CopyArgs &a, int64_t turns, cudaStream_t stream) {
+template <typename... Args>
+int launch_turns(void (*kernel)(Args...), int64_t turns, cudaStream_t stream, const Args &...args) {
     const int sms = sm_count();
     if (sms <= 0) return PA_ECUDA;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(turns, static_cast<int64_t>(sms) * 8));
-    const cudaError_t e = launch_maybe_cooperative(copy_blocks_kernel, dim3(static_cast<unsigned>(grid)), kCopyThreads,
-                                                   0, stream, false, pdl_on(), a);
+    const cudaError_t e = launch_maybe_cooperative(kernel, dim3(static_cast<unsigned>(grid)), kCopyThreads, 0, stream,
+                                                   false, pdl_on(), args...);
     return e == cudaSuccess ? PA_OK : PA_ECUDA;
 }
 
@@ -570,7 +649,7 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
         return PA_ECUDA;
     if (turns == 0 || own_copy) return PA_OK;
     c.list = a.list;
-    return pa::launch_copy(c, turns, stream);
+    return pa::launch_turns(pa::copy_blocks_kernel, turns, stream, c);
 }
 
 int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live, const int32_t *tables,
@@ -600,20 +679,21 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
     a.holes = reinterpret_cast<int32_t *>(ws);
     a.cta_count = reinterpret_cast<int32_t *>(ws + pa::up(4 * static_cast<size_t>(cache.num_blocks)));
     a.B = B, a.max_blocks = max_blocks_per_seq, a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
-    const int ctas = pa::plan_ctas(cache.num_blocks);
-    if (pa::launch_clustered(pa::compact_plan_kernel, dim3(ctas), ctas, pa::kPlanThreads, 0, stream, pa::pdl_on(), a) !=
-        cudaSuccess)
-        return PA_ECUDA;
-    if (B == 0 && n_pools == 0) return PA_OK;
     pa::CopyArgs c{};
     pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.list = a.list;
     if (B > 0) c.new_tables = new_tables;
     c.tables = tables, c.lens = lens, c.remap = remap, c.B = B, c.max_blocks = max_blocks_per_seq;
     // (at most half of the blocks move)
-    const int64_t turns = static_cast<int64_t>(cache.num_blocks / 2) * n_pools * pa::pieces_of(cache, elem_bytes);
-    const int64_t entries = static_cast<int64_t>(B) * max_blocks_per_seq / pa::kCopyThreads;
-    return pa::launch_copy(c, std::max(turns, entries), stream);
+    const int64_t turns = std::max(static_cast<int64_t>(cache.num_blocks / 2) * n_pools * pa::pieces_of(cache, elem_bytes),
+                                   static_cast<int64_t>(B) * max_blocks_per_seq / pa::kCopyThreads);
+    if (cache.num_blocks <= pa::kNearBlocks) return pa::launch_turns(pa::compact_near_kernel, turns, stream, a, c);
+    const int ctas = pa::plan_ctas(cache.num_blocks);
+    if (pa::launch_clustered(pa::compact_plan_kernel, dim3(ctas), ctas, pa::kPlanThreads, 0, stream, pa::pdl_on(), a) !=
+        cudaSuccess)
+        return PA_ECUDA;
+    if (B == 0 && n_pools == 0) return PA_OK;
+    return pa::launch_turns(pa::copy_blocks_kernel, turns, stream, c);
 }
 
 int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, const int32_t *pairs,
@@ -627,7 +707,8 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
     pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.pairs = reinterpret_cast<const int2 *>(pairs);
     c.n_pairs = n_pairs;
-    return pa::launch_copy(c, static_cast<int64_t>(n_pairs) * n_pools * pa::pieces_of(cache, elem_bytes), stream);
+    const int64_t turns = static_cast<int64_t>(n_pairs) * n_pools * pa::pieces_of(cache, elem_bytes);
+    return pa::launch_turns(pa::copy_blocks_kernel, turns, stream, c);
 }
 
 }  // extern "C"

@@ -169,7 +169,9 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
 
 float reciprocal(float scale) { return scale > 0x1p-60f && scale < 0x1p60f ? 1.f / scale : NAN; }
 
-// Tokens per group: one, and a CTA for each, where there are few; else four, and as
+// Tokens per group: one, and a CTA for each, where there are few (600 tokens of 32 heads
+// into FP8 pools: 3.4 us, with four 4.3); else four (1536 tokens of 36 heads: 6.3 us,
+// with one 8.9; 16384 of 32 into FP8 pools: 45.1, into bf16 43), and as
 // many CTAs as the GPU holds at once.
 constexpr int kFourFrom = 768;
 

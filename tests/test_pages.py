@@ -251,6 +251,34 @@ def test_compact_matches_the_model(rows, bs, mb, spare, hkv, d, n_pools, fp8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("nb", [1, 2, 255, 256, 257, 2047, 2048, 2049, 5001])
+@pytest.mark.parametrize("live", ["every", "odd", "upper half", "lower half", "last", "some"])
+def test_compact_at_pool_sizes(nb, live):
+    """Counts of every pattern, tables of single blocks that name some of the live ones."""
+    rng = random.Random(nb)
+    pick = {"every": lambda i: True, "odd": lambda i: i % 2, "upper half": lambda i: i >= nb // 2,
+            "lower half": lambda i: i < nb // 2, "last": lambda i: i == nb - 1, "some": lambda i: rng.random() < 0.4}[live]
+    refs = [rng.randint(1, 3) if pick(i) else 0 for i in range(nb)]
+    ids = [i for i in range(nb) if refs[i]][-7:]
+    tables, lens = [[i] for i in ids] + [[-1]], [16 - rng.randrange(16) for _ in ids] + [0]
+    pools = make_pools(2, nb, 16, 1, 64, True, nb)
+    before = [t.clone() for t in pools]
+    new = [torch.full((len(lens), 1), 77, dtype=torch.int32, device="cuda"), dev([77] * nb), dev([77] * nb), dev([77])]
+    status = dev([0])
+    ws = torch.full((pa.pa_compact_workspace_bytes(nb),), 255, dtype=torch.uint8, device="cuda")
+    pa.pa_blocks_compact(*new, dev(tables), dev(lens), dev(refs), pa.PoolSet(pools), ws, status=status)
+    torch.cuda.synchronize()
+    want = plain_compact(tables, lens, refs, 16)
+    assert status.item() == 0
+    assert [t.cpu().tolist() for t in new] == [want[0], want[1], want[2], [want[3]]]
+    moved = [i for i, to in enumerate(want[2]) if to >= 0 and to != i]
+    for pool, old in zip(pools, before):
+        if moved:
+            old[[want[2][i] for i in moved]] = old[moved]
+        assert torch.equal(pool, old)
+
+
+@pytest.mark.gpu
 def test_compact_reports_entries_that_name_no_live_block():
     new = [dev([[7, 7]]), dev([7, 7, 7]), dev([7, 7, 7]), dev([7])]
     status = dev([0])
