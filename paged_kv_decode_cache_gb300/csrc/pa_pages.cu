@@ -67,7 +67,7 @@ struct CopyList {
 };
 
 struct CopyArgs {
-    const CopyList *list;       // or null: `pairs`
+    const CopyList *list;       // the copies, or:
     const int2 *pairs;          // (source, destination), n of them, whole blocks
     int n_pairs;
     int n_pools;
@@ -438,20 +438,21 @@ __device__ __forceinline__ void rewrite_tables(const CopyArgs &a, NewId &&new_id
 // Moves the listed blocks' first rows in every pool.  CTAs take turns in a
 // stride, so that the list's length (which only the GPU knows) spreads over all of
 // them.  Destinations are free blocks and sources live ones, so turns never meet.
+template <bool kPairs>
 __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
     griddep_wait();
     griddep_launch_dependents();
-    if (a.new_tables) rewrite_tables(a, [&](int id) { return a.remap[id]; });
-    if (a.list) {
+    if (kPairs) {
+        copy_turns<kCopyThreads>(a, a.n_pairs, blockIdx.x, gridDim.x, [&](int k) {
+            const int2 e = a.pairs[k];
+            const bool bad = e.x >= a.num_blocks || e.y >= a.num_blocks || (e.x >= 0 && e.y < 0);
+            if (bad && threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+            return make_int4(bad ? -1 : e.x, e.y, a.block_size, 0);
+        });
+    } else {
+        if (a.new_tables) rewrite_tables(a, [&](int id) { return a.remap[id]; });
         copy_turns<kCopyThreads>(a, a.list->count, blockIdx.x, gridDim.x, Listed{a.list});
-        return;
     }
-    copy_turns<kCopyThreads>(a, a.n_pairs, blockIdx.x, gridDim.x, [&](int k) {
-        const int2 e = a.pairs[k];
-        const bool bad = e.x >= a.num_blocks || e.y >= a.num_blocks || (e.x >= 0 && e.y < 0);
-        if (bad && threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-        return make_int4(bad ? -1 : e.x, e.y, a.block_size, 0);
-    });
 }
 
 // The plan and the copy in one launch, for pools of up to kNearBlocks blocks: every CTA
@@ -649,7 +650,7 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
         return PA_ECUDA;
     if (turns == 0 || own_copy) return PA_OK;
     c.list = a.list;
-    return pa::launch_turns(pa::copy_blocks_kernel, turns, stream, c);
+    return pa::launch_turns(pa::copy_blocks_kernel<false>, turns, stream, c);
 }
 
 int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live, const int32_t *tables,
@@ -693,7 +694,7 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
         cudaSuccess)
         return PA_ECUDA;
     if (B == 0 && n_pools == 0) return PA_OK;
-    return pa::launch_turns(pa::copy_blocks_kernel, turns, stream, c);
+    return pa::launch_turns(pa::copy_blocks_kernel<false>, turns, stream, c);
 }
 
 int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, const int32_t *pairs,
@@ -708,7 +709,7 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
     c.pairs = reinterpret_cast<const int2 *>(pairs);
     c.n_pairs = n_pairs;
     const int64_t turns = static_cast<int64_t>(n_pairs) * n_pools * pa::pieces_of(cache, elem_bytes);
-    return pa::launch_turns(pa::copy_blocks_kernel, turns, stream, c);
+    return pa::launch_turns(pa::copy_blocks_kernel<true>, turns, stream, c);
 }
 
 }  // extern "C"
