@@ -30,33 +30,46 @@ constexpr int kOwnTurns = 16;          // turns of a copy that a lone planning C
 constexpr int kNearBlocks = 2048;     // blocks whose compaction is planned by every CTA
 constexpr int kPlanWords = 4096;       // words of counts and tables per planning CTA
 
-// Block-wide exclusive prefix sum over kThreads threads; *total gets the sum.
-template <int kThreads = kPlanThreads>
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+// Block-wide exclusive prefix sum over kThreads threads; *total gets the sum.  (T: two
+// counts in one 64-bit number share the shuffles and the barriers.)
+template <int kThreads = kPlanThreads, typename T = int>
+__device__ __forceinline__ T block_scan(T v, T *warp_sums, T *total) {
     constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int s = lane < kWarps ? warp_sums[lane] : 0;
+        T s = lane < kWarps ? warp_sums[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            const T y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
         if (lane < kWarps) warp_sums[lane] = s;
     }
     __syncthreads();
-    const int before = warp ? warp_sums[warp - 1] : 0;
+    const T before = warp ? warp_sums[warp - 1] : 0;
     *total = warp_sums[kWarps - 1];
     __syncthreads();  // (warp_sums is free again)
     return before + x - v;
+}
+
+// The CTAs' values of a cluster: *before gets the sum of those below this one, the result is the
+// sum of all.  `mine` in shared memory, which the caller keeps until the next cluster barrier.
+__device__ __forceinline__ int cluster_scan(int *mine, int value, int ctas, int *before) {
+    if (threadIdx.x == 0) *mine = value;
+    cluster_sync();
+    const int lane = threadIdx.x & 31, rank = static_cast<int>(cluster_ctarank());
+    int v = 0;
+    if (lane < ctas) v = __float_as_int(ld_shared_cluster(map_shared_rank(smem_u32(mine), lane)));
+    *before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
+    return __reduce_add_sync(0xffffffffu, v);
 }
 
 // What a plan hands to the copy kernel.
@@ -133,7 +146,6 @@ struct ForkArgs {
     int32_t *free_list;   // [B_new] the lowest free ids
     int32_t *tail_count;  // [num_blocks] new rows whose partial last block it is
     int32_t *tail_first;  // [num_blocks] the first of them
-    int32_t *cta_count;   // [kMaxPlanCtas]
     int B_old, B_new, max_blocks, num_blocks, block_size;
 };
 
@@ -195,7 +207,8 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
         if (kSmall) __syncthreads();
         else cluster_sync();
     };
-    __shared__ int32_t warp_sums[32];
+    __shared__ uint64_t warp_sums[32];
+    __shared__ int cta_free;
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31;
@@ -260,57 +273,61 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     }
     everyone();
 
-    // ---- which rows need a block (every CTA for itself), in row order
-    int needed = 0, copies = 0;
+    // ---- which rows need a block (every CTA for itself, in row order), and the lowest
+    // free ids: each CTA a slice, each thread a segment.  What both read is asked
+    // for at once, and both are counted in one scan.
     const int per_row = (a.B_new + kPlanThreads - 1) / kPlanThreads;
-    {
-        const int i0 = min(tid * per_row, a.B_new), i1 = min(i0 + per_row, a.B_new);
-        int mine = 0;  // rows that need a block, and << 16 those that copy into it
-        for (int i = i0; i < i1; ++i) {
-            int need = 0;
-            if (row_parent[i] >= 0) {
-                const int L = row_len[i], t = row_tail[i];
-                if (L % bs == 0) need = L < lmax;
-                else if (t >= 0 && !(get(tail_count + t) == get(refs + t) && get(tail_first + t) == i)) need = 1 | 1 << 16;
-            }
-            row_rank[i] = need;
-            mine += need;
-        }
-        int total;
-        int at = block_scan(mine, warp_sums, &total);
-        needed = total & 0xffff, copies = total >> 16;
-        for (int i = i0; i < i1; ++i) {
-            const int need = row_rank[i];
-            row_rank[i] = need ? at : -1;  // its block's rank, and << 16 its copy's
-            at += need;
-        }
-        __syncthreads();
+    const int i0 = min(tid * per_row, a.B_new), i1 = min(i0 + per_row, a.B_new);
+    const int slice = (a.num_blocks + ctas - 1) / ctas;
+    const int s0 = min(cta * slice, a.num_blocks), s1 = min(s0 + slice, a.num_blocks);
+    const int seg = (slice + kPlanThreads - 1) / kPlanThreads;
+    const int lo = min(s0 + tid * seg, s1), hi = min(lo + seg, s1);
+    uint32_t mine = 0, mine_free = 0;   // rows that need a block, and << 16 those that copy into it; free ids
+    uint64_t zero = 0;                  // the segment's first 64 ids: free or not
+    for (int i = i0; i < i1; ++i) {
+        const int L = row_len[i], t = row_tail[i];
+        const bool part = row_parent[i] >= 0 && L % bs != 0 && t >= 0;
+        const int makers = part ? get(tail_count + t) : 0, all = part ? get(refs + t) : 0;
+        const int first = part ? get(tail_first + t) : 0;
+        int need = row_parent[i] >= 0 && L % bs == 0 && L < lmax;
+        if (part && !(makers == all && first == i)) need = 1 | 1 << 16;
+        row_rank[i] = need;
+        mine += need;
     }
-
-    // ---- the `needed` lowest free ids: each CTA a slice, each thread a segment
-    int n_free = 0;
-    if (needed > 0) {  // (the same in every CTA)
-        const int slice = (a.num_blocks + ctas - 1) / ctas;
-        const int s0 = min(cta * slice, a.num_blocks), s1 = min(s0 + slice, a.num_blocks);
-        const int seg = (slice + kPlanThreads - 1) / kPlanThreads;
-        const int lo = min(s0 + tid * seg, s1), hi = min(lo + seg, s1);
-        int total, mine = 0;
-        for (int i = lo; i < hi; ++i) mine += get(refs + i) == 0;
-        int at = block_scan(mine, warp_sums, &total);
-        n_free = total;
-        if (!kSmall) {
-            if (tid == 0) a.cta_count[cta] = total;
-            cluster_sync();
-            n_free = 0;
-            for (int c = 0; c < ctas; ++c) {
-                const int n = __ldcg(a.cta_count + c);
-                if (c < cta) at += n;
-                n_free += n;
+    for (int j = lo; j < hi; j += 4) {
+        int count[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) count[u] = j + u < hi ? get(refs + j + u) : 1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (count[u] == 0) {
+                ++mine_free;
+                if (j + u - lo < 64) zero |= 1ull << (j + u - lo);
             }
+    }
+    uint64_t total;
+    const uint64_t before = block_scan<kPlanThreads, uint64_t>(static_cast<uint64_t>(mine_free) << 32 | mine, warp_sums, &total);
+    const int needed = total & 0xffff, copies = static_cast<int>(total >> 16 & 0xffff);
+    uint32_t rank_at = static_cast<uint32_t>(before);
+    for (int i = i0; i < i1; ++i) {
+        const int need = row_rank[i];
+        row_rank[i] = need ? static_cast<int>(rank_at) : -1;  // its block's rank, and << 16 its copy's
+        rank_at += need;
+    }
+    int n_free = static_cast<int>(total >> 32);
+    if (needed > 0) {  // (the same in every CTA)
+        int at = static_cast<int>(before >> 32);
+        if (!kSmall) {
+            int below;
+            n_free = cluster_scan(&cta_free, n_free, ctas, &below);
+            at += below;
         }
-        for (int i = lo; i < hi && at < needed; ++i)
-            if (get(refs + i) == 0) free_list[at++] = i;
+        for (; zero && at < needed; zero &= zero - 1) free_list[at++] = lo + __ffsll(static_cast<long long>(zero)) - 1;
+        for (int j = lo + 64; j < hi && at < needed; ++j)
+            if (get(refs + j) == 0) free_list[at++] = j;
         everyone();
+    } else {
+        __syncthreads();
     }
 
     // ---- the rows' last blocks, slots and copies
@@ -352,7 +369,6 @@ struct CompactArgs {
     int32_t *status;
     CopyList *list;
     int32_t *holes;       // [num_blocks] free ids below the live count, ascending
-    int32_t *cta_count;   // [kMaxPlanCtas]
     int B, max_blocks, num_blocks, block_size;
 };
 
@@ -362,6 +378,7 @@ struct CompactArgs {
 // below n has rank id - r.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
     __shared__ int32_t warp_sums[32];
+    __shared__ int cta_live;
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, cta = blockIdx.x, ctas = gridDim.x;
@@ -369,15 +386,10 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
     const int s0 = min(cta * slice, a.num_blocks), s1 = min(s0 + slice, a.num_blocks);
     const int seg = (slice + kPlanThreads - 1) / kPlanThreads;
     const int lo = min(s0 + tid * seg, s1), hi = min(lo + seg, s1);
-    int total, n = 0;
+    int total, below;
     int rank = block_scan(hi - lo - count_zero(a.refs, lo, hi), warp_sums, &total);
-    if (tid == 0) a.cta_count[cta] = total;
-    cluster_sync();
-    for (int c = 0; c < ctas; ++c) {
-        const int k = __ldcg(a.cta_count + c);
-        if (c < cta) rank += k;
-        n += k;
-    }
+    const int n = cluster_scan(&cta_live, total, ctas, &below);
+    rank += below;
     // ---- what stays, the holes, and how many blocks move
     int r = rank;
     for (int i = lo; i < hi; ++i) {
@@ -577,13 +589,13 @@ extern "C" {
 size_t pa_fork_workspace_bytes(int32_t B_old, int32_t B_new, int32_t num_blocks) {
     if (B_old < 0 || B_new < 0 || num_blocks <= 0) return 0;
     return pa::up(sizeof(pa::CopyList) + 16 * static_cast<size_t>(B_new)) + pa::up(4 * static_cast<size_t>(B_new)) +
-           2 * pa::up(4 * static_cast<size_t>(num_blocks)) + 256;
+           2 * pa::up(4 * static_cast<size_t>(num_blocks));
 }
 
 size_t pa_compact_workspace_bytes(int32_t num_blocks) {
     if (num_blocks <= 0) return 0;
     return pa::up(sizeof(pa::CopyList) + 16 * static_cast<size_t>(num_blocks)) +
-           pa::up(4 * static_cast<size_t>(num_blocks)) + 256;
+           pa::up(4 * static_cast<size_t>(num_blocks));
 }
 
 int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs, int64_t *slot_mapping,
@@ -622,7 +634,6 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     a.free_list = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(B_new)));
     a.tail_count = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(cache.num_blocks)));
     a.tail_first = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(cache.num_blocks)));
-    a.cta_count = reinterpret_cast<int32_t *>(take(256));
     a.B_old = B_old, a.B_new = B_new, a.max_blocks = max_blocks_per_seq;
     a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
     const int ctas = pa::plan_ctas(cache.num_blocks + static_cast<int64_t>(B_old + B_new) * max_blocks_per_seq);
@@ -678,7 +689,6 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
     a.list = reinterpret_cast<pa::CopyList *>(ws);
     ws += pa::up(sizeof(pa::CopyList) + 16 * static_cast<size_t>(cache.num_blocks));
     a.holes = reinterpret_cast<int32_t *>(ws);
-    a.cta_count = reinterpret_cast<int32_t *>(ws + pa::up(4 * static_cast<size_t>(cache.num_blocks)));
     a.B = B, a.max_blocks = max_blocks_per_seq, a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
     pa::CopyArgs c{};
     pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
