@@ -80,6 +80,23 @@ static_assert(kPfSmemBytes <= 227 * 1024, "shared memory");
 static_assert(kPfNP * kPfPBuf >= kPfRows * 128 * 4, "the epilogue stages fp32 rows in the P buffers");
 static_assert(kPfStage % 1024 == 0 && kPfQHalf % 1024 == 0 && kPfPPart % 1024 == 0, "swizzle atoms");
 
+// The sequence of this CTA: the blockIdx.z-th longest one (of up to 32), so that the
+// CTAs that start last, as others finish, have the least to do (8 sequences of 512 to
+// 2048 tokens, 512 of them queries: 91.7 us in index order with a cap and a prefix,
+// 86.1 longest first).
+__device__ __forceinline__ int longest_first(const DecodeParams &p) {
+    const int B = gridDim.z, z = blockIdx.z;
+    if (B == 1 || B > 32 || p.seq_len_const >= 0) return z;
+    const int lane = threadIdx.x & 31;
+    const int len = lane < B ? p.seq_lens[lane] : 0;
+    int rank = 0;
+    for (int j = 0; j < B; ++j) {
+        const int other = __shfl_sync(0xffffffffu, len, j);
+        rank += other > len || (other == len && j < lane);
+    }
+    return __ffs(static_cast<int>(__ballot_sync(0xffffffffu, lane < B && rank == z))) - 1;
+}
+
 template <bool SC>
 __global__ void __launch_bounds__(kPfThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -106,10 +123,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     griddep_wait();
     griddep_launch_dependents();
 
-    const int part = blockIdx.x, b = blockIdx.z;
+    const int part = blockIdx.x, b = longest_first(p);
     const int Hkv = p.num_kv_heads, Hq = p.num_q_heads;
     const int g = blockIdx.y % Hkv;
-    const int qi0 = static_cast<int>(blockIdx.y / Hkv) * p.q_per_cta;  // the tile's first query position
+    // the tile's first query position (the last tile, which sees most keys, first)
+    const int qi0 = static_cast<int>((gridDim.y - 1 - blockIdx.y) / Hkv) * p.q_per_cta;
     const int nq = min(p.q_per_cta, p.q_len - qi0);
     const int nrows = nq * G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
