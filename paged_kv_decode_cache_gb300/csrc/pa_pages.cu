@@ -185,7 +185,7 @@ __device__ __forceinline__ void for_entries(const int32_t *row, int n, int lane,
 // block takes a free one.
 // kSmall: one CTA, which keeps the counts and lists in shared memory, so that only the
 // first loads, the tables and the copies themselves wait for memory (4 beams of a
-// request: 9.7 -> 6.3 us).  `copy.list`: the plan's, for a copy so small that this CTA makes
+// request: 9.7 -> 6.0 us).  `copy.list`: the plan's, for a copy so small that this CTA makes
 // it itself; null: another launch does.
 template <bool kSmall>
 __global__ void __launch_bounds__(kPlanThreads)

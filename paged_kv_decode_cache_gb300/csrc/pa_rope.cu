@@ -43,6 +43,9 @@ struct RopeArgs {
 // computed (one per thread at a time, kept in shared memory for all heads) from
 // positions read a group earlier, and a thread's loads run kAhead tokens ahead,
 // across groups.
+// Bound by a launch for a decode step (8 tokens of 36 heads: 2.3 us), by memory for
+// prompts (16384 tokens of 32 heads into bf16 pools 43 us, 0.93 of the copy rate;
+// into FP8 pools 45, 0.77: the warps that make codes take longer than the others).
 template <bool F8, int TB, bool HALF>
 __global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
