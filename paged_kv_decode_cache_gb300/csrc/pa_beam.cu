@@ -17,8 +17,9 @@
 // for the candidates, 5 to 6 for the join and 2 for the launch; 4 rows of 32000
 // take 9, a chain of latencies.
 //
-// Sums: exp in fp32 from x - max (exact for bf16), fp32 sums of 8 per vector
-// and of a thread's vectors, 64 bits across threads and slices.  Scores are
+// Sums: 2^(k x - k max) in fp32 with one rounding of the exponent, k = log2 e in
+// fp32, by which lse is divided in the end; fp32 sums of 8 per vector and of a
+// thread's vectors, 64 bits across threads and slices.  Scores are
 // compared in 64 bits: bf16 logits repeat, and beams' scores come close to one
 // another, so a score rounded to fp32 could trade two candidates.
 #include <cuda_bf16.h>
@@ -48,6 +49,7 @@ constexpr int kDirect = 128;                  // entries that a join ranks witho
 constexpr int kHeads = 1024;                  // lists' first entries that make the bound
 // a score's two roundings in fp32, and its lse's: within 2^-24 of |cum| + |x| + |lse| each
 constexpr float kSlack = 4.76837158e-7f;      // 2^-21
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPool = 2 * kThreads;            // candidates of a slice at a time
 constexpr int kWaveCtas = 4 * 152;            // slices: one wave of 4 CTAs per SM
 
@@ -76,13 +78,20 @@ struct Vec {  // a 16-byte vector of logits
             w[e] = __float_as_uint(x);
         }
     }
-    __device__ static float max(const uint4 &v) {
+    __device__ static float max(const uint4 (&v)[kVecs]) {
         if constexpr (k16) {
             auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
-            const __nv_bfloat162 m = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+            __nv_bfloat162 m = h(v[0].x);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                m = __hmax2(__hmax2(m, __hmax2(h(v[j].x), h(v[j].y))), __hmax2(h(v[j].z), h(v[j].w)));
             return fmaxf(__low2float(m), __high2float(m));
         } else {
-            return fmaxf(fmaxf(get(v, 0), get(v, 1)), fmaxf(get(v, 2), get(v, 3)));
+            float m = get(v[0], 0);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                m = fmaxf(fmaxf(m, fmaxf(get(v[j], 0), get(v[j], 1))), fmaxf(get(v[j], 2), get(v[j], 3)));
+            return m;
         }
     }
 };
@@ -131,7 +140,7 @@ struct BeamArgs {
     int32_t eos;
     int beams, vocab, K, slices;
     int32_t *tickets;      // [groups], zero between calls
-    float *part_max;       // [rows, slices]
+    float *part_max;       // [rows, slices] times k
     double *part_sum;      // [rows, slices]
     uint64_t *part_list;   // [rows, slices, K] candidates
 };
@@ -200,10 +209,12 @@ struct Row {
         for (int j = 0; j < kVecs; ++j) {
             const int i = vector_of(c0, j);
             if (i < end && i < whole) continue;
+            raw[j] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
+            if (i >= end) continue;
             uint32_t w[4] = {V::kFill, V::kFill, V::kFill, V::kFill};
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (i < end && i * E + e < vocab) V::put(w, e, x[i * E + e]);
+                if (i * E + e < vocab) V::put(w, e, x[i * E + e]);
             raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
@@ -238,17 +249,17 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *w
     return key;
 }
 
-// ln z for z >= 1, to 2^-23 or so: CUDA's log(double) is a chain of some 60
+// log2 z for z >= 1, to 2^-23 or so: CUDA's log2(double) is a chain of some 60
 // FP64 instructions, 1 us here, which a GB300 SM issues at 1/64 of its FP32 rate.
-// z = 2^e m with m in [0.6875, 1.375): e ln 2 in 64 bits, and |ln m| < 0.38 in 32.
-__device__ __forceinline__ double log_of_sum(double z) {
+// z = 2^e m with m in [0.6875, 1.375): e in 64 bits, and |ln m| < 0.38 in 32.
+__device__ __forceinline__ double log2_of_sum(double z) {
     if (!(z < INFINITY)) return z;
     const uint64_t u = static_cast<uint64_t>(__double_as_longlong(z));
     const int up = (u >> 49 & 7) >= 3;   // 1.375 and above is halved
     const int e = static_cast<int>(u >> 52) - 1023 + up;
     const double m = __longlong_as_double(static_cast<long long>((u & 0xfffffffffffffull) | static_cast<uint64_t>(1023 - up) << 52));
     const float mf = static_cast<float>(m);
-    return e * 0.6931471805599453 + static_cast<double>(logf(mf) + static_cast<float>(m - mf) / mf);
+    return e + 1.4426950408889634 * (logf(mf) + static_cast<float>(m - mf) / mf);
 }
 
 // Sum of f(j) over j in [0, n) by a team of 2^t threads; every thread of the CTA calls.
@@ -418,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         }
         if (tid < K) a.part_list[part * K + tid] = slice == 0 && tid == 0 ? candidate(0.f, a.eos) : 0;
     } else {
-        float m = -INFINITY, sum = 0.f;   // this thread's maximum and sum of exp(x - m)
+        float m = -INFINITY;              // this thread's maximum
+        uint64_t sum2 = 0;                // and sum of 2^(x k - m k), in two halves
         float floor = -INFINITY;          // values at or below it are not among the slice's K largest
         bool overfull = false;
         int kept = 0;                     // the K largest so far, pool[0 .. kept)
@@ -438,32 +450,30 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 row.take(raw, ring[stage], c0, v1);
                 __syncwarp();    // (and are read: the next fetch may go there)
                 stage = stage == kStages - 1 ? 0 : stage + 1;
-                float cmax = V::max(raw[0]);
-#pragma unroll
-                for (int j = 1; j < kVecs; ++j) cmax = fmaxf(cmax, V::max(raw[j]));
+                const float cmax = V::max(raw);
                 from_float(*gmax, cmax);
                 bmax = fmaxf(bmax, cmax);
                 if (cmax > m) {
-                    sum *= fast_exp2((m - cmax) * 1.4426950408889634f);  // (m = -inf: 0)
+                    const float f = fast_exp2(m * kLog2e - cmax * kLog2e);  // (m = -inf: 0)
+                    sum2 = mul2(sum2, pack2(f, f));
                     m = cmax;
                 }
-                const float minus = m > -INFINITY ? -m : 0.f;   // (a NaN goes into the sum all the same)
+                const float minus = m > -INFINITY ? -(m * kLog2e) : 0.f;   // (a NaN goes into the sum all the same)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
-                    float e2[E];
+                    uint64_t two[E / 2];
 #pragma unroll
                     for (int e = 0; e < E; e += 2) {
-                        const uint64_t t = mul2(add2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(minus, minus)),
-                                                pack2(1.4426950408889634f, 1.4426950408889634f));
-                        unpack2(t, e2[e], e2[e + 1]);
-                        e2[e] = fast_exp2(e2[e]);
-                        e2[e + 1] = fast_exp2(e2[e + 1]);
+                        float a0, a1;
+                        unpack2(fma2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(kLog2e, kLog2e),
+                                     pack2(minus, minus)), a0, a1);
+                        two[e / 2] = pack2(fast_exp2(a0), fast_exp2(a1));
                     }
 #pragma unroll
-                    for (int o = E / 2; o > 0; o >>= 1)
+                    for (int o = E / 4; o > 0; o >>= 1)
 #pragma unroll
-                        for (int e = 0; e < o; ++e) e2[e] += e2[e + o];
-                    sum += e2[0];
+                        for (int e = 0; e < o; ++e) two[e] = add2(two[e], two[e + o]);
+                    sum2 = add2(sum2, two[0]);
                 }
             }
             // ---- the groups (a thread's values of a chunk) that may hold one of the K largest
@@ -517,14 +527,17 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         __syncthreads();
         if (overfull) kept = exact_slice<T>(row, v0, v1, K, pool, &count, ring[0]);
         // ---- the slice's maximum, sum and list
-        float top = m;
+        float sum, sum_odd, top = m * kLog2e;   // (2^top: what the sums count from)
+        const float ref = top;
+        unpack2(sum2, sum, sum_odd);
+        sum += sum_odd;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane == 0) red_max[warp] = top;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, red_max[i]);
-        double z = m > -INFINITY ? sum * fast_exp2((m - top) * 1.4426950408889634f) : sum;  // (sum: 0 or NaN)
+        double z = m > -INFINITY ? sum * fast_exp2(ref - top) : sum;  // (sum: 0 or NaN)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) red_sum[warp] = z;
@@ -570,11 +583,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         for (int i = lane; i < a.slices; i += 32) M = fmaxf(M, of_max[i]);
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         for (int i = lane; i < a.slices; i += 32)
-            z += of_sum[i] * (of_max[i] > -INFINITY ? fast_exp2((of_max[i] - M) * 1.4426950408889634f) : 1.f);
+            z += of_sum[i] * (of_max[i] > -INFINITY ? fast_exp2(of_max[i] - M) : 1.f);
         for (int o = 16; o > 0; o >>= 1)
             if (o < a.slices) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) {
-            const double row_lse = M > -INFINITY ? M + log_of_sum(z) : INFINITY;
+            const double row_lse = M > -INFINITY ? (M + log2_of_sum(z)) * (1.0 / kLog2e) : INFINITY;
             const float cum = beam_cum[w], l = static_cast<float>(row_lse);
             lse[w] = row_lse;
             base[w] = cum > -INFINITY && l < INFINITY ? fmaxf(cum - l, -FLT_MAX) : -INFINITY;   // (-inf: no candidates)
