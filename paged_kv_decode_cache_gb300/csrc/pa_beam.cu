@@ -224,15 +224,15 @@ struct Row {
 };
 
 // A key that at least K of the threads' keys reach (0: fewer than K are not 0).
-// Each warp's ceil(K / 8)-th largest, and the lowest of the eight: two barriers, and
-// for values in no order about twice as many keys reach it as the K-th largest.
-// Where a warp has too few keys, or values that rise along the row let far more
+// The ceil(K / warps)-th largest of each of the first `warps` warps, and the lowest of
+// those: two barriers, and for values in no order about twice as many keys reach it as
+// the K-th largest.  Where a warp has too few keys, or values that rise along the row let far more
 // reach it, the K-th largest, bit by bit from the top with a CTA-wide count per bit.
 template <int kKeyLow>
-__device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *warp_keys) {
+__device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *warp_keys, int warps = kThreads / 32) {
     const int lane = threadIdx.x & 31;
     uint32_t left = mine, best = 0;
-    for (int r = 0; r < (K + kThreads / 32 - 1) / (kThreads / 32); ++r) {
+    for (int r = (K + warps - 1) / warps; r > 0; --r) {
         best = __reduce_max_sync(0xffffffffu, left);
         const uint32_t who = __ballot_sync(0xffffffffu, left == best);
         if (lane == __ffs(who) - 1) left = 0;
@@ -241,7 +241,7 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *w
     __syncthreads();
     uint32_t key = warp_keys[0];
 #pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) key = min(key, warp_keys[i]);
+    for (int i = 1; i < kThreads / 32; ++i) key = min(key, i < warps ? warp_keys[i] : key);
     if (__syncthreads_count(key && mine >= key) <= 3 * K + 16 && key) return key;
     key = 0;
     for (int bit = 31; bit >= kKeyLow; --bit)
@@ -249,31 +249,32 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *w
     return key;
 }
 
-// log2 z for z >= 1, to 2^-23 or so: CUDA's log2(double) is a chain of some 60
-// FP64 instructions, 1 us here, which a GB300 SM issues at 1/64 of its FP32 rate.
-// z = 2^e m with m in [0.6875, 1.375): e in 64 bits, and |ln m| < 0.38 in 32.
-__device__ __forceinline__ double log2_of_sum(double z) {
-    if (!(z < INFINITY)) return z;
+// log2 z for z >= 1 as whole + the result, to 2^-23 or so, in integers and fp32: CUDA's
+// log2(double) is a chain of some 60 FP64 instructions, 1 us here, which a GB300 SM
+// issues at 1/64 of its FP32 rate.  z = 2^whole (m + r) with m, the first 24 bits, in
+// [0.6875, 1.375).  NaN for a NaN.
+__device__ __forceinline__ float log2_of_sum(double z, int *whole) {
     const uint64_t u = static_cast<uint64_t>(__double_as_longlong(z));
     const int up = (u >> 49 & 7) >= 3;   // 1.375 and above is halved
-    const int e = static_cast<int>(u >> 52) - 1023 + up;
-    const double m = __longlong_as_double(static_cast<long long>((u & 0xfffffffffffffull) | static_cast<uint64_t>(1023 - up) << 52));
-    const float mf = static_cast<float>(m);
-    return e + 1.4426950408889634 * (logf(mf) + static_cast<float>(m - mf) / mf);
+    *whole = static_cast<int>(u >> 52) - 1023 + up;
+    const float m = __uint_as_float(static_cast<uint32_t>(127 - up) << 23 | (static_cast<uint32_t>(u >> 29) & 0x7fffffu));
+    const float r = static_cast<float>(static_cast<uint32_t>(u) & 0x1fffffffu) * (up ? 0x1p-53f : 0x1p-52f);
+    return u >> 52 < 0x7ff ? kLog2e * (logf(m) + r / m) : NAN;
 }
 
 // Sum of f(j) over j in [0, n) by a team of 2^t threads; every thread of the CTA calls.
 template <typename F>
-__device__ __forceinline__ int team_sum(int n, int team, F &&f) {
+__device__ __forceinline__ int team_sum(int n, int t, F &&f) {
     int sum = 0;
 #pragma unroll 8
-    for (int j = threadIdx.x & (team - 1); j < n; j += team) sum += f(j);
-    for (int o = team >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int j = threadIdx.x & ((1 << t) - 1); j < n; j += 1 << t) sum += f(j);
+    for (int o = 1 << t >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
-// Threads of the CTA for each of n entries: a power of two, at most a warp.
+// log2 of the CTA's threads for each of n entries: a power of two, at most a warp.
 __device__ __forceinline__ int team_of(int n) {
-    return n > kThreads / 2 ? 1 : min(32, 1 << (31 - __clz(kThreads / max(n, 1))));
+    static_assert(kThreads == 256, "8 - t: entries of teams of 2^t");
+    return n <= 8 ? 5 : max(0, 8 - (32 - __clz(n - 1)));
 }
 
 // How many of pool[0 .. n) come before c; four at a time, so the pool has room for 3
@@ -477,7 +478,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 }
             }
             // ---- the groups (a thread's values of a chunk) that may hold one of the K largest
-            const uint32_t key = reached_by<V::kKeyLow>(bmax > floor ? order_key(bmax) : 0u, K, warp_keys);
+            // (a short slice fills the first warps only; the last of them counts if it can give its share)
+            const int full = min((b1 - b0) / kWarpVecs, kThreads / 32), rest = b1 - b0 >= kChunkVecs ? 0 : (b1 - b0) % kWarpVecs;
+            const int warps = max(1, full + (min(rest, 32) * (full + 1) >= K ? 1 : 0));
+            const uint32_t key = reached_by<V::kKeyLow>(bmax > floor ? order_key(bmax) : 0u, K, warp_keys, warps);
             const float cut = key ? key_value<V::kKeyLow>(key) : floor;
             const bool strict = key == 0;   // (fewer than K threads have any value above the floor: all such values)
             if (tid == 0) groups = 0, count = kept;
@@ -575,21 +579,27 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     }
     if (tid == 0) count = 0;
     __syncthreads();
-    for (int w = warp; w < a.beams; w += kThreads / 32) {   // a warp per beam
+    // ---- the rows' lse, a few threads per row
+    const int t_lse = a.slices > 16 ? 5 : 32 - __clz(a.slices - 1), team = 1 << t_lse;
+    for (int w0 = 0; w0 < a.beams; w0 += kThreads >> t_lse) {
+        const int w = w0 + (tid >> t_lse), first = w < a.beams ? tid & (team - 1) : a.slices;
         const float *of_max = slice_max + w * a.slices;
         const double *of_sum = slice_sum + w * a.slices;
         float M = -INFINITY;
         double z = 0.0;
-        for (int i = lane; i < a.slices; i += 32) M = fmaxf(M, of_max[i]);
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int i = lane; i < a.slices; i += 32)
+        for (int i = first; i < a.slices; i += team) M = fmaxf(M, of_max[i]);
+        for (int o = team >> 1; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int i = first; i < a.slices; i += team)
             z += of_sum[i] * (of_max[i] > -INFINITY ? fast_exp2(of_max[i] - M) : 1.f);
-        for (int o = 16; o > 0; o >>= 1)
-            if (o < a.slices) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (lane == 0) {
-            const double row_lse = M > -INFINITY ? (M + log2_of_sum(z)) * (1.0 / kLog2e) : INFINITY;
-            const float cum = beam_cum[w], l = static_cast<float>(row_lse);
-            lse[w] = row_lse;
+        for (int o = team >> 1; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (first == 0 && w < a.beams) {
+            int whole;
+            const float part = log2_of_sum(z, &whole);
+            // M + whole + part, exact but for part's last bits, as two floats
+            const float add = static_cast<float>(whole), top = M + add, back = top - M;
+            const float low = ((M - (top - back)) + (add - back)) + part;
+            const float cum = beam_cum[w], l = M > -INFINITY ? (top + low) * (1.f / kLog2e) : INFINITY;
+            lse[w] = M > -INFINITY ? (static_cast<double>(top) + low) * (1.0 / kLog2e) : INFINITY;
             base[w] = cum > -INFINITY && l < INFINITY ? fmaxf(cum - l, -FLT_MAX) : -INFINITY;   // (-inf: no candidates)
             slack[w] = kSlack * (fabsf(cum) + fabsf(l));
         }
@@ -631,16 +641,16 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         top_index[at] = w * a.vocab + candidate_entry(c);
     }
     __syncthreads();
-    const int n = count, team = team_of(n);
+    const int n = count, t = team_of(n);
     const int64_t out = static_cast<int64_t>(group) * K;
-    for (int i0 = 0; i0 < n; i0 += kThreads / team) {
-        const int i = i0 + tid / team;
+    for (int i0 = 0; i0 < n; i0 += kThreads >> t) {
+        const int i = i0 + (tid >> t);
         const uint64_t k = i < n ? top_keys[i] : 0;
         const int at = i < n ? top_index[i] : 0;
-        const int place = team_sum(n, team, [&](int j) {   // (no branch: short-circuits cost 50 ns per entry)
+        const int place = team_sum(n, t, [&](int j) {   // (no branch: short-circuits cost 50 ns per entry)
             return static_cast<int>(top_keys[j] > k) | (static_cast<int>(top_keys[j] == k) & static_cast<int>(top_index[j] < at));
         });
-        if (i < n && place < K && (tid & (team - 1)) == 0) {
+        if (i < n && place < K && (tid & ((1 << t) - 1)) == 0) {
             a.scores[out + place] = static_cast<float>(key_value(k));
             a.tokens[out + place] = at % a.vocab;
             a.parents[out + place] = first_row + at / a.vocab;
