@@ -689,32 +689,42 @@ int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, 
                                        scored_positions(G, q_len));
     const int tiles = static_cast<int>(round_up(seen, 16) / 16);
     const int P = pa_choose_num_splits_mq(B, q_len, Hq, Hkv, D, tiles, 16, sms);
-    if (P < 1 || B < 1 || k != Kernel::kTensorCore || prefill_shape(G, q_len)) return P;
-    // That rule fills one wave, which for batches of 20 to 150 CTAs leaves SMs idle (64 CTAs
-    // on 152 SMs: P = 2) and, when the sequences' lengths differ, waits for the
-    // longest one's partitions.  In units of one CTA streaming the longest sequence, P
-    // partitions take about
-    //   ceil(units P / SMs) / P                        sequences all of that length
-    //   max(1 / P, units / (2 SMs) + 1 / (2 P))        lengths spread evenly below it
-    // and each wave after the first about 8 us more (a chunk takes 1.05 us).  P has the least
-    // sum of the two, among those that keep at least 8 tiles.  FP8, sequences of 8
-    // heads up to 4096 tokens: 64 of them with P = 7 take 113 us full and 81 us spread
-    // (P = 2: 109 and 109); 40 with P = 7 78 and 61 (P = 3: 78 and 77); 100 with P = 3 150
-    // and 134 (P = 1: 201 and 200).
+    if (P < 1 || B < 1 || k != Kernel::kTensorCore) return P;
+    // Prefill-shaped: two 64-token chunks per partition, one for each softmax group, or more (29
+    // queries of 9 heads, 1383 tokens: P = 10 17.6 us, P = 29 20.3).
+    if (prefill_shape(G, q_len)) return std::min(P, (tiles + 7) / 8);
+    // The step's rule fills one wave, which for batches of 20 to 150 CTAs leaves SMs idle (64
+    // CTAs on 152 SMs: P = 2), when the sequences' lengths differ waits for the longest
+    // one's partitions, and splits what is too short to gain.  In microseconds, a
+    // CTA streams a chunk (128 rows of its heads) in 0.9; P partitions take the mean of
+    //   waves part                                     sequences all of the longest length
+    //   max(part, all / 2 SMs + part / 2)              lengths spread evenly below it
+    // with part a partition's chunks, and besides
+    //   in one wave 1.2 + 0.55 rows / P + 0.05 P       to merge (the CTAs share a unit's rows)
+    //   else 4                                         to combine, and 8 per wave after the first
+    // P has the least sum, among those with a tile or more, 8 from the second wave on.
+    // 32 / 8 heads, bf16: one sequence of 512 tokens P = 32 9.7 us (16: 11.3, 4: 18.5), of 48
+    // P = 1 9.1 (2: 16.8).  FP8, sequences of 8 heads up to 4096 tokens: 64 of them with P =
+    // 7 take 113 us full and 81 us spread (P = 2: 109 and 109); 40 with P = 7 78 and 61 (P =
+    // 3: 78 and 77); 100 with P = 3 150 and 134 (P = 1: 201 and 200).
     const int qpc = queries_per_cta(G, q_len);
     const double units = static_cast<double>(units_per_split(k, B, G, Hkv, qpc, (q_len + qpc - 1) / qpc));
     int hc = 1, gp = 1;
     tc_shape(G * qpc, Hkv, &hc, &gp);
-    const double wave_cost = 8.0 / (1.05 * std::max(1, tiles * 16 * hc / 128));
+    auto stream = [&](int t) { return 0.9 * std::ceil(t * 16 * hc / 128.0); };
     auto cost = [&](int n) {
-        const double waves = std::ceil(units * n / sms);
-        return waves / n + std::max(1.0 / n, units / (2.0 * sms) + 0.5 / n) + 2.0 * wave_cost * (waves - 1.0);
+        const double part = stream((tiles + n - 1) / n), waves = std::ceil(units * n / sms);
+        const double spread = std::max(part, stream(tiles) * units / (2.0 * sms) + 0.5 * part);
+        const double join = n == 1 ? 0.0 : waves > 1.0 ? 4.0 : 1.2 + 0.55 * hc * G * qpc / n + 0.05 * n;
+        return 0.5 * (waves * part + spread) + join + 8.0 * (waves - 1.0);
     };
-    int best = P;
-    for (int n = P + 1; n <= std::min(64, tiles / 8); ++n)
-        if (cost(n) < cost(best)) best = n;
-    const int chunk = static_cast<int>(round_up((static_cast<int64_t>(tiles) * 16 + best - 1) / best, 16));
-    return (tiles * 16 + chunk - 1) / chunk;   // (no empty partition)
+    int best = 1;
+    for (int n = 2; n <= std::min(64, tiles); ++n)
+        if ((units * n <= sms || n <= tiles / 8) && cost(n) < cost(best)) best = n;
+    // No empty partition, unless they are short: an empty one's CTA still merges its share (192
+    // tokens, 28 / 4 heads: P = 8 of two tiles, two of them empty, 10.4 us, P = 6 11.7).
+    const int part = (tiles + best - 1) / best;
+    return part < 4 ? best : (tiles + part - 1) / part;
 }
 
 int check_rules(const pa_score_rules *r) {

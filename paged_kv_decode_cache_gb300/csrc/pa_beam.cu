@@ -11,11 +11,11 @@
 // no barrier.  After up to 16 chunks, what K of the threads' maxima reach bounds
 // the K-th largest value from below, and only the groups that reach it (about twice K) are
 // read again, from L2, for the values themselves.  (Taking candidates out
-// while streaming cost as much again: 62 us against 30 for 256 rows of 151937 in
-// bf16.)  The last CTA of a request to finish joins its lists.  Those 30 us are
-// the stream's 17 (4.5 TB/s: one wave of CTAs, which all start and end at once), 6 to 7
-// for the candidates, 5 to 6 for the join and 2 for the launch; 4 rows of 32000
-// take 9, a chain of latencies.
+// while streaming cost as much again: 62 us against 32 for 256 rows of 151937 in
+// bf16.)  The last CTA of a request to finish joins its lists.  Those rows now take
+// 29 us: the stream 17 (4.5 TB/s: one wave of CTAs, which all start and end at once;
+// L2 prefetches and deeper rings made it slower), 6 for the candidates, 4 for
+// the join and 2 for the launch; 4 rows of 32000 take 8.7, a chain of latencies.
 //
 // Sums: 2^(k x - k max) in fp32 with one rounding of the exponent, k = log2 e in
 // fp32, by which lse is divided in the end; fp32 sums of 8 per vector and of a
