@@ -166,6 +166,21 @@ def test_large_logits(big):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("groups,beams,vocab,K", [
+    (1, 1, 40000, 1), (3, 1, 40001, 33), (2, 16, 20000, 12), (1, 7, 70000, 9), (60, 4, 20011, 16), (1, 33, 9000, 33),
+    (2, 8, 120001, 16), (1, 64, 3000, 5), (5, 12, 150, 20), (4, 2, 1025, 64),
+])
+def test_joins_of_every_size(dtype, groups, beams, vocab, K):
+    """Lists of a join: from one to many slices per row, few and many candidates; some beams done."""
+    g = torch.Generator().manual_seed(vocab + beams)
+    logits = (torch.randn(groups * beams, vocab, generator=g) * 2).to(dtype).cuda()
+    cum = spread((groups, beams), vocab + K)
+    fin = (torch.rand(groups, beams, generator=g) < 0.2).to(torch.uint8).cuda()
+    check(run(logits, cum, K, finished=fin, eos=vocab - 1), plain(logits, cum, fin.cpu().numpy(), vocab - 1, K))
+
+
+@pytest.mark.gpu
 def test_negative_zero_ties_with_zero():
     logits = torch.tensor([[-0.0, 0.0, -1.0, -0.0]], dtype=torch.bfloat16, device="cuda")
     assert run(logits, torch.zeros(1, 1, device="cuda"), 3)[1].tolist() == [[0, 1, 3]]

@@ -217,6 +217,38 @@ def test_matches_the_formula(n, hq, hkv, d, bs, rot, layout, scaling, packed, fa
         assert torch.equal(vc.flatten(0, 1)[slots[kept].cuda()], v[kept.cuda()])
 
 
+LONG_CASES = [  # prompts: CTAs that loop over groups of tokens, a last group that is not whole
+    (768, 4, 1, 64, 16, 64, "half", "none", False, 10),
+    (771, 70, 1, 128, 16, 96, "interleaved", "none", True, 50_000),    # heads in two parts
+    (3001, 16, 8, 128, 16, 64, "interleaved", "yarn", True, 2_000_000),
+    (10007, 3, 1, 64, 32, 48, "half", "banded", True, 100_000),
+    (20010, 1, 2, 64, 16, 64, "half", "linear", False, 2**31 - 1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", LONG_CASES)
+def test_prompts_match_the_formula(case, fp8):
+    test_matches_the_formula(*case, fp8)
+
+
+@pytest.mark.gpu
+def test_prompts_in_place_with_padding_and_bad_slots():
+    q, k, v, pos, slots, nb = inputs(9001, 6, 2, 64, 16, True, 8, 9000)
+    slots[::7] = -1
+    rope = pa.pa_rope_init(64, 10000.0)
+    pools = [torch.zeros(nb, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    out = torch.empty(9001, 6, 64, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_rope_write(out, q, k, v, pos.cuda(), slots.cuda(), pools[0], pools[1], rope, status=status)
+    assert status.item() == 0
+    slots[::7] = nb * 16      # past the pools: reported, not written
+    pa.pa_rope_write(q, q, k, v, pos.cuda(), slots.cuda(), pools[2], pools[3], rope, status=status)
+    assert status.item() == pa.PA_STATUS_BAD_SLOT
+    assert torch.equal(q, out) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+
+
 @pytest.mark.gpu
 def test_in_place_and_on_another_stream():
     q, k, v, pos, slots, nb = inputs(19, 8, 2, 128, 16, True, 5, 9000)
