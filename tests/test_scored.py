@@ -316,6 +316,39 @@ def test_more_refusals_and_an_empty_batch():
     assert pa.lib().pa_decode_scored(FAKE, None, FAKE, 1, FAKE, FAKE, d, *empty) == pa.PA_OK
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("Bn", [2, 31, 32, 33])
+def test_chunks_of_many_ragged_sequences(Bn):
+    """The kernel takes up to 32 sequences from the longest; equal, empty and short ones among them."""
+    rng = random.Random(Bn)
+    lens = [rng.choice([0, 7, 40, 40, 64, 65, rng.randint(1, 500)]) for _ in range(Bn)]
+    for splits in (1, 2):
+        case(Bn, 40, 4, 2, 128, 16, lens, seed=Bn, splits=splits, softcap=30.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Bn", [1, 16])
+@pytest.mark.parametrize("L", [15, 48, 112, 192, 320, 512])
+def test_short_calls_of_every_split(L, Bn, fp8):
+    """The rule's count, and partitions of a tile each, some of them empty."""
+    for Q, Hq, Hkv in ((1, 28, 4), (4, 16, 8)):
+        for splits in (0, -(-L // 16), -(-L // 16) + 1):
+            case(Bn, Q, Hq, Hkv, 128, 16, [max(0, L - 3 * b) for b in range(Bn)], fp8=fp8, splits=splits, seed=L,
+                 softcap=30.0)
+
+
+def test_split_counts_of_short_calls():
+    for L, most in ((1, 1), (3, 1), (7, 7), (32, 32), (600, 64)):   # tiles of a table
+        for B in (1, 4, 16, 64, 1000):
+            for heads in ((28, 4), (32, 8), (16, 8), (12, 2)):
+                for q_len in (1, 4, 40):
+                    P = pa.pa_scored_num_splits(B, q_len, *heads, 128, L, 16, sm_count=152)
+                    assert 1 <= P <= most
+                    if q_len == 40 and heads[0] * q_len >= 256 * heads[1]:
+                        assert P <= -(-L // 8)
+
+
 def test_split_counts():
     """Without a window the plain rule; with one, the rule for what can be seen."""
     for args in ((8, 1, 28, 4, 128, 256, 16), (1, 1, 12, 2, 128, 100, 16), (3, 4, 28, 4, 128, 64, 256), (2, 1, 8, 2, 64, 50, 16)):
