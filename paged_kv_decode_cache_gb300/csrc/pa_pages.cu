@@ -28,7 +28,10 @@ constexpr int kCopyThreads = 256;
 constexpr int kPiece = 16 * 1024;      // bytes of a block per CTA and turn
 constexpr int kOwnTurns = 16;          // turns of a copy that a lone planning CTA makes itself
 constexpr int kNearBlocks = 2048;     // blocks whose compaction is planned by every CTA
-constexpr int kPlanWords = 4096;       // words of counts and tables per planning CTA
+constexpr int kPlanWords = 2048;       // words of counts and tables per planning CTA
+// A fork that one CTA plans in shared memory: rows, and words of counts and tables (64 rows,
+// 6700 words: 10.0 us, with a cluster of 4 11.5; 112 rows, 4900 words: 12.4 and 11.7).
+constexpr int kNearRows = 64, kNearWords = 8192;
 
 // Block-wide exclusive prefix sum over kThreads threads; *total gets the sum.  (T: two
 // counts in one 64-bit number share the shuffles and the barriers.)
@@ -636,8 +639,9 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     a.tail_first = reinterpret_cast<int32_t *>(take(4 * static_cast<size_t>(cache.num_blocks)));
     a.B_old = B_old, a.B_new = B_new, a.max_blocks = max_blocks_per_seq;
     a.num_blocks = cache.num_blocks, a.block_size = cache.block_size;
-    const int ctas = pa::plan_ctas(cache.num_blocks + static_cast<int64_t>(B_old + B_new) * max_blocks_per_seq);
-    const bool small = ctas == 1;
+    const int64_t words = cache.num_blocks + static_cast<int64_t>(B_old + B_new) * max_blocks_per_seq;
+    const bool small = words <= pa::kNearWords && std::max(B_old, B_new) <= pa::kNearRows;
+    const int ctas = small ? 1 : std::max(2, pa::plan_ctas(words));
     const int64_t turns = static_cast<int64_t>(B_new) * n_pools * pa::pieces_of(cache, elem_bytes);
     const bool own_copy = small && turns <= pa::kOwnTurns;
     pa::CopyArgs c{};
@@ -651,9 +655,8 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done[small].load(std::memory_order_acquire) & bit)) {
-        // (small: fewer than 4096 words of counts and tables, rows up to the limit)
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (7 * pa::kMaxRows + 3 * pa::kPlanWords) * 4) != cudaSuccess)
+        const int most = small ? 7 * pa::kNearRows + 3 * pa::kNearWords : 6 * pa::kMaxRows;   // words
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
             return PA_ECUDA;
         smem_attr_done[small].fetch_or(bit, std::memory_order_release);
     }
