@@ -15,7 +15,7 @@
 // bf16.)  The last CTA of a request to finish joins its lists.  Those rows now take
 // 29 us: the stream 17 (4.5 TB/s: one wave of CTAs, which all start and end at once;
 // L2 prefetches and deeper rings made it slower), 6 for the candidates, 4 for
-// the join and 2 for the launch; 4 rows of 32000 take 8.7, a chain of latencies.
+// the join and 2 for the launch; 4 rows of 32000 take 8.5, a chain of latencies.
 //
 // Sums: 2^(k x - k max) in fp32 with one rounding of the exponent, k = log2 e in
 // fp32, by which lse is divided in the end; fp32 sums of 8 per vector and of a
@@ -556,12 +556,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     }
 
     // ---- the request's last CTA joins its rows' slices
-    __threadfence();
     __syncthreads();
-    if (tid == 0) ticket = atomicAdd(a.tickets + group, 1);
+    if (tid == 0) {   // (the fences of one thread, behind and before the CTA's barriers, order all its threads' accesses)
+        __threadfence();
+        ticket = atomicAdd(a.tickets + group, 1);
+        __threadfence();
+    }
     __syncthreads();
     if (ticket != a.beams * a.slices - 1) return;
-    __threadfence();
     if (tid == 0) a.tickets[group] = 0;
     // ---- everything the slices left, in one round trip
     const int lists = a.beams * a.slices, entries = lists * K;
