@@ -41,16 +41,14 @@ struct RopeArgs {
 // threads take neighbouring chunks, so that a warp reads and writes whole lines.
 // A CTA's groups are gridDim.x apart: while one is turned, the next one's angles are
 // computed (one per thread at a time, kept in shared memory for all heads) from
-// positions read a group earlier, and a thread's loads run kAhead tokens ahead,
-// across groups.
+// positions read a group earlier, and a thread's loads run a token ahead, across
+// groups (two tokens ahead 45.3 us, four 50.8; with 1280 threads per SM 48.2, with
+// 768 49.3: 16384 tokens of 32 heads into FP8 pools).
 // Bound by a launch for a decode step (8 tokens of 36 heads: 2.3 us), by memory for
-// prompts (16384 tokens of 32 heads into bf16 pools 43 us, 0.93 of the copy rate;
-// into FP8 pools 45, 0.77: the warps that make codes take longer than the others).
+// prompts (those 16384 tokens 41.2 us, 0.85 of the copy rate, into bf16 pools 43, 0.92).
 template <bool F8, int TB, bool HALF>
 __global__ void __launch_bounds__(kMaxThreads, 2)
 rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
-    constexpr int kAhead = TB < 2 ? 1 : 2;
-    static_assert(TB % kAhead == 0, "a token's registers are known at compile time");
     __shared__ __align__(16) float2 turn[2][TB][PA_ROPE_MAX_PAIRS];  // (cos, sin) of the pairs: this group's, the next one's
     __shared__ int32_t pos_s[2][TB];                             // positions of the next two groups
     __shared__ int64_t row_s[3][TB];                             // rows in the pools, in elements (-1: not written)
@@ -70,12 +68,12 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
     const int at_head = (head - (is_q ? 0 : is_v ? a.hq + a.hkv : a.hq)) * a.head_dim + e0;
     const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
     const __nv_bfloat16 *src = (is_q ? a.q : is_v ? a.v : a.k) + at_head;
-    uint4 lo[kAhead], hi[kAhead];
-    auto load = [&](int b, int64_t tok) {
-        lo[b] = hi[b] = make_uint4(0u, 0u, 0u, 0u);
+    uint4 lo, hi;
+    auto load = [&](int64_t tok) {
+        lo = hi = make_uint4(0u, 0u, 0u, 0u);
         if (tok < a.n && x < total) {
-            lo[b] = *reinterpret_cast<const uint4 *>(src + tok * stride);
-            hi[b] = *reinterpret_cast<const uint4 *>(src + tok * stride + apart);
+            lo = *reinterpret_cast<const uint4 *>(src + tok * stride);
+            hi = *reinterpret_cast<const uint4 *>(src + tok * stride + apart);
         }
     };
     auto row_of = [&](int64_t tok) -> int64_t {
@@ -95,8 +93,7 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
     auto tokens_from = [&](int64_t tok) { return static_cast<int>(min(static_cast<int64_t>(TB), a.n - tok)); };
 
     int64_t tok0 = static_cast<int64_t>(blockIdx.x) * TB;
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b) load(b, tok0 + b);
+    load(tok0);
     angles(0, tokens_from(tok0), [&](int at) { return a.positions[tok0 + at]; });
     if (tid < TB && tok0 + tid < a.n) row_s[0][tid] = row_of(tok0 + tid);
     if (tid < TB && tok0 + step + tid < a.n) {
@@ -113,14 +110,14 @@ rope_write_kernel(const RopeArgs a, const __grid_constant__ pa_rope rope) {
         const int tokens = tokens_from(tok0);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
-            const uint4 mine_lo = lo[t % kAhead], mine_hi = hi[t % kAhead];
+            const uint4 now_lo = lo, now_hi = hi;
             // (in place too: another token than the one written below)
-            if (TB > 1) load(t % kAhead, t + kAhead < TB ? tok0 + t + kAhead : tok0 + step + t + kAhead - TB);
+            if (TB > 1) load(t + 1 < TB ? tok0 + t + 1 : tok0 + step);
             if (t >= tokens || x >= total) continue;
             const int64_t row = row_s[row3][t];
             if (!is_q && row < 0) continue;
-            const uint32_t w0[4] = {mine_lo.x, mine_lo.y, mine_lo.z, mine_lo.w};
-            const uint32_t w1[4] = {mine_hi.x, mine_hi.y, mine_hi.z, mine_hi.w};
+            const uint32_t w0[4] = {now_lo.x, now_lo.y, now_lo.z, now_lo.w};
+            const uint32_t w1[4] = {now_hi.x, now_hi.y, now_hi.z, now_hi.w};
             float f0[8], f1[8];  // the two chunks' values
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -174,8 +171,7 @@ float reciprocal(float scale) { return scale > 0x1p-60f && scale < 0x1p60f ? 1.f
 
 // Tokens per group: one, and a CTA for each, where there are few (600 tokens of 32 heads
 // into FP8 pools: 3.4 us, with four 4.3); else four (1536 tokens of 36 heads: 6.3 us,
-// with one 8.9; 16384 of 32 into FP8 pools: 45.1, into bf16 43), and as
-// many CTAs as the GPU holds at once.
+// with one 8.9), and as many CTAs as the GPU holds at once.
 constexpr int kFourFrom = 768;
 
 template <bool F8, int TB>
