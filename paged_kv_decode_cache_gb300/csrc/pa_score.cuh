@@ -50,38 +50,48 @@ __device__ __forceinline__ Seen seen_by(const DecodeParams &p, int b, int L, int
 
 // c tanh(x / c) in log2 units: x and cap are times log2(e), inv_cap = 1 / cap.
 // With u = x / cap below 0.625, x (1 + u^2 p(u^2)) with a least-squares fit of
-// tanh(u) / u weighted towards its largest error: 6e-8 of the value in fp32.  Most
-// scores are small next to the cap, and a warp whose scores all are stops there (9
-// operations, two scores each); otherwise all take 1 - 2 / (e^2u + 1), whose
-// error is 2^-22 of the cap.
+// tanh(u) / u weighted towards its largest error: 6e-8 of the value in fp32.  From
+// there on 1 - 2 / (e^2u + 1), whose error is 2^-22 of the cap.  Each score takes the
+// form of its own size, so that its bits depend on it alone: a warp also holds rows
+// that no query sees, which may be anything.  The warp's vote only skips the second
+// form where no lane needs it (most scores are small next to the cap; 9 operations,
+// two scores each).
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], float inv_cap, float cap) {
     bool big = false;
     const float edge = 0.625f * cap;
+    const uint64_t ic = pack2(inv_cap, inv_cap);
+    auto near = [&](float x0, float x1, float &a, float &b) {
+        const uint64_t v = pack2(x0, x1), u = mul2(v, ic), t = mul2(u, u);
+        uint64_t p = fma2(t, pack2(-0x1.72ef1ep-8f, -0x1.72ef1ep-8f), pack2(0x1.515ceep-6f, 0x1.515ceep-6f));
+        p = fma2(t, p, pack2(-0x1.b81542p-5f, -0x1.b81542p-5f));
+        p = fma2(t, p, pack2(0x1.11058p-3f, 0x1.11058p-3f));
+        p = fma2(t, p, pack2(-0x1.555524p-2f, -0x1.555524p-2f));
+        unpack2(fma2(mul2(v, t), p, v), a, b);
+    };
 #pragma unroll
     for (int i = 0; i < N; ++i) big |= !(fabsf(x[i]) < edge);
     if (!__any_sync(0xffffffffu, big)) {
-        const uint64_t ic = pack2(inv_cap, inv_cap);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const uint64_t v = pack2(x[i], x[i + 1 < N ? i + 1 : i]);
-            const uint64_t u = mul2(v, ic), t = mul2(u, u);
-            uint64_t p = fma2(t, pack2(-0x1.72ef1ep-8f, -0x1.72ef1ep-8f), pack2(0x1.515ceep-6f, 0x1.515ceep-6f));
-            p = fma2(t, p, pack2(-0x1.b81542p-5f, -0x1.b81542p-5f));
-            p = fma2(t, p, pack2(0x1.11058p-3f, 0x1.11058p-3f));
-            p = fma2(t, p, pack2(-0x1.555524p-2f, -0x1.555524p-2f));
             float a, b;
-            unpack2(fma2(mul2(v, t), p, v), a, b);
+            near(x[i], x[i + 1 < N ? i + 1 : i], a, b);
             x[i] = a;
             if (i + 1 < N) x[i + 1] = b;
         }
         return;
     }
     const float k = 2.8853900817779268f * inv_cap;  // e^2u = 2^(k x)
+    auto pick = [&](float v, float small) {
+        const float far = fmaf(-cap, __fdividef(2.f, fast_exp2(fabsf(v) * k) + 1.f), cap);
+        return fabsf(v) < edge ? small : copysignf(far, v);
+    };
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float far = fmaf(-cap, __fdividef(2.f, fast_exp2(fabsf(x[i]) * k) + 1.f), cap);
-        x[i] = copysignf(far, x[i]);
+    for (int i = 0; i < N; i += 2) {
+        float a, b;
+        near(x[i], x[i + 1 < N ? i + 1 : i], a, b);
+        x[i] = pick(x[i], a);
+        if (i + 1 < N) x[i + 1] = pick(x[i + 1], b);
     }
 }
 
