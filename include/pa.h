@@ -659,8 +659,8 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
  * Beam search's selection: for every request (group) the K best continuations
  * over its beams and the vocabulary,
  *   score(w, v) = cum[w] + (x[w, v] - ln sum_u exp x[w, u]),
- * best first, ties to the lowest w * vocab + v, compared in 64 bits.  One launch,
- * one pass over the logits.
+ * best first, ties to the lowest w * vocab + v, compared in 64 bits.  One launch
+ * (per 4096 groups), one pass over the logits.
  * logits: device, row r = group * beams + w at r * row_stride elements, bf16
  * (PA_LOGITS_BF16) or fp32 (PA_LOGITS_F32), 16-byte aligned base, row_stride >= vocab
  * (rows need no alignment of their own).  -inf excludes an entry; a NaN or +inf
@@ -673,8 +673,9 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
  * entries have a score above -inf, the rest are (-inf, -1, -1).
  * beams <= 64, K <= 64, beams * vocab < 2^30.  workspace: device,
  * pa_beam_workspace_bytes(...) bytes, 256-byte aligned, zero-filled before its
- * first use and left ready for the next call (not by calls that overlap on the
- * GPU).  groups == 0 is a no-op.
+ * first use and left ready for the next call, of the same shape or of any other that
+ * it is large enough for (not by calls that overlap on the GPU).  groups == 0 is a
+ * no-op.
  */
 enum { PA_LOGITS_BF16 = 0, PA_LOGITS_F32 = 1 };
 int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void *logits,
@@ -683,7 +684,7 @@ int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void 
                    int32_t vocab, int32_t K, void *workspace, size_t workspace_bytes,
                    pa_stream_t stream);
 
-/* Workspace bytes of pa_beam_select (0 on bad arguments). */
+/* Workspace bytes of pa_beam_select (0 on bad arguments), enough for fewer groups too. */
 size_t pa_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t K,
                                int32_t logits_type);
 

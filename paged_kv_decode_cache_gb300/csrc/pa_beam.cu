@@ -52,6 +52,9 @@ constexpr float kSlack = 4.76837158e-7f;      // 2^-21
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPool = 2 * kThreads;            // candidates of a slice at a time
 constexpr int kWaveCtas = 4 * 152;            // slices: one wave of 4 CTAs per SM
+// Requests of one launch, and tickets at the workspace's start: their place is the same
+// for every shape, so no call's lists ever lie where another's tickets are.
+constexpr int kMaxTickets = 4096;
 
 template <int N>
 struct Int {
@@ -139,7 +142,8 @@ struct BeamArgs {
     const uint8_t *finished;
     int32_t eos;
     int beams, vocab, K, slices;
-    int32_t *tickets;      // [groups], zero between calls
+    int32_t row0;          // this launch's first row of the call
+    int32_t *tickets;      // [kMaxTickets], zero between calls
     float *part_max;       // [rows, slices] times k
     double *part_sum;      // [rows, slices]
     uint64_t *part_list;   // [rows, slices, K] candidates
@@ -655,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         if (i < n && place < K && (tid & ((1 << t) - 1)) == 0) {
             a.scores[out + place] = static_cast<float>(key_value(k));
             a.tokens[out + place] = at % a.vocab;
-            a.parents[out + place] = first_row + at / a.vocab;
+            a.parents[out + place] = a.row0 + first_row + at / a.vocab;
         }
     }
     for (int i = n + tid; i < K; i += kThreads) {  // fewer candidates than K
@@ -701,9 +705,11 @@ size_t pa_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int
     if (!pa::shape_ok(groups, beams, vocab, K) || !pa::shape_supported(groups, beams, vocab, K) ||
         !pa::elem_size(logits_type) || groups == 0)
         return 0;
-    const int64_t rows = static_cast<int64_t>(groups) * beams;
-    const size_t parts = static_cast<size_t>(rows) * pa::slices_of(rows, beams, vocab, K, pa::elem_size(logits_type));
-    return pa::up(4 * static_cast<size_t>(groups)) + pa::up(4 * parts) + pa::up(8 * parts) + pa::up(8 * parts * K);
+    const int64_t rows = static_cast<int64_t>(std::min<int32_t>(groups, pa::kMaxTickets)) * beams;
+    // (fewer rows are cut into more slices: enough for them too)
+    const int64_t most = rows * pa::slices_of(beams, beams, vocab, K, pa::elem_size(logits_type));
+    const size_t parts = std::max(rows, std::min<int64_t>(most, pa::kWaveCtas));
+    return 4 * pa::kMaxTickets + pa::up(4 * parts) + pa::up(8 * parts) + pa::up(8 * parts * K);
 }
 
 int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void *logits, int32_t logits_type,
@@ -721,16 +727,15 @@ int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void 
     if (!workspace || workspace_bytes < pa_beam_workspace_bytes(groups, beams, vocab, K, logits_type) ||
         !pa::is_aligned(workspace, 256))
         return PA_EWORKSPACE;
-    const int64_t rows = static_cast<int64_t>(groups) * beams;
+    const int64_t rows = static_cast<int64_t>(std::min<int32_t>(groups, pa::kMaxTickets)) * beams;  // of a launch
     pa::BeamArgs a{};
-    a.scores = scores, a.tokens = tokens, a.parents = parents;
-    a.logits = logits, a.row_stride = row_stride, a.cum = cum, a.finished = finished, a.eos = eos;
+    a.row_stride = row_stride, a.eos = eos;
     a.beams = beams, a.vocab = vocab, a.K = K;
     a.slices = pa::slices_of(rows, beams, vocab, K, pa::elem_size(logits_type));
     const size_t parts = static_cast<size_t>(rows) * a.slices;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.tickets = reinterpret_cast<int32_t *>(ws);
-    ws += pa::up(4 * static_cast<size_t>(groups));
+    ws += 4 * pa::kMaxTickets;
     a.part_max = reinterpret_cast<float *>(ws);
     ws += pa::up(4 * parts);
     a.part_sum = reinterpret_cast<double *>(ws);
@@ -747,9 +752,20 @@ int pa_beam_select(float *scores, int32_t *tokens, int32_t *parents, const void 
             return PA_ECUDA;
         smem_attr_done[logits_type].fetch_or(bit, std::memory_order_release);
     }
-    const cudaError_t e = pa::launch_maybe_cooperative(kern, dim3(static_cast<unsigned>(parts)), pa::kThreads, smem,
-                                                       stream, false, pa::pdl_on(), a);
-    return e == cudaSuccess ? PA_OK : PA_ECUDA;
+    for (int32_t g0 = 0; g0 < groups; g0 += pa::kMaxTickets) {
+        const int64_t r0 = static_cast<int64_t>(g0) * beams, n = std::min(groups - g0, pa::kMaxTickets);
+        a.row0 = static_cast<int32_t>(r0);
+        a.scores = scores + static_cast<int64_t>(g0) * K;
+        a.tokens = tokens + static_cast<int64_t>(g0) * K;
+        a.parents = parents + static_cast<int64_t>(g0) * K;
+        a.logits = static_cast<const uint8_t *>(logits) + r0 * row_stride * pa::elem_size(logits_type);
+        a.cum = cum + r0;
+        a.finished = finished ? finished + r0 : nullptr;
+        if (pa::launch_maybe_cooperative(kern, dim3(static_cast<unsigned>(n * beams * a.slices)), pa::kThreads, smem, stream,
+                                         false, pa::pdl_on(), a) != cudaSuccess)
+            return PA_ECUDA;
+    }
+    return PA_OK;
 }
 
 }  // extern "C"
