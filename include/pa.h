@@ -206,9 +206,10 @@ int pa_partition_tokens(int32_t max_blocks_per_seq, int32_t block_size, int32_t 
 
 /*
  * Bytes of workspace pa_decode_splitkv needs: fp32 partial outputs
- * [B, Hq, P, D], fp32 partial LSEs [B, Hq, P] and two int32 merge counters
- * per (sequence, head group) (at most 2 * B * Hq), each region 256-byte
- * aligned.
+ * [B, Hq, P, D], fp32 partial LSEs [B, Hq, P] and 1024 int32 merge counters,
+ * each region 256-byte aligned.  The counters are the last 4096 bytes of the
+ * workspace that a call is given (workspace_bytes rounded down to 256),
+ * whatever the shape.
  * 0 when num_splits <= 1.
  */
 size_t pa_splitkv_workspace_bytes(int32_t B, int32_t Hq, int32_t D, int32_t num_splits);
@@ -262,8 +263,9 @@ int pa_combine(void *out, float *lse, const float *part_o, const float *part_lse
  * pa_splitkv_workspace_bytes(B, Hq, D, P) bytes, 256-byte aligned, else
  * PA_EWORKSPACE.  It must be zero-filled before its first use (cudaMemset):
  * the merge counters in it start at zero and every completed call leaves
- * them at zero again, so a workspace can be reused call after call (not by
- * calls that overlap on the GPU).  A call that reported PA_STATUS_TIMEOUT
+ * them at zero again, so a workspace can be reused call after call, by calls of
+ * any shape, num_splits and entry point that it is large enough for, each given
+ * the same workspace_bytes (not by calls that overlap on the GPU).  A call that reported PA_STATUS_TIMEOUT
  * may leave them non-zero: zero the workspace again before reusing it.
  * Results equal pa_decode's up to fp32 rounding order.
  */

@@ -337,6 +337,18 @@ int scored_positions(int G, int q_len) {
     return prefill_shape(G, q_len) ? std::min(q_len, prefill_positions_per_tile(G)) : queries_per_cta(G, q_len);
 }
 
+// A split call's workspace: partial outputs, partial LSEs and, at its very end, the
+// merge counters, one per (sequence, head group) of a launch that merges in place (at
+// most half as many as CTAs fit on the GPU at once).  Their place depends on the
+// buffer's size alone, not on the shape or P, so that calls of different ones (layers
+// with different windows, batches that grow and shrink) can share a workspace: no
+// call's partials ever lie where another's counters are.
+constexpr int kMergeCounters = 1024;
+constexpr int64_t kCounterBytes = kMergeCounters * 4;
+int32_t *counters_of(void *workspace, size_t bytes) {
+    return reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + bytes / 256 * 256 - kCounterBytes);
+}
+
 // Query positions per tensor-core CTA for q_len queries of G heads each: as
 // many as fit the kernel's column limit (G * positions <= 32).
 int queries_per_cta(int G, int q_len) {
@@ -636,8 +648,7 @@ int pa_auto_num_splits(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t ma
 size_t pa_splitkv_workspace_bytes(int32_t B, int32_t Hq, int32_t D, int32_t num_splits) {
     if (B <= 0 || Hq <= 0 || D <= 0 || num_splits <= 1) return 0;
     const int64_t rows = static_cast<int64_t>(B) * Hq * num_splits;
-    return static_cast<size_t>(round_up(rows * D * 4, 256) + round_up(rows * 4, 256) +
-                               round_up(static_cast<int64_t>(B) * Hq * 8, 256));
+    return static_cast<size_t>(round_up(rows * D * 4, 256) + round_up(rows * 4, 256) + kCounterBytes);
 }
 
 int pa_decode_partial(float *part_o, float *part_lse, const void *q, const void *k_cache,
@@ -748,7 +759,7 @@ bool merge_in_launch(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t 
     if (pick_kernel(G * qpc, D, &k)) return false;
     if (k == Kernel::kTensorCore && prefill_shape(G, q_len)) return false;
     const int64_t units = units_per_split(k, B, G, Hkv, qpc, (q_len + qpc - 1) / qpc);
-    return units * P <= static_cast<int64_t>(sm_count) * ctas_per_sm(k);
+    return units * P <= static_cast<int64_t>(sm_count) * ctas_per_sm(k) && units <= kMergeCounters;
 }
 
 // Split-KV decode shared by pa_decode_splitkv, pa_decode_step, pa_decode_mq,
@@ -798,14 +809,12 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *part_o = reinterpret_cast<float *>(ws);
     float *part_lse = reinterpret_cast<float *>(ws + round_up(rows * cache.head_dim * 4, 256));
-    int32_t *counters = reinterpret_cast<int32_t *>(ws + round_up(rows * cache.head_dim * 4, 256) +
-                                                    round_up(rows * 4, 256));
+    int32_t *counters = counters_of(workspace, workspace_bytes);
     // One cooperative launch that merges its own partials when the whole grid
     // fits on the GPU at once and its merge tasks can hold every partition;
     // otherwise partials, then pa_combine.
     if (merge_in_launch(B, q_len, Hq, cache.num_kv_heads, cache.head_dim, P, sm_count_current())) {
-        if (library_scratch &&
-            cudaMemsetAsync(counters, 0, static_cast<size_t>(Bq) * Hq * 8, stream) != cudaSuccess)
+        if (library_scratch && cudaMemsetAsync(counters, 0, kCounterBytes, stream) != cudaSuccess)
             return PA_ECUDA;
         rc = run_decode(true, out, lse, part_o, part_lse, q, k_cache, v_cache, cache, block_tables,
                         max_blocks_per_seq, seq_lens, B, Hq, scale, P, status, stream, counters, nt,
@@ -1080,8 +1089,7 @@ int pa_decode_cascade(void *out, float *lse, const void *q, const void *k_cache,
     suf.part_offset = P1;
     suf.table_stride = max_blocks_per_seq;
     if (cascade_suffix_merges(B, Hq, cache.num_kv_heads, cache.head_dim, P1, P2, sm_count_current())) {
-        int32_t *counters = reinterpret_cast<int32_t *>(
-            ws + round_up(rows * PT * cache.head_dim * 4, 256) + round_up(rows * PT * 4, 256));
+        int32_t *counters = counters_of(workspace, workspace_bytes);
         rc = run_decode(true, out, lse, part_o, part_lse, q, k_cache, v_cache, cache,
                         block_tables + n_prefix_blocks, max_blocks_per_seq - n_prefix_blocks,
                         seq_lens, B, Hq, scale, P2, status, stream, counters, NewTokens(), 1,

@@ -253,7 +253,7 @@ __device__ void merge_split_group(const DecodeParams &p, int group, int part, in
                                   Sync sync, float *scratch = nullptr) {
     auto row_of = [&](int j) -> int64_t { return row_first + (j / per_block) * stride + j % per_block; };
     if (!p.counters) return;
-    int *arrive = p.counters + 2 * group;  // (the pair's second int is not used)
+    int *arrive = p.counters + group;
     const int P = p.num_splits;
     // Release: the barrier orders every thread's partial stores before thread
     // 0's gpu-scope release fence, which makes them visible before its arrival.
