@@ -604,16 +604,22 @@ int pa_rope_write_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t 
  *     is a new row's partial last block and no row before it has the same one;
  *     else its last block's L % bs token rows are copied, in every pool, into a
  *     free block that takes its place;
- *   - L is a multiple of the block size: it gets a free block (when L fills its
- *     table: none, and PA_STATUS_BAD_SEQLEN).
+ *   - L is a multiple of the block size: it gets a free block, which stands at
+ *     entry L / bs of its new table (when L fills its table: none, and
+ *     PA_STATUS_BAD_SEQLEN).  Until the token is written that block is the row's own:
+ *     a later call finds it there, by its count above 0, and treats it like a
+ *     partial last block without rows (kept, replaced for a row that would share
+ *     it, given back with the row).  So that entry of `tables` is such a block, or
+ *     -1, or names a free block; entries after it are not read.
  * Free blocks are those with no reference left, given out lowest id first in
- * row order; when they run out the row keeps sharing its last block,
+ * row order; when they run out the row keeps sharing its block,
  * its slot is -1 and PA_STATUS_NO_BLOCKS is set.
  * new_tables: device int32 [B_new, max_blocks_per_seq], -1 past the row's
  * blocks; new_lens: device int32 [B_new] (the parents' lengths: the caller adds
  * the token it writes); new_refs: device int32 [num_blocks]; slot_mapping:
  * device int64 [B_new], the slot of position L, -1 for none.
- * tables, lens: device int32 [B_old, max_blocks_per_seq], [B_old]; refs:
+ * tables, lens: device int32 [B_old, max_blocks_per_seq], [B_old], the lengths with
+ * every token that has been written, this step's among them; refs:
  * device int32 [num_blocks].  B_old, B_new <= 4096.
  * A table entry outside the pool sets PA_STATUS_BAD_BLOCK and becomes -1; a
  * parent >= B_old sets PA_STATUS_BAD_PARENT and counts as negative.

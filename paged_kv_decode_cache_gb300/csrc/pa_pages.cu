@@ -147,7 +147,7 @@ struct ForkArgs {
     int32_t *status;
     CopyList *list;
     int32_t *free_list;   // [B_new] the lowest free ids
-    int32_t *tail_count;  // [num_blocks] new rows whose partial last block it is
+    int32_t *tail_count;  // [num_blocks] new rows whose next token goes into it
     int32_t *tail_first;  // [num_blocks] the first of them
     int B_old, B_new, max_blocks, num_blocks, block_size;
 };
@@ -156,6 +156,14 @@ __device__ __forceinline__ int checked_len(int L, int lmax, int32_t *status) {
     if (L >= 0 && L <= lmax) return L;
     set_status(status, PA_STATUS_BAD_SEQLEN);
     return L < 0 ? 0 : lmax;
+}
+
+// The block that a row of length L (checked, below the table's tokens) has for its next
+// token, `entry` being its table's entry L / bs: its partial last block, or the one that
+// a fork gave it and that no token has gone into yet, which is in use; else -1.
+__device__ __forceinline__ int next_block(int entry, int L, int bs, const int32_t *refs, int num_blocks) {
+    if (entry < 0 || entry >= num_blocks) return -1;
+    return L % bs || refs[entry] > 0 ? entry : -1;
 }
 
 // The number of free ids a thread's segment [lo, hi) of the counts holds.
@@ -182,10 +190,10 @@ __device__ __forceinline__ void for_entries(const int32_t *row, int n, int lane,
 // Row i of the new state is row parents[i] of the old one, sharing its blocks.
 // An old row with c children changes every count of its blocks by c - 1, so
 // rows with one child (most of them) touch no count.  Then the block of the
-// next token, position L: a row keeps its partial last block when every
-// reference to it is some new row's last block and this is the first such
-// row; any other row copies it to a free block; a row that ends with a full
-// block takes a free one.
+// next token, position L: its partial last block, or the empty one that an earlier
+// fork gave it.  A row keeps it when every reference to it is some new row's block
+// for the next token and this is the first such row; any other row takes a free block
+// in its place and copies its rows, if any; so does a row that ends with a full block.
 // kSmall: one CTA, which keeps the counts and lists in shared memory, so that only the
 // first loads, the tables and the copies themselves wait for memory (4 beams of a
 // request: 9.7 -> 6.0 us).  `copy.list`: the plan's, for a copy so small that this CTA makes
@@ -196,11 +204,12 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     extern __shared__ int32_t smem[];
     int32_t *row_parent = smem;                     // [B_new], -1: no sequence
     int32_t *row_len = row_parent + a.B_new;        // [B_new]
-    int32_t *row_tail = row_len + a.B_new;          // [B_new] partial last block, -1: none, or outside the pool
+    int32_t *row_tail = row_len + a.B_new;          // [B_new] the block for its next token (next_block)
     int32_t *row_rank = row_tail + a.B_new;         // [B_new] needs a block: which one; else -1
     int32_t *children = row_rank + a.B_new;         // [B_old]
     int32_t *old_len = children + a.B_old;          // [B_old]
-    int32_t *near = old_len + a.B_old;              // kSmall: the arrays below
+    int32_t *old_tail = old_len + a.B_old;          // [B_old]
+    int32_t *near = old_tail + a.B_old;             // kSmall: the arrays below
     int32_t *refs = kSmall ? near : a.new_refs;                            // [num_blocks]
     int32_t *tail_count = kSmall ? near + a.num_blocks : a.tail_count;      // [num_blocks]
     int32_t *tail_first = kSmall ? near + 2 * a.num_blocks : a.tail_first;  // [num_blocks]
@@ -220,13 +229,18 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     const int bs = a.block_size, mb = a.max_blocks, lmax = mb * bs;
 
     // ---- the rows' parents and lengths (every CTA for itself), the counts copied
+    // (each thread's first loads are asked for at once, before the one that waits for a length)
+    const int len0 = tid < a.B_old ? a.lens[tid] : 0, parent0 = tid < a.B_new ? a.parents[tid] : -1;
+    const int refs0 = gid < a.num_blocks ? a.refs[gid] : 0;
     for (int j = tid; j < a.B_old; j += kPlanThreads) {
+        const int L = checked_len(j == tid ? len0 : a.lens[j], lmax, a.status);
         children[j] = 0;
-        old_len[j] = checked_len(a.lens[j], lmax, a.status);
+        old_len[j] = L;
+        old_tail[j] = L < lmax ? next_block(a.tables[static_cast<int64_t>(j) * mb + L / bs], L, bs, a.refs, a.num_blocks) : -1;
     }
-    for (int i = tid; i < a.B_new; i += kPlanThreads) row_parent[i] = a.parents[i];
+    for (int i = tid; i < a.B_new; i += kPlanThreads) row_parent[i] = i == tid ? parent0 : a.parents[i];
     for (int i = gid; i < a.num_blocks; i += gthreads) {
-        refs[i] = a.refs[i];
+        refs[i] = i == gid ? refs0 : a.refs[i];
         if (kSmall) tail_count[i] = 0, tail_first[i] = INT32_MAX;
     }
     __syncthreads();
@@ -238,28 +252,28 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
         }
         if (p >= 0) {
             L = old_len[p];
+            t = old_tail[p];
             atomicAdd(children + p, 1);
-            if (L % bs) t = a.tables[static_cast<int64_t>(p) * mb + L / bs];
-            if (t >= a.num_blocks) t = -1;
             if (!kSmall && cta == 0 && t >= 0) tail_count[t] = 0, tail_first[t] = INT32_MAX;
         }
         row_parent[i] = p < 0 ? -1 : p;
         row_len[i] = L;
-        row_tail[i] = t < 0 ? -1 : t;
+        row_tail[i] = t;
     }
     everyone();
 
     // ---- references dropped and added; tables copied (a warp per row)
+    auto blocks = [&](int L, int tail) { return L / bs + (L % bs || tail >= 0); };
     for (int j = gid >> 5; j < a.B_old; j += gthreads >> 5) {
         const int change = children[j] - 1;
         if (change == 0) continue;
-        for_entries(a.tables + static_cast<int64_t>(j) * mb, (old_len[j] + bs - 1) / bs, lane, [&](int, int id) {
+        for_entries(a.tables + static_cast<int64_t>(j) * mb, blocks(old_len[j], old_tail[j]), lane, [&](int, int id) {
             if (id >= 0 && id < a.num_blocks) atomicAdd(refs + id, change);
             else set_status(a.status, PA_STATUS_BAD_BLOCK);
         });
     }
     for (int i = gid >> 5; i < a.B_new; i += gthreads >> 5) {
-        const int p = row_parent[i], nb = (row_len[i] + bs - 1) / bs;
+        const int p = row_parent[i], nb = blocks(row_len[i], row_tail[i]);
         int32_t *row = a.new_tables + static_cast<int64_t>(i) * mb;
         if (lane == 0 && row_tail[i] >= 0) {
             atomicAdd(tail_count + row_tail[i], 1);
@@ -289,11 +303,10 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     uint64_t zero = 0;                  // the segment's first 64 ids: free or not
     for (int i = i0; i < i1; ++i) {
         const int L = row_len[i], t = row_tail[i];
-        const bool part = row_parent[i] >= 0 && L % bs != 0 && t >= 0;
-        const int makers = part ? get(tail_count + t) : 0, all = part ? get(refs + t) : 0;
-        const int first = part ? get(tail_first + t) : 0;
-        int need = row_parent[i] >= 0 && L % bs == 0 && L < lmax;
-        if (part && !(makers == all && first == i)) need = 1 | 1 << 16;
+        const int makers = t >= 0 ? get(tail_count + t) : 0, all = t >= 0 ? get(refs + t) : 0;
+        const int first = t >= 0 ? get(tail_first + t) : 0;
+        int need = row_parent[i] >= 0 && L % bs == 0 && L < lmax && t < 0;
+        if (t >= 0 && !(makers == all && first == i)) need = L % bs ? 1 | 1 << 16 : 1;
         row_rank[i] = need;
         mine += need;
     }
@@ -346,7 +359,7 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
                 id = get(free_list + rank);
                 a.new_tables[static_cast<int64_t>(i) * mb + e] = id;
                 refs[id] = 1;
-                if (off) atomicSub(refs + tail, 1);
+                if (tail >= 0) atomicSub(refs + tail, 1);
                 slot = static_cast<int64_t>(id) * bs + off;
             } else {
                 set_status(a.status, PA_STATUS_NO_BLOCKS);
@@ -354,7 +367,7 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
             if (off) entries[row_rank[i] >> 16] = make_int4(id < 0 ? -1 : tail, id, off, 0);
         } else if (row_parent[i] >= 0) {
             if (tail >= 0) slot = static_cast<int64_t>(tail) * bs + off;
-            else if (!off) set_status(a.status, PA_STATUS_BAD_SEQLEN);  // the table is full
+            else if (L == lmax) set_status(a.status, PA_STATUS_BAD_SEQLEN);  // the table is full
         }
         a.slots[i] = slot;
         a.new_lens[i] = L;
@@ -647,7 +660,7 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     pa::CopyArgs c{};
     pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.list = own_copy ? a.list : nullptr;
-    int smem = (4 * B_new + 2 * B_old) * 4;
+    int smem = (4 * B_new + 3 * B_old) * 4;
     if (small) smem += (3 * cache.num_blocks + B_new) * 4;
     auto kern = small ? pa::fork_plan_kernel<true> : pa::fork_plan_kernel<false>;
     static std::atomic<uint64_t> smem_attr_done[2];
@@ -655,7 +668,7 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done[small].load(std::memory_order_acquire) & bit)) {
-        const int most = small ? 7 * pa::kNearRows + 3 * pa::kNearWords : 6 * pa::kMaxRows;   // words
+        const int most = small ? 8 * pa::kNearRows + 3 * pa::kNearWords : 7 * pa::kMaxRows;   // words
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
             return PA_ECUDA;
         smem_attr_done[small].fetch_or(bit, std::memory_order_release);
