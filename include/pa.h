@@ -641,8 +641,11 @@ size_t pa_fork_workspace_bytes(int32_t B_old, int32_t B_new, int32_t num_blocks)
  * block (for holders other than the tables); new_refs: device int32
  * [num_blocks], the counts at their new ids, 0 from n on; new_tables: device
  * int32 [B, max_blocks_per_seq], the tables' entries remapped, -1 past each
- * row's blocks; n_live: device int32, n.  A used entry that names a free block
- * or lies outside the pool becomes -1 and sets PA_STATUS_BAD_BLOCK.  The moved blocks'
+ * row's blocks; n_live: device int32, n.  A row's blocks are those of its tokens
+ * and, where its length L is a multiple of the block size, the block in use that
+ * entry L / bs names, if it does: a fork gave it for the next token.  A used entry
+ * that names a free block or lies outside the pool becomes -1 and sets
+ * PA_STATUS_BAD_BLOCK.  The moved blocks'
  * old places keep their contents and are free.
  */
 int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live,
@@ -650,6 +653,20 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
                       int32_t max_blocks_per_seq, void *const *pools, int32_t n_pools,
                       int32_t elem_bytes, pa_cache_desc cache, void *workspace,
                       size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/*
+ * pa_blocks_compact that also moves the next tokens' slots: slots, device int64 [B]
+ * (as pa_sequences_fork gave them, negative: none), become new_slots, device int64
+ * [B].  Needed where a fork's slots are still to be written; a slot in a block that is
+ * free or outside the pool becomes -1 and sets PA_STATUS_BAD_SLOT.  Both NULL:
+ * pa_blocks_compact.
+ */
+int pa_blocks_compact_slots(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live,
+                            int64_t *new_slots, const int32_t *tables, const int32_t *lens,
+                            const int32_t *refs, const int64_t *slots, int32_t B,
+                            int32_t max_blocks_per_seq, void *const *pools, int32_t n_pools,
+                            int32_t elem_bytes, pa_cache_desc cache, void *workspace,
+                            size_t workspace_bytes, int32_t *status, pa_stream_t stream);
 
 /* Workspace bytes of pa_blocks_compact (0 on bad arguments). */
 size_t pa_compact_workspace_bytes(int32_t num_blocks);

@@ -32,7 +32,7 @@ struct Library {
     decltype(&::pa_decode_scored_fp8) decode_scored_fp8;
     decltype(&::pa_beam_select) beam_select;
     decltype(&::pa_sequences_fork) sequences_fork;
-    decltype(&::pa_blocks_compact) blocks_compact;
+    decltype(&::pa_blocks_compact_slots) blocks_compact_slots;
     decltype(&::pa_blocks_copy) blocks_copy;
     decltype(&::pa_strerror) strerror;
 } g_lib;
@@ -55,7 +55,7 @@ PyObject *init(PyObject *, PyObject *args) {
         !find(h, "pa_decode_scored", &g_lib.decode_scored) ||
         !find(h, "pa_decode_scored_fp8", &g_lib.decode_scored_fp8) ||
         !find(h, "pa_beam_select", &g_lib.beam_select) || !find(h, "pa_sequences_fork", &g_lib.sequences_fork) ||
-        !find(h, "pa_blocks_compact", &g_lib.blocks_compact) || !find(h, "pa_blocks_copy", &g_lib.blocks_copy) ||
+        !find(h, "pa_blocks_compact_slots", &g_lib.blocks_compact_slots) || !find(h, "pa_blocks_copy", &g_lib.blocks_copy) ||
         !find(h, "pa_strerror", &g_lib.strerror))
         return nullptr;
     for (PyObject *o : {error, raw_stream, current_device, set_device}) Py_INCREF(o);
@@ -467,9 +467,10 @@ PyObject *sequences_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace, status, stream)
+// blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace, status, stream,
+//                new_slots, slots)
 PyObject *blocks_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!count_is(n, 11)) return nullptr;
+    if (!count_is(n, 13)) return nullptr;
     Call c{"pa_blocks_compact"};
     const Pools *p = pools_of(c, a[7]);
     const Tensor nt = take(c, a[0], "new_tables", kI32, 2), nr = take(c, a[1], "new_refs", kI32, 1);
@@ -479,15 +480,20 @@ PyObject *blocks_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     size_t bytes = 0;
     void *space = take_space(c, a[8], &bytes);
     int32_t *status = take_status(c, a[9]);
+    const Tensor ns = take_optional(c, a[11], "new_slots", kI64, 1), slots = take_optional(c, a[12], "slots", kI64, 1);
     if (!c.ok) return nullptr;
     const int64_t B = tables.size[0], mb = tables.size[1], nb = p->desc.num_blocks;
     c.need(nt.is({B, mb}) && lens.is({B}) && refs.is({nb}) && nr.is({nb}) && remap.is({nb}) && live.is({1}),
            "tables [B, max_blocks], lens [B], counts and remap [num_blocks], n_live [1]") &&
+        c.need(ns.ndim == slots.ndim && (slots.ndim == 0 || (slots.is({B}) && ns.is({B}))),
+               "slots and new_slots must both be [B], or both be left out") &&
         c.need(fits_int({B, mb}), "a size is out of range");
     return run(c, a[10], [&](pa_stream_t s) {
-        return g_lib.blocks_compact(i32(nt), i32(nr), i32(remap), i32(live), i32(tables), i32(lens), i32(refs),
-                                    static_cast<int32_t>(B), static_cast<int32_t>(mb), p->at.data(),
-                                    static_cast<int32_t>(p->at.size()), p->elem_bytes, p->desc, space, bytes, status, s);
+        return g_lib.blocks_compact_slots(i32(nt), i32(nr), i32(remap), i32(live), static_cast<int64_t *>(ns.at),
+                                          i32(tables), i32(lens), i32(refs), static_cast<const int64_t *>(slots.at),
+                                          static_cast<int32_t>(B), static_cast<int32_t>(mb), p->at.data(),
+                                          static_cast<int32_t>(p->at.size()), p->elem_bytes, p->desc, space, bytes,
+                                          status, s);
     });
 }
 

@@ -93,6 +93,8 @@ struct CopyArgs {
     // tables to rewrite while at it (pa_blocks_compact), or null
     int32_t *new_tables;
     const int32_t *tables, *lens, *remap;
+    int64_t *new_slots;         // and the next tokens' slots, or null
+    const int64_t *slots;
     int B, max_blocks;
     uint8_t *pools[kMaxPools];
 };
@@ -445,7 +447,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
     }
 }
 
-// Rewrites the tables; new_id(id): where a block of the pool went, or -1.
+// Rewrites the tables, and the slots if there are any; new_id(id): where a block of the
+// pool went, or -1.  A row's entries are those of its tokens and, where its length is a
+// multiple of the block size, the block in use that a fork gave it for its next token.
 template <typename NewId>
 __device__ __forceinline__ void rewrite_tables(const CopyArgs &a, NewId &&new_id) {
     const int64_t n = static_cast<int64_t>(a.B) * a.max_blocks;
@@ -454,12 +458,22 @@ __device__ __forceinline__ void rewrite_tables(const CopyArgs &a, NewId &&new_id
         const int b = static_cast<int>(x / a.max_blocks), e = static_cast<int>(x % a.max_blocks);
         const int L = checked_len(a.lens[b], a.max_blocks * a.block_size, a.status);
         int id = -1;
-        if (e < (L + a.block_size - 1) / a.block_size) {
+        if (e * a.block_size <= L) {
             id = a.tables[x];
             id = id >= 0 && id < a.num_blocks ? new_id(id) : -1;
-            if (id < 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+            if (id < 0 && e * a.block_size < L) set_status(a.status, PA_STATUS_BAD_BLOCK);
         }
         a.new_tables[x] = id;
+    }
+    if (!a.slots) return;
+    for (int b = blockIdx.x * kCopyThreads + threadIdx.x; b < a.B; b += gridDim.x * kCopyThreads) {
+        const int64_t slot = a.slots[b], block = slot / a.block_size;
+        int id = -1;
+        if (slot >= 0) {
+            if (block < a.num_blocks) id = new_id(static_cast<int>(block));
+            if (id < 0) set_status(a.status, PA_STATUS_BAD_SLOT);
+        }
+        a.new_slots[b] = id < 0 ? -1 : static_cast<int64_t>(id) * a.block_size + slot % a.block_size;
     }
 }
 
@@ -684,12 +698,24 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
                       const int32_t *lens, const int32_t *refs, int32_t B, int32_t max_blocks_per_seq,
                       void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, void *workspace,
                       size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
+    return pa_blocks_compact_slots(new_tables, new_refs, remap, n_live, nullptr, tables, lens, refs, nullptr, B,
+                                   max_blocks_per_seq, pools, n_pools, elem_bytes, cache, workspace, workspace_bytes,
+                                   status, stream);
+}
+
+int pa_blocks_compact_slots(int32_t *new_tables, int32_t *new_refs, int32_t *remap, int32_t *n_live,
+                            int64_t *new_slots, const int32_t *tables, const int32_t *lens, const int32_t *refs,
+                            const int64_t *slots, int32_t B, int32_t max_blocks_per_seq, void *const *pools,
+                            int32_t n_pools, int32_t elem_bytes, pa_cache_desc cache, void *workspace,
+                            size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
     if (B < 0 || max_blocks_per_seq <= 0) return PA_EINVAL;
     int rc = pa::check_pools(pools, n_pools, elem_bytes, cache);
     if (rc) return rc;
     if (static_cast<int64_t>(max_blocks_per_seq) * cache.block_size > INT32_MAX / 2) return PA_EUNSUPPORTED;
     if (!new_refs || !remap || !n_live || !refs || (B > 0 && (!new_tables || !tables || !lens))) return PA_EINVAL;
     if (new_refs == refs || remap == refs || remap == new_refs) return PA_EINVAL;
+    if (!new_slots != !slots || (slots && new_slots == slots)) return PA_EINVAL;
+    if (!pa::is_aligned(slots, 8) || !pa::is_aligned(new_slots, 8)) return PA_EINVAL;
     for (const void *p : {static_cast<const void *>(new_tables), static_cast<const void *>(new_refs),
                           static_cast<const void *>(remap), static_cast<const void *>(n_live),
                           static_cast<const void *>(tables), static_cast<const void *>(lens),
@@ -709,7 +735,7 @@ int pa_blocks_compact(int32_t *new_tables, int32_t *new_refs, int32_t *remap, in
     pa::CopyArgs c{};
     pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.list = a.list;
-    if (B > 0) c.new_tables = new_tables;
+    if (B > 0) c.new_tables = new_tables, c.new_slots = new_slots, c.slots = slots;
     c.tables = tables, c.lens = lens, c.remap = remap, c.B = B, c.max_blocks = max_blocks_per_seq;
     // (at most half of the blocks move)
     const int64_t turns = std::max(static_cast<int64_t>(cache.num_blocks / 2) * n_pools * pa::pieces_of(cache, elem_bytes),

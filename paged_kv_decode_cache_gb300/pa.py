@@ -115,6 +115,8 @@ _SIGNATURES = {
     "pa_fork_workspace_bytes": ([_I32, _I32, _I32], _SZ),
     "pa_blocks_compact": ([_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _P, _I32, _I32, CacheDesc, _P, _SZ, _P,
                            _P], ctypes.c_int),
+    "pa_blocks_compact_slots": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _P, _I32, _I32, CacheDesc,
+                                 _P, _SZ, _P, _P], ctypes.c_int),
     "pa_compact_workspace_bytes": ([_I32], _SZ),
     "pa_blocks_copy": ([_P, _I32, _I32, CacheDesc, _P, _I32, _P, _P], ctypes.c_int),
     "pa_beam_select": ([_P, _P, _P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P],
@@ -679,10 +681,18 @@ def pa_sequences_fork(new_tables, new_lens, new_refs, slot_mapping, tables, lens
 
 
 def pa_blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace,
-                      status=None, stream=None):
-    """Live blocks moved to the front of every pool; remap: every old block id's new one (-1: free)."""
+                      status=None, stream=None, new_slots=None, slots=None):
+    """Live blocks moved to the front of every pool; remap: every old block id's new one (-1: free).
+    slots, new_slots (int64 [B]): a fork's slots that are still to be written, moved too."""
     (_native or _binding()).blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, _pools_of(pools),
-                                           workspace, status, stream)
+                                           workspace, status, stream, new_slots, slots)
+
+
+def pa_blocks_compact_slots(new_tables, new_refs, remap, n_live, new_slots, tables, lens, refs, slots, pools, workspace,
+                            status=None, stream=None):
+    """pa_blocks_compact with the next tokens' slots moved along."""
+    pa_blocks_compact(new_tables, new_refs, remap, n_live, tables, lens, refs, pools, workspace, status, stream, new_slots,
+                      slots)
 
 
 def pa_blocks_copy(pools, pairs, status=None, stream=None):
