@@ -18,7 +18,7 @@
 // the join and 2 for the launch; 4 rows of 32000 take 8.5, a chain of latencies.
 //
 // Sums: 2^(k x - k max) in fp32 with one rounding of the exponent, k = log2 e in
-// fp32, by which lse is divided in the end; fp32 sums of 8 per vector and of a
+// fp32, by which lse is divided in the end (exponent_unit); fp32 sums of 8 per vector and of a
 // thread's vectors, 64 bits across threads and slices.  Scores are
 // compared in 64 bits: bf16 logits repeat, and beams' scores come close to one
 // another, so a score rounded to fp32 could trade two candidates.
@@ -144,7 +144,7 @@ struct BeamArgs {
     int beams, vocab, K, slices;
     int32_t row0;          // this launch's first row of the call
     int32_t *tickets;      // [kMaxTickets], zero between calls
-    float *part_max;       // [rows, slices] times k
+    float *part_max;       // [rows, slices]
     double *part_sum;      // [rows, slices]
     uint64_t *part_list;   // [rows, slices, K] candidates
 };
@@ -253,12 +253,23 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int K, uint32_t *w
     return key;
 }
 
-// What a sum with maximum m counts from, in log2 units: the product ROUNDED, at every
-// place the same number.  (Contracted into an fma it would be another one, off by up to 2^-24
-// of itself: 0.003 in a score at logits of 60000.)
-__device__ __forceinline__ float log2_ref(float m) { return __fmul_rn(m, kLog2e); }
+// A sum with maximum m holds 2^(u x - u m), with u = k, and u m the product ROUNDED, at
+// every place the same number.  (Contracted into an fma it would be another one, off by
+// up to 2^-24 of itself: 0.003 in a score at logits of 60000.)  The terms carry the
+// product's rounding as a factor, which from 2^31 on could leave fp32's range (rows
+// masked with -1e30 or with the type's lowest value).  Beyond 2^30 therefore u = 1/2,
+// whose products are exact: values there are 128 apart or more, so that in either
+// unit only those equal to m count.
+constexpr float kFar = 0x1p30f;
+__device__ __forceinline__ float exponent_unit(float m) { return fabsf(m) <= kFar ? kLog2e : 0.5f; }
 
-// log2 z for z >= 1 as whole + the result, to 2^-23 or so, in integers and fp32: CUDA's
+// By what a sum with maximum a is multiplied to count from b >= a.
+__device__ __forceinline__ float ratio(float a, float b) {
+    if (fmaxf(fabsf(a), fabsf(b)) > kFar) return a == b ? 1.f : 0.f;   // (-inf: its sum is 0 or NaN)
+    return fast_exp2(__fsub_rn(__fmul_rn(a, kLog2e), __fmul_rn(b, kLog2e)));
+}
+
+// log2 z for a normal z as whole + the result, to 2^-23 or so, in integers and fp32: CUDA's
 // log2(double) is a chain of some 60 FP64 instructions, 1 us here, which a GB300 SM
 // issues at 1/64 of its FP32 rate.  z = 2^whole (m + r) with m, the first 24 bits, in
 // [0.6875, 1.375).  NaN for a NaN.
@@ -409,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     __shared__ float red_max[kThreads / 32];
     __shared__ double red_sum[kThreads / 32];
     __shared__ double lse[kMaxBeams];
-    __shared__ float beam_cum[kMaxBeams], base[kMaxBeams], slack[kMaxBeams];
+    __shared__ float beam_cum[kMaxBeams], base[kMaxBeams], slack[kMaxBeams], head[kMaxBeams];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -440,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         if (tid < K) a.part_list[part * K + tid] = slice == 0 && tid == 0 ? candidate(0.f, a.eos) : 0;
     } else {
         float m = -INFINITY;              // this thread's maximum
+        float unit = kLog2e, minus = 0.f; // (a NaN goes into the sum all the same)
         uint64_t sum2 = 0;                // and sum of 2^(x k - m k), in two halves
         float floor = -INFINITY;          // values at or below it are not among the slice's K largest
         bool overfull = false;
@@ -464,18 +476,19 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 from_float(*gmax, cmax);
                 bmax = fmaxf(bmax, cmax);
                 if (cmax > m) {
-                    const float f = fast_exp2(__fsub_rn(log2_ref(m), log2_ref(cmax)));  // (m = -inf: 0)
+                    const float f = ratio(m, cmax);   // (m = -inf: 0)
                     sum2 = mul2(sum2, pack2(f, f));
                     m = cmax;
+                    unit = exponent_unit(m);
+                    minus = -__fmul_rn(m, unit);
                 }
-                const float minus = m > -INFINITY ? -log2_ref(m) : 0.f;   // (a NaN goes into the sum all the same)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     uint64_t two[E / 2];
 #pragma unroll
                     for (int e = 0; e < E; e += 2) {
                         float a0, a1;
-                        unpack2(fma2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(kLog2e, kLog2e),
+                        unpack2(fma2(pack2(V::get(raw[j], e), V::get(raw[j], e + 1)), pack2(unit, unit),
                                      pack2(minus, minus)), a0, a1);
                         two[e / 2] = pack2(fast_exp2(a0), fast_exp2(a1));
                     }
@@ -540,8 +553,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         __syncthreads();
         if (overfull) kept = exact_slice<T>(row, v0, v1, K, pool, &count, ring[0]);
         // ---- the slice's maximum, sum and list
-        float sum, sum_odd, top = log2_ref(m);
-        const float ref = top;
+        float sum, sum_odd, top = m;
         unpack2(sum2, sum, sum_odd);
         sum += sum_odd;
 #pragma unroll
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, red_max[i]);
-        double z = m > -INFINITY ? sum * fast_exp2(__fsub_rn(ref, top)) : sum;  // (sum: 0 or NaN)
+        double z = sum * ratio(m, top);  // (m = -inf: 0 or NaN)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) red_sum[warp] = z;
@@ -601,15 +613,20 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         for (int i = first; i < a.slices; i += team) M = fmaxf(M, of_max[i]);
         for (int o = team >> 1; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         for (int i = first; i < a.slices; i += team)
-            z += of_sum[i] * (of_max[i] > -INFINITY ? fast_exp2(of_max[i] - M) : 1.f);
+            z += of_sum[i] * ratio(of_max[i], M);
         for (int o = team >> 1; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (first == 0 && w < a.beams) {
             int whole;
             const float part = log2_of_sum(z, &whole);
-            // M + whole + part, exact but for part's last bits, as two floats
-            const float add = static_cast<float>(whole), top = M + add, back = top - M;
-            const float low = ((M - (top - back)) + (add - back)) + part;
-            const float cum = beam_cum[w], l = M > -INFINITY ? (top + low) * (1.f / kLog2e) : INFINITY;
+            // the maximum's product + whole + part, exact but for part's last bits, as two
+            // floats; next to the range's ends the maximum itself stands beside them
+            const bool far = exponent_unit(M) != kLog2e;
+            const float ref = far ? 0.f : __fmul_rn(M, kLog2e);
+            const float add = static_cast<float>(whole), top = ref + add, back = top - ref;
+            const float low = ((ref - (top - back)) + (add - back)) + part;
+            const float cum = beam_cum[w];
+            head[w] = far ? M : 0.f;
+            const float l = M > -INFINITY ? (top + low) * (1.f / kLog2e) + head[w] : INFINITY;
             lse[w] = M > -INFINITY ? (static_cast<double>(top) + low) * (1.0 / kLog2e) : INFINITY;
             base[w] = cum > -INFINITY && l < INFINITY ? fmaxf(cum - l, -FLT_MAX) : -INFINITY;   // (-inf: no candidates)
             slack[w] = kSlack * (fabsf(cum) + fabsf(l));
@@ -645,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         const int w = static_cast<int>((i + 0.5f) * per_entry);
         const uint64_t c = keys[i];
         if (!range_of(w, c, lo, hi) || !(hi >= cut)) continue;
-        const double score = beam_cum[w] + (candidate_value(c) - lse[w]);   // (in 64 bits)
+        const double score = beam_cum[w] + ((candidate_value(c) - head[w]) - lse[w]);   // (in 64 bits)
         if (!(score > -INFINITY)) continue;
         const int at = atomicAdd(&count, 1);
         top_keys[at] = order_key(score);
