@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
     if (kPairs) {
         copy_turns<kCopyThreads>(a, a.n_pairs, blockIdx.x, gridDim.x, [&](int k) {
             const int2 e = a.pairs[k];
-            const bool bad = e.x >= a.num_blocks || e.y >= a.num_blocks || (e.x >= 0 && e.y < 0);
+            const bool bad = e.x >= 0 && (e.x >= a.num_blocks || e.y < 0 || e.y >= a.num_blocks);
             if (bad && threadIdx.x == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
             return make_int4(bad ? -1 : e.x, e.y, a.block_size, 0);
         });

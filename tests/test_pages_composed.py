@@ -270,3 +270,16 @@ def test_slots_refusals(slots, new_slots):
     assert pa.lib().pa_blocks_compact_slots(OTHER[0], OTHER[1], OTHER[2], OTHER[3], at(new_slots), OTHER[4], OTHER[5], OTHER[6],
                                             at(slots), 3, 4, POOLS, 2, 2, DESC, FAKE, pa.pa_compact_workspace_bytes(64), None,
                                             None) == pa.PA_EINVAL
+
+
+@pytest.mark.gpu
+def test_padding_pairs_are_skipped_whatever_their_destination():
+    pools = make_pools(2, 12, 16, 1, 64, False, 5)
+    before = [t.clone() for t in pools]
+    status = dev([0])
+    pa.pa_blocks_copy(pa.PoolSet(pools), dev([[-1, 12], [-1, -1], [-7, 1 << 30], [3, 0]]), status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for pool, old in zip(pools, before):
+        old[0] = old[3]
+        assert torch.equal(pool.view(torch.uint8), old.view(torch.uint8))
