@@ -3,8 +3,9 @@ binding's C++ calls (``_build/_pa_binding.so``, a CPython extension that reads
 torch tensors' fields; g++ and torch's headers).
 
 Each .cu file is compiled for sm_103a by its own nvcc process (in parallel),
-then linked into ``paged_kv_decode_cache_gb300/_build/libpagedattn.so``.
-The build is skipped when the library is newer than every source.
+then linked into ``paged_kv_decode_cache_gb300/_build/libpagedattn.so``, which
+needs neither g++ nor torch (``--library`` builds it alone).
+Either part's build is skipped when its file is newer than every source of it.
 ``-Xptxas -v`` output (registers, spills, shared memory per kernel) is kept
 in ``_build/ptxas.log``.
 """
@@ -38,16 +39,25 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def _newer(path: str, deps: list[str]) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+                  + _headers())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, glob.glob(os.path.join(CSRC, "*.cpp")) + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _extra_flags() -> list[str]:
@@ -83,14 +93,29 @@ def _compile_binding() -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    """The library and the binding, at the same time; a binding that does not compile raises after the
+    library has been built."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(build_binding, force)
+        build_library(force, verbose)
+        binding.result()
+    return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    if force or not binding_up_to_date():
+        os.makedirs(BUILD, exist_ok=True)
+        _compile_binding()
+    return BINDING
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    if not force and library_up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         results = list(ex.map(_compile, srcs))
-        binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for _, log in results:
             f.write(log)
@@ -108,4 +133,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose=True)
+    (build_library if "--library" in sys.argv else build)(force="--force" in sys.argv, verbose=True)
