@@ -5,7 +5,8 @@ torch tensors' fields; g++ and torch's headers).
 Each .cu file is compiled for sm_103a by its own nvcc process (in parallel),
 then linked into ``paged_kv_decode_cache_gb300/_build/libpagedattn.so``, which
 needs neither g++ nor torch (``--library`` builds it alone).
-Either part's build is skipped when its file is newer than every source of it.
+Either part's build is skipped when its file is newer than every source of it
+(and, for the binding, was built for this torch and Python).
 ``-Xptxas -v`` output (registers, spills, shared memory per kernel) is kept
 in ``_build/ptxas.log``.
 """
@@ -53,7 +54,23 @@ def library_up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, glob.glob(os.path.join(CSRC, "*.cpp")) + _headers())
+    return _newer(BINDING, glob.glob(os.path.join(CSRC, "*.cpp")) + _headers()) and binding_fits()
+
+
+def binding_abi() -> str:
+    """What the binding is compiled against, besides its sources: this Python and this torch, whose
+    headers' inlined functions it holds."""
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__}"
+
+
+def binding_fits() -> bool:
+    """Whether the binding was built for this Python and torch (noted beside it)."""
+    try:
+        with open(BINDING + ".abi") as f:
+            return f.read() == binding_abi()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -106,6 +123,8 @@ def build_binding(force: bool = False) -> str:
     if force or not binding_up_to_date():
         os.makedirs(BUILD, exist_ok=True)
         _compile_binding()
+        with open(BINDING + ".abi", "w") as f:
+            f.write(binding_abi())
     return BINDING
 
 

@@ -599,6 +599,9 @@ def _binding():
         path = _build.BINDING
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with paged_kv_decode_cache_gb300.build.build()")
+        if not _build.binding_fits():
+            raise RuntimeError(f"{path} was built for another torch or Python: build it again with "
+                               "paged_kv_decode_cache_gb300.build.build()")
         loader = importlib.machinery.ExtensionFileLoader("_pa_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_binding", loader))
         loader.exec_module(module)

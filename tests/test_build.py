@@ -59,3 +59,33 @@ def test_the_library_is_there_when_the_binding_does_not_compile(tools, monkeypat
 def test_the_library_alone_needs_no_torch(tools, monkeypatch):
     monkeypatch.setattr(B, "_compile_binding", lambda: pytest.fail("not asked for"))
     assert B.build_library() == B.LIB and os.path.exists(B.LIB)
+
+
+def test_another_torch_or_python_builds_the_binding_again(tools, monkeypatch):
+    """The binding reads tensors' fields through inlined headers: it fits the torch that it was built with."""
+    B.build()
+    tools("g++")
+    monkeypatch.setattr(B, "binding_abi", lambda: "cpython-999 torch 99.0")
+    assert not B.up_to_date() and B.library_up_to_date()
+    B.build()
+    assert len(tools("g++")) == 1 and tools("nvcc") == []
+    assert B.up_to_date()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(tools, monkeypatch):
+    from paged_kv_decode_cache_gb300 import pa
+    B.build()
+    monkeypatch.setattr(pa, "_native", None)
+    monkeypatch.setattr(pa, "lib", lambda: None)
+    monkeypatch.setattr(B, "binding_abi", lambda: "cpython-999 torch 99.0")
+    with pytest.raises(RuntimeError, match="another torch"):
+        pa._binding()
+    os.remove(B.BINDING)
+    with pytest.raises(RuntimeError, match="missing"):
+        pa._binding()
+
+
+def test_the_abi_names_torch_and_python():
+    import sysconfig
+    import torch
+    assert torch.__version__ in B.binding_abi() and sysconfig.get_config_var("SOABI") in B.binding_abi()
