@@ -394,17 +394,27 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // ---- pools that share tables ------------------------------------------------------------------
 
+// The tensors, not their addresses: what a tensor's memory is may change (set_, .data =,
+// resize_), and every call takes it anew.
 struct Pools {
-    std::vector<void *> at;
+    std::vector<at::Tensor> tensors;
     pa_cache_desc desc;
     int32_t elem_bytes;
     int device;
+};
+// A call's view of them (the library takes at most 256).
+constexpr size_t kMostPools = 256;
+struct PoolsNow {
+    void *at[kMostPools];
+    int32_t n;
+    pa_cache_desc desc;
+    int32_t elem_bytes;
 };
 constexpr const char *kPools = "_pa_binding.pools";
 
 void free_pools(PyObject *capsule) { delete static_cast<Pools *>(PyCapsule_GetPointer(capsule, kPools)); }
 
-// pools(tensor, ...) -> a handle; the tensors, alike in every respect, are kept alive by the caller
+// pools(tensor, ...) -> a handle that holds the tensors, alike in every respect
 PyObject *pools(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Call c{"PoolSet"};
     if (n < 1) return c.fail(PyExc_ValueError, "a PoolSet needs at least one pool"), nullptr;
@@ -418,7 +428,7 @@ PyObject *pools(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (i == 0) first = t;
             c.ok && c.need(t.is({first.size[0], first.size[1], first.size[2], first.size[3]}), "the pools differ in shape") &&
                 c.need(fits_int({t.size[0], t.size[1], t.size[2], t.size[3]}), "a size is out of range");
-            p->at.push_back(t.at);
+            if (c.ok) p->tensors.push_back(THPVariable_Unpack(a[i]));
         }
         p->desc = desc_of(first);
         p->elem_bytes = u8 ? 1 : 2;
@@ -431,11 +441,32 @@ PyObject *pools(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return capsule;
 }
 
-const Pools *pools_of(Call &c, PyObject *o) {
+void pools_of(Call &c, PyObject *o, PoolsNow *now) {
     const Pools *p = static_cast<const Pools *>(PyCapsule_GetPointer(o, kPools));
-    if (!p) return c.ok = false, nullptr;
+    if (!p) {
+        c.ok = false;
+        return;
+    }
     c.device = p->device;
-    return p;
+    now->desc = p->desc;
+    now->elem_bytes = p->elem_bytes;
+    now->n = static_cast<int32_t>(p->tensors.size());
+    const int64_t size[4] = {p->desc.num_blocks, p->desc.block_size, p->desc.num_kv_heads, p->desc.head_dim};
+    const c10::ScalarType type = p->elem_bytes == 1 ? c10::ScalarType::Byte : c10::ScalarType::BFloat16;
+    const size_t bytes = static_cast<size_t>(size[0]) * size[1] * size[2] * size[3] * p->elem_bytes;
+    for (size_t i = 0; i < p->tensors.size(); ++i) {
+        const at::Tensor &t = p->tensors[i];
+        const c10::IntArrayRef now_size = t.sizes();
+        const c10::Device device = t.device();
+        const bool same = now_size.size() == 4 && now_size[0] == size[0] && now_size[1] == size[1] && now_size[2] == size[2] &&
+                          now_size[3] == size[3] && t.scalar_type() == type && t.is_contiguous() && device.is_cuda() &&
+                          device.index() == p->device && t.has_storage() &&
+                          t.storage().nbytes() >= static_cast<size_t>(t.storage_offset()) * p->elem_bytes + bytes;
+        if (!c.need(same, "a pool is not the tensor any more (shape, type, device or size of its memory) that the "
+                          "PoolSet was made of"))
+            return;
+        if (i < kMostPools) now->at[i] = t.data_ptr();
+    }
 }
 
 int32_t *i32(const Tensor &t) { return static_cast<int32_t *>(t.at); }
@@ -445,7 +476,8 @@ int32_t *i32(const Tensor &t) { return static_cast<int32_t *>(t.at); }
 PyObject *sequences_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count_is(n, 12)) return nullptr;
     Call c{"pa_sequences_fork"};
-    const Pools *p = pools_of(c, a[8]);
+    PoolsNow p;
+    pools_of(c, a[8], &p);
     const Tensor nt = take(c, a[0], "new_tables", kI32, 2), nl = take(c, a[1], "new_lens", kI32, 1);
     const Tensor nr = take(c, a[2], "new_refs", kI32, 1), slots = take(c, a[3], "slot_mapping", kI64, 1);
     const Tensor tables = take(c, a[4], "tables", kI32, 2), lens = take(c, a[5], "lens", kI32, 1);
@@ -454,7 +486,7 @@ PyObject *sequences_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *space = take_space(c, a[9], &bytes);
     int32_t *status = take_status(c, a[10]);
     if (!c.ok) return nullptr;
-    const int64_t rows = parents.size[0], old = tables.size[0], mb = tables.size[1], nb = p->desc.num_blocks;
+    const int64_t rows = parents.size[0], old = tables.size[0], mb = tables.size[1], nb = p.desc.num_blocks;
     c.need(lens.is({old}) && refs.is({nb}) && nr.is({nb}), "tables, lens and refs must be [B, max_blocks], [B] and [num_blocks]") &&
         c.need(nt.is({rows, mb}) && nl.is({rows}) && slots.is({rows}),
                "the new tables, lens and slots must have a row for every parent") &&
@@ -462,8 +494,8 @@ PyObject *sequences_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return run(c, a[11], [&](pa_stream_t s) {
         return g_lib.sequences_fork(i32(nt), i32(nl), i32(nr), static_cast<int64_t *>(slots.at), i32(tables), i32(lens),
                                     i32(refs), i32(parents), static_cast<int32_t>(old), static_cast<int32_t>(rows),
-                                    static_cast<int32_t>(mb), p->at.data(), static_cast<int32_t>(p->at.size()),
-                                    p->elem_bytes, p->desc, space, bytes, status, s);
+                                    static_cast<int32_t>(mb), p.at, p.n,
+                                    p.elem_bytes, p.desc, space, bytes, status, s);
     });
 }
 
@@ -472,7 +504,8 @@ PyObject *sequences_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *blocks_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count_is(n, 13)) return nullptr;
     Call c{"pa_blocks_compact"};
-    const Pools *p = pools_of(c, a[7]);
+    PoolsNow p;
+    pools_of(c, a[7], &p);
     const Tensor nt = take(c, a[0], "new_tables", kI32, 2), nr = take(c, a[1], "new_refs", kI32, 1);
     const Tensor remap = take(c, a[2], "remap", kI32, 1), live = take(c, a[3], "n_live", kI32, 1);
     const Tensor tables = take(c, a[4], "tables", kI32, 2), lens = take(c, a[5], "lens", kI32, 1);
@@ -482,7 +515,7 @@ PyObject *blocks_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *status = take_status(c, a[9]);
     const Tensor ns = take_optional(c, a[11], "new_slots", kI64, 1), slots = take_optional(c, a[12], "slots", kI64, 1);
     if (!c.ok) return nullptr;
-    const int64_t B = tables.size[0], mb = tables.size[1], nb = p->desc.num_blocks;
+    const int64_t B = tables.size[0], mb = tables.size[1], nb = p.desc.num_blocks;
     c.need(nt.is({B, mb}) && lens.is({B}) && refs.is({nb}) && nr.is({nb}) && remap.is({nb}) && live.is({1}),
            "tables [B, max_blocks], lens [B], counts and remap [num_blocks], n_live [1]") &&
         c.need(ns.ndim == slots.ndim && (slots.ndim == 0 || (slots.is({B}) && ns.is({B}))),
@@ -491,8 +524,7 @@ PyObject *blocks_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return run(c, a[10], [&](pa_stream_t s) {
         return g_lib.blocks_compact_slots(i32(nt), i32(nr), i32(remap), i32(live), static_cast<int64_t *>(ns.at),
                                           i32(tables), i32(lens), i32(refs), static_cast<const int64_t *>(slots.at),
-                                          static_cast<int32_t>(B), static_cast<int32_t>(mb), p->at.data(),
-                                          static_cast<int32_t>(p->at.size()), p->elem_bytes, p->desc, space, bytes,
+                                          static_cast<int32_t>(B), static_cast<int32_t>(mb), p.at, p.n, p.elem_bytes, p.desc, space, bytes,
                                           status, s);
     });
 }
@@ -501,13 +533,14 @@ PyObject *blocks_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *blocks_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count_is(n, 4)) return nullptr;
     Call c{"pa_blocks_copy"};
-    const Pools *p = pools_of(c, a[0]);
+    PoolsNow p;
+    pools_of(c, a[0], &p);
     const Tensor pairs = take(c, a[1], "pairs", kI32, 2);
     int32_t *status = take_status(c, a[2]);
     if (!c.ok) return nullptr;
     c.need(pairs.size[1] == 2 && fits_int({pairs.size[0]}), "pairs must be [n, 2]");
     return run(c, a[3], [&](pa_stream_t s) {
-        return g_lib.blocks_copy(p->at.data(), static_cast<int32_t>(p->at.size()), p->elem_bytes, p->desc, i32(pairs),
+        return g_lib.blocks_copy(p.at, p.n, p.elem_bytes, p.desc, i32(pairs),
                                  static_cast<int32_t>(pairs.size[0]), status, s);
     });
 }

@@ -651,7 +651,8 @@ def pa_rope_write_fp8(q_out, q, k_new, v_new, positions, slot_mapping, k_cache, 
 class PoolSet:
     """The K and V pools (of every layer) that share block tables, as pa_sequences_fork,
     pa_blocks_compact and pa_blocks_copy take them: bf16 or uint8 tensors
-    [num_blocks, block_size, Hkv, D], all alike.  Holds the tensors."""
+    [num_blocks, block_size, Hkv, D], all alike.  Holds the tensors; each call uses the memory
+    that they have then, and refuses tensors whose shape has changed since."""
 
     def __init__(self, pools):
         self.pools = list(pools)
