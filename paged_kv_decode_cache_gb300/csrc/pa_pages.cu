@@ -210,8 +210,7 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     int32_t *row_rank = row_tail + a.B_new;         // [B_new] needs a block: which one; else -1
     int32_t *children = row_rank + a.B_new;         // [B_old]
     int32_t *old_len = children + a.B_old;          // [B_old]
-    int32_t *old_tail = old_len + a.B_old;          // [B_old]
-    int32_t *near = old_tail + a.B_old;             // kSmall: the arrays below
+    int32_t *near = old_len + a.B_old;              // kSmall: the arrays below
     int32_t *refs = kSmall ? near : a.new_refs;                            // [num_blocks]
     int32_t *tail_count = kSmall ? near + a.num_blocks : a.tail_count;      // [num_blocks]
     int32_t *tail_first = kSmall ? near + 2 * a.num_blocks : a.tail_first;  // [num_blocks]
@@ -231,14 +230,12 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     const int bs = a.block_size, mb = a.max_blocks, lmax = mb * bs;
 
     // ---- the rows' parents and lengths (every CTA for itself), the counts copied
-    // (each thread's first loads are asked for at once, before the one that waits for a length)
+    // (each thread's first loads are asked for at once)
     const int len0 = tid < a.B_old ? a.lens[tid] : 0, parent0 = tid < a.B_new ? a.parents[tid] : -1;
     const int refs0 = gid < a.num_blocks ? a.refs[gid] : 0;
     for (int j = tid; j < a.B_old; j += kPlanThreads) {
-        const int L = checked_len(j == tid ? len0 : a.lens[j], lmax, a.status);
         children[j] = 0;
-        old_len[j] = L;
-        old_tail[j] = L < lmax ? next_block(a.tables[static_cast<int64_t>(j) * mb + L / bs], L, bs, a.refs, a.num_blocks) : -1;
+        old_len[j] = checked_len(j == tid ? len0 : a.lens[j], lmax, a.status);
     }
     for (int i = tid; i < a.B_new; i += kPlanThreads) row_parent[i] = i == tid ? parent0 : a.parents[i];
     for (int i = gid; i < a.num_blocks; i += gthreads) {
@@ -254,8 +251,8 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
         }
         if (p >= 0) {
             L = old_len[p];
-            t = old_tail[p];
             atomicAdd(children + p, 1);
+            if (L < lmax) t = next_block(a.tables[static_cast<int64_t>(p) * mb + L / bs], L, bs, a.refs, a.num_blocks);
             if (!kSmall && cta == 0 && t >= 0) tail_count[t] = 0, tail_first[t] = INT32_MAX;
         }
         row_parent[i] = p < 0 ? -1 : p;
@@ -265,17 +262,17 @@ fork_plan_kernel(const ForkArgs a, const __grid_constant__ CopyArgs copy) {
     everyone();
 
     // ---- references dropped and added; tables copied (a warp per row)
-    auto blocks = [&](int L, int tail) { return L / bs + (L % bs || tail >= 0); };
     for (int j = gid >> 5; j < a.B_old; j += gthreads >> 5) {
-        const int change = children[j] - 1;
+        const int change = children[j] - 1, L = old_len[j];
         if (change == 0) continue;
-        for_entries(a.tables + static_cast<int64_t>(j) * mb, blocks(old_len[j], old_tail[j]), lane, [&](int, int id) {
+        for_entries(a.tables + static_cast<int64_t>(j) * mb, min(L / bs + 1, mb), lane, [&](int e, int id) {
+            if (e * bs >= L) id = next_block(id, L, bs, a.refs, a.num_blocks);   // (past a full block; -1 is no fault there)
+            else if (id < 0 || id >= a.num_blocks) set_status(a.status, PA_STATUS_BAD_BLOCK);
             if (id >= 0 && id < a.num_blocks) atomicAdd(refs + id, change);
-            else set_status(a.status, PA_STATUS_BAD_BLOCK);
         });
     }
     for (int i = gid >> 5; i < a.B_new; i += gthreads >> 5) {
-        const int p = row_parent[i], nb = blocks(row_len[i], row_tail[i]);
+        const int p = row_parent[i], nb = (row_len[i] + bs - 1) / bs + (row_len[i] % bs == 0 && row_tail[i] >= 0);
         int32_t *row = a.new_tables + static_cast<int64_t>(i) * mb;
         if (lane == 0 && row_tail[i] >= 0) {
             atomicAdd(tail_count + row_tail[i], 1);
@@ -674,7 +671,7 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     pa::CopyArgs c{};
     pa::set_pools(c, pools, n_pools, elem_bytes, cache, status);
     c.list = own_copy ? a.list : nullptr;
-    int smem = (4 * B_new + 3 * B_old) * 4;
+    int smem = (4 * B_new + 2 * B_old) * 4;
     if (small) smem += (3 * cache.num_blocks + B_new) * 4;
     auto kern = small ? pa::fork_plan_kernel<true> : pa::fork_plan_kernel<false>;
     static std::atomic<uint64_t> smem_attr_done[2];
@@ -682,7 +679,7 @@ int pa_sequences_fork(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs,
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ECUDA;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done[small].load(std::memory_order_acquire) & bit)) {
-        const int most = small ? 8 * pa::kNearRows + 3 * pa::kNearWords : 7 * pa::kMaxRows;   // words
+        const int most = small ? 7 * pa::kNearRows + 3 * pa::kNearWords : 6 * pa::kMaxRows;   // words
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most * 4) != cudaSuccess)
             return PA_ECUDA;
         smem_attr_done[small].fetch_or(bit, std::memory_order_release);
