@@ -502,8 +502,10 @@ int pa_decode_launches(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_
  * Rotary positions.  A plan holds, for every pair of dimensions that turns,
  * how far one position turns it; pa_rope_init fills it on the host once, and
  * calls read it by value.  The turn is a 64-bit fixed-point fraction of a full
- * turn (2^64 = one turn), so that position * turn modulo 2^64 is the exact
- * angle's fraction at any position: far positions lose nothing.
+ * turn (2^64 = one turn), rounded once from a 64-bit float (about 2^-54 of a turn
+ * for frequencies of up to a radian per position); position * turn modulo 2^64 is
+ * exact.  An angle is so off by about position * 2^-54 turns: 4e-10 radians at a
+ * million.
  */
 #define PA_ROPE_MAX_PAIRS 64
 typedef struct {
@@ -684,8 +686,12 @@ int pa_blocks_copy(void *const *pools, int32_t n_pools, int32_t elem_bytes, pa_c
  * Beam search's selection: for every request (group) the K best continuations
  * over its beams and the vocabulary,
  *   score(w, v) = cum[w] + (x[w, v] - ln sum_u exp x[w, u]),
- * best first, ties to the lowest w * vocab + v, compared in 64 bits.  One launch
- * (per 4096 groups), one pass over the logits.
+ * best first, ties to the lowest w * vocab + v.  A row's order is its logits' own;
+ * scores are formed and compared in 64 bits, from each row's ln sum, whose
+ * exponentials, their sums within a thread and the logarithm are in fp32: it is good to
+ * 2^-19, and entries of different beams that come nearer to one another than that may
+ * trade places (beams of equal rows have equal sums).  One launch (per 4096 groups),
+ * one pass over the logits.
  * logits: device, row r = group * beams + w at r * row_stride elements, bf16
  * (PA_LOGITS_BF16) or fp32 (PA_LOGITS_F32), 16-byte aligned base, row_stride >= vocab
  * (rows need no alignment of their own).  -inf excludes an entry; a NaN or +inf
@@ -756,9 +762,13 @@ int pa_decode_scored_fp8(void *out, float *lse, const void *q, int32_t q_len, co
                          const pa_score_rules *rules, int32_t num_splits, void *workspace,
                          size_t workspace_bytes, int32_t *status, pa_stream_t stream);
 
-/* Split count for pa_decode_scored by the rule of pa_choose_num_splits_mq over
- * the tokens that can be seen (max_prefix: 0 without prefix_lens); sm_count 0:
- * the current device's.  P >= 1, or PA_EINVAL / PA_EUNSUPPORTED / PA_ECUDA. */
+/* Split count for pa_decode_scored, over the tokens that can be seen (max_prefix: 0
+ * without prefix_lens): for the tensor-core decode kernel the one that takes the
+ * least time by a model of the stream, the merge and further waves; by
+ * pa_choose_num_splits_mq's rule for the CUDA-core kernel, and for the prefill-shaped
+ * one with at most a partition per 128 tokens.  It is what num_splits = 0 uses: size
+ * the workspace of such a call from it.  sm_count 0: the current device's.  P >= 1, or
+ * PA_EINVAL / PA_EUNSUPPORTED / PA_ECUDA. */
 int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D,
                          int32_t max_blocks_per_seq, int32_t block_size, int32_t window,
                          int32_t max_prefix, int32_t sm_count);

@@ -683,8 +683,9 @@ int pa_combine(void *out, float *lse, const float *part_o, const float *part_lse
 }
 
 namespace {
-// Partitions of a scored call: the rule of pa_choose_num_splits_mq over the
-// tokens that it can see, of which there are at least one tile.
+// Partitions of a scored call, over the tokens that it can see (at least one tile): a
+// model of its time for the tensor-core decode kernel, pa_choose_num_splits_mq's rule
+// for the others.
 int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_blocks_per_seq,
                   int32_t block_size, int32_t window, int32_t max_prefix, int sms) {
     if (window < 0 || max_prefix < 0 || q_len <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq <= 0 ||

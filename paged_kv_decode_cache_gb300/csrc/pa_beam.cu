@@ -15,13 +15,14 @@
 // bf16.)  The last CTA of a request to finish joins its lists.  Those rows now take
 // 29 us: the stream 17 (4.5 TB/s: one wave of CTAs, which all start and end at once;
 // L2 prefetches and deeper rings made it slower), 6 for the candidates, 4 for
-// the join and 2 for the launch; 4 rows of 32000 take 8.5, a chain of latencies.
+// the join and 2 for the launch; 4 rows of 32000 take 8.4, a chain of latencies.
 //
 // Sums: 2^(k x - k max) in fp32 with one rounding of the exponent, k = log2 e in
 // fp32, by which lse is divided in the end (exponent_unit); fp32 sums of 8 per vector and of a
-// thread's vectors, 64 bits across threads and slices.  Scores are
-// compared in 64 bits: bf16 logits repeat, and beams' scores come close to one
-// another, so a score rounded to fp32 could trade two candidates.
+// thread's vectors, 64 bits across threads and slices, the logarithm in fp32: an lse is
+// good to 2^-19.  Scores are formed and compared in 64 bits, so that candidates of one beam
+// keep their logits' order however large its score is (rounded to fp32 they could trade
+// places); those of different beams can, within their lses' error.
 #include <cuda_bf16.h>
 
 #include <algorithm>

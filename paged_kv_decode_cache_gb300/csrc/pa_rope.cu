@@ -3,9 +3,9 @@
 //
 // Pair (a, b) of a head at position p turns by t = p f: a' = m (a cos t - b sin t),
 // b' = m (a sin t + b cos t).  The plan holds f / 2 pi as a 64-bit fraction of a turn;
-// p times it modulo 2^64 is the angle's exact fraction, whose top 32 bits, as
-// a signed number of half turns, go to sincospi.  (p f in fp32 is off by p 2^-25
-// radians: 0.03 at a million.)
+// p times it modulo 2^64 is exact, so that the angle is off by the plan's own rounding,
+// about p 2^-54 turns; its top 32 bits, as a signed number of half turns, go to
+// sincospi.  (p f in fp32 is off by p 2^-25 radians: 0.03 at a million.)
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
