@@ -773,6 +773,149 @@ int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int3
                          int32_t max_blocks_per_seq, int32_t block_size, int32_t window,
                          int32_t max_prefix, int32_t sm_count);
 
+/*
+ * Long contexts.  Two ways to have a decode step read less of a long cache: it attends
+ * only the blocks that a cheap score picks for this query (pa_key_bounds,
+ * pa_blocks_select, pa_decode_selected), or tokens that attention has not looked at are
+ * thrown out for good (pa_weights_add, pa_cache_evict).
+ */
+
+/*
+ * Bounds of the keys, block by block: bounds[i, h, 0, d] and bounds[i, h, 1, d] are the
+ * least and the largest K[t, h, d] over the tokens t of block i.  Every block in which a
+ * sequence has a token in [starts[b], seq_lens[b]) gets its bounds anew from all of the
+ * sequence's tokens in it (starts NULL: 0), so a step's call passes the lengths
+ * before its tokens were written; other blocks' bounds are left as they were.  A NaN
+ * among a channel's keys makes both bounds NaN.  After pa_cache_evict every block of a row
+ * that was cut needs its bounds anew.
+ * bounds: device [num_blocks, Hkv, 2, D] of the pool's elements (elem_bytes 2: bf16, 1:
+ * e4m3 codes, compared as the values they stand for); k_cache the pool.  Rows that
+ * share a block have the same tokens in it.  max_new: a bound on seq_lens[b] -
+ * starts[b] that keeps a step's launch small, 0: none (a sequence with more new tokens
+ * sets PA_STATUS_BAD_SEQLEN, and its newest max_new count; so does a start below 0, which
+ * counts as 0).  seq_lens, starts: device int32 [B]; a length outside the table is
+ * clamped and sets PA_STATUS_BAD_SEQLEN; a block id outside the pool is skipped and sets
+ * PA_STATUS_BAD_BLOCK.  B <= 65535.
+ */
+int pa_key_bounds(void *bounds, const void *k_cache, int32_t elem_bytes, pa_cache_desc cache,
+                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                  const int32_t *starts, int32_t max_new, int32_t B, int32_t *status,
+                  pa_stream_t stream);
+
+/*
+ * Blocks chosen for a query.  No key of block j scores more, for query head g of KV
+ * head h, than
+ *   sum_d max(q[b,g,d] lo_d, q[b,g,d] hi_d)     (lo, hi: the block's bounds)
+ * and the block's score is the largest of these over the group's heads.  Of every
+ * sequence and KV head the first `first` blocks, the last `last` ones (the newest
+ * token's among them) and, of the others, those with the largest scores are taken, up
+ * to max_selected (K) in all, ties to the earlier block.  Scores are compared as 64-bit
+ * sums; a scale, or the scale of FP8 pools, would not change their order.  A block
+ * whose bounds hold an infinity or a NaN counts as larger than any finite score, as does
+ * every block for a group of queries with one; a block id outside the pool counts as
+ * the smallest and sets PA_STATUS_BAD_BLOCK.
+ * sel_tables: device int32 [B, Hkv, K], the chosen blocks' physical ids in the order of
+ * the sequence, -1 behind them; sel_lens: device int32 [B, Hkv], the tokens they hold of
+ * the sequence.  q: device bf16 [B, Hq, D].  bounds, elem_bytes: as pa_key_bounds
+ * leaves them.  1 <= last, first + last <= K; Hq / Hkv <= 32; max_blocks_per_seq <= 98304.
+ */
+int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_lens, const void *q,
+                     const void *bounds, int32_t elem_bytes, pa_cache_desc cache,
+                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                     const int32_t *seq_lens, int32_t B, int32_t Hq, int32_t first, int32_t last,
+                     int32_t *status, pa_stream_t stream);
+
+/*
+ * Decode attention in which every KV head reads blocks of its own: pa_decode_splitkv
+ * with the table row sel_tables[b, h] and the length sel_lens[b, h] in the place of
+ * sequence b's, for the query heads of KV head h.  sel_tables: device int32 [B, Hkv,
+ * max_selected]; sel_lens: device int32 [B, Hkv], the tokens of the list, all of its
+ * blocks full but the last.  A list without tokens gives out = 0 and lse = -inf.
+ * Supported: the shapes of pa_decode_splitkv (FP8: of pa_decode_splitkv_fp8), B * Hkv <=
+ * 65535.  num_splits 0: pa_auto_num_splits(B * Hkv, Hq / Hkv, 1, D, max_selected,
+ * block_size); workspace: pa_splitkv_workspace_bytes(B, Hq, D, P) bytes, with
+ * pa_decode_splitkv's contract.
+ */
+int pa_decode_selected(void *out, float *lse, const void *q, const void *k_cache,
+                       const void *v_cache, pa_cache_desc cache, const int32_t *sel_tables,
+                       int32_t max_selected, const int32_t *sel_lens, int32_t B, int32_t Hq,
+                       float scale, int32_t num_splits, void *workspace, size_t workspace_bytes,
+                       int32_t *status, pa_stream_t stream);
+
+/* pa_decode_selected over FP8 pools, as pa_decode_splitkv_fp8 reads them (head_dim 128 only). */
+int pa_decode_selected_fp8(void *out, float *lse, const void *q, const void *k_cache,
+                           const void *v_cache, pa_cache_desc cache, float k_scale, float v_scale,
+                           const int32_t *sel_tables, int32_t max_selected, const int32_t *sel_lens,
+                           int32_t B, int32_t Hq, float scale, int32_t num_splits, void *workspace,
+                           size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/*
+ * The attention weight that cached tokens draw.  For the queries i < q_len of
+ * sequence b (its last q_len tokens, as in pa_decode_mq), and every KV head h and token
+ * t < seq_lens[b]:
+ *   new_weights[b,h,t] = decay * weights[b,h,t] + sum_i sum_g exp(scale <q[b,i,g], K[t,h]> - lse[b,i,g])
+ * over the group's heads g and the queries that see t (t <= their position).  The q_len
+ * newest tokens have no weight yet: their sum alone is stored, and, with positions not
+ * NULL, positions[b,h,t] = ends[b] - seq_lens[b] + t, where ends[b] counts every token
+ * that the sequence has had, evicted ones too (NULL: seq_lens).  lse is what
+ * attention gave for these queries (one of -inf adds nothing), so a query's weights sum
+ * to one over the tokens it saw.  Places from seq_lens[b] on are left as they were.
+ * weights, new_weights: device fp32 [B, Hkv, room], the same buffer or two; positions:
+ * device int32 [B, Hkv, room]; q: device bf16 [B, q_len, Hq, D]; lse: device fp32 [B,
+ * q_len, Hq].  decay >= 0.  Sums are in fp32, in a fixed order.  1 <= q_len <= 65535,
+ * Hq / Hkv <= 32.  A length above room or the table's tokens is clamped and sets
+ * PA_STATUS_BAD_SEQLEN; tokens of a block outside the pool draw nothing
+ * (PA_STATUS_BAD_BLOCK).
+ */
+int pa_weights_add(float *new_weights, const float *weights, int32_t *positions, const void *q,
+                   int32_t q_len, const float *lse, const void *k_cache, pa_cache_desc cache,
+                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                   const int32_t *seq_lens, const int32_t *ends, int64_t room, int32_t B,
+                   int32_t Hq, float scale, float decay, int32_t *status, pa_stream_t stream);
+
+/* pa_weights_add over an FP8 pool: K = e4m3(code) * k_scale. */
+int pa_weights_add_fp8(float *new_weights, const float *weights, int32_t *positions, const void *q,
+                       int32_t q_len, const float *lse, const void *k_cache, pa_cache_desc cache,
+                       float k_scale, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                       const int32_t *seq_lens, const int32_t *ends, int64_t room, int32_t B,
+                       int32_t Hq, float scale, float decay, int32_t *status, pa_stream_t stream);
+
+/*
+ * Tokens evicted.  Sequence b, of L = lens[b] tokens, keeps n of them:
+ *   n = min(L, budget), or min(L, max(budget, F + first + recent)) where F > 0,
+ * F being its tokens up to the last block that has more than one reference: those
+ * cannot be thrown out for one holder alone, and stay where they are.  Which others
+ * stay is every layer's and KV head's own choice: tokens at positions below `first`,
+ * the `recent` newest (positions above that of token L - 1, less recent), and then
+ * the heaviest by weights, ties to the lower place; a NaN weighs like +inf.
+ * The tokens that stay and stand below n are not moved; the free places below n take
+ * the ones behind, the k-th place the k-th token, in both pools, new_weights and
+ * new_positions.  (So a sequence's tokens stand in no order, and differ from
+ * head to head; attention does not mind: keys carry their positions.  A
+ * distance bias or a window by place does.)  new_weights and new_positions get every
+ * place below n; places from n on are left as they were.
+ * new_lens: n; new_tables: the row's blocks, of a sequence that was cut the one with
+ * place n among them, whose slot is the next token's, -1 behind them; new_refs: refs less the
+ * blocks given back.  As in pa_blocks_compact, the block in use that entry L / bs
+ * names is the row's too when L is a multiple of the block size: given back where the
+ * sequence is cut, kept otherwise.  A row whose length lies outside its table or
+ * room (PA_STATUS_BAD_SEQLEN) or that names a free block or one outside the pool
+ * (PA_STATUS_BAD_BLOCK, the entry becomes -1) is not cut.
+ * pools: HOST array of n_pools = 2 * layers device pointers, every layer's K and V pool
+ * in turn, described by `cache` with elem_bytes per value; at most 256, read during
+ * the call only.  weights, new_weights: device fp32 [layers, B, Hkv, room]; positions,
+ * new_positions: device int32 alike, as pa_weights_add leaves them.  tables, lens, refs
+ * and their new ones: as for pa_sequences_fork.  Every new array is other memory than
+ * the old one.  1 <= budget, first + recent <= budget; min(room, max_blocks_per_seq *
+ * bs) <= 196608; B <= 65535.  Two launches.
+ */
+int pa_cache_evict(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs, float *new_weights,
+                   int32_t *new_positions, const int32_t *tables, const int32_t *lens,
+                   const int32_t *refs, const float *weights, const int32_t *positions, int64_t room,
+                   int32_t B, int32_t max_blocks_per_seq, void *const *pools, int32_t n_pools,
+                   int32_t elem_bytes, pa_cache_desc cache, int32_t budget, int32_t first,
+                   int32_t recent, int32_t *status, pa_stream_t stream);
+
 /* Static description of a return code. */
 const char *pa_strerror(int code);
 

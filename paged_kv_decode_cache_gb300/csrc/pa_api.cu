@@ -378,6 +378,7 @@ struct PassOpts {
     int32_t part_stride = 0;      // 0: the pass's own partition count
     int32_t part_offset = 0;
     int32_t table_stride = 0;     // 0: max_blocks
+    int32_t row_heads = 0;        // > 0: pa_decode_selected's rows, over pools of so many KV heads
 };
 
 // Scales of FP8 (e4m3) pools: a stored code c means c * scale.
@@ -429,6 +430,9 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
     p.seq_len_const = po.seq_len_const;
     p.seq_len_offset = po.seq_len_offset;
     if (po.table_stride) p.table_stride = po.table_stride;
+    p.row_heads = po.row_heads;
+    pa_cache_desc pool = c;  // as it lies in memory
+    if (po.row_heads) pool.num_kv_heads = po.row_heads;
     if ((po.table_stride || po.seq_len_const >= 0 || po.seq_len_offset || !po.causal ||
          po.part_offset) && k != Kernel::kTensorCore)
         return PA_EUNSUPPORTED;  // cascade passes: tensor cores only
@@ -464,8 +468,8 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
         p.q_per_cta = prefill_positions_per_tile(G);
         p.cluster_merge = 0;
         if (prefill_tiles(G, q_len) * c.num_kv_heads > 65535) return PA_EUNSUPPORTED;
-        rc = make_kv_map_heads(&kmap, k_cache, c, 1);
-        if (!rc) rc = make_kv_map_heads(&vmap, v_cache, c, 1);
+        rc = make_kv_map_heads(&kmap, k_cache, pool, 1);
+        if (!rc) rc = make_kv_map_heads(&vmap, v_cache, pool, 1);
         if (rc) return rc;
         e = pa::launch_prefill_tc(kmap, vmap, p, B, G, rules != nullptr, stream);
     } else if (k == Kernel::kTensorCore) {
@@ -477,21 +481,21 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
             p.scale_log2 = scale * f8->k_scale * 1.4426950408889634f;
             p.v_scale = f8->v_scale;
             p.k_scale = f8->k_scale;
-            rc = make_kv_map_fp8(&kmap, k_cache, c, HC);
-            if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, c, HC);
+            rc = make_kv_map_fp8(&kmap, k_cache, pool, HC);
+            if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, pool, HC);
             if (rc) return rc;
             e = rules ? pa::launch_decode_tc_f8_scored(HC, GP, G, kmap, vmap, p, B, stream)
                       : pa::launch_decode_tc_f8(HC, GP, G, kmap, vmap, p, B, stream);
         } else {
-            rc = make_kv_map_heads(&kmap, k_cache, c, HC);
-            if (!rc) rc = make_kv_map_heads(&vmap, v_cache, c, HC);
+            rc = make_kv_map_heads(&kmap, k_cache, pool, HC);
+            if (!rc) rc = make_kv_map_heads(&vmap, v_cache, pool, HC);
             if (rc) return rc;
             e = rules ? pa::launch_decode_tc_scored(HC, GP, G, kmap, vmap, p, B, stream)
                       : pa::launch_decode_tc(HC, GP, G, kmap, vmap, p, B, stream);
         }
     } else {
-        rc = make_kv_map(&kmap, k_cache, c);
-        if (!rc) rc = make_kv_map(&vmap, v_cache, c);
+        rc = make_kv_map(&kmap, k_cache, pool);
+        if (!rc) rc = make_kv_map(&vmap, v_cache, pool);
         if (rc) return rc;
         e = pa::launch_decode_cc(c.head_dim, G, kmap, vmap, p, B, rules != nullptr, stream);
     }
@@ -775,7 +779,7 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
                    float scale, int32_t num_splits, void *workspace, size_t workspace_bytes,
                    int32_t *status, cudaStream_t stream, const NewTokens &nt, int32_t q_len = 1,
                    const Fp8Scales *f8 = nullptr, bool library_scratch = false,
-                   const pa_score_rules *rules = nullptr) {
+                   const pa_score_rules *rules = nullptr, int32_t row_heads = 0) {
     int rc = check_decode_args(q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                                seq_lens, B, Hq, scale);
     if (rc) return rc;
@@ -783,6 +787,8 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
     if (num_splits < 0 || q_len < 1) return PA_EINVAL;
     if (static_cast<int64_t>(B) * q_len > kMaxRowsQ) return PA_EUNSUPPORTED;
     if (B == 0) return PA_OK;
+    PassOpts po;
+    po.row_heads = row_heads;
     int P = num_splits;
     if (P == 0) {
         const int sms = sm_count_current();
@@ -797,7 +803,7 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
     if (P == 1)
         return run_decode(false, out, lse, nullptr, nullptr, q, k_cache, v_cache, cache,
                           block_tables, max_blocks_per_seq, seq_lens, B, Hq, scale, 1, status,
-                          stream, nullptr, nt, q_len, f8, PassOpts(), rules);
+                          stream, nullptr, nt, q_len, f8, po, rules);
     // rows of the partials: (sequence, query position, head)
     const int32_t Bq = B * q_len;
     const size_t need = pa_splitkv_workspace_bytes(Bq, Hq, cache.head_dim, P);
@@ -819,12 +825,12 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
             return PA_ECUDA;
         rc = run_decode(true, out, lse, part_o, part_lse, q, k_cache, v_cache, cache, block_tables,
                         max_blocks_per_seq, seq_lens, B, Hq, scale, P, status, stream, counters, nt,
-                        q_len, f8, PassOpts(), rules);
+                        q_len, f8, po, rules);
         if (rc != PA_ETOOLARGE) return rc;
     }
     rc = run_decode(true, nullptr, nullptr, part_o, part_lse, q, k_cache, v_cache, cache,
                     block_tables, max_blocks_per_seq, seq_lens, B, Hq, scale, P, status, stream,
-                    nullptr, nt, q_len, f8, PassOpts(), rules);
+                    nullptr, nt, q_len, f8, po, rules);
     if (rc) return rc;
     cudaError_t e = pa::launch_combine(out, lse, part_o, part_lse, static_cast<int>(Bq * Hq), P,
                                        cache.head_dim, stream);
@@ -887,6 +893,46 @@ int pa_decode_scored_fp8(void *out, float *lse, const void *q, int32_t q_len, co
     return splitkv_common(out, lse, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                           seq_lens, B, Hq, scale, num_splits, workspace, workspace_bytes, status,
                           stream, NewTokens(), q_len, &f8, false, rules);
+}
+
+// pa_decode_selected(_fp8): every KV head's list of blocks as a sequence of its own,
+// with one KV head, whose place in the pools the kernels work out from its row.
+static int decode_selected(void *out, float *lse, const void *q, const void *k_cache, const void *v_cache,
+                           const pa_cache_desc &cache, const int32_t *sel_tables, int32_t max_selected,
+                           const int32_t *sel_lens, int32_t B, int32_t Hq, float scale, int32_t num_splits,
+                           void *workspace, size_t workspace_bytes, int32_t *status, cudaStream_t stream,
+                           const Fp8Scales *f8) {
+    const int rc = check_cache_desc(cache);
+    if (rc) return rc;
+    if (B < 0 || Hq <= 0 || Hq % cache.num_kv_heads != 0) return PA_EINVAL;
+    const int64_t rows = static_cast<int64_t>(B) * cache.num_kv_heads;
+    if (rows > kMaxGridZ) return PA_EUNSUPPORTED;
+    pa_cache_desc one = cache;
+    one.num_kv_heads = 1;
+    return splitkv_common(out, lse, q, k_cache, v_cache, one, sel_tables, max_selected, sel_lens,
+                          static_cast<int32_t>(rows), Hq / cache.num_kv_heads, scale, num_splits, workspace,
+                          workspace_bytes, status, stream, NewTokens(), 1, f8, false, nullptr, cache.num_kv_heads);
+}
+
+int pa_decode_selected(void *out, float *lse, const void *q, const void *k_cache, const void *v_cache,
+                       pa_cache_desc cache, const int32_t *sel_tables, int32_t max_selected,
+                       const int32_t *sel_lens, int32_t B, int32_t Hq, float scale, int32_t num_splits,
+                       void *workspace, size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
+    return decode_selected(out, lse, q, k_cache, v_cache, cache, sel_tables, max_selected, sel_lens, B, Hq, scale,
+                           num_splits, workspace, workspace_bytes, status, stream, nullptr);
+}
+
+int pa_decode_selected_fp8(void *out, float *lse, const void *q, const void *k_cache, const void *v_cache,
+                           pa_cache_desc cache, float k_scale, float v_scale, const int32_t *sel_tables,
+                           int32_t max_selected, const int32_t *sel_lens, int32_t B, int32_t Hq, float scale,
+                           int32_t num_splits, void *workspace, size_t workspace_bytes, int32_t *status,
+                           pa_stream_t stream) {
+    if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+        return PA_EINVAL;
+    if (cache.head_dim != 128) return PA_EUNSUPPORTED;
+    const Fp8Scales f8{k_scale, v_scale};
+    return decode_selected(out, lse, q, k_cache, v_cache, cache, sel_tables, max_selected, sel_lens, B, Hq, scale,
+                           num_splits, workspace, workspace_bytes, status, stream, &f8);
 }
 
 int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D,

@@ -34,6 +34,13 @@ struct Library {
     decltype(&::pa_sequences_fork) sequences_fork;
     decltype(&::pa_blocks_compact_slots) blocks_compact_slots;
     decltype(&::pa_blocks_copy) blocks_copy;
+    decltype(&::pa_key_bounds) key_bounds;
+    decltype(&::pa_blocks_select) blocks_select;
+    decltype(&::pa_decode_selected) decode_selected;
+    decltype(&::pa_decode_selected_fp8) decode_selected_fp8;
+    decltype(&::pa_weights_add) weights_add;
+    decltype(&::pa_weights_add_fp8) weights_add_fp8;
+    decltype(&::pa_cache_evict) cache_evict;
     decltype(&::pa_strerror) strerror;
 } g_lib;
 
@@ -56,7 +63,11 @@ PyObject *init(PyObject *, PyObject *args) {
         !find(h, "pa_decode_scored_fp8", &g_lib.decode_scored_fp8) ||
         !find(h, "pa_beam_select", &g_lib.beam_select) || !find(h, "pa_sequences_fork", &g_lib.sequences_fork) ||
         !find(h, "pa_blocks_compact_slots", &g_lib.blocks_compact_slots) || !find(h, "pa_blocks_copy", &g_lib.blocks_copy) ||
-        !find(h, "pa_strerror", &g_lib.strerror))
+        !find(h, "pa_key_bounds", &g_lib.key_bounds) || !find(h, "pa_blocks_select", &g_lib.blocks_select) ||
+        !find(h, "pa_decode_selected", &g_lib.decode_selected) ||
+        !find(h, "pa_decode_selected_fp8", &g_lib.decode_selected_fp8) ||
+        !find(h, "pa_weights_add", &g_lib.weights_add) || !find(h, "pa_weights_add_fp8", &g_lib.weights_add_fp8) ||
+        !find(h, "pa_cache_evict", &g_lib.cache_evict) || !find(h, "pa_strerror", &g_lib.strerror))
         return nullptr;
     for (PyObject *o : {error, raw_stream, current_device, set_device}) Py_INCREF(o);
     g_error = error, g_raw_stream = raw_stream, g_current_device = current_device, g_set_device = set_device;
@@ -545,6 +556,164 @@ PyObject *blocks_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// ---- long contexts ---------------------------------------------------------------------------
+
+float *f32(const Tensor &t) { return static_cast<float *>(t.at); }
+
+// The type of a pool argument: one-byte e4m3 codes, else bf16.
+Type pool_type(PyObject *o) {
+    return THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == c10::ScalarType::Byte ? kU8 : kBf16;
+}
+
+// key_bounds(bounds, k_cache, block_tables, seq_lens, starts, max_new, status, stream)
+PyObject *key_bounds(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count_is(n, 8)) return nullptr;
+    Call c{"pa_key_bounds"};
+    const Type type = pool_type(a[1]);
+    const Tensor kc = take(c, a[1], "k_cache", type, 4), bounds = take(c, a[0], "bounds", type, 4);
+    const Tensor bt = take(c, a[2], "block_tables", kI32, 2), sl = take(c, a[3], "seq_lens", kI32, 1);
+    const Tensor starts = take_optional(c, a[4], "starts", kI32, 1);
+    const int32_t max_new = a[5] == Py_None ? 0 : take_int(c, a[5], "max_new");
+    int32_t *status = take_status(c, a[6]);
+    if (!c.ok) return nullptr;
+    const int64_t B = bt.size[0];
+    c.need(bounds.is({kc.size[0], kc.size[2], 2, kc.size[3]}), "bounds must be [num_blocks, Hkv, 2, D] of k_cache's type") &&
+        c.need(sl.is({B}) && (starts.ndim == 0 || starts.is({B})), "seq_lens and starts must be [B]") &&
+        c.need(a[5] == Py_None || max_new > 0, "max_new must be positive") &&
+        c.need(fits_int({B, bt.size[1], kc.size[0], kc.size[1], kc.size[2]}), "a size is out of range");
+    return run(c, a[7], [&](pa_stream_t s) {
+        return g_lib.key_bounds(bounds.at, kc.at, type == kU8 ? 1 : 2, desc_of(kc), i32(bt), static_cast<int32_t>(bt.size[1]),
+                                i32(sl), i32(starts), max_new, static_cast<int32_t>(B), status, s);
+    });
+}
+
+// blocks_select(sel_tables, sel_lens, q, bounds, block_size, block_tables, seq_lens, first, last, status, stream)
+PyObject *blocks_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count_is(n, 11)) return nullptr;
+    Call c{"pa_blocks_select"};
+    const Type type = pool_type(a[3]);
+    const Tensor q = take(c, a[2], "q", kBf16, 3), bounds = take(c, a[3], "bounds", type, 4);
+    const Tensor st = take(c, a[0], "sel_tables", kI32, 3), sn = take(c, a[1], "sel_lens", kI32, 2);
+    const int32_t bs = take_int(c, a[4], "block_size");
+    const Tensor bt = take(c, a[5], "block_tables", kI32, 2), sl = take(c, a[6], "seq_lens", kI32, 1);
+    const int32_t first = take_int(c, a[7], "first"), last = take_int(c, a[8], "last");
+    int32_t *status = take_status(c, a[9]);
+    if (!c.ok) return nullptr;
+    const int64_t B = q.size[0], hq = q.size[1], d = q.size[2], hkv = bounds.size[1], K = st.size[2];
+    c.need(bounds.is({bounds.size[0], hkv, 2, d}), "bounds must be [num_blocks, Hkv, 2, D] with q's D") &&
+        c.need(st.is({B, hkv, K}) && sn.is({B, hkv}), "sel_tables must be [B, Hkv, K], sel_lens [B, Hkv]") &&
+        c.need(bt.size[0] == B && sl.is({B}), "block_tables and seq_lens must have a row for every query") &&
+        c.need(fits_int({B, hq, hkv, K, bt.size[1], bounds.size[0]}), "a size is out of range");
+    const pa_cache_desc desc{static_cast<int32_t>(bounds.size[0]), bs, static_cast<int32_t>(hkv), static_cast<int32_t>(d)};
+    return run(c, a[10], [&](pa_stream_t s) {
+        return g_lib.blocks_select(i32(st), static_cast<int32_t>(K), i32(sn), q.at, bounds.at, type == kU8 ? 1 : 2, desc, i32(bt),
+                                   static_cast<int32_t>(bt.size[1]), i32(sl), static_cast<int32_t>(B),
+                                   static_cast<int32_t>(hq), first, last, status, s);
+    });
+}
+
+// decode_selected(fp8, out, lse, q, k_cache, v_cache, k_scale, v_scale, sel_tables, sel_lens, scale, num_splits,
+//                 workspace, status, stream)
+PyObject *decode_selected(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count_is(n, 15)) return nullptr;
+    const bool fp8 = a[0] == Py_True;
+    Call c{fp8 ? "pa_decode_selected_fp8" : "pa_decode_selected"};
+    const Tensor q = take(c, a[3], "q", kBf16, 3), out = take(c, a[1], "out", kBf16, 3);
+    const Tensor lse = take_optional(c, a[2], "lse", kF32, 2);
+    const Tensor kc = take(c, a[4], "k_cache", fp8 ? kU8 : kBf16, 4), vc = take(c, a[5], "v_cache", fp8 ? kU8 : kBf16, 4);
+    const float ks = fp8 ? take_float(c, a[6]) : 1.f, vs = fp8 ? take_float(c, a[7]) : 1.f;
+    const Tensor st = take(c, a[8], "sel_tables", kI32, 3), sn = take(c, a[9], "sel_lens", kI32, 2);
+    const float scale = take_float(c, a[10]);
+    const int32_t splits = take_int(c, a[11], "num_splits");
+    size_t bytes = 0;
+    void *space = take_space(c, a[12], &bytes);
+    int32_t *status = take_status(c, a[13]);
+    if (!c.ok) return nullptr;
+    const int64_t B = q.size[0], hq = q.size[1], d = q.size[2], hkv = kc.size[2], K = st.size[2];
+    c.need(out.is({B, hq, d}) && kc.size[3] == d && vc.is({kc.size[0], kc.size[1], hkv, d}), "inconsistent out / q / cache shapes") &&
+        c.need(st.is({B, hkv, K}) && sn.is({B, hkv}), "sel_tables must be [B, Hkv, K], sel_lens [B, Hkv]") &&
+        c.need(lse.ndim == 0 || lse.is({B, hq}), "lse must be [B, Hq]") &&
+        c.need(fits_int({B, hq, K, kc.size[0], kc.size[1], hkv}), "a size is out of range");
+    const int32_t b = static_cast<int32_t>(B), h = static_cast<int32_t>(hq), k = static_cast<int32_t>(K);
+    return run(c, a[14], [&](pa_stream_t s) {
+        return fp8 ? g_lib.decode_selected_fp8(out.at, f32(lse), q.at, kc.at, vc.at, desc_of(kc), ks, vs, i32(st), k, i32(sn),
+                                               b, h, scale, splits, space, bytes, status, s)
+                   : g_lib.decode_selected(out.at, f32(lse), q.at, kc.at, vc.at, desc_of(kc), i32(st), k, i32(sn), b, h, scale,
+                                           splits, space, bytes, status, s);
+    });
+}
+
+// weights_add(fp8, new_weights, weights, positions, q, lse, k_cache, k_scale, block_tables, seq_lens, scale, ends,
+//             decay, status, stream)
+PyObject *weights_add(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count_is(n, 15)) return nullptr;
+    const bool fp8 = a[0] == Py_True;
+    Call c{fp8 ? "pa_weights_add_fp8" : "pa_weights_add"};
+    // q: [B, Hq, D], or [B, q_len, Hq, D]
+    const int nd = THPVariable_Check(a[4]) && THPVariable_Unpack(a[4]).dim() == 4 ? 4 : 3;
+    const Tensor q = take(c, a[4], "q", kBf16, nd), lse = take(c, a[5], "lse", kF32, nd - 1);
+    const Tensor nw = take(c, a[1], "new_weights", kF32, 3), w = take(c, a[2], "weights", kF32, 3);
+    const Tensor pos = take_optional(c, a[3], "positions", kI32, 3);
+    const Tensor kc = take(c, a[6], "k_cache", fp8 ? kU8 : kBf16, 4);
+    const float ks = fp8 ? take_float(c, a[7]) : 1.f;
+    const Tensor bt = take(c, a[8], "block_tables", kI32, 2), sl = take(c, a[9], "seq_lens", kI32, 1);
+    const float scale = take_float(c, a[10]);
+    const Tensor ends = take_optional(c, a[11], "ends", kI32, 1);
+    const float decay = take_float(c, a[12]);
+    int32_t *status = take_status(c, a[13]);
+    if (!c.ok) return nullptr;
+    const int64_t B = q.size[0], q_len = nd == 4 ? q.size[1] : 1, hq = q.size[nd - 2], d = q.size[nd - 1];
+    const int64_t hkv = kc.size[2], room = w.size[2];
+    bool lse_ok = true;
+    for (int i = 0; i < nd - 1; ++i) lse_ok &= lse.size[i] == q.size[i];
+    c.need(lse_ok, "lse must have q's shape without its last dimension") &&
+        c.need(w.is({B, hkv, room}) && nw.is({B, hkv, room}) && (pos.ndim == 0 || pos.is({B, hkv, room})),
+               "weights, new_weights and positions must be [B, Hkv, tokens]") &&
+        c.need(kc.size[3] == d && bt.size[0] == B && sl.is({B}) && (ends.ndim == 0 || ends.is({B})),
+               "inconsistent q / cache / table shapes") &&
+        c.need(fits_int({B, q_len, hq, bt.size[1], kc.size[0], kc.size[1], hkv}), "a size is out of range");
+    const int32_t mb = static_cast<int32_t>(bt.size[1]), b = static_cast<int32_t>(B), h = static_cast<int32_t>(hq);
+    const int32_t ql = static_cast<int32_t>(q_len);
+    return run(c, a[14], [&](pa_stream_t s) {
+        return fp8 ? g_lib.weights_add_fp8(f32(nw), f32(w), i32(pos), q.at, ql, f32(lse), kc.at, desc_of(kc), ks, i32(bt), mb,
+                                           i32(sl), i32(ends), room, b, h, scale, decay, status, s)
+                   : g_lib.weights_add(f32(nw), f32(w), i32(pos), q.at, ql, f32(lse), kc.at, desc_of(kc), i32(bt), mb, i32(sl),
+                                       i32(ends), room, b, h, scale, decay, status, s);
+    });
+}
+
+// cache_evict(new_tables, new_lens, new_refs, new_weights, new_positions, tables, lens, refs, weights, positions, pools,
+//             budget, first, recent, status, stream)
+PyObject *cache_evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!count_is(n, 16)) return nullptr;
+    Call c{"pa_cache_evict"};
+    PoolsNow p;
+    pools_of(c, a[10], &p);
+    const Tensor nt = take(c, a[0], "new_tables", kI32, 2), nl = take(c, a[1], "new_lens", kI32, 1);
+    const Tensor nr = take(c, a[2], "new_refs", kI32, 1);
+    const Tensor nw = take(c, a[3], "new_weights", kF32, 4), np = take(c, a[4], "new_positions", kI32, 4);
+    const Tensor tables = take(c, a[5], "tables", kI32, 2), lens = take(c, a[6], "lens", kI32, 1);
+    const Tensor refs = take(c, a[7], "refs", kI32, 1);
+    const Tensor w = take(c, a[8], "weights", kF32, 4), pos = take(c, a[9], "positions", kI32, 4);
+    const int32_t budget = take_int(c, a[11], "budget"), first = take_int(c, a[12], "first");
+    const int32_t recent = take_int(c, a[13], "recent");
+    int32_t *status = take_status(c, a[14]);
+    if (!c.ok) return nullptr;
+    const int64_t B = tables.size[0], mb = tables.size[1], nb = p.desc.num_blocks, room = w.size[3];
+    c.need(nt.is({B, mb}) && lens.is({B}) && nl.is({B}) && refs.is({nb}) && nr.is({nb}),
+           "tables must be [B, max_blocks], lens [B], counts [num_blocks], the new ones alike") &&
+        c.need(2 * w.size[0] == p.n, "pools must be a K and a V pool for every layer of the weights") &&
+        c.need(w.is({w.size[0], B, p.desc.num_kv_heads, room}) && nw.is({w.size[0], B, p.desc.num_kv_heads, room}) &&
+                   pos.is({w.size[0], B, p.desc.num_kv_heads, room}) && np.is({w.size[0], B, p.desc.num_kv_heads, room}),
+               "weights and positions must be [layers, B, Hkv, tokens], the new ones alike") &&
+        c.need(fits_int({B, mb}), "a size is out of range");
+    return run(c, a[15], [&](pa_stream_t s) {
+        return g_lib.cache_evict(i32(nt), i32(nl), i32(nr), f32(nw), i32(np), i32(tables), i32(lens), i32(refs), f32(w), i32(pos),
+                                 room, static_cast<int32_t>(B), static_cast<int32_t>(mb), p.at, p.n, p.elem_bytes, p.desc, budget,
+                                 first, recent, status, s);
+    });
+}
+
 // A C++ exception (a tensor without storage, for instance) as a Python one.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -569,6 +738,11 @@ PyMethodDef kMethods[] = {{"init", init, METH_VARARGS, nullptr},
                           method<sequences_fork>("sequences_fork"),
                           method<blocks_compact>("blocks_compact"),
                           method<blocks_copy>("blocks_copy"),
+                          method<key_bounds>("key_bounds"),
+                          method<blocks_select>("blocks_select"),
+                          method<decode_selected>("decode_selected"),
+                          method<weights_add>("weights_add"),
+                          method<cache_evict>("cache_evict"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pa_binding", "Calls of libpagedattn with torch tensors.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -105,6 +105,7 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     uint64_t *wbars = bars + warp * NST;
     float *pbuf = pbuf_all + warp * kTile * C::kPG;
     const uint64_t policy = l2_evict_first_policy();
+    const int pool_head = p.row_heads ? b % p.row_heads : g;  // the KV head that is read
 
     auto tile_phys = [&](int j) -> int {  // physical block of this warp's j-th tile
         const int tok0 = real(t_begin + (warp + j * NW) * kTile);
@@ -125,8 +126,8 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         mbar_arrive_expect_tx(&wbars[s], C::kStageBytes);
 #pragma unroll
         for (int sub = 0; sub < C::kSub; ++sub) {
-            tma_load_4d(kt + sub * kTile * kSubBytes, &kmap, 0, sub, g, row0, &wbars[s], policy);
-            tma_load_4d(vt + sub * kTile * kSubBytes, &vmap, 0, sub, g, row0, &wbars[s], policy);
+            tma_load_4d(kt + sub * kTile * kSubBytes, &kmap, 0, sub, pool_head, row0, &wbars[s], policy);
+            tma_load_4d(vt + sub * kTile * kSubBytes, &vmap, 0, sub, pool_head, row0, &wbars[s], policy);
         }
     };
 

@@ -331,7 +331,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         const int ln = threadIdx.x & 31;
         if (ln < kPre * C::kTiles) {
             const int c = ln / C::kTiles, tl = ln % C::kTiles;
-            const int bz = blockIdx.z, hg0 = (blockIdx.y % p.head_groups) * HC;
+            const int bz = blockIdx.z;
+            const int hg0 = p.row_heads ? bz % p.row_heads : static_cast<int>(blockIdx.y % p.head_groups) * HC;
             const int t0 = static_cast<int>(blockIdx.x) * p.chunk;
             int tok = t0 + c * C::kT + tl * kTile;
             const int lp = p.seq_len_const >= 0 ? p.seq_len_const
@@ -371,6 +372,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 
     const int part = blockIdx.x, b = blockIdx.z;
     const int g0 = (blockIdx.y % p.head_groups) * HC;
+    const int pool_head = p.row_heads ? b % p.row_heads : g0;  // the first KV head that is read
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size;
     // This CTA's queries: positions qi0 .. qi0 + nq - 1 of the q_len new ones
@@ -584,13 +586,13 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 __syncwarp();
                 if (valid && sub == 0)
                     tma_load_3d(ring + s * C::kStageBytes + tile * C::kBoxBytes, map, 0,
-                                phys * bs + real(tok0) % bs, g0, &full[s], policy);
+                                phys * bs + real(tok0) % bs, pool_head, &full[s], policy);
             } else {
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(__popc(vm)) * C::kBoxBytes);
                 __syncwarp();
                 if (valid)
                     tma_load_4d(ring + s * C::kStageBytes + sub * C::kSubTile + tile * C::kBoxBytes, map, 0,
-                                phys * bs + real(tok0) % bs, g0, sub, &full[s], policy);
+                                phys * bs + real(tok0) % bs, pool_head, sub, &full[s], policy);
             }
             issued = c + 1;
         }

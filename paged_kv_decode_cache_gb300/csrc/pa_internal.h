@@ -95,6 +95,9 @@ struct DecodeParams {
     int32_t window;
     const int32_t *prefix_lens;
     int32_t max_prefix;
+    // pa_decode_selected: > 0 where a "sequence" b is one KV head's own list of
+    // blocks (num_kv_heads is 1): it reads KV head b % row_heads of the pools.
+    int32_t row_heads;
 };
 
 // CUDA-core decode kernel launch (pa_decode_cc_d*.cu).  Returns a cudaError_t.

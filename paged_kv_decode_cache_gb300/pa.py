@@ -127,6 +127,19 @@ _SIGNATURES = {
     "pa_decode_scored_fp8": ([_P, _P, _P, _I32, _P, _P, CacheDesc, _F32, _F32, _P, _I32, _P, _I32, _I32,
                               _F32, _P, _I32, _P, _SZ, _P, _P], ctypes.c_int),
     "pa_scored_num_splits": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], ctypes.c_int),
+    "pa_key_bounds": ([_P, _P, _I32, CacheDesc, _P, _I32, _P, _P, _I32, _I32, _P, _P], ctypes.c_int),
+    "pa_blocks_select": ([_P, _I32, _P, _P, _P, _I32, CacheDesc, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _P],
+                         ctypes.c_int),
+    "pa_decode_selected": ([_P, _P, _P, _P, _P, CacheDesc, _P, _I32, _P, _I32, _I32, _F32, _I32, _P, _SZ, _P, _P],
+                           ctypes.c_int),
+    "pa_decode_selected_fp8": ([_P, _P, _P, _P, _P, CacheDesc, _F32, _F32, _P, _I32, _P, _I32, _I32, _F32, _I32, _P,
+                                _SZ, _P, _P], ctypes.c_int),
+    "pa_weights_add": ([_P, _P, _P, _P, _I32, _P, _P, CacheDesc, _P, _I32, _P, _P, _I64, _I32, _I32, _F32, _F32, _P, _P],
+                       ctypes.c_int),
+    "pa_weights_add_fp8": ([_P, _P, _P, _P, _I32, _P, _P, CacheDesc, _F32, _P, _I32, _P, _P, _I64, _I32, _I32, _F32, _F32,
+                            _P, _P], ctypes.c_int),
+    "pa_cache_evict": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _I32, _I32, CacheDesc, _I32, _I32,
+                        _I32, _P, _P], ctypes.c_int),
     "pa_set_option": ([_I32, _I32], ctypes.c_int),
     "pa_get_option": ([_I32], ctypes.c_int),
     "pa_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -745,3 +758,62 @@ def pa_decode_scored_fp8(out, lse, q, k_cache, v_cache, k_scale, v_scale, block_
     (_native or _binding()).decode_scored(True, out, lse, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
                                           scale, softcap, alibi_slopes, window, prefix_lens, max_prefix, num_splits,
                                           workspace, status, stream)
+
+
+# ---------------------------------------------------------------------------------------------
+# Long contexts: blocks selected by a cheap score, tokens evicted by the weight they drew.
+
+
+def pa_key_bounds(bounds, k_cache, block_tables, seq_lens, starts=None, max_new=None, status=None, stream=None):
+    """Every channel's least and largest key of the blocks with tokens [starts, seq_lens) (default: all of
+    them): bounds [num_blocks, Hkv, 2, D] of k_cache's type (bf16, or uint8 e4m3 codes).  max_new: a bound on
+    seq_lens - starts (default: the table's tokens)."""
+    (_native or _binding()).key_bounds(bounds, k_cache, block_tables, seq_lens, starts, max_new, status, stream)
+
+
+def pa_blocks_select(sel_tables, sel_lens, q, bounds, block_size, block_tables, seq_lens, first=1, last=1, status=None,
+                     stream=None):
+    """For every sequence and KV head its first and last blocks and those whose bounds promise the query most:
+    sel_tables [B, Hkv, K] (their ids in order, -1 behind them), sel_lens [B, Hkv] (their tokens)."""
+    (_native or _binding()).blocks_select(sel_tables, sel_lens, q, bounds, block_size, block_tables, seq_lens, first, last,
+                                          status, stream)
+
+
+def pa_decode_selected(out, lse, q, k_cache, v_cache, sel_tables, sel_lens, scale, num_splits=0, workspace=None,
+                       status=None, stream=None):
+    """Split-KV decode in which every KV head reads its own blocks: sel_tables [B, Hkv, K], sel_lens [B, Hkv]."""
+    (_native or _binding()).decode_selected(False, out, lse, q, k_cache, v_cache, None, None, sel_tables, sel_lens, scale,
+                                            num_splits, workspace, status, stream)
+
+
+def pa_decode_selected_fp8(out, lse, q, k_cache, v_cache, k_scale, v_scale, sel_tables, sel_lens, scale, num_splits=0,
+                           workspace=None, status=None, stream=None):
+    """pa_decode_selected over uint8 e4m3 pools with per-pool scales."""
+    (_native or _binding()).decode_selected(True, out, lse, q, k_cache, v_cache, k_scale, v_scale, sel_tables, sel_lens,
+                                            scale, num_splits, workspace, status, stream)
+
+
+def pa_weights_add(new_weights, weights, positions, q, lse, k_cache, block_tables, seq_lens, scale, ends=None, decay=1.0,
+                   status=None, stream=None):
+    """new_weights = decay * weights + the attention weight that every cached token draws from q ([B, Hq, D], or
+    [B, q_len, Hq, D]) with the lse that attention gave: [B, Hkv, tokens] fp32 (new_weights may be weights); the
+    q_len newest tokens start from nothing, and get their positions (int32 [B, Hkv, tokens], or None) from ends
+    (int32 [B], tokens so far, default seq_lens)."""
+    (_native or _binding()).weights_add(False, new_weights, weights, positions, q, lse, k_cache, None, block_tables,
+                                        seq_lens, scale, ends, decay, status, stream)
+
+
+def pa_weights_add_fp8(new_weights, weights, positions, q, lse, k_cache, k_scale, block_tables, seq_lens, scale, ends=None,
+                       decay=1.0, status=None, stream=None):
+    """pa_weights_add over a uint8 e4m3 pool."""
+    (_native or _binding()).weights_add(True, new_weights, weights, positions, q, lse, k_cache, k_scale, block_tables,
+                                        seq_lens, scale, ends, decay, status, stream)
+
+
+def pa_cache_evict(new_tables, new_lens, new_refs, new_weights, new_positions, tables, lens, refs, weights, positions,
+                   pools, budget, first=0, recent=0, status=None, stream=None):
+    """Cut sequences longer than budget to it: of every layer and KV head the tokens at the first `first` positions,
+    the `recent` newest and the heaviest others stay.  weights, positions [layers, B, Hkv, tokens]; pools: a PoolSet
+    of every layer's K and V pool in turn, whose rows are moved in place."""
+    (_native or _binding()).cache_evict(new_tables, new_lens, new_refs, new_weights, new_positions, tables, lens, refs,
+                                        weights, positions, _pools_of(pools), budget, first, recent, status, stream)
