@@ -809,15 +809,16 @@ int pa_key_bounds(void *bounds, const void *k_cache, int32_t elem_bytes, pa_cach
  * and the block's score is the largest of these over the group's heads.  Of every
  * sequence and KV head the first `first` blocks, the last `last` ones (the newest
  * token's among them) and, of the others, those with the largest scores are taken, up
- * to max_selected (K) in all, ties to the earlier block.  Scores are compared as 64-bit
- * sums; a scale, or the scale of FP8 pools, would not change their order.  A block
+ * to max_selected (K) in all, ties to the earlier block.  Scores are compared as sums
+ * of 45 bits or more (of 64-bit floats where products leave fp32's range), so only blocks
+ * that are alike to that tie; a scale, or that of FP8 pools, would not change their order.  A block
  * whose bounds hold an infinity or a NaN counts as larger than any finite score, as does
  * every block for a group of queries with one; a block id outside the pool counts as
  * the smallest and sets PA_STATUS_BAD_BLOCK.
  * sel_tables: device int32 [B, Hkv, K], the chosen blocks' physical ids in the order of
  * the sequence, -1 behind them; sel_lens: device int32 [B, Hkv], the tokens they hold of
  * the sequence.  q: device bf16 [B, Hq, D].  bounds, elem_bytes: as pa_key_bounds
- * leaves them.  1 <= last, first + last <= K; Hq / Hkv <= 32; max_blocks_per_seq <= 98304.
+ * leaves them.  1 <= last, first + last <= K; Hq / Hkv <= 32; max_blocks_per_seq <= 40960.
  */
 int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_lens, const void *q,
                      const void *bounds, int32_t elem_bytes, pa_cache_desc cache,

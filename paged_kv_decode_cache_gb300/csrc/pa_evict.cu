@@ -94,10 +94,6 @@ __global__ void __launch_bounds__(kLensThreads) evict_lens_kernel(const __grid_c
     for (int j = tid; j < a.max_blocks; j += kLensThreads) out[j] = j < min(stay, n_used) ? used_entry(a, row, j) : j < stay ? next : -1;
 }
 
-__device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // Rows src[p] -> dst[p] (places of this head in both pools of a layer) for the `count` pairs of this
 // warp, lane p's own; kChunks: 16-byte chunks of a row, kLanes / kChunks rows at once.
 template <int kChunks>
@@ -133,7 +129,7 @@ __device__ __forceinline__ void move_rows(uint8_t *k_pool, uint8_t *v_pool, int 
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint8_t evict_smem[];
     TopkShared &sh = *reinterpret_cast<TopkShared *>(evict_smem);
-    uint32_t *keys = reinterpret_cast<uint32_t *>(evict_smem + (sizeof(TopkShared) + 15) / 16 * 16);
+    uint32_t *keys = reinterpret_cast<uint32_t *>(evict_smem + kTopkSharedBytes);
     int32_t *holes = reinterpret_cast<int32_t *>(keys + a.slice);   // this CTA's pairs: [slice / 2] free places
     int32_t *movers = holes + a.slice / 2;                          // ... and the tokens that take them
     __shared__ int past_s;
@@ -186,11 +182,11 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_co
     }
     __syncthreads();
 
-    uint32_t need;
-    const uint32_t border =
-        cluster_threshold<uint32_t, kEvictThreads>([&](int i) { return keys[i]; }, mine, n, C, sh, true, &need);
+    const Border edge = cluster_threshold<kEvictThreads>([&](int i) { return keys[i]; }, mine, n, 0u, kSafe - 1u, C, sh, 0u);
+    const uint32_t border = edge.lo, need = edge.m == edge.inside ? ~0u : edge.m;
 
-    // ---- which tokens stay: those above the border, and the first `need` at it.  Every warp's share is contiguous.
+    // ---- which tokens stay: those above the border (or all from it on: none then counts as at it, or every one
+    // does), and the first `need` at it.  Every warp's share is contiguous.
     const int share = ((mine + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
     const int i0 = min(warp * share, mine), i1 = min(i0 + share, mine);
     uint32_t counts[4] = {0, 0, 0, 0}, before[4], total[4];  // above, at the border; the same below n
@@ -243,7 +239,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_co
     }
 }
 
-size_t evict_smem_bytes(int slice) { return (sizeof(TopkShared) + 15) / 16 * 16 + static_cast<size_t>(slice) * 8; }
+size_t evict_smem_bytes(int slice) { return kTopkSharedBytes + static_cast<size_t>(slice) * 8; }
 
 }  // namespace
 }  // namespace pa

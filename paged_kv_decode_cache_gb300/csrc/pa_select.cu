@@ -174,20 +174,23 @@ struct SelectArgs {
     int32_t *status;
     int32_t num_blocks, block_size, Hkv, G, max_blocks, K, first, last;
     int32_t ctas;            // of a cluster: a row of blocks
-    int32_t slice;           // blocks of a CTA, at most
+    int32_t room;            // keys in shared memory: blocks of a row, at most
 };
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelCtas = 8;              // portable cluster size
-constexpr int kSelMaxSlice = 12288;
+constexpr int kSelMaxBlocks = 40960;     // of a sequence: their keys in one CTA's shared memory
+constexpr uint32_t kSelFew = 32;         // the search for the border ends with so many keys near it
+constexpr int kSelList = 256;            // blocks near the border that are scored again at once
 constexpr uint32_t kForced = 0xffffffffu;   // keys above every finite score's: blocks that are always taken ...
 constexpr uint32_t kEndless = 0xfffffffeu;  // ... and blocks (or queries) with an infinity or a NaN
 constexpr uint32_t kFirstFinite = 0x00800000u, kPastFinite = 0xff800000u;
-// Of the sum of a score's |terms|, the error that its fp32 sum on tensor cores may have: 16
-// MMAs, each adding 16 exact products to the sum after aligning all 17 to the largest,
-// which cuts off at most 2^-23 of it from each.  16 * 17 * 2^-23 < 2^-14.
-constexpr float kScoreError = 6.103515625e-05f;
+// Of the sum of a score's |terms|, the error that its fp32 sum on tensor cores may have: 4
+// sums of at most 4 MMAs, each adding 16 exact products to the sum after aligning all 17 to
+// the largest, which cuts off at most 2^-23 of it from each, and 3 additions: 4 * 17 * 2^-23 +
+// 2^-22 < 2^-16.
+constexpr float kScoreError = 1.52587890625e-05f;
 constexpr float kScoreFloor = 1e-35f;  // what products and sums below fp32's normal range lose, at most
 
 // [min(q, 0), max(q, 0)] at channel x of 2 D.
@@ -195,64 +198,79 @@ __device__ __forceinline__ uint32_t signed_part(uint32_t q, bool upper) {
     return (q >> 15 != 0) != upper ? q : 0u;
 }
 
-// The score of block `phys` for KV head h in 64 bits, by one warp: the largest over the
-// query heads, of which those that a sum in fp32 puts more than 2 * err below the best one
-// are left out.
+// a + b = s + e, exactly.
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+    s = __fadd_rn(a, b);
+    const float t = __fsub_rn(s, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+
+// The score of block `phys` for KV head h by one warp, as an ordered key: a sum in two fp32
+// halves (products of bf16 are exact in fp32; such a sum keeps 45 bits and more), or, with
+// `wide`, in 64 bits, for products that fp32's range does not hold (fp64 runs at a 64th of
+// the rate).
 template <bool F8, int D>
-__device__ double score64(const SelectArgs &a, const uint16_t *q, int phys, int h, float err, int lane) {
-    constexpr int kPer = D / 32;
-    const int d0 = lane * kPer;
-    float lo[kPer], hi[kPer];
+__device__ uint64_t exact_score(const SelectArgs &a, const float *q, int phys, int h, bool wide, int lane) {
+    constexpr int kPer = D / 32;  // channels of a lane
     const uint8_t *row = a.bounds + (static_cast<int64_t>(phys) * a.Hkv + h) * 2 * D * (F8 ? 1 : 2);
+    float x[2][kPer];  // lo, hi
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if constexpr (F8) {
-            lo[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(row[d0 + i], __NV_E4M3)));
-            hi[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(row[D + d0 + i], __NV_E4M3)));
-        } else {
-            const uint16_t *r = reinterpret_cast<const uint16_t *>(row);
-            lo[i] = __uint_as_float(static_cast<uint32_t>(r[d0 + i]) << 16);
-            hi[i] = __uint_as_float(static_cast<uint32_t>(r[D + d0 + i]) << 16);
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+            uint32_t w;
+            if constexpr (F8) w = e4m3x2_to_bf16x2(*reinterpret_cast<const uint16_t *>(row + s * D + lane * kPer + i));
+            else w = *reinterpret_cast<const uint32_t *>(row + 2 * (s * D + lane * kPer + i));
+            x[s][i] = bf16lo(w), x[s][i + 1] = bf16hi(w);
         }
     }
-    float best = -INFINITY;
-    for (int pass = 0; pass < 2; ++pass) {
+    if (wide) {
         double top = -INFINITY;
         for (int g = 0; g < a.G; ++g) {
-            float f[kPer], s = 0.f;
+            double t = 0.0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                f[i] = __uint_as_float(static_cast<uint32_t>(q[g * D + d0 + i]) << 16);
-                s += fmaxf(f[i] * lo[i], f[i] * hi[i]);
+                const float f = q[g * D + lane * kPer + i];
+                t += static_cast<double>(f) * static_cast<double>(f < 0.f ? x[0][i] : x[1][i]);
             }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (pass == 0) {
-                best = fmaxf(best, s);
-            } else if (!(s < best - 2.f * err)) {  // (an overflow keeps every head)
-                double t = 0.0;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const float x = f[i] < 0.f ? lo[i] : hi[i];
-                    t += static_cast<double>(f[i]) * static_cast<double>(x);
-                }
-#pragma unroll
-                for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                top = t > top ? t : top;
-            }
+            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            top = t > top ? t : top;
         }
-        if (pass == 1) return top;
+        return double_key(top);
     }
-    return 0.0;
+    float top_s = -INFINITY, top_e = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < a.G; ++g) {
+        float s = 0.f, e = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float f = q[g * D + lane * kPer + i];
+            float r;
+            two_sum(s, __fmul_rn(f, f < 0.f ? x[0][i] : x[1][i]), s, r);
+            e = __fadd_rn(e, r);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
+            float r;
+            two_sum(s, s2, s, r);
+            e = __fadd_rn(__fadd_rn(e, e2), r);
+        }
+        two_sum(s, e, s, e);
+        if (s > top_s || (s == top_s && e > top_e)) top_s = s, top_e = e;
+    }
+    return double_key(static_cast<double>(top_s) + static_cast<double>(top_e));
 }
 
 // A cluster per (sequence, KV head), a range of its blocks per CTA.  Each warp scores 16
-// blocks at a time from registers; the scores stay in shared memory as ordered keys
-// and the cluster finds the K-th largest (pa_topk.cuh).  A sum in fp32 does not tell
-// neighbours apart that differ by less than its error, so blocks that the border may lie
-// among (usually none or one) are scored again in 64 bits: what is chosen is what
-// the 64-bit scores choose.  Bound by memory where a context is long (the bounds are read
-// once), by the chain of loads, meetings and passes where it is short.
+// blocks at a time from registers and stores the scores, as ordered keys, in the first
+// CTA's shared memory; the other CTAs leave, and that one finds the K-th largest
+// (pa_topk.cuh) and writes the list.  (A search by all eight meets once a pass, 0.7 us, and
+// took 15 of 48 us for 1025 blocks.)  A sum in fp32 does not tell neighbours apart that
+// differ by less than its error, so blocks that the border may lie among (a few) are
+// scored again, exactly for all that matters.  Bound by memory where a context is long (the
+// bounds are read once), by the chain of loads, meetings and passes where it is short.
 template <bool F8, int D>
 __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const SelectArgs a) {
     constexpr int kRowBytes = 2 * D * (F8 ? 1 : 2);
@@ -261,13 +279,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     extern __shared__ __align__(16) uint8_t sel_smem[];
     TopkShared &sh = *reinterpret_cast<TopkShared *>(sel_smem);
     const int tiles = (a.G + 7) / 8;                    // of 8 query heads
-    uint4 *qs = reinterpret_cast<uint4 *>(sel_smem + (sizeof(TopkShared) + 15) / 16 * 16);  // [tiles][kVecs][32 lanes]
-    uint64_t *wide = reinterpret_cast<uint64_t *>(qs + tiles * kVecs * 32);                 // [slice] 64-bit keys
-    uint32_t *keys = reinterpret_cast<uint32_t *>(wide + a.slice);                          // [slice]
-    uint16_t *list = reinterpret_cast<uint16_t *>(keys + a.slice);                          // [slice] whose they are
-    __shared__ uint32_t largest_s;   // of the finite bounds, as a float's bits
-    __shared__ float qsum_s[32];     // sum of |q| of every head, -1 where one is not finite
-    __shared__ uint32_t n_wide_s;
+    uint4 *qs = reinterpret_cast<uint4 *>(sel_smem + kTopkSharedBytes);   // [tiles][kVecs][32 lanes]: the MMA's columns
+    float *qf = reinterpret_cast<float *>(qs + tiles * kVecs * 32);       // [G][D]
+    uint32_t *keys = reinterpret_cast<uint32_t *>(qf + a.G * D);          // [room], the first CTA's
+    __shared__ uint64_t wide_s[kSelList];       // blocks near the border: their exact scores as ordered keys,
+    __shared__ int32_t list_s[kSelList], id_s[kSelList];  // which they are, their ids
+    __shared__ uint32_t window_s[4], largest_s; // the first CTA's: finite keys' least, largest, number; marks; largest bound
+    __shared__ float qsum_s[32];                // sum of |q| of every head, -1 where one is not finite
+    __shared__ uint32_t n_near_s, n_in_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int C = a.ctas, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int h = blockIdx.y, b = blockIdx.z, bs = a.block_size;
@@ -285,20 +304,44 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     const int64_t row = static_cast<int64_t>(b) * a.Hkv + h;
     int32_t *out = a.sel_tables + row * a.K;
     if (tid == 0 && rank == 0) a.sel_lens[row] = n <= a.K ? L : (a.K - 1) * bs + L - (n - 1) * bs;
-    auto entry = [&](int j) {
-        const int id = bt[j];
-        const bool ok = id >= 0 && id < a.num_blocks;
-        if (!ok && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-        return id;
-    };
     if (n <= a.K) {  // all of them
-        for (int j = rank * kSelThreads + tid; j < a.K; j += C * kSelThreads) out[j] = j < n ? entry(j) : -1;
+        for (int j = rank * kSelThreads + tid; j < a.K; j += C * kSelThreads) {
+            const int id = j < n ? bt[j] : -1;
+            if (j < n && (id < 0 || id >= a.num_blocks) && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+            out[j] = id;
+        }
         return;
     }
-    const int per = ((n + C - 1) / C + 15) / 16 * 16;
-    const int j0 = min(rank * per, n), j1 = min(j0 + per, n), mine = j1 - j0;
+    if (tid == 0) window_s[0] = ~0u, window_s[1] = window_s[2] = window_s[3] = largest_s = 0u, n_near_s = n_in_s = 0u;
+    for (int i = tid; i < kTopkBins; i += kSelThreads) sh.hist[0][i] = 0;
+    if (C > 1) cluster_arrive();  // (every CTA has started and set these up before any stores to another's)
 
-    // ---- the queries as the MMA's columns, the sums of their |values|
+    // ---- a warp's tiles of 16 blocks: ids a tile ahead, the first tile's bounds on their way
+    const int per = ((n + C - 1) / C + 15) / 16 * 16;
+    const int j0 = min(rank * per, n), j1 = min(j0 + per, n);
+    const int n_tiles = (j1 - j0 + 15) / 16;
+    int next_id = lane < 16 && j0 + warp * 16 + lane < j1 ? bt[j0 + warp * 16 + lane] : -1;
+    uint4 raw[2][kChunks];  // rows g and g + 8
+    uint32_t ok = 0u;       // the tile's rows that are there
+    auto load = [&](int tile) {
+        const int id = next_id, j = j0 + tile * 16 + (lane & 15);
+        const bool fits = id >= 0 && id < a.num_blocks, here = lane < 16 && j < j1;
+        if (here && !fits && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+        ok = __ballot_sync(0xffffffffu, here && fits);
+        const int jn = j + kSelWarps * 16;
+        next_id = lane < 16 && jn < j1 ? bt[jn] : -1;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int phys = __shfl_sync(0xffffffffu, id, g + 8 * r);
+            const bool there = (ok >> (g + 8 * r)) & 1u;
+            const uint8_t *at = a.bounds + (static_cast<int64_t>(there ? phys : 0) * a.Hkv + h) * kRowBytes + 16 * t;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) raw[r][c] = there ? load_once(at + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    if (warp < n_tiles) load(warp);
+
+    // ---- the queries as the MMA's columns, their values, the sums of their |values|
     const uint16_t *q = a.q + row * a.G * D;
     for (int i = tid; i < tiles * kVecs * 32; i += kSelThreads) {
         const int ln = i & 31, v = (i >> 5) % kVecs, head = (i >> 5) / kVecs * 8 + (ln >> 2);
@@ -315,18 +358,23 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     for (int head = warp; head < a.G; head += kSelWarps) {
         float s = 0.f;
         bool fine = true;
-        for (int i = lane; i < D; i += 32) {
-            const uint32_t u = q[head * D + i] & 0x7fffu;
-            fine = fine && u < 0x7f80u;
-            s += __uint_as_float(u << 16);
+#pragma unroll
+        for (int i = 2 * lane; i < D; i += 64) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(q + head * D + i);
+            const float x = bf16lo(w), y = bf16hi(w);
+            qf[head * D + i] = x, qf[head * D + i + 1] = y;
+            fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
+            s += fabsf(x) + fabsf(y);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         fine = __all_sync(0xffffffffu, fine);
         if (lane == 0) qsum_s[head] = fine ? s : -1.f;
     }
-    if (tid == 0) largest_s = 0u, n_wide_s = 0u;
+    if (C > 1) cluster_wait();
     __syncthreads();
+    auto first = [&](void *p) { return C > 1 ? map_shared_rank(smem_u32(p), 0) : smem_u32(p); };  // in the first CTA
+    const uint32_t keys0 = first(keys);
     float qsum = 0.f;
     bool q_fine = true;
     for (int i = 0; i < a.G; ++i) {
@@ -335,27 +383,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     }
 
     // ---- scores
-    uint32_t largest = 0u;
-    const int n_tiles = (mine + 15) / 16;
-    int next = -1;
-    if (warp < n_tiles && lane < 16 && j0 + warp * 16 + lane < j1) next = bt[j0 + warp * 16 + lane];
+    uint32_t largest = 0u, w_lo = ~0u, w_hi = 0u, w_in = 0u, w_above = 0u;
     for (int tile = warp; tile < n_tiles; tile += kSelWarps) {
-        const int id = next, j_lane = j0 + tile * 16 + (lane & 15);
-        const bool id_ok = lane < 16 && j_lane < j1 && id >= 0 && id < a.num_blocks;
-        if (lane < 16 && j_lane < j1 && !id_ok && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-        const uint32_t ok = __ballot_sync(0xffffffffu, id_ok);
-        const int jn = j_lane + kSelWarps * 16;
-        next = lane < 16 && jn < j1 ? bt[jn] : -1;
-        uint4 raw[2][kChunks];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int phys = __shfl_sync(0xffffffffu, id, g + 8 * r);
-            const bool there = (ok >> (g + 8 * r)) & 1u;
-            const uint8_t *at = a.bounds + (static_cast<int64_t>(there ? phys : 0) * a.Hkv + h) * kRowBytes + 16 * t;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) raw[r][c] = there ? load_once(at + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        uint32_t top[2] = {0u, 0u};  // largest |bound| of rows g and g + 8, per 16 (FP8: 8) bits
+        uint32_t top[2] = {0u, 0u};  // largest |bound| of the rows, per 16 (FP8: 8) bits
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -367,7 +397,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             }
         float best[2] = {-INFINITY, -INFINITY};
         for (int nt = 0; nt < tiles; ++nt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float part[4][4] = {}, acc[4];  // (four sums: shorter chains, and a quarter of the error)
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 uint4 x[Chunk<F8>::kVecs], y[Chunk<F8>::kVecs];
@@ -375,11 +405,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
                 widen<F8>(raw[1][c], y);
 #pragma unroll
                 for (int k = 0; k < Chunk<F8>::kVecs; ++k) {
-                    const uint4 w = qs[(nt * kVecs + c * Chunk<F8>::kVecs + k) * 32 + lane];
-                    mma_16x8x16(acc, x[k].x, y[k].x, x[k].y, y[k].y, w.x, w.y);
-                    mma_16x8x16(acc, x[k].z, y[k].z, x[k].w, y[k].w, w.z, w.w);
+                    const int v = c * Chunk<F8>::kVecs + k;
+                    const uint4 w = qs[(nt * kVecs + v) * 32 + lane];
+                    mma_16x8x16(part[2 * v & 3], x[k].x, y[k].x, x[k].y, y[k].y, w.x, w.y);
+                    mma_16x8x16(part[(2 * v + 1) & 3], x[k].z, y[k].z, x[k].w, y[k].w, w.z, w.w);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (nt * 8 + 2 * t + i < a.G) {
@@ -389,6 +422,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
                 }
             }
         }
+        const uint32_t there = ok;
+        if (tile + kSelWarps < n_tiles) load(tile + kSelWarps);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float s = best[r];
@@ -401,15 +436,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             }
             m = F8 ? max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24)) : max(m & 0xffffu, m >> 16);
             const bool fine = q_fine && m < (F8 ? 0x7fu : 0x7f80u);
-            const int i = tile * 16 + g + 8 * r, j = j0 + i;
+            const int j = j0 + tile * 16 + g + 8 * r;
             if (t == 0 && j < j1) {
                 uint32_t key;
                 if (j < a.first || j >= n - a.last) key = kForced;
-                else if (!((ok >> (g + 8 * r)) & 1u)) key = 0u;
+                else if (!((there >> (g + 8 * r)) & 1u)) key = 0u;
                 else if (!fine) key = kEndless;
                 else key = float_key(fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f));
-                keys[i] = key;
-                if (fine && key != kForced) {
+                if (C > 1) st_shared_cluster_u32(keys0 + 4 * j, key);
+                else keys[j] = key;
+                if (key >= kPastFinite) {
+                    ++w_above;
+                } else if (key) {
+                    ++w_in, w_lo = min(w_lo, key), w_hi = max(w_hi, key);
                     const uint32_t f = F8 ? __float_as_uint(__half2float(__half(
                                                 __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(m), __NV_E4M3))))
                                           : m << 16;
@@ -419,78 +458,128 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
         }
     }
     largest = __reduce_max_sync(0xffffffffu, largest);
-    if (lane == 0) atomicMax(&largest_s, largest);
+    w_lo = __reduce_min_sync(0xffffffffu, w_lo), w_hi = __reduce_max_sync(0xffffffffu, w_hi);
+    w_in = __reduce_add_sync(0xffffffffu, w_in), w_above = __reduce_add_sync(0xffffffffu, w_above);
+    if (lane == 0) {
+        const uint32_t w0 = first(window_s);
+        min_shared_cluster_u32(w0, w_lo), max_shared_cluster_u32(w0 + 4, w_hi);
+        add_shared_cluster_u32(w0 + 8, w_in), add_shared_cluster_u32(w0 + 12, w_above);
+        max_shared_cluster_u32(first(&largest_s), largest);
+    }
+    if (C > 1) {
+        cluster_arrive();
+        if (rank != 0) return;
+        cluster_wait();
+    }
     __syncthreads();
 
-    // ---- the border
-    const uint32_t m = a.K;
-    uint32_t need;
-    uint32_t border = cluster_threshold<uint32_t, kSelThreads>([&](int i) { return keys[i]; }, mine, m, C, sh, false, &need);
-    uint32_t before[2], total[2];
-    uint32_t past = border, tie = border;  // taken: keys above `past`, and the first `need` of those equal to `tie`
-    if (border >= kFirstFinite && border < kPastFinite) {
-        if (C > 1)
-            for (int r = 0; r < C; ++r)
-                largest = max(r ? largest : 0u, ld_shared_cluster_u32(map_shared_rank(smem_u32(&largest_s), r)));
-        else
-            largest = largest_s;
-        // every score is within err of its 64-bit one, and so is the border: what is more than
-        // 2 err from it is decided
-        const float err = fmaxf(kScoreError * qsum * __uint_as_float(largest), kScoreFloor);
-        if (qsum > 0.f && largest != 0u) {  // (else every score is 0, exactly)
-            const float at = key_float(border);
-            const uint32_t low = max(float_key(__fadd_rd(at, -2.f * err)), kFirstFinite);
-            const uint32_t high = min(float_key(__fadd_ru(at, 2.f * err)), kPastFinite - 1u);
-            uint32_t sides[2] = {0, 0};
-            for (int i = tid; i < mine; i += kSelThreads) {
+    // ---- the border, by the first CTA: taken are the keys above `to` and, of those from `from` to `to`, the first `need`
+    largest = largest_s;
+    auto key_at = [&](int i) { return keys[i]; };
+    Border w = border_of(a.K, kFirstFinite, kPastFinite - 1u, window_s[0], window_s[1], window_s[2], window_s[3]);
+    // (among the marks, and where every finite score is 0, keys are exact)
+    const bool plain = w.lo >= kPastFinite || w.hi < kFirstFinite || !(qsum > 0.f && largest != 0u);
+    w = cluster_narrow<kSelThreads>(key_at, n, w, 1, sh, plain ? 0u : kSelFew);
+    uint32_t from = w.lo, to = w.hi, need = w.m == w.inside ? ~0u : w.m;
+    if (!plain) {
+        // every score is within err of its exact one, and so is the border: what is more than
+        // 2 err from where the border may be is decided
+        const float size = qsum * __uint_as_float(largest), err = fmaxf(kScoreError * size, kScoreFloor);
+        const bool wide = !(size < 1e30f && size > 1e-18f);
+        if (need == ~0u) to = from;  // (all from there on are the K largest: the border is at the least of them)
+        uint32_t n_near, n_in;
+        for (;;) {
+            const uint32_t low = max(float_key(__fadd_rd(key_float(from), -2.f * err)), kFirstFinite);
+            const uint32_t high = min(float_key(__fadd_ru(key_float(to), 2.f * err)), kPastFinite - 1u);
+            uint32_t in = 0;
+            for (int i = tid; i < n; i += kSelThreads) {
                 const uint32_t k = keys[i];
-                sides[0] += k > high, sides[1] += k >= low && k <= high;
+                in += k > high;
+                if (k >= low && k <= high) {
+                    const uint32_t p = atomicAdd(&n_near_s, 1u);
+                    if (p < kSelList) list_s[p] = i, id_s[p] = bt[i];
+                }
             }
-            cluster_counts<kSelThreads>(sides, C, sh, 0, before, total);
-            if (total[1] == m - total[0]) {
-                past = low - 1u, tie = 1u;  // (no key is 1)
-            } else {
-                // scored again, a warp per block
-                for (int i0 = warp * 32; i0 < mine; i0 += kSelThreads) {
-                    const uint32_t k = i0 + lane < mine ? keys[i0 + lane] : 0u;
-                    uint32_t near = __ballot_sync(0xffffffffu, k >= low && k <= high);
-                    for (; near; near &= near - 1) {
-                        const int i = i0 + __ffs(near) - 1;
-                        const double s = score64<F8, D>(a, q, bt[j0 + i], h, err, lane);
-                        if (lane == 0) {
-                            const uint32_t p = atomicAdd(&n_wide_s, 1u);
-                            wide[p] = double_key(s), list[p] = static_cast<uint16_t>(i);
-                        }
+            __syncwarp();
+            in = __reduce_add_sync(0xffffffffu, in);
+            if (lane == 0 && in) atomicAdd(&n_in_s, in);
+            __syncthreads();
+            n_near = n_near_s, n_in = n_in_s;
+            if (from == to || n_near <= kSelList || n_near + n_in == a.K) {
+                from = low, to = high;
+                break;
+            }
+            for (int i = tid; i < kTopkBins; i += kSelThreads) sh.hist[0][i] = 0;
+            __syncthreads();
+            if (tid == 0) n_near_s = n_in_s = 0u;
+            w = cluster_narrow<kSelThreads>(key_at, n, w, 1, sh, 0u);
+            from = to = w.lo;  // (the K-th largest key, or a bound of those that are all taken)
+            __syncthreads();
+        }
+        need = a.K - n_in;
+        if (n_near == need) {
+            need = ~0u;  // all of them
+        } else if (n_near <= kSelList) {  // a warp per block, then ranked
+            for (uint32_t p = warp; p < n_near; p += kSelWarps) {
+                const uint64_t s = exact_score<F8, D>(a, qf, id_s[p], h, wide, lane);
+                if (lane == 0) wide_s[p] = s;
+            }
+            __syncthreads();
+            for (uint32_t p = tid; p < n_near; p += kSelThreads) {
+                uint32_t better = 0;
+                for (uint32_t o = 0; o < n_near; ++o)
+                    better += wide_s[o] > wide_s[p] || (wide_s[o] == wide_s[p] && list_s[o] < list_s[p]);
+                keys[list_s[p]] = better < need ? kForced : 0u;
+            }
+            need = 0u;
+            __syncthreads();
+        } else {
+            // too many (hundreds of blocks that are nearly alike): 31 bits of their exact scores at a time
+            const uint64_t last = double_key(static_cast<double>(key_float(to)) + 2.0 * err);
+            uint64_t base = double_key(static_cast<double>(key_float(from)) - 2.0 * err);
+            uint64_t span = last - base;
+            for (;;) {
+                const int shift = max(0, 64 - __clzll(static_cast<long long>(span)) - 31);
+                for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {
+                    const int i = i0 + lane;
+                    const uint32_t k = i < n ? keys[i] : 0u;
+                    uint32_t now = k > to ? kForced : 0u;
+                    for (uint32_t near = __ballot_sync(0xffffffffu, i < n && k >= from && k <= to); near; near &= near - 1) {
+                        const int j = __ffs(near) - 1;
+                        const uint64_t s = exact_score<F8, D>(a, qf, bt[i0 + j], h, wide, lane);
+                        const uint64_t off = s < base ? 0u : min(s - base, span);
+                        if (lane == j) now = static_cast<uint32_t>(off >> shift) + 1u;
                     }
+                    if (i < n) keys[i] = now;
                 }
                 __syncthreads();
-                const int n_wide = static_cast<int>(n_wide_s);
-                const uint64_t edge = cluster_threshold<uint64_t, kSelThreads>([&](int p) { return wide[p]; }, n_wide,
-                                                                               m - total[0], C, sh, false, &need);
-                for (int p = tid; p < n_wide; p += kSelThreads)
-                    keys[list[p]] = wide[p] > edge ? kForced : wide[p] == edge ? 1u : 0u;
-                past = high, tie = 1u;
+                w = cluster_threshold<kSelThreads>(key_at, n, a.K, 1u, kForced - 1u, 1, sh, 0u);
+                from = w.lo, to = w.hi, need = w.m == w.inside ? ~0u : w.m;
+                if (need == ~0u || shift == 0) break;
+                base += static_cast<uint64_t>(from - 1u) << shift;
+                span = (uint64_t(1) << shift) - 1u;
                 __syncthreads();
             }
         }
     }
 
-    // ---- the chosen blocks in their order: every warp's share of the range is contiguous
-    const int share = ((mine + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int i0 = min(warp * share, mine), i1 = min(i0 + share, mine);
-    uint32_t taken[2] = {0, 0};
-    for (int i = i0 + lane; i < i1; i += 32) taken[0] += keys[i] > past, taken[1] += keys[i] <= past && keys[i] == tie;
-    cluster_counts<kSelThreads>(taken, C, sh, 1, before, total);
+    // ---- the chosen blocks in their order: every warp's share of the row is contiguous
+    const int share = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    const int i0 = min(warp * share, n), i1 = min(i0 + share, n);
+    uint32_t taken[2] = {0, 0}, before[2], total[2];
+    for (int i = i0 + lane; i < i1; i += 32) taken[0] += keys[i] > to, taken[1] += keys[i] >= from && keys[i] <= to;
+    __syncwarp();
+    cluster_counts<kSelThreads>(taken, 1, sh, 1, before, total);
     for (int i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
-        const bool in = i + lane < i1 && k > past, even = i + lane < i1 && !in && k == tie;
+        const bool here = i + lane < i1;
+        const uint32_t k = here ? keys[i + lane] : 0u;
+        const bool in = here && k > to, even = here && k >= from && k <= to;
         const uint32_t ins = __ballot_sync(0xffffffffu, in), evens = __ballot_sync(0xffffffffu, even);
         const uint32_t below = (1u << lane) - 1u;
         const uint32_t tied = before[1] + __popc(evens & below);
-        if (in || (even && tied < need)) out[before[0] + __popc(ins & below) + min(tied, need)] = bt[j0 + i + lane];
+        if (in || (even && tied < need)) out[before[0] + __popc(ins & below) + min(tied, need)] = bt[i + lane];
         before[0] += __popc(ins), before[1] += __popc(evens);
     }
-    meet(C);  // (the others may still read this CTA's counts)
 }
 
 int bounds_slices(int row_chunks, int block_size) {
@@ -499,9 +588,9 @@ int bounds_slices(int row_chunks, int block_size) {
     return s;
 }
 
-size_t select_smem(bool f8, int D, int G, int slice) {
-    return (sizeof(TopkShared) + 15) / 16 * 16 + static_cast<size_t>((G + 7) / 8) * (2 * D / 32) * 32 * 16 +
-           static_cast<size_t>(slice) * 14;
+size_t select_smem(int D, int G, int room) {
+    return kTopkSharedBytes + static_cast<size_t>((G + 7) / 8) * (2 * D / 32) * 32 * 16 + static_cast<size_t>(G) * D * 4 +
+           static_cast<size_t>(room) * 4;
 }
 
 template <bool F8, int D>
@@ -514,12 +603,12 @@ cudaError_t launch_select(SelectArgs &a, int B, cudaStream_t stream) {
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(select_smem(F8, D, 32, kSelMaxSlice)));
+                                 static_cast<int>(select_smem(D, 32, kSelMaxBlocks)));
         if (e != cudaSuccess) return e;
         smem_attr_done.fetch_or(bit, std::memory_order_release);
     }
     return launch_clustered(kern, dim3(a.ctas, a.Hkv, B), a.ctas, kSelThreads,
-                            static_cast<int>(select_smem(F8, D, a.G, a.slice)), stream, pdl_on(), a);
+                            static_cast<int>(select_smem(D, a.G, a.room)), stream, pdl_on(), a);
 }
 
 }  // namespace
@@ -571,7 +660,7 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
     if (static_cast<int64_t>(max_blocks_per_seq) * cache.block_size > INT32_MAX / 2 ||
         static_cast<int64_t>(max_selected) * cache.block_size > INT32_MAX / 2)
         return PA_EUNSUPPORTED;
-    if (max_blocks_per_seq > pa::kSelCtas * pa::kSelMaxSlice) return PA_EUNSUPPORTED;
+    if (max_blocks_per_seq > pa::kSelMaxBlocks) return PA_EUNSUPPORTED;
     if (B == 0) return PA_OK;
     if (!sel_tables || !sel_lens || !q || !bounds || !block_tables || !seq_lens) return PA_EINVAL;
     if (!pa::is_aligned(q, 16) || !pa::is_aligned(bounds, 16) || !pa::is_aligned(sel_tables, 4) ||
@@ -583,8 +672,13 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
     a.bounds = static_cast<const uint8_t *>(bounds), a.tables = block_tables, a.lens = seq_lens, a.status = status;
     a.num_blocks = cache.num_blocks, a.block_size = cache.block_size, a.Hkv = cache.num_kv_heads;
     a.G = Hq / cache.num_kv_heads, a.max_blocks = max_blocks_per_seq, a.K = max_selected, a.first = first, a.last = last;
+    // a cluster of eight per row, or of fewer where those would not all be resident at once
+    const int sms = pa::sm_count();
+    if (sms <= 0) return PA_ECUDA;
+    const int64_t rows = static_cast<int64_t>(B) * cache.num_kv_heads;
     a.ctas = pa::kSelCtas;
-    a.slice = ((max_blocks_per_seq + a.ctas - 1) / a.ctas + 15) / 16 * 16;
+    while (a.ctas > 1 && rows * a.ctas > 2 * sms) a.ctas /= 2;
+    a.room = max_blocks_per_seq;
     cudaError_t e;
     if (elem_bytes == 1)
         e = cache.head_dim == 128 ? pa::launch_select<true, 128>(a, B, stream) : pa::launch_select<true, 64>(a, B, stream);

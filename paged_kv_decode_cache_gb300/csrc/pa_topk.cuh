@@ -2,12 +2,14 @@
 // pa_blocks_select and pa_cache_evict: a row's keys are spread over the cluster's
 // shared memory, a contiguous range per CTA, and stay there.
 //
-// cluster_threshold finds the m-th largest key by narrowing a range of key values: each
+// cluster_narrow finds the m-th largest key by narrowing a range of key values: each
 // pass counts the keys of the range in 2048 equal bins (shared-memory atomics in every
 // CTA, the counts added up through distributed shared memory) and keeps the bin that
 // holds the border.  The range starts at the keys' own least and largest, so keys of
 // one sign and a few exponents are split finely by the first pass; 32-bit keys take at
-// most 3 passes, 64-bit ones 6.
+// most 3.  A round trip through distributed shared memory costs most of a pass: every
+// thread has all its loads of one in flight at once (one after the other, 7 CTAs'
+// counts took 4 us a pass).
 #pragma once
 
 #include "pa_device.cuh"
@@ -36,10 +38,17 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ uint64_t ld_shared_cluster_u64(uint32_t addr) {
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void max_shared_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void min_shared_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_shared_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_cluster_v4(uint32_t addr) {
     uint4 v;
@@ -58,67 +67,44 @@ __device__ __forceinline__ void meet(int C) {
 
 struct TopkShared {
     alignas(16) uint32_t hist[2][kTopkBins];
-    alignas(16) uint64_t range[2];   // this CTA's least and largest key
-    uint64_t warp_lo[32], warp_hi[32];
+    alignas(16) uint32_t range[4];   // this CTA's least and largest key of the window, its keys above it and in it
     uint32_t warp_sum[32];
     uint32_t found[3];               // bin, keys above it, keys in it
     uint32_t warp_count[32][4];
     alignas(16) uint32_t count[2][4];  // this CTA's counts of cluster_counts
 };
+constexpr size_t kTopkSharedBytes = (sizeof(TopkShared) + 15) / 16 * 16;
+constexpr int kTopkCtas = 8;  // of a cluster, at most (a portable size)
 
-// The m-th largest (1 <= m <= their number) of the keys key(i), i in [0, n), of the
-// cluster's C CTAs; *need: how many of the keys equal to it are among the m largest.
-// With `any`, a value between it and the next smaller key will do (and *need counts
-// every key equal to it).  Every thread of the cluster calls it; `sh` lies at the same
-// offset of every CTA's shared memory.  The caller meets the cluster before the CTAs'
-// `sh` is used again or a CTA leaves.
-template <typename Key, int kThreads, typename F>
-__device__ Key cluster_threshold(F key, int n, uint32_t m, int C, TopkShared &sh, bool any, uint32_t *need) {
-    constexpr int kWarps = kThreads / 32;
+// Four values of every CTA of the cluster, at the same place of its shared memory: lane r of
+// each warp gets CTA r's (lanes from C on: zeros).
+__device__ __forceinline__ uint4 gather4(const uint32_t (&mine)[4], int C, int lane) {
+    if (C == 1) return lane == 0 ? *reinterpret_cast<const uint4 *>(mine) : make_uint4(0u, 0u, 0u, 0u);
+    return lane < C ? ld_shared_cluster_v4(map_shared_rank(smem_u32(mine), lane)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// The keys from lo to hi, `inside` of them in all, that hold the m-th largest of them.
+struct Border {
+    uint32_t lo, hi, inside, m;
+};
+
+// The m-th largest of the keys key(i), i in [0, n), of the cluster's C CTAs lies in `w`: narrowed until
+// it is one value (lo = hi), or all keys in it are among the m largest (m = inside), or there are at most
+// `few`.  Every thread of the cluster calls it; `sh` lies at the same offset of every CTA's shared
+// memory, its hist[0] is zero and the cluster has met since; it meets again before sh.hist is used again.
+template <int kThreads, typename F>
+__device__ Border cluster_narrow(F key, int n, Border w, int C, TopkShared &sh, uint32_t few) {
     constexpr int kPer = kTopkBins / kThreads;  // bins of a thread
     static_assert(kPer >= 4 && kPer % 4 == 0, "bins");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Key lo = ~Key(0), hi = 0;
-    for (int i = tid; i < n; i += kThreads) {
-        const Key k = key(i);
-        lo = k < lo ? k : lo;
-        hi = k > hi ? k : hi;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const Key a = __shfl_xor_sync(0xffffffffu, lo, d), b = __shfl_xor_sync(0xffffffffu, hi, d);
-        lo = a < lo ? a : lo;
-        hi = b > hi ? b : hi;
-    }
-    if (lane == 0) sh.warp_lo[warp] = lo, sh.warp_hi[warp] = hi;
-    for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[0][i] = 0;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) {
-            lo = sh.warp_lo[w] < lo ? static_cast<Key>(sh.warp_lo[w]) : lo;
-            hi = sh.warp_hi[w] > hi ? static_cast<Key>(sh.warp_hi[w]) : hi;
-        }
-        sh.range[0] = lo, sh.range[1] = hi;
-    }
-    meet(C);
-    lo = static_cast<Key>(sh.range[0]), hi = static_cast<Key>(sh.range[1]);
-    if (C > 1) {
-        for (int r = 0; r < C; ++r) {
-            const uint32_t at = map_shared_rank(smem_u32(sh.range), r);
-            const Key a = static_cast<Key>(ld_shared_cluster_u64(at)), b = static_cast<Key>(ld_shared_cluster_u64(at + 8));
-            lo = a < lo ? a : lo;
-            hi = b > hi ? b : hi;
-        }
-    }
     int buf = 0;
-    while (lo != hi) {
-        const Key span = hi - lo;
-        const int bits = sizeof(Key) == 8 ? 64 - __clzll(static_cast<long long>(span)) : 32 - __clz(static_cast<int>(span));
-        const int shift = bits > kTopkBits ? bits - kTopkBits : 0;
+    while (w.lo != w.hi && w.m != w.inside && w.inside > few) {
+        const uint32_t span = w.hi - w.lo;
+        const int shift = max(0, 32 - __clz(static_cast<int>(span)) - kTopkBits);
         for (int i = tid; i - lane < n; i += kThreads) {  // (whole warps)
-            const Key k = i < n ? key(i) : Key(0);
-            const bool in = i < n && k >= lo && k <= hi;
-            const uint32_t bin = static_cast<uint32_t>((k - lo) >> shift);
+            const uint32_t k = i < n ? key(i) : 0u;
+            const bool in = i < n && k >= w.lo && k <= w.hi;
+            const uint32_t bin = (k - w.lo) >> shift;
             // a warp's keys in one bin, as many equal ones are: one addition
             const uint32_t act = __ballot_sync(0xffffffffu, in);
             if (!act) continue;
@@ -138,10 +124,12 @@ __device__ Key cluster_threshold(F key, int n, uint32_t m, int C, TopkShared &sh
             uint4 v = *reinterpret_cast<const uint4 *>(&sh.hist[buf][bin0 + j]);
             if (C > 1) {
                 const uint32_t at = smem_u32(&sh.hist[buf][bin0 + j]), me = cluster_ctarank();
-                for (int r = 1; r < C; ++r) {
-                    const uint4 u = ld_shared_cluster_v4(map_shared_rank(at, (me + r) % C));
-                    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-                }
+                uint4 u[kTopkCtas - 1];
+#pragma unroll
+                for (int r = 1; r < kTopkCtas; ++r)
+                    u[r - 1] = r < C ? ld_shared_cluster_v4(map_shared_rank(at, (me + r) % C)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int r = 0; r < kTopkCtas - 1; ++r) v.x += u[r].x, v.y += u[r].y, v.z += u[r].z, v.w += u[r].w;
             }
             cnt[j] = v.x, cnt[j + 1] = v.y, cnt[j + 2] = v.z, cnt[j + 3] = v.w;
         }
@@ -156,31 +144,66 @@ __device__ Key cluster_threshold(F key, int n, uint32_t m, int C, TopkShared &sh
         if (lane == 31) sh.warp_sum[warp] = upto;
         for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[buf ^ 1][i] = 0;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += sh.warp_sum[w];
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0u);
         uint32_t above = upto - sum;
-        if (above < m && m <= upto) {
+        if (above < w.m && w.m <= upto) {
 #pragma unroll
             for (int j = kPer - 1; j >= 0; --j) {
-                if (above < m && m <= above + cnt[j]) {
-                    sh.found[0] = bin0 + j, sh.found[1] = above, sh.found[2] = cnt[j];
-                }
+                if (above < w.m && w.m <= above + cnt[j]) sh.found[0] = bin0 + j, sh.found[1] = above, sh.found[2] = cnt[j];
                 above += cnt[j];
             }
         }
         __syncthreads();
-        const Key from = lo + (static_cast<Key>(sh.found[0]) << shift);
-        const Key width = (Key(1) << shift) - 1;
-        m -= sh.found[1];
-        if (any && m == sh.found[2]) {  // the whole bin
-            *need = ~0u;
-            return from;
-        }
-        hi = hi - from < width ? hi : from + width;
-        lo = from;
+        w.lo += sh.found[0] << shift;
+        w.hi = min(w.hi - w.lo, (1u << shift) - 1u) + w.lo;
+        w.m -= sh.found[1], w.inside = sh.found[2];
         buf ^= 1;
     }
-    *need = m;
-    return lo;
+    return w;
+}
+
+// Which keys hold the m-th largest (1 <= m <= their number) of all: those in the window [low, high], where
+// most lie, those above it or those below.  `least`, `most`, `n_in`: of the keys in the window, the
+// least, the largest and their number, `n_above`: the number of those above it.
+__device__ __forceinline__ Border border_of(uint32_t m, uint32_t low, uint32_t high, uint32_t least, uint32_t most,
+                                            uint32_t n_in, uint32_t n_above) {
+    if (m <= n_above) return Border{high + 1u, ~0u, n_above, m};
+    if (m <= n_above + n_in) return Border{least, most, n_in, m - n_above};
+    return Border{0u, low - 1u, ~0u, m - n_above - n_in};
+}
+
+// The border of the m largest among the keys of all the cluster's CTAs, narrowed.  The CTA meets before
+// this (keys and `sh` are its threads' to use) and the cluster before `sh` is used again.
+template <int kThreads, typename F>
+__device__ Border cluster_threshold(F key, int n, uint32_t m, uint32_t low, uint32_t high, int C, TopkShared &sh, uint32_t few) {
+    constexpr int kWarps = kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t lo = ~0u, hi = 0u, n_above = 0u, n_in = 0u;
+    for (int i = tid; i < n; i += kThreads) {
+        const uint32_t k = key(i);
+        const bool in = k >= low && k <= high;
+        lo = in ? min(lo, k) : lo;
+        hi = in ? max(hi, k) : hi;
+        n_above += k > high, n_in += in;
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+    n_above = __reduce_add_sync(0xffffffffu, n_above), n_in = __reduce_add_sync(0xffffffffu, n_in);
+    if (lane == 0) sh.warp_count[warp][0] = lo, sh.warp_count[warp][1] = hi, sh.warp_count[warp][2] = n_above, sh.warp_count[warp][3] = n_in;
+    for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[0][i] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        const bool w = lane < kWarps;
+        lo = __reduce_min_sync(0xffffffffu, w ? sh.warp_count[lane][0] : ~0u);
+        hi = __reduce_max_sync(0xffffffffu, w ? sh.warp_count[lane][1] : 0u);
+        n_above = __reduce_add_sync(0xffffffffu, w ? sh.warp_count[lane][2] : 0u);
+        n_in = __reduce_add_sync(0xffffffffu, w ? sh.warp_count[lane][3] : 0u);
+        if (lane == 0) sh.range[0] = lo, sh.range[1] = hi, sh.range[2] = n_above, sh.range[3] = n_in;
+    }
+    meet(C);
+    const uint4 r = gather4(sh.range, C, lane);
+    lo = __reduce_min_sync(0xffffffffu, lane < C ? r.x : ~0u), hi = __reduce_max_sync(0xffffffffu, r.y);
+    n_above = __reduce_add_sync(0xffffffffu, r.z), n_in = __reduce_add_sync(0xffffffffu, r.w);
+    return cluster_narrow<kThreads>(key, n, border_of(m, low, high, lo, hi, n_in, n_above), C, sh, few);
 }
 
 // Sums of N counts over the cluster's CTAs: *total, and over the CTAs of lower rank and this CTA's
@@ -190,6 +213,7 @@ template <int kThreads, int N>
 __device__ void cluster_counts(const uint32_t (&v)[N], int C, TopkShared &sh, int slot, uint32_t (&before)[N],
                                uint32_t (&total)[N]) {
     static_assert(N <= 4, "counts");
+    constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t mine[N];
 #pragma unroll
@@ -199,28 +223,22 @@ __device__ void cluster_counts(const uint32_t (&v)[N], int C, TopkShared &sh, in
 #pragma unroll
         for (int i = 0; i < N; ++i) sh.warp_count[warp][i] = mine[i];
     __syncthreads();
-    if (tid < N) {
-        uint32_t s = 0;
-        for (int w = 0; w < kThreads / 32; ++w) s += sh.warp_count[w][tid];
-        sh.count[slot][tid] = s;
+    if (warp == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t s = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_count[lane][i] : 0u);
+            if (lane == i) sh.count[slot][i] = s;
+        }
     }
     meet(C);
     const int me = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const uint4 q = gather4(sh.count[slot], C, lane);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < N; ++i) before[i] = total[i] = 0;
-    for (int r = 0; r < C; ++r) {
-        const uint4 q = C > 1 ? ld_shared_cluster_v4(map_shared_rank(smem_u32(sh.count[slot]), r))
-                              : *reinterpret_cast<const uint4 *>(sh.count[slot]);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (r < me) before[i] += u[i];
-            total[i] += u[i];
-        }
+    for (int i = 0; i < N; ++i) {
+        total[i] = __reduce_add_sync(0xffffffffu, u[i]);
+        before[i] = __reduce_add_sync(0xffffffffu, (lane < me ? u[i] : 0u) + (lane < warp ? sh.warp_count[lane][i] : 0u));
     }
-    for (int w = 0; w < warp; ++w)
-#pragma unroll
-        for (int i = 0; i < N; ++i) before[i] += sh.warp_count[w][i];
 }
 
 }  // namespace pa

@@ -305,7 +305,7 @@ def test_bounds_refusals(kw, code):
     (dict(first=-1), pa.PA_EINVAL), (dict(last=0), pa.PA_EINVAL), (dict(first=5, last=4), pa.PA_EINVAL),
     (dict(first=2 ** 31 - 1, last=2), pa.PA_EINVAL), (dict(q=None), pa.PA_EINVAL), (dict(q=(1 << 20) + 8), pa.PA_EINVAL),
     (dict(Hq=5), pa.PA_EINVAL), (dict(Hq=66), pa.PA_EUNSUPPORTED), (dict(desc=pa.CacheDesc(64, 16, 2, 96)), pa.PA_EUNSUPPORTED),
-    (dict(mb=98305), pa.PA_EUNSUPPORTED), (dict(B=70000), pa.PA_EUNSUPPORTED), (dict(B=0, q=None), pa.PA_OK),
+    (dict(mb=40961), pa.PA_EUNSUPPORTED), (dict(B=70000), pa.PA_EUNSUPPORTED), (dict(B=0, q=None), pa.PA_OK),
 ])
 def test_select_refusals(kw, code):
     a = dict(K=8, q=FAKE, elem=2, desc=DESC, mb=7, B=4, Hq=4, first=1, last=1) | kw
