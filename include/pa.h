@@ -874,7 +874,8 @@ int pa_weights_add(float *new_weights, const float *weights, int32_t *positions,
                    const int32_t *seq_lens, const int32_t *ends, int64_t room, int32_t B,
                    int32_t Hq, float scale, float decay, int32_t *status, pa_stream_t stream);
 
-/* pa_weights_add over an FP8 pool: K = e4m3(code) * k_scale. */
+/* pa_weights_add over an FP8 pool: K = e4m3(code) * k_scale (q is rounded to fp16, as in
+ * pa_decode_splitkv_fp8: |q| must stay below 65504). */
 int pa_weights_add_fp8(float *new_weights, const float *weights, int32_t *positions, const void *q,
                        int32_t q_len, const float *lse, const void *k_cache, pa_cache_desc cache,
                        float k_scale, const int32_t *block_tables, int32_t max_blocks_per_seq,

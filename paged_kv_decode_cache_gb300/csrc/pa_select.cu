@@ -193,9 +193,18 @@ constexpr uint32_t kFirstFinite = 0x00800000u, kPastFinite = 0xff800000u;
 constexpr float kScoreError = 1.52587890625e-05f;
 constexpr float kScoreFloor = 1e-35f;  // what products and sums below fp32's normal range lose, at most
 
-// [min(q, 0), max(q, 0)] at channel x of 2 D.
-__device__ __forceinline__ uint32_t signed_part(uint32_t q, bool upper) {
-    return (q >> 15 != 0) != upper ? q : 0u;
+// The larger |values| of three pairs of 16-bit ones (bf16, or fp16 for FP8 pools); a NaN stays.
+template <bool F8>
+__device__ __forceinline__ uint32_t largest2(uint32_t m, uint32_t u, uint32_t v) {
+    if constexpr (F8) {
+        const __half2 a = __habs2(*reinterpret_cast<__half2 *>(&u)), b = __habs2(*reinterpret_cast<__half2 *>(&v));
+        const __half2 r = __hmax2_nan(__hmax2_nan(*reinterpret_cast<__half2 *>(&m), a), b);
+        return *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const __nv_bfloat162 a = __habs2(*reinterpret_cast<__nv_bfloat162 *>(&u)), b = __habs2(*reinterpret_cast<__nv_bfloat162 *>(&v));
+        const __nv_bfloat162 r = __hmax2_nan(__hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&m), a), b);
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
 }
 
 // a + b = s + e, exactly.
@@ -218,10 +227,13 @@ __device__ uint64_t exact_score(const SelectArgs &a, const float *q, int phys, i
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
         for (int i = 0; i < kPer; i += 2) {
-            uint32_t w;
-            if constexpr (F8) w = e4m3x2_to_bf16x2(*reinterpret_cast<const uint16_t *>(row + s * D + lane * kPer + i));
-            else w = *reinterpret_cast<const uint32_t *>(row + 2 * (s * D + lane * kPer + i));
-            x[s][i] = bf16lo(w), x[s][i + 1] = bf16hi(w);
+            if constexpr (F8) {
+                const float2 f = f16x2_values(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(row + s * D + lane * kPer + i)));
+                x[s][i] = f.x, x[s][i + 1] = f.y;
+            } else {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(row + 2 * (s * D + lane * kPer + i));
+                x[s][i] = bf16lo(w), x[s][i + 1] = bf16hi(w);
+            }
         }
     }
     if (wide) {
@@ -285,7 +297,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     __shared__ uint64_t wide_s[kSelList];       // blocks near the border: their exact scores as ordered keys,
     __shared__ int32_t list_s[kSelList], id_s[kSelList];  // which they are, their ids
     __shared__ uint32_t window_s[4], largest_s; // the first CTA's: finite keys' least, largest, number; marks; largest bound
-    __shared__ float qsum_s[32];                // sum of |q| of every head, -1 where one is not finite
+    __shared__ float qsum_s[32], qmax_s[32];    // sum of |q| of every head, -1 where one is not finite; the largest
     __shared__ uint32_t n_near_s, n_in_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int C = a.ctas, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -321,138 +333,150 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     const int j0 = min(rank * per, n), j1 = min(j0 + per, n);
     const int n_tiles = (j1 - j0 + 15) / 16;
     int next_id = lane < 16 && j0 + warp * 16 + lane < j1 ? bt[j0 + warp * 16 + lane] : -1;
-    uint4 raw[2][kChunks];  // rows g and g + 8
-    uint32_t ok = 0u;       // the tile's rows that are there
-    auto load = [&](int tile) {
+    constexpr int kSlots = 8 / kChunks;  // tiles on their way: 64 registers
+    uint4 raw[kSlots][2][kChunks];       // rows g and g + 8
+    uint32_t ok[kSlots];                 // the tiles' rows that are there
+    auto load = [&](int tile, uint4(&k)[2][kChunks], uint32_t &there_all) {
         const int id = next_id, j = j0 + tile * 16 + (lane & 15);
         const bool fits = id >= 0 && id < a.num_blocks, here = lane < 16 && j < j1;
         if (here && !fits && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-        ok = __ballot_sync(0xffffffffu, here && fits);
+        there_all = __ballot_sync(0xffffffffu, here && fits);
         const int jn = j + kSelWarps * 16;
         next_id = lane < 16 && jn < j1 ? bt[jn] : -1;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int phys = __shfl_sync(0xffffffffu, id, g + 8 * r);
-            const bool there = (ok >> (g + 8 * r)) & 1u;
+            const bool there = (there_all >> (g + 8 * r)) & 1u;
             const uint8_t *at = a.bounds + (static_cast<int64_t>(there ? phys : 0) * a.Hkv + h) * kRowBytes + 16 * t;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) raw[r][c] = there ? load_once(at + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < kChunks; ++c) k[r][c] = there ? load_once(at + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-    if (warp < n_tiles) load(warp);
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) load(warp + s * kSelWarps, raw[s], ok[s]);
 
-    // ---- the queries as the MMA's columns, their values, the sums of their |values|
+    // ---- the queries: their values, the sums of their |values|, and the MMA's columns
     const uint16_t *q = a.q + row * a.G * D;
-    for (int i = tid; i < tiles * kVecs * 32; i += kSelThreads) {
-        const int ln = i & 31, v = (i >> 5) % kVecs, head = (i >> 5) / kVecs * 8 + (ln >> 2);
-        const int x = vec_dim<F8>(v, ln & 3);
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (head < a.G) {
-            const uint4 in = *reinterpret_cast<const uint4 *>(q + head * D + x % D);
-            const bool up = x >= D;
-            auto both = [&](uint32_t u) { return signed_part(u & 0xffffu, up) | signed_part(u >> 16, up) << 16; };
-            w = make_uint4(both(in.x), both(in.y), both(in.z), both(in.w));
-        }
-        qs[i] = w;
-    }
     for (int head = warp; head < a.G; head += kSelWarps) {
-        float s = 0.f;
+        float s = 0.f, m = 0.f;
         bool fine = true;
 #pragma unroll
         for (int i = 2 * lane; i < D; i += 64) {
             const uint32_t w = *reinterpret_cast<const uint32_t *>(q + head * D + i);
             const float x = bf16lo(w), y = bf16hi(w);
-            qf[head * D + i] = x, qf[head * D + i + 1] = y;
+            *reinterpret_cast<float2 *>(qf + head * D + i) = make_float2(x, y);
             fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
-            s += fabsf(x) + fabsf(y);
+            s += fabsf(x) + fabsf(y), m = fmaxf(m, fmaxf(fabsf(x), fabsf(y)));
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = 16; o; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
         fine = __all_sync(0xffffffffu, fine);
-        if (lane == 0) qsum_s[head] = fine ? s : -1.f;
+        if (lane == 0) qsum_s[head] = fine ? s : -1.f, qmax_s[head] = m;
+    }
+    __syncthreads();
+    float qsum = 0.f, qmax = 0.f;
+    bool q_fine = true;
+    for (int i = 0; i < a.G; ++i) {
+        q_fine = q_fine && qsum_s[i] >= 0.f;
+        qsum = fmaxf(qsum, qsum_s[i]), qmax = fmaxf(qmax, qmax_s[i]);
+    }
+    // FP8: the columns are fp16, the queries scaled by a power of two so that the largest is below
+    // 2^15 and not below 2^14; what that cuts off small ones is below 2^-39 of the largest
+    const int shift = F8 && qmax > 0.f && q_fine ? 14 - ilogbf(qmax) : 0;
+    for (int i = tid; i < tiles * kVecs * 32; i += kSelThreads) {
+        const int ln = i & 31, v = (i >> 5) % kVecs, head = (i >> 5) / kVecs * 8 + (ln >> 2);
+        const int x = vec_dim<F8>(v, ln & 3);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (head < a.G) {
+            const float *f = qf + head * D + x % D;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float u = x >= D ? fmaxf(f[2 * k], 0.f) : fminf(f[2 * k], 0.f);
+                const float y = x >= D ? fmaxf(f[2 * k + 1], 0.f) : fminf(f[2 * k + 1], 0.f);
+                if constexpr (F8) {
+                    w[k] = to_f16x2(scalbnf(u, shift), scalbnf(y, shift));
+                } else {  // (the values are bf16)
+                    w[k] = __float_as_uint(u) >> 16 | (__float_as_uint(y) & 0xffff0000u);
+                }
+            }
+        }
+        qs[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (C > 1) cluster_wait();
     __syncthreads();
     auto first = [&](void *p) { return C > 1 ? map_shared_rank(smem_u32(p), 0) : smem_u32(p); };  // in the first CTA
     const uint32_t keys0 = first(keys);
-    float qsum = 0.f;
-    bool q_fine = true;
-    for (int i = 0; i < a.G; ++i) {
-        q_fine = q_fine && qsum_s[i] >= 0.f;
-        qsum = fmaxf(qsum, qsum_s[i]);
-    }
 
     // ---- scores
     uint32_t largest = 0u, w_lo = ~0u, w_hi = 0u, w_in = 0u, w_above = 0u;
-    for (int tile = warp; tile < n_tiles; tile += kSelWarps) {
-        uint32_t top[2] = {0u, 0u};  // largest |bound| of the rows, per 16 (FP8: 8) bits
+    for (int tile0 = warp; tile0 < n_tiles; tile0 += kSlots * kSelWarps) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int slot = 0; slot < kSlots; ++slot) {
+            const int tile = tile0 + slot * kSelWarps;
+            if (tile >= n_tiles) break;
+            uint32_t top[2] = {0u, 0u};  // largest |bound| of the rows, two of them side by side; a NaN stays
+            float best[2] = {-INFINITY, -INFINITY};
+            for (int nt = 0; nt < tiles; ++nt) {
+                float part[4][4] = {}, acc[4];  // (four sums: shorter chains, and a quarter of the error)
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const uint32_t w[4] = {raw[r][c].x, raw[r][c].y, raw[r][c].z, raw[r][c].w};
+                for (int c = 0; c < kChunks; ++c) {
+                    uint4 x[Chunk<F8>::kVecs], y[Chunk<F8>::kVecs];
+                    widen<F8>(raw[slot][0][c], x);
+                    widen<F8>(raw[slot][1][c], y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top[r] = F8 ? __vmaxu4(top[r], w[i] & 0x7f7f7f7fu) : __vmaxu2(top[r], w[i] & 0x7fff7fffu);
-            }
-        float best[2] = {-INFINITY, -INFINITY};
-        for (int nt = 0; nt < tiles; ++nt) {
-            float part[4][4] = {}, acc[4];  // (four sums: shorter chains, and a quarter of the error)
+                    for (int k = 0; k < Chunk<F8>::kVecs; ++k) {
+                        const int v = c * Chunk<F8>::kVecs + k;
+                        const uint4 w = qs[(nt * kVecs + v) * 32 + lane];
+                        mma_16x8x16<F8>(part[2 * v & 3], x[k].x, y[k].x, x[k].y, y[k].y, w.x, w.y);
+                        mma_16x8x16<F8>(part[(2 * v + 1) & 3], x[k].z, y[k].z, x[k].w, y[k].w, w.z, w.w);
+                        if (nt == 0) {
+                            top[0] = largest2<F8>(largest2<F8>(top[0], x[k].x, x[k].y), x[k].z, x[k].w);
+                            top[1] = largest2<F8>(largest2<F8>(top[1], y[k].x, y[k].y), y[k].z, y[k].w);
+                        }
+                    }
+                }
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                uint4 x[Chunk<F8>::kVecs], y[Chunk<F8>::kVecs];
-                widen<F8>(raw[0][c], x);
-                widen<F8>(raw[1][c], y);
+                for (int i = 0; i < 4; ++i) acc[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
 #pragma unroll
-                for (int k = 0; k < Chunk<F8>::kVecs; ++k) {
-                    const int v = c * Chunk<F8>::kVecs + k;
-                    const uint4 w = qs[(nt * kVecs + v) * 32 + lane];
-                    mma_16x8x16(part[2 * v & 3], x[k].x, y[k].x, x[k].y, y[k].y, w.x, w.y);
-                    mma_16x8x16(part[(2 * v + 1) & 3], x[k].z, y[k].z, x[k].w, y[k].w, w.z, w.w);
+                for (int i = 0; i < 2; ++i) {
+                    if (nt * 8 + 2 * t + i < a.G) {
+                        // (an overflow of finite values leaves the error infinite: any finite number will do)
+                        const float u = F8 ? scalbnf(acc[i], -shift) : acc[i], v = F8 ? scalbnf(acc[2 + i], -shift) : acc[2 + i];
+                        best[0] = fmaxf(best[0], u == u ? u : 0.f), best[1] = fmaxf(best[1], v == v ? v : 0.f);
+                    }
                 }
             }
+            const uint32_t there = ok[slot];
+            load(tile + kSlots * kSelWarps, raw[slot], ok[slot]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+            for (int r = 0; r < 2; ++r) {
+                float s = best[r];
+                uint32_t m = top[r];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (nt * 8 + 2 * t + i < a.G) {
-                    // (an overflow of finite values leaves the error infinite: any finite number will do)
-                    const float u = acc[i], v = acc[2 + i];
-                    best[0] = fmaxf(best[0], u == u ? u : 0.f), best[1] = fmaxf(best[1], v == v ? v : 0.f);
+                for (int o = 1; o < 4; o <<= 1) {
+                    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+                    m = largest2<F8>(m, __shfl_xor_sync(0xffffffffu, m, o), 0u);
                 }
-            }
-        }
-        const uint32_t there = ok;
-        if (tile + kSelWarps < n_tiles) load(tile + kSelWarps);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float s = best[r];
-            uint32_t m = top[r];
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-                const uint32_t v = __shfl_xor_sync(0xffffffffu, m, o);
-                m = F8 ? __vmaxu4(m, v) : __vmaxu2(m, v);
-            }
-            m = F8 ? max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24)) : max(m & 0xffffu, m >> 16);
-            const bool fine = q_fine && m < (F8 ? 0x7fu : 0x7f80u);
-            const int j = j0 + tile * 16 + g + 8 * r;
-            if (t == 0 && j < j1) {
-                uint32_t key;
-                if (j < a.first || j >= n - a.last) key = kForced;
-                else if (!((there >> (g + 8 * r)) & 1u)) key = 0u;
-                else if (!fine) key = kEndless;
-                else key = float_key(fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f));
-                if (C > 1) st_shared_cluster_u32(keys0 + 4 * j, key);
-                else keys[j] = key;
-                if (key >= kPastFinite) {
-                    ++w_above;
-                } else if (key) {
-                    ++w_in, w_lo = min(w_lo, key), w_hi = max(w_hi, key);
-                    const uint32_t f = F8 ? __float_as_uint(__half2float(__half(
-                                                __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(m), __NV_E4M3))))
-                                          : m << 16;
-                    largest = max(largest, f);
+                const float2 mm = F8 ? f16x2_values(m) : make_float2(bf16lo(m), bf16hi(m));
+                const bool fine = q_fine && mm.x < INFINITY && mm.y < INFINITY;
+                const int j = j0 + tile * 16 + g + 8 * r;
+                if (t == 0 && j < j1) {
+                    uint32_t key;
+                    if (j < a.first || j >= n - a.last) key = kForced;
+                    else if (!((there >> (g + 8 * r)) & 1u)) key = 0u;
+                    else if (!fine) key = kEndless;
+                    else key = float_key(fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f));
+                    if (C > 1) st_shared_cluster_u32(keys0 + 4 * j, key);
+                    else keys[j] = key;
+                    if (key >= kPastFinite) {
+                        ++w_above;
+                    } else if (key) {
+                        ++w_in, w_lo = min(w_lo, key), w_hi = max(w_hi, key);
+                        largest = max(largest, __float_as_uint(fmaxf(mm.x, mm.y)));
+                    }
                 }
             }
         }
