@@ -100,7 +100,7 @@ template <int kChunks>
 __device__ __forceinline__ void move_rows(uint8_t *k_pool, uint8_t *v_pool, int Hkv, int h, int src, int dst, int count,
                                           int lane) {
     constexpr int kRows = 32 / kChunks;   // pairs of one turn
-    constexpr int kTurns = 4;             // turns whose loads are in flight together
+    constexpr int kTurns = 2;             // turns whose loads are in flight together (of 32 warps per SM)
     const int sub = lane / kChunks, chunk = lane % kChunks;
     for (int p0 = 0; p0 < count; p0 += kRows * kTurns) {
         uint4 v[kTurns][2];
@@ -126,7 +126,7 @@ __device__ __forceinline__ void move_rows(uint8_t *k_pool, uint8_t *v_pool, int 
     }
 }
 
-__global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint8_t evict_smem[];
     TopkShared &sh = *reinterpret_cast<TopkShared *>(evict_smem);
     uint32_t *keys = reinterpret_cast<uint32_t *>(evict_smem + kTopkSharedBytes);
@@ -173,16 +173,31 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_co
     const int64_t newest = positions[L - 1];
     __syncthreads();
     const int fixed = past_s * bs;
-    for (int i = tid; i < mine; i += kEvictThreads) {
-        const int t = t0 + i;
-        const float w = weights[t];
-        const int p = positions[t];
-        const bool safe = t < fixed || p < a.first || p > newest - a.recent;
-        keys[i] = safe ? kSafe : float_key(w == w ? w : INFINITY);
+    // Keys; and every place below n gets what it has now (a place that comes free gets another's, later).
+    Window seen;
+    constexpr int kBatch = 4;  // loads on their way together (the stores would hold the next ones up)
+    for (int i0 = tid; i0 < mine; i0 += kBatch * kEvictThreads) {
+        float w[kBatch];
+        int p[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kEvictThreads;
+            w[j] = i < mine ? weights[t0 + i] : 0.f, p[j] = i < mine ? positions[t0 + i] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kEvictThreads, t = t0 + i;
+            if (i >= mine) break;
+            const bool safe = t < fixed || p[j] < a.first || p[j] > newest - a.recent;
+            const uint32_t k = safe ? kSafe : float_key(w[j] == w[j] ? w[j] : INFINITY);
+            keys[i] = k;
+            seen.see(k, 0u, kSafe - 1u);
+            if (t < n) new_weights[t] = w[j], new_positions[t] = p[j];
+        }
     }
     __syncthreads();
 
-    const Border edge = cluster_threshold<kEvictThreads>([&](int i) { return keys[i]; }, mine, n, 0u, kSafe - 1u, C, sh, 0u);
+    const Border edge = cluster_threshold<kEvictThreads>([&](int i) { return keys[i]; }, mine, seen, n, 0u, kSafe - 1u, C, sh, 0u);
     const uint32_t border = edge.lo, need = edge.m == edge.inside ? ~0u : edge.m;
 
     // ---- which tokens stay: those above the border (or all from it on: none then counts as at it, or every one
@@ -197,7 +212,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_co
     cluster_counts<kEvictThreads>(counts, C, sh, 0, before, total);
     const uint32_t kept_low = total[2] + min(total[3], need);  // of the first n
     const int pairs = n - static_cast<int>(kept_low);          // places that came free
-    const int per_cta = max(1, (pairs + C - 1) / C);
+    const int log_ctas = 31 - __clz(C);                        // pair p is CTA p % C's
     for (int i = i0; i < i1; i += 32) {
         const int t = t0 + i + lane;
         const bool here = i + lane < i1;
@@ -208,20 +223,18 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_co
         const uint32_t tied = before[1] + __popc(ats & below);
         const uint32_t kept = before[0] + __popc(aboves & below) + min(tied, need);  // tokens that stay before this one
         const bool stays = above || (at && tied < need);
-        if (here && stays && t < n) {
-            new_weights[t] = weights[t], new_positions[t] = positions[t];
-        } else if (here && stays != (t < n)) {
+        if (here && stays != (t < n)) {
             const int p = static_cast<int>(t < n ? t - kept : kept - kept_low);
-            const uint32_t where = smem_u32((t < n ? holes : movers) + p % per_cta);
-            if (C > 1) st_shared_cluster_u32(map_shared_rank(where, p / per_cta), static_cast<uint32_t>(t));
-            else (t < n ? holes : movers)[p] = t;
+            int32_t *where = (t < n ? holes : movers) + (p >> log_ctas);
+            if (C > 1) st_shared_cluster_u32(map_shared_rank(smem_u32(where), p & (C - 1)), static_cast<uint32_t>(t));
+            else *where = t;
         }
         before[0] += __popc(aboves), before[1] += __popc(ats);
     }
     meet(C);
 
     // ---- the rows
-    const int my_pairs = min(max(pairs - rank * per_cta, 0), per_cta);
+    const int my_pairs = (pairs - rank + C - 1) >> log_ctas;
     const int group = min(32, max(2, (my_pairs + kEvictWarps - 1) / kEvictWarps));
     uint8_t *k_pool = a.pools[2 * layer], *v_pool = a.pools[2 * layer + 1];
     for (int p0 = warp * group; p0 < my_pairs; p0 += kEvictWarps * group) {
@@ -286,7 +299,14 @@ extern "C" int pa_cache_evict(int32_t *new_tables, int32_t *new_lens, int32_t *n
     a.budget = budget, a.first = first, a.recent = recent;
     a.row_chunks = cache.head_dim * elem_bytes / 16;
     for (int i = 0; i < n_pools; ++i) a.pools[i] = static_cast<uint8_t *>(pools[i]);
-    a.ctas = pa::kEvictCtas;
+    // One CTA per row where it can be: its meetings and passes cost half of a cluster's.  More for
+    // rows of over 8192 tokens (two CTAs then fit an SM), and, of long rows, where there are few.
+    const int sms = pa::sm_count();
+    if (sms <= 0) return PA_ECUDA;
+    a.ctas = 1;
+    while (a.ctas < pa::kEvictCtas &&
+           (most > 8192 * a.ctas || (most >= 4096 * a.ctas && 2 * rows * a.ctas <= 2 * sms)))
+        a.ctas *= 2;
     a.slice = static_cast<int32_t>(((most + a.ctas - 1) / a.ctas + 31) / 32 * 32);
     const int copies = (cache.num_blocks + pa::kLensThreads - 1) / pa::kLensThreads;
     if (pa::launch_maybe_cooperative(pa::evict_lens_kernel, dim3(B + copies), pa::kLensThreads, 0, stream, false, pa::pdl_on(),

@@ -564,6 +564,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             uint64_t span = last - base;
             for (;;) {
                 const int shift = max(0, 64 - __clzll(static_cast<long long>(span)) - 31);
+                Window seen;
                 for (int i0 = warp * 32; i0 < n; i0 += kSelThreads) {
                     const int i = i0 + lane;
                     const uint32_t k = i < n ? keys[i] : 0u;
@@ -574,10 +575,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
                         const uint64_t off = s < base ? 0u : min(s - base, span);
                         if (lane == j) now = static_cast<uint32_t>(off >> shift) + 1u;
                     }
-                    if (i < n) keys[i] = now;
+                    if (i < n) keys[i] = now, seen.see(now, 1u, kForced - 1u);
                 }
                 __syncthreads();
-                w = cluster_threshold<kSelThreads>(key_at, n, a.K, 1u, kForced - 1u, 1, sh, 0u);
+                w = cluster_threshold<kSelThreads>(key_at, n, seen, a.K, 1u, kForced - 1u, 1, sh, 0u);
                 from = w.lo, to = w.hi, need = w.m == w.inside ? ~0u : w.m;
                 if (need == ~0u || shift == 0) break;
                 base += static_cast<uint64_t>(from - 1u) << shift;

@@ -172,22 +172,29 @@ __device__ __forceinline__ Border border_of(uint32_t m, uint32_t low, uint32_t h
     return Border{0u, low - 1u, ~0u, m - n_above - n_in};
 }
 
-// The border of the m largest among the keys of all the cluster's CTAs, narrowed.  The CTA meets before
-// this (keys and `sh` are its threads' to use) and the cluster before `sh` is used again.
+// What a thread has seen of its keys: the least and the largest in a window, how many lie in it, how
+// many above it.
+struct Window {
+    uint32_t lo = ~0u, hi = 0u, in = 0u, above = 0u;
+
+    __device__ __forceinline__ void see(uint32_t k, uint32_t low, uint32_t high) {
+        const bool inside = k >= low && k <= high;
+        lo = inside ? min(lo, k) : lo;
+        hi = inside ? max(hi, k) : hi;
+        above += k > high, in += inside;
+    }
+};
+
+// The border of the m largest among the keys of all the cluster's CTAs, narrowed; `seen`: what this
+// thread has seen of them, by the window [low, high].  The CTA meets before this (sh.warp_count has been
+// read), the cluster before `sh` is used again.
 template <int kThreads, typename F>
-__device__ Border cluster_threshold(F key, int n, uint32_t m, uint32_t low, uint32_t high, int C, TopkShared &sh, uint32_t few) {
+__device__ Border cluster_threshold(F key, int n, Window seen, uint32_t m, uint32_t low, uint32_t high, int C, TopkShared &sh,
+                                    uint32_t few) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t lo = ~0u, hi = 0u, n_above = 0u, n_in = 0u;
-    for (int i = tid; i < n; i += kThreads) {
-        const uint32_t k = key(i);
-        const bool in = k >= low && k <= high;
-        lo = in ? min(lo, k) : lo;
-        hi = in ? max(hi, k) : hi;
-        n_above += k > high, n_in += in;
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
-    n_above = __reduce_add_sync(0xffffffffu, n_above), n_in = __reduce_add_sync(0xffffffffu, n_in);
+    uint32_t lo = __reduce_min_sync(0xffffffffu, seen.lo), hi = __reduce_max_sync(0xffffffffu, seen.hi);
+    uint32_t n_above = __reduce_add_sync(0xffffffffu, seen.above), n_in = __reduce_add_sync(0xffffffffu, seen.in);
     if (lane == 0) sh.warp_count[warp][0] = lo, sh.warp_count[warp][1] = hi, sh.warp_count[warp][2] = n_above, sh.warp_count[warp][3] = n_in;
     for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[0][i] = 0;
     __syncthreads();
