@@ -26,6 +26,12 @@ cudaError_t launch_decode_tc_f8(int HC, int GP, int G, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, const DecodeParams &p, int B,
                                 cudaStream_t stream);
 
+// The same kernels with a list of blocks for every KV head (pa_decode_selected).
+cudaError_t launch_decode_tc_sel(int HC, int GP, int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                 const DecodeParams &p, int B, cudaStream_t stream);
+cudaError_t launch_decode_tc_f8_sel(int HC, int GP, int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                    const DecodeParams &p, int B, cudaStream_t stream);
+
 // The same kernels with score rules (pa_decode_scored).
 cudaError_t launch_decode_cc_d64_scored(int G, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                         const DecodeParams &p, int B, cudaStream_t stream);
@@ -378,7 +384,7 @@ struct PassOpts {
     int32_t part_stride = 0;      // 0: the pass's own partition count
     int32_t part_offset = 0;
     int32_t table_stride = 0;     // 0: max_blocks
-    int32_t row_heads = 0;        // > 0: pa_decode_selected's rows, over pools of so many KV heads
+    int32_t lists = 0;            // pa_decode_selected: a list of blocks for every KV head
 };
 
 // Scales of FP8 (e4m3) pools: a stored code c means c * scale.
@@ -430,9 +436,7 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
     p.seq_len_const = po.seq_len_const;
     p.seq_len_offset = po.seq_len_offset;
     if (po.table_stride) p.table_stride = po.table_stride;
-    p.row_heads = po.row_heads;
-    pa_cache_desc pool = c;  // as it lies in memory
-    if (po.row_heads) pool.num_kv_heads = po.row_heads;
+    p.lists = po.lists;
     if ((po.table_stride || po.seq_len_const >= 0 || po.seq_len_offset || !po.causal ||
          po.part_offset) && k != Kernel::kTensorCore)
         return PA_EUNSUPPORTED;  // cascade passes: tensor cores only
@@ -468,34 +472,37 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
         p.q_per_cta = prefill_positions_per_tile(G);
         p.cluster_merge = 0;
         if (prefill_tiles(G, q_len) * c.num_kv_heads > 65535) return PA_EUNSUPPORTED;
-        rc = make_kv_map_heads(&kmap, k_cache, pool, 1);
-        if (!rc) rc = make_kv_map_heads(&vmap, v_cache, pool, 1);
+        rc = make_kv_map_heads(&kmap, k_cache, c, 1);
+        if (!rc) rc = make_kv_map_heads(&vmap, v_cache, c, 1);
         if (rc) return rc;
         e = pa::launch_prefill_tc(kmap, vmap, p, B, G, rules != nullptr, stream);
     } else if (k == Kernel::kTensorCore) {
         int HC = 1, GP = 1;
         if (!tc_shape(G * qpc, c.num_kv_heads, &HC, &GP)) return PA_EUNSUPPORTED;
         p.head_groups = c.num_kv_heads / HC;
+        const int box_heads = po.lists ? 1 : HC;  // heads of one copy
         if (static_cast<int64_t>(p.head_groups) * ((q_len + qpc - 1) / qpc) > 65535) return PA_EUNSUPPORTED;
         if (f8) {
             p.scale_log2 = scale * f8->k_scale * 1.4426950408889634f;
             p.v_scale = f8->v_scale;
             p.k_scale = f8->k_scale;
-            rc = make_kv_map_fp8(&kmap, k_cache, pool, HC);
-            if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, pool, HC);
+            rc = make_kv_map_fp8(&kmap, k_cache, c, box_heads);
+            if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, c, box_heads);
             if (rc) return rc;
-            e = rules ? pa::launch_decode_tc_f8_scored(HC, GP, G, kmap, vmap, p, B, stream)
+            e = po.lists ? pa::launch_decode_tc_f8_sel(HC, GP, G, kmap, vmap, p, B, stream)
+                : rules ? pa::launch_decode_tc_f8_scored(HC, GP, G, kmap, vmap, p, B, stream)
                       : pa::launch_decode_tc_f8(HC, GP, G, kmap, vmap, p, B, stream);
         } else {
-            rc = make_kv_map_heads(&kmap, k_cache, pool, HC);
-            if (!rc) rc = make_kv_map_heads(&vmap, v_cache, pool, HC);
+            rc = make_kv_map_heads(&kmap, k_cache, c, box_heads);
+            if (!rc) rc = make_kv_map_heads(&vmap, v_cache, c, box_heads);
             if (rc) return rc;
-            e = rules ? pa::launch_decode_tc_scored(HC, GP, G, kmap, vmap, p, B, stream)
+            e = po.lists ? pa::launch_decode_tc_sel(HC, GP, G, kmap, vmap, p, B, stream)
+                : rules ? pa::launch_decode_tc_scored(HC, GP, G, kmap, vmap, p, B, stream)
                       : pa::launch_decode_tc(HC, GP, G, kmap, vmap, p, B, stream);
         }
     } else {
-        rc = make_kv_map(&kmap, k_cache, pool);
-        if (!rc) rc = make_kv_map(&vmap, v_cache, pool);
+        rc = make_kv_map(&kmap, k_cache, c);
+        if (!rc) rc = make_kv_map(&vmap, v_cache, c);
         if (rc) return rc;
         e = pa::launch_decode_cc(c.head_dim, G, kmap, vmap, p, B, rules != nullptr, stream);
     }
@@ -779,7 +786,7 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
                    float scale, int32_t num_splits, void *workspace, size_t workspace_bytes,
                    int32_t *status, cudaStream_t stream, const NewTokens &nt, int32_t q_len = 1,
                    const Fp8Scales *f8 = nullptr, bool library_scratch = false,
-                   const pa_score_rules *rules = nullptr, int32_t row_heads = 0) {
+                   const pa_score_rules *rules = nullptr, bool lists = false) {
     int rc = check_decode_args(q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                                seq_lens, B, Hq, scale);
     if (rc) return rc;
@@ -788,15 +795,18 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
     if (static_cast<int64_t>(B) * q_len > kMaxRowsQ) return PA_EUNSUPPORTED;
     if (B == 0) return PA_OK;
     PassOpts po;
-    po.row_heads = row_heads;
+    po.lists = lists;
     int P = num_splits;
     if (P == 0) {
         const int sms = sm_count_current();
         if (sms <= 0) return PA_ECUDA;
-        P = rules ? scored_splits(B, q_len, Hq, cache.num_kv_heads, cache.head_dim, max_blocks_per_seq,
-                                  cache.block_size, rules->window, rules->prefix_lens ? rules->max_prefix : 0, sms)
-                  : pa_choose_num_splits_mq(B, q_len, Hq, cache.num_kv_heads, cache.head_dim,
-                                            max_blocks_per_seq, cache.block_size, sms);
+        P = rules || lists ? scored_splits(B, q_len, Hq, cache.num_kv_heads, cache.head_dim, max_blocks_per_seq,
+                                           cache.block_size, rules ? rules->window : 0,
+                                           rules && rules->prefix_lens ? rules->max_prefix : 0, sms)
+                           : pa_choose_num_splits_mq(B, q_len, Hq, cache.num_kv_heads, cache.head_dim,
+                                                     max_blocks_per_seq, cache.block_size, sms);
+        // (pa_decode_selected: as many as a smaller workspace holds)
+        while (lists && P > 1 && (!workspace || workspace_bytes < pa_splitkv_workspace_bytes(B, Hq, cache.head_dim, P))) --P;
         if (P < 0) return P;
     }
     if (P > 65535) return PA_EUNSUPPORTED;
@@ -895,31 +905,12 @@ int pa_decode_scored_fp8(void *out, float *lse, const void *q, int32_t q_len, co
                           stream, NewTokens(), q_len, &f8, false, rules);
 }
 
-// pa_decode_selected(_fp8): every KV head's list of blocks as a sequence of its own,
-// with one KV head, whose place in the pools the kernels work out from its row.
-static int decode_selected(void *out, float *lse, const void *q, const void *k_cache, const void *v_cache,
-                           const pa_cache_desc &cache, const int32_t *sel_tables, int32_t max_selected,
-                           const int32_t *sel_lens, int32_t B, int32_t Hq, float scale, int32_t num_splits,
-                           void *workspace, size_t workspace_bytes, int32_t *status, cudaStream_t stream,
-                           const Fp8Scales *f8) {
-    const int rc = check_cache_desc(cache);
-    if (rc) return rc;
-    if (B < 0 || Hq <= 0 || Hq % cache.num_kv_heads != 0) return PA_EINVAL;
-    const int64_t rows = static_cast<int64_t>(B) * cache.num_kv_heads;
-    if (rows > kMaxGridZ) return PA_EUNSUPPORTED;
-    pa_cache_desc one = cache;
-    one.num_kv_heads = 1;
-    return splitkv_common(out, lse, q, k_cache, v_cache, one, sel_tables, max_selected, sel_lens,
-                          static_cast<int32_t>(rows), Hq / cache.num_kv_heads, scale, num_splits, workspace,
-                          workspace_bytes, status, stream, NewTokens(), 1, f8, false, nullptr, cache.num_kv_heads);
-}
-
 int pa_decode_selected(void *out, float *lse, const void *q, const void *k_cache, const void *v_cache,
                        pa_cache_desc cache, const int32_t *sel_tables, int32_t max_selected,
                        const int32_t *sel_lens, int32_t B, int32_t Hq, float scale, int32_t num_splits,
                        void *workspace, size_t workspace_bytes, int32_t *status, pa_stream_t stream) {
-    return decode_selected(out, lse, q, k_cache, v_cache, cache, sel_tables, max_selected, sel_lens, B, Hq, scale,
-                           num_splits, workspace, workspace_bytes, status, stream, nullptr);
+    return splitkv_common(out, lse, q, k_cache, v_cache, cache, sel_tables, max_selected, sel_lens, B, Hq, scale, num_splits,
+                          workspace, workspace_bytes, status, stream, NewTokens(), 1, nullptr, false, nullptr, true);
 }
 
 int pa_decode_selected_fp8(void *out, float *lse, const void *q, const void *k_cache, const void *v_cache,
@@ -931,8 +922,8 @@ int pa_decode_selected_fp8(void *out, float *lse, const void *q, const void *k_c
         return PA_EINVAL;
     if (cache.head_dim != 128) return PA_EUNSUPPORTED;
     const Fp8Scales f8{k_scale, v_scale};
-    return decode_selected(out, lse, q, k_cache, v_cache, cache, sel_tables, max_selected, sel_lens, B, Hq, scale,
-                           num_splits, workspace, workspace_bytes, status, stream, &f8);
+    return splitkv_common(out, lse, q, k_cache, v_cache, cache, sel_tables, max_selected, sel_lens, B, Hq, scale, num_splits,
+                          workspace, workspace_bytes, status, stream, NewTokens(), 1, &f8, false, nullptr, true);
 }
 
 int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D,

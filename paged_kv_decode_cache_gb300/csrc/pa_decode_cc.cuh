@@ -70,10 +70,11 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size;
 
-    int L = p.seq_lens[b];
+    const int list = p.lists ? b * p.num_kv_heads + g : b;  // whose blocks are read
+    int L = p.seq_lens[list];
     const int lmax = p.max_blocks * bs;
     if (L < 0 || L > lmax) {
-        if (tid == 0 && part == 0 && g == 0) set_status(p.status, PA_STATUS_BAD_SEQLEN);
+        if (tid == 0 && part == 0 && (g == 0 || p.lists)) set_status(p.status, PA_STATUS_BAD_SEQLEN);
         L = L < 0 ? 0 : lmax;
     }
     const int t_begin = part * p.chunk;
@@ -82,7 +83,7 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     auto real = [&](int t) { return SC ? sn.real(t) : t; };
     const int t_end = min(t_begin + p.chunk, SC ? sn.end : L);
     const int ntiles = t_end > t_begin ? (t_end - t_begin + kTile - 1) / kTile : 0;
-    const int32_t *bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+    const int32_t *bt = p.block_tables + static_cast<int64_t>(list) * p.max_blocks;
 
     // Query heads of this group, widened to fp32 and pre-scaled by scale*log2(e).
     const uint16_t *qg = p.q + (static_cast<int64_t>(b) * p.num_q_heads + g * G) * D;
@@ -105,7 +106,6 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     uint64_t *wbars = bars + warp * NST;
     float *pbuf = pbuf_all + warp * kTile * C::kPG;
     const uint64_t policy = l2_evict_first_policy();
-    const int pool_head = p.row_heads ? b % p.row_heads : g;  // the KV head that is read
 
     auto tile_phys = [&](int j) -> int {  // physical block of this warp's j-th tile
         const int tok0 = real(t_begin + (warp + j * NW) * kTile);
@@ -126,8 +126,8 @@ decode_cc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         mbar_arrive_expect_tx(&wbars[s], C::kStageBytes);
 #pragma unroll
         for (int sub = 0; sub < C::kSub; ++sub) {
-            tma_load_4d(kt + sub * kTile * kSubBytes, &kmap, 0, sub, pool_head, row0, &wbars[s], policy);
-            tma_load_4d(vt + sub * kTile * kSubBytes, &vmap, 0, sub, pool_head, row0, &wbars[s], policy);
+            tma_load_4d(kt + sub * kTile * kSubBytes, &kmap, 0, sub, g, row0, &wbars[s], policy);
+            tma_load_4d(vt + sub * kTile * kSubBytes, &vmap, 0, sub, g, row0, &wbars[s], policy);
         }
     };
 

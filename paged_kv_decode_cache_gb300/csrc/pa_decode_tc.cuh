@@ -273,7 +273,7 @@ __host__ __device__ constexpr int vt_row_k(int m) {
     return (m & ~15) | (((m >> 1) & 3) << 2) | (((m >> 3) & 1) << 1) | (m & 1);
 }
 
-template <int HC, int GP, bool F8, bool SC>
+template <int HC, int GP, bool F8, bool SC, bool SEL>
 __global__ void __launch_bounds__((TcCfg<HC, GP, F8, SC>::kThreads), 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const DecodeParams p, int G) {
@@ -281,6 +281,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     using C = TcCfg<HC, GP, F8, SC>;
     constexpr int kThreads = C::kThreads;
     constexpr int N = C::kN, NK = C::kNK, NV = C::kNV, NBP = C::kNBP, NBS = C::kNBS;
+    static_assert(!(SC && SEL), "lists of blocks have no score rules");
+    // What one copy loads: a tile of all HC heads, or (SEL: every head reads its own blocks)
+    // a tile of one of them.  A chunk's copies are its 16-row groups then, (tile, head).
+    constexpr int kBoxes = SEL ? C::kTiles * HC : C::kTiles;
+    constexpr int kBoxHeads = SEL ? HC : 1;
+    constexpr int kBoxBytes = SEL ? kTile * kSubBytes : C::kBoxBytes;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -329,14 +335,15 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (threadIdx.x >= 32 * kTcPvWarp && threadIdx.x < 32 * (kTcPvWarp + 1)) {
         constexpr int kPre = F8 ? 4 : 2;  // chunks
         const int ln = threadIdx.x & 31;
-        if (ln < kPre * C::kTiles) {
-            const int c = ln / C::kTiles, tl = ln % C::kTiles;
+        if (ln < kPre * kBoxes) {
+            const int c = ln / kBoxes, tl = ln % kBoxes / kBoxHeads;
             const int bz = blockIdx.z;
-            const int hg0 = p.row_heads ? bz % p.row_heads : static_cast<int>(blockIdx.y % p.head_groups) * HC;
+            const int hg0 = static_cast<int>(blockIdx.y % p.head_groups) * HC + (SEL ? ln % kBoxHeads : 0);
+            const int64_t list = SEL ? static_cast<int64_t>(bz) * p.num_kv_heads + hg0 : bz;
             const int t0 = static_cast<int>(blockIdx.x) * p.chunk;
             int tok = t0 + c * C::kT + tl * kTile;
             const int lp = p.seq_len_const >= 0 ? p.seq_len_const
-                                                : *reinterpret_cast<const volatile int32_t *>(p.seq_lens + bz) -
+                                                : *reinterpret_cast<const volatile int32_t *>(p.seq_lens + list) -
                                                       p.seq_len_offset;
             int lim = min(t0 + p.chunk, min(lp, p.max_blocks * p.block_size));
             int place = tok;  // its real place in the sequence
@@ -350,7 +357,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
             if (tok < lim && tok >= t0) {
                 const int phys = *reinterpret_cast<const volatile int32_t *>(
-                    p.block_tables + static_cast<int64_t>(bz) * p.table_stride + place / p.block_size);
+                    p.block_tables + list * p.table_stride + place / p.block_size);
                 if (phys >= 0 && phys < p.num_blocks) {
                     const int row = phys * p.block_size + place % p.block_size;
                     if constexpr (F8) {
@@ -372,7 +379,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 
     const int part = blockIdx.x, b = blockIdx.z;
     const int g0 = (blockIdx.y % p.head_groups) * HC;
-    const int pool_head = p.row_heads ? b % p.row_heads : g0;  // the first KV head that is read
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int bs = p.block_size;
     // This CTA's queries: positions qi0 .. qi0 + nq - 1 of the q_len new ones
@@ -393,8 +399,27 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     auto col_row = [&](int hh, int c) -> int64_t {
         return row0 + static_cast<int64_t>(c / G) * Hq + hh * G + c % G;
     };
-    const int32_t *bt = p.block_tables + static_cast<int64_t>(b) * p.table_stride;
-    int L = p.seq_len_const >= 0 ? p.seq_len_const : p.seq_lens[b] - p.seq_len_offset;
+    // SEL: this thread's head among the CTA's HC (of the 16 rows that it owns, or of the copy that
+    // it issues), its list and length; L is the longest one's, `least` the shortest one's.
+    const int own_head = !SEL ? 0 : warp < 4 ? (tid >> 4) % HC : (lane >> 1) % HC;
+    const int32_t *bt = p.block_tables + (SEL ? static_cast<int64_t>(b) * p.num_kv_heads + g0 + own_head
+                                              : static_cast<int64_t>(b)) * p.table_stride;
+    int L = 0, own_len = 0, least = 0;
+    if constexpr (SEL) {
+        const int32_t *lens = p.seq_lens + static_cast<int64_t>(b) * p.num_kv_heads + g0;
+#pragma unroll
+        for (int hh = 0; hh < HC; ++hh) {
+            int x = lens[hh];
+            if (x < 0 || x > lmax) {
+                if (tid == 0 && part == 0) set_status(p.status, PA_STATUS_BAD_SEQLEN);
+                x = x < 0 ? 0 : lmax;
+            }
+            if (hh == own_head) own_len = x;
+            L = max(L, x), least = hh ? min(least, x) : x;
+        }
+    } else {
+        L = p.seq_len_const >= 0 ? p.seq_len_const : p.seq_lens[b] - p.seq_len_offset;
+    }
     constexpr int kQLoads = (N * (D / 8) + kThreads - 1) / kThreads;
     uint4 qv[kQLoads];
 #pragma unroll
@@ -410,8 +435,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // tile `tile` of a chunk; both lanes of a tile look its block up.
     const bool producer = warp == kTcTmaKWarp || warp == kTcTmaVWarp;
     const bool is_v = warp == kTcTmaVWarp;
-    const int tile = lane >> 1, sub = lane & 1;
-    const bool carrier = producer && lane < 2 * C::kTiles;
+    const int box = lane >> 1, tile = box / kBoxHeads, sub = lane & 1;
+    const bool carrier = producer && lane < 2 * kBoxes;
     int *my_look = look_ring + (is_v ? (kTcLook + 1) * 32 : 0) + lane;  // slot j at my_look[32 * j]
     Seen sn{};  // SC: the partition counts virtual tokens, sn.real() of which are read
     auto real = [&](int t) { return SC ? sn.real(t) : t; };
@@ -459,6 +484,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if constexpr (SC) sn = seen_by(p, b, L, qbase, nq, tid == 0 && part == 0 && g0 == 0);
     const int t_end = min(t_begin + p.chunk, SC ? sn.end : max(0, min(L, p.causal ? qbase + nq : L)));
     const int nch = t_end > t_begin ? (t_end - t_begin + C::kT - 1) / C::kT : 0;
+    const int own_end = SEL ? min(t_begin + p.chunk, own_len) : t_end;  // where this thread's head's range ends
     if (SC && p.slopes) t_first = t_begin + (nch - 1) * C::kT;
     if (producer && SC) {  // (a token's place depends on the length)
 #pragma unroll
@@ -545,7 +571,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
             const int tok0 = chunk_at(c) + tile * kTile;
             bool valid = false;
-            if (carrier && tok0 < t_end) {
+            if (carrier && tok0 < own_end) {
                 if (phys >= 0 && phys < p.num_blocks) valid = true;
                 else if (!is_v && sub == 0) set_status(p.status, PA_STATUS_BAD_BLOCK);
             }
@@ -582,17 +608,17 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 // one box per tile (16 rows x HC heads x 128 one-byte codes) into the
                 // code stage, from which the converter warps widen it into TMEM
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(__popc(vm & 0x55555555u)) * C::kBoxBytes);
+                    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(__popc(vm & 0x55555555u)) * kBoxBytes);
                 __syncwarp();
                 if (valid && sub == 0)
-                    tma_load_3d(ring + s * C::kStageBytes + tile * C::kBoxBytes, map, 0,
-                                phys * bs + real(tok0) % bs, pool_head, &full[s], policy);
+                    tma_load_3d(ring + s * C::kStageBytes + box * kBoxBytes, map, 0,
+                                phys * bs + real(tok0) % bs, g0 + own_head, &full[s], policy);
             } else {
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(__popc(vm)) * C::kBoxBytes);
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(__popc(vm)) * kBoxBytes);
                 __syncwarp();
                 if (valid)
-                    tma_load_4d(ring + s * C::kStageBytes + sub * C::kSubTile + tile * C::kBoxBytes, map, 0,
-                                phys * bs + real(tok0) % bs, pool_head, sub, &full[s], policy);
+                    tma_load_4d(ring + s * C::kStageBytes + sub * C::kSubTile + box * kBoxBytes, map, 0,
+                                phys * bs + real(tok0) % bs, g0 + own_head, sub, &full[s], policy);
             }
             issued = c + 1;
         }
@@ -816,8 +842,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tc5::fence_after_sync();
             const uint32_t vm = static_cast<uint32_t>(mk);
             const int tok_c = chunk_at(c);
-            constexpr uint32_t kAllTiles = 0x55555555u & ((1u << (2 * C::kTiles)) - 1u);
-            const bool whole = (vm & kAllTiles) == kAllTiles && tok_c + C::kT <= t_end;
+            constexpr uint32_t kAllTiles = 0x55555555u & ((1u << (2 * kBoxes)) - 1u);
+            const bool whole = (vm & kAllTiles) == kAllTiles && tok_c + C::kT <= (SEL ? min(t_end, least) : t_end);
             // SC: rows inside the range that no query sees (before the window, past the
             // prefix) get zero codes here, in the few chunks that have any, so that the
             // passes below stay as they are without rules (masks computed in them cost
@@ -856,10 +882,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                         uint32_t ka = 0xffffffffu, kb = 0xffffffffu;
                         if (!whole) {
                             const int tl = (2 * k + gg) / HC;
-                            const bool tile_ok = (vm >> (2 * tl)) & 1u;
+                            const bool tile_ok = (vm >> (2 * (SEL ? 2 * k + gg : tl))) & 1u;
                             const int r0 = tok_c + tl * kTile + 2 * (lane & 3);
-                            ka = (tile_ok && r0 < t_end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 1 < t_end ? 0xffff0000u : 0u);
-                            kb = (tile_ok && r0 + 8 < t_end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 9 < t_end ? 0xffff0000u : 0u);
+                            // (SEL: the group is head (2 k + gg) % HC's; lane 2 i of this warp knows head i's range)
+                            const int end = SEL ? __shfl_sync(0xffffffffu, own_end, 2 * ((2 * k + gg) % HC)) : t_end;
+                            ka = (tile_ok && r0 < end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 1 < end ? 0xffff0000u : 0u);
+                            kb = (tile_ok && r0 + 8 < end ? 0x0000ffffu : 0u) | (tile_ok && r0 + 9 < end ? 0xffff0000u : 0u);
                         }
                         // repetition g = 2 k + gg of the store: columns 8 g + 2 (t % 4) (+ 1)
                         w[8 * k + 4 * gg + 0] = a.x & ka;  // dim 2 (t / 4): lane t / 4, rows of h = 0
@@ -941,7 +969,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             }
             ok = __all_sync(0xffffffffu, ok);
             const bool in_pool =
-                chunk_at(c) + my_tok < t_end && ((static_cast<uint32_t>(mk) >> (2 * my_tile)) & 1u);
+                chunk_at(c) + my_tok < own_end && ((static_cast<uint32_t>(mk) >> (2 * (SEL ? tid >> 4 : my_tile))) & 1u);
             float sv[GP];  // this row's head's GP scores
             if (ok) {
                 tc5::fence_after_sync();
@@ -1193,11 +1221,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                                               reinterpret_cast<float *>(ps));
 }
 
-template <int HC, int GP, bool F8, bool SC = false>
+template <int HC, int GP, bool F8, bool SC = false, bool SEL = false>
 cudaError_t launch_tc_instance(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                const DecodeParams &p, int B, int G, cudaStream_t stream) {
     using C = TcCfg<HC, GP, F8, SC>;
-    auto kern = decode_tc_kernel<HC, GP, F8, SC>;
+    auto kern = decode_tc_kernel<HC, GP, F8, SC, SEL>;
     static std::atomic<uint64_t> smem_attr_done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

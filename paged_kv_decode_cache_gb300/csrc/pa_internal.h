@@ -95,9 +95,10 @@ struct DecodeParams {
     int32_t window;
     const int32_t *prefix_lens;
     int32_t max_prefix;
-    // pa_decode_selected: > 0 where a "sequence" b is one KV head's own list of
-    // blocks (num_kv_heads is 1): it reads KV head b % row_heads of the pools.
-    int32_t row_heads;
+    // pa_decode_selected: block_tables [B, Hkv, max_blocks] and seq_lens [B, Hkv], a list of
+    // blocks for every KV head (the tensor-core kernel's SEL instances; the CUDA-core one
+    // looks here).
+    int32_t lists;
 };
 
 // CUDA-core decode kernel launch (pa_decode_cc_d*.cu).  Returns a cudaError_t.

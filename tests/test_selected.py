@@ -56,7 +56,7 @@ def case(hq, hkv, d, bs, lens, splits, fp8=False, seed=1, extra=0, stream=None, 
             out[b, hs], lse[b, hs] = attention64(as64(q[b, hs]), k * ks, v * vs, scale)
     for p in pools:   # what no list names is never looked at
         p.view(nb * bs, hkv, d)[~used] = 0x7F if fp8 else math.nan
-    P = splits or pa.pa_auto_num_splits(Bn * hkv, G, 1, d, width, bs)
+    P = splits or pa.pa_scored_num_splits(Bn, 1, hq, hkv, d, width, bs)
     ws = torch.zeros(max(1, pa.pa_splitkv_workspace_bytes(Bn, hq, d, P)), dtype=torch.uint8, device="cuda")
     got, z = torch.full((Bn, hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((Bn, hq), 7.0, device="cuda")
     pools = [p.cuda() for p in pools]
@@ -128,6 +128,24 @@ def test_selected_is_plain_decode_where_every_head_reads_everything():
 
 
 @pytest.mark.gpu
+def test_selected_takes_the_splits_that_its_workspace_holds():
+    """num_splits = 0 with less workspace than the rule's count needs, or none."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
+    q, k, v = rnd(1, 8, 128), rnd(80, 16, 2, 128), rnd(80, 16, 2, 128)
+    t, n = torch.arange(80, device="cuda").int().expand(1, 2, 80).contiguous(), i32([[1280, 1111]])
+    P = pa.pa_scored_num_splits(1, 1, 8, 2, 128, 80, 16)
+    assert P > 4
+    outs = []
+    for size in (pa.pa_splitkv_workspace_bytes(1, 8, 128, P), pa.pa_splitkv_workspace_bytes(1, 8, 128, 3), 4096, 0):
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda") if size else None
+        outs.append(torch.empty_like(q))
+        pa.pa_decode_selected(outs[-1], None, q, k, v, t, n, 0.1, workspace=ws)
+    for x in outs[1:]:
+        assert ((x.double() - outs[0].double()).abs() <= 2.0 ** -7 * outs[0].double().abs() + 2.0 ** -11).all()
+
+
+@pytest.mark.gpu
 def test_selected_reports_bad_blocks_and_lengths():
     g = torch.Generator(device="cuda").manual_seed(1)
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
@@ -150,7 +168,7 @@ FAKE = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced: these calls fail
     (dict(q=None), pa.PA_EINVAL), (dict(B=-1), pa.PA_EINVAL), (dict(K=0), pa.PA_EINVAL), (dict(Hq=5), pa.PA_EINVAL),
     (dict(Hq=0), pa.PA_EINVAL), (dict(splits=-1), pa.PA_EINVAL), (dict(splits=3), pa.PA_EWORKSPACE),
     (dict(scale=math.inf), pa.PA_EINVAL), (dict(out=None), pa.PA_EINVAL), (dict(Hq=66), pa.PA_EUNSUPPORTED),
-    (dict(B=40000), pa.PA_EUNSUPPORTED), (dict(desc=pa.CacheDesc(64, 16, 2, 96)), pa.PA_EUNSUPPORTED),
+    (dict(B=70000), pa.PA_EUNSUPPORTED), (dict(desc=pa.CacheDesc(64, 16, 2, 96)), pa.PA_EUNSUPPORTED),
     (dict(desc=pa.CacheDesc(64, 16, 0, 128)), pa.PA_EINVAL), (dict(B=0), pa.PA_OK),
 ])
 def test_selected_refusals(kw, code):
