@@ -833,8 +833,8 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
  * max_selected]; sel_lens: device int32 [B, Hkv], the tokens of the list, all of its
  * blocks full but the last.  A list without tokens gives out = 0 and lse = -inf.
  * Supported: the shapes of pa_decode_splitkv (FP8: of pa_decode_splitkv_fp8).
- * num_splits 0: pa_scored_num_splits(B, 1, Hq, Hkv, D, max_selected, block_size, 0, 0, 0),
- * or fewer, as many as the workspace holds; workspace: pa_splitkv_workspace_bytes(B,
+ * num_splits 0: pa_auto_num_splits(B, Hq, Hkv, D, max_selected, block_size), or fewer,
+ * as many as the workspace holds; workspace: pa_splitkv_workspace_bytes(B,
  * Hq, D, P) bytes, with pa_decode_splitkv's contract.
  */
 int pa_decode_selected(void *out, float *lse, const void *q, const void *k_cache,

@@ -56,7 +56,7 @@ def case(hq, hkv, d, bs, lens, splits, fp8=False, seed=1, extra=0, stream=None, 
             out[b, hs], lse[b, hs] = attention64(as64(q[b, hs]), k * ks, v * vs, scale)
     for p in pools:   # what no list names is never looked at
         p.view(nb * bs, hkv, d)[~used] = 0x7F if fp8 else math.nan
-    P = splits or pa.pa_scored_num_splits(Bn, 1, hq, hkv, d, width, bs)
+    P = splits or pa.pa_auto_num_splits(Bn, hq, hkv, d, width, bs)
     ws = torch.zeros(max(1, pa.pa_splitkv_workspace_bytes(Bn, hq, d, P)), dtype=torch.uint8, device="cuda")
     got, z = torch.full((Bn, hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((Bn, hq), 7.0, device="cuda")
     pools = [p.cuda() for p in pools]
@@ -134,7 +134,7 @@ def test_selected_takes_the_splits_that_its_workspace_holds():
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
     q, k, v = rnd(1, 8, 128), rnd(80, 16, 2, 128), rnd(80, 16, 2, 128)
     t, n = torch.arange(80, device="cuda").int().expand(1, 2, 80).contiguous(), i32([[1280, 1111]])
-    P = pa.pa_scored_num_splits(1, 1, 8, 2, 128, 80, 16)
+    P = pa.pa_auto_num_splits(1, 8, 2, 128, 80, 16)
     assert P > 4
     outs = []
     for size in (pa.pa_splitkv_workspace_bytes(1, 8, 128, P), pa.pa_splitkv_workspace_bytes(1, 8, 128, 3), 4096, 0):
