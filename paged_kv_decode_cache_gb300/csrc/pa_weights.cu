@@ -11,6 +11,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_mma.cuh"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 namespace {
@@ -34,20 +35,17 @@ struct WeightsArgs {
 constexpr int kWThreads = 256;
 constexpr int kWWarps = kWThreads / 32;
 constexpr int kWFew = 32;                               // columns (queries x heads) of the streaming kernel, at most
-constexpr int kWTiles = 2;                              // wide kernel: tiles of 16 tokens of a warp
-constexpr int kWTokens = kWWarps * kWTiles * kTile;     // ... tokens of a CTA
-constexpr int kWColumns = 128;                          // ... columns in shared memory at once
 
-// Columns c0 .. c0 + here - 1 of a (sequence, KV head) into shared memory: the MMA's operands,
-// the lse in log2 units, and the last token that each sees (-1: none).
+// The columns (query, head of the group) of a (sequence, KV head) into shared memory: the
+// MMA's operands, the lse in log2 units, and the last token that each sees (-1: none).
 template <bool F8, int D>
-__device__ __forceinline__ void load_columns(const WeightsArgs &a, int b, int h, int first_new, int c0, int here, uint4 *qs,
+__device__ __forceinline__ void load_columns(const WeightsArgs &a, int b, int h, int first_new, int here, uint4 *qs,
                                              float *lse_s, int *last_s) {
     constexpr int kVecs = D / 32;
     const int tiles = (here + 7) / 8;
     for (int i = threadIdx.x; i < tiles * kVecs * 32; i += kWThreads) {
         const int ln = i & 31, v = (i >> 5) % kVecs, col = (i >> 5) / kVecs * 8 + (ln >> 2);
-        const int64_t row = (static_cast<int64_t>(b) * a.q_len + (c0 + col) / a.G) * a.Hkv * a.G + h * a.G + (c0 + col) % a.G;
+        const int64_t row = (static_cast<int64_t>(b) * a.q_len + col / a.G) * a.Hkv * a.G + h * a.G + col % a.G;
         uint4 w = col < here ? *reinterpret_cast<const uint4 *>(a.q + row * D + vec_dim<F8>(v, ln & 3))
                              : make_uint4(0u, 0u, 0u, 0u);
         if constexpr (F8)
@@ -56,8 +54,8 @@ __device__ __forceinline__ void load_columns(const WeightsArgs &a, int b, int h,
         qs[i] = w;
     }
     for (int col = threadIdx.x; col < tiles * 8; col += kWThreads) {
-        const int i = (c0 + col) / a.G;
-        const int64_t row = (static_cast<int64_t>(b) * a.q_len + i) * a.Hkv * a.G + h * a.G + (c0 + col) % a.G;
+        const int i = col / a.G;
+        const int64_t row = (static_cast<int64_t>(b) * a.q_len + i) * a.Hkv * a.G + h * a.G + col % a.G;
         const float lse = col < here ? a.lse[row] : -INFINITY;
         lse_s[col] = lse * 1.4426950408889634f;
         last_s[col] = lse == -INFINITY ? -1 : first_new + i;  // (a query that saw nothing adds nothing)
@@ -146,7 +144,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 #pragma unroll
     for (int s = 0; s < kSlots / 2; ++s) was[s] = load_old(s);
     const int columns = a.q_len * a.G, col_tiles = kOne ? 1 : (columns + 7) / 8;
-    load_columns<F8, D>(a, b, h, first_new, 0, columns, qs, lse_s, last_s);
+    load_columns<F8, D>(a, b, h, first_new, columns, qs, lse_s, last_s);
     __syncthreads();
     const int shift = a.ends ? a.ends[b] - L : 0;  // a token's position less its place
     uint4 q1[kOne ? kVecs : 1];
@@ -209,18 +207,89 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
     }
 }
 
-// More columns: a CTA per 256 tokens of a (sequence, KV head), 32 to a warp, whose keys it keeps
-// in registers while the columns (query, head of the group) pass through shared memory, up
-// to 128 at a time.
+// ---- more columns (a window of queries over a long context): tensor cores --------------------
+//
+// S[128 tokens, N] = K[128, D] . Q^T[D, N] per tile, N <= 256 columns (query, head of the
+// group) at a time, by tcgen05.mma into TMEM; a thread per token then adds up its row's
+// exponentials.  16 exponentials a clock and SM bound it: 128 x N of them a tile take
+// 8 N clocks, the MMA 4 N, and the tile's keys come in meanwhile.
+//
+// Warps 0-7 (two groups of four): the exponentials of every second tile; a group's lane is the
+// token.  Warps 8-15: keys from the pool into a ring of 32 KB stages, as the MMA reads them
+// (K-major, 128-byte swizzle; e4m3 codes widened to fp16 on the way); a tile's loads are in
+// registers while its stage is still read.  Warp 16: issues the MMAs.  Every wait is bounded.
+constexpr int kXThreads = 17 * 32;
+constexpr int kXLoadWarp = 8, kXMmaWarp = 16;
+constexpr int kXLoadRows = 16;           // tokens of a loading warp
+constexpr int kXRows = 128;              // tokens of a tile
+constexpr int kXStages = 3;
+constexpr int kXMostTiles = 32;          // of a CTA
+constexpr int kXColumns = 256;           // at once
+
+template <int D>
+struct XShape {
+    static constexpr int kHalves = D / 64;                       // 64-element sub-rows
+    static constexpr int kStageBytes = kHalves * kXRows * kSubBytes;
+    // dynamic shared memory: stages, queries, sums, -lse, last tokens, barriers
+    static constexpr int q_bytes(int n) { return kHalves * n * kSubBytes; }
+    static constexpr int sums_at(int n) { return kXStages * kStageBytes + q_bytes(n); }
+    static constexpr int bytes(int n) {
+        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + (2 * kXStages + 5) * 8 + 16 + 1024;
+    }
+};
+
+// The sum over columns [n0, n1) of a row in TMEM of 2^(s scale + nl): 16 columns at a time, the next
+// ones on their way.  kMasked: only columns that see token tok.
+template <bool kMasked>
+__device__ __forceinline__ float row_sum(uint32_t row, int n1, float scale, const float *nl, const int *last, int tok) {
+    uint32_t cur[16], nxt[16];
+    uint64_t sum2 = 0;
+    float sum = 0.f;
+    const uint64_t scale2 = pack2(scale, scale);
+    tc5::ld_32x32b_x16_nowait(row, cur);
+    tc5::wait_ld();
+    for (int n = 0; n < n1; n += 16) {
+        if (n + 16 < n1) tc5::ld_32x32b_x16_nowait(row + n + 16, nxt);
+        if (!kMasked && n + 16 <= n1) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(nl + n + i);
+                const uint64_t a = fma2(pack2(__uint_as_float(cur[i]), __uint_as_float(cur[i + 1])), scale2, z.x);
+                const uint64_t b = fma2(pack2(__uint_as_float(cur[i + 2]), __uint_as_float(cur[i + 3])), scale2, z.y);
+                float e[4];
+                unpack2(a, e[0], e[1]);
+                unpack2(b, e[2], e[3]);
+                sum2 = add2(sum2, pack2(fast_exp2(e[0]), fast_exp2(e[1])));
+                sum2 = add2(sum2, pack2(fast_exp2(e[2]), fast_exp2(e[3])));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (n + i < n1 && (!kMasked || tok <= last[n + i])) sum += fast_exp2(fmaf(__uint_as_float(cur[i]), scale, nl[n + i]));
+        }
+        tc5::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) cur[i] = nxt[i];
+    }
+    float a, b;
+    unpack2(sum2, a, b);
+    return sum + (a + b);
+}
+
 template <bool F8, int D>
-__global__ void __launch_bounds__(kWThreads, 2) weights_wide_kernel(const WeightsArgs a) {
-    constexpr int kRowBytes = D * (F8 ? 1 : 2);
-    constexpr int kChunks = kRowBytes / 64;
-    constexpr int kVecs = kChunks * Chunk<F8>::kVecs;
-    extern __shared__ uint4 qs[];                       // [column tiles][kVecs][32 lanes]
-    __shared__ float lse_s[kWColumns];                  // in log2 units
-    __shared__ int last_s[kWColumns];                   // last token that the column sees, -1: none
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+__global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsArgs a, int tiles_max, int n_most, uint32_t tmem_cols) {
+    using X = XShape<D>;
+    extern __shared__ uint8_t x_smem[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(x_smem) + 1023) & ~uintptr_t(1023));
+    uint8_t *qs = smem + kXStages * X::kStageBytes;
+    float *sums = reinterpret_cast<float *>(smem + X::sums_at(n_most));      // [tiles][128], over the chunks of columns
+    float *nl = sums + kXMostTiles * kXRows;                                  // -lse of every column, log2 units
+    int *last_s = reinterpret_cast<int *>(nl + kXColumns);                    // last token that it sees
+    uint64_t *bars = reinterpret_cast<uint64_t *>(last_s + kXColumns);
+    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 2, *drain = sfree + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, b = blockIdx.z, bs = a.block_size;
     griddep_wait();
     griddep_launch_dependents();
@@ -230,86 +299,164 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_wide_kernel(const Weight
         if (tid == 0 && blockIdx.x == 0 && h == 0) set_status(a.status, PA_STATUS_BAD_SEQLEN);
         L = L < 0 ? 0 : most;
     }
-    const int tok0 = static_cast<int>(blockIdx.x) * kWTokens;
+    const int tok0 = static_cast<int>(blockIdx.x) * tiles_max * kXRows;
     if (tok0 >= L) return;
-    const int n_cols = a.q_len * a.G, first_new = L - a.q_len;
+    const int tiles = min(tiles_max, (L - tok0 + kXRows - 1) / kXRows);
+    const int first_new = L - a.q_len, n_cols = a.q_len * a.G;
+    const int32_t *table = a.tables + static_cast<int64_t>(b) * a.max_blocks;
 
-    // ---- this warp's keys
-    uint4 raw[kWTiles][2][kChunks];
-    const int w0 = tok0 + warp * kWTiles * kTile;
-    bool there[kWTiles];
-#pragma unroll
-    for (int i = 0; i < kWTiles; ++i) {
-        const int at = w0 + i * kTile;
-        there[i] = at < L;
-        int phys = 0;
-        if (there[i]) {
-            phys = a.tables[static_cast<int64_t>(b) * a.max_blocks + at / bs];
-            if (phys < 0 || phys >= a.num_blocks) {
-                if (lane == 0 && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-                there[i] = false;
-                phys = 0;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int tok = at + g + 8 * r;
-            const bool ok = there[i] && tok < L;
-            const uint8_t *row = a.keys + ((static_cast<int64_t>(phys) * bs + tok % bs) * a.Hkv + h) * kRowBytes + 16 * t;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) raw[i][r][c] = ok ? load_once(row + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
-        }
+    if (warp == kXMmaWarp) tc5::tmem_alloc(tmem_slot, tmem_cols);
+    if (tid == 0) {
+        for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], kXMmaWarp - kXLoadWarp), mbar_init(&kempty[i], 1u);
+        for (int i = 0; i < 2; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], 4u);
+        mbar_init(drain, 1u);
+        *abort_flag = 0;
     }
+    fence_barrier_init();
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return mbar_try_wait(bar, parity) || mbar_wait_or_abort_slow(bar, parity, abort_flag, a.status);
+    };
 
-    // ---- the columns
-    float sum[kWTiles][2] = {};
-    for (int c0 = 0; c0 < n_cols; c0 += kWColumns) {
-        const int here = min(kWColumns, n_cols - c0), tiles = (here + 7) / 8;
-        if (c0) __syncthreads();
-        load_columns<F8, D>(a, b, h, first_new, c0, here, qs, lse_s, last_s);
-        __syncthreads();
-        for (int nt = 0; nt < tiles; ++nt) {
-            float acc[kWTiles][4] = {};
+    const bool loads = warp >= kXLoadWarp && warp < kXMmaWarp;
+    bool good = true;
+    uint32_t tmem = 0;
+    int it = 0;   // tiles of the chunks before this one
+    for (int c0 = 0; c0 < n_cols; c0 += n_most, it += tiles) {
+        const int here = min(n_most, n_cols - c0), N = (here + 15) / 16 * 16;
+        const bool first = c0 == 0, final = c0 + here == n_cols;
+        // (the chunk before this one is read; TMEM and the barriers are set up)
+        if (__syncthreads_or(!first && *abort_flag != 0)) break;
+        tmem = *tmem_slot;
+        for (int i = tid; i < N * (D / 8); i += kXThreads) {
+            const int n = i / (D / 8), ch = i % (D / 8);
+            const int64_t row = (static_cast<int64_t>(b) * a.q_len + (c0 + n) / a.G) * a.Hkv * a.G + h * a.G + (c0 + n) % a.G;
+            uint4 w = n < here ? *reinterpret_cast<const uint4 *>(a.q + row * D + 8 * ch) : make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (F8)
+                w = make_uint4(to_f16x2(bf16lo(w.x), bf16hi(w.x)), to_f16x2(bf16lo(w.y), bf16hi(w.y)),
+                               to_f16x2(bf16lo(w.z), bf16hi(w.z)), to_f16x2(bf16lo(w.w), bf16hi(w.w)));
+            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * (N * kSubBytes) + swz128(n, ch & 7)) = w;
+        }
+        bool no_lse = false;
+        for (int n = tid; n < N; n += kXThreads) {
+            const int i = (c0 + n) / a.G;
+            const int64_t row = (static_cast<int64_t>(b) * a.q_len + i) * a.Hkv * a.G + h * a.G + (c0 + n) % a.G;
+            const float lse = n < here ? a.lse[row] : 0.f;
+            nl[n] = -lse * 1.4426950408889634f;
+            last_s[n] = lse == -INFINITY ? -1 : first_new + i;
+            no_lse = no_lse || lse == -INFINITY;
+        }
+        fence_proxy_async_smem();
+        tc5::fence_before_sync();
+        const bool odd = __syncthreads_or(no_lse);  // a column of the chunk has no lse
+        tc5::fence_after_sync();
+
+        if (loads) {
+            // a loading warp's 16 rows of a tile: kPer chunks of 16 bytes a lane
+            constexpr int kRowChunks = D * (F8 ? 1 : 2) / 16, kPer = kXLoadRows * kRowChunks / 32;
+            constexpr int kRowsAtOnce = 32 / kRowChunks;
+            uint4 k[kPer];
+            auto load = [&](int tile) {
+                const int mine = tok0 + tile * kXRows + (warp - kXLoadWarp) * kXLoadRows + lane;   // lane's token: its place
+                int place = -1;
+                if (lane < kXLoadRows && mine < L) {
+                    const int phys = table[mine / bs];
+                    if (phys >= 0 && phys < a.num_blocks) place = phys * bs + mine % bs;
+                    else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                }
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                uint4 w[Chunk<F8>::kVecs];
+                for (int j = 0; j < kPer; ++j) {
+                    const int at = __shfl_sync(0xffffffffu, place, j * kRowsAtOnce + lane / kRowChunks);
+                    k[j] = at >= 0 ? load_once(a.keys + (static_cast<int64_t>(at) * a.Hkv + h) * (D * (F8 ? 1 : 2)) + 16 * (lane % kRowChunks))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto store = [&](uint8_t *stage) {
 #pragma unroll
-                for (int k = 0; k < Chunk<F8>::kVecs; ++k) w[k] = qs[(nt * kVecs + c * Chunk<F8>::kVecs + k) * 32 + lane];
+                for (int j = 0; j < kPer; ++j) {
+                    const int r = (warp - kXLoadWarp) * kXLoadRows + j * kRowsAtOnce + lane / kRowChunks, c = lane % kRowChunks;
+                    uint4 w[Chunk<F8>::kVecs];
+                    widen<F8>(k[j], w);
 #pragma unroll
-                for (int i = 0; i < kWTiles; ++i) {
-                    uint4 x[Chunk<F8>::kVecs], y[Chunk<F8>::kVecs];
-                    widen<F8>(raw[i][0][c], x);
-                    widen<F8>(raw[i][1][c], y);
-#pragma unroll
-                    for (int k = 0; k < Chunk<F8>::kVecs; ++k) {
-                        mma_16x8x16<F8>(acc[i], x[k].x, y[k].x, x[k].y, y[k].y, w[k].x, w[k].y);
-                        mma_16x8x16<F8>(acc[i], x[k].z, y[k].z, x[k].w, y[k].w, w[k].z, w[k].w);
+                    for (int v = 0; v < Chunk<F8>::kVecs; ++v) {
+                        const int ch = c * Chunk<F8>::kVecs + v;
+                        *reinterpret_cast<uint4 *>(stage + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7)) = w[v];
                     }
                 }
+            };
+            load(0);
+            for (int i = 0; i < tiles && good; ++i) {
+                const int u = it + i, s = u % kXStages;
+                if (u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
+                if (!good) break;
+                store(smem + s * X::kStageBytes);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kfull[s]);
+                if (i + 1 < tiles) load(i + 1);
             }
+        } else if (warp == kXMmaWarp) {
+            if (lane == 0) {
+                const uint32_t idesc = tc5::idesc_bf16_f32(kXRows, N, false, false, F8);
+                for (int i = 0; i < tiles && good; ++i) {
+                    const int u = it + i, s = u % kXStages, buf = u & 1;
+                    good = (u < 2 || wait(&sfree[buf], (u / 2 - 1) & 1)) && wait(&kfull[s], (u / kXStages) & 1);
+                    if (!good) break;
+                    tc5::fence_after_sync();
+                    const uint8_t *kt = smem + s * X::kStageBytes;
 #pragma unroll
-            for (int i = 0; i < kWTiles; ++i)
-                add_columns(sum[i], acc[i], a.scale_log2, lse_s + nt * 8 + 2 * t, last_s + nt * 8 + 2 * t, w0 + i * kTile + g);
+                    for (int j = 0; j < D / 16; ++j) {
+                        const int half = j >> 2, off = (j & 3) * 32;
+                        tc5::mma_bf16(tmem + buf * (tmem_cols / 2), tc5::sw128_desc(kt + half * (kXRows * kSubBytes) + off, 16, 1024),
+                                      tc5::sw128_desc(qs + half * (N * kSubBytes) + off, 16, 1024), idesc, j > 0);
+                    }
+                    tc5::commit(&kempty[s]);
+                    tc5::commit(&sdone[buf]);
+                }
+                if (!good) {  // let what was issued finish before TMEM is freed
+                    tc5::commit(drain);
+                    mbar_wait_bounded(drain, 0);
+                }
+            }
+            __syncwarp();
+        } else {
+            const int group = warp >> 2, r = tid & 127;   // this thread's row
+            for (int i = 0; i < tiles && good; ++i) {
+                const int u = it + i;
+                if ((u & 1) != group) continue;
+                const int tok = tok0 + i * kXRows + r;
+                int phys = 0;
+                float was = 0.f;
+                if (final && tok < L) {
+                    phys = table[tok / bs];
+                    if (tok < first_new) was = a.old[(static_cast<int64_t>(b) * a.Hkv + h) * a.room + tok];
+                }
+                good = __all_sync(0xffffffffu, wait(&sdone[group], (u / 2) & 1));
+                if (!good) break;
+                tc5::fence_after_sync();
+                const uint32_t at = tc5::taddr(tmem, 32 * (warp & 3), group * (tmem_cols / 2));
+                // (a tile with new tokens has queries that do not see all of it)
+                const bool all = !odd && tok0 + (i + 1) * kXRows <= first_new;
+                float v = all ? row_sum<false>(at, here, a.scale_log2, nl, last_s, tok)
+                              : row_sum<true>(at, here, a.scale_log2, nl, last_s, tok);
+                tc5::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfree[group]);
+                if (!first) v += sums[i * kXRows + r];
+                if (!final) {
+                    sums[i * kXRows + r] = v;
+                } else if (tok < L) {
+                    const int64_t x = (static_cast<int64_t>(b) * a.Hkv + h) * a.room + tok;
+                    if (phys < 0 || phys >= a.num_blocks) v = 0.f;
+                    const bool fresh = tok >= first_new;
+                    a.out[x] = fresh ? v : fmaf(a.decay, was, v);
+                    if (fresh && a.positions) a.positions[x] = tok + (a.ends ? a.ends[b] - L : 0);
+                }
+            }
         }
     }
-
-    // ---- the four lanes of a token, and what it had
-    const int64_t base = (static_cast<int64_t>(b) * a.Hkv + h) * a.room;
-    const int shift = a.ends ? a.ends[b] - L : 0;  // a token's position less its place
-#pragma unroll
-    for (int i = 0; i < kWTiles; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float s = sum[i][r];
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            const int tok = w0 + i * kTile + g + 8 * r;
-            if (t != 0 || tok >= L) continue;
-            if (!there[i]) s = 0.f;
-            const bool fresh = tok >= first_new;
-            a.out[base + tok] = fresh ? s : fmaf(a.decay, a.old[base + tok], s);
-            if (fresh && a.positions) a.positions[base + tok] = tok + shift;
-        }
+    tc5::fence_before_sync();
+    __syncthreads();
+    if (warp == kXMmaWarp) tc5::tmem_free(tmem, tmem_cols);
 }
 
 template <bool F8, int D>
@@ -325,10 +472,33 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
                                         dim3(static_cast<unsigned>((most + span - 1) / span), a.Hkv, B), kWThreads, 0, stream,
                                         false, pdl_on(), a, pairs);
     }
-    const int smem = static_cast<int>((std::min<int64_t>(kWColumns, columns) + 7) / 8 * 8) * D * 2;
-    return launch_maybe_cooperative(weights_wide_kernel<F8, D>,
-                                    dim3(static_cast<unsigned>((most + kWTokens - 1) / kWTokens), a.Hkv, B), kWThreads, smem,
-                                    stream, false, pdl_on(), a);
+    // 256 columns at a time, or shares of them that differ by little
+    const int64_t chunks = (columns + kXColumns - 1) / kXColumns;
+    const int n_most = static_cast<int>(((columns + chunks - 1) / chunks + 15) / 16 * 16);
+    uint32_t cols = 64;  // of TMEM: two buffers
+    while (cols < 2u * n_most) cols *= 2;
+    // the tiles of a CTA: the fewest rounds of tiles over all SMs, a CTA's start counted as two
+    const int64_t tiles = (most + kXRows - 1) / kXRows, rows = static_cast<int64_t>(a.Hkv) * B, sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int n = 1; n <= kXMostTiles; ++n) {
+        const int64_t c = ((tiles + n - 1) / n * rows + sms - 1) / sms * (std::min<int64_t>(n, tiles) * chunks + 2);
+        if (c < cost) cost = c, best = n;
+    }
+    auto kern = weights_tc_kernel<F8, D>;
+    static std::atomic<uint64_t> smem_attr_done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XShape<D>::bytes(kXColumns));
+        if (e != cudaSuccess) return e;
+        smem_attr_done.fetch_or(bit, std::memory_order_release);
+    }
+    return launch_maybe_cooperative(kern, dim3(static_cast<unsigned>((tiles + best - 1) / best), a.Hkv, B), kXThreads,
+                                    XShape<D>::bytes(n_most), stream, false, pdl_on(), a, best, n_most, cols);
 }
 
 int weights_add(float *new_weights, const float *weights, int32_t *positions, const void *q, int32_t q_len, const float *lse,
