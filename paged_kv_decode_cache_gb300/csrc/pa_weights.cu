@@ -216,72 +216,69 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 //
 // Warps 0-7 (two groups of four): the exponentials of every second tile; a group's lane is the
 // token.  Warps 8-15: keys from the pool into a ring of 32 KB stages, as the MMA reads them
-// (K-major, 128-byte swizzle; e4m3 codes widened to fp16 on the way); a tile's loads are in
-// registers while its stage is still read.  Warp 16: issues the MMAs.  Every wait is bounded.
+// (K-major, 128-byte swizzle; e4m3 codes widened to fp16 on the way), by asynchronous copies
+// two tiles ahead.  Warp 16: issues the MMAs.  Every wait is bounded.
 constexpr int kXThreads = 17 * 32;
 constexpr int kXLoadWarp = 8, kXMmaWarp = 16;
 constexpr int kXLoadRows = 16;           // tokens of a loading warp
 constexpr int kXRows = 128;              // tokens of a tile
-constexpr int kXStages = 3;
+constexpr int kXAhead = 2;               // tiles whose copies are on their way
+constexpr int kXCodes = kXAhead + 1;     // FP8: tiles in the ring of codes
 constexpr int kXMostTiles = 32;          // of a CTA
 constexpr int kXColumns = 256;           // at once
 
-template <int D>
+template <bool F8, int D>
 struct XShape {
     static constexpr int kHalves = D / 64;                       // 64-element sub-rows
+    static constexpr int kStages = F8 ? 2 : 4;
     static constexpr int kStageBytes = kHalves * kXRows * kSubBytes;
-    // dynamic shared memory: stages, queries, sums, -lse, last tokens, barriers
+    // dynamic shared memory: stages, codes, queries, sums, -lse, last tokens, barriers
+    static constexpr int kCodeBytes = F8 ? kXCodes * kXRows * D : 0;
     static constexpr int q_bytes(int n) { return kHalves * n * kSubBytes; }
-    static constexpr int sums_at(int n) { return kXStages * kStageBytes + q_bytes(n); }
+    static constexpr int q_at() { return kStages * kStageBytes + kCodeBytes; }
+    static constexpr int sums_at(int n) { return q_at() + q_bytes(n); }
     static constexpr int bytes(int n) {
-        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + (2 * kXStages + 5) * 8 + 16 + 1024;
+        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
     }
 };
 
-// The sum over columns [n0, n1) of a row in TMEM of 2^(s scale + nl): 16 columns at a time, the next
-// ones on their way.  kMasked: only columns that see token tok.
+// The sum over the columns below n1 of a row in TMEM of 2^(s scale + nl), 32 at a time, in four
+// sums (a single chain of additions would take as long as the exponentials).  kMasked: only
+// columns that see token tok.
 template <bool kMasked>
 __device__ __forceinline__ float row_sum(uint32_t row, int n1, float scale, const float *nl, const int *last, int tok) {
-    uint32_t cur[16], nxt[16];
-    uint64_t sum2 = 0;
-    float sum = 0.f;
-    const uint64_t scale2 = pack2(scale, scale);
-    tc5::ld_32x32b_x16_nowait(row, cur);
-    tc5::wait_ld();
-    for (int n = 0; n < n1; n += 16) {
-        if (n + 16 < n1) tc5::ld_32x32b_x16_nowait(row + n + 16, nxt);
-        if (!kMasked && n + 16 <= n1) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const ulonglong2 z = *reinterpret_cast<const ulonglong2 *>(nl + n + i);
-                const uint64_t a = fma2(pack2(__uint_as_float(cur[i]), __uint_as_float(cur[i + 1])), scale2, z.x);
-                const uint64_t b = fma2(pack2(__uint_as_float(cur[i + 2]), __uint_as_float(cur[i + 3])), scale2, z.y);
-                float e[4];
-                unpack2(a, e[0], e[1]);
-                unpack2(b, e[2], e[3]);
-                sum2 = add2(sum2, pack2(fast_exp2(e[0]), fast_exp2(e[1])));
-                sum2 = add2(sum2, pack2(fast_exp2(e[2]), fast_exp2(e[3])));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (n + i < n1 && (!kMasked || tok <= last[n + i])) sum += fast_exp2(fmaf(__uint_as_float(cur[i]), scale, nl[n + i]));
-        }
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t x[32];
+    int n = 0;
+    for (; !kMasked && n + 32 <= n1; n += 32) {
+        tc5::ld_32x32b_x32_nowait(row + n, x);
         tc5::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) cur[i] = nxt[i];
+        for (int i = 0; i < 32; i += 4) {
+            const float4 z = *reinterpret_cast<const float4 *>(nl + n + i);
+            sum[0] += fast_exp2(fmaf(__uint_as_float(x[i]), scale, z.x));
+            sum[1] += fast_exp2(fmaf(__uint_as_float(x[i + 1]), scale, z.y));
+            sum[2] += fast_exp2(fmaf(__uint_as_float(x[i + 2]), scale, z.z));
+            sum[3] += fast_exp2(fmaf(__uint_as_float(x[i + 3]), scale, z.w));
+        }
     }
-    float a, b;
-    unpack2(sum2, a, b);
-    return sum + (a + b);
+    for (; n < n1; n += 32) {
+        tc5::ld_32x32b_x32_nowait(row + n, x);
+        tc5::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (n + i < n1 && (!kMasked || tok <= last[n + i])) sum[i & 3] += fast_exp2(fmaf(__uint_as_float(x[i]), scale, nl[n + i]));
+    }
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 template <bool F8, int D>
 __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsArgs a, int tiles_max, int n_most, uint32_t tmem_cols) {
-    using X = XShape<D>;
+    using X = XShape<F8, D>;
+    constexpr int kXStages = X::kStages;
     extern __shared__ uint8_t x_smem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(x_smem) + 1023) & ~uintptr_t(1023));
-    uint8_t *qs = smem + kXStages * X::kStageBytes;
+    uint8_t *codes = smem + kXStages * X::kStageBytes, *qs = smem + X::q_at();
     float *sums = reinterpret_cast<float *>(smem + X::sums_at(n_most));      // [tiles][128], over the chunks of columns
     float *nl = sums + kXMostTiles * kXRows;                                  // -lse of every column, log2 units
     int *last_s = reinterpret_cast<int *>(nl + kXColumns);                    // last token that it sees
@@ -351,49 +348,69 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
         tc5::fence_after_sync();
 
         if (loads) {
-            // a loading warp's 16 rows of a tile: kPer chunks of 16 bytes a lane
+            // A loading warp's 16 rows of a tile: kPer chunks of 16 bytes a lane, copied
+            // asynchronously kXAhead tiles ahead, straight into the stage, or (FP8) into the
+            // lane's own part of a ring of codes, which it widens into the stage later.
             constexpr int kRowChunks = D * (F8 ? 1 : 2) / 16, kPer = kXLoadRows * kRowChunks / 32;
             constexpr int kRowsAtOnce = 32 / kRowChunks;
-            uint4 k[kPer];
-            auto load = [&](int tile) {
-                const int mine = tok0 + tile * kXRows + (warp - kXLoadWarp) * kXLoadRows + lane;   // lane's token: its place
-                int place = -1;
-                if (lane < kXLoadRows && mine < L) {
-                    const int phys = table[mine / bs];
-                    if (phys >= 0 && phys < a.num_blocks) place = phys * bs + mine % bs;
-                    else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-                }
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int at = __shfl_sync(0xffffffffu, place, j * kRowsAtOnce + lane / kRowChunks);
-                    k[j] = at >= 0 ? load_once(a.keys + (static_cast<int64_t>(at) * a.Hkv + h) * (D * (F8 ? 1 : 2)) + 16 * (lane % kRowChunks))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                }
+            const int lw = warp - kXLoadWarp;
+            uint8_t *own = codes + (lw * 32 + lane) * 16;
+            auto place_of = [&](int i) {  // of this lane's token (lanes 0 to 15) of tile i in the pool
+                const int mine = tok0 + i * kXRows + lw * kXLoadRows + lane;
+                if (lane >= kXLoadRows || i >= tiles || mine >= L) return -1;
+                const int phys = table[mine / bs];
+                if (phys >= 0 && phys < a.num_blocks) return phys * bs + mine % bs;
+                if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                return -1;
             };
-            auto store = [&](uint8_t *stage) {
+            int place = place_of(0);
+            auto issue = [&](int i) {  // tile i: one commit group
+                const int now = place;
+                place = place_of(i + 1);
+                if (i < tiles) {
+                    const int u = it + i;
+                    if (!F8 && u >= kXStages) good = good && __all_sync(0xffffffffu, wait(&kempty[u % kXStages], (u / kXStages - 1) & 1));
+                    if (good) {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int r = (warp - kXLoadWarp) * kXLoadRows + j * kRowsAtOnce + lane / kRowChunks, c = lane % kRowChunks;
-                    uint4 w[Chunk<F8>::kVecs];
-                    widen<F8>(k[j], w);
-#pragma unroll
-                    for (int v = 0; v < Chunk<F8>::kVecs; ++v) {
-                        const int ch = c * Chunk<F8>::kVecs + v;
-                        *reinterpret_cast<uint4 *>(stage + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7)) = w[v];
+                        for (int j = 0; j < kPer; ++j) {
+                            const int at = __shfl_sync(0xffffffffu, now, j * kRowsAtOnce + lane / kRowChunks);
+                            const int r = lw * kXLoadRows + j * kRowsAtOnce + lane / kRowChunks, ch = lane % kRowChunks;
+                            const uint8_t *from = a.keys + (static_cast<int64_t>(max(at, 0)) * a.Hkv + h) * (D * (F8 ? 1 : 2)) + 16 * ch;
+                            uint8_t *to = F8 ? own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512
+                                             : smem + (u % kXStages) * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7);
+                            cp_async_16_or_zero(to, from, at >= 0);
+                        }
                     }
                 }
+                cp_async_commit();
             };
-            load(0);
+#pragma unroll
+            for (int i = 0; i < kXAhead; ++i) issue(i);
             for (int i = 0; i < tiles && good; ++i) {
+                issue(i + kXAhead);
+                cp_async_wait<kXAhead>();
                 const int u = it + i, s = u % kXStages;
-                if (u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
+                if constexpr (F8) {
+                    if (u >= kXStages) good = good && __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
+                    if (!good) break;
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        const int r = lw * kXLoadRows + j * kRowsAtOnce + lane / kRowChunks, c = lane % kRowChunks;
+                        uint4 w[Chunk<F8>::kVecs];
+                        widen<F8>(*reinterpret_cast<const uint4 *>(own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512), w);
+#pragma unroll
+                        for (int v = 0; v < Chunk<F8>::kVecs; ++v) {
+                            const int ch = c * Chunk<F8>::kVecs + v;
+                            *reinterpret_cast<uint4 *>(smem + s * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7)) = w[v];
+                        }
+                    }
+                }
                 if (!good) break;
-                store(smem + s * X::kStageBytes);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kfull[s]);
-                if (i + 1 < tiles) load(i + 1);
             }
+            cp_async_wait<0>();
         } else if (warp == kXMmaWarp) {
             if (lane == 0) {
                 const uint32_t idesc = tc5::idesc_bf16_f32(kXRows, N, false, false, F8);
@@ -475,8 +492,8 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
     // 256 columns at a time, or shares of them that differ by little
     const int64_t chunks = (columns + kXColumns - 1) / kXColumns;
     const int n_most = static_cast<int>(((columns + chunks - 1) / chunks + 15) / 16 * 16);
-    uint32_t cols = 64;  // of TMEM: two buffers
-    while (cols < 2u * n_most) cols *= 2;
+    uint32_t cols = 64;  // of TMEM: two buffers, each read in 32 columns
+    while (cols < 2u * ((n_most + 31) / 32 * 32)) cols *= 2;
     // the tiles of a CTA: the fewest rounds of tiles over all SMs, a CTA's start counted as two
     const int64_t tiles = (most + kXRows - 1) / kXRows, rows = static_cast<int64_t>(a.Hkv) * B, sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
@@ -493,12 +510,12 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XShape<D>::bytes(kXColumns));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XShape<F8, D>::bytes(kXColumns));
         if (e != cudaSuccess) return e;
         smem_attr_done.fetch_or(bit, std::memory_order_release);
     }
     return launch_maybe_cooperative(kern, dim3(static_cast<unsigned>((tiles + best - 1) / best), a.Hkv, B), kXThreads,
-                                    XShape<D>::bytes(n_most), stream, false, pdl_on(), a, best, n_most, cols);
+                                    XShape<F8, D>::bytes(n_most), stream, false, pdl_on(), a, best, n_most, cols);
 }
 
 int weights_add(float *new_weights, const float *weights, int32_t *positions, const void *q, int32_t q_len, const float *lse,
