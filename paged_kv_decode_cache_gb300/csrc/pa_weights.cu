@@ -215,14 +215,15 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 // 8 N clocks, the MMA 4 N, and the tile's keys come in meanwhile.
 //
 // Warps 0-7 (two groups of four): the exponentials of every second tile; a group's lane is the
-// token.  Warps 8-15: keys from the pool into a ring of 32 KB stages, as the MMA reads them
-// (K-major, 128-byte swizzle; e4m3 codes widened to fp16 on the way), by asynchronous copies
-// two tiles ahead.  Warp 16: issues the MMAs.  Every wait is bounded.
+// token.  TMEM is in quarters, two per group, so that a group has the next scores while
+// the MMA makes those after them (with one buffer per group it waited 1.1 of 2.8 us).  Warps 8-15: keys from the pool into a ring of 32 KB stages, as the MMA reads them
+// (K-major, 128-byte swizzle; e4m3 codes widened to fp16 on the way), by asynchronous copies.
+// Warp 16: issues the MMAs.  Every wait is bounded.
 constexpr int kXThreads = 17 * 32;
 constexpr int kXLoadWarp = 8, kXMmaWarp = 16;
 constexpr int kXLoadRows = 16;           // tokens of a loading warp
 constexpr int kXRows = 128;              // tokens of a tile
-constexpr int kXAhead = 2;               // tiles whose copies are on their way
+constexpr int kXAhead = 2;               // FP8: tiles whose copies are on their way
 constexpr int kXCodes = kXAhead + 1;     // FP8: tiles in the ring of codes
 constexpr int kXMostTiles = 32;          // of a CTA
 constexpr int kXColumns = 256;           // at once
@@ -238,7 +239,7 @@ struct XShape {
     static constexpr int q_at() { return kStages * kStageBytes + kCodeBytes; }
     static constexpr int sums_at(int n) { return q_at() + q_bytes(n); }
     static constexpr int bytes(int n) {
-        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
+        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + (2 * kStages + 9) * 8 + 16 + 1024;
     }
 };
 
@@ -248,26 +249,40 @@ struct XShape {
 template <bool kMasked>
 __device__ __forceinline__ float row_sum(uint32_t row, int n1, float scale, const float *nl, const int *last, int tok) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t x[32];
+    auto add4 = [&](const uint32_t *x, int n) {
+        const float4 z = *reinterpret_cast<const float4 *>(nl + n);
+        const float e[4] = {fast_exp2(fmaf(__uint_as_float(x[0]), scale, z.x)), fast_exp2(fmaf(__uint_as_float(x[1]), scale, z.y)),
+                            fast_exp2(fmaf(__uint_as_float(x[2]), scale, z.z)), fast_exp2(fmaf(__uint_as_float(x[3]), scale, z.w))};
+        int4 l;
+        if (kMasked) l = *reinterpret_cast<const int4 *>(last + n);
+        sum[0] += !kMasked || tok <= l.x ? e[0] : 0.f;
+        sum[1] += !kMasked || tok <= l.y ? e[1] : 0.f;
+        sum[2] += !kMasked || tok <= l.z ? e[2] : 0.f;
+        sum[3] += !kMasked || tok <= l.w ? e[3] : 0.f;
+    };
     int n = 0;
-    for (; !kMasked && n + 32 <= n1; n += 32) {
+    for (; n + 32 <= n1; n += 32) {
+        uint32_t x[32];
         tc5::ld_32x32b_x32_nowait(row + n, x);
         tc5::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 z = *reinterpret_cast<const float4 *>(nl + n + i);
-            sum[0] += fast_exp2(fmaf(__uint_as_float(x[i]), scale, z.x));
-            sum[1] += fast_exp2(fmaf(__uint_as_float(x[i + 1]), scale, z.y));
-            sum[2] += fast_exp2(fmaf(__uint_as_float(x[i + 2]), scale, z.z));
-            sum[3] += fast_exp2(fmaf(__uint_as_float(x[i + 3]), scale, z.w));
-        }
+        for (int i = 0; i < 32; i += 4) add4(x + i, n + i);
     }
-    for (; n < n1; n += 32) {
-        tc5::ld_32x32b_x32_nowait(row + n, x);
+    for (; n < n1; n += 16) {
+        uint32_t x[16];
+        tc5::ld_32x32b_x16_nowait(row + n, x);
         tc5::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (n + i < n1 && (!kMasked || tok <= last[n + i])) sum[i & 3] += fast_exp2(fmaf(__uint_as_float(x[i]), scale, nl[n + i]));
+        for (int i = 0; i < 16; i += 4) {
+            if (n + i + 4 <= n1) {
+                add4(x + i, n + i);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (n + i + j < n1 && (!kMasked || tok <= last[n + i + j]))
+                        sum[j] += fast_exp2(fmaf(__uint_as_float(x[i + j]), scale, nl[n + i + j]));
+            }
+        }
     }
     return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
@@ -283,7 +298,7 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
     float *nl = sums + kXMostTiles * kXRows;                                  // -lse of every column, log2 units
     int *last_s = reinterpret_cast<int *>(nl + kXColumns);                    // last token that it sees
     uint64_t *bars = reinterpret_cast<uint64_t *>(last_s + kXColumns);
-    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 2, *drain = sfree + 2;
+    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 4, *drain = sfree + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -304,8 +319,8 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
 
     if (warp == kXMmaWarp) tc5::tmem_alloc(tmem_slot, tmem_cols);
     if (tid == 0) {
-        for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], kXMmaWarp - kXLoadWarp), mbar_init(&kempty[i], 1u);
-        for (int i = 0; i < 2; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], 4u);
+        for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], 32 * (kXMmaWarp - kXLoadWarp)), mbar_init(&kempty[i], 1u);
+        for (int i = 0; i < 4; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], 4u);
         mbar_init(drain, 1u);
         *abort_flag = 0;
     }
@@ -321,6 +336,11 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
     for (int c0 = 0; c0 < n_cols; c0 += n_most, it += tiles) {
         const int here = min(n_most, n_cols - c0), N = (here + 15) / 16 * 16;
         const bool first = c0 == 0, final = c0 + here == n_cols;
+        // TMEM holds four quarters, two for each group of warps: the two parts of a tile's columns, or
+        // (up to 128 columns) two tiles of the group in turn
+        const int parts = n_most > kXColumns / 2 ? 2 : 1, part = parts == 1 ? N : (N / 2 + 31) / 32 * 32;
+        auto quarter = [&](int u, int e) { return 2 * (u & 1) + (parts == 2 ? e : (u >> 1) & 1); };
+        auto turn = [&](int u) { return parts == 2 ? u >> 1 : u >> 2; };   // how often it was used before
         // (the chunk before this one is read; TMEM and the barriers are set up)
         if (__syncthreads_or(!first && *abort_flag != 0)) break;
         tmem = *tmem_slot;
@@ -349,48 +369,56 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
 
         if (loads) {
             // A loading warp's 16 rows of a tile: kPer chunks of 16 bytes a lane, copied
-            // asynchronously kXAhead tiles ahead, straight into the stage, or (FP8) into the
-            // lane's own part of a ring of codes, which it widens into the stage later.
+            // asynchronously straight into the stage, whose barrier their completion arrives on;
+            // or (FP8), kXAhead tiles ahead, into the lane's own part of a ring of codes, which it
+            // widens into the stage later.  The fence to the MMA's proxy is the MMA warp's, after
+            // that barrier: here it would wait for the copies of the next tiles, too (1.6 us a
+            // tile).
             constexpr int kRowChunks = D * (F8 ? 1 : 2) / 16, kPer = kXLoadRows * kRowChunks / 32;
             constexpr int kRowsAtOnce = 32 / kRowChunks;
             const int lw = warp - kXLoadWarp;
             uint8_t *own = codes + (lw * 32 + lane) * 16;
-            auto place_of = [&](int i) {  // of this lane's token (lanes 0 to 15) of tile i in the pool
-                const int mine = tok0 + i * kXRows + lw * kXLoadRows + lane;
-                if (lane >= kXLoadRows || i >= tiles || mine >= L) return -1;
-                const int phys = table[mine / bs];
-                if (phys >= 0 && phys < a.num_blocks) return phys * bs + mine % bs;
-                if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-                return -1;
-            };
-            int place = place_of(0);
-            auto issue = [&](int i) {  // tile i: one commit group
-                const int now = place;
-                place = place_of(i + 1);
-                if (i < tiles) {
+            // (its rows of a tile lie in one block: lane i knows their place in the pool for tile i)
+            static_assert(kXLoadRows == kTile && kXMostTiles == 32, "a place per lane");
+            int places = -1;
+            const int row0 = tok0 + lane * kXRows + lw * kXLoadRows;
+            if (lane < tiles && row0 < L) {
+                const int phys = table[row0 / bs];
+                if (phys >= 0 && phys < a.num_blocks) places = phys * bs + row0 % bs;
+                else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+            }
+            const uint8_t *keys = a.keys + static_cast<int64_t>(h) * (D * (F8 ? 1 : 2)) + 16 * (lane % kRowChunks);
+            const int stride = a.Hkv * D * (F8 ? 1 : 2), my_row = lane / kRowChunks;
+            auto issue = [&](int i) {  // tile i (FP8: one commit group)
+                const int place = __shfl_sync(0xffffffffu, places, i & 31);
+                if (i < tiles && good) {
                     const int u = it + i;
-                    if (!F8 && u >= kXStages) good = good && __all_sync(0xffffffffu, wait(&kempty[u % kXStages], (u / kXStages - 1) & 1));
+                    if (!F8 && u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[u % kXStages], (u / kXStages - 1) & 1));
                     if (good) {
+                        const int left = place >= 0 ? L - (tok0 + i * kXRows + lw * kXLoadRows) : 0;  // rows that are there
+                        const uint8_t *from = keys + static_cast<int64_t>(max(place, 0) + my_row) * stride;
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) {
-                            const int at = __shfl_sync(0xffffffffu, now, j * kRowsAtOnce + lane / kRowChunks);
-                            const int r = lw * kXLoadRows + j * kRowsAtOnce + lane / kRowChunks, ch = lane % kRowChunks;
-                            const uint8_t *from = a.keys + (static_cast<int64_t>(max(at, 0)) * a.Hkv + h) * (D * (F8 ? 1 : 2)) + 16 * ch;
+                            const int r = j * kRowsAtOnce + my_row, ch = lane % kRowChunks;
                             uint8_t *to = F8 ? own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512
-                                             : smem + (u % kXStages) * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7);
-                            cp_async_16_or_zero(to, from, at >= 0);
+                                             : smem + (u % kXStages) * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) +
+                                                   swz128(lw * kXLoadRows + r, ch & 7);
+                            cp_async_16_or_zero(to, from + static_cast<int64_t>(j * kRowsAtOnce) * stride, r < left);
                         }
+                        if (!F8) cp_async_arrive(&kfull[u % kXStages]);
                     }
                 }
-                cp_async_commit();
+                if (F8) cp_async_commit();
             };
+            if constexpr (!F8) {
+                for (int i = 0; i < tiles && good; ++i) issue(i);
+            } else {
 #pragma unroll
-            for (int i = 0; i < kXAhead; ++i) issue(i);
-            for (int i = 0; i < tiles && good; ++i) {
-                issue(i + kXAhead);
-                cp_async_wait<kXAhead>();
-                const int u = it + i, s = u % kXStages;
-                if constexpr (F8) {
+                for (int i = 0; i < kXAhead; ++i) issue(i);
+                for (int i = 0; i < tiles && good; ++i) {
+                    issue(i + kXAhead);
+                    cp_async_wait<kXAhead>();
+                    const int u = it + i, s = u % kXStages;
                     if (u >= kXStages) good = good && __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
                     if (!good) break;
 #pragma unroll
@@ -404,30 +432,36 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
                             *reinterpret_cast<uint4 *>(smem + s * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7)) = w[v];
                         }
                     }
+                    mbar_arrive(&kfull[s]);
                 }
-                if (!good) break;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kfull[s]);
             }
             cp_async_wait<0>();
         } else if (warp == kXMmaWarp) {
             if (lane == 0) {
-                const uint32_t idesc = tc5::idesc_bf16_f32(kXRows, N, false, false, F8);
+                // (descriptors count 16 bytes: what is added to them is worked out before the loop)
+                const uint64_t k0 = tc5::sw128_desc(smem, 16, 1024), q0 = tc5::sw128_desc(qs, 16, 1024);
+                const uint32_t q_half = static_cast<uint32_t>(N * kSubBytes) >> 4;
+                const uint32_t idesc0 = tc5::idesc_bf16_f32(kXRows, min(part, N), false, false, F8);
+                const uint32_t idesc1 = tc5::idesc_bf16_f32(kXRows, max(N - part, 16), false, false, F8);
                 for (int i = 0; i < tiles && good; ++i) {
-                    const int u = it + i, s = u % kXStages, buf = u & 1;
-                    good = (u < 2 || wait(&sfree[buf], (u / 2 - 1) & 1)) && wait(&kfull[s], (u / kXStages) & 1);
-                    if (!good) break;
-                    tc5::fence_after_sync();
-                    const uint8_t *kt = smem + s * X::kStageBytes;
+                    const int u = it + i, s = u % kXStages;
+                    good = wait(&kfull[s], (u / kXStages) & 1);
+                    fence_proxy_async_smem();  // (the keys are copied and written by the generic proxy)
+                    const uint64_t kd = k0 + static_cast<uint32_t>(s * (X::kStageBytes >> 4));
+                    for (int e = 0; e < parts && good; ++e) {
+                        const int at = quarter(u, e);
+                        good = turn(u) == 0 || wait(&sfree[at], (turn(u) - 1) & 1);
+                        if (!good) break;
+                        tc5::fence_after_sync();
+                        const uint64_t qd = q0 + static_cast<uint32_t>(e * part * (kSubBytes >> 4));
+                        const uint32_t to = tmem + at * (tmem_cols / 4), idesc = e ? idesc1 : idesc0;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        const int half = j >> 2, off = (j & 3) * 32;
-                        tc5::mma_bf16(tmem + buf * (tmem_cols / 2), tc5::sw128_desc(kt + half * (kXRows * kSubBytes) + off, 16, 1024),
-                                      tc5::sw128_desc(qs + half * (N * kSubBytes) + off, 16, 1024), idesc, j > 0);
+                        for (int j = 0; j < D / 16; ++j)
+                            tc5::mma_bf16(to, kd + ((j >> 2) * (kXRows * kSubBytes) + (j & 3) * 32) / 16,
+                                          qd + (j >> 2) * q_half + (j & 3) * 2, idesc, j > 0);
+                        tc5::commit(&sdone[at]);
                     }
-                    tc5::commit(&kempty[s]);
-                    tc5::commit(&sdone[buf]);
+                    if (good) tc5::commit(&kempty[s]);
                 }
                 if (!good) {  // let what was issued finish before TMEM is freed
                     tc5::commit(drain);
@@ -447,17 +481,22 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
                     phys = table[tok / bs];
                     if (tok < first_new) was = a.old[(static_cast<int64_t>(b) * a.Hkv + h) * a.room + tok];
                 }
-                good = __all_sync(0xffffffffu, wait(&sdone[group], (u / 2) & 1));
-                if (!good) break;
-                tc5::fence_after_sync();
-                const uint32_t at = tc5::taddr(tmem, 32 * (warp & 3), group * (tmem_cols / 2));
                 // (a tile with new tokens has queries that do not see all of it)
                 const bool all = !odd && tok0 + (i + 1) * kXRows <= first_new;
-                float v = all ? row_sum<false>(at, here, a.scale_log2, nl, last_s, tok)
-                              : row_sum<true>(at, here, a.scale_log2, nl, last_s, tok);
-                tc5::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfree[group]);
+                float v = 0.f;
+                for (int e = 0; e < parts; ++e) {
+                    const int at = quarter(u, e), n0 = e * part, n1 = min(part, here - n0);
+                    good = __all_sync(0xffffffffu, wait(&sdone[at], turn(u) & 1));
+                    if (!good) break;
+                    tc5::fence_after_sync();
+                    const uint32_t row = tc5::taddr(tmem, 32 * (warp & 3), at * (tmem_cols / 4));
+                    v += all ? row_sum<false>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok)
+                             : row_sum<true>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok);
+                    tc5::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfree[at]);
+                }
+                if (!good) break;
                 if (!first) v += sums[i * kXRows + r];
                 if (!final) {
                     sums[i * kXRows + r] = v;
@@ -492,8 +531,9 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
     // 256 columns at a time, or shares of them that differ by little
     const int64_t chunks = (columns + kXColumns - 1) / kXColumns;
     const int n_most = static_cast<int>(((columns + chunks - 1) / chunks + 15) / 16 * 16);
-    uint32_t cols = 64;  // of TMEM: two buffers, each read in 32 columns
-    while (cols < 2u * ((n_most + 31) / 32 * 32)) cols *= 2;
+    const int quarter = (n_most > kXColumns / 2 ? (n_most / 2 + 31) / 32 * 32 : n_most) + 31;
+    uint32_t cols = 128;  // of TMEM, each quarter read in 32 columns
+    while (cols < 4u * (quarter / 32 * 32)) cols *= 2;
     // the tiles of a CTA: the fewest rounds of tiles over all SMs, a CTA's start counted as two
     const int64_t tiles = (most + kXRows - 1) / kXRows, rows = static_cast<int64_t>(a.Hkv) * B, sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
