@@ -133,18 +133,17 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const Bounds
         const bool mine = slice < a.slices && c < a.row_chunks;
         if (mine && slice < rows) {
             Range<F8> r;
-            const uint4 *at = keys + c;
-            int i = slice;
-            r.take(load_once(at + static_cast<int64_t>(i) * a.row_chunks), true);
-            i += a.slices;
-            for (; i + 3 * a.slices < rows; i += 4 * a.slices) {
-                uint4 v[4];
+            constexpr int kBatch = 8;  // rows on their way together (one after the other, then 4, then 3: 83 us for 16 prompts)
+            for (int i0 = slice; i0 < rows; i0 += kBatch * a.slices) {
+                uint4 v[kBatch];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = load_once(at + static_cast<int64_t>(i + k * a.slices) * a.row_chunks);
+                for (int k = 0; k < kBatch; ++k) {  // (past the last row: the first one again)
+                    const int i = i0 + k * a.slices;
+                    v[k] = load_once(keys + c + static_cast<int64_t>(i < rows ? i : i0) * a.row_chunks);
+                }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r.take(v[k], false);
+                for (int k = 0; k < kBatch; ++k) r.take(v[k], i0 == slice && k == 0);
             }
-            for (; i < rows; i += a.slices) r.take(load_once(at + static_cast<int64_t>(i) * a.row_chunks), false);
             part[0][tid] = Range<F8>::pack(r.lo), part[1][tid] = Range<F8>::pack(r.hi);
         }
         __syncthreads();
