@@ -99,24 +99,47 @@ struct Range {
     }
 };
 
-// A CTA per block that has new tokens.  Thread (slice, chunk) goes through every
-// `slices`-th row of its 16 bytes of channels; the slices meet in shared memory.  Bound by
-// memory: every key of the touched blocks is read once.
+// A sequence's length and its first touched block; false where it has none.
+__device__ __forceinline__ bool touched_blocks(const BoundsArgs &a, int b, bool report, int *len, int *first) {
+    int L = a.lens[b], from = a.starts ? a.starts[b] : 0;
+    const int most = a.max_blocks * a.block_size;
+    bool bad = L < 0 || L > most || from < 0;
+    L = min(max(L, 0), most);
+    from = max(from, 0);
+    if (L - from > a.max_new) bad = true, from = L - a.max_new;
+    if (bad && report) set_status(a.status, PA_STATUS_BAD_SEQLEN);
+    *len = L, *first = from / a.block_size;
+    return from < L;
+}
+
+// The bounds of 16 bytes of channels over rows slice, slice + step, ... of `rows`, kBatch of them on
+// their way together; at: row 0's.
+template <int kBatch, bool F8>
+__device__ __forceinline__ void range_of_rows(Range<F8> &r, const uint4 *at, int64_t stride, int slice, int step, int rows) {
+    for (int i0 = slice; i0 < rows; i0 += kBatch * step) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {  // (past the last row: the batch's first one again)
+            const int i = i0 + k * step;
+            v[k] = load_once(at + (i < rows ? i : i0) * stride);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) r.take(v[k], i0 == slice && k == 0);
+    }
+}
+
+// Few blocks (a decode step's): a CTA per block that has new tokens.  Thread (slice, chunk)
+// goes through every `slices`-th row of its 16 bytes of channels; the slices meet in shared
+// memory.  Bound by the chain length - block id - keys.
 template <bool F8>
 __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const BoundsArgs a) {
     __shared__ uint4 part[2][kBoundsThreads];
     griddep_wait();
     griddep_launch_dependents();
     const int b = blockIdx.y, tid = threadIdx.x, bs = a.block_size;
-    int L = a.lens[b], from = a.starts ? a.starts[b] : 0;
-    const int most = a.max_blocks * bs;
-    bool bad = L < 0 || L > most || from < 0;
-    L = min(max(L, 0), most);
-    from = max(from, 0);
-    if (L - from > a.max_new) bad = true, from = L - a.max_new;
-    if (bad && tid == 0 && blockIdx.x == 0) set_status(a.status, PA_STATUS_BAD_SEQLEN);
-    if (from >= L) return;
-    const int j = from / bs + static_cast<int>(blockIdx.x);
+    int L, first;
+    if (!touched_blocks(a, b, tid == 0 && blockIdx.x == 0, &L, &first)) return;
+    const int j = first + static_cast<int>(blockIdx.x);
     if (j * bs >= L) return;
     const int phys = a.tables[static_cast<int64_t>(b) * a.max_blocks + j];
     if (phys < 0 || phys >= a.num_blocks) {
@@ -133,17 +156,7 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const Bounds
         const bool mine = slice < a.slices && c < a.row_chunks;
         if (mine && slice < rows) {
             Range<F8> r;
-            constexpr int kBatch = 8;  // rows on their way together (one after the other, then 4, then 3: 83 us for 16 prompts)
-            for (int i0 = slice; i0 < rows; i0 += kBatch * a.slices) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {  // (past the last row: the first one again)
-                    const int i = i0 + k * a.slices;
-                    v[k] = load_once(keys + c + static_cast<int64_t>(i < rows ? i : i0) * a.row_chunks);
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) r.take(v[k], i0 == slice && k == 0);
-            }
+            range_of_rows<8>(r, keys + c, a.row_chunks, slice, a.slices, rows);
             part[0][tid] = Range<F8>::pack(r.lo), part[1][tid] = Range<F8>::pack(r.hi);
         }
         __syncthreads();
@@ -158,6 +171,44 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const Bounds
             }
         }
         __syncthreads();
+    }
+}
+
+// Many blocks (whole prompts): a CTA per 4 of them, a thread for 16 bytes of channels of a block, all
+// of its rows.  Bound by memory: every key of the touched blocks is read once (360 MB in 53 us, the
+// rate of a plain copy; 8 rows of a thread on their way leave room for half the threads: 60 us).
+constexpr int kBoundsSpan = 4;
+template <bool F8>
+__global__ void __launch_bounds__(kBoundsThreads) key_bounds_many_kernel(const BoundsArgs a) {
+    __shared__ int32_t ids[kBoundsSpan];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int b = blockIdx.y, tid = threadIdx.x, bs = a.block_size;
+    int L, first;
+    if (!touched_blocks(a, b, tid == 0 && blockIdx.x == 0, &L, &first)) return;
+    const int j0 = first + static_cast<int>(blockIdx.x) * kBoundsSpan;
+    if (j0 * bs >= L) return;
+    if (tid < kBoundsSpan) {
+        int phys = -1;
+        if (j0 + tid < a.max_blocks && (j0 + tid) * bs < L) {
+            phys = a.tables[static_cast<int64_t>(b) * a.max_blocks + j0 + tid];
+            if (phys < 0 || phys >= a.num_blocks) {
+                set_status(a.status, PA_STATUS_BAD_BLOCK);
+                phys = -1;
+            }
+        }
+        ids[tid] = phys;
+    }
+    __syncthreads();
+    for (int i = tid; i < kBoundsSpan * a.row_chunks; i += kBoundsThreads) {
+        const int k = i / a.row_chunks, c = i % a.row_chunks, phys = ids[k];
+        if (phys < 0) continue;
+        Range<F8> r;
+        range_of_rows<4>(r, reinterpret_cast<const uint4 *>(a.keys) + static_cast<int64_t>(phys) * bs * a.row_chunks + c, a.row_chunks,
+                      0, 1, min(bs, L - (j0 + k) * bs));
+        uint4 *out = reinterpret_cast<uint4 *>(a.bounds) + static_cast<int64_t>(phys) * a.row_chunks * 2;
+        out += 2 * (c / a.head_chunks) * a.head_chunks + c % a.head_chunks;
+        out[0] = Range<F8>::pack(r.lo), out[a.head_chunks] = Range<F8>::pack(r.hi);
     }
 }
 
@@ -304,6 +355,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     griddep_wait();
     griddep_launch_dependents();
 
+    // the queries' values, on their way with the length
+    const int64_t row = static_cast<int64_t>(b) * a.Hkv + h;
+    const uint32_t *q2 = reinterpret_cast<const uint32_t *>(a.q + row * a.G * D);
+    for (int i = tid; i < a.G * D / 2; i += kSelThreads) {
+        const uint32_t w = q2[i];
+        *reinterpret_cast<float2 *>(qf + 2 * i) = make_float2(bf16lo(w), bf16hi(w));
+    }
     int L = a.lens[b];
     const int most = a.max_blocks * bs;
     if (L < 0 || L > most) {
@@ -312,7 +370,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     }
     const int n = (L + bs - 1) / bs;  // blocks
     const int32_t *bt = a.tables + static_cast<int64_t>(b) * a.max_blocks;
-    const int64_t row = static_cast<int64_t>(b) * a.Hkv + h;
     int32_t *out = a.sel_tables + row * a.K;
     if (tid == 0 && rank == 0) a.sel_lens[row] = n <= a.K ? L : (a.K - 1) * bs + L - (n - 1) * bs;
     if (n <= a.K) {  // all of them
@@ -332,7 +389,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     const int j0 = min(rank * per, n), j1 = min(j0 + per, n);
     const int n_tiles = (j1 - j0 + 15) / 16;
     int next_id = lane < 16 && j0 + warp * 16 + lane < j1 ? bt[j0 + warp * 16 + lane] : -1;
-    constexpr int kSlots = 8 / kChunks;  // tiles on their way: 64 registers
+    constexpr int kSlots = 1;            // tiles on their way
     uint4 raw[kSlots][2][kChunks];       // rows g and g + 8
     uint32_t ok[kSlots];                 // the tiles' rows that are there
     auto load = [&](int tile, uint4(&k)[2][kChunks], uint32_t &there_all) {
@@ -354,18 +411,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) load(warp + s * kSelWarps, raw[s], ok[s]);
 
-    // ---- the queries: their values, the sums of their |values|, and the MMA's columns
-    const uint16_t *q = a.q + row * a.G * D;
+    // ---- the sums of the queries' |values|, and the MMA's columns
+    __syncthreads();
     for (int head = warp; head < a.G; head += kSelWarps) {
         float s = 0.f, m = 0.f;
         bool fine = true;
 #pragma unroll
-        for (int i = 2 * lane; i < D; i += 64) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(q + head * D + i);
-            const float x = bf16lo(w), y = bf16hi(w);
-            *reinterpret_cast<float2 *>(qf + head * D + i) = make_float2(x, y);
-            fine = fine && fabsf(x) < INFINITY && fabsf(y) < INFINITY;
-            s += fabsf(x) + fabsf(y), m = fmaxf(m, fmaxf(fabsf(x), fabsf(y)));
+        for (int i = lane; i < D; i += 32) {
+            const float x = fabsf(qf[head * D + i]);
+            fine = fine && x < INFINITY;
+            s += x, m = fmaxf(m, x);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -385,6 +440,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     // FP8: the columns are fp16, the queries scaled by a power of two so that the largest is below
     // 2^15 and not below 2^14; what that cuts off small ones is below 2^-39 of the largest
     const int shift = F8 && qmax > 0.f && q_fine ? 14 - ilogbf(qmax) : 0;
+    const float up0 = exp2f(static_cast<float>(shift / 2)), up1 = exp2f(static_cast<float>(shift - shift / 2));
+    const float down0 = 1.f / up0, down1 = 1.f / up1;  // (2^shift itself may lie outside fp32)
     for (int i = tid; i < tiles * kVecs * 32; i += kSelThreads) {
         const int ln = i & 31, v = (i >> 5) % kVecs, head = (i >> 5) / kVecs * 8 + (ln >> 2);
         const int x = vec_dim<F8>(v, ln & 3);
@@ -396,7 +453,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
                 const float u = x >= D ? fmaxf(f[2 * k], 0.f) : fminf(f[2 * k], 0.f);
                 const float y = x >= D ? fmaxf(f[2 * k + 1], 0.f) : fminf(f[2 * k + 1], 0.f);
                 if constexpr (F8) {
-                    w[k] = to_f16x2(scalbnf(u, shift), scalbnf(y, shift));
+                    w[k] = to_f16x2(u * up0 * up1, y * up0 * up1);
                 } else {  // (the values are bf16)
                     w[k] = __float_as_uint(u) >> 16 | (__float_as_uint(y) & 0xffff0000u);
                 }
@@ -443,7 +500,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
                 for (int i = 0; i < 2; ++i) {
                     if (nt * 8 + 2 * t + i < a.G) {
                         // (an overflow of finite values leaves the error infinite: any finite number will do)
-                        const float u = F8 ? scalbnf(acc[i], -shift) : acc[i], v = F8 ? scalbnf(acc[2 + i], -shift) : acc[2 + i];
+                        const float u = F8 ? acc[i] * down0 * down1 : acc[i], v = F8 ? acc[2 + i] * down0 * down1 : acc[2 + i];
                         best[0] = fmaxf(best[0], u == u ? u : 0.f), best[1] = fmaxf(best[1], v == v ? v : 0.f);
                     }
                 }
@@ -665,8 +722,16 @@ int pa_key_bounds(void *bounds, const void *k_cache, int32_t elem_bytes, pa_cach
     a.slices = pa::bounds_slices(a.row_chunks, cache.block_size);
     // so many new tokens lie in at most this many blocks
     const int blocks = std::min(max_blocks_per_seq, (a.max_new - 1 + cache.block_size - 1) / cache.block_size + 1);
-    const cudaError_t e = pa::launch_maybe_cooperative(elem_bytes == 1 ? pa::key_bounds_kernel<true> : pa::key_bounds_kernel<false>,
-                                                       dim3(blocks, B), pa::kBoundsThreads, 0, stream, false, pa::pdl_on(), a);
+    // The kernel for many blocks, where its CTAs fill the GPU several times over (16 prompts of 2048 to
+    // 16384 tokens: 68 us with a CTA per block).
+    const int sms = pa::sm_count();
+    if (sms <= 0) return PA_ECUDA;
+    const bool many = static_cast<int64_t>(blocks) * B >= 32ll * pa::kBoundsSpan * sms;
+    auto kern = many ? (elem_bytes == 1 ? pa::key_bounds_many_kernel<true> : pa::key_bounds_many_kernel<false>)
+                     : (elem_bytes == 1 ? pa::key_bounds_kernel<true> : pa::key_bounds_kernel<false>);
+    const cudaError_t e = pa::launch_maybe_cooperative(
+        kern, dim3(many ? (blocks + pa::kBoundsSpan - 1) / pa::kBoundsSpan : blocks, B), pa::kBoundsThreads, 0, stream, false,
+        pa::pdl_on(), a);
     return e == cudaSuccess ? PA_OK : PA_ECUDA;
 }
 
@@ -696,12 +761,13 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
     a.bounds = static_cast<const uint8_t *>(bounds), a.tables = block_tables, a.lens = seq_lens, a.status = status;
     a.num_blocks = cache.num_blocks, a.block_size = cache.block_size, a.Hkv = cache.num_kv_heads;
     a.G = Hq / cache.num_kv_heads, a.max_blocks = max_blocks_per_seq, a.K = max_selected, a.first = first, a.last = last;
-    // a cluster of eight per row, or of fewer where those would not all be resident at once
+    // a cluster of eight per row, or of fewer where those would run in more than two waves (128 rows of up
+    // to 8192 blocks: 8 CTAs 73 us, 4 70, 2 84, 1 128)
     const int sms = pa::sm_count();
     if (sms <= 0) return PA_ECUDA;
     const int64_t rows = static_cast<int64_t>(B) * cache.num_kv_heads;
     a.ctas = pa::kSelCtas;
-    while (a.ctas > 1 && rows * a.ctas > 2 * sms) a.ctas /= 2;
+    while (a.ctas > 1 && rows * a.ctas > 4 * sms) a.ctas /= 2;
     a.room = max_blocks_per_seq;
     cudaError_t e;
     if (elem_bytes == 1)

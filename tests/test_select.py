@@ -71,6 +71,31 @@ def test_bounds(hkv, d, bs, lens, starts, max_new, fp8):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hkv,d,bs,mb", [(4, 128, 16, 520), (1, 64, 16, 600), (3, 64, 48, 500)])
+def test_bounds_of_many_blocks(hkv, d, bs, mb, fp8):
+    """Tables that would hold enough blocks for the kernel of whole prompts."""
+    rng = random.Random(mb)
+    lens = [0, 1, bs, bs + 1] + [rng.randint(1, 12 * bs) for _ in range(36)]
+    starts = [rng.randint(0, n) if rng.random() < 0.5 else 0 for n in lens]
+    tables, _, nb = layout(lens, bs, seed=mb, extra=mb)
+    k = pool(nb, bs, hkv, d, fp8, 5, tables, lens)
+    before = pool(nb, hkv, 2, d, fp8, 6)
+    got, status = before.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_key_bounds(got, k.cuda(), i32(tables), i32(lens), starts=i32(starts), status=status)
+    assert status.item() == 0 and same_values(got, plain_bounds(before, k, tables, lens, starts, bs))
+    tables[7][0], tables[9][0] = nb, -1
+    got = before.cuda()
+    pa.pa_key_bounds(got, k.cuda(), i32(tables), i32(lens), status=status)
+    good = [t if i not in (7, 9) else [tables[0][0] if x < 0 or x >= nb else x for x in t] for i, t in enumerate(tables)]
+    want = plain_bounds(before, k, [t for i, t in enumerate(good) if i not in (7, 9)],
+                        [n for i, n in enumerate(lens) if i not in (7, 9)], [0] * len(lens), bs)
+    for i in (7, 9):
+        want = plain_bounds(want, k, [good[i]], [lens[i]], [bs], bs)
+    assert status.item() == pa.PA_STATUS_BAD_BLOCK and same_values(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
 def test_bounds_of_nan_infinity_and_zeros(fp8):
     k = encode(torch.zeros(3, 16, 2, 64), fp8)
     if fp8:
