@@ -197,7 +197,7 @@ def _prepare_attend(c, s, g, r):
     s["lse"] = torch.empty(b, c["heads"], dtype=torch.float32, device="cuda")
     if own:  # the workspace that a program keeps
         from paged_kv_decode_cache_gb300 import pa
-        p = pa.pa_auto_num_splits(b, c["heads"], hkv, d, keep, bs)
+        p = pa.pa_selected_num_splits(b, c["heads"], hkv, d, keep, bs)
         s["workspace"] = torch.zeros(max(1, pa.pa_splitkv_workspace_bytes(b, c["heads"], d, p)), dtype=torch.uint8,
                                      device="cuda")
     return s
