@@ -833,8 +833,7 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
  * max_selected]; sel_lens: device int32 [B, Hkv], the tokens of the list, all of its
  * blocks full but the last.  A list without tokens gives out = 0 and lse = -inf.
  * Supported: the shapes of pa_decode_splitkv (FP8: of pa_decode_splitkv_fp8).
- * num_splits 0: pa_auto_num_splits(B, Hq, Hkv, D, max_selected, block_size), or fewer,
- * as many as the workspace holds; workspace: pa_splitkv_workspace_bytes(B,
+ * num_splits 0: pa_selected_num_splits, or fewer, as many as the workspace holds; workspace: pa_splitkv_workspace_bytes(B,
  * Hq, D, P) bytes, with pa_decode_splitkv's contract.
  */
 int pa_decode_selected(void *out, float *lse, const void *q, const void *k_cache,
@@ -849,6 +848,12 @@ int pa_decode_selected_fp8(void *out, float *lse, const void *q, const void *k_c
                            const int32_t *sel_tables, int32_t max_selected, const int32_t *sel_lens,
                            int32_t B, int32_t Hq, float scale, int32_t num_splits, void *workspace,
                            size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* Split count for pa_decode_selected, the one that takes the least time by a model of the
+ * stream, the merge and further waves, for lists that are mostly full.  It is what num_splits = 0
+ * uses.  sm_count 0: the current device's.  P >= 1, or PA_EINVAL / PA_EUNSUPPORTED / PA_ECUDA. */
+int pa_selected_num_splits(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_selected,
+                           int32_t block_size, int32_t sm_count);
 
 /*
  * The attention weight that cached tokens draw.  For the queries i < q_len of

@@ -696,9 +696,9 @@ int pa_combine(void *out, float *lse, const float *part_o, const float *part_lse
 namespace {
 // Partitions of a scored call, over the tokens that it can see (at least one tile): a
 // model of its time for the tensor-core decode kernel, pa_choose_num_splits_mq's rule
-// for the others.
+// for the others.  `full`: the sequences are lists of blocks, most as long as the longest.
 int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_blocks_per_seq,
-                  int32_t block_size, int32_t window, int32_t max_prefix, int sms) {
+                  int32_t block_size, int32_t window, int32_t max_prefix, int sms, bool full = false) {
     if (window < 0 || max_prefix < 0 || q_len <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq <= 0 ||
         block_size <= 0 || block_size % 16 != 0)
         return PA_EINVAL;
@@ -729,7 +729,9 @@ int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, 
     // 32 / 8 heads, bf16: one sequence of 512 tokens P = 32 9.7 us (16: 11.3, 4: 18.5), of 48
     // P = 1 9.1 (2: 16.8).  FP8, sequences of 8 heads up to 4096 tokens: 64 of them with P =
     // 7 take 113 us full and 81 us spread (P = 2: 109 and 109); 40 with P = 7 78 and 61 (P =
-    // 3: 78 and 77); 100 with P = 3 150 and 134 (P = 1: 201 and 200).
+    // 3: 78 and 77); 100 with P = 3 150 and 134 (P = 1: 201 and 200).  Lists of blocks (full):
+    // 64 x 8 of 2048 FP8 tokens P = 2 87 us (4: 98, 7: 97, 1: 146), 1 x 2 of 1024 tokens P = 16 9.8
+    // (32: 12.3).
     const int qpc = queries_per_cta(G, q_len);
     const double units = static_cast<double>(units_per_split(k, B, G, Hkv, qpc, (q_len + qpc - 1) / qpc));
     int hc = 1, gp = 1;
@@ -739,7 +741,7 @@ int scored_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int32_t D, 
         const double part = stream((tiles + n - 1) / n), waves = std::ceil(units * n / sms);
         const double spread = std::max(part, stream(tiles) * units / (2.0 * sms) + 0.5 * part);
         const double join = n == 1 ? 0.0 : waves > 1.0 ? 4.0 : 1.2 + 0.55 * hc * G * qpc / n + 0.05 * n;
-        return 0.5 * (waves * part + spread) + join + 8.0 * (waves - 1.0);
+        return (full ? waves * part : 0.5 * (waves * part + spread)) + join + 8.0 * (waves - 1.0);
     };
     int best = 1;
     for (int n = 2; n <= std::min(64, tiles); ++n)
@@ -800,10 +802,9 @@ int splitkv_common(void *out, float *lse, const void *q, const void *k_cache, co
     if (P == 0) {
         const int sms = sm_count_current();
         if (sms <= 0) return PA_ECUDA;
-        // (Lists of blocks are mostly full, which the scored rule does not expect: 64 x 8 lists of 128
-        // blocks with P = 2 by the plain rule 87 us, P = 4 98.)
-        P = rules ? scored_splits(B, q_len, Hq, cache.num_kv_heads, cache.head_dim, max_blocks_per_seq,
-                                  cache.block_size, rules->window, rules->prefix_lens ? rules->max_prefix : 0, sms)
+        P = rules || lists ? scored_splits(B, q_len, Hq, cache.num_kv_heads, cache.head_dim, max_blocks_per_seq,
+                                           cache.block_size, rules ? rules->window : 0,
+                                           rules && rules->prefix_lens ? rules->max_prefix : 0, sms, lists)
                   : pa_choose_num_splits_mq(B, q_len, Hq, cache.num_kv_heads, cache.head_dim,
                                             max_blocks_per_seq, cache.block_size, sms);
         // (pa_decode_selected: as many as a smaller workspace holds)
@@ -933,6 +934,13 @@ int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int3
     const int sms = sm_count > 0 ? sm_count : sm_count == 0 ? sm_count_current() : 0;
     if (sms <= 0) return sm_count < 0 ? PA_EINVAL : PA_ECUDA;
     return scored_splits(B, q_len, Hq, Hkv, D, max_blocks_per_seq, block_size, window, max_prefix, sms);
+}
+
+int pa_selected_num_splits(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_selected, int32_t block_size,
+                           int32_t sm_count) {
+    const int sms = sm_count > 0 ? sm_count : sm_count == 0 ? sm_count_current() : 0;
+    if (sms <= 0) return sm_count < 0 ? PA_EINVAL : PA_ECUDA;
+    return scored_splits(B, 1, Hq, Hkv, D, max_selected, block_size, 0, 0, sms, true);
 }
 
 int pa_cache_write_fp8(const void *k_new, const void *v_new, const int64_t *slot_mapping,

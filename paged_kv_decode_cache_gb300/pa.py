@@ -134,6 +134,7 @@ _SIGNATURES = {
                            ctypes.c_int),
     "pa_decode_selected_fp8": ([_P, _P, _P, _P, _P, CacheDesc, _F32, _F32, _P, _I32, _P, _I32, _I32, _F32, _I32, _P,
                                 _SZ, _P, _P], ctypes.c_int),
+    "pa_selected_num_splits": ([_I32] * 7, ctypes.c_int),
     "pa_weights_add": ([_P, _P, _P, _P, _I32, _P, _P, CacheDesc, _P, _I32, _P, _P, _I64, _I32, _I32, _F32, _F32, _P, _P],
                        ctypes.c_int),
     "pa_weights_add_fp8": ([_P, _P, _P, _P, _I32, _P, _P, CacheDesc, _F32, _P, _I32, _P, _P, _I64, _I32, _I32, _F32, _F32,
@@ -777,6 +778,12 @@ def pa_blocks_select(sel_tables, sel_lens, q, bounds, block_size, block_tables, 
     sel_tables [B, Hkv, K] (their ids in order, -1 behind them), sel_lens [B, Hkv] (their tokens)."""
     (_native or _binding()).blocks_select(sel_tables, sel_lens, q, bounds, block_size, block_tables, seq_lens, first, last,
                                           status, stream)
+
+
+def pa_selected_num_splits(B: int, Hq: int, Hkv: int, D: int, max_selected: int, block_size: int, sm_count: int = 0) -> int:
+    r = lib().pa_selected_num_splits(B, Hq, Hkv, D, max_selected, block_size, sm_count)
+    _check("pa_selected_num_splits", min(r, 0))
+    return r
 
 
 def pa_decode_selected(out, lse, q, k_cache, v_cache, sel_tables, sel_lens, scale, num_splits=0, workspace=None,

@@ -56,7 +56,7 @@ def case(hq, hkv, d, bs, lens, splits, fp8=False, seed=1, extra=0, stream=None, 
             out[b, hs], lse[b, hs] = attention64(as64(q[b, hs]), k * ks, v * vs, scale)
     for p in pools:   # what no list names is never looked at
         p.view(nb * bs, hkv, d)[~used] = 0x7F if fp8 else math.nan
-    P = splits or pa.pa_auto_num_splits(Bn, hq, hkv, d, width, bs)
+    P = splits or pa.pa_selected_num_splits(Bn, hq, hkv, d, width, bs)
     ws = torch.zeros(max(1, pa.pa_splitkv_workspace_bytes(Bn, hq, d, P)), dtype=torch.uint8, device="cuda")
     got, z = torch.full((Bn, hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((Bn, hq), 7.0, device="cuda")
     pools = [p.cuda() for p in pools]
@@ -134,7 +134,7 @@ def test_selected_takes_the_splits_that_its_workspace_holds():
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
     q, k, v = rnd(1, 8, 128), rnd(80, 16, 2, 128), rnd(80, 16, 2, 128)
     t, n = torch.arange(80, device="cuda").int().expand(1, 2, 80).contiguous(), i32([[1280, 1111]])
-    P = pa.pa_auto_num_splits(1, 8, 2, 128, 80, 16)
+    P = pa.pa_selected_num_splits(1, 8, 2, 128, 80, 16)
     assert P > 4
     outs = []
     for size in (pa.pa_splitkv_workspace_bytes(1, 8, 128, P), pa.pa_splitkv_workspace_bytes(1, 8, 128, 3), 4096, 0):
@@ -185,6 +185,21 @@ def test_selected_refuses_what_its_kernels_do_not_take():
     tail = (FAKE, 7, FAKE, 4, 18, 0.1, 1, None, 0, None, None)
     assert pa.lib().pa_decode_selected(FAKE, None, FAKE, FAKE, FAKE, d64, *tail) == pa.PA_EUNSUPPORTED   # 9 heads of 64
     assert pa.lib().pa_decode_selected_fp8(FAKE, None, FAKE, FAKE, FAKE, d64, 1.0, 1.0, *tail) == pa.PA_EUNSUPPORTED
+
+
+def test_selected_split_counts():
+    for tiles in (1, 3, 64, 128, 1000):
+        for Bn in (1, 4, 64, 1000):
+            for heads in ((28, 4), (16, 8), (12, 2)):
+                P = pa.pa_selected_num_splits(Bn, *heads, 128, tiles, 16, sm_count=152)
+                assert 1 <= P <= min(64, tiles)
+    assert pa.pa_selected_num_splits(64, 16, 8, 128, 128, 16, sm_count=152) == 2
+    assert pa.pa_selected_num_splits(1, 12, 2, 128, 64, 16, sm_count=152) == 16
+    assert pa.pa_selected_num_splits(8, 8, 2, 64, 64, 16, sm_count=152) == pa.pa_choose_num_splits(8, 8, 2, 64, 64, 16, 152)
+    for a in ((8, 28, 4, 128, 0, 16, 152), (8, 28, 4, 128, 8, 15, 152), (8, 27, 4, 128, 8, 16, 152), (8, 28, 4, 128, 8, 16, -1)):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_selected_num_splits(*a[:6], sm_count=a[6])
+        assert e.value.code == pa.PA_EINVAL
 
 
 @pytest.mark.gpu
