@@ -515,6 +515,7 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
 namespace pa {
 int check_cache(const pa_cache_desc &c) { return check_cache_desc(c); }
 int sm_count() { return sm_count_current(); }
+int make_head_map(CUtensorMap *map, const void *base, const pa_cache_desc &c) { return make_kv_map_heads(map, base, c, 1); }
 bool pdl_on() { return pdl_enabled(); }
 }  // namespace pa
 

@@ -216,12 +216,18 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 //
 // Warps 0-7 (two groups of four): the exponentials of every second tile; a group's lane is the
 // token.  TMEM is in quarters, two per group, so that a group has the next scores while
-// the MMA makes those after them (with one buffer per group it waited 1.1 of 2.8 us).  Warps 8-15: keys from the pool into a ring of 32 KB stages, as the MMA reads them
-// (K-major, 128-byte swizzle; e4m3 codes widened to fp16 on the way), by asynchronous copies.
-// Warp 16: issues the MMAs.  Every wait is bounded.
-constexpr int kXThreads = 17 * 32;
-constexpr int kXLoadWarp = 8, kXMmaWarp = 16;
-constexpr int kXLoadRows = 16;           // tokens of a loading warp
+// the MMA makes those after them (with one buffer per group it waited 1.1 of 2.8 us).  Keys come
+// into a ring of stages as the MMA reads them (K-major, 128-byte swizzle): by TMA from one warp
+// (8 warps of asynchronous copies took issue slots from the exponentials: 51 us for a window that
+// takes 43), or for FP8 pools by 8 warps, which widen the codes to fp16 on the way.  The last warp
+// issues the MMAs.  Every wait is bounded.
+template <bool F8>
+struct XWarps {
+    static constexpr int kLoad = 8;                  // the first loading warp, after the exponentials'
+    static constexpr int kMma = F8 ? 16 : 9;
+    static constexpr int kThreads = 32 * (kMma + 1);
+};
+constexpr int kXLoadRows = 16;           // FP8: tokens of a loading warp
 constexpr int kXRows = 128;              // tokens of a tile
 constexpr int kXAhead = 2;               // FP8: tiles whose copies are on their way
 constexpr int kXCodes = kXAhead + 1;     // FP8: tiles in the ring of codes
@@ -288,9 +294,11 @@ __device__ __forceinline__ float row_sum(uint32_t row, int n1, float scale, cons
 }
 
 template <bool F8, int D>
-__global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsArgs a, int tiles_max, int n_most, uint32_t tmem_cols) {
+__global__ void __launch_bounds__(XWarps<F8>::kThreads, 1)
+weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, int tiles_max, int n_most, uint32_t tmem_cols) {
     using X = XShape<F8, D>;
-    constexpr int kXStages = X::kStages;
+    constexpr int kXStages = X::kStages, kXThreads = XWarps<F8>::kThreads;
+    constexpr int kXLoadWarp = XWarps<F8>::kLoad, kXMmaWarp = XWarps<F8>::kMma;
     extern __shared__ uint8_t x_smem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(x_smem) + 1023) & ~uintptr_t(1023));
     uint8_t *codes = smem + kXStages * X::kStageBytes, *qs = smem + X::q_at();
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
 
     if (warp == kXMmaWarp) tc5::tmem_alloc(tmem_slot, tmem_cols);
     if (tid == 0) {
-        for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], 32 * (kXMmaWarp - kXLoadWarp)), mbar_init(&kempty[i], 1u);
+        for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], F8 ? 32 * (kXMmaWarp - kXLoadWarp) : 1), mbar_init(&kempty[i], 1u);
         for (int i = 0; i < 4; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], 4u);
         mbar_init(drain, 1u);
         *abort_flag = 0;
@@ -368,51 +376,68 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
         tc5::fence_after_sync();
 
         if (loads) {
-            // A loading warp's 16 rows of a tile: kPer chunks of 16 bytes a lane, copied
-            // asynchronously straight into the stage, whose barrier their completion arrives on;
-            // or (FP8), kXAhead tiles ahead, into the lane's own part of a ring of codes, which it
-            // widens into the stage later.  The fence to the MMA's proxy is the MMA warp's, after
-            // that barrier: here it would wait for the copies of the next tiles, too (1.6 us a
-            // tile).
-            constexpr int kRowChunks = D * (F8 ? 1 : 2) / 16, kPer = kXLoadRows * kRowChunks / 32;
-            constexpr int kRowsAtOnce = 32 / kRowChunks;
-            const int lw = warp - kXLoadWarp;
-            uint8_t *own = codes + (lw * 32 + lane) * 16;
-            // (its rows of a tile lie in one block: lane i knows their place in the pool for tile i)
-            static_assert(kXLoadRows == kTile && kXMostTiles == 32, "a place per lane");
-            int places = -1;
-            const int row0 = tok0 + lane * kXRows + lw * kXLoadRows;
-            if (lane < tiles && row0 < L) {
-                const int phys = table[row0 / bs];
-                if (phys >= 0 && phys < a.num_blocks) places = phys * bs + row0 % bs;
-                else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-            }
-            const uint8_t *keys = a.keys + static_cast<int64_t>(h) * (D * (F8 ? 1 : 2)) + 16 * (lane % kRowChunks);
-            const int stride = a.Hkv * D * (F8 ? 1 : 2), my_row = lane / kRowChunks;
-            auto issue = [&](int i) {  // tile i (FP8: one commit group)
-                const int place = __shfl_sync(0xffffffffu, places, i & 31);
-                if (i < tiles && good) {
-                    const int u = it + i;
-                    if (!F8 && u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[u % kXStages], (u / kXStages - 1) & 1));
-                    if (good) {
+            if constexpr (!F8) {
+                // lane 2 i + half: 16 tokens of a tile, 64 channels.  (Places of no token, and tokens of a block
+                // outside the pool, keep what the stage had: their rows' scores are not used.)
+                const int sub = lane / X::kHalves, half = lane % X::kHalves;
+                const bool carrier = sub < kXRows / kTile;
+                auto block_of = [&](int i) {
+                    const int tok = tok0 + i * kXRows + sub * kTile;
+                    return carrier && i < tiles && tok < L ? table[tok / bs] : -1;
+                };
+                int next = block_of(0), after = block_of(1);  // two tiles ahead
+                const uint64_t policy = l2_evict_first_policy();
+                int issued = it;
+                for (int i = 0; i < tiles && good; ++i) {
+                    const int u = it + i, s = u % kXStages, phys = next, tok = tok0 + i * kXRows + sub * kTile;
+                    next = after, after = block_of(i + 2);
+                    const bool there = carrier && tok < L, valid = there && phys >= 0 && phys < a.num_blocks;
+                    if (there && !valid && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                    const uint32_t copies = __popc(__ballot_sync(0xffffffffu, valid));
+                    if (u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
+                    if (!good) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&kfull[s], copies * kTile * kSubBytes);
+                    __syncwarp();
+                    if (valid)
+                        tma_load_4d(smem + s * X::kStageBytes + half * (kXRows * kSubBytes) + sub * kTile * kSubBytes, &map, 0,
+                                    phys * bs + tok % bs, h, half, &kfull[s], policy);
+                    issued = u + 1;
+                }
+                // (the copies land before this CTA leaves, whatever became of the other warps)
+                for (int u = max(0, issued - kXStages); u < issued; ++u) mbar_wait_bounded(&kfull[u % kXStages], (u / kXStages) & 1);
+            } else {
+                // A loading warp's 16 rows of a tile: kPer chunks of 16 bytes a lane, copied
+                // asynchronously kXAhead tiles ahead into the lane's own part of a ring of codes, which it
+                // widens into the stage later.  The fence to the MMA's proxy is the MMA warp's, after the
+                // stage's barrier: here it would wait for the copies of the next tiles, too.
+                constexpr int kRowChunks = D * (F8 ? 1 : 2) / 16, kPer = kXLoadRows * kRowChunks / 32;
+                constexpr int kRowsAtOnce = 32 / kRowChunks;
+                const int lw = warp - kXLoadWarp;
+                uint8_t *own = codes + (lw * 32 + lane) * 16;
+                // (its rows of a tile lie in one block: lane i knows their place in the pool for tile i)
+                static_assert(kXLoadRows == kTile && kXMostTiles == 32, "a place per lane");
+                int places = -1;
+                const int row0 = tok0 + lane * kXRows + lw * kXLoadRows;
+                if (lane < tiles && row0 < L) {
+                    const int phys = table[row0 / bs];
+                    if (phys >= 0 && phys < a.num_blocks) places = phys * bs + row0 % bs;
+                    else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                }
+                const uint8_t *keys = a.keys + static_cast<int64_t>(h) * (D * (F8 ? 1 : 2)) + 16 * (lane % kRowChunks);
+                const int stride = a.Hkv * D * (F8 ? 1 : 2), my_row = lane / kRowChunks;
+                auto issue = [&](int i) {  // tile i (a commit group)
+                    const int place = __shfl_sync(0xffffffffu, places, i & 31);
+                    if (i < tiles) {
+                        const int u = it + i;
                         const int left = place >= 0 ? L - (tok0 + i * kXRows + lw * kXLoadRows) : 0;  // rows that are there
                         const uint8_t *from = keys + static_cast<int64_t>(max(place, 0) + my_row) * stride;
 #pragma unroll
-                        for (int j = 0; j < kPer; ++j) {
-                            const int r = j * kRowsAtOnce + my_row, ch = lane % kRowChunks;
-                            uint8_t *to = F8 ? own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512
-                                             : smem + (u % kXStages) * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) +
-                                                   swz128(lw * kXLoadRows + r, ch & 7);
-                            cp_async_16_or_zero(to, from + static_cast<int64_t>(j * kRowsAtOnce) * stride, r < left);
-                        }
-                        if (!F8) cp_async_arrive(&kfull[u % kXStages]);
+                        for (int j = 0; j < kPer; ++j)
+                            cp_async_16_or_zero(own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512,
+                                                from + static_cast<int64_t>(j * kRowsAtOnce) * stride, j * kRowsAtOnce + my_row < left);
                     }
-                }
-                if (F8) cp_async_commit();
-            };
-            if constexpr (!F8) {
-                for (int i = 0; i < tiles && good; ++i) issue(i);
-            } else {
+                    cp_async_commit();
+                };
 #pragma unroll
                 for (int i = 0; i < kXAhead; ++i) issue(i);
                 for (int i = 0; i < tiles && good; ++i) {
@@ -434,8 +459,8 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
                     }
                     mbar_arrive(&kfull[s]);
                 }
+                cp_async_wait<0>();
             }
-            cp_async_wait<0>();
         } else if (warp == kXMmaWarp) {
             if (lane == 0) {
                 // (descriptors count 16 bytes: what is added to them is worked out before the loop)
@@ -446,7 +471,7 @@ __global__ void __launch_bounds__(kXThreads, 1) weights_tc_kernel(const WeightsA
                 for (int i = 0; i < tiles && good; ++i) {
                     const int u = it + i, s = u % kXStages;
                     good = wait(&kfull[s], (u / kXStages) & 1);
-                    fence_proxy_async_smem();  // (the keys are copied and written by the generic proxy)
+                    if (F8) fence_proxy_async_smem();  // (the generic proxy has written the keys)
                     const uint64_t kd = k0 + static_cast<uint32_t>(s * (X::kStageBytes >> 4));
                     for (int e = 0; e < parts && good; ++e) {
                         const int at = quarter(u, e);
@@ -554,8 +579,11 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
         if (e != cudaSuccess) return e;
         smem_attr_done.fetch_or(bit, std::memory_order_release);
     }
-    return launch_maybe_cooperative(kern, dim3(static_cast<unsigned>((tiles + best - 1) / best), a.Hkv, B), kXThreads,
-                                    XShape<F8, D>::bytes(n_most), stream, false, pdl_on(), a, best, n_most, cols);
+    CUtensorMap map{};
+    if (!F8 && make_head_map(&map, a.keys, pa_cache_desc{a.num_blocks, a.block_size, a.Hkv, D}) != PA_OK)
+        return cudaErrorUnknown;
+    return launch_maybe_cooperative(kern, dim3(static_cast<unsigned>((tiles + best - 1) / best), a.Hkv, B), XWarps<F8>::kThreads,
+                                    XShape<F8, D>::bytes(n_most), stream, false, pdl_on(), map, a, best, n_most, cols);
 }
 
 int weights_add(float *new_weights, const float *weights, int32_t *positions, const void *q, int32_t q_len, const float *lse,
