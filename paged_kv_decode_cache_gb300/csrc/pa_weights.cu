@@ -211,20 +211,21 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 //
 // S[128 tokens, N] = K[128, D] . Q^T[D, N] per tile, N <= 256 columns (query, head of the
 // group) at a time, by tcgen05.mma into TMEM; a thread per token then adds up its row's
-// exponentials.  16 exponentials a clock and SM bound it: 128 x N of them a tile take
-// 8 N clocks, the MMA 4 N, and the tile's keys come in meanwhile.
+// exponentials.  Per tile N products of 128 x D, 128 N exponentials and D keys a token; with
+// everything overlapped none of the three takes 1 us.
 //
-// Warps 0-7 (two groups of four): the exponentials of every second tile; a group's lane is the
-// token.  TMEM is in quarters, two per group, so that a group has the next scores while
-// the MMA makes those after them (with one buffer per group it waited 1.1 of 2.8 us).  Keys come
-// into a ring of stages as the MMA reads them (K-major, 128-byte swizzle): by TMA from one warp
-// (8 warps of asynchronous copies took issue slots from the exponentials: 51 us for a window that
-// takes 43), or for FP8 pools by 8 warps, which widen the codes to fp16 on the way.  The last warp
-// issues the MMAs.  Every wait is bounded.
+// Two tiles' scores are in TMEM (four of up to 128 columns), and four groups of four warps
+// add them up, two a tile (one), a half of the columns each, while the MMA makes others.  An
+// MMA of 128 columns takes as long as one of 224, so halves with buffers of their own
+// were no faster (47 us for the window below).  Keys come into a ring of stages as the MMA
+// reads them (K-major, 128-byte swizzle): by TMA from one warp (8 warps of asynchronous
+// copies: 5 us more), or for FP8 pools by 8 warps, which widen the codes to fp16 on the
+// way.  The last warp issues the MMAs.  Every wait is bounded.
+constexpr int kXGroups = 4;
 template <bool F8>
 struct XWarps {
-    static constexpr int kLoad = 8;                  // the first loading warp, after the exponentials'
-    static constexpr int kMma = F8 ? 16 : 9;
+    static constexpr int kLoad = 4 * kXGroups;       // the first loading warp, after the exponentials'
+    static constexpr int kMma = kLoad + (F8 ? 8 : 1);
     static constexpr int kThreads = 32 * (kMma + 1);
 };
 constexpr int kXLoadRows = 16;           // FP8: tokens of a loading warp
@@ -245,7 +246,7 @@ struct XShape {
     static constexpr int q_at() { return kStages * kStageBytes + kCodeBytes; }
     static constexpr int sums_at(int n) { return q_at() + q_bytes(n); }
     static constexpr int bytes(int n) {
-        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + (2 * kStages + 9) * 8 + 16 + 1024;
+        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + 4 * kXRows * 4 + (2 * kStages + 11) * 8 + 16 + 1024;
     }
 };
 
@@ -305,8 +306,9 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
     float *sums = reinterpret_cast<float *>(smem + X::sums_at(n_most));      // [tiles][128], over the chunks of columns
     float *nl = sums + kXMostTiles * kXRows;                                  // -lse of every column, log2 units
     int *last_s = reinterpret_cast<int *>(nl + kXColumns);                    // last token that it sees
-    uint64_t *bars = reinterpret_cast<uint64_t *>(last_s + kXColumns);
-    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 4, *drain = sfree + 4;
+    float *other = reinterpret_cast<float *>(last_s + kXColumns);             // [2][2][128]: a tile's second half's sums
+    uint64_t *bars = reinterpret_cast<uint64_t *>(other + 4 * kXRows);
+    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 4, *hdone = sfree + 4, *drain = hdone + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -328,7 +330,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
     if (warp == kXMmaWarp) tc5::tmem_alloc(tmem_slot, tmem_cols);
     if (tid == 0) {
         for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], F8 ? 32 * (kXMmaWarp - kXLoadWarp) : 1), mbar_init(&kempty[i], 1u);
-        for (int i = 0; i < 4; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], 4u);
+        for (int i = 0; i < 4; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], n_most > kXColumns / 2 ? 8u : 4u);
+        for (int i = 0; i < 2; ++i) mbar_init(&hdone[i], 4u);
         mbar_init(drain, 1u);
         *abort_flag = 0;
     }
@@ -344,11 +347,11 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
     for (int c0 = 0; c0 < n_cols; c0 += n_most, it += tiles) {
         const int here = min(n_most, n_cols - c0), N = (here + 15) / 16 * 16;
         const bool first = c0 == 0, final = c0 + here == n_cols;
-        // TMEM holds four quarters, two for each group of warps: the two parts of a tile's columns, or
-        // (up to 128 columns) two tiles of the group in turn
-        const int parts = n_most > kXColumns / 2 ? 2 : 1, part = parts == 1 ? N : (N / 2 + 31) / 32 * 32;
-        auto quarter = [&](int u, int e) { return 2 * (u & 1) + (parts == 2 ? e : (u >> 1) & 1); };
-        auto turn = [&](int u) { return parts == 2 ? u >> 1 : u >> 2; };   // how often it was used before
+        // over 128 columns: tile u in buffer u & 1, a half of its columns for each of two groups; else in
+        // buffer u & 3, a group's own
+        const int halves = n_most > kXColumns / 2 ? 2 : 1, part = halves == 1 ? N : (N / 2 + 31) / 32 * 32;
+        const int buffers = 4 / halves;
+        const uint32_t width = tmem_cols / buffers;
         // (the chunk before this one is read; TMEM and the barriers are set up)
         if (__syncthreads_or(!first && *abort_flag != 0)) break;
         tmem = *tmem_slot;
@@ -466,27 +469,20 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 // (descriptors count 16 bytes: what is added to them is worked out before the loop)
                 const uint64_t k0 = tc5::sw128_desc(smem, 16, 1024), q0 = tc5::sw128_desc(qs, 16, 1024);
                 const uint32_t q_half = static_cast<uint32_t>(N * kSubBytes) >> 4;
-                const uint32_t idesc0 = tc5::idesc_bf16_f32(kXRows, min(part, N), false, false, F8);
-                const uint32_t idesc1 = tc5::idesc_bf16_f32(kXRows, max(N - part, 16), false, false, F8);
+                const uint32_t idesc = tc5::idesc_bf16_f32(kXRows, N, false, false, F8);
                 for (int i = 0; i < tiles && good; ++i) {
-                    const int u = it + i, s = u % kXStages;
-                    good = wait(&kfull[s], (u / kXStages) & 1);
+                    const int u = it + i, s = u % kXStages, at = u % buffers, turn = u / buffers;
+                    good = wait(&kfull[s], (u / kXStages) & 1) && (turn == 0 || wait(&sfree[at], (turn - 1) & 1));
+                    if (!good) break;
                     if (F8) fence_proxy_async_smem();  // (the generic proxy has written the keys)
+                    tc5::fence_after_sync();
                     const uint64_t kd = k0 + static_cast<uint32_t>(s * (X::kStageBytes >> 4));
-                    for (int e = 0; e < parts && good; ++e) {
-                        const int at = quarter(u, e);
-                        good = turn(u) == 0 || wait(&sfree[at], (turn(u) - 1) & 1);
-                        if (!good) break;
-                        tc5::fence_after_sync();
-                        const uint64_t qd = q0 + static_cast<uint32_t>(e * part * (kSubBytes >> 4));
-                        const uint32_t to = tmem + at * (tmem_cols / 4), idesc = e ? idesc1 : idesc0;
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            tc5::mma_bf16(to, kd + ((j >> 2) * (kXRows * kSubBytes) + (j & 3) * 32) / 16,
-                                          qd + (j >> 2) * q_half + (j & 3) * 2, idesc, j > 0);
-                        tc5::commit(&sdone[at]);
-                    }
-                    if (good) tc5::commit(&kempty[s]);
+                    for (int j = 0; j < D / 16; ++j)
+                        tc5::mma_bf16(tmem + at * width, kd + ((j >> 2) * (kXRows * kSubBytes) + (j & 3) * 32) / 16,
+                                      q0 + (j >> 2) * q_half + (j & 3) * 2, idesc, j > 0);
+                    tc5::commit(&sdone[at]);
+                    tc5::commit(&kempty[s]);
                 }
                 if (!good) {  // let what was issued finish before TMEM is freed
                     tc5::commit(drain);
@@ -496,32 +492,41 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
             __syncwarp();
         } else {
             const int group = warp >> 2, r = tid & 127;   // this thread's row
+            const int at = group / halves, e = group % halves, n0 = e * part, n1 = min(part, here - n0);
             for (int i = 0; i < tiles && good; ++i) {
-                const int u = it + i;
-                if ((u & 1) != group) continue;
+                const int u = it + i, turn = u / buffers;
+                if (u % buffers != at) continue;
+                const bool writes = e == 0;               // (the second half's sums go to the first one's threads)
                 const int tok = tok0 + i * kXRows + r;
                 int phys = 0;
                 float was = 0.f;
-                if (final && tok < L) {
+                if (writes && final && tok < L) {
                     phys = table[tok / bs];
                     if (tok < first_new) was = a.old[(static_cast<int64_t>(b) * a.Hkv + h) * a.room + tok];
                 }
                 // (a tile with new tokens has queries that do not see all of it)
                 const bool all = !odd && tok0 + (i + 1) * kXRows <= first_new;
-                float v = 0.f;
-                for (int e = 0; e < parts; ++e) {
-                    const int at = quarter(u, e), n0 = e * part, n1 = min(part, here - n0);
-                    good = __all_sync(0xffffffffu, wait(&sdone[at], turn(u) & 1));
-                    if (!good) break;
-                    tc5::fence_after_sync();
-                    const uint32_t row = tc5::taddr(tmem, 32 * (warp & 3), at * (tmem_cols / 4));
-                    v += all ? row_sum<false>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok)
-                             : row_sum<true>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok);
-                    tc5::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sfree[at]);
-                }
+                good = __all_sync(0xffffffffu, wait(&sdone[at], turn & 1));
                 if (!good) break;
+                tc5::fence_after_sync();
+                const uint32_t row = tc5::taddr(tmem, 32 * (warp & 3), at * width + n0);
+                float v = all ? row_sum<false>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok)
+                              : row_sum<true>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok);
+                float *half = other + (2 * (u & 1) + (turn & 1)) * kXRows + r;
+                if (!writes) *half = v;
+                tc5::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sfree[at]);
+                    if (!writes) mbar_arrive(&hdone[u & 1]);
+                }
+                if (!writes) continue;
+                if (halves == 2) {
+                    // (written again two turns on, which the MMA begins only after this group's next turn)
+                    good = __all_sync(0xffffffffu, wait(&hdone[u & 1], turn & 1));
+                    if (!good) break;
+                    v += *half;
+                }
                 if (!first) v += sums[i * kXRows + r];
                 if (!final) {
                     sums[i * kXRows + r] = v;
@@ -556,9 +561,8 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
     // 256 columns at a time, or shares of them that differ by little
     const int64_t chunks = (columns + kXColumns - 1) / kXColumns;
     const int n_most = static_cast<int>(((columns + chunks - 1) / chunks + 15) / 16 * 16);
-    const int quarter = (n_most > kXColumns / 2 ? (n_most / 2 + 31) / 32 * 32 : n_most) + 31;
-    uint32_t cols = 128;  // of TMEM, each quarter read in 32 columns
-    while (cols < 4u * (quarter / 32 * 32)) cols *= 2;
+    uint32_t cols = 128;  // of TMEM: four buffers, or two of over 128 columns, read 32 columns at a time
+    while (cols < (n_most > kXColumns / 2 ? 2u : 4u) * ((n_most + 31) / 32 * 32)) cols *= 2;
     // the tiles of a CTA: the fewest rounds of tiles over all SMs, a CTA's start counted as two
     const int64_t tiles = (most + kXRows - 1) / kXRows, rows = static_cast<int64_t>(a.Hkv) * B, sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
