@@ -786,8 +786,9 @@ int pa_scored_num_splits(int32_t B, int32_t q_len, int32_t Hq, int32_t Hkv, int3
  * sequence has a token in [starts[b], seq_lens[b]) gets its bounds anew from all of the
  * sequence's tokens in it (starts NULL: 0), so a step's call passes the lengths
  * before its tokens were written; other blocks' bounds are left as they were.  A NaN
- * among a channel's keys makes both bounds NaN.  After pa_cache_evict every block of a row
- * that was cut needs its bounds anew.
+ * among a channel's keys makes both bounds NaN.  Bounds go by block id: after
+ * pa_cache_evict every block of a row that was cut needs its bounds anew (starts NULL),
+ * after pa_blocks_compact every block that moved.
  * bounds: device [num_blocks, Hkv, 2, D] of the pool's elements (elem_bytes 2: bf16, 1:
  * e4m3 codes, compared as the values they stand for); k_cache the pool.  Rows that
  * share a block have the same tokens in it.  max_new: a bound on seq_lens[b] -
@@ -833,8 +834,9 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
  * max_selected]; sel_lens: device int32 [B, Hkv], the tokens of the list, all of its
  * blocks full but the last.  A list without tokens gives out = 0 and lse = -inf.
  * Supported: the shapes of pa_decode_splitkv (FP8: of pa_decode_splitkv_fp8).
- * num_splits 0: pa_selected_num_splits, or fewer, as many as the workspace holds; workspace: pa_splitkv_workspace_bytes(B,
- * Hq, D, P) bytes, with pa_decode_splitkv's contract.
+ * num_splits 0: pa_selected_num_splits, or fewer, as many as the workspace holds;
+ * workspace: pa_splitkv_workspace_bytes(B, Hq, D, P) bytes, with pa_decode_splitkv's
+ * contract.
  */
 int pa_decode_selected(void *out, float *lse, const void *q, const void *k_cache,
                        const void *v_cache, pa_cache_desc cache, const int32_t *sel_tables,
@@ -863,7 +865,8 @@ int pa_selected_num_splits(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_
  * over the group's heads g and the queries that see t (t <= their position).  The q_len
  * newest tokens have no weight yet: their sum alone is stored, and, with positions not
  * NULL, positions[b,h,t] = ends[b] - seq_lens[b] + t, where ends[b] counts every token
- * that the sequence has had, evicted ones too (NULL: seq_lens).  lse is what
+ * that the sequence has had, evicted ones too (NULL: seq_lens).  (So before a prompt's
+ * last q_len queries the older tokens' weights are 0, their positions t.)  lse is what
  * attention gave for these queries (one of -inf adds nothing), so a query's weights sum
  * to one over the tokens it saw.  Places from seq_lens[b] on are left as they were.
  * weights, new_weights: device fp32 [B, Hkv, room], the same buffer or two; positions:
@@ -913,8 +916,9 @@ int pa_weights_add_fp8(float *new_weights, const float *weights, int32_t *positi
  * the call only.  weights, new_weights: device fp32 [layers, B, Hkv, room]; positions,
  * new_positions: device int32 alike, as pa_weights_add leaves them.  tables, lens, refs
  * and their new ones: as for pa_sequences_fork.  Every new array is other memory than
- * the old one.  1 <= budget, first + recent <= budget; min(room, max_blocks_per_seq *
- * bs) <= 196608; B <= 65535.  Two launches.
+ * the old one.  (pa_sequences_fork moves no weights and positions: a new row's are its
+ * parent's.)  1 <= budget, first + recent <= budget; min(room, max_blocks_per_seq * bs)
+ * <= 196608; B <= 65535.  Two launches.
  */
 int pa_cache_evict(int32_t *new_tables, int32_t *new_lens, int32_t *new_refs, float *new_weights,
                    int32_t *new_positions, const int32_t *tables, const int32_t *lens,

@@ -11,7 +11,10 @@
 // Two launches.  evict_lens_kernel works out every sequence's n, and writes the new
 // lengths, tables and counts.  evict_kernel has a thread-block cluster per (layer,
 // sequence, head): it finds the n-th largest weight over its shared memory (pa_topk.cuh),
-// lists the free places and the tokens for them, and moves the rows.
+// lists the free places and the tokens for them, and moves the rows.  Bound by the chain of the
+// search where few tokens are thrown out (the 8 x 4 rows of a step, 64 of 1088 tokens each: 10.7 us),
+// by memory and the search's passes where many are (8 layers of 4 FP8 prompts of up to 16384 tokens: 94 us; moving the rows
+// alone takes 38 at a copy's rate).
 #include <algorithm>
 
 #include "pa_device.cuh"

@@ -59,7 +59,6 @@ __device__ __forceinline__ uint32_t to_f16x2(float a, float b) {
 template <bool F8>
 struct Chunk {
     static constexpr int kVecs = F8 ? 2 : 1;
-    static constexpr int kValues = 8 * kVecs;
 };
 template <bool F8>
 __device__ __forceinline__ void widen(const uint4 &in, uint4 (&out)[Chunk<F8>::kVecs]) {

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_many_kernel(const B
         if (phys < 0) continue;
         Range<F8> r;
         range_of_rows<4>(r, reinterpret_cast<const uint4 *>(a.keys) + static_cast<int64_t>(phys) * bs * a.row_chunks + c, a.row_chunks,
-                      0, 1, min(bs, L - (j0 + k) * bs));
+                         0, 1, min(bs, L - (j0 + k) * bs));
         uint4 *out = reinterpret_cast<uint4 *>(a.bounds) + static_cast<int64_t>(phys) * a.row_chunks * 2;
         out += 2 * (c / a.head_chunks) * a.head_chunks + c % a.head_chunks;
         out[0] = Range<F8>::pack(r.lo), out[a.head_chunks] = Range<F8>::pack(r.hi);
@@ -332,7 +332,8 @@ __device__ uint64_t exact_score(const SelectArgs &a, const float *q, int phys, i
 // took 15 of 48 us for 1025 blocks.)  A sum in fp32 does not tell neighbours apart that
 // differ by less than its error, so blocks that the border may lie among (a few) are
 // scored again, exactly for all that matters.  Bound by memory where a context is long (the
-// bounds are read once), by the chain of loads, meetings and passes where it is short.
+// bounds are read once), by the chain of loads, meetings and passes where it is short: 2 rows of
+// 1025 blocks take 10.4 us, 64 rows of 2048 (34 MB) 17, 128 ragged FP8 rows of up to 8192 (135 MB) 73.
 template <bool F8, int D>
 __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const SelectArgs a) {
     constexpr int kRowBytes = 2 * D * (F8 ? 1 : 2);
@@ -389,9 +390,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     const int j0 = min(rank * per, n), j1 = min(j0 + per, n);
     const int n_tiles = (j1 - j0 + 15) / 16;
     int next_id = lane < 16 && j0 + warp * 16 + lane < j1 ? bt[j0 + warp * 16 + lane] : -1;
-    constexpr int kSlots = 1;            // tiles on their way
-    uint4 raw[kSlots][2][kChunks];       // rows g and g + 8
-    uint32_t ok[kSlots];                 // the tiles' rows that are there
+    uint4 raw[2][kChunks];               // rows g and g + 8 of the tile on its way
+    uint32_t ok;                         // its rows that are there
     auto load = [&](int tile, uint4(&k)[2][kChunks], uint32_t &there_all) {
         const int id = next_id, j = j0 + tile * 16 + (lane & 15);
         const bool fits = id >= 0 && id < a.num_blocks, here = lane < 16 && j < j1;
@@ -408,8 +408,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             for (int c = 0; c < kChunks; ++c) k[r][c] = there ? load_once(at + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s) load(warp + s * kSelWarps, raw[s], ok[s]);
+    load(warp, raw, ok);
 
     // ---- the sums of the queries' |values|, and the MMA's columns
     __syncthreads();
@@ -468,71 +467,66 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
 
     // ---- scores
     uint32_t largest = 0u, w_lo = ~0u, w_hi = 0u, w_in = 0u, w_above = 0u;
-    for (int tile0 = warp; tile0 < n_tiles; tile0 += kSlots * kSelWarps) {
+    for (int tile = warp; tile < n_tiles; tile += kSelWarps) {
+        uint32_t top[2] = {0u, 0u};  // largest |bound| of the rows, two of them side by side; a NaN stays
+        float best[2] = {-INFINITY, -INFINITY};
+        for (int nt = 0; nt < tiles; ++nt) {
+            float part[4][4] = {}, acc[4];  // (four sums: shorter chains, and a quarter of the error)
 #pragma unroll
-        for (int slot = 0; slot < kSlots; ++slot) {
-            const int tile = tile0 + slot * kSelWarps;
-            if (tile >= n_tiles) break;
-            uint32_t top[2] = {0u, 0u};  // largest |bound| of the rows, two of them side by side; a NaN stays
-            float best[2] = {-INFINITY, -INFINITY};
-            for (int nt = 0; nt < tiles; ++nt) {
-                float part[4][4] = {}, acc[4];  // (four sums: shorter chains, and a quarter of the error)
+            for (int c = 0; c < kChunks; ++c) {
+                uint4 x[Chunk<F8>::kVecs], y[Chunk<F8>::kVecs];
+                widen<F8>(raw[0][c], x);
+                widen<F8>(raw[1][c], y);
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    uint4 x[Chunk<F8>::kVecs], y[Chunk<F8>::kVecs];
-                    widen<F8>(raw[slot][0][c], x);
-                    widen<F8>(raw[slot][1][c], y);
-#pragma unroll
-                    for (int k = 0; k < Chunk<F8>::kVecs; ++k) {
-                        const int v = c * Chunk<F8>::kVecs + k;
-                        const uint4 w = qs[(nt * kVecs + v) * 32 + lane];
-                        mma_16x8x16<F8>(part[2 * v & 3], x[k].x, y[k].x, x[k].y, y[k].y, w.x, w.y);
-                        mma_16x8x16<F8>(part[(2 * v + 1) & 3], x[k].z, y[k].z, x[k].w, y[k].w, w.z, w.w);
-                        if (nt == 0) {
-                            top[0] = largest2<F8>(largest2<F8>(top[0], x[k].x, x[k].y), x[k].z, x[k].w);
-                            top[1] = largest2<F8>(largest2<F8>(top[1], y[k].x, y[k].y), y[k].z, y[k].w);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (nt * 8 + 2 * t + i < a.G) {
-                        // (an overflow of finite values leaves the error infinite: any finite number will do)
-                        const float u = F8 ? acc[i] * down0 * down1 : acc[i], v = F8 ? acc[2 + i] * down0 * down1 : acc[2 + i];
-                        best[0] = fmaxf(best[0], u == u ? u : 0.f), best[1] = fmaxf(best[1], v == v ? v : 0.f);
+                for (int k = 0; k < Chunk<F8>::kVecs; ++k) {
+                    const int v = c * Chunk<F8>::kVecs + k;
+                    const uint4 w = qs[(nt * kVecs + v) * 32 + lane];
+                    mma_16x8x16<F8>(part[2 * v & 3], x[k].x, y[k].x, x[k].y, y[k].y, w.x, w.y);
+                    mma_16x8x16<F8>(part[(2 * v + 1) & 3], x[k].z, y[k].z, x[k].w, y[k].w, w.z, w.w);
+                    if (nt == 0) {
+                        top[0] = largest2<F8>(largest2<F8>(top[0], x[k].x, x[k].y), x[k].z, x[k].w);
+                        top[1] = largest2<F8>(largest2<F8>(top[1], y[k].x, y[k].y), y[k].z, y[k].w);
                     }
                 }
             }
-            const uint32_t there = ok[slot];
-            load(tile + kSlots * kSelWarps, raw[slot], ok[slot]);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float s = best[r];
-                uint32_t m = top[r];
+            for (int i = 0; i < 4; ++i) acc[i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-                    m = largest2<F8>(m, __shfl_xor_sync(0xffffffffu, m, o), 0u);
+            for (int i = 0; i < 2; ++i) {
+                if (nt * 8 + 2 * t + i < a.G) {
+                    // (an overflow of finite values leaves the error infinite: any finite number will do)
+                    const float u = F8 ? acc[i] * down0 * down1 : acc[i], v = F8 ? acc[2 + i] * down0 * down1 : acc[2 + i];
+                    best[0] = fmaxf(best[0], u == u ? u : 0.f), best[1] = fmaxf(best[1], v == v ? v : 0.f);
                 }
-                const float2 mm = F8 ? f16x2_values(m) : make_float2(bf16lo(m), bf16hi(m));
-                const bool fine = q_fine && mm.x < INFINITY && mm.y < INFINITY;
-                const int j = j0 + tile * 16 + g + 8 * r;
-                if (t == 0 && j < j1) {
-                    uint32_t key;
-                    if (j < a.first || j >= n - a.last) key = kForced;
-                    else if (!((there >> (g + 8 * r)) & 1u)) key = 0u;
-                    else if (!fine) key = kEndless;
-                    else key = float_key(fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f));
-                    if (C > 1) st_shared_cluster_u32(keys0 + 4 * j, key);
-                    else keys[j] = key;
-                    if (key >= kPastFinite) {
-                        ++w_above;
-                    } else if (key) {
-                        ++w_in, w_lo = min(w_lo, key), w_hi = max(w_hi, key);
-                        largest = max(largest, __float_as_uint(fmaxf(mm.x, mm.y)));
-                    }
+            }
+        }
+        const uint32_t there = ok;
+        load(tile + kSelWarps, raw, ok);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float s = best[r];
+            uint32_t m = top[r];
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+                m = largest2<F8>(m, __shfl_xor_sync(0xffffffffu, m, o), 0u);
+            }
+            const float2 mm = F8 ? f16x2_values(m) : make_float2(bf16lo(m), bf16hi(m));
+            const bool fine = q_fine && mm.x < INFINITY && mm.y < INFINITY;
+            const int j = j0 + tile * 16 + g + 8 * r;
+            if (t == 0 && j < j1) {
+                uint32_t key;
+                if (j < a.first || j >= n - a.last) key = kForced;
+                else if (!((there >> (g + 8 * r)) & 1u)) key = 0u;
+                else if (!fine) key = kEndless;
+                else key = float_key(fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f));
+                if (C > 1) st_shared_cluster_u32(keys0 + 4 * j, key);
+                else keys[j] = key;
+                if (key >= kPastFinite) {
+                    ++w_above;
+                } else if (key) {
+                    ++w_in, w_lo = min(w_lo, key), w_hi = max(w_hi, key);
+                    largest = max(largest, __float_as_uint(fmaxf(mm.x, mm.y)));
                 }
             }
         }

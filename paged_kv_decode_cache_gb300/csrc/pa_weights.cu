@@ -79,7 +79,9 @@ __device__ __forceinline__ void add_columns(float (&sum)[2], const float (&acc)[
 // registers of keys (8 KB a warp) on their way: a tile's registers are loaded again as soon
 // as its products are done.  With up to 8 columns (kOne) the queries stay in registers.
 // The four lanes that share a token add up two tiles at once and end with a token each, so
-// that old and new weights are whole lines.
+// that old and new weights are whole lines.  A 7B-shaped step (34 MB of keys) takes 9.2 us, half of
+// them the launch and the first loads' chain; 32 ragged FP8 sequences of up to 16384 tokens (294
+// MB) 57 to 63 us, 0.7 to 0.77 of a copy's rate.
 template <bool F8, int D, bool kOne>
 __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs a, int pairs) {
     constexpr int kRowBytes = D * (F8 ? 1 : 2);
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
     float *out = a.out + (old - a.old);
     int32_t *positions = a.positions ? a.positions + (old - a.old) : nullptr;
     const uint8_t *keys = a.keys + h * kRowBytes + 16 * t;
-    const int stride = a.Hkv * kRowBytes;                  // between rows (check_cache: below 2^31)
+    const int stride = a.Hkv * kRowBytes;                  // between rows
     uint4 raw[kSlots][2][kChunks];
     float was[kSlots / 2];
     auto load = [&](int i, uint4(&k)[2][kChunks]) {        // tile i
@@ -211,8 +213,11 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 //
 // S[128 tokens, N] = K[128, D] . Q^T[D, N] per tile, N <= 256 columns (query, head of the
 // group) at a time, by tcgen05.mma into TMEM; a thread per token then adds up its row's
-// exponentials.  Per tile N products of 128 x D, 128 N exponentials and D keys a token; with
-// everything overlapped none of the three takes 1 us.
+// exponentials.  Per tile N products of 128 x D (0.4 us for 224 columns), 128 N exponentials (1.0
+// us at 32 a clock) and 32 KB of keys (0.75 us at an SM's share of the memory), all overlapped.  32
+// queries of 7 heads over 4 x 32768 tokens take 46 us (memory alone: 20), a tile 1.2 us: what the
+// exponentials take with their loads from TMEM and of -lse from shared memory.  (Both in registers,
+// a thread's columns the same in every row: 61 us, spills.)
 //
 // Two tiles' scores are in TMEM (four of up to 128 columns), and four groups of four warps
 // add them up, two a tile (one), a half of the columns each, while the MMA makes others.  An
@@ -413,7 +418,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 // asynchronously kXAhead tiles ahead into the lane's own part of a ring of codes, which it
                 // widens into the stage later.  The fence to the MMA's proxy is the MMA warp's, after the
                 // stage's barrier: here it would wait for the copies of the next tiles, too.
-                constexpr int kRowChunks = D * (F8 ? 1 : 2) / 16, kPer = kXLoadRows * kRowChunks / 32;
+                constexpr int kRowChunks = D / 16, kPer = kXLoadRows * kRowChunks / 32;
                 constexpr int kRowsAtOnce = 32 / kRowChunks;
                 const int lw = warp - kXLoadWarp;
                 uint8_t *own = codes + (lw * 32 + lane) * 16;
@@ -426,8 +431,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                     if (phys >= 0 && phys < a.num_blocks) places = phys * bs + row0 % bs;
                     else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
                 }
-                const uint8_t *keys = a.keys + static_cast<int64_t>(h) * (D * (F8 ? 1 : 2)) + 16 * (lane % kRowChunks);
-                const int stride = a.Hkv * D * (F8 ? 1 : 2), my_row = lane / kRowChunks;
+                const uint8_t *keys = a.keys + static_cast<int64_t>(h) * D + 16 * (lane % kRowChunks);
+                const int stride = a.Hkv * D, my_row = lane / kRowChunks;
                 auto issue = [&](int i) {  // tile i (a commit group)
                     const int place = __shfl_sync(0xffffffffu, places, i & 31);
                     if (i < tiles) {
@@ -447,7 +452,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                     issue(i + kXAhead);
                     cp_async_wait<kXAhead>();
                     const int u = it + i, s = u % kXStages;
-                    if (u >= kXStages) good = good && __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
+                    if (u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
                     if (!good) break;
 #pragma unroll
                     for (int j = 0; j < kPer; ++j) {

@@ -161,6 +161,24 @@ def test_selected_reports_bad_blocks_and_lengths():
             assert status.item() == bit
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("splits", [1, 3])
+def test_selected_on_cuda_cores_with_the_grid_merge_and_plain_launches(use_kernel, merge_path, splits):
+    """The kernels and launches that the switches choose."""
+    use_kernel("cuda_core")
+    case(8, 2, 128, 16, ragged(3, 2, 500, 5), splits)
+    use_kernel("auto")
+    merge_path("grid")
+    for d, fp8 in ((128, False), (128, True), (64, False)):
+        case(8, 2, d, 16, ragged(3, 2, 500, 6), splits, fp8)
+    prev = pa.pa_get_option(pa.PA_OPT_PDL)
+    pa.pa_set_option(pa.PA_OPT_PDL, 0)
+    try:
+        case(8, 2, 128, 16, ragged(3, 2, 500, 7), splits)
+    finally:
+        pa.pa_set_option(pa.PA_OPT_PDL, prev)
+
+
 FAKE = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced: these calls fail validation first
 
 
