@@ -225,6 +225,7 @@ struct SelectArgs {
     int32_t num_blocks, block_size, Hkv, G, max_blocks, K, first, last;
     int32_t ctas;            // of a cluster: a row of blocks
     int32_t room;            // keys in shared memory: blocks of a row, at most
+    int32_t B, sorted;       // sorted: the longest sequences' clusters first
 };
 
 constexpr int kSelThreads = 256;
@@ -232,6 +233,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelCtas = 8;              // portable cluster size
 constexpr int kSelMaxBlocks = 40960;     // of a sequence: their keys in one CTA's shared memory
 constexpr uint32_t kSelFew = 32;         // the search for the border ends with so many keys near it
+constexpr int kSelSorted = 256;          // sequences that are put in order, at a time
+constexpr int kSelBatch = 4;             // keys that a thread reads together
 constexpr int kSelList = 256;            // blocks near the border that are scored again at once
 constexpr uint32_t kForced = 0xffffffffu;   // keys above every finite score's: blocks that are always taken ...
 constexpr uint32_t kEndless = 0xfffffffeu;  // ... and blocks (or queries) with an infinity or a NaN
@@ -255,6 +258,26 @@ __device__ __forceinline__ uint32_t largest2(uint32_t m, uint32_t u, uint32_t v)
         const __nv_bfloat162 r = __hmax2_nan(__hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&m), a), b);
         return *reinterpret_cast<const uint32_t *>(&r);
     }
+}
+
+// The z-th of the sequences by length, the longest first (of kSelSorted of them at a time, in their
+// order among equals), by the CTA.
+__device__ __forceinline__ int sequence_by_length(const SelectArgs &a, int z) {
+    __shared__ __align__(16) int32_t lens_s[kSelSorted];
+    __shared__ int32_t found_s;
+    const int tid = threadIdx.x, base = z / kSelSorted * kSelSorted, n = min(kSelSorted, a.B - base);
+    const int mine = tid < n ? a.lens[base + tid] : INT32_MIN;
+    lens_s[tid] = mine;
+    __syncthreads();
+    int rank = 0;
+    for (int j = 0; j < n; j += 4) {  // (those behind the last one are the least)
+        const int4 x = *reinterpret_cast<const int4 *>(lens_s + j);
+        rank += (x.x > mine || (x.x == mine && j < tid)) + (x.y > mine || (x.y == mine && j + 1 < tid)) +
+                (x.z > mine || (x.z == mine && j + 2 < tid)) + (x.w > mine || (x.w == mine && j + 3 < tid));
+    }
+    if (tid < n && rank == z - base) found_s = tid;
+    __syncthreads();
+    return base + found_s;
 }
 
 // a + b = s + e, exactly.
@@ -333,7 +356,7 @@ __device__ uint64_t exact_score(const SelectArgs &a, const float *q, int phys, i
 // differ by less than its error, so blocks that the border may lie among (a few) are
 // scored again, exactly for all that matters.  Bound by memory where a context is long (the
 // bounds are read once), by the chain of loads, meetings and passes where it is short: 2 rows of
-// 1025 blocks take 10.4 us, 64 rows of 2048 (34 MB) 17, 128 ragged FP8 rows of up to 8192 (135 MB) 73.
+// 1025 blocks take 10.4 us, 32 rows of 2048 (34 MB) 16.5, 128 ragged FP8 rows of up to 8192 (135 MB) 50.
 template <bool F8, int D>
 __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const SelectArgs a) {
     constexpr int kRowBytes = 2 * D * (F8 ? 1 : 2);
@@ -346,15 +369,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     float *qf = reinterpret_cast<float *>(qs + tiles * kVecs * 32);       // [G][D]
     uint32_t *keys = reinterpret_cast<uint32_t *>(qf + a.G * D);          // [room], the first CTA's
     __shared__ uint64_t wide_s[kSelList];       // blocks near the border: their exact scores as ordered keys,
-    __shared__ int32_t list_s[kSelList], id_s[kSelList];  // which they are, their ids
+    __shared__ int32_t list_s[kSelList];        // which they are
     __shared__ uint32_t window_s[4], largest_s; // the first CTA's: finite keys' least, largest, number; marks; largest bound
     __shared__ float qsum_s[32], qmax_s[32];    // sum of |q| of every head, -1 where one is not finite; the largest
     __shared__ uint32_t n_near_s, n_in_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int C = a.ctas, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int h = blockIdx.y, b = blockIdx.z, bs = a.block_size;
+    const int h = blockIdx.y, bs = a.block_size;
     griddep_wait();
     griddep_launch_dependents();
+    const int b = a.sorted ? sequence_by_length(a, blockIdx.z) : static_cast<int>(blockIdx.z);
 
     // the queries' values, on their way with the length
     const int64_t row = static_cast<int64_t>(b) * a.Hkv + h;
@@ -566,12 +590,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             const uint32_t low = max(float_key(__fadd_rd(key_float(from), -2.f * err)), kFirstFinite);
             const uint32_t high = min(float_key(__fadd_ru(key_float(to), 2.f * err)), kPastFinite - 1u);
             uint32_t in = 0;
-            for (int i = tid; i < n; i += kSelThreads) {
-                const uint32_t k = keys[i];
-                in += k > high;
-                if (k >= low && k <= high) {
-                    const uint32_t p = atomicAdd(&n_near_s, 1u);
-                    if (p < kSelList) list_s[p] = i, id_s[p] = bt[i];
+            for (int i0 = tid; i0 < n; i0 += kSelBatch * kSelThreads) {
+                uint32_t k[kSelBatch];
+#pragma unroll
+                for (int j = 0; j < kSelBatch; ++j) k[j] = i0 + j * kSelThreads < n ? keys[i0 + j * kSelThreads] : 0u;
+#pragma unroll
+                for (int j = 0; j < kSelBatch; ++j) {
+                    in += k[j] > high;
+                    if (k[j] >= low && k[j] <= high) {
+                        const uint32_t p = atomicAdd(&n_near_s, 1u);
+                        if (p < kSelList) list_s[p] = i0 + j * kSelThreads;
+                    }
                 }
             }
             __syncwarp();
@@ -595,7 +624,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             need = ~0u;  // all of them
         } else if (n_near <= kSelList) {  // a warp per block, then ranked
             for (uint32_t p = warp; p < n_near; p += kSelWarps) {
-                const uint64_t s = exact_score<F8, D>(a, qf, id_s[p], h, wide, lane);
+                const uint64_t s = exact_score<F8, D>(a, qf, bt[list_s[p]], h, wide, lane);
                 if (lane == 0) wide_s[p] = s;
             }
             __syncthreads();
@@ -645,15 +674,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
     for (int i = i0 + lane; i < i1; i += 32) taken[0] += keys[i] > to, taken[1] += keys[i] >= from && keys[i] <= to;
     __syncwarp();
     cluster_counts<kSelThreads>(taken, 1, sh, 1, before, total);
-    for (int i = i0; i < i1; i += 32) {
-        const bool here = i + lane < i1;
-        const uint32_t k = here ? keys[i + lane] : 0u;
-        const bool in = here && k > to, even = here && k >= from && k <= to;
-        const uint32_t ins = __ballot_sync(0xffffffffu, in), evens = __ballot_sync(0xffffffffu, even);
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t tied = before[1] + __popc(evens & below);
-        if (in || (even && tied < need)) out[before[0] + __popc(ins & below) + min(tied, need)] = bt[i + lane];
-        before[0] += __popc(ins), before[1] += __popc(evens);
+    for (int i = i0; i < i1; i += 32 * kSelBatch) {
+        uint32_t k[kSelBatch];
+        int32_t id[kSelBatch];
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j) {  // (ids on their way together)
+            const int x = i + 32 * j + lane;
+            k[j] = x < i1 ? keys[x] : 0u;
+            if (x < i1 && k[j] >= from) id[j] = bt[x];
+        }
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j) {
+            const bool here = i + 32 * j + lane < i1, in = here && k[j] > to, even = here && k[j] >= from && k[j] <= to;
+            const uint32_t ins = __ballot_sync(0xffffffffu, in), evens = __ballot_sync(0xffffffffu, even);
+            const uint32_t below = (1u << lane) - 1u;
+            const uint32_t tied = before[1] + __popc(evens & below);
+            if (in || (even && tied < need)) out[before[0] + __popc(ins & below) + min(tied, need)] = id[j];
+            before[0] += __popc(ins), before[1] += __popc(evens);
+        }
     }
 }
 
@@ -756,13 +794,16 @@ int pa_blocks_select(int32_t *sel_tables, int32_t max_selected, int32_t *sel_len
     a.num_blocks = cache.num_blocks, a.block_size = cache.block_size, a.Hkv = cache.num_kv_heads;
     a.G = Hq / cache.num_kv_heads, a.max_blocks = max_blocks_per_seq, a.K = max_selected, a.first = first, a.last = last;
     // a cluster of eight per row, or of fewer where those would run in more than two waves (128 rows of up
-    // to 8192 blocks: 8 CTAs 73 us, 4 70, 2 84, 1 128)
+    // to 8192 blocks: 8 CTAs 60 us, 4 50, 2 80, 1 125)
     const int sms = pa::sm_count();
     if (sms <= 0) return PA_ECUDA;
     const int64_t rows = static_cast<int64_t>(B) * cache.num_kv_heads;
     a.ctas = pa::kSelCtas;
     while (a.ctas > 1 && rows * a.ctas > 4 * sms) a.ctas /= 2;
     a.room = max_blocks_per_seq;
+    // the longest first where there is a second wave, which then has the short ones (62 -> 50 us; where
+    // all run at once the order is 0.3 us of latency)
+    a.B = B, a.sorted = B > 1 && rows * a.ctas > 2 * sms;
     cudaError_t e;
     if (elem_bytes == 1)
         e = cache.head_dim == 128 ? pa::launch_select<true, 128>(a, B, stream) : pa::launch_select<true, 64>(a, B, stream);

@@ -96,18 +96,21 @@ __device__ Border cluster_narrow(F key, int n, Border w, int C, TopkShared &sh, 
     while (w.lo != w.hi && w.m != w.inside && w.inside > few) {
         const uint32_t span = w.hi - w.lo;
         const int shift = max(0, 32 - __clz(static_cast<int>(span)) - kTopkBits);
-        for (int i = tid; i - lane < n; i += kThreads) {  // (whole warps)
-            const uint32_t k = i < n ? key(i) : 0u;
-            const bool in = i < n && k >= w.lo && k <= w.hi;
-            const uint32_t bin = (k - w.lo) >> shift;
-            // a warp's keys in one bin, as many equal ones are: one addition
-            const uint32_t act = __ballot_sync(0xffffffffu, in);
-            if (!act) continue;
-            const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
-            if (__all_sync(0xffffffffu, !in || bin == first)) {
-                if (lane == 0) atomicAdd(&sh.hist[buf][first], static_cast<uint32_t>(__popc(act)));
-            } else if (in) {
-                atomicAdd(&sh.hist[buf][bin], 1u);
+        constexpr int kBatch = 4;  // keys read together (the additions would hold the next ones up)
+        for (int i0 = tid; i0 - lane < n; i0 += kBatch * kThreads) {  // (whole warps)
+            uint32_t k[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kThreads < n ? key(i0 + j * kThreads) : 0u;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const bool in = i0 + j * kThreads < n && k[j] >= w.lo && k[j] <= w.hi;
+                const uint32_t bin = (k[j] - w.lo) >> shift;
+                // a warp's keys in one bin, as many equal ones are: one addition
+                const uint32_t act = __ballot_sync(0xffffffffu, in);
+                const uint32_t first = __shfl_sync(0xffffffffu, bin, act ? __ffs(act) - 1 : 0);
+                const bool one = __all_sync(0xffffffffu, !in || bin == first);
+                if (in && (!one || lane == __ffs(act) - 1))
+                    atomicAdd(&sh.hist[buf][bin], one ? static_cast<uint32_t>(__popc(act)) : 1u);
             }
         }
         meet(C);

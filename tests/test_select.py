@@ -203,6 +203,16 @@ def test_select(hq, hkv, d, bs, lens, K, first, last, fp8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Bn,hkv,fp8", [(300, 1, False), (259, 2, True), (40, 8, False)])
+def test_select_in_many_rows(Bn, hkv, fp8):
+    """More clusters than run at once: sequences are taken by length, some of them equal."""
+    rng = random.Random(Bn)
+    lens = [rng.choice([0, 16, 200, 200, 333, rng.randint(1, 700)]) for _ in range(Bn)]
+    tables, _, nb = layout(lens, 16, seed=Bn)
+    check(queries(Bn, 2 * hkv, 64, Bn), make_bounds(nb, hkv, 64, fp8, Bn + 1), tables, lens, 16, 6, 1, 1)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(6))
 def test_select_scores_that_fp32_does_not_tell_apart(seed):
     """Hundreds of blocks that differ in one small channel by one step: sums in 64 bits tell them apart, sums in fp32
