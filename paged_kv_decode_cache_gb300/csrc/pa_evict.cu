@@ -12,9 +12,9 @@
 // lengths, tables and counts.  evict_kernel has a thread-block cluster per (layer,
 // sequence, head): it finds the n-th largest weight over its shared memory (pa_topk.cuh),
 // lists the free places and the tokens for them, and moves the rows.  Bound by the chain of the
-// search where few tokens are thrown out (the 8 x 4 rows of a step, 64 of 1088 tokens each: 10.7 us),
-// by memory and the search's passes where many are (8 layers of 4 FP8 prompts of up to 16384 tokens: 94 us; moving the rows
-// alone takes 38 at a copy's rate).
+// search where few tokens are thrown out (the 8 x 4 rows of a step, 64 of 1088 tokens each: 9.7 us);
+// where many are (8 layers of 4 FP8 prompts of up to 16384 tokens: 67 us, half of the copy's rate for
+// what is read and written) by the search, 24 us for all rows side by side, and then by memory.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -30,6 +30,8 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictCtas = 8;             // portable cluster size
 constexpr int kEvictMaxSlice = 24576;     // tokens of a CTA
+constexpr size_t kEvictSmemOfTwo = 113 * 1024;  // shared memory of a CTA of which two fit an SM
+constexpr int kMoveTurns = 4;             // of a warp's ring of rows
 constexpr uint32_t kSafe = 0xffffffffu;   // key of a token that stays whatever its weight
 
 struct EvictArgs {
@@ -43,7 +45,7 @@ struct EvictArgs {
     int64_t room;
     int32_t B, Hkv, max_blocks, num_blocks, block_size;
     int32_t budget, first, recent;
-    int32_t ctas, slice;           // of a cluster; tokens of a CTA at most
+    int32_t ctas, slice, moves;    // of a cluster; tokens and moved rows of a CTA at most
     int32_t row_chunks;            // 16-byte chunks of one head's row in a pool
     uint8_t *pools[kEvictMaxPools];  // a layer's K and V in turn
 };
@@ -97,35 +99,40 @@ __global__ void __launch_bounds__(kLensThreads) evict_lens_kernel(const __grid_c
     for (int j = tid; j < a.max_blocks; j += kLensThreads) out[j] = j < min(stay, n_used) ? used_entry(a, row, j) : j < stay ? next : -1;
 }
 
-// Rows src[p] -> dst[p] (places of this head in both pools of a layer) for the `count` pairs of this
-// warp, lane p's own; kChunks: 16-byte chunks of a row, kLanes / kChunks rows at once.
+// Words of shared memory for keys, and for the rows on their way.
+__host__ __device__ constexpr int evict_keys(int slice) {
+    return slice > kEvictWarps * kMoveTurns * 256 ? slice : kEvictWarps * kMoveTurns * 256;
+}
+
+// Rows src[p] -> dst[p], p < n (places of this head in both pools of a layer; in shared memory), by the
+// CTA; kChunks: 16-byte chunks of a row.  A warp has kMoveTurns - 1 turns of 32 chunks of each pool on
+// their way to its part of `stage`, from which every lane takes what it copied itself.  (Through
+// registers, two turns at a time: the prompts 87 us; with 2 or 5 turns on their way 69 and 77.)
 template <int kChunks>
-__device__ __forceinline__ void move_rows(uint8_t *k_pool, uint8_t *v_pool, int Hkv, int h, int src, int dst, int count,
-                                          int lane) {
-    constexpr int kRows = 32 / kChunks;   // pairs of one turn
-    constexpr int kTurns = 2;             // turns whose loads are in flight together (of 32 warps per SM)
-    const int sub = lane / kChunks, chunk = lane % kChunks;
-    for (int p0 = 0; p0 < count; p0 += kRows * kTurns) {
-        uint4 v[kTurns][2];
-        int64_t to[kTurns];
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int p = p0 + i * kRows + sub;
-            const int from = __shfl_sync(0xffffffffu, src, p & 31), into = __shfl_sync(0xffffffffu, dst, p & 31);
-            const int64_t at = (static_cast<int64_t>(from) * Hkv + h) * kChunks + chunk;
-            to[i] = p < count ? (static_cast<int64_t>(into) * Hkv + h) * kChunks + chunk : -1;
-            if (to[i] >= 0) {
-                v[i][0] = reinterpret_cast<const uint4 *>(k_pool)[at];
-                v[i][1] = reinterpret_cast<const uint4 *>(v_pool)[at];
-            }
+__device__ __forceinline__ void move_rows(uint4 *k_pool, uint4 *v_pool, int Hkv, int h, const int32_t *src, const int32_t *dst,
+                                          int n, uint4 *stage) {
+    constexpr int kRows = 32 / kChunks, kStep = kEvictWarps * kRows;  // pairs of a turn, of all warps' turns
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int p0 = warp * kRows + lane / kChunks, chunk = lane % kChunks;
+    stage += warp * (kMoveTurns * 64) + lane;
+    auto at = [&](int place) { return (static_cast<int64_t>(place) * Hkv + h) * kChunks + chunk; };
+    auto issue = [&](int p, int slot) {
+        if (p < n) {
+            const int64_t x = at(src[p]);
+            cp_async_16(stage + 64 * slot, k_pool + x);
+            cp_async_16(stage + 64 * slot + 32, v_pool + x);
         }
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            if (to[i] >= 0) {
-                reinterpret_cast<uint4 *>(k_pool)[to[i]] = v[i][0];
-                reinterpret_cast<uint4 *>(v_pool)[to[i]] = v[i][1];
-            }
-        }
+    for (int i = 0; i < kMoveTurns - 1; ++i) issue(p0 + i * kStep, i);
+    int slot = 0, next = kMoveTurns - 1;
+    for (int p = p0; p < n; p += kStep) {
+        issue(p + (kMoveTurns - 1) * kStep, next);
+        cp_async_wait<kMoveTurns - 1>();
+        const int64_t x = at(dst[p]);
+        k_pool[x] = stage[64 * slot], v_pool[x] = stage[64 * slot + 32];
+        slot = slot + 1 == kMoveTurns ? 0 : slot + 1, next = next + 1 == kMoveTurns ? 0 : next + 1;
     }
 }
 
@@ -133,8 +140,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     extern __shared__ __align__(16) uint8_t evict_smem[];
     TopkShared &sh = *reinterpret_cast<TopkShared *>(evict_smem);
     uint32_t *keys = reinterpret_cast<uint32_t *>(evict_smem + kTopkSharedBytes);
-    int32_t *holes = reinterpret_cast<int32_t *>(keys + a.slice);   // this CTA's pairs: [slice / 2] free places
-    int32_t *movers = holes + a.slice / 2;                          // ... and the tokens that take them
+    int32_t *holes = reinterpret_cast<int32_t *>(keys + evict_keys(a.slice));   // this CTA's pairs: [moves] free places
+    int32_t *movers = holes + a.moves;                              // ... and the tokens that take them
     __shared__ int past_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bs = a.block_size;
     const int C = a.ctas, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -200,7 +207,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     }
     __syncthreads();
 
-    const Border edge = cluster_threshold<kEvictThreads>([&](int i) { return keys[i]; }, mine, seen, n, 0u, kSafe - 1u, C, sh, 0u);
+    auto key_at = [&](int i) { return keys[i]; };
+    Border edge = cluster_threshold<kEvictThreads>(key_at, mine, seen, n, 0u, kSafe - 1u, C, sh, kTopkFew);
+    edge = cluster_finish<kEvictThreads>(key_at, mine, edge, C, sh);
     const uint32_t border = edge.lo, need = edge.m == edge.inside ? ~0u : edge.m;
 
     // ---- which tokens stay: those above the border (or all from it on: none then counts as at it, or every one
@@ -238,24 +247,41 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
 
     // ---- the rows
     const int my_pairs = (pairs - rank + C - 1) >> log_ctas;
-    const int group = min(32, max(2, (my_pairs + kEvictWarps - 1) / kEvictWarps));
-    uint8_t *k_pool = a.pools[2 * layer], *v_pool = a.pools[2 * layer + 1];
-    for (int p0 = warp * group; p0 < my_pairs; p0 += kEvictWarps * group) {
-        const int count = min(group, my_pairs - p0);
-        int src = 0, dst = 0;
-        if (lane < count) {
-            const int to = holes[p0 + lane], from = movers[p0 + lane];
-            src = table[from / bs] * bs + from % bs;
-            dst = table[to / bs] * bs + to % bs;
-            new_weights[to] = weights[from], new_positions[to] = positions[from];
+    // their places, and the weights and positions of the tokens that move
+    for (int p0 = tid; p0 < my_pairs; p0 += kBatch * kEvictThreads) {
+        float w[kBatch];
+        int pos[kBatch], to[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int p = p0 + j * kEvictThreads;
+            if (p >= my_pairs) break;
+            const int from = movers[p];
+            to[j] = holes[p];
+            w[j] = weights[from], pos[j] = positions[from];
+            movers[p] = table[from / bs] * bs + from % bs;
+            holes[p] = table[to[j] / bs] * bs + to[j] % bs;
         }
-        if (a.row_chunks == 16) move_rows<16>(k_pool, v_pool, a.Hkv, h, src, dst, count, lane);
-        else if (a.row_chunks == 8) move_rows<8>(k_pool, v_pool, a.Hkv, h, src, dst, count, lane);
-        else move_rows<4>(k_pool, v_pool, a.Hkv, h, src, dst, count, lane);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (p0 + j * kEvictThreads < my_pairs) new_weights[to[j]] = w[j], new_positions[to[j]] = pos[j];
     }
+    __syncthreads();
+    uint4 *k_pool = reinterpret_cast<uint4 *>(a.pools[2 * layer]), *v_pool = reinterpret_cast<uint4 *>(a.pools[2 * layer + 1]);
+    uint4 *stage = reinterpret_cast<uint4 *>(keys);  // (the keys have been used)
+    if (a.row_chunks == 16) move_rows<16>(k_pool, v_pool, a.Hkv, h, movers, holes, my_pairs, stage);
+    else if (a.row_chunks == 8) move_rows<8>(k_pool, v_pool, a.Hkv, h, movers, holes, my_pairs, stage);
+    else move_rows<4>(k_pool, v_pool, a.Hkv, h, movers, holes, my_pairs, stage);
 }
 
-size_t evict_smem_bytes(int slice) { return kTopkSharedBytes + static_cast<size_t>(slice) * 8; }
+size_t evict_smem_bytes(int slice, int moves) {
+    return kTopkSharedBytes + static_cast<size_t>(evict_keys(slice)) * 4 + static_cast<size_t>(moves) * 8;
+}
+// Rows that a sequence of up to `most` tokens moves, per CTA of C: no more than there are tokens behind the
+// new length n, or below it that may leave (n less those that others hold, at most the budget).
+int evict_moves(int64_t most, int budget, int C) {
+    return static_cast<int>((std::min<int64_t>(budget, most / 2) + C - 1) / C + 1) / 2 * 2;
+}
+int evict_slice(int64_t most, int C) { return static_cast<int>(((most + C - 1) / C + 31) / 32 * 32); }
 
 }  // namespace
 }  // namespace pa
@@ -302,15 +328,17 @@ extern "C" int pa_cache_evict(int32_t *new_tables, int32_t *new_lens, int32_t *n
     a.budget = budget, a.first = first, a.recent = recent;
     a.row_chunks = cache.head_dim * elem_bytes / 16;
     for (int i = 0; i < n_pools; ++i) a.pools[i] = static_cast<uint8_t *>(pools[i]);
-    // One CTA per row where it can be: its meetings and passes cost half of a cluster's.  More for
-    // rows of over 8192 tokens (two CTAs then fit an SM), and, of long rows, where there are few.
+    // One CTA per row where it can be: its meetings and passes cost half of a cluster's, and more rows are
+    // under way at once (256 rows of 16384 tokens: 1 CTA 67 us, 2 76, 4 92).  More where two would not fit
+    // an SM, and, of long rows, where there are few.
     const int sms = pa::sm_count();
     if (sms <= 0) return PA_ECUDA;
     a.ctas = 1;
     while (a.ctas < pa::kEvictCtas &&
-           (most > 8192 * a.ctas || (most >= 4096 * a.ctas && 2 * rows * a.ctas <= 2 * sms)))
+           (pa::evict_smem_bytes(pa::evict_slice(most, a.ctas), pa::evict_moves(most, budget, a.ctas)) > pa::kEvictSmemOfTwo ||
+            (most >= 4096 * a.ctas && 2 * rows * a.ctas <= 2 * sms)))
         a.ctas *= 2;
-    a.slice = static_cast<int32_t>(((most + a.ctas - 1) / a.ctas + 31) / 32 * 32);
+    a.slice = pa::evict_slice(most, a.ctas), a.moves = pa::evict_moves(most, budget, a.ctas);
     const int copies = (cache.num_blocks + pa::kLensThreads - 1) / pa::kLensThreads;
     if (pa::launch_maybe_cooperative(pa::evict_lens_kernel, dim3(B + copies), pa::kLensThreads, 0, stream, false, pa::pdl_on(),
                                      a) != cudaSuccess)
@@ -322,12 +350,12 @@ extern "C" int pa_cache_evict(int32_t *new_tables, int32_t *new_lens, int32_t *n
     const uint64_t bit = 1ull << (dev & 63);
     if (!(smem_attr_done.load(std::memory_order_acquire) & bit)) {
         if (cudaFuncSetAttribute(pa::evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(pa::evict_smem_bytes(pa::kEvictMaxSlice))) != cudaSuccess)
+                                 static_cast<int>(pa::evict_smem_bytes(pa::kEvictMaxSlice, pa::kEvictMaxSlice / 2 + 2))) != cudaSuccess)
             return PA_ECUDA;
         smem_attr_done.fetch_or(bit, std::memory_order_release);
     }
     const cudaError_t e = pa::launch_clustered(pa::evict_kernel, dim3(static_cast<unsigned>(rows * a.ctas)), a.ctas,
-                                               pa::kEvictThreads, static_cast<int>(pa::evict_smem_bytes(a.slice)), stream,
+                                               pa::kEvictThreads, static_cast<int>(pa::evict_smem_bytes(a.slice, a.moves)), stream,
                                                pa::pdl_on(), a);
     return e == cudaSuccess ? PA_OK : PA_ECUDA;
 }

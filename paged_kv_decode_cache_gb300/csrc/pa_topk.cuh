@@ -18,6 +18,7 @@ namespace pa {
 
 constexpr int kTopkBits = 11;
 constexpr int kTopkBins = 1 << kTopkBits;
+constexpr int kTopkFew = 64;   // keys that cluster_finish ranks, at most
 
 // Larger floats have larger keys; -0 and 0 have the same one.  No key is 0 or 0xffffffff
 // but a NaN's.
@@ -33,6 +34,11 @@ __device__ __forceinline__ uint64_t double_key(double x) {
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -67,6 +73,8 @@ struct TopkShared {
     uint32_t found[3];               // bin, keys above it, keys in it
     uint32_t warp_count[32][4];
     alignas(16) uint32_t count[2][4];  // this CTA's counts of cluster_counts
+    uint32_t n_few, few[kTopkFew];   // this CTA's keys of cluster_finish,
+    uint32_t all[kTopkFew];          // the cluster's
 };
 constexpr size_t kTopkSharedBytes = (sizeof(TopkShared) + 15) / 16 * 16;
 constexpr int kTopkCtas = 8;  // of a cluster, at most (a portable size)
@@ -195,6 +203,7 @@ __device__ Border cluster_threshold(F key, int n, Window seen, uint32_t m, uint3
     uint32_t n_above = __reduce_add_sync(0xffffffffu, seen.above), n_in = __reduce_add_sync(0xffffffffu, seen.in);
     if (lane == 0) sh.warp_count[warp][0] = lo, sh.warp_count[warp][1] = hi, sh.warp_count[warp][2] = n_above, sh.warp_count[warp][3] = n_in;
     for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[0][i] = 0;
+    if (tid == 0) sh.n_few = 0;
     __syncthreads();
     if (warp == 0) {
         const bool w = lane < kWarps;
@@ -209,6 +218,49 @@ __device__ Border cluster_threshold(F key, int n, Window seen, uint32_t m, uint3
     lo = __reduce_min_sync(0xffffffffu, lane < C ? r.x : ~0u), hi = __reduce_max_sync(0xffffffffu, r.y);
     n_above = __reduce_add_sync(0xffffffffu, r.z), n_in = __reduce_add_sync(0xffffffffu, r.w);
     return cluster_narrow<kThreads>(key, n, border_of(m, low, high, lo, hi, n_in, n_above), C, sh, few);
+}
+
+// The border of cluster_threshold(few = kTopkFew), narrowed to one value: the keys left are listed and
+// ranked, in one pass and one meeting (a further pass or two of cluster_narrow, 1 to 3 us each, otherwise).
+// Once per kernel; the cluster meets before a CTA leaves.
+template <int kThreads, typename F>
+__device__ Border cluster_finish(F key, int n, Border w, int C, TopkShared &sh) {
+    static_assert(kThreads >= kTopkFew * kTopkCtas, "a thread per key of every CTA");
+    if (w.lo == w.hi || w.m == w.inside) return w;
+    const int tid = threadIdx.x;
+    constexpr int kBatch = 4;
+    for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+        uint32_t k[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kThreads < n ? key(i0 + j * kThreads) : 0u;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (i0 + j * kThreads < n && k[j] >= w.lo && k[j] <= w.hi) sh.few[atomicAdd(&sh.n_few, 1u)] = k[j];
+    }
+    meet(C);
+    const int r = tid / kTopkFew, i = tid % kTopkFew;
+    uint32_t here = 0, at = 0;  // keys of CTA r, and of those before it
+    if (C == 1) {
+        if (r == 0) here = sh.n_few;
+        if (r == 0 && i < here) sh.all[i] = sh.few[i];
+    } else if (r < C) {
+        uint32_t c[kTopkCtas];
+#pragma unroll
+        for (int q = 0; q < kTopkCtas; ++q) c[q] = q < C ? ld_shared_cluster_u32(map_shared_rank(smem_u32(&sh.n_few), q)) : 0u;
+        const uint32_t k = ld_shared_cluster_u32(map_shared_rank(smem_u32(&sh.few[i]), r));
+#pragma unroll
+        for (int q = 0; q < kTopkCtas; ++q) here = q == r ? c[q] : here, at += q < r ? c[q] : 0u;
+        if (i < here) sh.all[at + i] = k;
+    }
+    __syncthreads();
+    if (tid < w.inside) {
+        const uint32_t mine = sh.all[tid];
+        uint32_t above = 0, even = 0;
+        for (uint32_t j = 0; j < w.inside; ++j) above += sh.all[j] > mine, even += sh.all[j] == mine;
+        if (above < w.m && w.m <= above + even) sh.found[0] = mine, sh.found[1] = above, sh.found[2] = even;
+    }
+    __syncthreads();
+    return Border{sh.found[0], sh.found[0], sh.found[2], w.m - sh.found[1]};
 }
 
 // Sums of N counts over the cluster's CTAs: *total, and over the CTAs of lower rank and this CTA's
