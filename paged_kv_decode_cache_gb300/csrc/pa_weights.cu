@@ -7,6 +7,7 @@
 // every time.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -211,92 +212,107 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 
 // ---- more columns (a window of queries over a long context): tensor cores --------------------
 //
-// S[128 tokens, N] = K[128, D] . Q^T[D, N] per tile, N <= 256 columns (query, head of the
-// group) at a time, by tcgen05.mma into TMEM; a thread per token then adds up its row's
-// exponentials.  Per tile N products of 128 x D (0.4 us for 224 columns), 128 N exponentials (1.0
-// us at 32 a clock) and 32 KB of keys (0.75 us at an SM's share of the memory), all overlapped.  32
-// queries of 7 heads over 4 x 32768 tokens take 46 us (memory alone: 20), a tile 1.2 us: what the
-// exponentials take with their loads from TMEM and of -lse from shared memory.  (Both in registers,
-// a thread's columns the same in every row: 61 us, spills.)
+// S[128 tokens, N] = K[128, D] . Q^T[D, N] per tile, N <= 256 columns (query, head of the group)
+// at a time, by tcgen05.mma into one of two buffers in TMEM; groups of four warps, each with
+// a share of the columns, add up their rows' exponentials, and the last warp joins the groups'
+// sums and writes the weights.  Per tile N products of 128 x D (0.5 us for 224 columns), 128 N
+// exponentials (0.5 us at 32 a clock) and 32 KB of keys (0.75 us at an SM's share of the
+// memory), all overlapped.  -lse stays in registers, a thread's columns being the same in every
+// row: loads of it from shared memory compete with the MMA's operands there.  32 queries of 7 heads
+// over 4 x 32768 tokens take 37.7 us (memory alone: 20), 6 queries 30: 5 us of start, 0.85 us a
+// tile (of a ring of four, each 2 to 3 us on its way), and 8 of 152 SMs without a share.
 //
-// Two tiles' scores are in TMEM (four of up to 128 columns), and four groups of four warps
-// add them up, two a tile (one), a half of the columns each, while the MMA makes others.  An
-// MMA of 128 columns takes as long as one of 224, so halves with buffers of their own
-// were no faster (47 us for the window below).  Keys come into a ring of stages as the MMA
-// reads them (K-major, 128-byte swizzle): by TMA from one warp (8 warps of asynchronous
-// copies: 5 us more), or for FP8 pools by 8 warps, which widen the codes to fp16 on the
-// way.  The last warp issues the MMAs.  Every wait is bounded.
-constexpr int kXGroups = 4;
+// Keys come into a ring of stages as the MMA reads them (K-major, 128-byte swizzle): by TMA from
+// one warp (8 warps of asynchronous copies: 5 us more), or for FP8 pools by 8 warps, which widen the
+// codes to fp16 on the way (50 us, bound by that).  Every wait is bounded.
+constexpr int kXColumns = 256;           // at once
 template <bool F8>
 struct XWarps {
-    static constexpr int kLoad = 4 * kXGroups;       // the first loading warp, after the exponentials'
+    static constexpr int kGroups = F8 ? 2 : 4;       // of four warps, for the exponentials (F8: registers for no more)
+    static constexpr int kPart = kXColumns / kGroups;  // columns of a group, at most
+    static constexpr int kLoad = 4 * kGroups;        // the first loading warp, after the exponentials'
     static constexpr int kMma = kLoad + (F8 ? 8 : 1);
-    static constexpr int kThreads = 32 * (kMma + 1);
+    static constexpr int kFinal = kMma + 1;
+    static constexpr int kThreads = 32 * (kFinal + 1);
 };
 constexpr int kXLoadRows = 16;           // FP8: tokens of a loading warp
 constexpr int kXRows = 128;              // tokens of a tile
 constexpr int kXAhead = 2;               // FP8: tiles whose copies are on their way
 constexpr int kXCodes = kXAhead + 1;     // FP8: tiles in the ring of codes
+constexpr int kXLook = 4;                // tiles whose old weights are on their way
 constexpr int kXMostTiles = 32;          // of a CTA
-constexpr int kXColumns = 256;           // at once
 
 template <bool F8, int D>
 struct XShape {
     static constexpr int kHalves = D / 64;                       // 64-element sub-rows
     static constexpr int kStages = F8 ? 2 : 4;
     static constexpr int kStageBytes = kHalves * kXRows * kSubBytes;
-    // dynamic shared memory: stages, codes, queries, sums, -lse, last tokens, barriers
+    // dynamic shared memory: stages, codes, queries, sums, -lse, last tokens, groups' sums, barriers, places
     static constexpr int kCodeBytes = F8 ? kXCodes * kXRows * D : 0;
     static constexpr int q_bytes(int n) { return kHalves * n * kSubBytes; }
     static constexpr int q_at() { return kStages * kStageBytes + kCodeBytes; }
     static constexpr int sums_at(int n) { return q_at() + q_bytes(n); }
     static constexpr int bytes(int n) {
-        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + 4 * kXRows * 4 + (2 * kStages + 11) * 8 + 16 + 1024;
+        return sums_at(n) + kXMostTiles * kXRows * 4 + 2 * kXColumns * 4 + 4 * XWarps<F8>::kGroups * kXRows * 4 +
+               (2 * kStages + 13) * 8 + 16 + kXMostTiles * kXRows / kTile * 4 + 1024;
     }
 };
 
-// The sum over the columns below n1 of a row in TMEM of 2^(s scale + nl), 32 at a time, in four
-// sums (a single chain of additions would take as long as the exponentials).  kMasked: only
-// columns that see token tok.
-template <bool kMasked>
-__device__ __forceinline__ float row_sum(uint32_t row, int n1, float scale, const float *nl, const int *last, int tok) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    auto add4 = [&](const uint32_t *x, int n) {
-        const float4 z = *reinterpret_cast<const float4 *>(nl + n);
-        const float e[4] = {fast_exp2(fmaf(__uint_as_float(x[0]), scale, z.x)), fast_exp2(fmaf(__uint_as_float(x[1]), scale, z.y)),
-                            fast_exp2(fmaf(__uint_as_float(x[2]), scale, z.z)), fast_exp2(fmaf(__uint_as_float(x[3]), scale, z.w))};
-        int4 l;
-        if (kMasked) l = *reinterpret_cast<const int4 *>(last + n);
-        sum[0] += !kMasked || tok <= l.x ? e[0] : 0.f;
-        sum[1] += !kMasked || tok <= l.y ? e[1] : 0.f;
-        sum[2] += !kMasked || tok <= l.z ? e[2] : 0.f;
-        sum[3] += !kMasked || tok <= l.w ? e[3] : 0.f;
-    };
-    int n = 0;
-    for (; n + 32 <= n1; n += 32) {
-        uint32_t x[32];
-        tc5::ld_32x32b_x32_nowait(row + n, x);
-        tc5::wait_ld();
+// The sums over the columns below n1 of a warp's 32 rows in TMEM of 2^(s scale + nl), nl of this
+// thread's columns in registers.  Thread t reads columns 2 (t % 4), + 1 (mod 8) of rows t / 4 + 8 k; the
+// four lanes of a row then add up, and thread t ends with row t / 4 + 8 (t % 4).  kMasked: only columns
+// that see the row's token, tok + the row.
+template <bool kMasked, int kCols>
+__device__ __forceinline__ float row_sums(uint32_t rows, int n1, float scale, const uint64_t (&nl)[kCols / 8], const int *last,
+                                          int tok) {
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+    const uint64_t scale2 = pack2(scale, scale);
+    uint64_t sum2[4] = {0u, 0u, 0u, 0u};  // two columns' sums side by side
+    uint32_t x[2][16];                    // (one is on its way while the other is added up)
+    auto add = [&](auto whole, int half, int blk) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) add4(x + i, n + i);
-    }
-    for (; n < n1; n += 16) {
-        uint32_t x[16];
-        tc5::ld_32x32b_x16_nowait(row + n, x);
-        tc5::wait_ld();
+        for (int r = 0; r < 4; ++r) {
+            const int n = 32 * blk + 8 * r + 2 * t;
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            if (n + i + 4 <= n1) {
-                add4(x + i, n + i);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 3; ++j)
-                    if (n + i + j < n1 && (!kMasked || tok <= last[n + i + j]))
-                        sum[j] += fast_exp2(fmaf(__uint_as_float(x[i + j]), scale, nl[n + i + j]));
+            for (int k = 0; k < 2; ++k) {
+                float e0, e1;
+                unpack2(fma2(pack2(__uint_as_float(x[half][4 * r + 2 * k]), __uint_as_float(x[half][4 * r + 2 * k + 1])), scale2,
+                             nl[4 * blk + r]), e0, e1);
+                e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+                if constexpr (!whole.value) {
+                    const int seer = tok + g + 16 * half + 8 * k;
+                    e0 = n < n1 && (!kMasked || seer <= last[n]) ? e0 : 0.f;
+                    e1 = n + 1 < n1 && (!kMasked || seer <= last[n + 1]) ? e1 : 0.f;
+                }
+                sum2[2 * half + k] = add2(sum2[2 * half + k], pack2(e0, e1));
             }
         }
+    };
+    auto add_block = [&](auto whole, int blk) {
+        tc5::wait_ld_of(x[0]);
+        tc5::ld_16x256b_x4_nowait(rows + (16u << 16) + 32 * blk, x[1]);
+        add(whole, 0, blk);
+        tc5::wait_ld_of(x[1]);
+        if (32 * blk + 32 < n1) tc5::ld_16x256b_x4_nowait(rows + 32 * blk + 32, x[0]);
+        add(whole, 1, blk);
+    };
+    if (n1 > 0) tc5::ld_16x256b_x4_nowait(rows, x[0]);
+#pragma unroll
+    for (int blk = 0; blk < kCols / 32; ++blk) {
+        if (32 * blk >= n1) break;
+        if (!kMasked && 32 * blk + 32 <= n1) add_block(std::true_type{}, blk);
+        else add_block(std::false_type{}, blk);
     }
-    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    float sum[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float e0, e1;
+        unpack2(sum2[k], e0, e1);
+        sum[k] = e0 + e1;
+    }
+    const float v0 = (t & 1 ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, t & 1 ? sum[0] : sum[1], 1);
+    const float v1 = (t & 1 ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, t & 1 ? sum[2] : sum[3], 1);
+    return (t & 2 ? v1 : v0) + __shfl_xor_sync(0xffffffffu, t & 2 ? v0 : v1, 2);
 }
 
 template <bool F8, int D>
@@ -304,18 +320,20 @@ __global__ void __launch_bounds__(XWarps<F8>::kThreads, 1)
 weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, int tiles_max, int n_most, uint32_t tmem_cols) {
     using X = XShape<F8, D>;
     constexpr int kXStages = X::kStages, kXThreads = XWarps<F8>::kThreads;
-    constexpr int kXLoadWarp = XWarps<F8>::kLoad, kXMmaWarp = XWarps<F8>::kMma;
+    constexpr int kXLoadWarp = XWarps<F8>::kLoad, kXMmaWarp = XWarps<F8>::kMma, kXFinalWarp = XWarps<F8>::kFinal;
+    constexpr int kGroups = XWarps<F8>::kGroups;
     extern __shared__ uint8_t x_smem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(x_smem) + 1023) & ~uintptr_t(1023));
     uint8_t *codes = smem + kXStages * X::kStageBytes, *qs = smem + X::q_at();
     float *sums = reinterpret_cast<float *>(smem + X::sums_at(n_most));      // [tiles][128], over the chunks of columns
     float *nl = sums + kXMostTiles * kXRows;                                  // -lse of every column, log2 units
     int *last_s = reinterpret_cast<int *>(nl + kXColumns);                    // last token that it sees
-    float *other = reinterpret_cast<float *>(last_s + kXColumns);             // [2][2][128]: a tile's second half's sums
-    uint64_t *bars = reinterpret_cast<uint64_t *>(other + 4 * kXRows);
-    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 4, *hdone = sfree + 4, *drain = hdone + 2;
+    float *other = reinterpret_cast<float *>(last_s + kXColumns);             // [4][groups][128]: a tile's sums by group
+    uint64_t *bars = reinterpret_cast<uint64_t *>(other + 4 * kGroups * kXRows);
+    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 2, *hdone = sfree + 2, *hfree = hdone + 4, *drain = hfree + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *places = reinterpret_cast<int *>(tmem_slot + 2);                     // of 16 tokens each, -1: none
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, b = blockIdx.z, bs = a.block_size;
     griddep_wait();
@@ -335,8 +353,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
     if (warp == kXMmaWarp) tc5::tmem_alloc(tmem_slot, tmem_cols);
     if (tid == 0) {
         for (int i = 0; i < kXStages; ++i) mbar_init(&kfull[i], F8 ? 32 * (kXMmaWarp - kXLoadWarp) : 1), mbar_init(&kempty[i], 1u);
-        for (int i = 0; i < 4; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], n_most > kXColumns / 2 ? 8u : 4u);
-        for (int i = 0; i < 2; ++i) mbar_init(&hdone[i], 4u);
+        for (int i = 0; i < 4; ++i) mbar_init(&hdone[i], 4u * kGroups), mbar_init(&hfree[i], 1u);
+        for (int i = 0; i < 2; ++i) mbar_init(&sdone[i], 1u), mbar_init(&sfree[i], 4u * kGroups);
         mbar_init(drain, 1u);
         *abort_flag = 0;
     }
@@ -352,11 +370,8 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
     for (int c0 = 0; c0 < n_cols; c0 += n_most, it += tiles) {
         const int here = min(n_most, n_cols - c0), N = (here + 15) / 16 * 16;
         const bool first = c0 == 0, final = c0 + here == n_cols;
-        // over 128 columns: tile u in buffer u & 1, a half of its columns for each of two groups; else in
-        // buffer u & 3, a group's own
-        const int halves = n_most > kXColumns / 2 ? 2 : 1, part = halves == 1 ? N : (N / 2 + 31) / 32 * 32;
-        const int buffers = 4 / halves;
-        const uint32_t width = tmem_cols / buffers;
+        const int part = ((N + kGroups - 1) / kGroups + 31) / 32 * 32;  // a group's columns
+        const uint32_t width = tmem_cols / 2;                           // tile u is in buffer u & 1
         // (the chunk before this one is read; TMEM and the barriers are set up)
         if (__syncthreads_or(!first && *abort_flag != 0)) break;
         tmem = *tmem_slot;
@@ -368,6 +383,15 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 w = make_uint4(to_f16x2(bf16lo(w.x), bf16hi(w.x)), to_f16x2(bf16lo(w.y), bf16hi(w.y)),
                                to_f16x2(bf16lo(w.z), bf16hi(w.z)), to_f16x2(bf16lo(w.w), bf16hi(w.w)));
             *reinterpret_cast<uint4 *>(qs + (ch >> 3) * (N * kSubBytes) + swz128(n, ch & 7)) = w;
+        }
+        // the places in the pool of all tiles' 16 tokens each, looked up at once
+        if (first) {
+            for (int x = tid; x < tiles * (kXRows / kTile); x += kXThreads) {
+                const int tok = tok0 + x * kTile, phys = tok < L ? table[tok / bs] : -1;
+                const bool fits = phys >= 0 && phys < a.num_blocks;
+                if (tok < L && !fits && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                places[x] = fits ? phys * bs + tok % bs : -1;
+            }
         }
         bool no_lse = false;
         for (int n = tid; n < N; n += kXThreads) {
@@ -389,18 +413,11 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 // outside the pool, keep what the stage had: their rows' scores are not used.)
                 const int sub = lane / X::kHalves, half = lane % X::kHalves;
                 const bool carrier = sub < kXRows / kTile;
-                auto block_of = [&](int i) {
-                    const int tok = tok0 + i * kXRows + sub * kTile;
-                    return carrier && i < tiles && tok < L ? table[tok / bs] : -1;
-                };
-                int next = block_of(0), after = block_of(1);  // two tiles ahead
                 const uint64_t policy = l2_evict_first_policy();
                 int issued = it;
                 for (int i = 0; i < tiles && good; ++i) {
-                    const int u = it + i, s = u % kXStages, phys = next, tok = tok0 + i * kXRows + sub * kTile;
-                    next = after, after = block_of(i + 2);
-                    const bool there = carrier && tok < L, valid = there && phys >= 0 && phys < a.num_blocks;
-                    if (there && !valid && h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
+                    const int u = it + i, s = u % kXStages, place = carrier ? places[i * (kXRows / kTile) + sub] : -1;
+                    const bool valid = place >= 0;
                     const uint32_t copies = __popc(__ballot_sync(0xffffffffu, valid));
                     if (u >= kXStages) good = __all_sync(0xffffffffu, wait(&kempty[s], (u / kXStages - 1) & 1));
                     if (!good) break;
@@ -408,7 +425,7 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                     __syncwarp();
                     if (valid)
                         tma_load_4d(smem + s * X::kStageBytes + half * (kXRows * kSubBytes) + sub * kTile * kSubBytes, &map, 0,
-                                    phys * bs + tok % bs, h, half, &kfull[s], policy);
+                                    place, h, half, &kfull[s], policy);
                     issued = u + 1;
                 }
                 // (the copies land before this CTA leaves, whatever became of the other warps)
@@ -422,21 +439,12 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 constexpr int kRowsAtOnce = 32 / kRowChunks;
                 const int lw = warp - kXLoadWarp;
                 uint8_t *own = codes + (lw * 32 + lane) * 16;
-                // (its rows of a tile lie in one block: lane i knows their place in the pool for tile i)
-                static_assert(kXLoadRows == kTile && kXMostTiles == 32, "a place per lane");
-                int places = -1;
-                const int row0 = tok0 + lane * kXRows + lw * kXLoadRows;
-                if (lane < tiles && row0 < L) {
-                    const int phys = table[row0 / bs];
-                    if (phys >= 0 && phys < a.num_blocks) places = phys * bs + row0 % bs;
-                    else if (h == 0) set_status(a.status, PA_STATUS_BAD_BLOCK);
-                }
+                static_assert(kXLoadRows == kTile, "a place for a warp's rows");
                 const uint8_t *keys = a.keys + static_cast<int64_t>(h) * D + 16 * (lane % kRowChunks);
                 const int stride = a.Hkv * D, my_row = lane / kRowChunks;
                 auto issue = [&](int i) {  // tile i (a commit group)
-                    const int place = __shfl_sync(0xffffffffu, places, i & 31);
                     if (i < tiles) {
-                        const int u = it + i;
+                        const int u = it + i, place = places[i * (kXRows / kTile) + lw];
                         const int left = place >= 0 ? L - (tok0 + i * kXRows + lw * kXLoadRows) : 0;  // rows that are there
                         const uint8_t *from = keys + static_cast<int64_t>(max(place, 0) + my_row) * stride;
 #pragma unroll
@@ -476,8 +484,10 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 const uint32_t q_half = static_cast<uint32_t>(N * kSubBytes) >> 4;
                 const uint32_t idesc = tc5::idesc_bf16_f32(kXRows, N, false, false, F8);
                 for (int i = 0; i < tiles && good; ++i) {
-                    const int u = it + i, s = u % kXStages, at = u % buffers, turn = u / buffers;
-                    good = wait(&kfull[s], (u / kXStages) & 1) && (turn == 0 || wait(&sfree[at], (turn - 1) & 1));
+                    const int u = it + i, s = u % kXStages, at = u & 1, turn = u >> 1;
+                    // (tile u's sums go where those of tile u - 4 were)
+                    good = wait(&kfull[s], (u / kXStages) & 1) && (turn == 0 || wait(&sfree[at], (turn - 1) & 1)) &&
+                           (u < 4 || wait(&hfree[u & 3], ((u >> 2) - 1) & 1));
                     if (!good) break;
                     if (F8) fence_proxy_async_smem();  // (the generic proxy has written the keys)
                     tc5::fence_after_sync();
@@ -495,53 +505,78 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                 }
             }
             __syncwarp();
-        } else {
-            const int group = warp >> 2, r = tid & 127;   // this thread's row
-            const int at = group / halves, e = group % halves, n0 = e * part, n1 = min(part, here - n0);
-            for (int i = 0; i < tiles && good; ++i) {
-                const int u = it + i, turn = u / buffers;
-                if (u % buffers != at) continue;
-                const bool writes = e == 0;               // (the second half's sums go to the first one's threads)
-                const int tok = tok0 + i * kXRows + r;
-                int phys = 0;
-                float was = 0.f;
-                if (writes && final && tok < L) {
-                    phys = table[tok / bs];
-                    if (tok < first_new) was = a.old[(static_cast<int64_t>(b) * a.Hkv + h) * a.room + tok];
+        } else if (warp == kXFinalWarp) {
+            // joins the groups' sums: four rows of a tile a lane, their old weights kXLook tiles ahead (one tile
+            // ahead, every tile waits for memory's latency: 1.1 us)
+            const int64_t base = (static_cast<int64_t>(b) * a.Hkv + h) * a.room;
+            const int shift = a.ends ? a.ends[b] - L : 0;  // a token's position less its place
+            float was[kXLook][4];
+            auto look = [&](int i, float(&w)[4]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int tok = tok0 + i * kXRows + 32 * j + lane;
+                    w[j] = final && i < tiles && tok < first_new ? a.old[base + tok] : 0.f;
                 }
+            };
+#pragma unroll
+            for (int i = 0; i < kXLook; ++i) look(i, was[i]);
+            for (int i0 = 0; i0 < tiles && good; i0 += kXLook) {
+#pragma unroll
+                for (int ahead = 0; ahead < kXLook; ++ahead) {
+                    const int i = i0 + ahead, u = it + i;
+                    if (i >= tiles) break;
+                    good = __all_sync(0xffffffffu, wait(&hdone[u & 3], (u >> 2) & 1));
+                    if (!good) break;
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float *part_s = other + (u & 3) * kGroups * kXRows + 32 * j + lane;
+                        v[j] = part_s[0];
+#pragma unroll
+                        for (int e = 1; e < kGroups; ++e) v[j] += part_s[e * kXRows];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&hfree[u & 3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = 32 * j + lane, tok = tok0 + i * kXRows + row;
+                        if (!first) v[j] += sums[i * kXRows + row];
+                        if (!final) {
+                            sums[i * kXRows + row] = v[j];
+                        } else if (tok < L) {
+                            if (places[(i * kXRows + row) / kTile] < 0) v[j] = 0.f;
+                            const bool fresh = tok >= first_new;
+                            a.out[base + tok] = fresh ? v[j] : fmaf(a.decay, was[ahead][j], v[j]);
+                            if (fresh && a.positions) a.positions[base + tok] = tok + shift;
+                        }
+                    }
+                    look(i + kXLook, was[ahead]);
+                }
+            }
+        } else {
+            const int group = warp >> 2, r = 32 * (warp & 3) + (lane >> 2) + 8 * (lane & 3);  // the row that it ends with
+            const int n0 = group * part, n1 = min(part, here - n0);
+            uint64_t nl_r[XWarps<F8>::kPart / 8];  // -lse of this thread's columns, two by two
+#pragma unroll
+            for (int i = 0; i < XWarps<F8>::kPart / 8; ++i) {
+                const int n = 8 * i + 2 * (lane & 3);
+                nl_r[i] = pack2(n < n1 ? nl[n0 + n] : 0.f, n + 1 < n1 ? nl[n0 + n + 1] : 0.f);
+            }
+            for (int i = 0; i < tiles && good; ++i) {
+                const int u = it + i, at = u & 1;
                 // (a tile with new tokens has queries that do not see all of it)
                 const bool all = !odd && tok0 + (i + 1) * kXRows <= first_new;
-                good = __all_sync(0xffffffffu, wait(&sdone[at], turn & 1));
+                good = __all_sync(0xffffffffu, wait(&sdone[at], (u >> 1) & 1));
                 if (!good) break;
                 tc5::fence_after_sync();
-                const uint32_t row = tc5::taddr(tmem, 32 * (warp & 3), at * width + n0);
-                float v = all ? row_sum<false>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok)
-                              : row_sum<true>(row, n1, a.scale_log2, nl + n0, last_s + n0, tok);
-                float *half = other + (2 * (u & 1) + (turn & 1)) * kXRows + r;
-                if (!writes) *half = v;
+                const uint32_t rows = tc5::taddr(tmem, 32 * (warp & 3), at * width + n0);
+                const int tok = tok0 + i * kXRows + 32 * (warp & 3);
+                other[((u & 3) * kGroups + group) * kXRows + r] =
+                    all ? row_sums<false, XWarps<F8>::kPart>(rows, n1, a.scale_log2, nl_r, last_s + n0, tok)
+                        : row_sums<true, XWarps<F8>::kPart>(rows, n1, a.scale_log2, nl_r, last_s + n0, tok);
                 tc5::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sfree[at]);
-                    if (!writes) mbar_arrive(&hdone[u & 1]);
-                }
-                if (!writes) continue;
-                if (halves == 2) {
-                    // (written again two turns on, which the MMA begins only after this group's next turn)
-                    good = __all_sync(0xffffffffu, wait(&hdone[u & 1], turn & 1));
-                    if (!good) break;
-                    v += *half;
-                }
-                if (!first) v += sums[i * kXRows + r];
-                if (!final) {
-                    sums[i * kXRows + r] = v;
-                } else if (tok < L) {
-                    const int64_t x = (static_cast<int64_t>(b) * a.Hkv + h) * a.room + tok;
-                    if (phys < 0 || phys >= a.num_blocks) v = 0.f;
-                    const bool fresh = tok >= first_new;
-                    a.out[x] = fresh ? v : fmaf(a.decay, was, v);
-                    if (fresh && a.positions) a.positions[x] = tok + (a.ends ? a.ends[b] - L : 0);
-                }
+                if (lane == 0) mbar_arrive(&sfree[at]), mbar_arrive(&hdone[u & 3]);
             }
         }
     }
@@ -566,8 +601,8 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
     // 256 columns at a time, or shares of them that differ by little
     const int64_t chunks = (columns + kXColumns - 1) / kXColumns;
     const int n_most = static_cast<int>(((columns + chunks - 1) / chunks + 15) / 16 * 16);
-    uint32_t cols = 128;  // of TMEM: four buffers, or two of over 128 columns, read 32 columns at a time
-    while (cols < (n_most > kXColumns / 2 ? 2u : 4u) * ((n_most + 31) / 32 * 32)) cols *= 2;
+    uint32_t cols = 64;  // of TMEM: two buffers, read 32 columns at a time
+    while (cols < 2u * ((n_most + 31) / 32 * 32)) cols *= 2;
     // the tiles of a CTA: the fewest rounds of tiles over all SMs, a CTA's start counted as two
     const int64_t tiles = (most + kXRows - 1) / kXRows, rows = static_cast<int64_t>(a.Hkv) * B, sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
