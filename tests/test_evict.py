@@ -201,6 +201,19 @@ def test_evict_twice_is_once_and_on_another_stream():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("budget,first,recent", [(100000, 4, 30000), (50, 0, 1)])
+def test_evict_from_the_most_tokens(budget, first, recent):
+    Cache([196608], 256, 1, 64, 1, fp8=True, seed=8).check(budget, first, recent)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread", [0.0, 1e-6, 40.0])
+def test_evict_weights_that_are_alike_or_far_apart(spread):
+    """One value for all, a few neighbouring ones, and some that under- and overflow: the border among many keys."""
+    Cache([5000, 1200, 300], 16, 2, 64, 1, seed=9, spread=spread).check(200, 2, 20)
+
+
+@pytest.mark.gpu
 def test_evict_many_rows():
     rng = random.Random(6)
     Cache([rng.randint(0, 300) for _ in range(70)], 16, 4, 64, 2, fp8=True, seed=6).check(100, 2, 20)

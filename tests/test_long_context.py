@@ -3,7 +3,9 @@ their last queries gave to their tokens, then steps add a token each, attend the
 the weights and cut again.  A plain model on the CPU, in 64 bits, keeps every token's row by its place; tolerances are
 those of the operators' own tests."""
 import math
+import os
 import random
+import re
 
 import pytest
 import torch
@@ -277,6 +279,37 @@ def test_a_step_of_selected_attention_in_a_graph():
         for name in ("lens", "sel", "n", "out", "lse", "w", "pos", "bounds", "kc"):
             assert torch.equal(eager[name], graphed[name]), (i, name)
     assert eager["lens"].tolist() == [n + steps for n in start]
+
+
+@pytest.mark.gpu
+def test_the_readmes_step_runs():
+    """The README's calls as they stand there: a sequence above the budget is cut, what is attended is what the lists say."""
+    with open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "README.md")) as f:
+        code = [x for x in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "pa_cache_evict" in x]
+    assert len(code) == 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device="cuda")   # noqa: E731
+    Bn, mb, nb, lens = 2, 80, 170, [1100, 900]
+    tables = torch.randperm(nb, generator=torch.Generator().manual_seed(2))[:Bn * mb].int().view(Bn, mb).cuda()
+    for b, n in enumerate(lens):
+        tables[b, -(-n // BS):] = -1
+    refs = torch.bincount(tables[tables >= 0].long(), minlength=nb).int()
+    slots = torch.tensor([int(tables[b, (n - 1) // BS]) * BS + (n - 1) % BS for b, n in enumerate(lens)], device="cuda")
+    ns = dict(torch=torch, pa=pa, num_blocks=nb, Hkv=HKV, D=D, bs=BS, scale=SCALE, layer=0, k_cache=rnd(nb, BS, HKV, D),
+              v_cache=rnd(nb, BS, HKV, D), block_tables=tables, seq_lens=i32(lens), ends=i32(lens), refs=refs, k_new=rnd(Bn, HKV, D),
+              v_new=rnd(Bn, HKV, D), slot_mapping=slots, q=rnd(Bn, HQ, D), sel=z(Bn, HKV, 64), sel_lens=z(Bn, HKV),
+              out=rnd(Bn, HQ, D), lse=z(Bn, HQ, t=torch.float32), ws=z(1 << 22, t=torch.uint8),
+              weights=torch.rand(1, Bn, HKV, mb * BS, generator=g, device="cuda"),
+              positions=torch.arange(mb * BS, device="cuda").int().expand(1, Bn, HKV, mb * BS).contiguous(),
+              new_tables=torch.empty_like(tables), new_lens=z(Bn), new_refs=z(nb), new_weights=z(1, Bn, HKV, mb * BS, t=torch.float32),
+              new_positions=z(1, Bn, HKV, mb * BS))
+    ns["pools"] = pa.PoolSet([ns["k_cache"], ns["v_cache"]])
+    exec(compile(code[0], "README.md", "exec"), ns)
+    assert ns["new_lens"].tolist() == [1024, 900]
+    assert (ns["new_tables"] >= 0).sum(1).tolist() == [65, 57] and int(ns["new_refs"].sum()) == 65 + 57
+    assert ((ns["sel"] >= 0).sum(-1) == torch.tensor([[64], [57]], device="cuda")).all()
+    assert torch.isfinite(ns["lse"]).all() and ns["new_positions"][0, 0, :, :1024].unique(dim=-1).shape[-1] == 1024
 
 
 @pytest.mark.gpu

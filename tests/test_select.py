@@ -213,6 +213,13 @@ def test_select_in_many_rows(Bn, hkv, fp8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [40960 * 16, 40960 * 16 - 33, 16 * 16 + 1])
+def test_select_of_the_most_blocks(n):
+    tables, _, nb = layout([40960 * 16], 16, seed=5)
+    check(queries(1, 32, 64, 5), make_bounds(nb, 1, 64, True, 6), tables, [n], 16, 500, 2, 3)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(6))
 def test_select_scores_that_fp32_does_not_tell_apart(seed):
     """Hundreds of blocks that differ in one small channel by one step: sums in 64 bits tell them apart, sums in fp32

@@ -100,6 +100,13 @@ def test_weights_of_a_long_ragged_batch(q_len):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weights_of_a_whole_prompt(fp8):
+    """More queries than tokens in one sequence, chunks of columns that go over many tiles."""
+    case(2, 1, 64, 16, [1300, 700], q_len=1000, fp8=fp8, seed=4, ends=[1400, 700])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sharp", [0.0, 12.0])
 def test_weights_of_flat_and_sharp_queries(sharp):
     case(8, 2, 128, 16, [1, 200, 333], 4, sharp=sharp, seed=5)
