@@ -245,8 +245,9 @@ int make_kv_map_heads(CUtensorMap *map, const void *base, const pa_cache_desc &c
 
 // An FP8 pool (one-byte e4m3 codes) for the tensor-core kernel: a 3-D view
 // (128 codes = one token row of one head, token rows, heads); one box is 16
-// token rows of HC heads, head-major, 128-byte swizzled.
-int make_kv_map_fp8(CUtensorMap *map, const void *base, const pa_cache_desc &c, int HC) {
+// token rows of HC heads, head-major, 128-byte swizzled.  `alone`: the heads next to the
+// box's are not read (a list of blocks for every head), so L2 fetches no more than its rows.
+int make_kv_map_fp8(CUtensorMap *map, const void *base, const pa_cache_desc &c, int HC, bool alone = false) {
     auto enc = encode_fn();
     if (!enc) return PA_ECUDA;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim),
@@ -258,7 +259,8 @@ int make_kv_map_fp8(CUtensorMap *map, const void *base, const pa_cache_desc &c, 
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                     alone && c.num_kv_heads > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PA_OK : PA_ECUDA;
 }
 
@@ -486,8 +488,8 @@ int run_decode(bool split, void *out, float *lse, float *part_o, float *part_lse
             p.scale_log2 = scale * f8->k_scale * 1.4426950408889634f;
             p.v_scale = f8->v_scale;
             p.k_scale = f8->k_scale;
-            rc = make_kv_map_fp8(&kmap, k_cache, c, box_heads);
-            if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, c, box_heads);
+            rc = make_kv_map_fp8(&kmap, k_cache, c, box_heads, po.lists);
+            if (!rc) rc = make_kv_map_fp8(&vmap, v_cache, c, box_heads, po.lists);
             if (rc) return rc;
             e = po.lists ? pa::launch_decode_tc_f8_sel(HC, GP, G, kmap, vmap, p, B, stream)
                 : rules ? pa::launch_decode_tc_f8_scored(HC, GP, G, kmap, vmap, p, B, stream)
