@@ -80,9 +80,9 @@ __device__ __forceinline__ void add_columns(float (&sum)[2], const float (&acc)[
 // registers of keys (8 KB a warp) on their way: a tile's registers are loaded again as soon
 // as its products are done.  With up to 8 columns (kOne) the queries stay in registers.
 // The four lanes that share a token add up two tiles at once and end with a token each, so
-// that old and new weights are whole lines.  A 7B-shaped step (34 MB of keys) takes 9.2 us, half of
+// that old and new weights are whole lines.  A 7B-shaped step (34 MB of keys) takes 7.7 us, 4 of
 // them the launch and the first loads' chain; 32 ragged FP8 sequences of up to 16384 tokens (294
-// MB) 57 to 63 us, 0.7 to 0.77 of a copy's rate.
+// MB) 57 to 66 us, 0.66 to 0.77 of a copy's rate.
 template <bool F8, int D, bool kOne>
 __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs a, int pairs) {
     constexpr int kRowBytes = D * (F8 ? 1 : 2);
@@ -589,10 +589,21 @@ template <bool F8, int D>
 cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream_t stream) {
     const int64_t columns = static_cast<int64_t>(a.q_len) * a.G;
     if (columns <= kWFew) {
-        // long runs of tokens, but CTAs for four waves and more
-        const int64_t all = (most + 2 * kTile - 1) / (2 * kTile) * a.Hkv * B, sms = sm_count();
+        // The pairs of a warp that take the least time by a model in microseconds: a CTA's start 4, each
+        // pair at an SM's share of the memory (two CTAs an SM, 22 bytes a nanosecond each); rows three
+        // quarters full, and, in waves, one more for the ends.  (8 x 4 rows of 4096 bf16 tokens: 1 pair 10.2
+        // us, 2 8.3, 4 9.5; of 16384 1 29, 4 25, 8 24; 32 x 8 ragged FP8 rows 1 112, 4 68, 8 61; 16 pairs
+        // were worse or the same.)
+        const int64_t sms = sm_count();
+        if (sms <= 0) return cudaErrorInvalidDevice;
         int pairs = 1;
-        while (pairs < 16 && all >= 2 * pairs * kWWarps * 8 * sms) pairs *= 2;
+        double least = 0.0;
+        for (int n = 1; n <= 8; n *= 2) {
+            const int64_t span = static_cast<int64_t>(n) * kWWarps * 2 * kTile;
+            const double full = static_cast<double>((most + span - 1) / span) * a.Hkv * B / (2.0 * sms);
+            const double cost = (full > 1.0 ? 0.75 * full + 1.0 : 1.0) * (4.0 + static_cast<double>(span) * D * (F8 ? 1 : 2) / 22e3);
+            if (n == 1 || cost < least) least = cost, pairs = n;
+        }
         const int64_t span = static_cast<int64_t>(pairs) * kWWarps * 2 * kTile;
         return launch_maybe_cooperative(columns <= 8 ? weights_kernel<F8, D, true> : weights_kernel<F8, D, false>,
                                         dim3(static_cast<unsigned>((most + span - 1) / span), a.Hkv, B), kWThreads, 0, stream,
