@@ -363,3 +363,48 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for s, want in zip(sides, alone):
             assert all(torch.equal(a, b) for a, b in zip(s.results(), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_blocks_past_32_bits_of_a_large_pool(fp8):
+    """The same blocks at the front of a small pool and behind 2^32 bytes of a large one: the same results."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)   # noqa: E731
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device="cuda")   # noqa: E731
+    Bn, hq, hkv, mb, nb = 2, 16, 8, 30, 64
+    far = (2 ** 32 // (BS * hkv * D * (1 if fp8 else 2))) + 5
+    code = (lambda x: x.to(torch.float8_e4m3fn).view(torch.uint8)) if fp8 else (lambda x: x)
+    k, v = code(rnd(nb, BS, hkv, D)), code(rnd(nb, BS, hkv, D))
+    tables = torch.randperm(nb, generator=torch.Generator().manual_seed(2))[:Bn * mb].int().view(Bn, mb).cuda()
+    lens, q, window = i32([mb * BS - 3, 333]), rnd(Bn, hq, D), rnd(Bn, 40, hq, D)
+    lse = torch.full((Bn, 40, hq), 7.0, device="cuda")
+    results = []
+    for base in (0, far):
+        pools = []
+        for x in (k, v):
+            pool = torch.empty(base + nb, BS, hkv, D, dtype=x.dtype, device="cuda")
+            pool[base:] = x
+            pools.append(pool)
+        t = tables + base
+        refs = z(base + nb)
+        refs[t.flatten().long()] = 1
+        bounds = z(base + nb, hkv, 2, D, t=k.dtype)
+        sel, n, out, ws = z(Bn, hkv, 9), z(Bn, hkv), torch.empty_like(q), z(1 << 22, t=torch.uint8)
+        w, pos = z(1, Bn, hkv, mb * BS, t=torch.float32), z(1, Bn, hkv, mb * BS)
+        pa.pa_key_bounds(bounds, pools[0], t, lens)
+        pa.pa_blocks_select(sel, n, q, bounds, BS, t, lens)
+        scales = (0.5, 0.5) if fp8 else ()
+        (pa.pa_decode_selected_fp8 if fp8 else pa.pa_decode_selected)(out, None, q, *pools, *scales, sel, n, SCALE, workspace=ws)
+        for queries, z_ in ((window, lse), (q, lse[:, 0].contiguous())):
+            if fp8:
+                pa.pa_weights_add_fp8(w[0], w[0], pos[0], queries, z_, pools[0], 0.5, t, lens, SCALE)
+            else:
+                pa.pa_weights_add(w[0], w[0], pos[0], queries, z_, pools[0], t, lens, SCALE)
+        pos.copy_(torch.arange(mb * BS, device="cuda").int().expand_as(pos))
+        new = [torch.zeros_like(x) for x in (t, lens, refs, w, pos)]
+        pa.pa_cache_evict(*new, t, lens, refs, w, pos, pa.PoolSet(pools), 200, 4, 16)
+        results.append([bounds[base:], sel - base * (sel >= 0), n, out, w, new[0] - base * (new[0] >= 0), new[1], new[2][base:]] +
+                       new[3:] + [p[base:] for p in pools])
+    for i, (a, b) in enumerate(zip(*results)):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), i
