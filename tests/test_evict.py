@@ -214,6 +214,41 @@ def test_evict_weights_that_are_alike_or_far_apart(spread):
 
 
 @pytest.mark.gpu
+def test_evict_with_plain_launches():
+    prev = pa.pa_get_option(pa.PA_OPT_PDL)
+    pa.pa_set_option(pa.PA_OPT_PDL, 0)
+    try:
+        Cache([300, 700, 20], 16, 2, 128, 2, seed=5, again=True).check(128, 4, 9, twice=True)
+    finally:
+        pa.pa_set_option(pa.PA_OPT_PDL, prev)
+
+
+@pytest.mark.gpu
+def test_evict_right_after_the_weights():
+    """Weights and positions written by the kernel before, over and over: every call sees the last ones."""
+    c = Cache([900, 500], 16, 2, 64, 1, seed=11)
+    pools = [x.cuda().view(torch.bfloat16) for x in c.pools]
+    t, n, r = i32(c.tables), i32(c.lens), i32(c.refs)
+    w, p = torch.zeros_like(c.weights).cuda(), torch.zeros_like(c.positions).cuda()
+    q, lse = torch.zeros(2, 900, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 900, 2, device="cuda")
+    new = [torch.zeros_like(x) for x in (t, n, r, w, p)]
+    got = []
+    for i in range(40):
+        lse.fill_(float(-i))   # (every query gives each token that it sees e^i)
+        pa.pa_weights_add(w[0], w[0], p[0], q, lse, pools[0], t, n, 0.1)
+        pa.pa_cache_evict(*new, t, n, r, w, p, pa.PoolSet([x.clone() for x in pools]), 100, 1, 3)
+        got.append([x.clone() for x in (w, new[3], new[4])])
+    torch.cuda.synchronize()
+    for i, (before, weights, positions) in enumerate(got):
+        for b, L in enumerate(c.lens):
+            m = min(L, 100)
+            # the earliest tokens are seen by the most queries: they, and the newest, stay in their order
+            src = list(range(m - 3)) + list(range(L - 3, L))
+            assert torch.equal(weights[0, b, :, :m], before[0, b][:, src]), i
+            assert (positions[0, b, :, :m].cpu() == torch.tensor(src)).all(), i
+
+
+@pytest.mark.gpu
 def test_evict_many_rows():
     rng = random.Random(6)
     Cache([rng.randint(0, 300) for _ in range(70)], 16, 4, 64, 2, fp8=True, seed=6).check(100, 2, 20)
