@@ -5,8 +5,8 @@
 // The tokens that stay and stand below n are left where they are; the places below n that
 // came free take the ones that stand behind, the k-th place the k-th token.  So a row
 // is read only behind n and written only below it: nothing that moves meets anything
-// else, in any order, and a call that is repeated does the same again.  What moves is
-// at least what any packing moves.
+// else, in any order, and a call that is repeated does the same again.  No packing moves
+// fewer rows.
 //
 // Two launches.  evict_lens_kernel works out every sequence's n, and writes the new
 // lengths, tables and counts.  evict_kernel has a thread-block cluster per (layer,
@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kLensThreads) evict_lens_kernel(const __grid_c
     // the block that a fork gave for the next token is the row's own, too
     const int next = L % bs == 0 && L < most ? used_entry(a, row, L / bs) : -1;
     const int stay = n < L ? static_cast<int>(n) / bs + 1 : n_used + (next >= 0);
-    for (int j = tid; j < a.max_blocks; j += kLensThreads) out[j] = j < min(stay, n_used) ? used_entry(a, row, j) : j < stay ? next : -1;
+    for (int j = tid; j < a.max_blocks; j += kLensThreads)
+        out[j] = j < min(stay, n_used) ? used_entry(a, row, j) : j < stay ? next : -1;
 }
 
 // Words of shared memory for keys, and for the rows on their way.

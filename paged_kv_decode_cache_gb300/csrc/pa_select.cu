@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_many_kernel(const B
         const int k = i / a.row_chunks, c = i % a.row_chunks, phys = ids[k];
         if (phys < 0) continue;
         Range<F8> r;
-        range_of_rows<4>(r, reinterpret_cast<const uint4 *>(a.keys) + static_cast<int64_t>(phys) * bs * a.row_chunks + c, a.row_chunks,
-                         0, 1, min(bs, L - (j0 + k) * bs));
+        const uint4 *keys = reinterpret_cast<const uint4 *>(a.keys) + static_cast<int64_t>(phys) * bs * a.row_chunks;
+        range_of_rows<4>(r, keys + c, a.row_chunks, 0, 1, min(bs, L - (j0 + k) * bs));
         uint4 *out = reinterpret_cast<uint4 *>(a.bounds) + static_cast<int64_t>(phys) * a.row_chunks * 2;
         out += 2 * (c / a.head_chunks) * a.head_chunks + c % a.head_chunks;
         out[0] = Range<F8>::pack(r.lo), out[a.head_chunks] = Range<F8>::pack(r.hi);

@@ -1,6 +1,7 @@
 // Selection of the m largest of many keys by the CTAs of a thread-block cluster, for
 // pa_blocks_select and pa_cache_evict: a row's keys are spread over the cluster's
-// shared memory, a contiguous range per CTA, and stay there.
+// shared memory, a contiguous range per CTA, and stay there (pa_blocks_select's are all in
+// one CTA's, and C = 1).
 //
 // cluster_narrow finds the m-th largest key by narrowing a range of key values: each
 // pass counts the keys of the range in 2048 equal bins (shared-memory atomics in every
@@ -201,7 +202,10 @@ __device__ Border cluster_threshold(F key, int n, Window seen, uint32_t m, uint3
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t lo = __reduce_min_sync(0xffffffffu, seen.lo), hi = __reduce_max_sync(0xffffffffu, seen.hi);
     uint32_t n_above = __reduce_add_sync(0xffffffffu, seen.above), n_in = __reduce_add_sync(0xffffffffu, seen.in);
-    if (lane == 0) sh.warp_count[warp][0] = lo, sh.warp_count[warp][1] = hi, sh.warp_count[warp][2] = n_above, sh.warp_count[warp][3] = n_in;
+    if (lane == 0) {
+        sh.warp_count[warp][0] = lo, sh.warp_count[warp][1] = hi;
+        sh.warp_count[warp][2] = n_above, sh.warp_count[warp][3] = n_in;
+    }
     for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[0][i] = 0;
     if (tid == 0) sh.n_few = 0;
     __syncthreads();

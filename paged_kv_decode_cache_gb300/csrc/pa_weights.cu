@@ -330,7 +330,10 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
     int *last_s = reinterpret_cast<int *>(nl + kXColumns);                    // last token that it sees
     float *other = reinterpret_cast<float *>(last_s + kXColumns);             // [4][groups][128]: a tile's sums by group
     uint64_t *bars = reinterpret_cast<uint64_t *>(other + 4 * kGroups * kXRows);
-    uint64_t *kfull = bars, *kempty = bars + kXStages, *sdone = bars + 2 * kXStages, *sfree = sdone + 2, *hdone = sfree + 2, *hfree = hdone + 4, *drain = hfree + 4;
+    uint64_t *kfull = bars, *kempty = bars + kXStages;              // a stage holds keys, has been read
+    uint64_t *sdone = bars + 2 * kXStages, *sfree = sdone + 2;      // a buffer holds scores, has been read
+    uint64_t *hdone = sfree + 2, *hfree = hdone + 4;                // a slot holds the groups' sums, has been read
+    uint64_t *drain = hfree + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *places = reinterpret_cast<int *>(tmem_slot + 2);                     // of 16 tokens each, -1: none
@@ -466,11 +469,13 @@ weights_tc_kernel(const __grid_constant__ CUtensorMap map, const WeightsArgs a, 
                     for (int j = 0; j < kPer; ++j) {
                         const int r = lw * kXLoadRows + j * kRowsAtOnce + lane / kRowChunks, c = lane % kRowChunks;
                         uint4 w[Chunk<F8>::kVecs];
-                        widen<F8>(*reinterpret_cast<const uint4 *>(own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512), w);
+                        const uint8_t *at = own + ((u % kXCodes) * kPer + j) * (kXMmaWarp - kXLoadWarp) * 512;
+                        widen<F8>(*reinterpret_cast<const uint4 *>(at), w);
 #pragma unroll
                         for (int v = 0; v < Chunk<F8>::kVecs; ++v) {
                             const int ch = c * Chunk<F8>::kVecs + v;
-                            *reinterpret_cast<uint4 *>(smem + s * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7)) = w[v];
+                            uint8_t *to = smem + s * X::kStageBytes + (ch >> 3) * (kXRows * kSubBytes) + swz128(r, ch & 7);
+                            *reinterpret_cast<uint4 *>(to) = w[v];
                         }
                     }
                     mbar_arrive(&kfull[s]);
