@@ -896,7 +896,7 @@ int pa_weights_add_fp8(float *new_weights, const float *weights, int32_t *positi
  * F being its tokens up to the last block that has more than one reference: those
  * cannot be thrown out for one holder alone, and stay where they are.  Which others
  * stay is every layer's and KV head's own choice: tokens at positions below `first`,
- * the `recent` newest (positions above that of token L - 1, less recent), and then
+ * the newest (positions above the largest of the L tokens', less `recent`), and then
  * the heaviest by weights, ties to the lower place; a NaN weighs like +inf.
  * The tokens that stay and stand below n are not moved; the free places below n take
  * the ones behind, the k-th place the k-th token, in both pools, new_weights and

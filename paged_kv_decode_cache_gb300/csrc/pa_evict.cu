@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     uint32_t *keys = reinterpret_cast<uint32_t *>(evict_smem + kTopkSharedBytes);
     int32_t *holes = reinterpret_cast<int32_t *>(keys + evict_keys(a.slice));   // this CTA's pairs: [moves] free places
     int32_t *movers = holes + a.moves;                              // ... and the tokens that take them
-    __shared__ int past_s;
+    __shared__ int past_s, newest_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bs = a.block_size;
     const int C = a.ctas, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int64_t row = blockIdx.x / C;   // (layer, sequence, head)
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         }
     }
     // tokens of blocks that others hold too, and those before them, stay in their places
-    if (tid == 0) past_s = 0;
+    if (tid == 0) past_s = 0, newest_s = INT32_MIN;
     __syncthreads();
     int past = 0;
     for (int j = tid; j < n_used; j += kEvictThreads)
@@ -181,32 +181,46 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     if (past) atomicMax(&past_s, past);
     const int per = ((L + C - 1) / C + 31) / 32 * 32;
     const int t0 = min(rank * per, L), mine = min(t0 + per, L) - t0;
-    const int64_t newest = positions[L - 1];
     __syncthreads();
     const int fixed = past_s * bs;
     // Keys; and every place below n gets what it has now (a place that comes free gets another's, later).
+    // The newest token stands in the last place, unless the row was cut and had no token since, which
+    // the largest position tells: then the keys are made again (a pass for that position first would
+    // read every row's positions twice).
     Window seen;
     constexpr int kBatch = 4;  // loads on their way together (the stores would hold the next ones up)
-    for (int i0 = tid; i0 < mine; i0 += kBatch * kEvictThreads) {
-        float w[kBatch];
-        int p[kBatch];
+    for (int newest = positions[L - 1];;) {
+        seen = Window();
+        int largest = INT32_MIN;
+        for (int i0 = tid; i0 < mine; i0 += kBatch * kEvictThreads) {
+            float w[kBatch];
+            int p[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kEvictThreads;
-            w[j] = i < mine ? weights[t0 + i] : 0.f, p[j] = i < mine ? positions[t0 + i] : 0;
-        }
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * kEvictThreads;
+                w[j] = i < mine ? weights[t0 + i] : 0.f, p[j] = i < mine ? positions[t0 + i] : INT32_MIN;
+            }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kEvictThreads, t = t0 + i;
-            if (i >= mine) break;
-            const bool safe = t < fixed || p[j] < a.first || p[j] > newest - a.recent;
-            const uint32_t k = safe ? kSafe : float_key(w[j] == w[j] ? w[j] : INFINITY);
-            keys[i] = k;
-            seen.see(k, 0u, kSafe - 1u);
-            if (t < n) new_weights[t] = w[j], new_positions[t] = p[j];
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * kEvictThreads, t = t0 + i;
+                if (i >= mine) break;
+                largest = max(largest, p[j]);
+                const bool safe = t < fixed || p[j] < a.first || p[j] > static_cast<int64_t>(newest) - a.recent;
+                const uint32_t k = safe ? kSafe : float_key(w[j] == w[j] ? w[j] : INFINITY);
+                keys[i] = k;
+                seen.see(k, 0u, kSafe - 1u);
+                if (t < n) new_weights[t] = w[j], new_positions[t] = p[j];
+            }
         }
+        __syncwarp();
+        largest = __reduce_max_sync(0xffffffffu, largest);
+        if (lane == 0) atomicMax(&newest_s, largest);
+        meet(C);
+        if (C > 1 && lane < C) largest = static_cast<int>(ld_shared_cluster_u32(map_shared_rank(smem_u32(&newest_s), lane)));
+        largest = C > 1 ? __reduce_max_sync(0xffffffffu, largest) : newest_s;
+        if (largest == newest) break;
+        newest = largest;
     }
-    __syncthreads();
 
     auto key_at = [&](int i) { return keys[i]; };
     Border edge = cluster_threshold<kEvictThreads>(key_at, mine, seen, n, 0u, kSafe - 1u, C, sh, kTopkFew);
