@@ -1,5 +1,5 @@
 """Sequences that are cut again before a token was appended (pa_cache_evict): a cut leaves a row in no order, so its newest
-tokens are found by their positions, not by their places."""
+tokens are found by their positions, not by their places.  And what a call reads stays bit for bit as it was."""
 import math
 import random
 
@@ -8,6 +8,8 @@ import torch
 
 import test_evict
 from paged_kv_decode_cache_gb300 import build as B
+from paged_kv_decode_cache_gb300 import pa
+from paged_model import i32
 from test_evict import Cache
 
 
@@ -111,3 +113,17 @@ def test_a_prefix_let_go_between_two_cuts(monkeypatch):
     c.weights, c.positions = c.weights[:, :1].contiguous(), c.positions[:, :1].contiguous()
     c.check(40, 2, 16)
     newest_stay(c, next_of(c, c.run(40, 2, 16)), 16)
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("again", [False, True])
+def test_what_a_call_reads_stays_as_it_was(again):
+    c = Cache([300, 64, 200, 7], 16, 2, 64, 2, seed=2, shared=2, again=again)
+    c.weights[..., ::9], c.weights[..., 4::31] = math.nan, -0.0
+    t, n, r, w, p = i32(c.tables), i32(c.lens), i32(c.refs), c.weights.cuda(), c.positions.cuda()
+    pools = [x.cuda().view(torch.bfloat16) for x in c.pools]
+    old = [x.clone() for x in (t, n, r, w, p)]
+    new = [torch.zeros_like(x) for x in old]
+    pa.pa_cache_evict(*new, t, n, r, w, p, pa.PoolSet(pools), 50, first=2, recent=9)
+    for x, y in zip((t, n, r, w, p), old):
+        assert torch.equal(x.view(torch.int32), y.view(torch.int32))
+    assert new[1].tolist() == [50, 50, 50, 7] and int(new[2].sum()) < int(r.sum())
