@@ -867,8 +867,14 @@ int pa_selected_num_splits(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_
  * NULL, positions[b,h,t] = ends[b] - seq_lens[b] + t, where ends[b] counts every token
  * that the sequence has had, evicted ones too (NULL: seq_lens).  (So before a prompt's
  * last q_len queries the older tokens' weights are 0, their positions t.)  lse is what
- * attention gave for these queries (one of -inf adds nothing), so a query's weights sum
- * to one over the tokens it saw.  Places from seq_lens[b] on are left as they were.
+ * plain attention of these queries over all seq_lens[b] tokens gave, with the same scale:
+ * pa_decode's, pa_decode_splitkv's, pa_decode_step's, pa_decode_cascade's or
+ * pa_decode_mq's (FP8: pa_decode_splitkv_fp8's or pa_decode_step_fp8's), or
+ * pa_decode_scored's and pa_decode_scored_fp8's without rules; one of -inf adds nothing.  Then a
+ * query's weights sum to one over the tokens it saw.  The lse of pa_decode_scored under a
+ * rule belongs to other scores and that of pa_decode_selected to fewer tokens: the call
+ * cannot tell, and what it adds with them is no attention weight (a token outside the lists
+ * may draw more than one).  Places from seq_lens[b] on are left as they were.
  * weights, new_weights: device fp32 [B, Hkv, room], the same buffer or two; positions:
  * device int32 [B, Hkv, room]; q: device bf16 [B, q_len, Hq, D]; lse: device fp32 [B,
  * q_len, Hq].  decay >= 0.  Sums are in fp32, in a fixed order.  1 <= q_len <= 65535,

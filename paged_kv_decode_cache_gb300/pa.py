@@ -805,7 +805,10 @@ def pa_weights_add(new_weights, weights, positions, q, lse, k_cache, block_table
     """new_weights = decay * weights + the attention weight that every cached token draws from q ([B, Hq, D], or
     [B, q_len, Hq, D]) with the lse that attention gave: [B, Hkv, tokens] fp32 (new_weights may be weights); the
     q_len newest tokens start from nothing, and get their positions (int32 [B, Hkv, tokens], or None) from ends
-    (int32 [B], tokens so far, default seq_lens)."""
+    (int32 [B], tokens so far, default seq_lens).  lse is that of plain attention over all tokens: of pa_decode,
+    pa_decode_splitkv, pa_decode_step, pa_decode_cascade, pa_decode_mq, pa_decode_splitkv_fp8, pa_decode_step_fp8, or
+    pa_decode_scored and pa_decode_scored_fp8 without rules; not that of pa_decode_scored under a rule or of
+    pa_decode_selected."""
     (_native or _binding()).weights_add(False, new_weights, weights, positions, q, lse, k_cache, None, block_tables,
                                         seq_lens, scale, ends, decay, status, stream)
 
