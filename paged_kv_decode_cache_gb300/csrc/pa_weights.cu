@@ -3,8 +3,9 @@
 //   w[t] <- decay w[t] + sum over the queries i and the group's heads g that see t of
 //           exp(scale <q_ig, K_t> - lse_ig),
 // the softmax's own probabilities, rebuilt from the log-sum-exp that attention gave.  Every
-// key is read once; a token's sum belongs to one warp, so no atomics and the same bits
-// every time.
+// key is read once (by the tensor cores' kernel once per 256 columns).  A token's sum belongs to one
+// warp, or, there, to two or four with a share of the columns each, whose sums another warp adds up in
+// their order: no atomics, and the same bits every time.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
