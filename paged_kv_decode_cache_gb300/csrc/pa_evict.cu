@@ -12,8 +12,8 @@
 // lengths, tables and counts.  evict_kernel has a thread-block cluster per (layer,
 // sequence, head): it finds the n-th largest weight over its shared memory (pa_topk.cuh),
 // lists the free places and the tokens for them, and moves the rows.  Bound by the chain of the
-// search where few tokens are thrown out (the 8 x 4 rows of a step, 64 of 1088 tokens each: 9.7 us);
-// where many are (8 layers of 4 FP8 prompts of up to 16384 tokens: 67 us, half of the copy's rate for
+// search where few tokens are thrown out (the 8 x 4 rows of a step, 64 of 1088 tokens each: 9.9 us);
+// where many are (8 layers of 4 FP8 prompts of up to 16384 tokens: 68 us, half of the copy's rate for
 // what is read and written) by the search, 24 us for all rows side by side, and then by memory.
 #include <algorithm>
 
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     // Keys; and every place below n gets what it has now (a place that comes free gets another's, later).
     // The newest token stands in the last place, unless the row was cut and had no token since, which
     // the largest position tells: then the keys are made again (a pass for that position first would
-    // read every row's positions twice).
+    // read every row's positions twice; a step's rows 9.9 us, made again 10.5, the prompts' 68 and 73).
     Window seen;
     constexpr int kBatch = 4;  // loads on their way together (the stores would hold the next ones up)
     for (int newest = positions[L - 1];;) {
@@ -345,7 +345,8 @@ extern "C" int pa_cache_evict(int32_t *new_tables, int32_t *new_lens, int32_t *n
     for (int i = 0; i < n_pools; ++i) a.pools[i] = static_cast<uint8_t *>(pools[i]);
     // One CTA per row where it can be: its meetings and passes cost half of a cluster's, and more rows are
     // under way at once (256 rows of 16384 tokens: 1 CTA 67 us, 2 76, 4 92).  More where two would not fit
-    // an SM, and, of long rows, where there are few.
+    // an SM, and, of long rows, where there are few.  (By the room, the lengths are not known here: a
+    // step's 32 rows of 1088 tokens 9.9 us, with room for 4096 12.5, for 16384 and more 19.)
     const int sms = pa::sm_count();
     if (sms <= 0) return PA_ECUDA;
     a.ctas = 1;

@@ -356,7 +356,8 @@ __device__ uint64_t exact_score(const SelectArgs &a, const float *q, int phys, i
 // differ by less than its error, so blocks that the border may lie among (a few) are
 // scored again, exactly for all that matters.  Bound by memory where a context is long (the
 // bounds are read once), by the chain of loads, meetings and passes where it is short: 2 rows of
-// 1025 blocks take 10.4 us, 32 rows of 2048 (34 MB) 16.5, 128 ragged FP8 rows of up to 8192 (135 MB) 50.
+// 1025 blocks take 10 to 11 us, 32 rows of 2048 (34 MB) 16.5, 128 ragged FP8 rows of up to 8192 (135 MB) 54
+// to 58.
 template <bool F8, int D>
 __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const SelectArgs a) {
     constexpr int kRowBytes = 2 * D * (F8 ? 1 : 2);
@@ -637,7 +638,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) blocks_select_kernel(const Sel
             need = 0u;
             __syncthreads();
         } else {
-            // too many (hundreds of blocks that are nearly alike): 31 bits of their exact scores at a time
+            // too many (hundreds of blocks that are nearly alike): 31 bits of their exact scores at a time, all
+            // of them scored again for each (one row of 8192 blocks that are all alike: 3 ms, 32 such rows 4.6,
+            // where bounds that differ take 42 us)
             const uint64_t last = double_key(static_cast<double>(key_float(to)) + 2.0 * err);
             uint64_t base = double_key(static_cast<double>(key_float(from)) - 2.0 * err);
             uint64_t span = last - base;

@@ -83,7 +83,7 @@ __device__ __forceinline__ void add_columns(float (&sum)[2], const float (&acc)[
 // The four lanes that share a token add up two tiles at once and end with a token each, so
 // that old and new weights are whole lines.  A 7B-shaped step (34 MB of keys) takes 7.7 us, 4 of
 // them the launch and the first loads' chain; 32 ragged FP8 sequences of up to 16384 tokens (294
-// MB) 57 to 66 us, 0.66 to 0.77 of a copy's rate.
+// MB) 58 to 68 us, 0.64 to 0.76 of a copy's rate.
 template <bool F8, int D, bool kOne>
 __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs a, int pairs) {
     constexpr int kRowBytes = D * (F8 ? 1 : 2);
@@ -220,12 +220,13 @@ __global__ void __launch_bounds__(kWThreads, 2) weights_kernel(const WeightsArgs
 // exponentials (0.5 us at 32 a clock) and 32 KB of keys (0.75 us at an SM's share of the
 // memory), all overlapped.  -lse stays in registers, a thread's columns being the same in every
 // row: loads of it from shared memory compete with the MMA's operands there.  32 queries of 7 heads
-// over 4 x 32768 tokens take 37.7 us (memory alone: 20), 6 queries 30: 5 us of start, 0.85 us a
-// tile (of a ring of four, each 2 to 3 us on its way), and 8 of 152 SMs without a share.
+// over 4 x 32768 tokens take 38 us (memory alone: 20) on 144 of 152 SMs: 10 of start and end and
+// 0.98 for each of a CTA's 29 tiles (8192 tokens, 8 tiles: 17.7; 16384, 15 tiles: 24.5); 6 queries 30:
+// 7 and 0.8.
 //
 // Keys come into a ring of stages as the MMA reads them (K-major, 128-byte swizzle): by TMA from
 // one warp (8 warps of asynchronous copies: 5 us more), or for FP8 pools by 8 warps, which widen the
-// codes to fp16 on the way (50 us, bound by that).  Every wait is bounded.
+// codes to fp16 on the way (54 us, 1.5 a tile: bound by that).  Every wait is bounded.
 constexpr int kXColumns = 256;           // at once
 template <bool F8>
 struct XWarps {
@@ -599,7 +600,8 @@ cudaError_t launch_weights(const WeightsArgs &a, int B, int64_t most, cudaStream
         // pair at an SM's share of the memory (two CTAs an SM, 22 bytes a nanosecond each); rows three
         // quarters full, and, in waves, one more for the ends.  (8 x 4 rows of 4096 bf16 tokens: 1 pair 10.2
         // us, 2 8.3, 4 9.5; of 16384 1 29, 4 25, 8 24; 32 x 8 ragged FP8 rows 1 112, 4 68, 8 61; 16 pairs
-        // were worse or the same.)
+        // were worse or the same.)  The lengths are not known here: rows much shorter than their tables get
+        // more pairs than they need (8 x 4 rows of 4096 tokens in tables for 8192 9.5 us, 32768 9.8, 131072 14.9).
         const int64_t sms = sm_count();
         if (sms <= 0) return cudaErrorInvalidDevice;
         int pairs = 1;
